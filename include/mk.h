@@ -384,6 +384,103 @@ MK_API int mk_decode_step_static(const mk_model_desc* d, const mk_weights* w, co
  * Errors: INVALID_ARG, UNSUPPORTED (as mk_create's description checks). */
 MK_API int mk_static_bytes(const mk_model_desc* d, int32_t grid, int64_t* need_out, int64_t* capacity_out);
 
+/* ---- a K/V cache held in 4 bits ----
+ *
+ * Format.  K and V of one (position, kv head) are cut into groups of 64 values
+ * along head_dim.  A group shares the scale s = bfloat16(max|x| / 7) (fp32
+ * division, round to nearest even); a value's code is the magnitude
+ * m = min(7, rint(|x| / s)) in bits 0..2 and the sign in bit 3 (0 for m = 0),
+ * and stands for +-m * s.  A group whose scale rounds to 0 holds zeros; one
+ * with a NaN or an infinity has a NaN scale and reads back as NaN.
+ * A pool of one layer is [n_pages][n_kv_heads][record]: a page holds 128
+ * positions, a record is two tiles of 64 positions, and a tile is
+ *     K codes  uint8    [64][head_dim / 2]   (even index in the low nibble)
+ *     K scales bfloat16 [64][head_dim / 64]
+ *     V codes, V scales likewise
+ * (17408 bytes a record at head_dim 128, 8704 at 64; 16-bit K/V take 65536 and
+ * 32768).  A tile is one contiguous range, so a reader moves it with one copy.
+ *
+ * The pool, the table and the lengths belong to the caller and lie on the
+ * current device.  The calls only enqueue on `stream`: no allocation, no
+ * synchronisation, so they can be captured into a graph, which reads lengths,
+ * table and n_new anew at every replay.
+ *
+ * Sequence i of a call has lengths[i] positions, the row's own new ones among
+ * them, position p in slot p % 128 of page table[i][p / 128].  Of the call's
+ * `rows` rows of sequence i the first n_new[i] are real (all of them where
+ * n_new is NULL); row r < n_new[i] is position lengths[i] - n_new[i] + r.  A row
+ * past n_new[i], or whose position would be negative, is padding.
+ *
+ * status (optional, device int32[1], the caller clears it) receives
+ * MK_ERR_DEVICE_INDEX if a length is outside [0, 128 * max_pages], an n_new
+ * outside [0, rows] or a page that is needed outside [0, n_pages).  Such a
+ * length or n_new is held to its range and such a page is left out: nothing is
+ * stored there, zeros are loaded, and attention does not see its positions. */
+typedef struct mk_kv4_cache {
+  void* pool;             /* 16-byte aligned */
+  const int32_t* table;   /* device int32 [n_seqs][max_pages] */
+  const int32_t* lengths; /* device int32 [n_seqs] */
+  const int32_t* n_new;   /* device int32 [n_seqs], or NULL */
+  int32_t* status;        /* device int32 [1], or NULL */
+  int32_t n_pages;        /* pages of the pool */
+  int32_t n_kv_heads;     /* 1..1024 */
+  int32_t head_dim;       /* 64 or 128 */
+  int32_t n_seqs;         /* sequences of the call; 0: nothing is done */
+  int32_t max_pages;      /* entries of a table row */
+  int32_t rows;           /* rows of each sequence; 0: nothing is done; n_seqs x rows <= 524287 */
+} mk_kv4_cache;
+
+/* Rows of heads [n_seqs][rows][heads][head_dim] in a caller's device memory:
+ * strides in elements, head_dim contiguous; the address and every stride are
+ * multiples of 16 bytes (a stride of a dimension of size 1 may be 0). */
+typedef struct mk_kv4_rows {
+  const void* data;
+  int64_t seq_stride, row_stride, head_stride;
+} mk_kv4_rows;
+
+/* Bytes of one page of one layer (0 for heads that are not supported). */
+MK_API size_t mk_kv4_page_bytes(int32_t n_kv_heads, int32_t head_dim);
+
+/* Store the new rows' K and V (dtype MK_BF16 or MK_F32, heads: n_kv_heads) in
+ * their places; padding rows are not read or stored.  Two sequences of a call
+ * must not name the same place (a page shared by two sequences is read by
+ * both, written by neither).  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+MK_API int mk_kv4_store(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype,
+                        void* stream);
+
+/* Write what the new rows' places hold to k and v (+-m * s, rounded to dtype);
+ * zeros for padding rows.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+MK_API int mk_kv4_load(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype,
+                       void* stream);
+
+/* Causal attention of the new rows over the cache (which holds their own K and
+ * V already): row r of sequence i sees positions below
+ * lengths[i] - n_new[i] + r + 1; query head h reads kv head
+ * h / (n_heads / n_kv_heads); weights softmax(scale * q . k).  out gets the
+ * rows in q's dtype, lse (may be NULL) float32 [n_seqs][rows][n_heads] the
+ * natural logarithm of the sum of exp(scale * q . k).  A row that sees nothing
+ * (padding, a length of 0) gets zeros and -infinity.  Positions past the
+ * length are never used, whatever their slots hold.
+ * workspace: device memory of at least mk_kv4_attention_bytes, 16-byte
+ * aligned; its contents before the call do not matter, and calls that may
+ * overlap on the GPU need workspaces of their own.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, const mk_kv4_rows* q, int32_t dtype,
+                            float scale, const mk_kv4_rows* out, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that mk_kv4_attention needs for calls of this shape (any
+ * lengths).  0 for a description that mk_kv4_attention refuses, or that needs none. */
+MK_API size_t mk_kv4_attention_bytes(const mk_kv4_cache* c, int32_t n_heads, int32_t dtype);
+
+/* Copy page src_host[i] to page dst_host[i] in every layer of a pool
+ * [n_layers][n_pages][page_bytes] (device, 16-byte aligned, page_bytes a
+ * multiple of 16), whatever its pages hold.  The lists are host int32[n], read
+ * during the call.  The moves run at once: destinations must be distinct, and
+ * none may be a source.  Enqueues on `stream`.  Errors: INVALID_ARG, CUDA. */
+MK_API int mk_page_copy(void* pool, int32_t n_layers, int32_t n_pages, size_t page_bytes,
+                        const int32_t* src_host, const int32_t* dst_host, int32_t n, void* stream);
+
 /* Message of the calling thread's last failure ("" if none). */
 MK_API const char* mk_last_error(void);
 

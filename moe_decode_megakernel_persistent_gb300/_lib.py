@@ -68,6 +68,18 @@ class mk_info(C.Structure):
                 ("last_chunk", C.c_int32), ("last_units", C.c_int32)]
 
 
+class mk_kv4_cache(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("table", C.c_void_p), ("lengths", C.c_void_p),
+                ("n_new", C.c_void_p), ("status", C.c_void_p), ("n_pages", C.c_int32),
+                ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("n_seqs", C.c_int32),
+                ("max_pages", C.c_int32), ("rows", C.c_int32)]
+
+
+class mk_kv4_rows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("seq_stride", C.c_int64), ("row_stride", C.c_int64),
+                ("head_stride", C.c_int64)]
+
+
 # every symbol include/mk.h declares, with its ctypes signature
 SIGNATURES = {
     "mk_create": (C.c_int, [C.POINTER(mk_model_desc), C.POINTER(mk_weights), C.POINTER(C.c_void_p)]),
@@ -97,6 +109,17 @@ SIGNATURES = {
                                         C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.POINTER(C.c_int32),
                                         C.POINTER(C.c_int32), C.POINTER(C.c_int32), C.c_int32,
                                         C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "mk_kv4_page_bytes": (C.c_size_t, [C.c_int32, C.c_int32]),
+    "mk_kv4_store": (C.c_int, [C.POINTER(mk_kv4_cache), C.POINTER(mk_kv4_rows), C.POINTER(mk_kv4_rows),
+                               C.c_int32, C.c_void_p]),
+    "mk_kv4_load": (C.c_int, [C.POINTER(mk_kv4_cache), C.POINTER(mk_kv4_rows), C.POINTER(mk_kv4_rows),
+                              C.c_int32, C.c_void_p]),
+    "mk_kv4_attention": (C.c_int, [C.POINTER(mk_kv4_cache), C.c_int32, C.POINTER(mk_kv4_rows), C.c_int32,
+                                   C.c_float, C.POINTER(mk_kv4_rows), C.c_void_p, C.c_void_p, C.c_size_t,
+                                   C.c_void_p]),
+    "mk_kv4_attention_bytes": (C.c_size_t, [C.POINTER(mk_kv4_cache), C.c_int32, C.c_int32]),
+    "mk_page_copy": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_size_t, C.c_void_p,
+                               C.c_void_p, C.c_int32, C.c_void_p]),
     "mk_static_bytes": (C.c_int, [C.POINTER(mk_model_desc), C.c_int32, C.POINTER(C.c_int64),
                                   C.POINTER(C.c_int64)]),
 }
@@ -239,6 +262,35 @@ def mk_decode_step_static(desc: mk_model_desc, weights: mk_weights, packed_dev: 
                                         block_table_dev, max_pages_per_seq, _i32(slots),
                                         _i32(positions, n), _i32(pages, n), n, tokens_dev,
                                         out_tokens_dev, status_dev or None, stream))
+
+
+def mk_kv4_page_bytes(n_kv_heads: int, head_dim: int) -> int:
+    return int(load().mk_kv4_page_bytes(n_kv_heads, head_dim))
+
+
+def mk_kv4_store(cache: mk_kv4_cache, k: mk_kv4_rows, v: mk_kv4_rows, dtype: int, stream: int = 0):
+    _check(load().mk_kv4_store(cache, k, v, dtype, stream))
+
+
+def mk_kv4_load(cache: mk_kv4_cache, k: mk_kv4_rows, v: mk_kv4_rows, dtype: int, stream: int = 0):
+    _check(load().mk_kv4_load(cache, k, v, dtype, stream))
+
+
+def mk_kv4_attention(cache: mk_kv4_cache, n_heads: int, q: mk_kv4_rows, dtype: int, scale: float,
+                     out: mk_kv4_rows, lse_dev: int | None, workspace_dev: int, workspace_bytes: int,
+                     stream: int = 0):
+    _check(load().mk_kv4_attention(cache, n_heads, q, dtype, scale, out, lse_dev, workspace_dev,
+                                   workspace_bytes, stream))
+
+
+def mk_kv4_attention_bytes(cache: mk_kv4_cache, n_heads: int, dtype: int) -> int:
+    return int(load().mk_kv4_attention_bytes(cache, n_heads, dtype))
+
+
+def mk_page_copy(pool_dev: int, n_layers: int, n_pages: int, page_bytes: int, src, dst, stream: int = 0):
+    """src, dst: host lists of page indices of the same length."""
+    _check(load().mk_page_copy(pool_dev, n_layers, n_pages, page_bytes, _i32(src), _i32(dst, len(src)),
+                               len(src), stream))
 
 
 def mk_last_error() -> str:

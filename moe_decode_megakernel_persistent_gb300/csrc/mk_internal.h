@@ -145,6 +145,12 @@ struct KvXfer {
 };
 int launch_kv_xfer(const KvXfer& a, cudaStream_t st);
 
+// Page moves of every layer of a pool [n_layers][n_pages][page_bytes]
+// (mk_pages.cu); the caller has checked that no page is written twice or both
+// read and written.
+int launch_page_copy(void* pool, int n_layers, int n_pages, size_t page_bytes, const int32_t* src, const int32_t* dst,
+                     int n, cudaStream_t st);
+
 // Chunked prefill (mk_prefill.cu): chunks of more than kMaxBatch positions
 // run as per-layer GEMMs over all rows of the chunk.
 constexpr int kMaxPrefill = 4096;
