@@ -460,7 +460,8 @@ MK_API int mk_kv4_load(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4
  * rows in q's dtype, lse (may be NULL) float32 [n_seqs][rows][n_heads] the
  * natural logarithm of the sum of exp(scale * q . k).  A row that sees nothing
  * (padding, a length of 0) gets zeros and -infinity.  Positions past the
- * length are never used, whatever their slots hold.
+ * length are never used, whatever their slots hold.  |scale| < 1e18; magnitudes of
+ * q and V up to 2^50 are kept whole, terms weight * value below 2^-60 may be lost.
  * workspace: device memory of at least mk_kv4_attention_bytes, 16-byte
  * aligned; its contents before the call do not matter, and calls that may
  * overlap on the GPU need workspaces of their own.

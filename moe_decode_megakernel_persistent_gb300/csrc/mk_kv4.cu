@@ -1,79 +1,20 @@
-// The 4-bit paged K/V cache of the C ABI: storing rows, loading them back and
-// attention over them, on pools the caller owns (include/mk.h describes the
-// format and the calls).
+// The 4-bit paged K/V cache of the C ABI: storing rows and loading them back, on
+// pools the caller owns (include/mk.h describes the format and the calls;
+// mk_kv4_attention.cu reads the cache).
 //
 // Format.  A row of one (position, kv head) is cut into groups of 64 values
 // along head_dim; a group shares s = bf16(max|x| / 7), and a value is a sign
 // bit and a magnitude min(7, rint(|x| / s)).  It is the symmetric int4 rule of
 // the weights with the code kept as sign and magnitude instead of two's
 // complement (-8 cannot occur: |x| / s <= 7 * (1 + 2^-8)).
-#include <cuda_bf16.h>
-
 #include <algorithm>
-#include <cfloat>
 #include <climits>
 #include <string>
 
-#include "mk_internal.h"
+#include "mk_kv4.cuh"
 
 namespace mk {
 namespace {
-
-constexpr int kTile = 64;    // positions of a tile
-constexpr int kGroup = 64;   // values that share a scale
-
-// A tile of one kv head: K codes, K scales, V codes, V scales.
-template <int HD>
-struct Tile {
-  static constexpr int ROW = HD / 2;             // code bytes of a row
-  static constexpr int NG = HD / kGroup;         // scales of a row
-  static constexpr int CODES = kTile * ROW;
-  static constexpr int SCALES = kTile * NG * 2;
-  static constexpr int V = CODES + SCALES;       // offset of the V half
-  static constexpr int BYTES = 2 * V;
-  static constexpr int RECORD = kPageTokens / kTile * BYTES;
-};
-
-struct Kv4Args {
-  uint8_t* pool;
-  const int32_t* table;
-  const int32_t* lengths;
-  const int32_t* n_new;
-  int32_t* status;
-  int32_t n_pages, n_kv_heads, n_seqs, max_pages, rows;
-};
-
-__device__ __forceinline__ void refuse(int32_t* status) {
-  if (status) atomicCAS(status, 0, MK_ERR_DEVICE_INDEX);
-}
-
-// Length and new rows of a sequence, held to what the table and the call can hold.
-__device__ __forceinline__ void seq_extent(const Kv4Args& a, int s, int& len, int& nn) {
-  len = a.lengths[s];
-  nn = a.n_new ? a.n_new[s] : a.rows;
-  const long long most = (long long)a.max_pages * kPageTokens;
-  if (len < 0 || len > most || nn < 0 || nn > a.rows) refuse(a.status);
-  len = (int)max(0ll, min((long long)len, most));
-  nn = max(0, min(nn, a.rows));
-}
-
-// The page of position p of sequence s, or -1.
-__device__ __forceinline__ int page_of(const Kv4Args& a, int s, int p) {
-  const int page = a.table[(size_t)s * a.max_pages + p / kPageTokens];
-  if (page >= 0 && page < a.n_pages) return page;
-  refuse(a.status);
-  return -1;
-}
-
-template <int HD>
-__device__ __forceinline__ uint8_t* tile_of(const Kv4Args& a, int page, int head, int p) {
-  return a.pool + ((size_t)page * a.n_kv_heads + head) * Tile<HD>::RECORD + (size_t)(p % kPageTokens / kTile) * Tile<HD>::BYTES;
-}
-
-struct Rows {
-  const void* p;
-  long long seq, row, head;  // strides in elements
-};
 
 __device__ __forceinline__ float4 read4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 read4(const __nv_bfloat16* p) {
@@ -182,63 +123,6 @@ __global__ void __launch_bounds__(256) k_kv4_load(const __grid_constant__ Kv4Arg
          x);
 }
 
-// Attention, plain: one block per (sequence, row, head), tiles of 64 positions,
-// online softmax in fp32; a thread takes a position for the scores and a
-// dimension for the values.
-template <int HD, class T>
-__global__ void __launch_bounds__(HD) k_kv4_attention_plain(const __grid_constant__ Kv4Args a, int n_heads, Rows q,
-                                                            float scale, Rows out, float* lse) {
-  __shared__ float qs[HD], ps[kTile], red[2];
-  const int h = blockIdx.x % n_heads, row = blockIdx.x / n_heads % a.rows, seq = blockIdx.x / n_heads / a.rows;
-  const int g = h / (n_heads / a.n_kv_heads), tid = threadIdx.x;
-  int len, nn;
-  seq_extent(a, seq, len, nn);
-  const int lim = row < nn ? max(0, len - nn + row + 1) : 0;
-  qs[tid] = (float)(reinterpret_cast<const T*>(q.p) + seq * q.seq + row * q.row + h * q.head)[tid];
-  float m = -FLT_MAX, l = 0.f, o = 0.f;
-  for (int t0 = 0; t0 < lim; t0 += kTile) {
-    const int page = page_of(a, seq, t0);
-    const uint8_t* t = tile_of<HD>(a, max(page, 0), g, t0);
-    __syncthreads();
-    if (tid < kTile) {
-      float s = -INFINITY;
-      if (t0 + tid < lim && page >= 0) {
-        s = 0.f;
-        for (int d = 0; d < HD; ++d) {
-          const float ks = __uint_as_float(
-              (uint32_t)*reinterpret_cast<const uint16_t*>(t + Tile<HD>::CODES + (tid * Tile<HD>::NG + d / kGroup) * 2) << 16);
-          s = fmaf(qs[d], value_of(t[tid * Tile<HD>::ROW + d / 2] >> (4 * (d % 2)), ks), s);
-        }
-        s *= scale;
-      }
-      ps[tid] = s;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      float mx = -INFINITY;
-      for (int i = 0; i < kTile; ++i) mx = fmaxf(mx, ps[i]);
-      red[0] = fmaxf(m, mx);
-    }
-    __syncthreads();
-    const float mn = red[0];
-    const float corr = expf(m - mn);
-    m = mn;
-    l *= corr;
-    o *= corr;
-    for (int i = 0; i < kTile && t0 + i < lim; ++i) {
-      if (ps[i] == -INFINITY) continue;
-      const float p = expf(ps[i] - m);
-      const float vs = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(
-                                           t + Tile<HD>::V + Tile<HD>::CODES + (i * Tile<HD>::NG + tid / kGroup) * 2) << 16);
-      l += p;
-      o = fmaf(p, value_of(t[Tile<HD>::V + i * Tile<HD>::ROW + tid / 2] >> (4 * (tid % 2)), vs), o);
-    }
-  }
-  (reinterpret_cast<T*>(const_cast<void*>(out.p)) + seq * out.seq + row * out.row + h * out.head)[tid] =
-      (T)(l == 0.f ? 0.f : o / l);
-  if (lse && tid == 0) lse[((size_t)seq * a.rows + row) * n_heads + h] = l == 0.f ? -INFINITY : m + logf(l);
-}
-
 int cuda_status(const char* what) {
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? MK_OK : host_fail(MK_ERR_CUDA, (std::string(what) + ": " + cudaGetErrorString(e)).c_str());
@@ -246,8 +130,10 @@ int cuda_status(const char* what) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+}  // namespace
+
 // Checks of a cache description; *empty says that the call has no row.
-int check_cache(const mk_kv4_cache* c, bool* empty) {
+int kv4_check_cache(const mk_kv4_cache* c, bool* empty) {
   if (!c) return host_fail(MK_ERR_INVALID_ARG, "cache is NULL");
   if (c->head_dim != 64 && c->head_dim != 128) return host_fail(MK_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
   if (c->n_kv_heads < 1 || c->n_kv_heads > 1024) return host_fail(MK_ERR_INVALID_ARG, "n_kv_heads must be in [1, 1024]");
@@ -263,7 +149,7 @@ int check_cache(const mk_kv4_cache* c, bool* empty) {
   return MK_OK;
 }
 
-int check_rows(const mk_kv4_rows* r, int dtype, const char* what) {
+int kv4_check_rows(const mk_kv4_rows* r, int dtype, const char* what) {
   if (dtype != MK_F32 && dtype != MK_BF16) return host_fail(MK_ERR_INVALID_ARG, "dtype must be MK_F32 or MK_BF16");
   const int per = dtype == MK_F32 ? 4 : 8;  // elements of 16 bytes
   if (!r || !r->data || !aligned16(r->data) || r->seq_stride % per || r->row_stride % per || r->head_stride % per)
@@ -271,13 +157,6 @@ int check_rows(const mk_kv4_rows* r, int dtype, const char* what) {
   return MK_OK;
 }
 
-Kv4Args args_of(const mk_kv4_cache& c) {
-  return {static_cast<uint8_t*>(c.pool), c.table, c.lengths, c.n_new, c.status, c.n_pages, c.n_kv_heads, c.n_seqs,
-          c.max_pages, c.rows};
-}
-Rows rows_of(const mk_kv4_rows& r) { return {r.data, r.seq_stride, r.row_stride, r.head_stride}; }
-
-}  // namespace
 }  // namespace mk
 
 using namespace mk;
@@ -305,11 +184,11 @@ extern "C" MK_API int mk_kv4_store(const mk_kv4_cache* c, const mk_kv4_rows* k, 
                                    void* stream) {
   host_clear_error();
   bool empty = false;
-  if (int r = check_cache(c, &empty)) return r;
+  if (int r = kv4_check_cache(c, &empty)) return r;
   if (empty) return MK_OK;
-  if (int r = check_rows(k, dtype, "k")) return r;
-  if (int r = check_rows(v, dtype, "v")) return r;
-  MK_KV4_LAUNCH(k_kv4_store, c->head_dim, dtype, kv4_blocks(*c), 256, (cudaStream_t)stream, args_of(*c), rows_of(*k), rows_of(*v));
+  if (int r = kv4_check_rows(k, dtype, "k")) return r;
+  if (int r = kv4_check_rows(v, dtype, "v")) return r;
+  MK_KV4_LAUNCH(k_kv4_store, c->head_dim, dtype, kv4_blocks(*c), 256, (cudaStream_t)stream, kv4_args(*c), kv4_rows(*k), kv4_rows(*v));
   return cuda_status("kv4 store");
 }
 
@@ -317,37 +196,10 @@ extern "C" MK_API int mk_kv4_load(const mk_kv4_cache* c, const mk_kv4_rows* k, c
                                   void* stream) {
   host_clear_error();
   bool empty = false;
-  if (int r = check_cache(c, &empty)) return r;
+  if (int r = kv4_check_cache(c, &empty)) return r;
   if (empty) return MK_OK;
-  if (int r = check_rows(k, dtype, "k")) return r;
-  if (int r = check_rows(v, dtype, "v")) return r;
-  MK_KV4_LAUNCH(k_kv4_load, c->head_dim, dtype, kv4_blocks(*c), 256, (cudaStream_t)stream, args_of(*c), rows_of(*k), rows_of(*v));
+  if (int r = kv4_check_rows(k, dtype, "k")) return r;
+  if (int r = kv4_check_rows(v, dtype, "v")) return r;
+  MK_KV4_LAUNCH(k_kv4_load, c->head_dim, dtype, kv4_blocks(*c), 256, (cudaStream_t)stream, kv4_args(*c), kv4_rows(*k), kv4_rows(*v));
   return cuda_status("kv4 load");
-}
-
-extern "C" MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, const mk_kv4_rows* q, int32_t dtype,
-                                       float scale, const mk_kv4_rows* out, float* lse, void* workspace,
-                                       size_t workspace_bytes, void* stream) {
-  host_clear_error();
-  bool empty = false;
-  if (int r = check_cache(c, &empty)) return r;
-  if (n_heads < 1 || n_heads % c->n_kv_heads || n_heads > 4096)
-    return host_fail(MK_ERR_INVALID_ARG, "n_heads must be a multiple of n_kv_heads, at most 4096");
-  if (!(scale > -FLT_MAX && scale < FLT_MAX)) return host_fail(MK_ERR_INVALID_ARG, "scale must be finite");
-  if (empty) return MK_OK;
-  if (int r = check_rows(q, dtype, "q")) return r;
-  if (int r = check_rows(out, dtype, "out")) return r;
-  (void)workspace;
-  (void)workspace_bytes;
-  const int grid = c->n_seqs * c->rows * n_heads;
-  MK_KV4_LAUNCH(k_kv4_attention_plain, c->head_dim, dtype, grid, c->head_dim, (cudaStream_t)stream, args_of(*c), n_heads,
-                rows_of(*q), scale, rows_of(*out), lse);
-  return cuda_status("kv4 attention");
-}
-
-extern "C" MK_API size_t mk_kv4_attention_bytes(const mk_kv4_cache* c, int32_t n_heads, int32_t dtype) {
-  (void)c;
-  (void)n_heads;
-  (void)dtype;
-  return 0;
 }

@@ -1,0 +1,790 @@
+// Causal attention over the 4-bit paged K/V cache (mk_kv4_attention): single
+// rows of a decode step, drafted rows and prompt chunks.
+//
+// Mathematics.  For a row q and the positions p it sees, s_p = c q . K_p,
+// out = sum_p e^(s_p - m) V_p / sum_p e^(s_p - m).  K_p = ks (codes), one scale
+// per group of 64 dimensions, so q . K_p = sum_groups ks_g (q_g . code_g): the
+// products run on the codes and the scale multiplies their fp32 sum.  V's scale
+// multiplies the weight instead (one weight per group), so neither K nor V is
+// ever formed: tensor cores (mma.sync m16n8k16) take the codes as they are.
+//
+// A code becomes a bf16 operand without arithmetic.  The nibble of a byte,
+// moved to bits 15 (sign) and 6..4 (magnitude) of a half word, is the bf16
+// subnormal +-m 2^-129, exactly.  One byte permutation doubles two bytes into
+// the halves of a word (two positions for V, two dimensions for K), one mask
+// takes the high nibbles and one shift and mask the low ones: 1 instruction a
+// value (the magic-number form takes 1.5).  The other operand carries 2^64 (q,
+// or the weights), and the fp32 results 2^-65: they stay far from fp32's ends.
+//
+// Roundings to fewer bits: a bf16 q is exact; an fp32 q is split into three bf16
+// parts (24 bits).  The weights times V's scales are split into two bf16 parts
+// for bf16 rows (16 bits: 2^-17 of a weight, where the output itself is rounded to
+// 2^-9) and three for fp32 rows.  Everything else is fp32.
+//
+// Layout.  K is the mma's A operand (16 positions x 16 dimensions) and q its B
+// operand, so that the query columns of one kv head (rows x heads of the group)
+// fill tiles of 8 columns; a step of 4 heads with one row takes one tile whose
+// columns 4..7 carry the weights' low parts.  The weights come out transposed
+// for the second product (V^T x weights^T) and turn with movmatrix.
+//
+// Work.  The tiles of 64 positions of all (sequence, column tile, kv head)
+// items are laid end to end and cut into equal runs, one for each block, from
+// the lengths on the device: a ragged batch costs what its sum costs, and a
+// captured graph follows the lengths.  A warp streams the block's tiles (one
+// bulk copy of 8.5 KB each) through a shared-memory ring; four warps take 16
+// positions of each tile, with running maxima of their own (moved only when a
+// score passes them by 2^8) and one merge at the end of an item.  An item cut
+// between blocks is joined by a second kernel, launched so that its start
+// overlaps the first one's end.
+#include <algorithm>
+#include <atomic>
+#include <cfloat>
+#include <climits>
+#include <string>
+#include <type_traits>
+
+#include "mk_kv4.cuh"
+
+namespace mk {
+namespace {
+
+constexpr int kAttWarps = 4;                       // 16 positions of a tile each
+constexpr int kAttThreads = 32 * (kAttWarps + 1);  // and the streaming warp
+constexpr int kRing = 4;                           // tiles in flight
+constexpr uint64_t kWaitNs = 1000000000ull;        // bound of every wait
+constexpr float kLow = -1e30f;                     // running maximum of a column that has seen nothing
+constexpr float kLazy = 8.f;                       // a maximum moves when a score passes it by this (log2)
+constexpr float kUp = 18446744073709551616.f;      // 2^64, carried by the B operands
+constexpr float kDown = 36893488147419103232.f;    // 2^65 = 2^129 / 2^64, taken out of the results
+
+struct AttArgs {
+  Kv4Args a;
+  Rows q, out;
+  float* lse;
+  float c;              // scale * log2(e) * 2^65
+  int32_t n_heads, gqa;
+  int32_t cols;         // rows * gqa: query columns of a (sequence, kv head)
+  int32_t n_ctiles;     // column tiles of it
+  int32_t n_entries;    // n_seqs * n_ctiles
+  long long* total;     // workspace: tiles of the call
+  longlong2* item;      // workspace: [n_entries * n_kv_heads] first tile and block, or -1 (done)
+  float* part;          // workspace: [2 * grid][columns][HD + 4] partial results
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Wait for a phase; gives up after kWaitNs (and at once when another warp of the
+// block has): then *give_up is set and the block runs to its end without data.
+__device__ __noinline__ void bar_wait_long(uint32_t bar, uint32_t parity, volatile int* give_up, int32_t* status) {
+  const uint64_t t0 = now_ns();
+  for (uint32_t i = 0;; ++i) {
+    if (bar_try(bar, parity) || *give_up) return;
+    if ((i & 15u) == 15u && now_ns() - t0 > kWaitNs) {
+      *give_up = 1;
+      if (status) atomicCAS(status, 0, MK_ERR_BARRIER_TIMEOUT);
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile int* give_up, int32_t* status) {
+  if (!bar_try(bar, parity)) bar_wait_long(bar, parity, give_up, status);
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+__device__ __forceinline__ uint32_t turn(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {  // bf16x2
+  uint32_t y;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  return y;
+}
+__device__ __forceinline__ float low_f(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float high_f(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr uint32_t kNib = 0x80708070u;
+
+// Column tile j of sequence s: how many tiles of positions its columns see.
+__device__ __forceinline__ int tiles_of(const AttArgs& p, int e, int CT) {
+  const int s = e / p.n_ctiles, j = e - s * p.n_ctiles;
+  int len, nn;
+  seq_extent(p.a, s, len, nn);
+  if (j * CT / p.gqa >= nn) return 0;                                     // its rows are padding
+  const int r = min((min((j + 1) * CT, p.cols) - 1) / p.gqa, nn - 1);     // its last row
+  const int end = len - nn + r + 1;
+  return end <= 0 ? 0 : (end + kTile - 1) / kTile;
+}
+
+// The runs of a block: its tiles [pos, hi) cut at items.
+struct Runs {
+  long long pos, hi, base;  // base: the first tile of entry e
+  int e, nt, head, t0, t1;
+  __device__ __forceinline__ bool next(const AttArgs& p, int CT) {  // the run at pos; false: none is left
+    if (pos >= hi) return false;
+    for (;; ++e) {
+      if (e >= p.n_entries) return false;  // lengths that change under the call
+      nt = tiles_of(p, e, CT);
+      const long long n = (long long)nt * p.a.n_kv_heads;
+      if (pos < base + n) break;
+      base += n;
+    }
+    const int at = (int)(pos - base);  // below n_kv_heads * nt <= 2^10 * 2^25: held to 31 bits by the entry point
+    head = at / nt;
+    t0 = at - head * nt;
+    t1 = (int)min((long long)nt, t0 + (hi - pos));
+    return true;
+  }
+};
+
+template <int HD, class T, int NT, bool PACK>
+struct Shape {
+  static_assert(!PACK || (NT == 1 && !std::is_same<T, float>::value), "packed columns are for bf16");
+  static constexpr bool F32 = std::is_same<T, float>::value;
+  static constexpr int CT = PACK ? 4 : 8 * NT;   // columns of a tile
+  static constexpr int NG = HD / kGroup;
+  static constexpr int QP = F32 ? 3 : 1;         // parts of q
+  static constexpr int WP = F32 ? 3 : (PACK ? 1 : 2);  // parts of the weights (packed: both in one operand)
+  static constexpr int RS = HD + 2;              // floats of a column in the reduction buffer
+  static constexpr int RED = kAttWarps * 8 * NT * RS * 4;
+  static constexpr int SMEM = kRing * Tile<HD>::BYTES + RED;
+  // blocks of an SM: by registers (two column tiles, or three parts, need more) and shared memory
+  static constexpr int BLOCKS = NT == 1 ? (F32 ? 3 : 4) : (F32 ? 2 : 3);
+};
+
+template <int HD, class T, int NT, bool PACK>
+__global__ void __launch_bounds__(kAttThreads, (Shape<HD, T, NT, PACK>::BLOCKS))
+    k_kv4_attention(const __grid_constant__ AttArgs p) {
+  using S = Shape<HD, T, NT, PACK>;
+  using L = Tile<HD>;
+  constexpr int NG = S::NG, CT = S::CT;
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ __align__(8) uint64_t full[kRing], empty[kRing];
+  __shared__ int loaded[kRing];
+  __shared__ float sm_m[kAttWarps][8 * NT], sm_l[kAttWarps][8 * NT];
+  __shared__ long long s_lo, s_hi, s_base;
+  __shared__ int s_entry;
+  __shared__ volatile int give_up;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[i])) : "memory");
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&empty[i])), "n"(kAttWarps) : "memory");
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    give_up = 0;
+  }
+  if (w == 0) {  // this block's share
+    long long total = 0;
+    for (int e = lane; e < p.n_entries; e += 32) total += tiles_of(p, e, CT);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total *= p.a.n_kv_heads;
+    const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+    if (blockIdx.x == 0 && lane == 0) *p.total = total;
+    long long base = 0;
+    int entry = 0;
+    if (lo < hi) {
+      for (int e0 = 0; e0 < p.n_entries; e0 += 32) {
+        const long long n = e0 + lane < p.n_entries ? (long long)tiles_of(p, e0 + lane, CT) * p.a.n_kv_heads : 0;
+        long long incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += up;
+        }
+        const uint32_t has = __ballot_sync(0xffffffffu, lo < base + incl);
+        if (has) {
+          const int f = __ffs(has) - 1;
+          entry = e0 + f;
+          base += __shfl_sync(0xffffffffu, incl - n, f);
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    if (lane == 0) {
+      s_lo = lo;
+      s_hi = hi;
+      s_base = base;
+      s_entry = entry;
+    }
+  }
+  __syncthreads();
+  Runs run;
+  run.pos = s_lo;
+  run.hi = s_hi;
+  run.base = s_base;
+  run.e = s_entry;
+  const long long lo = s_lo;
+  uint32_t k = 0;  // tiles streamed / used so far
+
+  if (w == kAttWarps) {  // ---- the streaming warp
+    uint32_t issued = 0;
+    while (run.next(p, CT)) {
+      const int seq = run.e / p.n_ctiles;
+      for (int t = run.t0; t < run.t1;) {
+        const int g0 = t / 2;  // pages of the run, 32 at a time
+        const int page = g0 + lane <= (run.t1 - 1) / 2 ? page_of(p.a, seq, (g0 + lane) * kPageTokens) : -1;
+        for (; t < run.t1 && t / 2 < g0 + 32; ++t, ++k) {
+          const int pg = __shfl_sync(0xffffffffu, page, t / 2 - g0), st = k % kRing;
+          if (k >= kRing) bar_wait(smem_addr(&empty[st]), (k / kRing - 1) & 1, &give_up, p.a.status);
+          __syncwarp();
+          if (lane == 0 && !give_up) {
+            const uint32_t bar = smem_addr(&full[st]);
+            loaded[st] = pg >= 0;
+            if (pg >= 0) {
+              asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "n"(L::BYTES) : "memory");
+              asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                               smem_addr(sm + st * L::BYTES)),
+                           "l"(tile_of<HD>(p.a, pg, run.head, t * kTile)), "n"(L::BYTES), "r"(bar)
+                           : "memory");
+            }
+            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+            issued = k + 1;
+          }
+          __syncwarp();
+        }
+      }
+      run.pos += run.t1 - run.t0;
+    }
+    if (lane == 0 && give_up) {  // the copies in flight land before the block ends
+      int none = 0;
+      for (uint32_t i = issued > kRing ? issued - kRing : 0; i < issued; ++i)
+        bar_wait_long(smem_addr(&full[i % kRing]), (i / kRing) & 1, &none, nullptr);
+    }
+    return;
+  }
+
+  // ---- the computing warps: lane (g, t) of the mma fragments
+  const int g = lane >> 2, t4 = lane & 3;
+  while (run.next(p, CT)) {
+    const int seq = run.e / p.n_ctiles, j = run.e - seq * p.n_ctiles;
+    int len, nn;
+    seq_extent(p.a, seq, len, nn);
+    // the B fragments of q: column nt * 8 + g, dimensions 64 h + 16 t + 8 i + 4 jj + {0, 2 | 1, 3}
+    uint2 qf[S::QP][NT][NG][2][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int col = j * CT + (PACK ? (g & 3) : nt * 8 + g);
+      const bool there = col < p.cols;
+      const int row = there ? col / p.gqa : 0, hd = there ? col - row * p.gqa : 0;
+      const T* src = reinterpret_cast<const T*>(p.q.p) + seq * p.q.seq + row * p.q.row +
+                     (run.head * p.gqa + hd) * p.q.head + 16 * t4;
+#pragma unroll
+      for (int h = 0; h < NG; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (there) {
+              if constexpr (S::F32) x = *reinterpret_cast<const float4*>(src + 64 * h + 8 * i + 4 * jj);
+              else {
+                const uint2 v = *reinterpret_cast<const uint2*>(src + 64 * h + 8 * i + 4 * jj);
+                x = make_float4(low_f(v.x), high_f(v.x), low_f(v.y), high_f(v.y));
+              }
+            }
+            x.x *= kUp, x.y *= kUp, x.z *= kUp, x.w *= kUp;
+#pragma unroll
+            for (int q = 0; q < S::QP; ++q) {
+              const uint2 b = make_uint2(pack2(x.x, x.z), pack2(x.y, x.w));
+              qf[q][nt][h][i][jj] = b;
+              if (q + 1 < S::QP) x.x -= low_f(b.x), x.z -= high_f(b.x), x.y -= low_f(b.y), x.w -= high_f(b.y);
+            }
+          }
+    }
+    // positions that this lane's columns see (columns nt * 8 + 2 t, + 1), and what all columns see
+    int lim[NT][2], all = INT_MAX;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int col = j * CT + (PACK ? ((2 * t4 + x) & 3) : nt * 8 + 2 * t4 + x), row = col / p.gqa;
+        lim[nt][x] = col < p.cols && row < nn ? max(0, len - nn + row + 1) : 0;
+        if (col < p.cols) all = min(all, lim[nt][x]);
+      }
+    all = min(all, __shfl_xor_sync(0xffffffffu, all, 1));
+    all = min(all, __shfl_xor_sync(0xffffffffu, all, 2));
+    float m[NT][2], l[NT][2], o[NT][NG][4][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = kLow;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int h = 0; h < NG; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nt][h][i][0] = o[nt][h][i][1] = o[nt][h][i][2] = o[nt][h][i][3] = 0.f;
+    }
+
+    for (int t = run.t0; t < run.t1; ++t, ++k) {
+      const int st = k % kRing;
+      bar_wait(smem_addr(&full[st]), (k / kRing) & 1, &give_up, p.a.status);
+      const int p0 = t * kTile + 16 * w;  // this warp's first position
+      if (loaded[st] && !give_up) {
+        const uint32_t tile = smem_addr(sm + st * L::BYTES);
+        const uint32_t kr = tile + (16 * w + g) * L::ROW + 8 * t4;
+        float a[NT][NG][4];
+#pragma unroll
+        for (int h = 0; h < NG; ++h) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) a[nt][h][0] = a[nt][h][1] = a[nt][h][2] = a[nt][h][3] = 0.f;
+          const uint2 u0 = lds64(kr + 32 * h), u1 = lds64(kr + 8 * L::ROW + 32 * h);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+              const uint32_t x0 = __byte_perm(i ? u0.y : u0.x, 0, jj ? 0x3322 : 0x1100);
+              const uint32_t x1 = __byte_perm(i ? u1.y : u1.x, 0, jj ? 0x3322 : 0x1100);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int q = S::QP - 1; q >= 0; --q)
+                  mma16816(a[nt][h], (x0 << 4) & kNib, (x1 << 4) & kNib, x0 & kNib, x1 & kNib, qf[q][nt][h][i][jj]);
+            }
+        }
+        // scales of positions g and g + 8
+        float ks[2][NG], vs[2][NG];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t at = tile + L::CODES + (16 * w + g + 8 * r) * NG * 2;
+          const uint32_t x = NG == 2 ? lds32(at) : lds16(at), y = NG == 2 ? lds32(at + L::V) : lds16(at + L::V);
+          ks[r][0] = low_f(x);
+          vs[r][0] = low_f(y) * kUp;
+          if constexpr (NG == 2) {
+            ks[r][1] = high_f(x);
+            vs[r][1] = high_f(y) * kUp;
+          }
+        }
+        // scores in log2 units: element x + 2 r is column 2 t + x, position g + 8 r
+        float s[NT][4];
+        bool over = false;
+        const bool cut = p0 + 16 > all;  // some column does not see all of these positions
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = a[nt][0][e] * ks[e >> 1][0];
+            if constexpr (NG == 2) v = fmaf(a[nt][1][e], ks[e >> 1][1], v);
+            v *= p.c;
+            if (cut && p0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) v = -INFINITY;
+            s[nt][e] = v;
+            over |= v > m[nt][e & 1] + kLazy;
+          }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float v = fmaxf(fmaxf(s[nt][x], s[nt][x + 2]), m[nt][x]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+              const float f = exp2_fast(m[nt][x] - v);
+              m[nt][x] = v;
+              l[nt][x] *= f;
+#pragma unroll
+              for (int h = 0; h < NG; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  o[nt][h][i][x] *= f;
+                  o[nt][h][i][x + 2] *= f;
+                }
+            }
+        }
+        // weights times V's scales, as B fragments
+        uint2 wf[S::WP][NT][NG];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float wt[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            wt[e] = exp2_fast(s[nt][e] - m[nt][e & 1]);
+            l[nt][e & 1] += wt[e];
+          }
+#pragma unroll
+          for (int h = 0; h < NG; ++h) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[e] = wt[e] * vs[e >> 1][h];
+              // a scale behind what the column sees may be anything
+              if (cut && p0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) v[e] = 0.f;
+            }
+            if constexpr (PACK) {
+              // columns 0..3 (lanes t < 2) take the high parts, 4..7 the low parts
+              const uint32_t keep = t4 < 2 ? 0u : 0xFFFFFFFFu;
+              uint32_t b[2];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const uint32_t hi = pack2(v[2 * r], v[2 * r + 1]) & keep;
+                b[r] = turn(pack2(v[2 * r] - low_f(hi), v[2 * r + 1] - high_f(hi)));
+              }
+              wf[0][nt][h] = make_uint2(b[0], b[1]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < S::WP; ++q) {
+                const uint32_t b0 = pack2(v[0], v[1]), b1 = pack2(v[2], v[3]);
+                wf[q][nt][h] = make_uint2(turn(b0), turn(b1));
+                if (q + 1 < S::WP) v[0] -= low_f(b0), v[1] -= high_f(b0), v[2] -= low_f(b1), v[3] -= high_f(b1);
+              }
+            }
+          }
+        }
+        // V: positions 2 t, 2 t + 1 and 2 t + 8, 2 t + 9, dimensions 64 h + 8 g + {0..7}
+        const uint32_t vr = tile + L::V + (16 * w + 2 * t4) * L::ROW + 4 * g;
+#pragma unroll
+        for (int h = 0; h < NG; ++h) {
+          const uint32_t v0 = lds32(vr + 32 * h), v1 = lds32(vr + L::ROW + 32 * h);
+          const uint32_t v8 = lds32(vr + 8 * L::ROW + 32 * h), v9 = lds32(vr + 9 * L::ROW + 32 * h);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t sel = 0x4400u + 0x1111u * i;
+            const uint32_t x = __byte_perm(v0, v1, sel), y = __byte_perm(v8, v9, sel);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (S::F32) {  // a tile's terms are summed on their own, then added
+                float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = S::WP - 1; q >= 0; --q)
+                  mma16816(f, (x << 4) & kNib, x & kNib, (y << 4) & kNib, y & kNib, wf[q][nt][h]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][h][i][e] += f[e];
+              } else {
+#pragma unroll
+                for (int q = 0; q < S::WP; ++q)
+                  mma16816(o[nt][h][i], (x << 4) & kNib, x & kNib, (y << 4) & kNib, y & kNib, wf[q][nt][h]);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[st])) : "memory");
+    }
+
+    // ---- the item's end: the four warps' sums joined
+    float* red = reinterpret_cast<float*>(sm + kRing * L::BYTES);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], d);
+        if (g == 0) {
+          sm_m[w][nt * 8 + 2 * t4 + x] = m[nt][x];
+          sm_l[w][nt * 8 + 2 * t4 + x] = l[nt][x];
+        }
+      }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kAttWarps) : "memory");
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int col = nt * 8 + 2 * t4 + x;
+        float M = sm_m[0][col];
+#pragma unroll
+        for (int i = 1; i < kAttWarps; ++i) M = fmaxf(M, sm_m[i][col]);
+        const float f = exp2_fast(m[nt][x] - M);
+        float* dst = red + (w * 8 * NT + col) * S::RS + 8 * g;
+#pragma unroll
+        for (int h = 0; h < NG; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float2*>(dst + 64 * h + 2 * i) = make_float2(o[nt][h][i][x] * f, o[nt][h][i][x + 2] * f);
+      }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kAttWarps) : "memory");
+    const bool whole = run.t0 == 0 && run.t1 == run.nt;
+    const size_t slot = 2 * (size_t)blockIdx.x + (run.pos == lo ? 0 : 1);
+    for (int x = tid; x < CT * HD / 2; x += 32 * kAttWarps) {
+      const int c = x / (HD / 2), d = x % (HD / 2) * 2;
+      float M = kLow, l_sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kAttWarps; ++i) M = fmaxf(M, sm_m[i][c]);
+      float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kAttWarps; ++i) {
+        l_sum += sm_l[i][c] * exp2_fast(sm_m[i][c] - M);
+        const float2 y = *reinterpret_cast<const float2*>(red + (i * 8 * NT + c) * S::RS + d);
+        v.x += y.x, v.y += y.y;
+        if constexpr (PACK) {
+          const float2 z = *reinterpret_cast<const float2*>(red + (i * 8 * NT + c + 4) * S::RS + d);
+          v.x += z.x, v.y += z.y;
+        }
+      }
+      if (give_up) l_sum = v.x = v.y = NAN;
+      const int col = j * CT + c;
+      if (col >= p.cols) continue;
+      if (whole) {
+        const int row = col / p.gqa, hd = run.head * p.gqa + col - row * p.gqa;
+        const float f = l_sum == 0.f ? 0.f : kDown / l_sum;
+        T* dst = reinterpret_cast<T*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row + hd * p.out.head + d;
+        if constexpr (S::F32) *reinterpret_cast<float2*>(dst) = make_float2(v.x * f, v.y * f);
+        else *reinterpret_cast<uint32_t*>(dst) = pack2(v.x * f, v.y * f);
+        if (p.lse && d == 0)
+          p.lse[((size_t)seq * p.a.rows + row) * p.n_heads + hd] =
+              l_sum == 0.f ? -INFINITY : (M + log2f(l_sum)) * 0.69314718055994530942f;
+      } else {
+        float* dst = p.part + (slot * CT + c) * (HD + 4);
+        *reinterpret_cast<float2*>(dst + d) = v;
+        if (d == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(M, l_sum);
+      }
+    }
+    if (tid == 0 && run.t0 == 0)
+      p.item[(size_t)run.e * p.a.n_kv_heads + run.head] = make_longlong2(whole ? -1 : run.pos, blockIdx.x);
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kAttWarps) : "memory");
+    run.pos += run.t1 - run.t0;
+  }
+}
+
+// Items cut between blocks: block (item, column) joins the partial results in
+// the blocks' order, each warp every NW-th of them with a running maximum, the
+// warps at the end.  Items without a tile (nothing seen) get zeros here.
+template <int HD, class T>
+__global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArgs p, int CT, int G) {
+  constexpr int V = HD / 32;  // dimensions of a lane
+  __shared__ float red[16][HD], red_m[16], red_l[16];
+  const int e = blockIdx.x / p.a.n_kv_heads, head = blockIdx.x - e * p.a.n_kv_heads;
+  const int seq = e / p.n_ctiles, j = e - seq * p.n_ctiles;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, NW = blockDim.x >> 5;
+  const int nt = tiles_of(p, e, CT);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const longlong2 it = nt ? p.item[blockIdx.x] : make_longlong2(0, 0);
+  const long long total = *p.total;
+  if (nt && (it.x < 0 || it.y < 0 || it.y >= G)) return;
+  for (int c = blockIdx.y; c < CT && j * CT + c < p.cols; c += gridDim.y) {
+    float m = kLow, l = 0.f, o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = 0.f;
+    if (nt) {
+#pragma unroll 4
+      for (long long b = it.y + w; total * b / G < it.x + nt; b += NW) {
+        const long long lo = total * b / G;
+        if (b >= G) break;
+        if (lo == total * (b + 1) / G) continue;  // a block without tiles
+        const float* src = p.part + ((2 * b + (lo >= it.x ? 0 : 1)) * CT + c) * (HD + 4);
+        const float2 ml = *reinterpret_cast<const float2*>(src + HD);
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = src[lane * V + i];
+        const float M = fmaxf(m, ml.x), f0 = exp2_fast(m - M), f1 = exp2_fast(ml.x - M);
+        m = M;
+        l = l * f0 + ml.y * f1;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = o[i] * f0 + v[i] * f1;
+      }
+    }
+    __syncthreads();
+    if (lane == 0) {
+      red_m[w] = m;
+      red_l[w] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) red[w][lane * V + i] = o[i];
+    __syncthreads();
+    const int col = j * CT + c, row = col / p.gqa, hd = head * p.gqa + col - row * p.gqa;
+    for (int d = threadIdx.x; d < HD; d += blockDim.x) {
+      float M = kLow, ls = 0.f, v = 0.f;
+      for (int i = 0; i < NW; ++i) M = fmaxf(M, red_m[i]);
+      for (int i = 0; i < NW; ++i) {
+        const float f = exp2_fast(red_m[i] - M);
+        ls += red_l[i] * f;
+        v += red[i][d] * f;
+      }
+      const float r = ls == 0.f ? 0.f : v * (kDown / ls);
+      (reinterpret_cast<T*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row + hd * p.out.head)[d] = (T)r;
+      if (p.lse && d == 0)
+        p.lse[((size_t)seq * p.a.rows + row) * p.n_heads + hd] =
+            ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994530942f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+struct Plan {
+  const void *main, *join;
+  int id;                    // of the variant
+  int CT, smem, blocks;      // columns of a tile, shared memory and blocks of an SM
+  int n_ctiles, n_entries, items, grid, join_y, join_threads;
+  size_t item_off, part_off, bytes;
+};
+
+template <int HD, class T, int NT, bool PACK>
+void take(Plan* pl) {
+  using S = Shape<HD, T, NT, PACK>;
+  pl->main = reinterpret_cast<const void*>(&k_kv4_attention<HD, T, NT, PACK>);
+  pl->join = reinterpret_cast<const void*>(&k_kv4_join<HD, T>);
+  pl->id = (HD == 64 ? 0 : 8) + (S::F32 ? 4 : 0) + (PACK ? 0 : NT);
+  pl->CT = S::CT;
+  pl->smem = S::SMEM;
+  pl->blocks = S::BLOCKS;
+}
+
+// One column tile where the columns fit it, two from 9 on (a tile of the cache
+// then serves 16 columns); up to 4 bf16 columns share a tile with their low parts.
+template <int HD>
+void take_for(Plan* pl, int cols, int dtype) {
+  if (dtype == MK_F32) cols <= 8 ? take<HD, float, 1, false>(pl) : take<HD, float, 2, false>(pl);
+  else if (cols <= 4) take<HD, __nv_bfloat16, 1, true>(pl);
+  else if (cols <= 8) take<HD, __nv_bfloat16, 1, false>(pl);
+  else take<HD, __nv_bfloat16, 2, false>(pl);
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 152;
+  }
+  return n;
+}
+
+// Variant, grid and workspace of a call with rows; false: too many columns.
+bool plan_of(const mk_kv4_cache& c, int n_heads, int dtype, Plan* pl) {
+  const long long cols = (long long)c.rows * (n_heads / c.n_kv_heads);
+  if (cols > INT_MAX / 64) return false;
+  if (c.head_dim == 64) take_for<64>(pl, (int)cols, dtype);
+  else take_for<128>(pl, (int)cols, dtype);
+  const long long ct = (cols + pl->CT - 1) / pl->CT, entries = ct * c.n_seqs, items = entries * c.n_kv_heads;
+  const long long most = 2ll * c.max_pages;  // tiles of an item
+  if (items > INT_MAX / 32 || most * c.n_kv_heads > INT_MAX) return false;
+  pl->n_ctiles = (int)ct;
+  pl->n_entries = (int)entries;
+  pl->items = (int)items;
+  pl->grid = (int)std::min<long long>((long long)pl->blocks * sm_count(), items * most);
+  // an item is joined from about grid / items blocks: as many warps for each column
+  int nw = 2;
+  while (nw < 16 && nw * 2 * items <= pl->grid) nw *= 2;
+  pl->join_threads = 32 * nw;
+  pl->join_y = items < 2048 ? pl->CT : 1;
+  pl->item_off = 16;
+  pl->part_off = pl->item_off + (size_t)items * sizeof(longlong2);
+  pl->bytes = pl->part_off + 2 * (size_t)pl->grid * pl->CT * (c.head_dim + 4) * sizeof(float);
+  return true;
+}
+
+// The kernels take more shared memory than the default: asked for once per device.
+cudaError_t allow_smem(const Plan& pl) {
+  static std::atomic<uint32_t> done[64];  // variants, by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done[dev].load() >> pl.id & 1u)) return cudaSuccess;
+  e = cudaFuncSetAttribute(pl.main, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
+  if (e == cudaSuccess && dev < 64) done[dev].fetch_or(1u << pl.id);
+  return e;
+}
+
+int check_attention(const mk_kv4_cache* c, int n_heads, int dtype, bool* empty) {
+  if (int r = kv4_check_cache(c, empty)) return r;
+  if (n_heads < 1 || n_heads % c->n_kv_heads || n_heads > 4096)
+    return host_fail(MK_ERR_INVALID_ARG, "n_heads must be a multiple of n_kv_heads, at most 4096");
+  if (dtype != MK_F32 && dtype != MK_BF16) return host_fail(MK_ERR_INVALID_ARG, "dtype must be MK_F32 or MK_BF16");
+  return MK_OK;
+}
+
+}  // namespace
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" MK_API size_t mk_kv4_attention_bytes(const mk_kv4_cache* c, int32_t n_heads, int32_t dtype) {
+  bool empty = false;
+  Plan pl;
+  if (check_attention(c, n_heads, dtype, &empty) || empty || !plan_of(*c, n_heads, dtype, &pl)) return 0;
+  return pl.bytes;
+}
+
+extern "C" MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, const mk_kv4_rows* q, int32_t dtype,
+                                       float scale, const mk_kv4_rows* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  host_clear_error();
+  bool empty = false;
+  if (int r = check_attention(c, n_heads, dtype, &empty)) return r;
+  if (!(scale > -1e18f && scale < 1e18f)) return host_fail(MK_ERR_INVALID_ARG, "scale must lie within +-1e18");
+  if (empty) return MK_OK;
+  if (int r = kv4_check_rows(q, dtype, "q")) return r;
+  if (int r = kv4_check_rows(out, dtype, "out")) return r;
+  Plan pl;
+  if (!plan_of(*c, n_heads, dtype, &pl))
+    return host_fail(MK_ERR_INVALID_ARG, "n_seqs x rows x n_heads or max_pages x n_kv_heads is too large");
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < pl.bytes)
+    return host_fail(MK_ERR_INVALID_ARG, "workspace is NULL, not 16-byte aligned or smaller than mk_kv4_attention_bytes");
+  AttArgs p;
+  p.a = kv4_args(*c);
+  p.q = kv4_rows(*q);
+  p.out = kv4_rows(*out);
+  p.lse = lse;
+  p.c = (float)((double)scale * 1.4426950408889634 * (double)kDown);
+  p.n_heads = n_heads;
+  p.gqa = n_heads / c->n_kv_heads;
+  p.cols = c->rows * p.gqa;
+  p.n_ctiles = pl.n_ctiles;
+  p.n_entries = pl.n_entries;
+  char* ws = static_cast<char*>(workspace);
+  p.total = reinterpret_cast<long long*>(ws);
+  p.item = reinterpret_cast<longlong2*>(ws + pl.item_off);
+  p.part = reinterpret_cast<float*>(ws + pl.part_off);
+  cudaError_t e = allow_smem(pl);
+  if (e == cudaSuccess) {
+    void* args[] = {&p};
+    e = cudaLaunchKernel(pl.main, dim3(pl.grid), dim3(kAttThreads), args, pl.smem, (cudaStream_t)stream);
+  }
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(pl.items, pl.join_y);
+    cfg.blockDim = dim3(pl.join_threads);
+    cfg.stream = (cudaStream_t)stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    void* args[] = {&p, &pl.CT, &pl.grid};
+    e = cudaLaunchKernelExC(&cfg, pl.join, args);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return host_fail(MK_ERR_CUDA, (std::string("kv4 attention: ") + cudaGetErrorString(e)).c_str());
+  }
+  return MK_OK;
+}

@@ -13,7 +13,7 @@ def record(hd):
 
 def quantise(x):
     """Codes (int64, sign in bit 3) [..., hd] and scales (bfloat16) [..., hd / 64]."""
-    y = x.float().double().reshape(*x.shape[:-1], -1, GROUP)
+    y = x.float().double().reshape(*x.shape[:-1], x.shape[-1] // GROUP, GROUP)
     top = y.abs().amax(-1, keepdim=True)
     bad = ~torch.isfinite(y).all(-1, keepdim=True)
     # the definition divides in fp32; the fp64 quotient rounded to fp32 is that division
@@ -29,7 +29,7 @@ def quantise(x):
 def values(code, scale):
     """What codes and scales stand for, float64."""
     v = (code & 7).double() * (1 - 2 * ((code >> 3) & 1).double())
-    return (v.reshape(*v.shape[:-1], -1, GROUP) * scale.double().unsqueeze(-1)).reshape(v.shape)
+    return (v.reshape(*v.shape[:-1], v.shape[-1] // GROUP, GROUP) * scale.double().unsqueeze(-1)).reshape(v.shape)
 
 
 def put(pool, hd, page, slot, head, kv, code, scale):

@@ -142,7 +142,7 @@ def check(q, pool, table, lengths, n_new=None, scale=None, out=None, lse=None, l
             assert out[i, r].abs().max() == 0 and (lse[i, r] == -math.inf).all(), (i, r)
         if lo >= nn:
             continue
-        k, v = R.cache_values(pool, hd, table[i, :-(-ln // R.PAGE)].long().clamp(min=0), ln)
+        k, v = R.cache_values(pool, hd, table[i, :-(-ln // R.PAGE)].long().clamp(0, pool.shape[0] - 1), ln)
         lost = None if left_out is None else left_out[i]
         o, l, A, D = R.attend(q[i, lo:nn], k if lost is None else k.nan_to_num(), v if lost is None else v.nan_to_num(),
                               ln - nn + lo, sc, lost)

@@ -66,9 +66,15 @@ def test_rows_and_types_are_refused(lib):
         assert code(L.mk_kv4_attention, c, 2, rows(), dt, 1.0, rows(), None, 0x8000, 1 << 40) == inv
     for heads in (0, 3, -2, 8192):
         assert code(L.mk_kv4_attention, c, heads, rows(), L.MK_BF16, 1.0, rows(), None, 0x8000, 1 << 40) == inv
-    for scale in (float("inf"), float("nan"), -float("inf")):
+    for scale in (float("inf"), float("nan"), -float("inf"), 1e18, -2e30):
         assert code(L.mk_kv4_attention, c, 2, rows(), L.MK_BF16, scale, rows(), None, 0x8000, 1 << 40) == inv
     assert code(L.mk_kv4_store, None, rows(), rows(), L.MK_BF16) == inv
+    # a workspace that is missing, misaligned or too small
+    need = L.mk_kv4_attention_bytes(c, 2, L.MK_BF16)
+    assert need > 0
+    for ws, n in ((0, need), (0x8008, need), (0x8000, need - 1)):
+        assert code(L.mk_kv4_attention, c, 2, rows(), L.MK_BF16, 1.0, rows(), None, ws, n) == inv
+        assert "workspace" in L.mk_last_error()
 
 
 def test_calls_without_rows_launch_nothing(lib):
