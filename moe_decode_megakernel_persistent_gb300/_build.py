@@ -1,4 +1,5 @@
-"""In-tree build of libmk.so (the C-ABI library) with nvcc for sm_103a.
+"""In-tree build of libmk.so (the C-ABI library) with nvcc for sm_103a, and of
+the Python module _torch (tensor calls on it) with the host compiler.
 
 The translation units compile in parallel (the decode kernel's file once
 per group of its instantiations, MK_KERNEL_PART 0..3); the shared object
@@ -17,6 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmk.so")
+MODULE = os.path.join(PKG, "_torch.so")
 BUILD = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -42,10 +44,26 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MODULE):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _module_commands(obj: str, out: str) -> list:
+    """The host compiler's two commands for the Python module: against the
+    installed torch, this interpreter and libmk.so next to it."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    cxx, cuda = os.environ.get("CXX", "g++"), os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [f"-I{d}" for d in (*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE)]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return [[cxx, "-O2", "-std=c++17", "-fPIC", abi, *inc, "-c", os.path.join(CSRC, "mk_torch.cpp"), "-o", obj],
+            [cxx, "-shared", obj, "-o", out, "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + libs,
+             "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -69,8 +87,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    def run(cmd, what):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{what} failed:\n{r.stderr[-6000:]}")
+
+    mod_tmp = MODULE + ".tmp"
+    mod_compile, mod_link = _module_commands(os.path.join(BUILD, "mk_torch.o"), mod_tmp)
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        module = ex.submit(run, mod_compile, "the Python module's compilation")
         objs = list(ex.map(compile_one, SOURCES))
+        module.result()
     tmp = LIB + ".tmp"
     # cuBLAS (the chunked prefill's GEMMs) is found through the toolkit's
     # library directory
@@ -81,6 +108,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIB)
+    run(mod_link, "the Python module's link")
+    os.replace(mod_tmp, MODULE)
     return LIB
 
 

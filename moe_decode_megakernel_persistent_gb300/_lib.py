@@ -110,14 +110,12 @@ SIGNATURES = {
                                         C.POINTER(C.c_int32), C.POINTER(C.c_int32), C.c_int32,
                                         C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
     "mk_kv4_page_bytes": (C.c_size_t, [C.c_int32, C.c_int32]),
-    "mk_kv4_store": (C.c_int, [C.POINTER(mk_kv4_cache), C.POINTER(mk_kv4_rows), C.POINTER(mk_kv4_rows),
-                               C.c_int32, C.c_void_p]),
-    "mk_kv4_load": (C.c_int, [C.POINTER(mk_kv4_cache), C.POINTER(mk_kv4_rows), C.POINTER(mk_kv4_rows),
-                              C.c_int32, C.c_void_p]),
-    "mk_kv4_attention": (C.c_int, [C.POINTER(mk_kv4_cache), C.c_int32, C.POINTER(mk_kv4_rows), C.c_int32,
-                                   C.c_float, C.POINTER(mk_kv4_rows), C.c_void_p, C.c_void_p, C.c_size_t,
-                                   C.c_void_p]),
-    "mk_kv4_attention_bytes": (C.c_size_t, [C.POINTER(mk_kv4_cache), C.c_int32, C.c_int32]),
+    # the structures by reference, or their bytes
+    "mk_kv4_store": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p]),
+    "mk_kv4_load": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p]),
+    "mk_kv4_attention": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_float, C.c_void_p,
+                                   C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "mk_kv4_attention_bytes": (C.c_size_t, [C.c_void_p, C.c_int32, C.c_int32]),
     "mk_page_copy": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_size_t, C.c_void_p,
                                C.c_void_p, C.c_int32, C.c_void_p]),
     "mk_static_bytes": (C.c_int, [C.POINTER(mk_model_desc), C.c_int32, C.POINTER(C.c_int64),
@@ -125,6 +123,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_module = None
 
 
 def load(path: str = LIB_PATH):
@@ -142,6 +141,19 @@ def load(path: str = LIB_PATH):
         f.argtypes = args
     _lib = lib
     return lib
+
+
+def torch_module():
+    """The module _torch (csrc/mk_torch.cpp): the tensor calls of kv4 and pages."""
+    global _module
+    if _module is None:
+        load()
+        import torch  # noqa: F401  (the module is linked against its libraries)
+
+        from . import _torch
+        _torch.set_error(MKError)
+        _module = _torch
+    return _module
 
 
 def _check(code: int):
@@ -268,29 +280,36 @@ def mk_kv4_page_bytes(n_kv_heads: int, head_dim: int) -> int:
     return int(load().mk_kv4_page_bytes(n_kv_heads, head_dim))
 
 
+def _ref(x):
+    return None if x is None else C.byref(x)
+
+
 def mk_kv4_store(cache: mk_kv4_cache, k: mk_kv4_rows, v: mk_kv4_rows, dtype: int, stream: int = 0):
-    _check(load().mk_kv4_store(cache, k, v, dtype, stream))
+    _check(load().mk_kv4_store(_ref(cache), _ref(k), _ref(v), dtype, stream))
 
 
 def mk_kv4_load(cache: mk_kv4_cache, k: mk_kv4_rows, v: mk_kv4_rows, dtype: int, stream: int = 0):
-    _check(load().mk_kv4_load(cache, k, v, dtype, stream))
+    _check(load().mk_kv4_load(_ref(cache), _ref(k), _ref(v), dtype, stream))
 
 
 def mk_kv4_attention(cache: mk_kv4_cache, n_heads: int, q: mk_kv4_rows, dtype: int, scale: float,
                      out: mk_kv4_rows, lse_dev: int | None, workspace_dev: int, workspace_bytes: int,
                      stream: int = 0):
-    _check(load().mk_kv4_attention(cache, n_heads, q, dtype, scale, out, lse_dev, workspace_dev,
+    _check(load().mk_kv4_attention(_ref(cache), n_heads, _ref(q), dtype, scale, _ref(out), lse_dev, workspace_dev,
                                    workspace_bytes, stream))
 
 
 def mk_kv4_attention_bytes(cache: mk_kv4_cache, n_heads: int, dtype: int) -> int:
-    return int(load().mk_kv4_attention_bytes(cache, n_heads, dtype))
+    return int(load().mk_kv4_attention_bytes(_ref(cache), n_heads, dtype))
 
 
 def mk_page_copy(pool_dev: int, n_layers: int, n_pages: int, page_bytes: int, src, dst, stream: int = 0):
     """src, dst: host lists of page indices of the same length."""
-    _check(load().mk_page_copy(pool_dev, n_layers, n_pages, page_bytes, _i32(src), _i32(dst, len(src)),
-                               len(src), stream))
+    n = len(src)
+    if len(dst) != n:
+        raise ValueError(f"expected {n} values, got {len(dst)}")
+    kind = C.c_int32 * n
+    _check(load().mk_page_copy(pool_dev, n_layers, n_pages, page_bytes, kind(*src), kind(*dst), n, stream))
 
 
 def mk_last_error() -> str:

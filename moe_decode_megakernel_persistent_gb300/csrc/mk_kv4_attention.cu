@@ -8,32 +8,35 @@
 // multiplies the weight instead (one weight per group), so neither K nor V is
 // ever formed: tensor cores (mma.sync m16n8k16) take the codes as they are.
 //
-// A code becomes a bf16 operand without arithmetic.  The nibble of a byte,
-// moved to bits 15 (sign) and 6..4 (magnitude) of a half word, is the bf16
-// subnormal +-m 2^-129, exactly.  One byte permutation doubles two bytes into
-// the halves of a word (two positions for V, two dimensions for K), one mask
-// takes the high nibbles and one shift and mask the low ones: 1 instruction a
-// value (the magic-number form takes 1.5).  The other operand carries 2^64 (q,
-// or the weights), and the fp32 results 2^-65: they stay far from fp32's ends.
-//
-// Roundings to fewer bits: a bf16 q is exact; an fp32 q is split into three bf16
-// parts (24 bits).  The weights times V's scales are split into two bf16 parts
-// for bf16 rows (16 bits: 2^-17 of a weight, where the output itself is rounded to
-// 2^-9) and three for fp32 rows.  Everything else is fp32.
+// A code becomes an operand without arithmetic.  The nibble of a byte, moved to
+// bits 15 (sign) and 6..4 (magnitude) of a half word, is the subnormal
+// +-m 2^-129 of bf16 and +-m 2^-20 of fp16, exactly.  One byte permutation
+// doubles two bytes into the halves of a word (two positions for V, two
+// dimensions for K), one mask takes the high nibbles and one shift and mask the
+// low ones: 1 instruction a value (the magic-number form takes 1.5).
+//   q . code runs in bf16: q carries 2^64, so that the products (2^-65) stay far
+// from fp32's ends whatever q's size.  A bf16 q is exact; an fp32 q is split into
+// three bf16 parts (24 bits).
+//   weight x V code runs in fp16: the weight (at most 2^8, see below) times V's
+// scale is normalised by a power of two that follows the largest scale the warp
+// has met, to at most 2^14; fp16 then keeps 11 bits over 28 binades below it and
+// the weight is rounded by 2^-12 at most, where the output is rounded to 2^-9.  For
+// fp32 rows it is split into two parts (22 bits).
+// Everything else is fp32.
 //
 // Layout.  K is the mma's A operand (16 positions x 16 dimensions) and q its B
 // operand, so that the query columns of one kv head (rows x heads of the group)
-// fill tiles of 8 columns; a step of 4 heads with one row takes one tile whose
-// columns 4..7 carry the weights' low parts.  The weights come out transposed
-// for the second product (V^T x weights^T) and turn with movmatrix.
+// fill tiles of 8 columns and the 4 heads of a single row cost one.  The weights
+// come out transposed for the second product (V^T x weights^T) and turn with
+// movmatrix.
 //
 // Work.  The tiles of 64 positions of all (sequence, column tile, kv head)
 // items are laid end to end and cut into equal runs, one for each block, from
 // the lengths on the device: a ragged batch costs what its sum costs, and a
-// captured graph follows the lengths.  A warp streams the block's tiles (one
-// bulk copy of 8.5 KB each) through a shared-memory ring; four warps take 16
-// positions of each tile, with running maxima of their own (moved only when a
-// score passes them by 2^8) and one merge at the end of an item.  An item cut
+// captured graph follows the lengths.  A block's tiles stream (one bulk copy of
+// 8.5 KB each) through a shared-memory ring, refilled by its warps in turn; each
+// warp takes 16 positions of a tile, with running maxima of its own (moved only
+// when a score passes them by 2^8) and one merge at the end of an item.  An item cut
 // between blocks is joined by a second kernel, launched so that its start
 // overlaps the first one's end.
 #include <algorithm>
@@ -43,19 +46,20 @@
 #include <string>
 #include <type_traits>
 
+#include <cuda_fp16.h>
+
 #include "mk_kv4.cuh"
 
 namespace mk {
 namespace {
 
-constexpr int kAttWarps = 4;                       // 16 positions of a tile each
-constexpr int kAttThreads = 32 * (kAttWarps + 1);  // and the streaming warp
-constexpr int kRing = 4;                           // tiles in flight
 constexpr uint64_t kWaitNs = 1000000000ull;        // bound of every wait
+constexpr int kList = 256;                         // steps whose addresses a block looks up at a time
 constexpr float kLow = -1e30f;                     // running maximum of a column that has seen nothing
 constexpr float kLazy = 8.f;                       // a maximum moves when a score passes it by this (log2)
-constexpr float kUp = 18446744073709551616.f;      // 2^64, carried by the B operands
-constexpr float kDown = 36893488147419103232.f;    // 2^65 = 2^129 / 2^64, taken out of the results
+constexpr float kUp = 18446744073709551616.f;      // 2^64, carried by q
+constexpr double kDown = 36893488147419103232.0;   // 2^65 = 2^129 / 2^64, taken out of the scores
+constexpr float kCode = 1048576.f;                 // 2^20, taken out of the second product
 
 struct AttArgs {
   Kv4Args a;
@@ -103,22 +107,29 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 }
 // Wait for a phase; gives up after kWaitNs (and at once when another warp of the
 // block has): then *give_up is set and the block runs to its end without data.
-__device__ __noinline__ void bar_wait_long(uint32_t bar, uint32_t parity, volatile int* give_up, int32_t* status) {
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* give_up, int32_t* status) {
   const uint64_t t0 = now_ns();
   for (uint32_t i = 0;; ++i) {
-    if (bar_try(bar, parity) || *give_up) return;
+    if (bar_try(bar, parity)) return true;
+    if (*give_up) return false;
     if ((i & 15u) == 15u && now_ns() - t0 > kWaitNs) {
       *give_up = 1;
       if (status) atomicCAS(status, 0, MK_ERR_BARRIER_TIMEOUT);
-      return;
+      return false;
     }
   }
 }
-__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile int* give_up, int32_t* status) {
-  if (!bar_try(bar, parity)) bar_wait_long(bar, parity, give_up, status);
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* give_up, int32_t* status) {
+  return bar_try(bar, parity) || bar_wait_long(bar, parity, give_up, status);
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -134,6 +145,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {  // bf16x2
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
   return y;
 }
+__device__ __forceinline__ uint32_t pack2h(float lo, float hi) {  // f16x2
+  uint32_t y;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  return y;
+}
+__device__ __forceinline__ float low_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)x)); }
+__device__ __forceinline__ float high_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x >> 16))); }
 __device__ __forceinline__ float low_f(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float high_f(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -143,26 +161,26 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 constexpr uint32_t kNib = 0x80708070u;
 
-// Column tile j of sequence s: how many tiles of positions its columns see.
-__device__ __forceinline__ int tiles_of(const AttArgs& p, int e, int CT) {
+// Column tile j of sequence s: how many steps of SP positions its columns see.
+__device__ __forceinline__ int tiles_of(const AttArgs& p, int e, int CT, int SP) {
   const int s = e / p.n_ctiles, j = e - s * p.n_ctiles;
   int len, nn;
   seq_extent(p.a, s, len, nn);
   if (j * CT / p.gqa >= nn) return 0;                                     // its rows are padding
   const int r = min((min((j + 1) * CT, p.cols) - 1) / p.gqa, nn - 1);     // its last row
   const int end = len - nn + r + 1;
-  return end <= 0 ? 0 : (end + kTile - 1) / kTile;
+  return end <= 0 ? 0 : (end + SP - 1) / SP;
 }
 
 // The runs of a block: its tiles [pos, hi) cut at items.
 struct Runs {
   long long pos, hi, base;  // base: the first tile of entry e
   int e, nt, head, t0, t1;
-  __device__ __forceinline__ bool next(const AttArgs& p, int CT) {  // the run at pos; false: none is left
+  __device__ __forceinline__ bool next(const AttArgs& p, int CT, int SP) {  // the run at pos; false: none is left
     if (pos >= hi) return false;
     for (;; ++e) {
       if (e >= p.n_entries) return false;  // lengths that change under the call
-      nt = tiles_of(p, e, CT);
+      nt = tiles_of(p, e, CT, SP);
       const long long n = (long long)nt * p.a.n_kv_heads;
       if (pos < base + n) break;
       base += n;
@@ -175,47 +193,51 @@ struct Runs {
   }
 };
 
-template <int HD, class T, int NT, bool PACK>
+// NT column tiles; W warps of U units of 16 positions in each step; R steps in
+// the ring; B blocks of an SM.
+template <int HD, class T, int NT, int W, int U, int R, int B>
 struct Shape {
-  static_assert(!PACK || (NT == 1 && !std::is_same<T, float>::value), "packed columns are for bf16");
   static constexpr bool F32 = std::is_same<T, float>::value;
-  static constexpr int CT = PACK ? 4 : 8 * NT;   // columns of a tile
+  static constexpr int CT = 8 * NT;              // columns of a tile
   static constexpr int NG = HD / kGroup;
   static constexpr int QP = F32 ? 3 : 1;         // parts of q
-  static constexpr int WP = F32 ? 3 : (PACK ? 1 : 2);  // parts of the weights (packed: both in one operand)
+  static constexpr int WP = F32 ? 2 : 1;         // parts of the weights
+  static constexpr bool QS = NT > 2;             // q's fragments in shared memory, to leave registers to the sums
   static constexpr int RS = HD + 2;              // floats of a column in the reduction buffer
-  static constexpr int RED = kAttWarps * 8 * NT * RS * 4;
-  static constexpr int SMEM = kRing * Tile<HD>::BYTES + RED;
-  // blocks of an SM: by registers (two column tiles, or three parts, need more) and shared memory
-  static constexpr int BLOCKS = NT == 1 ? (F32 ? 3 : 4) : (F32 ? 2 : 3);
+  static constexpr int SP = 16 * W * U;          // positions of a step: 64 or 128, within a page
+  static constexpr int BYTES = SP / kTile * Tile<HD>::BYTES;
+  static constexpr int RED = W * CT * RS * 4;
+  static constexpr int QB = QS ? NT * NG * 4 * 32 * 8 : 0;
+  static constexpr int SMEM = R * BYTES + RED + QB;
 };
 
-template <int HD, class T, int NT, bool PACK>
-__global__ void __launch_bounds__(kAttThreads, (Shape<HD, T, NT, PACK>::BLOCKS))
-    k_kv4_attention(const __grid_constant__ AttArgs p) {
-  using S = Shape<HD, T, NT, PACK>;
+template <int HD, class T, int NT, int W, int U, int R, int B>
+__global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_constant__ AttArgs p) {
+  using S = Shape<HD, T, NT, W, U, R, B>;
   using L = Tile<HD>;
-  constexpr int NG = S::NG, CT = S::CT;
+  constexpr int NG = S::NG, CT = S::CT, SP = S::SP, NTHR = 32 * W;
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ __align__(8) uint64_t full[kRing], empty[kRing];
-  __shared__ int loaded[kRing];
-  __shared__ float sm_m[kAttWarps][8 * NT], sm_l[kAttWarps][8 * NT];
+  __shared__ __align__(8) uint64_t full[R], empty[R];
+  __shared__ unsigned long long list[kList];  // where the block's next steps lie (0: a page outside the pool)
+  __shared__ uint32_t issued[R];              // 1 + the last step copied into each stage
+  __shared__ float sm_m[W][CT], sm_l[W][CT];
   __shared__ long long s_lo, s_hi, s_base;
   __shared__ int s_entry;
   __shared__ volatile int give_up;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
+    for (int i = 0; i < R; ++i) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[i])) : "memory");
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&empty[i])), "n"(kAttWarps) : "memory");
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&empty[i])), "n"(W) : "memory");
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int i = 0; i < R; ++i) issued[i] = 0;
     give_up = 0;
   }
   if (w == 0) {  // this block's share
     long long total = 0;
-    for (int e = lane; e < p.n_entries; e += 32) total += tiles_of(p, e, CT);
+    for (int e = lane; e < p.n_entries; e += 32) total += tiles_of(p, e, CT, SP);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     total *= p.a.n_kv_heads;
@@ -225,7 +247,7 @@ __global__ void __launch_bounds__(kAttThreads, (Shape<HD, T, NT, PACK>::BLOCKS))
     int entry = 0;
     if (lo < hi) {
       for (int e0 = 0; e0 < p.n_entries; e0 += 32) {
-        const long long n = e0 + lane < p.n_entries ? (long long)tiles_of(p, e0 + lane, CT) * p.a.n_kv_heads : 0;
+        const long long n = e0 + lane < p.n_entries ? (long long)tiles_of(p, e0 + lane, CT, SP) * p.a.n_kv_heads : 0;
         long long incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -256,56 +278,53 @@ __global__ void __launch_bounds__(kAttThreads, (Shape<HD, T, NT, PACK>::BLOCKS))
   run.base = s_base;
   run.e = s_entry;
   const long long lo = s_lo;
-  uint32_t k = 0;  // tiles streamed / used so far
-
-  if (w == kAttWarps) {  // ---- the streaming warp
-    uint32_t issued = 0;
-    while (run.next(p, CT)) {
-      const int seq = run.e / p.n_ctiles;
-      for (int t = run.t0; t < run.t1;) {
-        const int g0 = t / 2;  // pages of the run, 32 at a time
-        const int page = g0 + lane <= (run.t1 - 1) / 2 ? page_of(p.a, seq, (g0 + lane) * kPageTokens) : -1;
-        for (; t < run.t1 && t / 2 < g0 + 32; ++t, ++k) {
-          const int pg = __shfl_sync(0xffffffffu, page, t / 2 - g0), st = k % kRing;
-          if (k >= kRing) bar_wait(smem_addr(&empty[st]), (k / kRing - 1) & 1, &give_up, p.a.status);
-          __syncwarp();
-          if (lane == 0 && !give_up) {
-            const uint32_t bar = smem_addr(&full[st]);
-            loaded[st] = pg >= 0;
-            if (pg >= 0) {
-              asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "n"(L::BYTES) : "memory");
-              asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                               smem_addr(sm + st * L::BYTES)),
-                           "l"(tile_of<HD>(p.a, pg, run.head, t * kTile)), "n"(L::BYTES), "r"(bar)
-                           : "memory");
-            }
-            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-            issued = k + 1;
-          }
-          __syncwarp();
-        }
-      }
-      run.pos += run.t1 - run.t0;
+  const uint32_t n_steps = (uint32_t)(s_hi - lo);
+  uint32_t k = 0;  // steps done
+  // Address of the block's step i, looked up by one thread (all of a window at once).
+  auto look_up = [&](uint32_t i) {
+    Runs r;
+    r.pos = lo + i;
+    r.hi = s_hi;
+    r.base = s_base;
+    r.e = s_entry;
+    if (!r.next(p, CT, SP)) return;
+    const int pg = page_of(p.a, r.e / p.n_ctiles, r.t0 * SP);
+    list[i % kList] = pg < 0 ? 0 : (unsigned long long)tile_of<HD>(p.a, pg, r.head, r.t0 * SP);
+  };
+  // Copy step i into its stage, which is free; one thread.
+  auto copy_step = [&](uint32_t i) {
+    const int st = i % R;
+    const uint32_t bar = smem_addr(&full[st]);
+    const unsigned long long src = list[i % kList];
+    issued[st] = src ? i + 1 : 0;
+    if (src) {
+      asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "n"(S::BYTES) : "memory");
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                       smem_addr(sm + st * S::BYTES)),
+                   "l"(src), "n"(S::BYTES), "r"(bar)
+                   : "memory");
     }
-    if (lane == 0 && give_up) {  // the copies in flight land before the block ends
-      int none = 0;
-      for (uint32_t i = issued > kRing ? issued - kRing : 0; i < issued; ++i)
-        bar_wait_long(smem_addr(&full[i % kRing]), (i / kRing) & 1, &none, nullptr);
-    }
-    return;
-  }
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+  };
+  for (uint32_t i = tid; i < kList; i += NTHR) look_up(i);
+  __syncthreads();
+  if (tid == 0)
+    for (uint32_t i = 0; i < R && i < n_steps; ++i) copy_step(i);
+  __syncwarp();
 
-  // ---- the computing warps: lane (g, t) of the mma fragments
+  // lane (g, t) of the mma fragments
   const int g = lane >> 2, t4 = lane & 3;
-  while (run.next(p, CT)) {
+  while (run.next(p, CT, SP)) {
     const int seq = run.e / p.n_ctiles, j = run.e - seq * p.n_ctiles;
     int len, nn;
     seq_extent(p.a, seq, len, nn);
     // the B fragments of q: column nt * 8 + g, dimensions 64 h + 16 t + 8 i + 4 jj + {0, 2 | 1, 3}
-    uint2 qf[S::QP][NT][NG][2][2];
+    uint2 qf[S::QS ? 1 : S::QP][S::QS ? 1 : NT][NG][2][2];
+    uint2* qsm = reinterpret_cast<uint2*>(sm + R * S::BYTES + S::RED);  // [nt][h][i][lane][jj]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int col = j * CT + (PACK ? (g & 3) : nt * 8 + g);
+      if (S::QS && nt % W != w) continue;
+      const int col = j * CT + nt * 8 + g;
       const bool there = col < p.cols;
       const int row = there ? col / p.gqa : 0, hd = there ? col - row * p.gqa : 0;
       const T* src = reinterpret_cast<const T*>(p.q.p) + seq * p.q.seq + row * p.q.row +
@@ -325,27 +344,39 @@ __global__ void __launch_bounds__(kAttThreads, (Shape<HD, T, NT, PACK>::BLOCKS))
               }
             }
             x.x *= kUp, x.y *= kUp, x.z *= kUp, x.w *= kUp;
+            if constexpr (S::QS) {
+              qsm[(((nt * NG + h) * 2 + i) * 32 + lane) * 2 + jj] = make_uint2(pack2(x.x, x.z), pack2(x.y, x.w));
+            } else {
 #pragma unroll
-            for (int q = 0; q < S::QP; ++q) {
-              const uint2 b = make_uint2(pack2(x.x, x.z), pack2(x.y, x.w));
-              qf[q][nt][h][i][jj] = b;
-              if (q + 1 < S::QP) x.x -= low_f(b.x), x.z -= high_f(b.x), x.y -= low_f(b.y), x.w -= high_f(b.y);
+              for (int q = 0; q < S::QP; ++q) {
+                const uint2 b = make_uint2(pack2(x.x, x.z), pack2(x.y, x.w));
+                qf[q][nt][h][i][jj] = b;
+                if (q + 1 < S::QP) x.x -= low_f(b.x), x.z -= high_f(b.x), x.y -= low_f(b.y), x.w -= high_f(b.y);
+              }
             }
           }
     }
-    // positions that this lane's columns see (columns nt * 8 + 2 t, + 1), and what all columns see
-    int lim[NT][2], all = INT_MAX;
+    if constexpr (S::QS) asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
+    // positions that this lane's columns see (columns nt * 8 + 2 t, + 1), what
+    // all columns see and what any does
+    int lim[NT][2], all = INT_MAX, any = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int col = j * CT + (PACK ? ((2 * t4 + x) & 3) : nt * 8 + 2 * t4 + x), row = col / p.gqa;
+        const int col = j * CT + nt * 8 + 2 * t4 + x, row = col / p.gqa;
         lim[nt][x] = col < p.cols && row < nn ? max(0, len - nn + row + 1) : 0;
         if (col < p.cols) all = min(all, lim[nt][x]);
+        any = max(any, lim[nt][x]);
       }
-    all = min(all, __shfl_xor_sync(0xffffffffu, all, 1));
-    all = min(all, __shfl_xor_sync(0xffffffffu, all, 2));
-    float m[NT][2], l[NT][2], o[NT][NG][4][4];
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      all = min(all, __shfl_xor_sync(0xffffffffu, all, d));
+      any = max(any, __shfl_xor_sync(0xffffffffu, any, d));
+    }
+    // running maximum (log2) and sum of each column, the weighted sums, and the
+    // normalisation of V's scales: they are below cap, and enter times vmul = 2^6 / cap
+    float m[NT][2], l[NT][2], o[NT][NG][4][4], cap = 0.f, vmul = 1.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = kLow;
@@ -356,145 +387,205 @@ __global__ void __launch_bounds__(kAttThreads, (Shape<HD, T, NT, PACK>::BLOCKS))
         for (int i = 0; i < 4; ++i) o[nt][h][i][0] = o[nt][h][i][1] = o[nt][h][i][2] = o[nt][h][i][3] = 0.f;
     }
 
-    for (int t = run.t0; t < run.t1; ++t, ++k) {
-      const int st = k % kRing;
-      bar_wait(smem_addr(&full[st]), (k / kRing) & 1, &give_up, p.a.status);
-      const int p0 = t * kTile + 16 * w;  // this warp's first position
-      if (loaded[st] && !give_up) {
-        const uint32_t tile = smem_addr(sm + st * L::BYTES);
-        const uint32_t kr = tile + (16 * w + g) * L::ROW + 8 * t4;
-        float a[NT][NG][4];
+    // 16 positions from p0 on, rows r0.. of a tile (`tile`: the K codes of row r0);
+    // CUT: some column does not see all of them
+    auto unit = [&](uint32_t tile, int r0, int p0, auto cut_) {
+      constexpr bool CUT = decltype(cut_)::value;
+      const uint32_t kr = tile + g * L::ROW + 8 * t4;
+      // scales of positions g and g + 8
+      float ks[2][NG], vs[2][NG];
 #pragma unroll
-        for (int h = 0; h < NG; ++h) {
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t at = tile + L::CODES + (g + 8 * r) * NG * 2 - r0 * (L::ROW - NG * 2);
+        const uint32_t x = NG == 2 ? lds32(at) : lds16(at);
+        uint32_t y = NG == 2 ? lds32(at + L::V) : lds16(at + L::V);
+        if (CUT && p0 + g + 8 * r >= any) y = 0;  // a slot behind the end may hold anything
+        ks[r][0] = low_f(x);
+        vs[r][0] = low_f(y);
+        if constexpr (NG == 2) {
+          ks[r][1] = high_f(x);
+          vs[r][1] = high_f(y);
+        }
+      }
+      // scores without the factor c: element x + 2 r is column 2 t + x, position g + 8 r
+      float v[NT][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) a[nt][h][0] = a[nt][h][1] = a[nt][h][2] = a[nt][h][3] = 0.f;
-          const uint2 u0 = lds64(kr + 32 * h), u1 = lds64(kr + 8 * L::ROW + 32 * h);
+      for (int h = 0; h < NG; ++h) {
+        float a[NT][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+        for (int nt = 0; nt < NT; ++nt) a[nt][0] = a[nt][1] = a[nt][2] = a[nt][3] = 0.f;
+        const uint2 u0 = lds64(kr + 32 * h), u1 = lds64(kr + 8 * L::ROW + 32 * h);
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-              const uint32_t x0 = __byte_perm(i ? u0.y : u0.x, 0, jj ? 0x3322 : 0x1100);
-              const uint32_t x1 = __byte_perm(i ? u1.y : u1.x, 0, jj ? 0x3322 : 0x1100);
+        for (int i = 0; i < 2; ++i) {
+          uint2 qs[NT][2];
+          if constexpr (S::QS) {
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint4 b = *reinterpret_cast<const uint4*>(qsm + (((nt * NG + h) * 2 + i) * 32 + lane) * 2);
+              qs[nt][0] = make_uint2(b.x, b.y);
+              qs[nt][1] = make_uint2(b.z, b.w);
+            }
+          }
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const uint32_t x0 = __byte_perm(i ? u0.y : u0.x, 0, jj ? 0x3322 : 0x1100);
+            const uint32_t x1 = __byte_perm(i ? u1.y : u1.x, 0, jj ? 0x3322 : 0x1100);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (S::QS) {
+                mma_bf16(a[nt], (x0 << 4) & kNib, (x1 << 4) & kNib, x0 & kNib, x1 & kNib, qs[nt][jj]);
+              } else {
 #pragma unroll
                 for (int q = S::QP - 1; q >= 0; --q)
-                  mma16816(a[nt][h], (x0 << 4) & kNib, (x1 << 4) & kNib, x0 & kNib, x1 & kNib, qf[q][nt][h][i][jj]);
+                  mma_bf16(a[nt], (x0 << 4) & kNib, (x1 << 4) & kNib, x0 & kNib, x1 & kNib, qf[q][nt][h][i][jj]);
+              }
             }
-        }
-        // scales of positions g and g + 8
-        float ks[2][NG], vs[2][NG];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint32_t at = tile + L::CODES + (16 * w + g + 8 * r) * NG * 2;
-          const uint32_t x = NG == 2 ? lds32(at) : lds16(at), y = NG == 2 ? lds32(at + L::V) : lds16(at + L::V);
-          ks[r][0] = low_f(x);
-          vs[r][0] = low_f(y) * kUp;
-          if constexpr (NG == 2) {
-            ks[r][1] = high_f(x);
-            vs[r][1] = high_f(y) * kUp;
           }
         }
-        // scores in log2 units: element x + 2 r is column 2 t + x, position g + 8 r
-        float s[NT][4];
-        bool over = false;
-        const bool cut = p0 + 16 > all;  // some column does not see all of these positions
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = a[nt][0][e] * ks[e >> 1][0];
-            if constexpr (NG == 2) v = fmaf(a[nt][1][e], ks[e >> 1][1], v);
-            v *= p.c;
-            if (cut && p0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) v = -INFINITY;
-            s[nt][e] = v;
-            over |= v > m[nt][e & 1] + kLazy;
-          }
-        if (__any_sync(0xffffffffu, over)) {
+          for (int e = 0; e < 4; ++e) v[nt][e] = h ? fmaf(a[nt][e], ks[e >> 1][h], v[nt][e]) : a[nt][e] * ks[e >> 1][h];
+      }
+      // distance to the running maxima; a maximum or the cap that is passed moves
+      float d[NT][4];
+      bool over = false;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              float v = fmaxf(fmaxf(s[nt][x], s[nt][x + 2]), m[nt][x]);
-#pragma unroll
-              for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-              const float f = exp2_fast(m[nt][x] - v);
-              m[nt][x] = v;
-              l[nt][x] *= f;
-#pragma unroll
-              for (int h = 0; h < NG; ++h)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  o[nt][h][i][x] *= f;
-                  o[nt][h][i][x + 2] *= f;
-                }
-            }
+        for (int e = 0; e < 4; ++e) {
+          d[nt][e] = fmaf(v[nt][e], p.c, -m[nt][e & 1]);
+          if (CUT && p0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) d[nt][e] = -INFINITY;
+          over |= d[nt][e] > kLazy;
         }
-        // weights times V's scales, as B fragments
-        uint2 wf[S::WP][NT][NG];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float wt[4];
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            wt[e] = exp2_fast(s[nt][e] - m[nt][e & 1]);
-            l[nt][e & 1] += wt[e];
-          }
+        for (int h = 0; h < NG; ++h) over |= vs[r][h] > cap;
+      if (__any_sync(0xffffffffu, over)) {
+        float top = 0.f;
 #pragma unroll
-          for (int h = 0; h < NG; ++h) {
-            float v[4];
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[e] = wt[e] * vs[e >> 1][h];
-              // a scale behind what the column sees may be anything
-              if (cut && p0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) v[e] = 0.f;
-            }
-            if constexpr (PACK) {
-              // columns 0..3 (lanes t < 2) take the high parts, 4..7 the low parts
-              const uint32_t keep = t4 < 2 ? 0u : 0xFFFFFFFFu;
-              uint32_t b[2];
+          for (int h = 0; h < NG; ++h) top = fmaxf(top, vs[r][h]);
 #pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const uint32_t hi = pack2(v[2 * r], v[2 * r + 1]) & keep;
-                b[r] = turn(pack2(v[2 * r] - low_f(hi), v[2 * r + 1] - high_f(hi)));
-              }
-              wf[0][nt][h] = make_uint2(b[0], b[1]);
-            } else {
-#pragma unroll
-              for (int q = 0; q < S::WP; ++q) {
-                const uint32_t b0 = pack2(v[0], v[1]), b1 = pack2(v[2], v[3]);
-                wf[q][nt][h] = make_uint2(turn(b0), turn(b1));
-                if (q + 1 < S::WP) v[0] -= low_f(b0), v[1] -= high_f(b0), v[2] -= low_f(b1), v[3] -= high_f(b1);
-              }
-            }
-          }
+        for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        float move = 1.f;
+        if (top > cap) {  // the next power of two, and 2^3 of room
+          const int e = min(max((int)(__float_as_uint(top) >> 23) + 4, 8), 254);
+          const float mul = __uint_as_float((uint32_t)(260 - e) << 23);
+          move = mul / vmul;
+          cap = __uint_as_float((uint32_t)e << 23);
+          vmul = mul;
         }
-        // V: positions 2 t, 2 t + 1 and 2 t + 8, 2 t + 9, dimensions 64 h + 8 g + {0..7}
-        const uint32_t vr = tile + L::V + (16 * w + 2 * t4) * L::ROW + 4 * g;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float t = m[nt][x];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (d[nt][x + 2 * r] != -INFINITY) t = fmaxf(t, v[nt][x + 2 * r] * p.c);
+#pragma unroll
+            for (int y = 4; y < 32; y <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, y));
+            const float f = exp2_fast(m[nt][x] - t);
+            m[nt][x] = t;
+            l[nt][x] *= f;
+            const float fo = f * move;
+#pragma unroll
+            for (int h = 0; h < NG; ++h)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[nt][h][i][x] *= fo;
+                o[nt][h][i][x + 2] *= fo;
+              }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (d[nt][x + 2 * r] != -INFINITY) d[nt][x + 2 * r] = fmaf(v[nt][x + 2 * r], p.c, -t);
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int h = 0; h < NG; ++h) vs[r][h] *= vmul;
+      // weights times V's scales, as B fragments
+      uint2 wf[S::WP][NT][NG];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          d[nt][e] = exp2_fast(d[nt][e]);
+          l[nt][e & 1] += d[nt][e];
+        }
 #pragma unroll
         for (int h = 0; h < NG; ++h) {
-          const uint32_t v0 = lds32(vr + 32 * h), v1 = lds32(vr + L::ROW + 32 * h);
-          const uint32_t v8 = lds32(vr + 8 * L::ROW + 32 * h), v9 = lds32(vr + 9 * L::ROW + 32 * h);
+          float x[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t sel = 0x4400u + 0x1111u * i;
-            const uint32_t x = __byte_perm(v0, v1, sel), y = __byte_perm(v8, v9, sel);
+          for (int e = 0; e < 4; ++e) {
+            x[e] = d[nt][e] * vs[e >> 1][h];
+            if (CUT && p0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) x[e] = 0.f;  // whatever the scale there
+          }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if constexpr (S::F32) {  // a tile's terms are summed on their own, then added
-                float f[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int q = 0; q < S::WP; ++q) {
+            const uint32_t b0 = pack2h(x[0], x[1]), b1 = pack2h(x[2], x[3]);
+            wf[q][nt][h] = make_uint2(turn(b0), turn(b1));
+            if (q + 1 < S::WP) x[0] -= low_h(b0), x[1] -= high_h(b0), x[2] -= low_h(b1), x[3] -= high_h(b1);
+          }
+        }
+      }
+      // V: positions 2 t, 2 t + 1 and 2 t + 8, 2 t + 9, dimensions 64 h + 8 g + {0..7}
+      const uint32_t vr = tile + L::V + 2 * t4 * L::ROW + 4 * g;
 #pragma unroll
-                for (int q = S::WP - 1; q >= 0; --q)
-                  mma16816(f, (x << 4) & kNib, x & kNib, (y << 4) & kNib, y & kNib, wf[q][nt][h]);
+      for (int h = 0; h < NG; ++h) {
+        const uint32_t v0 = lds32(vr + 32 * h), v1 = lds32(vr + L::ROW + 32 * h);
+        const uint32_t v8 = lds32(vr + 8 * L::ROW + 32 * h), v9 = lds32(vr + 9 * L::ROW + 32 * h);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[nt][h][i][e] += f[e];
-              } else {
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t sel = 0x4400u + 0x1111u * i;
+          const uint32_t x = __byte_perm(v0, v1, sel), y = __byte_perm(v8, v9, sel);
 #pragma unroll
-                for (int q = 0; q < S::WP; ++q)
-                  mma16816(o[nt][h][i], (x << 4) & kNib, x & kNib, (y << 4) & kNib, y & kNib, wf[q][nt][h]);
-              }
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (S::F32) {  // a tile's terms are summed on their own, then added
+              float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int q = S::WP - 1; q >= 0; --q)
+                mma_f16(f, (x << 4) & kNib, x & kNib, (y << 4) & kNib, y & kNib, wf[q][nt][h]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][h][i][e] += f[e];
+            } else {
+              mma_f16(o[nt][h][i], (x << 4) & kNib, x & kNib, (y << 4) & kNib, y & kNib, wf[0][nt][h]);
             }
           }
+        }
+      }
+    };
+
+#pragma unroll 1
+    for (int t = run.t0; t < run.t1; ++t, ++k) {
+      if (k % (kList / 2) == 0 && k) {  // half of the addresses are used up: the next ones
+        asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
+        for (uint32_t i = tid; i < kList / 2; i += NTHR) look_up(k + kList / 2 + i);
+        asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
+      }
+      // the stage of the last step is refilled as soon as all warps have left it
+      if (k && k - 1 + R < n_steps && w == (int)(k % W)) {
+        const bool free = bar_wait(smem_addr(&empty[(k - 1) % R]), ((k - 1) / R) & 1, &give_up, p.a.status);
+        if (free && lane == 0) copy_step(k - 1 + R);
+        __syncwarp();
+      }
+      const int st = k % R;
+      const bool fine = bar_wait(smem_addr(&full[st]), (k / R) & 1, &give_up, p.a.status);
+      if (fine && issued[st]) {
+        // this warp's first position, its tile and row
+        const int at = 16 * U * w, p0 = t * SP + at, r0 = at % kTile;
+        const uint32_t tile = smem_addr(sm + st * S::BYTES) + at / kTile * L::BYTES + r0 * L::ROW;
+        if (p0 + 16 * U <= all) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) unit(tile + 16 * u * L::ROW, r0 + 16 * u, p0 + 16 * u, std::false_type());
+        } else {
+#pragma unroll 1
+          for (int u = 0; u < U; ++u)
+            if (p0 + 16 * u < any) unit(tile + 16 * u * L::ROW, r0 + 16 * u, p0 + 16 * u, std::true_type());
         }
       }
       __syncwarp();
@@ -502,7 +593,7 @@ __global__ void __launch_bounds__(kAttThreads, (Shape<HD, T, NT, PACK>::BLOCKS))
     }
 
     // ---- the item's end: the four warps' sums joined
-    float* red = reinterpret_cast<float*>(sm + kRing * L::BYTES);
+    float* red = reinterpret_cast<float*>(sm + R * S::BYTES);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -514,7 +605,8 @@ __global__ void __launch_bounds__(kAttThreads, (Shape<HD, T, NT, PACK>::BLOCKS))
           sm_l[w][nt * 8 + 2 * t4 + x] = l[nt][x];
         }
       }
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kAttWarps) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
+    const float undo = kCode / vmul;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -522,40 +614,35 @@ __global__ void __launch_bounds__(kAttThreads, (Shape<HD, T, NT, PACK>::BLOCKS))
         const int col = nt * 8 + 2 * t4 + x;
         float M = sm_m[0][col];
 #pragma unroll
-        for (int i = 1; i < kAttWarps; ++i) M = fmaxf(M, sm_m[i][col]);
-        const float f = exp2_fast(m[nt][x] - M);
-        float* dst = red + (w * 8 * NT + col) * S::RS + 8 * g;
+        for (int i = 1; i < W; ++i) M = fmaxf(M, sm_m[i][col]);
+        const float f = exp2_fast(m[nt][x] - M) * undo;
+        float* dst = red + (w * CT + col) * S::RS + 8 * g;
 #pragma unroll
         for (int h = 0; h < NG; ++h)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<float2*>(dst + 64 * h + 2 * i) = make_float2(o[nt][h][i][x] * f, o[nt][h][i][x + 2] * f);
       }
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kAttWarps) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
     const bool whole = run.t0 == 0 && run.t1 == run.nt;
     const size_t slot = 2 * (size_t)blockIdx.x + (run.pos == lo ? 0 : 1);
-    for (int x = tid; x < CT * HD / 2; x += 32 * kAttWarps) {
+    const int ncol = min(CT, p.cols - j * CT);
+    for (int x = tid; x < ncol * HD / 2; x += NTHR) {
       const int c = x / (HD / 2), d = x % (HD / 2) * 2;
       float M = kLow, l_sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kAttWarps; ++i) M = fmaxf(M, sm_m[i][c]);
+      for (int i = 0; i < W; ++i) M = fmaxf(M, sm_m[i][c]);
       float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < kAttWarps; ++i) {
+      for (int i = 0; i < W; ++i) {
         l_sum += sm_l[i][c] * exp2_fast(sm_m[i][c] - M);
-        const float2 y = *reinterpret_cast<const float2*>(red + (i * 8 * NT + c) * S::RS + d);
+        const float2 y = *reinterpret_cast<const float2*>(red + (i * CT + c) * S::RS + d);
         v.x += y.x, v.y += y.y;
-        if constexpr (PACK) {
-          const float2 z = *reinterpret_cast<const float2*>(red + (i * 8 * NT + c + 4) * S::RS + d);
-          v.x += z.x, v.y += z.y;
-        }
       }
       if (give_up) l_sum = v.x = v.y = NAN;
-      const int col = j * CT + c;
-      if (col >= p.cols) continue;
       if (whole) {
-        const int row = col / p.gqa, hd = run.head * p.gqa + col - row * p.gqa;
-        const float f = l_sum == 0.f ? 0.f : kDown / l_sum;
+        const int col = j * CT + c, row = col / p.gqa, hd = run.head * p.gqa + col - row * p.gqa;
+        const float f = l_sum == 0.f ? 0.f : 1.f / l_sum;
         T* dst = reinterpret_cast<T*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row + hd * p.out.head + d;
         if constexpr (S::F32) *reinterpret_cast<float2*>(dst) = make_float2(v.x * f, v.y * f);
         else *reinterpret_cast<uint32_t*>(dst) = pack2(v.x * f, v.y * f);
@@ -570,8 +657,13 @@ __global__ void __launch_bounds__(kAttThreads, (Shape<HD, T, NT, PACK>::BLOCKS))
     }
     if (tid == 0 && run.t0 == 0)
       p.item[(size_t)run.e * p.a.n_kv_heads + run.head] = make_longlong2(whole ? -1 : run.pos, blockIdx.x);
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kAttWarps) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
     run.pos += run.t1 - run.t0;
+  }
+  if (give_up && tid == 0) {  // copies in flight land before the block ends
+    int none = 0;
+    for (int i = 0; i < R; ++i)
+      if (issued[i]) bar_wait_long(smem_addr(&full[i]), ((issued[i] - 1) / R) & 1, &none, nullptr);
   }
 }
 
@@ -579,13 +671,13 @@ __global__ void __launch_bounds__(kAttThreads, (Shape<HD, T, NT, PACK>::BLOCKS))
 // the blocks' order, each warp every NW-th of them with a running maximum, the
 // warps at the end.  Items without a tile (nothing seen) get zeros here.
 template <int HD, class T>
-__global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArgs p, int CT, int G) {
+__global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArgs p, int CT, int SP, int G) {
   constexpr int V = HD / 32;  // dimensions of a lane
   __shared__ float red[16][HD], red_m[16], red_l[16];
   const int e = blockIdx.x / p.a.n_kv_heads, head = blockIdx.x - e * p.a.n_kv_heads;
   const int seq = e / p.n_ctiles, j = e - seq * p.n_ctiles;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, NW = blockDim.x >> 5;
-  const int nt = tiles_of(p, e, CT);
+  const int nt = tiles_of(p, e, CT, SP);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const longlong2 it = nt ? p.item[blockIdx.x] : make_longlong2(0, 0);
   const long long total = *p.total;
@@ -629,7 +721,7 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
         ls += red_l[i] * f;
         v += red[i][d] * f;
       }
-      const float r = ls == 0.f ? 0.f : v * (kDown / ls);
+      const float r = ls == 0.f ? 0.f : v / ls;
       (reinterpret_cast<T*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row + hd * p.out.head)[d] = (T)r;
       if (p.lse && d == 0)
         p.lse[((size_t)seq * p.a.rows + row) * p.n_heads + hd] =
@@ -643,30 +735,34 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
 struct Plan {
   const void *main, *join;
   int id;                    // of the variant
-  int CT, smem, blocks;      // columns of a tile, shared memory and blocks of an SM
+  int CT, SP, smem, blocks, threads;  // columns of a tile, positions of a step; blocks of an SM
   int n_ctiles, n_entries, items, grid, join_y, join_threads;
   size_t item_off, part_off, bytes;
 };
 
-template <int HD, class T, int NT, bool PACK>
+template <int HD, class T, int NT, int W, int U, int R, int B>
 void take(Plan* pl) {
-  using S = Shape<HD, T, NT, PACK>;
-  pl->main = reinterpret_cast<const void*>(&k_kv4_attention<HD, T, NT, PACK>);
+  using S = Shape<HD, T, NT, W, U, R, B>;
+  pl->main = reinterpret_cast<const void*>(&k_kv4_attention<HD, T, NT, W, U, R, B>);
   pl->join = reinterpret_cast<const void*>(&k_kv4_join<HD, T>);
-  pl->id = (HD == 64 ? 0 : 8) + (S::F32 ? 4 : 0) + (PACK ? 0 : NT);
+  pl->id = (HD == 64 ? 0 : 16) + (S::F32 ? 8 : 0) + NT;
   pl->CT = S::CT;
+  pl->SP = S::SP;
   pl->smem = S::SMEM;
-  pl->blocks = S::BLOCKS;
+  pl->blocks = B;
+  pl->threads = 32 * W;
 }
 
-// One column tile where the columns fit it, two from 9 on (a tile of the cache
-// then serves 16 columns); up to 4 bf16 columns share a tile with their low parts.
+// As many column tiles as the columns fill, so that the cache's tiles are
+// unpacked once for all of them: up to four for bf16 rows, two for fp32 rows
+// (registers hold the sums of 32 and 16 columns).
 template <int HD>
 void take_for(Plan* pl, int cols, int dtype) {
-  if (dtype == MK_F32) cols <= 8 ? take<HD, float, 1, false>(pl) : take<HD, float, 2, false>(pl);
-  else if (cols <= 4) take<HD, __nv_bfloat16, 1, true>(pl);
-  else if (cols <= 8) take<HD, __nv_bfloat16, 1, false>(pl);
-  else take<HD, __nv_bfloat16, 2, false>(pl);
+  if (dtype == MK_F32) cols <= 8 ? take<HD, float, 1, 4, 1, 4, 3>(pl) : take<HD, float, 2, 4, 1, 4, 2>(pl);
+  else if (cols <= 8) take<HD, __nv_bfloat16, 1, 4, 2, 2, 4>(pl);
+  else if (cols <= 16) take<HD, __nv_bfloat16, 2, 4, 1, 4, 3>(pl);
+  else if (cols <= 24) take<HD, __nv_bfloat16, 3, 4, 1, 4, 2>(pl);
+  else take<HD, __nv_bfloat16, 4, 4, 1, 4, 2>(pl);
 }
 
 int sm_count() {
@@ -685,7 +781,7 @@ bool plan_of(const mk_kv4_cache& c, int n_heads, int dtype, Plan* pl) {
   if (c.head_dim == 64) take_for<64>(pl, (int)cols, dtype);
   else take_for<128>(pl, (int)cols, dtype);
   const long long ct = (cols + pl->CT - 1) / pl->CT, entries = ct * c.n_seqs, items = entries * c.n_kv_heads;
-  const long long most = 2ll * c.max_pages;  // tiles of an item
+  const long long most = (long long)c.max_pages * (kPageTokens / pl->SP);  // steps of an item
   if (items > INT_MAX / 32 || most * c.n_kv_heads > INT_MAX) return false;
   pl->n_ctiles = (int)ct;
   pl->n_entries = (int)entries;
@@ -754,7 +850,7 @@ extern "C" MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, c
   p.q = kv4_rows(*q);
   p.out = kv4_rows(*out);
   p.lse = lse;
-  p.c = (float)((double)scale * 1.4426950408889634 * (double)kDown);
+  p.c = (float)((double)scale * 1.4426950408889634 * kDown);
   p.n_heads = n_heads;
   p.gqa = n_heads / c->n_kv_heads;
   p.cols = c->rows * p.gqa;
@@ -767,7 +863,7 @@ extern "C" MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, c
   cudaError_t e = allow_smem(pl);
   if (e == cudaSuccess) {
     void* args[] = {&p};
-    e = cudaLaunchKernel(pl.main, dim3(pl.grid), dim3(kAttThreads), args, pl.smem, (cudaStream_t)stream);
+    e = cudaLaunchKernel(pl.main, dim3(pl.grid), dim3(pl.threads), args, pl.smem, (cudaStream_t)stream);
   }
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
@@ -779,7 +875,7 @@ extern "C" MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, c
     cfg.stream = (cudaStream_t)stream;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    void* args[] = {&p, &pl.CT, &pl.grid};
+    void* args[] = {&p, &pl.CT, &pl.SP, &pl.grid};
     e = cudaLaunchKernelExC(&cfg, pl.join, args);
   }
   if (e != cudaSuccess) {

@@ -101,7 +101,7 @@ def attend(q, k, v, first, scale, left_out=None):
     return out, lse, A, D
 
 
-def bounds(A, D, lse, n, hd, dtype):
+def bounds(A, D, lse, n, hd, dtype, top):
     """How far out and lse may be off, by arithmetic.
 
     A score is a sum of hd products, exact in the products and rounded at most
@@ -109,14 +109,15 @@ def bounds(A, D, lse, n, hd, dtype):
     handful of roundings, and then enters an exponential whose argument, of
     magnitude at most 2 D + |lse|, is rounded a few times and whose result is off
     by 2^-22: delta below is the relative error of a weight.  Numerator and
-    denominator sum n terms (n 2^-24 each at worst), the weights enter the
-    second product in two bf16 parts (2^-16), in three (2^-24) for fp32.  A term
-    weight * value below 2^-60 may be lost whole (fp32 ends at 2^-126, weights
-    below that of the largest are zero, and a kernel may carry a power of two up
-    to 2^66): n 2^-60 in all, whatever the result's size."""
+    denominator sum n terms (n 2^-24 each at worst).  For bf16 rows the weights
+    enter the second product rounded to fp16 (half a step: 2^-11), for fp32 rows
+    in two fp16 parts (2^-22).  fp16 ends at 2^-25 in absolute terms, where the
+    weights are normalised so that the largest possible term is 2^6 to 2^14: a
+    term is off by 2^-28 of the largest scale's (2^-27 covers it), fp32 rows' low
+    parts likewise.  top is the largest |value| / 7, at least the largest scale."""
     e = 2.0 ** -24
     delta = (2 * hd + 16) * e * D + 8 * e * (2 * D + 1) + 2.0 ** -21
-    part = 2.0 ** -16 if dtype == torch.bfloat16 else 2.0 ** -23
-    inner = A * (2 * delta + 2 * n * e + part + 8 * e)[..., None] + n * 2.0 ** -60
+    part = 2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -22
+    inner = A * (2 * delta + 2 * n * e + part + 8 * e)[..., None] + n * 2.0 ** -27 * top
     # the result's own rounding: half a step of its type
     return inner, torch.finfo(dtype).eps / 2, delta + n * e + 4 * e * (1 + lse.abs())

@@ -146,7 +146,7 @@ def check(q, pool, table, lengths, n_new=None, scale=None, out=None, lse=None, l
         lost = None if left_out is None else left_out[i]
         o, l, A, D = R.attend(q[i, lo:nn], k if lost is None else k.nan_to_num(), v if lost is None else v.nan_to_num(),
                               ln - nn + lo, sc, lost)
-        inner, half, le = R.bounds(A, D, l, ln, hd, q.dtype)
+        inner, half, le = R.bounds(A, D, l, ln, hd, q.dtype, float(v.nan_to_num().abs().max()))
         got = out[i, lo:nn].double()
         blind = l == -math.inf                  # rows that see nothing
         assert (got[blind] == 0).all()
