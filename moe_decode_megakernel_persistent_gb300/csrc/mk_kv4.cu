@@ -16,83 +16,78 @@
 namespace mk {
 namespace {
 
-__device__ __forceinline__ float4 read4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 read4(const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xFFFF0000u));
+// Eight values of a row.
+struct V8 {
+  float x[8];
+};
+__device__ __forceinline__ V8 read8(const float* p) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
 }
-__device__ __forceinline__ void write4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void write4(__nv_bfloat16* p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  uint2 w;
-  w.x = *reinterpret_cast<const uint32_t*>(&a);
-  w.y = *reinterpret_cast<const uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(p) = w;
+__device__ __forceinline__ V8 read8(const __nv_bfloat16* p) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  V8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v.x[2 * i] = __uint_as_float(u[i] << 16);
+    v.x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+  return v;
+}
+__device__ __forceinline__ void write8(float* p, const V8& v) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v.x[0], v.x[1], v.x[2], v.x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v.x[4], v.x[5], v.x[6], v.x[7]);
+}
+__device__ __forceinline__ void write8(__nv_bfloat16* p, const V8& v) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x[2 * i], v.x[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// Sixteen lanes take one group of one row: four values each.
+// A thread's part of a token's rows: eight values of one group, so that eight
+// lanes take a group (one 16-byte load of bf16, one 4-byte store of codes each)
+// and a token is 16 * NG * n_kv_heads parts.
 template <int HD>
-struct Unit {
-  int seq, row, head, kv, group, lane;
-  bool valid;
-  __device__ __forceinline__ Unit(const Kv4Args& a) {
-    const long long u = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / 16;
-    lane = threadIdx.x % 16;
-    const long long total = (long long)a.n_seqs * a.rows * a.n_kv_heads * 2 * Tile<HD>::NG;
-    valid = u < total;
-    long long r = valid ? u : 0;
-    group = (int)(r % Tile<HD>::NG);
-    r /= Tile<HD>::NG;
-    kv = (int)(r % 2);
-    r /= 2;
-    head = (int)(r % a.n_kv_heads);
-    r /= a.n_kv_heads;
-    row = (int)(r % a.rows);
-    seq = (int)(r / a.rows);
+struct Part {
+  int kv, head, group, lane;
+  __device__ __forceinline__ explicit Part(int i, int n_kv_heads) {
+    lane = i % 8;
+    group = i / 8 % Tile<HD>::NG;
+    head = i / (8 * Tile<HD>::NG);
+    kv = head >= n_kv_heads;
+    head -= kv ? n_kv_heads : 0;
   }
 };
 
-// Largest |x| of a group as bits (a NaN's are above an infinity's).
-__device__ __forceinline__ uint32_t group_max(float4 x) {
-  uint32_t u = max(max(__float_as_uint(fabsf(x.x)), __float_as_uint(fabsf(x.y))),
-                   max(__float_as_uint(fabsf(x.z)), __float_as_uint(fabsf(x.w))));
+constexpr int kThreadsKv = 256;  // the most threads of a block
+
+// Rows of one pass over a block's threads (a block stays within a sequence).
+inline int pass_rows(int parts, int rows) { return std::max(1, std::min(kThreadsKv / parts, rows)); }
+
+// The N rows row0 + j * step of a sequence: the tile half that each one's values
+// of this part lie in (null: padding, or a page outside the pool) and its row
+// there.
+template <int HD, int N>
+__device__ __forceinline__ void places_of(const Kv4Args& a, const Part<HD>& pt, int seq, int row0, int step,
+                                          uint8_t* (&t)[N], int (&at)[N]) {
+  int len, nn, p[N], page[N];
+  seq_extent(a, seq, len, nn);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, o));
-  return u;
-}
-
-__device__ __forceinline__ uint32_t code_of(float x, float s) {
-  const float m = s > 0.f ? fminf(rintf(fabsf(x) / s), 7.f) : 0.f;
-  return (uint32_t)m | (m > 0.f && x < 0.f ? 8u : 0u);
-}
-
-template <int HD, class T>
-__global__ void __launch_bounds__(256) k_kv4_store(const __grid_constant__ Kv4Args a, Rows k, Rows v) {
-  const Unit<HD> u(a);
-  int len, nn;
-  seq_extent(a, u.seq, len, nn);
-  const int p = len - nn + u.row;
-  const bool there = u.valid && u.row < nn && p >= 0;
-  const int page = there ? page_of(a, u.seq, p) : -1;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (page >= 0) {
-    const Rows& r = u.kv ? v : k;
-    x = read4(reinterpret_cast<const T*>(r.p) + u.seq * r.seq + u.row * r.row + u.head * r.head + u.group * kGroup + 4 * u.lane);
+  for (int j = 0; j < N; ++j) {
+    const int row = row0 + j * step;
+    p[j] = row < nn ? len - nn + row : -1;
+    page[j] = p[j] >= 0 ? page_of(a, seq, p[j]) : -1;
   }
-  const uint32_t top = group_max(x);  // every lane of the warp takes part
-  if (page < 0) return;
-  uint8_t* t = tile_of<HD>(a, page, u.head, p) + u.kv * Tile<HD>::V;
-  const int r = p % kTile;
-  // a group with a NaN or an infinity reads back as NaN
-  const bool finite = top < 0x7F800000u;
-  const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.f);
-  const float s = finite ? __bfloat162float(sb) : 0.f;
-  const uint32_t c = code_of(x.x, s) | (code_of(x.y, s) << 4) | (code_of(x.z, s) << 8) | (code_of(x.w, s) << 12);
-  *reinterpret_cast<uint16_t*>(t + r * Tile<HD>::ROW + u.group * (kGroup / 2) + 2 * u.lane) = (uint16_t)c;
-  if (u.lane == 0)
-    *reinterpret_cast<uint16_t*>(t + Tile<HD>::CODES + (r * Tile<HD>::NG + u.group) * 2) =
-        finite ? __bfloat16_as_ushort(sb) : (uint16_t)0x7FC0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    at[j] = p[j] % kTile;
+    t[j] = page[j] >= 0 ? tile_of<HD>(a, page[j], pt.head, p[j]) + pt.kv * Tile<HD>::V : nullptr;
+  }
 }
 
 __device__ __forceinline__ float value_of(uint32_t code, float s) {
@@ -100,27 +95,94 @@ __device__ __forceinline__ float value_of(uint32_t code, float s) {
   return code & 8u ? -m : m;
 }
 
-template <int HD, class T>
-__global__ void __launch_bounds__(256) k_kv4_load(const __grid_constant__ Kv4Args a, Rows k, Rows v) {
-  const Unit<HD> u(a);
-  if (!u.valid) return;
-  int len, nn;
-  seq_extent(a, u.seq, len, nn);
-  const int p = len - nn + u.row;
-  const int page = u.row < nn && p >= 0 ? page_of(a, u.seq, p) : -1;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (page >= 0) {
-    const uint8_t* t = tile_of<HD>(a, page, u.head, p) + u.kv * Tile<HD>::V;
-    const int r = p % kTile;
-    const uint32_t c = *reinterpret_cast<const uint16_t*>(t + r * Tile<HD>::ROW + u.group * (kGroup / 2) + 2 * u.lane);
-    const float s = __uint_as_float(
-        (uint32_t)*reinterpret_cast<const uint16_t*>(t + Tile<HD>::CODES + (r * Tile<HD>::NG + u.group) * 2) << 16);
-    x = make_float4(value_of(c, s), value_of(c >> 4, s), value_of(c >> 8, s), value_of(c >> 12, s));
+// One pass over the rows each way, N tokens in flight per thread: bound by the
+// bytes for long calls, for short ones by two dependent reads (length, page),
+// which the rows' own reads do not wait for.
+// The division |x| / s is the IEEE quotient: r = RN(1 / s), q = RN(x r), then
+// q + r (x - q s) in two fused steps (Markstein), which rounds correctly where
+// nothing under- or overflows; scales outside [2^-60, 2^60] take the division itself.
+template <int HD, class T, int N>
+__global__ void __launch_bounds__(kThreadsKv) k_kv4_store(const __grid_constant__ Kv4Args a, Rows k, Rows v, int tp, int chunks) {
+  const int parts = 16 * Tile<HD>::NG * a.n_kv_heads;
+  const int seq = blockIdx.x / chunks, row_base = (blockIdx.x - seq * chunks) * tp * N;
+  const int tk = parts < (int)blockDim.x ? threadIdx.x / parts : 0, row0 = row_base + tk;
+  for (int i0 = 0; i0 < parts; i0 += blockDim.x) {
+    const int i = i0 + threadIdx.x - tk * parts;
+    const bool mine = tk < tp && i < parts;
+    const Part<HD> pt(mine ? i : 0, a.n_kv_heads);
+    const Rows& r = pt.kv ? v : k;
+    const T* src = reinterpret_cast<const T*>(r.p) + seq * r.seq + pt.head * r.head + pt.group * kGroup + 8 * pt.lane;
+    V8 x[N];
+    uint8_t* t[N];
+    int at[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = read8(src + min(row0 + j * tp, a.rows - 1) * r.row);
+    places_of<HD, N>(a, pt, seq, row0, tp, t, at);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      // largest |x| of the group as bits (a NaN's are above an infinity's); every lane takes part
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(fabsf(x[j].x[e])));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (!t[j] || !mine) continue;
+      // a group with a NaN or an infinity reads back as NaN
+      const bool finite = top < 0x7F800000u;
+      const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.f);
+      const float s = finite ? __bfloat162float(sb) : 0.f;
+      uint32_t c = 0;
+      if (s >= 8.6736174e-19f && s <= 1.1529215e18f) {
+        const float rs = __frcp_rn(s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float y = fabsf(x[j].x[e]), q0 = y * rs, q = fmaf(fmaf(-q0, s, y), rs, q0);
+          const uint32_t m = __float_as_uint(q + 12582912.f) & 7u;  // rounds to even; at most 7 (q <= 7 (1 + 2^-8))
+          c |= (m | (m ? __float_as_uint(x[j].x[e]) >> 28 & 8u : 0u)) << (4 * e);
+        }
+      } else if (s > 0.f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t m = (uint32_t)fminf(rintf(fabsf(x[j].x[e]) / s), 7.f);
+          c |= (m | (m && x[j].x[e] < 0.f ? 8u : 0u)) << (4 * e);
+        }
+      }
+      *reinterpret_cast<uint32_t*>(t[j] + at[j] * Tile<HD>::ROW + pt.group * (kGroup / 2) + 4 * pt.lane) = c;
+      if (pt.lane == 0)
+        *reinterpret_cast<uint16_t*>(t[j] + Tile<HD>::CODES + (at[j] * Tile<HD>::NG + pt.group) * 2) =
+            finite ? __bfloat16_as_ushort(sb) : (uint16_t)0x7FC0;
+    }
   }
-  const Rows& r = u.kv ? v : k;
-  write4(reinterpret_cast<T*>(const_cast<void*>(r.p)) + u.seq * r.seq + u.row * r.row + u.head * r.head +
-             u.group * kGroup + 4 * u.lane,
-         x);
+}
+
+template <int HD, class T, int N>
+__global__ void __launch_bounds__(kThreadsKv) k_kv4_load(const __grid_constant__ Kv4Args a, Rows k, Rows v, int tp, int chunks) {
+  const int parts = 16 * Tile<HD>::NG * a.n_kv_heads;
+  const int seq = blockIdx.x / chunks, row_base = (blockIdx.x - seq * chunks) * tp * N;
+  const int tk = parts < (int)blockDim.x ? threadIdx.x / parts : 0, row0 = row_base + tk;
+  if (tk >= tp) return;
+  for (int i = threadIdx.x - tk * parts; i < parts; i += blockDim.x) {
+    const Part<HD> pt(i, a.n_kv_heads);
+    const Rows& r = pt.kv ? v : k;
+    T* dst = reinterpret_cast<T*>(const_cast<void*>(r.p)) + seq * r.seq + pt.head * r.head + pt.group * kGroup + 8 * pt.lane;
+    uint8_t* t[N];
+    int at[N];
+    uint32_t c[N], sc[N];
+    places_of<HD, N>(a, pt, seq, row0, tp, t, at);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      c[j] = t[j] ? *reinterpret_cast<const uint32_t*>(t[j] + at[j] * Tile<HD>::ROW + pt.group * (kGroup / 2) + 4 * pt.lane) : 0u;
+      sc[j] = t[j] ? *reinterpret_cast<const uint16_t*>(t[j] + Tile<HD>::CODES + (at[j] * Tile<HD>::NG + pt.group) * 2) : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (row0 + j * tp >= a.rows) continue;
+      V8 x;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x.x[e] = value_of(c[j] >> (4 * e), __uint_as_float(sc[j] << 16));
+      write8(dst + (row0 + j * tp) * r.row, x);
+    }
+  }
 }
 
 int cuda_status(const char* what) {
@@ -166,19 +228,26 @@ extern "C" MK_API size_t mk_kv4_page_bytes(int32_t n_kv_heads, int32_t head_dim)
   return (size_t)n_kv_heads * (head_dim == 64 ? Tile<64>::RECORD : Tile<128>::RECORD);
 }
 
-// Launch KERNEL<head_dim, element type> with GRID blocks of BLOCK threads.
-#define MK_KV4_LAUNCH(KERNEL, HD, DT, GRID, BLOCK, ST, ...)                                      \
-  do {                                                                                           \
-    if (HD == 64 && DT == MK_F32) KERNEL<64, float><<<GRID, BLOCK, 0, ST>>>(__VA_ARGS__);        \
-    else if (HD == 64) KERNEL<64, __nv_bfloat16><<<GRID, BLOCK, 0, ST>>>(__VA_ARGS__);           \
-    else if (DT == MK_F32) KERNEL<128, float><<<GRID, BLOCK, 0, ST>>>(__VA_ARGS__);              \
-    else KERNEL<128, __nv_bfloat16><<<GRID, BLOCK, 0, ST>>>(__VA_ARGS__);                        \
+// Launch KERNEL<head_dim, element type, rows in flight>: two rows a thread once
+// that still gives every SM two blocks (7.1 us against 7.8 with one and 8.5 with
+// four, for 4096 tokens of 4 heads of 128), one below (a step of a few sequences
+// is bound by its chain of reads).
+#define MK_KV4_LAUNCH(KERNEL, C, DT, ST, ...)                                                                        \
+  do {                                                                                                               \
+    const int parts_ = 16 * ((C).head_dim / kGroup) * (C).n_kv_heads, tp_ = pass_rows(parts_, (C).rows);              \
+    const int threads_ = std::min(kThreadsKv, tp_ * parts_);                                                         \
+    const int c2_ = ((C).rows + 2 * tp_ - 1) / (2 * tp_), c1_ = ((C).rows + tp_ - 1) / tp_;                           \
+    if ((C).n_seqs * c2_ >= 304) MK_KV4_LAUNCH_N(KERNEL, 2, C, DT, ST, __VA_ARGS__, tp_, c2_);                       \
+    else MK_KV4_LAUNCH_N(KERNEL, 1, C, DT, ST, __VA_ARGS__, tp_, c1_);                                               \
   } while (0)
-
-static int kv4_blocks(const mk_kv4_cache& c) {
-  const long long units = (long long)c.n_seqs * c.rows * c.n_kv_heads * 2 * (c.head_dim / kGroup);
-  return (int)((units * 16 + 255) / 256);
-}
+#define MK_KV4_LAUNCH_N(KERNEL, N, C, DT, ST, A, K, V, TP, CH)                                                       \
+  do {                                                                                                               \
+    const int g_ = (C).n_seqs * CH;                                                                                  \
+    if ((C).head_dim == 64 && DT == MK_F32) KERNEL<64, float, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);           \
+    else if ((C).head_dim == 64) KERNEL<64, __nv_bfloat16, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);              \
+    else if (DT == MK_F32) KERNEL<128, float, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);                          \
+    else KERNEL<128, __nv_bfloat16, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);                                    \
+  } while (0)
 
 extern "C" MK_API int mk_kv4_store(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype,
                                    void* stream) {
@@ -188,7 +257,7 @@ extern "C" MK_API int mk_kv4_store(const mk_kv4_cache* c, const mk_kv4_rows* k, 
   if (empty) return MK_OK;
   if (int r = kv4_check_rows(k, dtype, "k")) return r;
   if (int r = kv4_check_rows(v, dtype, "v")) return r;
-  MK_KV4_LAUNCH(k_kv4_store, c->head_dim, dtype, kv4_blocks(*c), 256, (cudaStream_t)stream, kv4_args(*c), kv4_rows(*k), kv4_rows(*v));
+  MK_KV4_LAUNCH(k_kv4_store, *c, dtype, (cudaStream_t)stream, kv4_args(*c), kv4_rows(*k), kv4_rows(*v));
   return cuda_status("kv4 store");
 }
 
@@ -200,6 +269,6 @@ extern "C" MK_API int mk_kv4_load(const mk_kv4_cache* c, const mk_kv4_rows* k, c
   if (empty) return MK_OK;
   if (int r = kv4_check_rows(k, dtype, "k")) return r;
   if (int r = kv4_check_rows(v, dtype, "v")) return r;
-  MK_KV4_LAUNCH(k_kv4_load, c->head_dim, dtype, kv4_blocks(*c), 256, (cudaStream_t)stream, kv4_args(*c), kv4_rows(*k), kv4_rows(*v));
+  MK_KV4_LAUNCH(k_kv4_load, *c, dtype, (cudaStream_t)stream, kv4_args(*c), kv4_rows(*k), kv4_rows(*v));
   return cuda_status("kv4 load");
 }

@@ -135,6 +135,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
 }
+// The first product of a chain: d = a b.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t turn(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -387,87 +394,120 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
         for (int i = 0; i < 4; ++i) o[nt][h][i][0] = o[nt][h][i][1] = o[nt][h][i][2] = o[nt][h][i][3] = 0.f;
     }
 
-    // 16 positions from p0 on, rows r0.. of a tile (`tile`: the K codes of row r0);
-    // CUT: some column does not see all of them
-    auto unit = [&](uint32_t tile, int r0, int p0, auto cut_) {
+    // U x 16 positions from p0 on, rows r0.. of a tile (`tile`: the K codes of
+    // row r0); CUT: some column does not see all of them
+    auto step = [&](uint32_t tile, int r0, int p0, auto cut_) {
       constexpr bool CUT = decltype(cut_)::value;
+      constexpr int HG = NT > 2 ? 1 : NG;  // groups of dimensions in flight
       const uint32_t kr = tile + g * L::ROW + 8 * t4;
       // scales of positions g and g + 8
-      float ks[2][NG], vs[2][NG];
+      float ks[U][2][NG], vs[U][2][NG];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t at = tile + L::CODES + (g + 8 * r) * NG * 2 - r0 * (L::ROW - NG * 2);
-        const uint32_t x = NG == 2 ? lds32(at) : lds16(at);
-        uint32_t y = NG == 2 ? lds32(at + L::V) : lds16(at + L::V);
-        if (CUT && p0 + g + 8 * r >= any) y = 0;  // a slot behind the end may hold anything
-        ks[r][0] = low_f(x);
-        vs[r][0] = low_f(y);
-        if constexpr (NG == 2) {
-          ks[r][1] = high_f(x);
-          vs[r][1] = high_f(y);
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t at = tile + L::CODES + (16 * u + g + 8 * r) * NG * 2 - r0 * (L::ROW - NG * 2);
+          const uint32_t x = NG == 2 ? lds32(at) : lds16(at);
+          uint32_t y = NG == 2 ? lds32(at + L::V) : lds16(at + L::V);
+          if (CUT && p0 + 16 * u + g + 8 * r >= any) y = 0;  // a slot behind the end may hold anything
+          ks[u][r][0] = low_f(x);
+          vs[u][r][0] = low_f(y);
+          if constexpr (NG == 2) {
+            ks[u][r][1] = high_f(x);
+            vs[u][r][1] = high_f(y);
+          }
         }
-      }
       // scores without the factor c: element x + 2 r is column 2 t + x, position g + 8 r
-      float v[NT][4];
+      float v[U][NT][4];
 #pragma unroll
-      for (int h = 0; h < NG; ++h) {
-        float a[NT][4];
+      for (int hb = 0; hb < NG; hb += HG) {
+        float a[U][HG][NT][4];
+        uint2 kw[U][HG][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) a[nt][0] = a[nt][1] = a[nt][2] = a[nt][3] = 0.f;
-        const uint2 u0 = lds64(kr + 32 * h), u1 = lds64(kr + 8 * L::ROW + 32 * h);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int h = 0; h < HG; ++h)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) kw[u][h][r] = lds64(kr + (16 * u + 8 * r) * L::ROW + 32 * (hb + h));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          uint2 qs[NT][2];
+          uint2 qs[HG][NT][2];
           if constexpr (S::QS) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint4 b = *reinterpret_cast<const uint4*>(qsm + (((nt * NG + h) * 2 + i) * 32 + lane) * 2);
-              qs[nt][0] = make_uint2(b.x, b.y);
-              qs[nt][1] = make_uint2(b.z, b.w);
-            }
-          }
+            for (int h = 0; h < HG; ++h)
 #pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            const uint32_t x0 = __byte_perm(i ? u0.y : u0.x, 0, jj ? 0x3322 : 0x1100);
-            const uint32_t x1 = __byte_perm(i ? u1.y : u1.x, 0, jj ? 0x3322 : 0x1100);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if constexpr (S::QS) {
-                mma_bf16(a[nt], (x0 << 4) & kNib, (x1 << 4) & kNib, x0 & kNib, x1 & kNib, qs[nt][jj]);
-              } else {
-#pragma unroll
-                for (int q = S::QP - 1; q >= 0; --q)
-                  mma_bf16(a[nt], (x0 << 4) & kNib, (x1 << 4) & kNib, x0 & kNib, x1 & kNib, qf[q][nt][h][i][jj]);
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint4 b = *reinterpret_cast<const uint4*>(qsm + (((nt * NG + hb + h) * 2 + i) * 32 + lane) * 2);
+                qs[h][nt][0] = make_uint2(b.x, b.y);
+                qs[h][nt][1] = make_uint2(b.z, b.w);
               }
-            }
           }
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+            for (int h = 0; h < HG; ++h)
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                const uint2 u0 = kw[u][h][0], u1 = kw[u][h][1];
+                const uint32_t x0 = __byte_perm(i ? u0.y : u0.x, 0, jj ? 0x3322 : 0x1100);
+                const uint32_t x1 = __byte_perm(i ? u1.y : u1.x, 0, jj ? 0x3322 : 0x1100);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if constexpr (S::QS) {
+                    if (i == 0 && jj == 0)
+                      mma_bf16_first(a[u][h][nt], (x0 << 4) & kNib, (x1 << 4) & kNib, x0 & kNib, x1 & kNib, qs[h][nt][jj]);
+                    else
+                      mma_bf16(a[u][h][nt], (x0 << 4) & kNib, (x1 << 4) & kNib, x0 & kNib, x1 & kNib, qs[h][nt][jj]);
+                  } else {
+#pragma unroll
+                    for (int q = S::QP - 1; q >= 0; --q)
+                      if (i == 0 && jj == 0 && q == S::QP - 1)
+                        mma_bf16_first(a[u][h][nt], (x0 << 4) & kNib, (x1 << 4) & kNib, x0 & kNib, x1 & kNib,
+                                       qf[q][nt][hb + h][i][jj]);
+                      else
+                        mma_bf16(a[u][h][nt], (x0 << 4) & kNib, (x1 << 4) & kNib, x0 & kNib, x1 & kNib,
+                                 qf[q][nt][hb + h][i][jj]);
+                  }
+                }
+              }
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int h = 0; h < HG; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[u][nt][e] = hb + h ? fmaf(a[u][h][nt][e], ks[u][e >> 1][hb + h], v[u][nt][e])
+                                     : a[u][h][nt][e] * ks[u][e >> 1][0];
+      }
+      // distance to the running maxima; a maximum or the cap that is passed moves
+      float d[U][NT][4];
+      bool over = false;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[nt][e] = h ? fmaf(a[nt][e], ks[e >> 1][h], v[nt][e]) : a[nt][e] * ks[e >> 1][h];
-      }
-      // distance to the running maxima; a maximum or the cap that is passed moves
-      float d[NT][4];
-      bool over = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          d[nt][e] = fmaf(v[nt][e], p.c, -m[nt][e & 1]);
-          if (CUT && p0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) d[nt][e] = -INFINITY;
-          over |= d[nt][e] > kLazy;
-        }
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int h = 0; h < NG; ++h) over |= vs[r][h] > cap;
-      if (__any_sync(0xffffffffu, over)) {
-        float top = 0.f;
+          for (int e = 0; e < 4; ++e) {
+            d[u][nt][e] = fmaf(v[u][nt][e], p.c, -m[nt][e & 1]);
+            if (CUT && p0 + 16 * u + g + 8 * (e >> 1) >= lim[nt][e & 1]) d[u][nt][e] = -INFINITY;
+            over |= d[u][nt][e] > kLazy;
+          }
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int h = 0; h < NG; ++h) top = fmaxf(top, vs[r][h]);
+          for (int h = 0; h < NG; ++h) over |= vs[u][r][h] > cap;
+      }
+      if (__any_sync(0xffffffffu, over)) {
+        float top = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int h = 0; h < NG; ++h) top = fmaxf(top, vs[u][r][h]);
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
         float move = 1.f;
@@ -484,8 +524,10 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
           for (int x = 0; x < 2; ++x) {
             float t = m[nt][x];
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-              if (d[nt][x + 2 * r] != -INFINITY) t = fmaxf(t, v[nt][x + 2 * r] * p.c);
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                if (d[u][nt][x + 2 * r] != -INFINITY) t = fmaxf(t, v[u][nt][x + 2 * r] * p.c);
 #pragma unroll
             for (int y = 4; y < 32; y <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, y));
             const float f = exp2_fast(m[nt][x] - t);
@@ -500,64 +542,71 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
                 o[nt][h][i][x + 2] *= fo;
               }
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-              if (d[nt][x + 2 * r] != -INFINITY) d[nt][x + 2 * r] = fmaf(v[nt][x + 2 * r], p.c, -t);
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                if (d[u][nt][x + 2 * r] != -INFINITY) d[u][nt][x + 2 * r] = fmaf(v[u][nt][x + 2 * r], p.c, -t);
           }
       }
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int h = 0; h < NG; ++h) vs[r][h] *= vmul;
       // weights times V's scales, as B fragments
-      uint2 wf[S::WP][NT][NG];
+      uint2 wf[U][S::WP][NT][NG];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          d[nt][e] = exp2_fast(d[nt][e]);
-          l[nt][e & 1] += d[nt][e];
-        }
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int h = 0; h < NG; ++h) {
-          float x[4];
+          for (int h = 0; h < NG; ++h) vs[u][r][h] *= vmul;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[e] = d[nt][e] * vs[e >> 1][h];
-            if (CUT && p0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) x[e] = 0.f;  // whatever the scale there
+            d[u][nt][e] = exp2_fast(d[u][nt][e]);
+            l[nt][e & 1] += d[u][nt][e];
           }
 #pragma unroll
-          for (int q = 0; q < S::WP; ++q) {
-            const uint32_t b0 = pack2h(x[0], x[1]), b1 = pack2h(x[2], x[3]);
-            wf[q][nt][h] = make_uint2(turn(b0), turn(b1));
-            if (q + 1 < S::WP) x[0] -= low_h(b0), x[1] -= high_h(b0), x[2] -= low_h(b1), x[3] -= high_h(b1);
+          for (int h = 0; h < NG; ++h) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[e] = d[u][nt][e] * vs[u][e >> 1][h];
+              if (CUT && p0 + 16 * u + g + 8 * (e >> 1) >= lim[nt][e & 1]) x[e] = 0.f;  // whatever the scale there
+            }
+#pragma unroll
+            for (int q = 0; q < S::WP; ++q) {
+              const uint32_t b0 = pack2h(x[0], x[1]), b1 = pack2h(x[2], x[3]);
+              wf[u][q][nt][h] = make_uint2(turn(b0), turn(b1));
+              if (q + 1 < S::WP) x[0] -= low_h(b0), x[1] -= high_h(b0), x[2] -= low_h(b1), x[3] -= high_h(b1);
+            }
           }
         }
       }
       // V: positions 2 t, 2 t + 1 and 2 t + 8, 2 t + 9, dimensions 64 h + 8 g + {0..7}
       const uint32_t vr = tile + L::V + 2 * t4 * L::ROW + 4 * g;
 #pragma unroll
-      for (int h = 0; h < NG; ++h) {
-        const uint32_t v0 = lds32(vr + 32 * h), v1 = lds32(vr + L::ROW + 32 * h);
-        const uint32_t v8 = lds32(vr + 8 * L::ROW + 32 * h), v9 = lds32(vr + 9 * L::ROW + 32 * h);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t sel = 0x4400u + 0x1111u * i;
-          const uint32_t x = __byte_perm(v0, v1, sel), y = __byte_perm(v8, v9, sel);
+        for (int h = 0; h < NG; ++h) {
+          const uint32_t at = vr + 16 * u * L::ROW + 32 * h;
+          const uint32_t v0 = lds32(at), v1 = lds32(at + L::ROW), v8 = lds32(at + 8 * L::ROW), v9 = lds32(at + 9 * L::ROW);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (S::F32) {  // a tile's terms are summed on their own, then added
-              float f[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t sel = 0x4400u + 0x1111u * i;
+            const uint32_t x = __byte_perm(v0, v1, sel), y = __byte_perm(v8, v9, sel);
 #pragma unroll
-              for (int q = S::WP - 1; q >= 0; --q)
-                mma_f16(f, (x << 4) & kNib, x & kNib, (y << 4) & kNib, y & kNib, wf[q][nt][h]);
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (S::F32) {  // a unit's terms are summed on their own, then added
+                float f[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[nt][h][i][e] += f[e];
-            } else {
-              mma_f16(o[nt][h][i], (x << 4) & kNib, x & kNib, (y << 4) & kNib, y & kNib, wf[0][nt][h]);
+                for (int q = S::WP - 1; q >= 0; --q)
+                  mma_f16(f, (x << 4) & kNib, x & kNib, (y << 4) & kNib, y & kNib, wf[u][q][nt][h]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][h][i][e] += f[e];
+              } else {
+                mma_f16(o[nt][h][i], (x << 4) & kNib, x & kNib, (y << 4) & kNib, y & kNib, wf[u][0][nt][h]);
+              }
             }
           }
         }
-      }
     };
 
 #pragma unroll 1
@@ -579,14 +628,8 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
         // this warp's first position, its tile and row
         const int at = 16 * U * w, p0 = t * SP + at, r0 = at % kTile;
         const uint32_t tile = smem_addr(sm + st * S::BYTES) + at / kTile * L::BYTES + r0 * L::ROW;
-        if (p0 + 16 * U <= all) {
-#pragma unroll
-          for (int u = 0; u < U; ++u) unit(tile + 16 * u * L::ROW, r0 + 16 * u, p0 + 16 * u, std::false_type());
-        } else {
-#pragma unroll 1
-          for (int u = 0; u < U; ++u)
-            if (p0 + 16 * u < any) unit(tile + 16 * u * L::ROW, r0 + 16 * u, p0 + 16 * u, std::true_type());
-        }
+        if (p0 + 16 * U <= all) step(tile, r0, p0, std::false_type());
+        else if (p0 < any) step(tile, r0, p0, std::true_type());
       }
       __syncwarp();
       if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[st])) : "memory");
