@@ -38,7 +38,8 @@
 // warp takes 16 positions of a tile, with running maxima of its own (moved only
 // when a score passes them by 2^8) and one merge at the end of an item.  An item cut
 // between blocks is joined by a second kernel, launched so that its start
-// overlaps the first one's end.
+// overlaps the first one's end.  Short work instead makes each item a cluster of
+// blocks that join through their shared memory, in one kernel.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -67,9 +68,12 @@ struct AttArgs {
   float* lse;
   float c;              // scale * log2(e) * 2^65
   int32_t n_heads, gqa;
+  int32_t gqa_log;      // log2(gqa), or -1
   int32_t cols;         // rows * gqa: query columns of a (sequence, kv head)
   int32_t n_ctiles;     // column tiles of it
   int32_t n_entries;    // n_seqs * n_ctiles
+  int32_t cluster;      // > 0: an item is one cluster of so many blocks (a power of two), and there is no workspace
+  int32_t cluster_log;
   long long* total;     // workspace: tiles of the call
   longlong2* item;      // workspace: [n_entries * n_kv_heads] first tile and block, or -1 (done)
   float* part;          // workspace: [2 * grid][columns][HD + 4] partial results
@@ -161,6 +165,16 @@ __device__ __forceinline__ float low_h(uint32_t x) { return __half2float(__ushor
 __device__ __forceinline__ float high_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x >> 16))); }
 __device__ __forceinline__ float low_f(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float high_f(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
+// Store into another block's shared memory of the cluster.
+__device__ __forceinline__ void put_peer(const float* local, int rank, float2 v) {
+  uint32_t y;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(smem_addr(local)), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(y), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -168,13 +182,18 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 constexpr uint32_t kNib = 0x80708070u;
 
+// The row of a query column.
+__device__ __forceinline__ int row_of(const AttArgs& p, int col) {
+  return p.gqa_log >= 0 ? col >> p.gqa_log : col / p.gqa;
+}
+
 // Column tile j of sequence s: how many steps of SP positions its columns see.
 __device__ __forceinline__ int tiles_of(const AttArgs& p, int e, int CT, int SP) {
-  const int s = e / p.n_ctiles, j = e - s * p.n_ctiles;
+  const int s = p.n_ctiles == 1 ? e : e / p.n_ctiles, j = e - s * p.n_ctiles;
   int len, nn;
   seq_extent(p.a, s, len, nn);
-  if (j * CT / p.gqa >= nn) return 0;                                     // its rows are padding
-  const int r = min((min((j + 1) * CT, p.cols) - 1) / p.gqa, nn - 1);     // its last row
+  if (row_of(p, j * CT) >= nn) return 0;                                  // its rows are padding
+  const int r = min(row_of(p, min((j + 1) * CT, p.cols) - 1), nn - 1);    // its last row
   const int end = len - nn + r + 1;
   return end <= 0 ? 0 : (end + SP - 1) / SP;
 }
@@ -227,12 +246,18 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
   __shared__ __align__(8) uint64_t full[R], empty[R];
   __shared__ unsigned long long list[kList];  // where the block's next steps lie (0: a page outside the pool)
   __shared__ uint32_t issued[R];              // 1 + the last step copied into each stage
-  __shared__ float sm_m[W][CT], sm_l[W][CT];
+  __shared__ float2 sm_ml[W][CT];  // a run's maximum and sum of each warp and column
   __shared__ long long s_lo, s_hi, s_base;
   __shared__ int s_entry;
   __shared__ volatile int give_up;
+  __shared__ int pages[NTHR];  // cluster: the first pages of the item's sequence
+  // cluster: the partial results of the columns that this block joins, column c
+  // (joined by block c mod cluster) of block r in [r][c / cluster][HD | M, sum]
+  float* fin = reinterpret_cast<float*>(sm + S::SMEM);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // a block's shared memory is there to be written once the block runs
+  if (p.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   if (tid == 0) {
     for (int i = 0; i < R; ++i) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[i])) : "memory");
@@ -242,7 +267,75 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     for (int i = 0; i < R; ++i) issued[i] = 0;
     give_up = 0;
   }
-  if (w == 0) {  // this block's share
+  // lane (g, t) of the mma fragments
+  const int g = lane >> 2, t4 = lane & 3;
+  // the B fragments of q: column nt * 8 + g, dimensions 64 h + 16 t + 8 i + 4 jj + {0, 2 | 1, 3}
+  uint2 qf[S::QS ? 1 : S::QP][S::QS ? 1 : NT][NG][2][2];
+  uint2* qsm = reinterpret_cast<uint2*>(sm + R * S::BYTES + S::RED);  // [nt][h][i][lane][jj]
+  auto load_q = [&](int seq, int j, int head) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (S::QS && nt % W != w) continue;
+      const int col = j * CT + nt * 8 + g;
+      const bool there = col < p.cols;
+      const int row = there ? row_of(p, col) : 0, hd = there ? col - row * p.gqa : 0;
+      const T* src = reinterpret_cast<const T*>(p.q.p) + seq * p.q.seq + row * p.q.row +
+                     (head * p.gqa + hd) * p.q.head + 16 * t4;
+#pragma unroll
+      for (int h = 0; h < NG; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (there) {
+              if constexpr (S::F32) x = *reinterpret_cast<const float4*>(src + 64 * h + 8 * i + 4 * jj);
+              else {
+                const uint2 v = *reinterpret_cast<const uint2*>(src + 64 * h + 8 * i + 4 * jj);
+                x = make_float4(low_f(v.x), high_f(v.x), low_f(v.y), high_f(v.y));
+              }
+            }
+            x.x *= kUp, x.y *= kUp, x.z *= kUp, x.w *= kUp;
+            if constexpr (S::QS) {
+              qsm[(((nt * NG + h) * 2 + i) * 32 + lane) * 2 + jj] = make_uint2(pack2(x.x, x.z), pack2(x.y, x.w));
+            } else {
+#pragma unroll
+              for (int q = 0; q < S::QP; ++q) {
+                const uint2 b = make_uint2(pack2(x.x, x.z), pack2(x.y, x.w));
+                qf[q][nt][h][i][jj] = b;
+                if (q + 1 < S::QP) x.x -= low_f(b.x), x.z -= high_f(b.x), x.y -= low_f(b.y), x.w -= high_f(b.y);
+              }
+            }
+          }
+    }
+    if constexpr (S::QS) asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
+  };
+  // Dimensions d, d + 1 of a column's result from its sums.
+  auto put_out = [&](int seq, int col, int head, int d, float M, float l_sum, float2 v) {
+    const int row = row_of(p, col), hd = head * p.gqa + col - row * p.gqa;
+    const float f = l_sum == 0.f ? 0.f : 1.f / l_sum;
+    T* dst = reinterpret_cast<T*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row + hd * p.out.head + d;
+    if constexpr (S::F32) *reinterpret_cast<float2*>(dst) = make_float2(v.x * f, v.y * f);
+    else *reinterpret_cast<uint32_t*>(dst) = pack2(v.x * f, v.y * f);
+    if (p.lse && d == 0)
+      p.lse[((size_t)seq * p.a.rows + row) * p.n_heads + hd] =
+          l_sum == 0.f ? -INFINITY : (M + log2f(l_sum)) * 0.69314718055994530942f;
+  };
+  Runs run;
+  long long lo;
+  if (p.cluster) {  // this block's share of its cluster's item, at once with the first reads of pages and q
+    const int item = blockIdx.x >> p.cluster_log, rank = blockIdx.x & (p.cluster - 1);
+    const int e = item / p.a.n_kv_heads, head = item - e * p.a.n_kv_heads;
+    const int seq = p.n_ctiles == 1 ? e : e / p.n_ctiles;
+    const int page = tid < p.a.max_pages ? p.a.table[(size_t)seq * p.a.max_pages + tid] : -1;
+    const uint32_t nt = tiles_of(p, e, CT, SP);  // at most 2^24
+    load_q(seq, e - seq * p.n_ctiles, head);
+    run.base = 0;
+    run.e = e;
+    lo = run.pos = (long long)head * nt + (nt * rank >> p.cluster_log);
+    run.hi = (long long)head * nt + (nt * (rank + 1) >> p.cluster_log);
+    pages[tid] = page;
+  } else if (w == 0) {  // this block's share of all tiles
     long long total = 0;
     for (int e = lane; e < p.n_entries; e += 32) total += tiles_of(p, e, CT, SP);
 #pragma unroll
@@ -279,23 +372,31 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     }
   }
   __syncthreads();
-  Runs run;
-  run.pos = s_lo;
-  run.hi = s_hi;
-  run.base = s_base;
-  run.e = s_entry;
-  const long long lo = s_lo;
-  const uint32_t n_steps = (uint32_t)(s_hi - lo);
+  if (!p.cluster) {
+    lo = run.pos = s_lo;
+    run.hi = s_hi;
+    run.base = s_base;
+    run.e = s_entry;
+  }
+  const Runs mine = run;
+  const uint32_t n_steps = (uint32_t)(run.hi - lo);
   uint32_t k = 0;  // steps done
   // Address of the block's step i, looked up by one thread (all of a window at once).
   auto look_up = [&](uint32_t i) {
-    Runs r;
-    r.pos = lo + i;
-    r.hi = s_hi;
-    r.base = s_base;
-    r.e = s_entry;
+    Runs r = mine;
+    r.pos += i;
     if (!r.next(p, CT, SP)) return;
-    const int pg = page_of(p.a, r.e / p.n_ctiles, r.t0 * SP);
+    const int at = r.t0 * SP / kPageTokens;
+    int pg;
+    if (p.cluster && at < NTHR) {
+      pg = pages[at];
+      if (pg < 0 || pg >= p.a.n_pages) {
+        refuse(p.a.status);
+        pg = -1;
+      }
+    } else {
+      pg = page_of(p.a, p.n_ctiles == 1 ? r.e : r.e / p.n_ctiles, r.t0 * SP);
+    }
     list[i % kList] = pg < 0 ? 0 : (unsigned long long)tile_of<HD>(p.a, pg, r.head, r.t0 * SP);
   };
   // Copy step i into its stage, which is free; one thread.
@@ -313,57 +414,18 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     }
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
   };
-  for (uint32_t i = tid; i < kList; i += NTHR) look_up(i);
+  for (uint32_t i = tid; i < kList && i < n_steps; i += NTHR) {
+    look_up(i);
+    if (i < R) copy_step(i);
+  }
   __syncthreads();
-  if (tid == 0)
-    for (uint32_t i = 0; i < R && i < n_steps; ++i) copy_step(i);
-  __syncwarp();
+  if (p.cluster > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 
-  // lane (g, t) of the mma fragments
-  const int g = lane >> 2, t4 = lane & 3;
   while (run.next(p, CT, SP)) {
-    const int seq = run.e / p.n_ctiles, j = run.e - seq * p.n_ctiles;
+    const int seq = p.n_ctiles == 1 ? run.e : run.e / p.n_ctiles, j = run.e - seq * p.n_ctiles;
     int len, nn;
     seq_extent(p.a, seq, len, nn);
-    // the B fragments of q: column nt * 8 + g, dimensions 64 h + 16 t + 8 i + 4 jj + {0, 2 | 1, 3}
-    uint2 qf[S::QS ? 1 : S::QP][S::QS ? 1 : NT][NG][2][2];
-    uint2* qsm = reinterpret_cast<uint2*>(sm + R * S::BYTES + S::RED);  // [nt][h][i][lane][jj]
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (S::QS && nt % W != w) continue;
-      const int col = j * CT + nt * 8 + g;
-      const bool there = col < p.cols;
-      const int row = there ? col / p.gqa : 0, hd = there ? col - row * p.gqa : 0;
-      const T* src = reinterpret_cast<const T*>(p.q.p) + seq * p.q.seq + row * p.q.row +
-                     (run.head * p.gqa + hd) * p.q.head + 16 * t4;
-#pragma unroll
-      for (int h = 0; h < NG; ++h)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (there) {
-              if constexpr (S::F32) x = *reinterpret_cast<const float4*>(src + 64 * h + 8 * i + 4 * jj);
-              else {
-                const uint2 v = *reinterpret_cast<const uint2*>(src + 64 * h + 8 * i + 4 * jj);
-                x = make_float4(low_f(v.x), high_f(v.x), low_f(v.y), high_f(v.y));
-              }
-            }
-            x.x *= kUp, x.y *= kUp, x.z *= kUp, x.w *= kUp;
-            if constexpr (S::QS) {
-              qsm[(((nt * NG + h) * 2 + i) * 32 + lane) * 2 + jj] = make_uint2(pack2(x.x, x.z), pack2(x.y, x.w));
-            } else {
-#pragma unroll
-              for (int q = 0; q < S::QP; ++q) {
-                const uint2 b = make_uint2(pack2(x.x, x.z), pack2(x.y, x.w));
-                qf[q][nt][h][i][jj] = b;
-                if (q + 1 < S::QP) x.x -= low_f(b.x), x.z -= high_f(b.x), x.y -= low_f(b.y), x.w -= high_f(b.y);
-              }
-            }
-          }
-    }
-    if constexpr (S::QS) asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
+    if (!p.cluster) load_q(seq, j, run.head);
     // positions that this lane's columns see (columns nt * 8 + 2 t, + 1), what
     // all columns see and what any does
     int lim[NT][2], all = INT_MAX, any = 0;
@@ -371,7 +433,7 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int col = j * CT + nt * 8 + 2 * t4 + x, row = col / p.gqa;
+        const int col = j * CT + nt * 8 + 2 * t4 + x, row = row_of(p, col);
         lim[nt][x] = col < p.cols && row < nn ? max(0, len - nn + row + 1) : 0;
         if (col < p.cols) all = min(all, lim[nt][x]);
         any = max(any, lim[nt][x]);
@@ -635,78 +697,102 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
       if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[st])) : "memory");
     }
 
-    // ---- the item's end: the four warps' sums joined
+    // ---- the run's end: the warps' sums joined
     float* red = reinterpret_cast<float*>(sm + R * S::BYTES);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], d);
-        if (g == 0) {
-          sm_m[w][nt * 8 + 2 * t4 + x] = m[nt][x];
-          sm_l[w][nt * 8 + 2 * t4 + x] = l[nt][x];
-        }
-      }
-    asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
     const float undo = kCode / vmul;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int col = nt * 8 + 2 * t4 + x;
-        float M = sm_m[0][col];
 #pragma unroll
-        for (int i = 1; i < W; ++i) M = fmaxf(M, sm_m[i][col]);
-        const float f = exp2_fast(m[nt][x] - M) * undo;
+        for (int d = 4; d < 32; d <<= 1) l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], d);
+        if (g == 0) sm_ml[w][col] = make_float2(m[nt][x], l[nt][x]);
         float* dst = red + (w * CT + col) * S::RS + 8 * g;
 #pragma unroll
         for (int h = 0; h < NG; ++h)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float2*>(dst + 64 * h + 2 * i) = make_float2(o[nt][h][i][x] * f, o[nt][h][i][x + 2] * f);
+            *reinterpret_cast<float2*>(dst + 64 * h + 2 * i) = make_float2(o[nt][h][i][x] * undo, o[nt][h][i][x + 2] * undo);
       }
     asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
-    const bool whole = run.t0 == 0 && run.t1 == run.nt;
+    const bool whole = p.cluster <= 1 && run.t0 == 0 && run.t1 == run.nt;
     const size_t slot = 2 * (size_t)blockIdx.x + (run.pos == lo ? 0 : 1);
     const int ncol = min(CT, p.cols - j * CT);
     for (int x = tid; x < ncol * HD / 2; x += NTHR) {
       const int c = x / (HD / 2), d = x % (HD / 2) * 2;
       float M = kLow, l_sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < W; ++i) M = fmaxf(M, sm_m[i][c]);
+      for (int i = 0; i < W; ++i) M = fmaxf(M, sm_ml[i][c].x);
       float2 v = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        l_sum += sm_l[i][c] * exp2_fast(sm_m[i][c] - M);
+        const float f = exp2_fast(sm_ml[i][c].x - M);
+        l_sum += sm_ml[i][c].y * f;
         const float2 y = *reinterpret_cast<const float2*>(red + (i * CT + c) * S::RS + d);
-        v.x += y.x, v.y += y.y;
+        v.x += y.x * f, v.y += y.y * f;
       }
       if (give_up) l_sum = v.x = v.y = NAN;
       if (whole) {
-        const int col = j * CT + c, row = col / p.gqa, hd = run.head * p.gqa + col - row * p.gqa;
-        const float f = l_sum == 0.f ? 0.f : 1.f / l_sum;
-        T* dst = reinterpret_cast<T*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row + hd * p.out.head + d;
-        if constexpr (S::F32) *reinterpret_cast<float2*>(dst) = make_float2(v.x * f, v.y * f);
-        else *reinterpret_cast<uint32_t*>(dst) = pack2(v.x * f, v.y * f);
-        if (p.lse && d == 0)
-          p.lse[((size_t)seq * p.a.rows + row) * p.n_heads + hd] =
-              l_sum == 0.f ? -INFINITY : (M + log2f(l_sum)) * 0.69314718055994530942f;
+        put_out(seq, j * CT + c, run.head, d, M, l_sum, v);
+      } else if (p.cluster) {
+        const int rank = blockIdx.x & (p.cluster - 1), slots = (CT + p.cluster - 1) >> p.cluster_log;
+        float* to = fin + (rank * slots + (c >> p.cluster_log)) * S::RS;
+        put_peer(to + d, c & (p.cluster - 1), v);
+        if (d == 0) put_peer(to + HD, c & (p.cluster - 1), make_float2(M, l_sum));
       } else {
         float* dst = p.part + (slot * CT + c) * (HD + 4);
         *reinterpret_cast<float2*>(dst + d) = v;
         if (d == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(M, l_sum);
       }
     }
-    if (tid == 0 && run.t0 == 0)
+    if (!p.cluster && tid == 0 && run.t0 == 0)
       p.item[(size_t)run.e * p.a.n_kv_heads + run.head] = make_longlong2(whole ? -1 : run.pos, blockIdx.x);
-    asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
     run.pos += run.t1 - run.t0;
+    if (run.pos < run.hi) asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");  // the buffers are used again
   }
   if (give_up && tid == 0) {  // copies in flight land before the block ends
     int none = 0;
     for (int i = 0; i < R; ++i)
       if (issued[i]) bar_wait_long(smem_addr(&full[i]), ((issued[i] - 1) / R) & 1, &none, nullptr);
+  }
+
+  // ---- a cluster's item: the blocks have stored their sums with the block that
+  // joins the column; it adds them in the blocks' order
+  if (p.cluster) {
+    const int item = blockIdx.x >> p.cluster_log, rank = blockIdx.x & (p.cluster - 1);
+    const int e = item / p.a.n_kv_heads, head = item - e * p.a.n_kv_heads;
+    const int seq = p.n_ctiles == 1 ? e : e / p.n_ctiles, j = e - seq * p.n_ctiles, ncol = min(CT, p.cols - j * CT);
+    if (p.cluster == 1) {
+      if (n_steps == 0)
+        for (int x = tid; x < ncol * HD / 2; x += NTHR)
+          put_out(seq, j * CT + x / (HD / 2), head, x % (HD / 2) * 2, kLow, 0.f, make_float2(0.f, 0.f));
+      return;
+    }
+    const int slots = (CT + p.cluster - 1) >> p.cluster_log;
+    if (n_steps == 0)  // nothing to add: a sum of 0 stands for it
+      for (int c = tid; c < ncol; c += NTHR)
+        put_peer(fin + (rank * slots + (c >> p.cluster_log)) * S::RS + HD, c & (p.cluster - 1), make_float2(kLow, 0.f));
+    cluster_sync();
+    for (int x = tid; x < slots * (HD / 2); x += NTHR) {
+      const int sl = x / (HD / 2), d = x % (HD / 2) * 2, c = (sl << p.cluster_log) + rank;
+      if (c >= ncol) break;
+      float M = kLow, l_sum = 0.f;
+      float2 v = make_float2(0.f, 0.f);
+#pragma unroll 4
+      for (int r = 0; r < p.cluster; ++r) M = fmaxf(M, fin[(r * slots + sl) * S::RS + HD]);
+#pragma unroll 4
+      for (int r = 0; r < p.cluster; ++r) {
+        const float* from = fin + (r * slots + sl) * S::RS;
+        const float2 ml = *reinterpret_cast<const float2*>(from + HD), y = *reinterpret_cast<const float2*>(from + d);
+        const float f = exp2_fast(ml.x - M);
+        if (ml.x != kLow || ml.y != 0.f) {
+          l_sum += ml.y * f;
+          v.x += y.x * f, v.y += y.y * f;
+        }
+      }
+      put_out(seq, j * CT + c, head, d, M, l_sum, v);
+    }
   }
 }
 
@@ -775,11 +861,14 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
 
 // ---------------------------------------------------------------- host
 
+constexpr int kShort = 4;  // steps of a block, at most, for work that counts as short
+
 struct Plan {
   const void *main, *join;
   int id;                    // of the variant
-  int CT, SP, smem, blocks, threads;  // columns of a tile, positions of a step; blocks of an SM
+  int CT, SP, smem, base_smem, blocks, threads;  // columns of a tile, positions of a step; blocks of an SM
   int n_ctiles, n_entries, items, grid, join_y, join_threads;
+  int cluster;               // blocks of an item's cluster; 0: the tiles of all items in equal runs
   size_t item_off, part_off, bytes;
 };
 
@@ -791,7 +880,7 @@ void take(Plan* pl) {
   pl->id = (HD == 64 ? 0 : 16) + (S::F32 ? 8 : 0) + NT;
   pl->CT = S::CT;
   pl->SP = S::SP;
-  pl->smem = S::SMEM;
+  pl->smem = pl->base_smem = S::SMEM;
   pl->blocks = B;
   pl->threads = 32 * W;
 }
@@ -829,7 +918,22 @@ bool plan_of(const mk_kv4_cache& c, int n_heads, int dtype, Plan* pl) {
   pl->n_ctiles = (int)ct;
   pl->n_entries = (int)entries;
   pl->items = (int)items;
-  pl->grid = (int)std::min<long long>((long long)pl->blocks * sm_count(), items * most);
+  const long long room = (long long)pl->blocks * sm_count();  // blocks that run at once
+  pl->cluster = 0;
+  if (items * most <= kShort * room) {
+    // Short work: an item is a cluster of up to 16 blocks, as many as run at
+    // once, joined through their shared memory.  It saves the second kernel and
+    // the scan of all lengths; a ragged batch is not levelled, which matters
+    // once the blocks have more than a few steps.
+    int n = 1;
+    while (n < 16 && 2 * n <= most && 2 * n * items <= room) n *= 2;
+    pl->cluster = n;
+    if (n > 1) pl->smem += n * ((pl->CT + n - 1) / n) * (c.head_dim + 2) * (int)sizeof(float);
+    pl->grid = (int)(items * n);
+    pl->item_off = pl->part_off = pl->bytes = 0;
+    return true;
+  }
+  pl->grid = (int)std::min<long long>(room, items * most);
   // an item is joined from about grid / items blocks: as many warps for each column
   int nw = 2;
   while (nw < 16 && nw * 2 * items <= pl->grid) nw *= 2;
@@ -848,7 +952,9 @@ cudaError_t allow_smem(const Plan& pl) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && (done[dev].load() >> pl.id & 1u)) return cudaSuccess;
-  e = cudaFuncSetAttribute(pl.main, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
+  // a cluster's blocks take 16 x (columns / 16, rounded up) partial columns more, at most
+  e = cudaFuncSetAttribute(pl.main, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.base_smem + (pl.CT + 16) * 130 * 4);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(pl.main, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev < 64) done[dev].fetch_or(1u << pl.id);
   return e;
 }
@@ -886,7 +992,7 @@ extern "C" MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, c
   Plan pl;
   if (!plan_of(*c, n_heads, dtype, &pl))
     return host_fail(MK_ERR_INVALID_ARG, "n_seqs x rows x n_heads or max_pages x n_kv_heads is too large");
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < pl.bytes)
+  if (pl.bytes && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < pl.bytes))
     return host_fail(MK_ERR_INVALID_ARG, "workspace is NULL, not 16-byte aligned or smaller than mk_kv4_attention_bytes");
   AttArgs p;
   p.a = kv4_args(*c);
@@ -899,24 +1005,45 @@ extern "C" MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, c
   p.cols = c->rows * p.gqa;
   p.n_ctiles = pl.n_ctiles;
   p.n_entries = pl.n_entries;
-  char* ws = static_cast<char*>(workspace);
-  p.total = reinterpret_cast<long long*>(ws);
-  p.item = reinterpret_cast<longlong2*>(ws + pl.item_off);
-  p.part = reinterpret_cast<float*>(ws + pl.part_off);
-  cudaError_t e = allow_smem(pl);
-  if (e == cudaSuccess) {
-    void* args[] = {&p};
-    e = cudaLaunchKernel(pl.main, dim3(pl.grid), dim3(pl.threads), args, pl.smem, (cudaStream_t)stream);
+  p.cluster = pl.cluster;
+  p.cluster_log = p.gqa_log = -1;
+  for (int i = 0; i < 13; ++i) {
+    if (pl.cluster == 1 << i) p.cluster_log = i;
+    if (p.gqa == 1 << i) p.gqa_log = i;
   }
+  p.total = nullptr;
+  p.item = nullptr;
+  p.part = nullptr;
+  if (!pl.cluster) {
+    char* ws = static_cast<char*>(workspace);
+    p.total = reinterpret_cast<long long*>(ws);
+    p.item = reinterpret_cast<longlong2*>(ws + pl.item_off);
+    p.part = reinterpret_cast<float*>(ws + pl.part_off);
+  }
+  cudaError_t e = allow_smem(pl);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  cfg.gridDim = dim3(pl.grid);
+  cfg.blockDim = dim3(pl.threads);
+  cfg.dynamicSmemBytes = pl.smem;
+  cfg.stream = (cudaStream_t)stream;
+  cfg.attrs = at;
   if (e == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
+    if (pl.cluster > 1) {
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = pl.cluster;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.numAttrs = 1;
+    }
+    void* args[] = {&p};
+    e = cudaLaunchKernelExC(&cfg, pl.main, args);
+  }
+  if (e == cudaSuccess && !pl.cluster) {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(pl.items, pl.join_y);
     cfg.blockDim = dim3(pl.join_threads);
-    cfg.stream = (cudaStream_t)stream;
-    cfg.attrs = at;
+    cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     void* args[] = {&p, &pl.CT, &pl.SP, &pl.grid};
     e = cudaLaunchKernelExC(&cfg, pl.join, args);

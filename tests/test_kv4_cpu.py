@@ -70,6 +70,8 @@ def test_rows_and_types_are_refused(lib):
         assert code(L.mk_kv4_attention, c, 2, rows(), L.MK_BF16, scale, rows(), None, 0x8000, 1 << 40) == inv
     assert code(L.mk_kv4_store, None, rows(), rows(), L.MK_BF16) == inv
     # a workspace that is missing, misaligned or too small
+    assert L.mk_kv4_attention_bytes(c, 2, L.MK_BF16) == 0      # short work needs none
+    c = cache(n_pages=1 << 20, max_pages=1 << 20)
     need = L.mk_kv4_attention_bytes(c, 2, L.MK_BF16)
     assert need > 0
     for ws, n in ((0, need), (0x8008, need), (0x8000, need - 1)):
