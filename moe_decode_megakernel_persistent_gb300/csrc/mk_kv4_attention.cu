@@ -332,8 +332,12 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     load_q(seq, e - seq * p.n_ctiles, head);
     run.base = 0;
     run.e = e;
-    lo = run.pos = (long long)head * nt + (nt * rank >> p.cluster_log);
-    run.hi = (long long)head * nt + (nt * (rank + 1) >> p.cluster_log);
+    run.head = head;
+    run.nt = nt;
+    run.t0 = nt * rank >> p.cluster_log;
+    run.t1 = nt * (rank + 1) >> p.cluster_log;
+    lo = run.pos = run.t0;
+    run.hi = run.t1;
     pages[tid] = page;
   } else if (w == 0) {  // this block's share of all tiles
     long long total = 0;
@@ -384,17 +388,22 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
   // Address of the block's step i, looked up by one thread (all of a window at once).
   auto look_up = [&](uint32_t i) {
     Runs r = mine;
-    r.pos += i;
-    if (!r.next(p, CT, SP)) return;
-    const int at = r.t0 * SP / kPageTokens;
     int pg;
-    if (p.cluster && at < NTHR) {
-      pg = pages[at];
-      if (pg < 0 || pg >= p.a.n_pages) {
-        refuse(p.a.status);
-        pg = -1;
+    if (p.cluster) {
+      r.t0 += i;
+      const int at = r.t0 * SP / kPageTokens;
+      if (at < NTHR) {
+        pg = pages[at];
+        if (pg < 0 || pg >= p.a.n_pages) {
+          refuse(p.a.status);
+          pg = -1;
+        }
+      } else {
+        pg = page_of(p.a, p.n_ctiles == 1 ? r.e : r.e / p.n_ctiles, r.t0 * SP);
       }
     } else {
+      r.pos += i;
+      if (!r.next(p, CT, SP)) return;
       pg = page_of(p.a, p.n_ctiles == 1 ? r.e : r.e / p.n_ctiles, r.t0 * SP);
     }
     list[i % kList] = pg < 0 ? 0 : (unsigned long long)tile_of<HD>(p.a, pg, r.head, r.t0 * SP);
@@ -421,7 +430,8 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
   __syncthreads();
   if (p.cluster > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 
-  while (run.next(p, CT, SP)) {
+  // a cluster's block has one run, set above
+  for (bool more = p.cluster ? n_steps > 0 : run.next(p, CT, SP); more; more = !p.cluster && run.next(p, CT, SP)) {
     const int seq = p.n_ctiles == 1 ? run.e : run.e / p.n_ctiles, j = run.e - seq * p.n_ctiles;
     int len, nn;
     seq_extent(p.a, seq, len, nn);
@@ -675,7 +685,8 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     for (int t = run.t0; t < run.t1; ++t, ++k) {
       if (k % (kList / 2) == 0 && k) {  // half of the addresses are used up: the next ones
         asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
-        for (uint32_t i = tid; i < kList / 2; i += NTHR) look_up(k + kList / 2 + i);
+        for (uint32_t i = tid; i < kList / 2; i += NTHR)
+          if (k + kList / 2 + i < n_steps) look_up(k + kList / 2 + i);
         asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
       }
       // the stage of the last step is refilled as soon as all warps have left it
@@ -776,20 +787,27 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     cluster_sync();
     for (int x = tid; x < slots * (HD / 2); x += NTHR) {
       const int sl = x / (HD / 2), d = x % (HD / 2) * 2, c = (sl << p.cluster_log) + rank;
-      if (c >= ncol) break;
-      float M = kLow, l_sum = 0.f;
-      float2 v = make_float2(0.f, 0.f);
-#pragma unroll 4
-      for (int r = 0; r < p.cluster; ++r) M = fmaxf(M, fin[(r * slots + sl) * S::RS + HD]);
-#pragma unroll 4
-      for (int r = 0; r < p.cluster; ++r) {
-        const float* from = fin + (r * slots + sl) * S::RS;
-        const float2 ml = *reinterpret_cast<const float2*>(from + HD), y = *reinterpret_cast<const float2*>(from + d);
-        const float f = exp2_fast(ml.x - M);
-        if (ml.x != kLow || ml.y != 0.f) {
-          l_sum += ml.y * f;
-          v.x += y.x * f, v.y += y.y * f;
-        }
+      if (c >= ncol) break;  // (a warp's elements are of one column)
+      // lane r takes block r's maximum and sum, every lane all blocks' values
+      const float* from = fin + sl * S::RS;
+      float2 ml = make_float2(kLow, 0.f);
+      if ((lane & 15) < p.cluster) ml = *reinterpret_cast<const float2*>(from + (lane & 15) * slots * S::RS + HD);
+      float M = ml.x;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const uint32_t some = __ballot_sync(0xffffffffu, ml.x != kLow || ml.y != 0.f);  // others have stored no values
+      const float f = exp2_fast(ml.x - M);
+      float l_sum = ml.y * f;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) l_sum += __shfl_xor_sync(0xffffffffu, l_sum, o);
+      float2 y[16], v = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        y[r] = some >> r & 1u ? *reinterpret_cast<const float2*>(from + r * slots * S::RS + d) : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float fr = __shfl_sync(0xffffffffu, f, r);
+        if (some >> r & 1u) v.x += y[r].x * fr, v.y += y[r].y * fr;
       }
       put_out(seq, j * CT + c, head, d, M, l_sum, v);
     }
