@@ -185,6 +185,20 @@ MK_API int mk_pack_weights(const mk_model_desc* d, const mk_weights* w, void* ds
  * Errors: INVALID_ARG, STATE, CUDA. */
 MK_API int mk_kv_alloc(mk_ctx* ctx, int32_t n_pages);
 
+/* mk_kv_alloc with a choice of the cache's format: MK_BF16 (what mk_kv_alloc
+ * makes), or MK_INT4_G64 for the 4-bit cache (its format and sizes are with
+ * mk_kv4_store below; pages of all layers [layer][page]), which takes 17 / 64 of
+ * the bytes.  Every call of the context works on either.  With the 4-bit cache
+ * a new position's K and V are rounded to bf16, then to 4 bits, before it
+ * attends; a decode step is one launch of the step kernel per layer (o_proj to
+ * the next layer's QKV) with the cache's store and attention between them,
+ * chunks of more than 16 positions store and attend layer by layer;
+ * mk_kv_write rounds what it stores and mk_kv_read returns what the codes stand
+ * for, rounded to bf16.  MK_DBG_TIMING is refused (MK_ERR_UNSUPPORTED, by the
+ * launching call).  Also allocates a step's staging and workspace.
+ * Errors: INVALID_ARG, STATE, CUDA. */
+MK_API int mk_kv_alloc_fmt(mk_ctx* ctx, int32_t n_pages, int32_t format);
+
 /* Prefill: run n (1..4096) prompt tokens of sequence seq_id at positions
  * start_pos .. start_pos+n-1 through the model, writing their K/V into
  * pages taken from the pool.  The chunk limit follows "rec Megakernel and
@@ -262,6 +276,28 @@ MK_API int mk_kv_read(mk_ctx* ctx, int32_t seq_id, int32_t start_pos, int32_t n,
  * block-table entries with a kernel on `stream`.
  * Errors: INVALID_ARG, STATE, CUDA. */
 MK_API int mk_seq_fork(mk_ctx* ctx, int32_t src_seq, int32_t dst_seq, int32_t n_tokens, void* stream);
+
+/* mk_seq_fork at any n_tokens in 1 .. src_seq's length: whole pages are shared,
+ * a partly filled last one is copied into a page from the pool (so that either
+ * sequence goes on writing in a page of its own).  A prompt then reuses a cached
+ * prefix to the token.  Errors: as mk_seq_fork, NO_PAGES (nothing is done). */
+MK_API int mk_seq_fork_at(mk_ctx* ctx, int32_t src_seq, int32_t dst_seq, int32_t n_tokens, void* stream);
+
+/* Drop a sequence's positions from n_tokens (1 .. its length) on: drafted tokens
+ * that were rejected, or a conversation taken back.  Pages behind them return
+ * to the pool (shared ones stay with their other holders); a partly filled last
+ * page that another sequence holds too is first copied into one from the pool.
+ * The freed pages become reusable by launches enqueued after this call.
+ * Errors: INVALID_ARG, STATE (not open), NO_PAGES (nothing is done), CUDA. */
+MK_API int mk_seq_truncate(mk_ctx* ctx, int32_t seq_id, int32_t n_tokens, void* stream);
+
+/* Move the pages in use to the lowest page numbers (each move a copy of the page
+ * in every layer) and enter them in the block table, so that pages
+ * 0 .. n_pages - free_pages - 1 are the ones in use and one range of the pool
+ * holds all of the cache.  What the sequences hold does not change.
+ * *moved_out (may be NULL) receives the number of pages moved.  Enqueues on
+ * `stream`.  Errors: INVALID_ARG, STATE, CUDA. */
+MK_API int mk_kv_compact(mk_ctx* ctx, int32_t* moved_out, void* stream);
 
 /* Current length (positions written) of a sequence; -1 if it is not open. */
 MK_API int32_t mk_seq_length(mk_ctx* ctx, int32_t seq_id);

@@ -84,6 +84,7 @@ class mk_kv4_rows(C.Structure):
 SIGNATURES = {
     "mk_create": (C.c_int, [C.POINTER(mk_model_desc), C.POINTER(mk_weights), C.POINTER(C.c_void_p)]),
     "mk_kv_alloc": (C.c_int, [C.c_void_p, C.c_int32]),
+    "mk_kv_alloc_fmt": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32]),
     "mk_prefill_chunk": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_int32,
                                    C.c_void_p, C.c_void_p]),
     "mk_decode_step": (C.c_int, [C.c_void_p, C.POINTER(C.c_int32), C.c_void_p,
@@ -92,6 +93,9 @@ SIGNATURES = {
     "mk_kv_write": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p]),
     "mk_kv_read": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p]),
     "mk_seq_fork": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p]),
+    "mk_seq_fork_at": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p]),
+    "mk_seq_truncate": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_void_p]),
+    "mk_kv_compact": (C.c_int, [C.c_void_p, C.POINTER(C.c_int32), C.c_void_p]),
     "mk_seq_length": (C.c_int32, [C.c_void_p, C.c_int32]),
     "mk_sync": (C.c_int, [C.c_void_p, C.c_void_p]),
     "mk_set_debug": (C.c_int, [C.c_void_p, C.c_uint32, C.c_uint32, C.c_void_p, C.c_size_t,
@@ -183,6 +187,10 @@ def mk_kv_alloc(ctx: int, n_pages: int):
     _check(load().mk_kv_alloc(ctx, n_pages))
 
 
+def mk_kv_alloc_fmt(ctx: int, n_pages: int, fmt: int):
+    _check(load().mk_kv_alloc_fmt(ctx, n_pages, fmt))
+
+
 def mk_prefill_chunk(ctx: int, seq_id: int, tokens_dev: int, n: int, start_pos: int,
                      out_token_dev: int | None, stream: int = 0):
     _check(load().mk_prefill_chunk(ctx, seq_id, tokens_dev, n, start_pos, out_token_dev, stream))
@@ -209,6 +217,21 @@ def mk_kv_read(ctx: int, seq_id: int, start_pos: int, n: int, dst_dev: int, stre
 
 def mk_seq_fork(ctx: int, src_seq: int, dst_seq: int, n_tokens: int, stream: int = 0):
     _check(load().mk_seq_fork(ctx, src_seq, dst_seq, n_tokens, stream))
+
+
+def mk_seq_fork_at(ctx: int, src_seq: int, dst_seq: int, n_tokens: int, stream: int = 0):
+    _check(load().mk_seq_fork_at(ctx, src_seq, dst_seq, n_tokens, stream))
+
+
+def mk_seq_truncate(ctx: int, seq_id: int, n_tokens: int, stream: int = 0):
+    _check(load().mk_seq_truncate(ctx, seq_id, n_tokens, stream))
+
+
+def mk_kv_compact(ctx: int, stream: int = 0) -> int:
+    """Returns the number of pages moved."""
+    moved = C.c_int32()
+    _check(load().mk_kv_compact(ctx, C.byref(moved), stream))
+    return moved.value
 
 
 def mk_seq_length(ctx: int, seq_id: int) -> int:

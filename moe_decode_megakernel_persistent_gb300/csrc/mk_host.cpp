@@ -74,6 +74,11 @@ struct mk_ctx {
   uint16_t* kv_dev = nullptr;
   int32_t n_pages = 0;
   size_t kv_bytes = 0;
+  int kv_format = MK_BF16;          // MK_BF16, or MK_INT4_G64: the 4-bit cache
+  uint16_t* kv_stage = nullptr;     // 4-bit: one layer's new K/V of a step, one bf16 page for each row
+  int32_t* kv_seqs = nullptr;       // 4-bit: lengths, then block-table rows, of the call's sequences
+  void* kv_ws = nullptr;            // 4-bit: the attention's workspace of a step
+  size_t kv_ws_bytes = 0;
   std::vector<int32_t> free_pages;  // stack; back() is handed out next
   std::vector<int32_t> page_ref;    // sequences holding each page (forked sequences share pages)
   int32_t* block_table_dev = nullptr;
@@ -209,7 +214,89 @@ void attention_split(const mk_ctx* c, const int32_t* pos, int n, int* chunk, int
   host_attention_split_impl(c->d.n_kv_heads, c->grid, c->kern.tile_tokens, pos, n, chunk, units);
 }
 
-// One launch over `n` rows.  Pages for positions that start a new page are
+// Bytes of one page of one layer.
+size_t kv_page_bytes(const mk_ctx* c) {
+  return c->kv_format == MK_INT4_G64 ? mk_kv4_page_bytes(c->d.n_kv_heads, c->d.head_dim)
+                                     : sizeof(uint16_t) * 2 * (size_t)c->d.n_kv_heads * kPageTokens * c->d.head_dim;
+}
+
+// The 4-bit cache's kernels' arguments for layer l: n_seqs sequences (entered
+// by launch_step_seqs) of `rows` new rows, lengths at most `longest`.
+Kv4Args kv4_args_of(const mk_ctx* c, int l, int n_seqs, int rows, int longest) {
+  Kv4Args k{};
+  k.pool = reinterpret_cast<uint8_t*>(c->kv_dev) + (size_t)l * c->n_pages * kv_page_bytes(c);
+  k.table = c->block_table_dev;
+  k.lengths = c->kv_seqs;
+  k.status = c->sc.err;
+  k.n_pages = c->n_pages;
+  k.n_kv_heads = c->d.n_kv_heads;
+  k.n_seqs = n_seqs;
+  k.max_pages = (longest + kPageTokens - 1) / kPageTokens;
+  k.rows = rows;
+  k.slots = c->kv_seqs + kMaxBatch;
+  k.table_stride = c->max_pages_per_seq;
+  return k;
+}
+
+// A step over the 4-bit cache.  The step kernel's phases run as they are, but
+// for attention: the QKV phase leaves its K/V (bf16) in one page per row, and
+// between it and o_proj the rows are stored in 4 bits and attend to the cache.
+// One launch of the step kernel covers o_proj to the next layer's QKV.
+template <class Go>
+int launch_kv4(mk_ctx* c, StepArgs& a, int n, cudaStream_t st, const Go& go) {
+  const mk_model_desc& d = c->d;
+  const int QD = d.n_heads * d.head_dim, slot_row = d.head_dim;
+  const bool chunk = n > 1 && a.slot[0] == a.slot[1];  // rows of one sequence, else one row each of n
+  const long long page = 2ll * d.n_kv_heads * kPageTokens * d.head_dim;  // elements of a staged page
+  StepSeqs q{};
+  int longest = 0;
+  q.n = chunk ? 1 : n;
+  for (int i = 0; i < n; ++i) {
+    if (chunk && a.pos[i] != a.pos[0] + i) return fail(MK_ERR_STATE, "rows of one sequence must be consecutive");
+    longest = std::max(longest, a.pos[i] + 1);
+    q.slot[i] = a.slot[i];
+    q.len[i] = a.pos[i] + 1;
+    a.cur_page[i] = i;
+  }
+  if (chunk) q.len[0] = longest;
+  if (int r = launch_step_seqs(q, c->kv_seqs, c->kv_seqs + kMaxBatch, st)) return r;
+  a.n_units = 0;  // no attention in the step kernel
+  a.n_pages = kMaxBatch;
+  const size_t layer = (size_t)kMaxBatch * page;  // the kernel adds this much for each layer
+  const float scale = 1.f / std::sqrt((float)d.head_dim);
+  const bool split = c->dbg_flags & MK_DBG_SPLIT;
+  for (int l = 0; l <= d.n_layers; ++l) {
+    // the rest of layer l - 1, then layer l's QKV (or lm_head)
+    const int lo = l ? 4 * l - 2 : 0, hi = l < d.n_layers ? 4 * l + 1 : 4 * l, lm = l == d.n_layers;
+    a.kv = reinterpret_cast<uint16_t*>(reinterpret_cast<uintptr_t>(c->kv_stage) - sizeof(uint16_t) * layer * l);
+    cudaError_t e = cudaSuccess;
+    if (split) {
+      for (int s = lo; s < hi && e == cudaSuccess; ++s) e = go(s, s + 1, 0);
+      if (e == cudaSuccess && lm) e = go(hi, hi, 1);
+    } else {
+      e = go(lo, hi, lm);
+    }
+    if (e != cudaSuccess) return fail(MK_ERR_CUDA, std::string("cudaLaunchCooperativeKernel: ") + cudaGetErrorString(e));
+    if (lm) break;
+    const Kv4Args k = kv4_args_of(c, l, q.n, chunk ? n : 1, longest);
+    const Kv4Rows kr{c->kv_stage, chunk ? 0 : page, chunk ? page : 0, (long long)kPageTokens * d.head_dim, slot_row};
+    Kv4Rows vr = kr;
+    vr.p = c->kv_stage + page / 2;
+    if (int r = kv4_store(k, d.head_dim, kr, vr, MK_BF16, st)) return r;
+    const Kv4Rows qr{a.sc.q, chunk ? 0 : QD, chunk ? QD : 0, d.head_dim, 0};
+    const Kv4Rows out{a.sc.attn, qr.seq, qr.row, qr.head, 0};
+    if (int r = kv4_attention(k, d.head_dim, d.n_heads, qr, MK_F32, scale, out, nullptr, c->kv_ws, c->kv_ws_bytes, st))
+      return r;
+    if (a.trace) {
+      float* to = a.trace + (size_t)d.n_layers * n * d.hidden + (size_t)l * n * QD;
+      e = cudaMemcpyAsync(to, a.sc.attn, sizeof(float) * n * QD, cudaMemcpyDeviceToDevice, st);
+      if (e != cudaSuccess) return fail(MK_ERR_CUDA, std::string("attention trace: ") + cudaGetErrorString(e));
+    }
+  }
+  return MK_OK;
+}
+
+// One launch over `n` rows (a 4-bit cache: one for each layer).  Pages for positions that start a new page are
 // taken from the pool here (rolled back if the pool runs dry).
 int launch(mk_ctx* c, const int32_t* slots, const int32_t* positions, int n,
            const int32_t* tokens_dev, int32_t* out_dev, int out_first, cudaStream_t st) {
@@ -219,6 +306,8 @@ int launch(mk_ctx* c, const int32_t* slots, const int32_t* positions, int n,
   if ((c->dbg_flags & MK_DBG_TIMING) &&
       c->trace_bytes < sizeof(uint64_t) * (size_t)c->grid * (16 * (size_t)c->d.n_layers + 2 + 3 * kRingLog))
     return fail(MK_ERR_INVALID_ARG, "timing buffer is smaller than 8 * grid * (16 * n_layers + 2 + 3072) bytes");
+  if ((c->dbg_flags & MK_DBG_TIMING) && c->kv_format != MK_BF16)
+    return fail(MK_ERR_UNSUPPORTED, "MK_DBG_TIMING needs the bf16 cache (its stamps are of the one launch of a step)");
   StepArgs a;
   std::memset(&a, 0, sizeof(a));
   std::vector<std::pair<int, int32_t>> taken;  // (slot, page) handed out by this call
@@ -306,6 +395,14 @@ int launch(mk_ctx* c, const int32_t* slots, const int32_t* positions, int n,
   };
   const int groups = 4 * c->d.n_layers;
   cudaError_t e = cudaSuccess;
+  if (c->kv_format != MK_BF16) {
+    if (int r = launch_kv4(c, a, n, st, go)) {
+      rollback();
+      return r;
+    }
+    c->last_chunk = c->last_units = 0;
+    return MK_OK;
+  }
   if (c->dbg_flags & MK_DBG_SPLIT) {
     // one launch per phase group, then lm_head: kernel boundaries in place of
     // the grid barriers between groups
@@ -511,23 +608,51 @@ MK_API int mk_create(const mk_model_desc* d, const mk_weights* w, mk_ctx** out) 
   return MK_OK;
 }
 
-MK_API int mk_kv_alloc(mk_ctx* c, int32_t n_pages) {
+MK_API int mk_kv_alloc(mk_ctx* c, int32_t n_pages) { return mk_kv_alloc_fmt(c, n_pages, MK_BF16); }
+
+MK_API int mk_kv_alloc_fmt(mk_ctx* c, int32_t n_pages, int32_t format) {
   g_err.clear();
   if (!c) return fail(MK_ERR_INVALID_ARG, "ctx is NULL");
   if (n_pages < 1) return fail(MK_ERR_INVALID_ARG, "n_pages must be >= 1");
+  if (format != MK_BF16 && format != MK_INT4_G64)
+    return fail(MK_ERR_INVALID_ARG, "the cache's format must be MK_BF16 or MK_INT4_G64");
   if (c->kv_dev) return fail(MK_ERR_STATE, "the KV pool is already allocated");
   const mk_model_desc& d = c->d;
-  c->kv_bytes = sizeof(uint16_t) * (size_t)d.n_layers * n_pages * 2 * d.n_kv_heads * kPageTokens * d.head_dim;
-  MK_CUDA(cudaMalloc(&c->kv_dev, c->kv_bytes));
+  c->kv_format = format;
+  c->kv_bytes = (size_t)d.n_layers * n_pages * kv_page_bytes(c);
   const size_t bt = sizeof(int32_t) * (size_t)d.max_seqs * c->max_pages_per_seq;
-  cudaError_t e = cudaMalloc(&c->block_table_dev, bt);
+  cudaError_t e = cudaMalloc(&c->kv_dev, c->kv_bytes);
+  if (e == cudaSuccess) e = cudaMalloc(&c->block_table_dev, bt);
   if (e == cudaSuccess) e = cudaMemset(c->block_table_dev, 0xFF, bt);
+  if (format == MK_INT4_G64) {
+    // the step's workspace: the largest of any number of rows and of any lengths
+    Kv4Args k{};
+    k.n_kv_heads = d.n_kv_heads;
+    k.max_pages = c->max_pages_per_seq;
+    c->kv_ws_bytes = 0;
+    for (int n = 1; n <= kMaxBatch; ++n)
+      for (int one = 0; one < 2; ++one) {
+        size_t b = 0;
+        k.n_seqs = one ? 1 : n;
+        k.rows = one ? n : 1;
+        if (kv4_attention_bytes(k, d.head_dim, d.n_heads, MK_F32, &b)) c->kv_ws_bytes = std::max(c->kv_ws_bytes, b);
+      }
+    if (e == cudaSuccess)
+      e = cudaMalloc(&c->kv_stage, sizeof(uint16_t) * kMaxBatch * 2 * (size_t)d.n_kv_heads * kPageTokens * d.head_dim);
+    if (e == cudaSuccess) e = cudaMalloc(&c->kv_seqs, sizeof(int32_t) * 2 * kMaxBatch);
+    if (e == cudaSuccess && c->kv_ws_bytes) e = cudaMalloc(&c->kv_ws, c->kv_ws_bytes);
+    // codes and scales of slots that nothing has stored are never read, but a
+    // page copy carries them
+    if (e == cudaSuccess) e = cudaMemset(c->kv_dev, 0, c->kv_bytes);
+  }
   if (e != cudaSuccess) {
-    cudaFree(c->kv_dev);
-    cudaFree(c->block_table_dev);
-    c->kv_dev = nullptr;
-    c->block_table_dev = nullptr;
-    return fail(MK_ERR_CUDA, std::string("block table: ") + cudaGetErrorString(e));
+    void* bufs[] = {c->kv_dev, c->block_table_dev, c->kv_stage, c->kv_seqs, c->kv_ws};
+    for (void* b : bufs) cudaFree(b);
+    c->kv_dev = c->kv_stage = nullptr;
+    c->block_table_dev = c->kv_seqs = nullptr;
+    c->kv_ws = nullptr;
+    c->kv_format = MK_BF16;
+    return fail(MK_ERR_CUDA, std::string("KV pool: ") + cudaGetErrorString(e));
   }
   c->n_pages = n_pages;
   c->page_ref.assign(n_pages, 0);
@@ -590,7 +715,21 @@ static int prefill_gemm_chunk(mk_ctx* c, int32_t seq_id, const int32_t* tokens_d
   a.final_norm = c->final_norm;
   a.lm_pk = c->lm_pk;
   a.rope = c->rope_dev;
-  a.kv = c->kv_dev;
+  if (c->kv_format == MK_INT4_G64) {
+    a.kv4 = reinterpret_cast<uint8_t*>(c->kv_dev);
+    a.kv4_len = c->kv_seqs;
+    a.kv4_slot = c->kv_seqs + kMaxBatch;
+    StepSeqs q{};
+    q.n = 1;
+    q.len[0] = start_pos + n;
+    q.slot[0] = seq_id;
+    if (int r = launch_step_seqs(q, c->kv_seqs, c->kv_seqs + kMaxBatch, st)) {
+      rollback();
+      return r;
+    }
+  } else {
+    a.kv = c->kv_dev;
+  }
   a.block_table = c->block_table_dev;
   a.n_pages = c->n_pages;
   a.max_pages_per_seq = c->max_pages_per_seq;
@@ -709,6 +848,36 @@ static KvXfer xfer_base(const mk_ctx* c, int32_t seq_id) {
   return x;
 }
 
+// Enter pages of a sequence in its block-table row, from page index `first` on.
+static int enter_pages(const mk_ctx* c, int32_t seq_id, int first, const int32_t* pages, int n, cudaStream_t st) {
+  for (int i0 = 0; i0 < n; i0 += kMaxUpd) {
+    KvXfer x = xfer_base(c, seq_id);
+    x.upd_index0 = first + i0;
+    for (int i = i0; i < std::min(n, i0 + kMaxUpd); ++i) x.upd[x.n_upd++] = PageUpd{seq_id, first + i, pages[i]};
+    if (int r = launch_kv_xfer(x, st)) return r;
+  }
+  return MK_OK;
+}
+
+// K/V of positions [start, start + n) of a sequence of the 4-bit cache, between
+// its pages and a caller's buffer [n_layers][n][K|V][n_kv_heads][head_dim].
+static int kv4_rows_of_seq(const mk_ctx* c, int32_t seq_id, int32_t start, int32_t n, const uint16_t* buf, bool store,
+                           cudaStream_t st) {
+  StepSeqs q{};
+  q.n = 1;
+  q.len[0] = start + n;
+  q.slot[0] = seq_id;
+  if (int r = launch_step_seqs(q, c->kv_seqs, c->kv_seqs + kMaxBatch, st)) return r;
+  const long long kd = (long long)c->d.n_kv_heads * c->d.head_dim;
+  for (int l = 0; l < c->d.n_layers; ++l) {
+    const Kv4Args k = kv4_args_of(c, l, 1, n, start + n);
+    const uint16_t* at = buf + (size_t)l * n * 2 * kd;
+    const Kv4Rows kr{at, 0, 2 * kd, c->d.head_dim, 0}, vr{at + kd, 0, 2 * kd, c->d.head_dim, 0};
+    if (int r = (store ? kv4_store : kv4_load)(k, c->d.head_dim, kr, vr, MK_BF16, st)) return r;
+  }
+  return MK_OK;
+}
+
 MK_API int mk_kv_write(mk_ctx* c, int32_t seq_id, int32_t start_pos, int32_t n, const void* src_dev,
                        void* stream) {
   g_err.clear();
@@ -727,6 +896,27 @@ MK_API int mk_kv_write(mk_ctx* c, int32_t seq_id, int32_t start_pos, int32_t n, 
   const int have = (int)q.pages.size();
   const int need = (start_pos + n + kPageTokens - 1) / kPageTokens - have;
   if (need > (int)c->free_pages.size()) return fail(MK_ERR_NO_PAGES, "KV page pool exhausted");
+  if (c->kv_format == MK_INT4_G64) {
+    for (int i = 0; i < need; ++i) {
+      const int32_t pg = c->free_pages.back();
+      c->free_pages.pop_back();
+      c->page_ref[pg] = 1;
+      q.pages.push_back(pg);
+    }
+    int r = enter_pages(c, seq_id, have, q.pages.data() + have, std::max(need, 0), (cudaStream_t)stream);
+    if (!r) r = kv4_rows_of_seq(c, seq_id, start_pos, n, static_cast<const uint16_t*>(src_dev), true, (cudaStream_t)stream);
+    if (r) {
+      for (int i = 0; i < need; ++i) {
+        c->page_ref[q.pages.back()] = 0;
+        c->free_pages.push_back(q.pages.back());
+        q.pages.pop_back();
+      }
+      return r;
+    }
+    q.open = true;
+    q.len = std::max(q.len, start_pos + n);
+    return MK_OK;
+  }
   // segments of at most kMaxUpd - 1 pages, so one launch carries every new page it touches
   const int seg = (kMaxUpd - 1) * kPageTokens;
   const uint16_t* src = static_cast<const uint16_t*>(src_dev);
@@ -791,6 +981,8 @@ MK_API int mk_kv_read(mk_ctx* c, int32_t seq_id, int32_t start_pos, int32_t n, v
   const Seq& q = c->seqs[seq_id];
   if (!q.open || start_pos < 0 || (long long)start_pos + n > q.len)
     return fail(MK_ERR_STATE, "positions must lie within the open sequence");
+  if (c->kv_format == MK_INT4_G64)
+    return kv4_rows_of_seq(c, seq_id, start_pos, n, static_cast<const uint16_t*>(dst_dev), false, (cudaStream_t)stream);
   KvXfer x = xfer_base(c, seq_id);
   x.start = start_pos;
   x.n = n;
@@ -799,7 +991,9 @@ MK_API int mk_kv_read(mk_ctx* c, int32_t seq_id, int32_t start_pos, int32_t n, v
   return launch_kv_xfer(x, (cudaStream_t)stream);
 }
 
-MK_API int mk_seq_fork(mk_ctx* c, int32_t src_seq, int32_t dst_seq, int32_t n_tokens, void* stream) {
+// Open dst as src's first n positions: whole pages shared, a partly filled last
+// one copied.
+static int seq_fork(mk_ctx* c, int32_t src_seq, int32_t dst_seq, int32_t n_tokens, bool whole_pages, void* stream) {
   g_err.clear();
   if (!c) return fail(MK_ERR_INVALID_ARG, "ctx is NULL");
   if (src_seq < 0 || src_seq >= c->d.max_seqs || dst_seq < 0 || dst_seq >= c->d.max_seqs || src_seq == dst_seq)
@@ -809,19 +1003,109 @@ MK_API int mk_seq_fork(mk_ctx* c, int32_t src_seq, int32_t dst_seq, int32_t n_to
   Seq& b = c->seqs[dst_seq];
   if (!a.open) return fail(MK_ERR_STATE, "source sequence is not open");
   if (b.open) return fail(MK_ERR_STATE, "destination sequence is already open");
-  if (n_tokens < kPageTokens || n_tokens % kPageTokens != 0 || n_tokens > a.len)
+  if (whole_pages && (n_tokens < kPageTokens || n_tokens % kPageTokens != 0 || n_tokens > a.len))
     return fail(MK_ERR_INVALID_ARG, "n_tokens must be a positive multiple of 128 within the source's length");
+  if (n_tokens < 1 || n_tokens > a.len) return fail(MK_ERR_INVALID_ARG, "n_tokens must be within 1 .. the source's length");
   const int np = n_tokens / kPageTokens;
-  for (int i0 = 0; i0 < np; i0 += kMaxUpd) {
-    KvXfer x = xfer_base(c, dst_seq);
-    x.upd_index0 = i0;
-    for (int i = i0; i < std::min(np, i0 + kMaxUpd); ++i) x.upd[x.n_upd++] = PageUpd{dst_seq, i, a.pages[i]};
-    if (int r = launch_kv_xfer(x, (cudaStream_t)stream)) return r;
+  std::vector<int32_t> pages(a.pages.begin(), a.pages.begin() + np);
+  if (n_tokens % kPageTokens) {
+    if (c->free_pages.empty()) return fail(MK_ERR_NO_PAGES, "KV page pool exhausted");
+    pages.push_back(c->free_pages.back());
+    if (int r = launch_page_copy(c->kv_dev, c->d.n_layers, c->n_pages, kv_page_bytes(c), &a.pages[np], &pages.back(), 1,
+                                 (cudaStream_t)stream))
+      return r;
   }
-  b.pages.assign(a.pages.begin(), a.pages.begin() + np);
-  for (int32_t pg : b.pages) ++c->page_ref[pg];
+  if (int r = enter_pages(c, dst_seq, 0, pages.data(), (int)pages.size(), (cudaStream_t)stream)) return r;
+  if ((int)pages.size() > np) c->free_pages.pop_back();
+  for (int32_t pg : pages) ++c->page_ref[pg];
+  b.pages = pages;
   b.open = true;
   b.len = n_tokens;
+  return MK_OK;
+}
+
+MK_API int mk_seq_fork(mk_ctx* c, int32_t src_seq, int32_t dst_seq, int32_t n_tokens, void* stream) {
+  return seq_fork(c, src_seq, dst_seq, n_tokens, true, stream);
+}
+
+MK_API int mk_seq_fork_at(mk_ctx* c, int32_t src_seq, int32_t dst_seq, int32_t n_tokens, void* stream) {
+  return seq_fork(c, src_seq, dst_seq, n_tokens, false, stream);
+}
+
+MK_API int mk_seq_truncate(mk_ctx* c, int32_t seq_id, int32_t n_tokens, void* stream) {
+  g_err.clear();
+  if (!c) return fail(MK_ERR_INVALID_ARG, "ctx is NULL");
+  if (seq_id < 0 || seq_id >= c->d.max_seqs) return fail(MK_ERR_INVALID_ARG, "seq_id out of range");
+  Seq& q = c->seqs[seq_id];
+  if (!q.open) return fail(MK_ERR_STATE, "sequence is not open");
+  if (n_tokens < 1 || n_tokens > q.len) return fail(MK_ERR_INVALID_ARG, "n_tokens must be within 1 .. the sequence's length");
+  const int keep = (n_tokens + kPageTokens - 1) / kPageTokens;
+  // the next position goes into the last kept page: one that another sequence
+  // holds too is copied first
+  const int last = keep - 1;
+  if (n_tokens % kPageTokens && c->page_ref[q.pages[last]] > 1) {
+    if (c->free_pages.empty()) return fail(MK_ERR_NO_PAGES, "KV page pool exhausted");
+    const int32_t pg = c->free_pages.back();
+    if (int r = launch_page_copy(c->kv_dev, c->d.n_layers, c->n_pages, kv_page_bytes(c), &q.pages[last], &pg, 1,
+                                 (cudaStream_t)stream))
+      return r;
+    if (int r = enter_pages(c, seq_id, last, &pg, 1, (cudaStream_t)stream)) return r;
+    c->free_pages.pop_back();
+    --c->page_ref[q.pages[last]];
+    c->page_ref[pg] = 1;
+    q.pages[last] = pg;
+  }
+  while ((int)q.pages.size() > keep) {
+    if (--c->page_ref[q.pages.back()] == 0) c->free_pages.push_back(q.pages.back());
+    q.pages.pop_back();
+  }
+  q.len = n_tokens;
+  return MK_OK;
+}
+
+MK_API int mk_kv_compact(mk_ctx* c, int32_t* moved_out, void* stream) {
+  g_err.clear();
+  if (moved_out) *moved_out = 0;
+  if (!c) return fail(MK_ERR_INVALID_ARG, "ctx is NULL");
+  if (!c->kv_dev) return fail(MK_ERR_STATE, "mk_kv_alloc has not been called");
+  int32_t live = 0;
+  for (int32_t r : c->page_ref) live += r > 0;
+  std::vector<int32_t> src, dst, to(c->n_pages);
+  for (int32_t p = 0, f = 0; p < c->n_pages; ++p) {
+    to[p] = p;
+    if (p < live || c->page_ref[p] == 0) continue;
+    while (c->page_ref[f] > 0) ++f;  // a free page below `live`: there is one for each live page above
+    src.push_back(p);
+    dst.push_back(f);
+    to[p] = f++;
+  }
+  if (src.empty()) return MK_OK;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (int r = launch_page_copy(c->kv_dev, c->d.n_layers, c->n_pages, kv_page_bytes(c), src.data(), dst.data(), (int)src.size(), st))
+    return r;
+  // the block table's entries of the moved pages, whatever sequences they are of
+  KvXfer x = xfer_base(c, 0);
+  for (size_t s = 0; s < c->seqs.size(); ++s)
+    for (size_t i = 0; i < c->seqs[s].pages.size(); ++i) {
+      const int32_t pg = c->seqs[s].pages[i];
+      if (to[pg] == pg) continue;
+      x.upd[x.n_upd++] = PageUpd{(int32_t)s, (int32_t)i, to[pg]};
+      if (x.n_upd == kMaxUpd) {
+        if (int r = launch_kv_xfer(x, st)) return r;
+        x.n_upd = 0;
+      }
+    }
+  if (x.n_upd)
+    if (int r = launch_kv_xfer(x, st)) return r;
+  for (Seq& q : c->seqs)
+    for (int32_t& pg : q.pages) pg = to[pg];
+  for (size_t i = 0; i < src.size(); ++i) {
+    c->page_ref[dst[i]] = c->page_ref[src[i]];
+    c->page_ref[src[i]] = 0;
+  }
+  c->free_pages.clear();
+  for (int32_t p = c->n_pages - 1; p >= live; --p) c->free_pages.push_back(p);
+  if (moved_out) *moved_out = (int32_t)src.size();
   return MK_OK;
 }
 
@@ -838,7 +1122,7 @@ MK_API int mk_sync(mk_ctx* c, void* stream) {
   MK_CUDA(cudaMemcpy(err, c->sc.err, sizeof(err), cudaMemcpyDeviceToHost));
   if (err[0] != 0) {
     MK_CUDA(cudaMemset(c->sc.err, 0, sizeof(err)));
-    static const char* sites[] = {"?", "grid barrier", "page table", "attention unit", "token id",
+    static const char* sites[] = {"4-bit cache (length or page)", "grid barrier", "page table", "attention unit", "token id",
                                   "weight ring", "shared-memory plan", "flagged residual word"};
     const int site = err[1] >= 1 && err[1] <= SITE_FLAG ? err[1] : 0;
     return fail(err[0], std::string("device reported error ") + std::to_string(err[0]) + " at " +
@@ -908,6 +1192,9 @@ MK_API int mk_destroy(mk_ctx* c) {
   cudaFree(c->scratch_dev);
   cudaFree(c->kv_dev);
   cudaFree(c->block_table_dev);
+  cudaFree(c->kv_stage);
+  cudaFree(c->kv_seqs);
+  cudaFree(c->kv_ws);
   prefill_free(c->prefill);
   delete c;
   if (e != cudaSuccess) return fail(MK_ERR_CUDA, std::string("cudaDeviceSynchronize: ") + cudaGetErrorString(e));

@@ -45,7 +45,21 @@ __global__ void __launch_bounds__(256) kv_xfer_kernel(const __grid_constant__ Kv
   }
 }
 
+__global__ void step_seqs_kernel(const __grid_constant__ StepSeqs a, int32_t* len, int32_t* slot) {
+  const int i = threadIdx.x;
+  if (i < a.n) {
+    len[i] = a.len[i];
+    slot[i] = a.slot[i];
+  }
+}
+
 }  // namespace
+
+int launch_step_seqs(const StepSeqs& a, int32_t* len_dev, int32_t* slot_dev, cudaStream_t st) {
+  step_seqs_kernel<<<1, 32, 0, st>>>(a, len_dev, slot_dev);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? MK_OK : host_fail(MK_ERR_CUDA, cudaGetErrorString(e));
+}
 
 int launch_kv_xfer(const KvXfer& a, cudaStream_t st) {
   const long long words = (long long)a.n_layers * a.n * 2 * a.n_kv_heads * (a.head_dim / 8);

@@ -102,7 +102,7 @@ __device__ __forceinline__ float value_of(uint32_t code, float s) {
 // q + r (x - q s) in two fused steps (Markstein), which rounds correctly where
 // nothing under- or overflows; scales outside [2^-60, 2^60] take the division itself.
 template <int HD, class T, int N>
-__global__ void __launch_bounds__(kThreadsKv) k_kv4_store(const __grid_constant__ Kv4Args a, Rows k, Rows v, int tp, int chunks) {
+__global__ void __launch_bounds__(kThreadsKv) k_kv4_store(const __grid_constant__ Kv4Args a, Kv4Rows k, Kv4Rows v, int tp, int chunks) {
   const int parts = 16 * Tile<HD>::NG * a.n_kv_heads;
   const int seq = blockIdx.x / chunks, row_base = (blockIdx.x - seq * chunks) * tp * N;
   const int tk = parts < (int)blockDim.x ? threadIdx.x / parts : 0, row0 = row_base + tk;
@@ -110,13 +110,22 @@ __global__ void __launch_bounds__(kThreadsKv) k_kv4_store(const __grid_constant_
     const int i = i0 + threadIdx.x - tk * parts;
     const bool mine = tk < tp && i < parts;
     const Part<HD> pt(mine ? i : 0, a.n_kv_heads);
-    const Rows& r = pt.kv ? v : k;
+    const Kv4Rows& r = pt.kv ? v : k;
     const T* src = reinterpret_cast<const T*>(r.p) + seq * r.seq + pt.head * r.head + pt.group * kGroup + 8 * pt.lane;
     V8 x[N];
     uint8_t* t[N];
     int at[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = read8(src + min(row0 + j * tp, a.rows - 1) * r.row);
+    for (int j = 0; j < N; ++j) {
+      const int row = min(row0 + j * tp, a.rows - 1);
+      long long off = row * r.row;
+      if (r.slot) {  // rows that lie in their slots of a page
+        int len, nn;
+        seq_extent(a, seq, len, nn);
+        off += max(len - nn + row, 0) % kPageTokens * r.slot;
+      }
+      x[j] = read8(src + off);
+    }
     places_of<HD, N>(a, pt, seq, row0, tp, t, at);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -156,14 +165,14 @@ __global__ void __launch_bounds__(kThreadsKv) k_kv4_store(const __grid_constant_
 }
 
 template <int HD, class T, int N>
-__global__ void __launch_bounds__(kThreadsKv) k_kv4_load(const __grid_constant__ Kv4Args a, Rows k, Rows v, int tp, int chunks) {
+__global__ void __launch_bounds__(kThreadsKv) k_kv4_load(const __grid_constant__ Kv4Args a, Kv4Rows k, Kv4Rows v, int tp, int chunks) {
   const int parts = 16 * Tile<HD>::NG * a.n_kv_heads;
   const int seq = blockIdx.x / chunks, row_base = (blockIdx.x - seq * chunks) * tp * N;
   const int tk = parts < (int)blockDim.x ? threadIdx.x / parts : 0, row0 = row_base + tk;
   if (tk >= tp) return;
   for (int i = threadIdx.x - tk * parts; i < parts; i += blockDim.x) {
     const Part<HD> pt(i, a.n_kv_heads);
-    const Rows& r = pt.kv ? v : k;
+    const Kv4Rows& r = pt.kv ? v : k;
     T* dst = reinterpret_cast<T*>(const_cast<void*>(r.p)) + seq * r.seq + pt.head * r.head + pt.group * kGroup + 8 * pt.lane;
     uint8_t* t[N];
     int at[N];
@@ -219,6 +228,44 @@ int kv4_check_rows(const mk_kv4_rows* r, int dtype, const char* what) {
   return MK_OK;
 }
 
+
+// Launch KERNEL<head_dim, element type, rows in flight>: two rows a thread once
+// that still gives every SM two blocks (7.1 us against 7.8 with one and 8.5 with
+// four, for 4096 tokens of 4 heads of 128), one below (a step of a few sequences
+// is bound by its chain of reads).
+#define MK_KV4_LAUNCH(KERNEL, C, HDIM, DT, ST, ...)                                                                        \
+  do {                                                                                                               \
+    const int parts_ = 16 * (HDIM / kGroup) * (C).n_kv_heads, tp_ = pass_rows(parts_, (C).rows);              \
+    const int threads_ = std::min(kThreadsKv, tp_ * parts_);                                                         \
+    const int c2_ = ((C).rows + 2 * tp_ - 1) / (2 * tp_), c1_ = ((C).rows + tp_ - 1) / tp_;                           \
+    if ((C).n_seqs * c2_ >= 304) MK_KV4_LAUNCH_N(KERNEL, 2, C, HDIM, DT, ST, __VA_ARGS__, tp_, c2_);                       \
+    else MK_KV4_LAUNCH_N(KERNEL, 1, C, HDIM, DT, ST, __VA_ARGS__, tp_, c1_);                                               \
+  } while (0)
+#define MK_KV4_LAUNCH_N(KERNEL, N, C, HDIM, DT, ST, A, K, V, TP, CH)                                                       \
+  do {                                                                                                               \
+    const int g_ = (C).n_seqs * CH;                                                                                  \
+    if (HDIM == 64 && DT == MK_F32) KERNEL<64, float, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);           \
+    else if (HDIM == 64) KERNEL<64, __nv_bfloat16, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);              \
+    else if (DT == MK_F32) KERNEL<128, float, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);                          \
+    else KERNEL<128, __nv_bfloat16, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);                                    \
+  } while (0)
+
+int kv4_store(const Kv4Args& a, int head_dim, const Kv4Rows& k, const Kv4Rows& v, int dtype, cudaStream_t st) {
+  MK_KV4_LAUNCH(k_kv4_store, a, head_dim, dtype, st, a, k, v);
+  return cuda_status("kv4 store");
+}
+
+int kv4_load(const Kv4Args& a, int head_dim, const Kv4Rows& k, const Kv4Rows& v, int dtype, cudaStream_t st) {
+  MK_KV4_LAUNCH(k_kv4_load, a, head_dim, dtype, st, a, k, v);
+  return cuda_status("kv4 load");
+}
+
+Kv4Args kv4_args(const mk_kv4_cache& c) {
+  return {static_cast<uint8_t*>(c.pool), c.table, c.lengths, c.n_new, c.status, c.n_pages, c.n_kv_heads, c.n_seqs,
+          c.max_pages, c.rows, nullptr, c.max_pages};
+}
+Kv4Rows kv4_rows(const mk_kv4_rows& r) { return {r.data, r.seq_stride, r.row_stride, r.head_stride, 0}; }
+
 }  // namespace mk
 
 using namespace mk;
@@ -228,47 +275,24 @@ extern "C" MK_API size_t mk_kv4_page_bytes(int32_t n_kv_heads, int32_t head_dim)
   return (size_t)n_kv_heads * (head_dim == 64 ? Tile<64>::RECORD : Tile<128>::RECORD);
 }
 
-// Launch KERNEL<head_dim, element type, rows in flight>: two rows a thread once
-// that still gives every SM two blocks (7.1 us against 7.8 with one and 8.5 with
-// four, for 4096 tokens of 4 heads of 128), one below (a step of a few sequences
-// is bound by its chain of reads).
-#define MK_KV4_LAUNCH(KERNEL, C, DT, ST, ...)                                                                        \
-  do {                                                                                                               \
-    const int parts_ = 16 * ((C).head_dim / kGroup) * (C).n_kv_heads, tp_ = pass_rows(parts_, (C).rows);              \
-    const int threads_ = std::min(kThreadsKv, tp_ * parts_);                                                         \
-    const int c2_ = ((C).rows + 2 * tp_ - 1) / (2 * tp_), c1_ = ((C).rows + tp_ - 1) / tp_;                           \
-    if ((C).n_seqs * c2_ >= 304) MK_KV4_LAUNCH_N(KERNEL, 2, C, DT, ST, __VA_ARGS__, tp_, c2_);                       \
-    else MK_KV4_LAUNCH_N(KERNEL, 1, C, DT, ST, __VA_ARGS__, tp_, c1_);                                               \
-  } while (0)
-#define MK_KV4_LAUNCH_N(KERNEL, N, C, DT, ST, A, K, V, TP, CH)                                                       \
-  do {                                                                                                               \
-    const int g_ = (C).n_seqs * CH;                                                                                  \
-    if ((C).head_dim == 64 && DT == MK_F32) KERNEL<64, float, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);           \
-    else if ((C).head_dim == 64) KERNEL<64, __nv_bfloat16, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);              \
-    else if (DT == MK_F32) KERNEL<128, float, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);                          \
-    else KERNEL<128, __nv_bfloat16, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);                                    \
-  } while (0)
-
-extern "C" MK_API int mk_kv4_store(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype,
-                                   void* stream) {
+// The checks of a store or load, then the launch.
+static int store_or_load(int (*f)(const Kv4Args&, int, const Kv4Rows&, const Kv4Rows&, int, cudaStream_t),
+                         const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype, void* stream) {
   host_clear_error();
   bool empty = false;
   if (int r = kv4_check_cache(c, &empty)) return r;
   if (empty) return MK_OK;
   if (int r = kv4_check_rows(k, dtype, "k")) return r;
   if (int r = kv4_check_rows(v, dtype, "v")) return r;
-  MK_KV4_LAUNCH(k_kv4_store, *c, dtype, (cudaStream_t)stream, kv4_args(*c), kv4_rows(*k), kv4_rows(*v));
-  return cuda_status("kv4 store");
+  return f(kv4_args(*c), c->head_dim, kv4_rows(*k), kv4_rows(*v), dtype, (cudaStream_t)stream);
+}
+
+extern "C" MK_API int mk_kv4_store(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype,
+                                   void* stream) {
+  return store_or_load(kv4_store, c, k, v, dtype, stream);
 }
 
 extern "C" MK_API int mk_kv4_load(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype,
                                   void* stream) {
-  host_clear_error();
-  bool empty = false;
-  if (int r = kv4_check_cache(c, &empty)) return r;
-  if (empty) return MK_OK;
-  if (int r = kv4_check_rows(k, dtype, "k")) return r;
-  if (int r = kv4_check_rows(v, dtype, "v")) return r;
-  MK_KV4_LAUNCH(k_kv4_load, *c, dtype, (cudaStream_t)stream, kv4_args(*c), kv4_rows(*k), kv4_rows(*v));
-  return cuda_status("kv4 load");
+  return store_or_load(kv4_load, c, k, v, dtype, stream);
 }

@@ -22,15 +22,6 @@ struct Tile {
   static constexpr int RECORD = kPageTokens / kTile * BYTES;
 };
 
-struct Kv4Args {
-  uint8_t* pool;
-  const int32_t* table;
-  const int32_t* lengths;
-  const int32_t* n_new;
-  int32_t* status;
-  int32_t n_pages, n_kv_heads, n_seqs, max_pages, rows;
-};
-
 __device__ __forceinline__ void refuse(int32_t* status) {
   if (status) atomicCAS(status, 0, MK_ERR_DEVICE_INDEX);
 }
@@ -45,9 +36,13 @@ __device__ __forceinline__ void seq_extent(const Kv4Args& a, int s, int& len, in
   nn = max(0, min(nn, a.rows));
 }
 
+__device__ __forceinline__ const int32_t* table_row(const Kv4Args& a, int s) {
+  return a.table + (size_t)(a.slots ? a.slots[s] : s) * a.table_stride;
+}
+
 // The page of position p of sequence s, or -1.
 __device__ __forceinline__ int page_of(const Kv4Args& a, int s, int p) {
-  const int page = a.table[(size_t)s * a.max_pages + p / kPageTokens];
+  const int page = table_row(a, s)[p / kPageTokens];
   if (page >= 0 && page < a.n_pages) return page;
   refuse(a.status);
   return -1;
@@ -58,19 +53,11 @@ __device__ __forceinline__ uint8_t* tile_of(const Kv4Args& a, int page, int head
   return a.pool + ((size_t)page * a.n_kv_heads + head) * Tile<HD>::RECORD + (size_t)(p % kPageTokens / kTile) * Tile<HD>::BYTES;
 }
 
-struct Rows {
-  const void* p;
-  long long seq, row, head;  // strides in elements
-};
-
 // Host checks shared by the entry points (mk_kv4.cu): of a cache description
 // (*empty: the call has no row), and of rows.
 int kv4_check_cache(const mk_kv4_cache* c, bool* empty);
 int kv4_check_rows(const mk_kv4_rows* r, int dtype, const char* what);
-inline Kv4Args kv4_args(const mk_kv4_cache& c) {
-  return {static_cast<uint8_t*>(c.pool), c.table, c.lengths, c.n_new, c.status, c.n_pages, c.n_kv_heads, c.n_seqs,
-          c.max_pages, c.rows};
-}
-inline Rows kv4_rows(const mk_kv4_rows& r) { return {r.data, r.seq_stride, r.row_stride, r.head_stride}; }
+Kv4Args kv4_args(const mk_kv4_cache& c);
+Kv4Rows kv4_rows(const mk_kv4_rows& r);
 
 }  // namespace mk

@@ -64,7 +64,7 @@ constexpr float kCode = 1048576.f;                 // 2^20, taken out of the sec
 
 struct AttArgs {
   Kv4Args a;
-  Rows q, out;
+  Kv4Rows q, out;
   float* lse;
   float c;              // scale * log2(e) * 2^65
   int32_t n_heads, gqa;
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     const int item = blockIdx.x >> p.cluster_log, rank = blockIdx.x & (p.cluster - 1);
     const int e = item / p.a.n_kv_heads, head = item - e * p.a.n_kv_heads;
     const int seq = p.n_ctiles == 1 ? e : e / p.n_ctiles;
-    const int page = tid < p.a.max_pages ? p.a.table[(size_t)seq * p.a.max_pages + tid] : -1;
+    const int page = tid < p.a.max_pages ? table_row(p.a, seq)[tid] : -1;
     const uint32_t nt = tiles_of(p, e, CT, SP);  // at most 2^24
     load_q(seq, e - seq * p.n_ctiles, head);
     run.base = 0;
@@ -925,10 +925,10 @@ int sm_count() {
 }
 
 // Variant, grid and workspace of a call with rows; false: too many columns.
-bool plan_of(const mk_kv4_cache& c, int n_heads, int dtype, Plan* pl) {
+bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
   const long long cols = (long long)c.rows * (n_heads / c.n_kv_heads);
   if (cols > INT_MAX / 64) return false;
-  if (c.head_dim == 64) take_for<64>(pl, (int)cols, dtype);
+  if (head_dim == 64) take_for<64>(pl, (int)cols, dtype);
   else take_for<128>(pl, (int)cols, dtype);
   const long long ct = (cols + pl->CT - 1) / pl->CT, entries = ct * c.n_seqs, items = entries * c.n_kv_heads;
   const long long most = (long long)c.max_pages * (kPageTokens / pl->SP);  // steps of an item
@@ -946,7 +946,7 @@ bool plan_of(const mk_kv4_cache& c, int n_heads, int dtype, Plan* pl) {
     int n = 1;
     while (n < 16 && 2 * n <= most && 2 * n * items <= room) n *= 2;
     pl->cluster = n;
-    if (n > 1) pl->smem += n * ((pl->CT + n - 1) / n) * (c.head_dim + 2) * (int)sizeof(float);
+    if (n > 1) pl->smem += n * ((pl->CT + n - 1) / n) * (head_dim + 2) * (int)sizeof(float);
     pl->grid = (int)(items * n);
     pl->item_off = pl->part_off = pl->bytes = 0;
     return true;
@@ -959,7 +959,7 @@ bool plan_of(const mk_kv4_cache& c, int n_heads, int dtype, Plan* pl) {
   pl->join_y = items < 2048 ? pl->CT : 1;
   pl->item_off = 16;
   pl->part_off = pl->item_off + (size_t)items * sizeof(longlong2);
-  pl->bytes = pl->part_off + 2 * (size_t)pl->grid * pl->CT * (c.head_dim + 4) * sizeof(float);
+  pl->bytes = pl->part_off + 2 * (size_t)pl->grid * pl->CT * (head_dim + 4) * sizeof(float);
   return true;
 }
 
@@ -977,50 +977,31 @@ cudaError_t allow_smem(const Plan& pl) {
   return e;
 }
 
-int check_attention(const mk_kv4_cache* c, int n_heads, int dtype, bool* empty) {
-  if (int r = kv4_check_cache(c, empty)) return r;
-  if (n_heads < 1 || n_heads % c->n_kv_heads || n_heads > 4096)
-    return host_fail(MK_ERR_INVALID_ARG, "n_heads must be a multiple of n_kv_heads, at most 4096");
-  if (dtype != MK_F32 && dtype != MK_BF16) return host_fail(MK_ERR_INVALID_ARG, "dtype must be MK_F32 or MK_BF16");
-  return MK_OK;
-}
-
 }  // namespace
-}  // namespace mk
 
-using namespace mk;
-
-extern "C" MK_API size_t mk_kv4_attention_bytes(const mk_kv4_cache* c, int32_t n_heads, int32_t dtype) {
-  bool empty = false;
+bool kv4_attention_bytes(const Kv4Args& a, int head_dim, int n_heads, int dtype, size_t* bytes) {
   Plan pl;
-  if (check_attention(c, n_heads, dtype, &empty) || empty || !plan_of(*c, n_heads, dtype, &pl)) return 0;
-  return pl.bytes;
+  if (!plan_of(a, head_dim, n_heads, dtype, &pl)) return false;
+  *bytes = pl.bytes;
+  return true;
 }
 
-extern "C" MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, const mk_kv4_rows* q, int32_t dtype,
-                                       float scale, const mk_kv4_rows* out, float* lse, void* workspace,
-                                       size_t workspace_bytes, void* stream) {
-  host_clear_error();
-  bool empty = false;
-  if (int r = check_attention(c, n_heads, dtype, &empty)) return r;
-  if (!(scale > -1e18f && scale < 1e18f)) return host_fail(MK_ERR_INVALID_ARG, "scale must lie within +-1e18");
-  if (empty) return MK_OK;
-  if (int r = kv4_check_rows(q, dtype, "q")) return r;
-  if (int r = kv4_check_rows(out, dtype, "out")) return r;
+int kv4_attention(const Kv4Args& a, int head_dim, int n_heads, const Kv4Rows& q, int dtype, float scale,
+                  const Kv4Rows& out, float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   Plan pl;
-  if (!plan_of(*c, n_heads, dtype, &pl))
+  if (!plan_of(a, head_dim, n_heads, dtype, &pl))
     return host_fail(MK_ERR_INVALID_ARG, "n_seqs x rows x n_heads or max_pages x n_kv_heads is too large");
   if (pl.bytes && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < pl.bytes))
     return host_fail(MK_ERR_INVALID_ARG, "workspace is NULL, not 16-byte aligned or smaller than mk_kv4_attention_bytes");
   AttArgs p;
-  p.a = kv4_args(*c);
-  p.q = kv4_rows(*q);
-  p.out = kv4_rows(*out);
+  p.a = a;
+  p.q = q;
+  p.out = out;
   p.lse = lse;
   p.c = (float)((double)scale * 1.4426950408889634 * kDown);
   p.n_heads = n_heads;
-  p.gqa = n_heads / c->n_kv_heads;
-  p.cols = c->rows * p.gqa;
+  p.gqa = n_heads / a.n_kv_heads;
+  p.cols = a.rows * p.gqa;
   p.n_ctiles = pl.n_ctiles;
   p.n_entries = pl.n_entries;
   p.cluster = pl.cluster;
@@ -1044,7 +1025,7 @@ extern "C" MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, c
   cfg.gridDim = dim3(pl.grid);
   cfg.blockDim = dim3(pl.threads);
   cfg.dynamicSmemBytes = pl.smem;
-  cfg.stream = (cudaStream_t)stream;
+  cfg.stream = stream;
   cfg.attrs = at;
   if (e == cudaSuccess) {
     if (pl.cluster > 1) {
@@ -1071,4 +1052,37 @@ extern "C" MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, c
     return host_fail(MK_ERR_CUDA, (std::string("kv4 attention: ") + cudaGetErrorString(e)).c_str());
   }
   return MK_OK;
+}
+
+}  // namespace mk
+
+using namespace mk;
+
+static int check_attention(const mk_kv4_cache* c, int n_heads, int dtype, bool* empty) {
+  if (int r = kv4_check_cache(c, empty)) return r;
+  if (n_heads < 1 || n_heads % c->n_kv_heads || n_heads > 4096)
+    return host_fail(MK_ERR_INVALID_ARG, "n_heads must be a multiple of n_kv_heads, at most 4096");
+  if (dtype != MK_F32 && dtype != MK_BF16) return host_fail(MK_ERR_INVALID_ARG, "dtype must be MK_F32 or MK_BF16");
+  return MK_OK;
+}
+
+extern "C" MK_API size_t mk_kv4_attention_bytes(const mk_kv4_cache* c, int32_t n_heads, int32_t dtype) {
+  bool empty = false;
+  size_t bytes = 0;
+  if (check_attention(c, n_heads, dtype, &empty) || empty) return 0;
+  return kv4_attention_bytes(kv4_args(*c), c->head_dim, n_heads, dtype, &bytes) ? bytes : 0;
+}
+
+extern "C" MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, const mk_kv4_rows* q, int32_t dtype,
+                                       float scale, const mk_kv4_rows* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  host_clear_error();
+  bool empty = false;
+  if (int r = check_attention(c, n_heads, dtype, &empty)) return r;
+  if (!(scale > -1e18f && scale < 1e18f)) return host_fail(MK_ERR_INVALID_ARG, "scale must lie within +-1e18");
+  if (empty) return MK_OK;
+  if (int r = kv4_check_rows(q, dtype, "q")) return r;
+  if (int r = kv4_check_rows(out, dtype, "out")) return r;
+  return kv4_attention(kv4_args(*c), c->head_dim, n_heads, kv4_rows(*q), dtype, scale, kv4_rows(*out), lse, workspace,
+                       workspace_bytes, (cudaStream_t)stream);
 }

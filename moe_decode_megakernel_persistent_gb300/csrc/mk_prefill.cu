@@ -59,6 +59,9 @@ struct PrefillWork {
   float* lm_v = nullptr;     // lm_head per-block best logit
   int32_t* lm_i = nullptr;   // and token
   std::vector<int32_t> cnt_host;
+  uint16_t* kv = nullptr;    // 4-bit cache: the chunk's K and V, bf16 [M][K|V][n_kv][HD]
+  void* kv4_ws = nullptr;    // and the attention's workspace
+  size_t kv4_ws_bytes = 0;
 };
 
 namespace {
@@ -179,10 +182,11 @@ __global__ void k_widen_int3(const uint8_t* rec, int rec_bytes, int K, long long
   }
 }
 
-// QKV records -> roped q (fp32) and K / V (bf16) into the pages.
+// QKV records -> roped q (fp32) and K / V (bf16) into the pages, or (4-bit
+// cache: rows not null) into rows [M][K|V][n_kv][HD].
 __global__ void k_qkv_epi(const float* C, int NQKV, int NH, int NKV, int HD, const float2* rope, int start, int M,
                           float* Q, uint16_t* kv, const int32_t* bt, int slot, int mpps, int n_pages, int layer,
-                          int32_t* err) {
+                          int32_t* err, uint16_t* rows) {
   const int HALF = HD / 2, NQP = NH * HALF, NKP = NKV * HALF, QD = NH * HD;
   const long long total = (long long)M * (NQP + 2 * NKP);
   for (long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x; idx < total;
@@ -200,6 +204,12 @@ __global__ void k_qkv_epi(const float* C, int NQKV, int NH, int NKV, int HD, con
         Q[(size_t)i * QD + hh * HD + ii + HALF] = e1;
         continue;
       }
+      if (rows) {
+        uint16_t* dst = rows + (size_t)i * 2 * NKV * HD + hh * HD;
+        dst[ii] = f2bf(e0);
+        dst[ii + HALF] = f2bf(e1);
+        continue;
+      }
       const int page = bt[slot * mpps + pos / kPageTokens];
       if (page < 0 || page >= n_pages) {
         if (atomicCAS(err, 0, MK_ERR_DEVICE_INDEX) == 0) { err[1] = SITE_PAGE; err[2] = pos; }
@@ -211,6 +221,12 @@ __global__ void k_qkv_epi(const float* C, int NQKV, int NH, int NKV, int HD, con
       dst[ii + HALF] = f2bf(e1);
     } else {
       const int q = p - NQP - NKP, g = q / HALF, ii = q % HALF;
+      if (rows) {
+        uint16_t* dst = rows + ((size_t)i * 2 + 1) * NKV * HD + g * HD;
+        dst[ii] = f2bf(v0);
+        dst[ii + HALF] = f2bf(v1);
+        continue;
+      }
       const int page = bt[slot * mpps + pos / kPageTokens];
       if (page < 0 || page >= n_pages) continue;
       uint16_t* dst = kv + ((((size_t)layer * n_pages + page) * 2 + 1) * NKV + g) * (size_t)(kPageTokens * HD) +
@@ -611,7 +627,7 @@ void prefill_free(PrefillWork* w) {
   if (!w) return;
   if (w->blas) cublasDestroy(w->blas);
   void* bufs[] = {w->X, w->Hr, w->Q, w->O, w->A, w->C, w->D, w->Wb, w->Z, w->logits, w->ids, w->wts, w->cnt,
-                  w->ent, w->pos_of, w->lm_v, w->lm_i};
+                  w->ent, w->pos_of, w->lm_v, w->lm_i, w->kv, w->kv4_ws};
   for (void* p : bufs) cudaFree(p);
   delete w;
 }
@@ -665,6 +681,22 @@ int prefill_run(PrefillWork** pw, const PrefillArgs& a, cudaStream_t st) {
     alloc((void**)&w->pos_of, 4 * ent);
     alloc((void**)&w->lm_v, 4 * kLmBlocks);
     alloc((void**)&w->lm_i, 4 * kLmBlocks);
+    if (a.kv4) {
+      // the attention's workspace for any chunk: the largest one's
+      Kv4Args k{};
+      k.n_kv_heads = d.NKV;
+      k.n_seqs = 1;
+      k.max_pages = a.max_pages_per_seq;
+      for (int rows : {kMaxBatch + 1, 32, 64, 128, 512, kMaxPrefill}) {
+        size_t b = 0;
+        k.rows = rows;
+        if (!kv4_attention_bytes(k, d.HD, d.NH, MK_F32, &b))
+          return host_fail(MK_ERR_UNSUPPORTED, "a chunk's attention over the 4-bit cache is too large");
+        w->kv4_ws_bytes = std::max(w->kv4_ws_bytes, b);
+      }
+      alloc((void**)&w->kv, 2 * MM * 2 * d.KD);
+      alloc(&w->kv4_ws, w->kv4_ws_bytes);
+    }
     if (e != cudaSuccess) return host_fail(MK_ERR_CUDA, (std::string("prefill workspace: ") + cudaGetErrorString(e)).c_str());
     w->max_m = kMaxPrefill;
     w->cnt_host.resize(2 * E + 1);
@@ -695,10 +727,19 @@ int prefill_run(PrefillWork** pw, const PrefillArgs& a, cudaStream_t st) {
     if (int r = gemm(w, d, M, d.NQKV, d.H, W, d.H, w.A, lo, w.C, d.NQKV)) return r;
     k_qkv_epi<<<grid_for((long long)M * d.NQKV / 2), TB, 0, st>>>(w.C, d.NQKV, d.NH, d.NKV, d.HD, a.rope, a.start, M,
                                                                    w.Q, a.kv, a.block_table, a.slot,
-                                                                   a.max_pages_per_seq, a.n_pages, l, a.err);
+                                                                   a.max_pages_per_seq, a.n_pages, l, a.err, w.kv);
     dim3 ag((M + 15) / 16, d.NKV);
     const float scale = 1.f / sqrtf((float)d.HD);
-    if (d.HD == 128 && d.NH == 4 * d.NKV) {
+    if (a.kv4) {
+      // the chunk's rows are stored, then attend to the cache that holds them
+      const int QD = d.QD, KD = d.KD;
+      Kv4Args k{a.kv4 + (size_t)l * a.n_pages * mk_kv4_page_bytes(d.NKV, d.HD), a.block_table, a.kv4_len, nullptr, a.err,
+                a.n_pages, d.NKV, 1, (a.start + M + kPageTokens - 1) / kPageTokens, M, a.kv4_slot, a.max_pages_per_seq};
+      if (int r = kv4_store(k, d.HD, {w.kv, 0, 2 * KD, d.HD, 0}, {w.kv + KD, 0, 2 * KD, d.HD, 0}, MK_BF16, st)) return r;
+      if (int r = kv4_attention(k, d.HD, d.NH, {w.Q, 0, QD, d.HD, 0}, MK_F32, scale, {w.O, 0, QD, d.HD, 0}, nullptr,
+                                w.kv4_ws, w.kv4_ws_bytes, st))
+        return r;
+    } else if (d.HD == 128 && d.NH == 4 * d.NKV) {
       k_attention<128, 4><<<ag, 256, att_smem, st>>>(w.Q, a.kv, a.block_table, a.slot, a.max_pages_per_seq,
                                                      a.n_pages, l, d.NKV, a.start, M, scale, w.O);
     } else if (d.HD == 64 && d.NH == 2 * d.NKV) {

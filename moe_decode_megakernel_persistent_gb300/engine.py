@@ -62,7 +62,12 @@ class Engine:
     """One library context: weights, KV pool, sequences."""
 
     def __init__(self, shape, weights: dict, n_pages: int, max_batch: int = 16,
-                 max_ctx: int = 16384, max_seqs: int = 64, device: Optional[int] = None):
+                 max_ctx: int = 16384, max_seqs: int = 64, device: Optional[int] = None,
+                 kv_dtype: str = "bf16"):
+        """kv_dtype: the cache's format, "bf16" or "int4" (4 bits with scales:
+        3.8 times the positions in the same memory)."""
+        if kv_dtype not in ("bf16", "int4"):
+            raise ValueError('kv_dtype must be "bf16" or "int4"')
         L.load()
         if device is not None:
             torch.cuda.set_device(device)
@@ -87,7 +92,7 @@ class Engine:
         w = L.mk_weights(embed=_ptr(weights[("embed",)]), final_norm=_ptr(weights[("final_norm",)]),
                          lm_head=_lin(weights[("lm_head",)]), layers=layers)
         self.ctx = L.mk_create(self.desc, w)
-        L.mk_kv_alloc(self.ctx, n_pages)
+        L.mk_kv_alloc_fmt(self.ctx, n_pages, L.WDTYPES[kv_dtype])
         self.trace = None
         self.max_batch = max_batch
 
@@ -140,6 +145,19 @@ class Engine:
         """Open dst_seq sharing the pages of src_seq's first n_tokens
         positions (a multiple of 128)."""
         L.mk_seq_fork(self.ctx, src_seq, dst_seq, n_tokens, self.stream)
+
+    def fork_at(self, src_seq: int, dst_seq: int, n_tokens: int):
+        """Open dst_seq as src_seq's first n_tokens positions, any number of
+        them: whole pages are shared, a partly filled last one is copied."""
+        L.mk_seq_fork_at(self.ctx, src_seq, dst_seq, n_tokens, self.stream)
+
+    def truncate(self, seq_id: int, n_tokens: int):
+        """Drop the positions from n_tokens on (rejected drafts)."""
+        L.mk_seq_truncate(self.ctx, seq_id, n_tokens, self.stream)
+
+    def compact(self) -> int:
+        """Move the pages in use to the lowest page numbers; returns how many moved."""
+        return L.mk_kv_compact(self.ctx, self.stream)
 
     def seq_length(self, seq_id: int) -> int:
         return L.mk_seq_length(self.ctx, seq_id)
@@ -259,11 +277,15 @@ class PrefixCache:
     The workload is the one "rec Megakernel and Tempo9 Compared", §1 (Prefix
     cache) measures: a second turn over the same 8,022-token prompt reuses
     7,936 tokens (62 pages), and returning to a prompt after another one
-    reuses it again when its entry is still held."""
+    reuses it again when its entry is still held.
 
-    def __init__(self, engine: Engine, capacity: int = 4):
+    With whole_pages=False the prefix is reused to the token (mk_seq_fork_at: the
+    last, partly filled page is copied): 8,021 of 8,022 tokens."""
+
+    def __init__(self, engine: Engine, capacity: int = 4, whole_pages: bool = True):
         self.e = engine
         self.capacity = capacity
+        self.whole_pages = whole_pages
         self.entries: list = []      # [(seq_id, tokens as a host list)], most recent last
 
     def _match(self, toks: list) -> tuple:
@@ -273,7 +295,8 @@ class PrefixCache:
             lim = min(len(et), len(toks) - 1)   # keep >= 1 token to prefill (it yields the next token)
             while n < lim and et[n] == toks[n]:
                 n += 1
-            n = n // 128 * 128
+            if self.whole_pages:
+                n = n // 128 * 128
             if n > best_n:
                 best, best_n = sid, n
         return best, best_n
@@ -284,7 +307,7 @@ class PrefixCache:
         toks = tokens.cpu().tolist()
         src, n = self._match(toks)
         if src is not None:
-            self.e.fork(src, seq_id, n)
+            (self.e.fork if self.whole_pages else self.e.fork_at)(src, seq_id, n)
             self.entries = [x for x in self.entries if x[0] != src] + [x for x in self.entries if x[0] == src]
         out = self.e.prefill(seq_id, tokens[n:], start_pos=n, out=out)
         return out, n
