@@ -74,8 +74,8 @@ struct AttArgs {
   int32_t n_entries;    // n_seqs * n_ctiles
   int32_t cluster;      // > 0: an item is one cluster of so many blocks (a power of two), and there is no workspace
   int32_t cluster_log;
-  long long* total;     // workspace: tiles of the call
-  longlong2* item;      // workspace: [n_entries * n_kv_heads] first tile and block, or -1 (done)
+  long long* total;     // workspace: places of the call (Runs)
+  longlong2* item;      // workspace: [n_entries * n_kv_heads] first place and first block, or -1 (done)
   float* part;          // workspace: [2 * grid][columns][HD + 4] partial results
 };
 
@@ -198,26 +198,42 @@ __device__ __forceinline__ int tiles_of(const AttArgs& p, int e, int CT, int SP)
   return end <= 0 ? 0 : (end + SP - 1) / SP;
 }
 
-// The runs of a block: its tiles [pos, hi) cut at items.
+// The runs of a block.  All items are laid end to end, each as kOver places (an
+// item's set-up and end cost a block about as much as so many steps) and then
+// its steps; the block takes the steps of the places [pos, hi).
+constexpr int kOver = 4;
 struct Runs {
-  long long pos, hi, base;  // base: the first tile of entry e
+  long long pos, hi, base;  // base: the first place of entry e
   int e, nt, head, t0, t1;
-  __device__ __forceinline__ bool next(const AttArgs& p, int CT, int SP) {  // the run at pos; false: none is left
-    if (pos >= hi) return false;
-    for (;; ++e) {
-      if (e >= p.n_entries) return false;  // lengths that change under the call
-      nt = tiles_of(p, e, CT, SP);
-      const long long n = (long long)nt * p.a.n_kv_heads;
-      if (pos < base + n) break;
-      base += n;
+  __device__ __forceinline__ bool next(const AttArgs& p, int CT, int SP) {  // the next run; false: none is left
+    for (;;) {
+      if (pos >= hi) return false;
+      for (;; ++e) {
+        if (e >= p.n_entries) return false;  // lengths that change under the call
+        nt = tiles_of(p, e, CT, SP);
+        const long long n = nt ? (long long)(nt + kOver) * p.a.n_kv_heads : 0;
+        if (pos < base + n) break;
+        base += n;
+      }
+      const int len = nt + kOver, at = (int)(pos - base);  // held to 31 bits by the entry point
+      head = at / len;
+      const int in = at - head * len;
+      const int out = (int)min((long long)len, in + (hi - pos));
+      pos += out - in;
+      t0 = max(0, in - kOver);
+      t1 = max(0, out - kOver);
+      if (t1 > t0) return true;
     }
-    const int at = (int)(pos - base);  // below n_kv_heads * nt <= 2^10 * 2^25: held to 31 bits by the entry point
-    head = at / nt;
-    t0 = at - head * nt;
-    t1 = (int)min((long long)nt, t0 + (hi - pos));
-    return true;
   }
 };
+// The first place of block b of G: the places cut into equal runs.
+__device__ __forceinline__ long long first_place(long long total, long long b, int G) {
+  if (total * G < 1ll << 32) return (uint32_t)total * (uint32_t)b / (uint32_t)G;
+  return total * b / G;
+}
+// A partial run that starts inside an item, and one that ends inside it: a
+// block has one of each at most, with a place of its own in the workspace.
+__device__ __forceinline__ int part_slot(long long block, int t0) { return (int)(2 * block) + (t0 > 0 ? 0 : 1); }
 
 // NT column tiles; W warps of U units of 16 positions in each step; R steps in
 // the ring; B blocks of an SM.
@@ -247,8 +263,7 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
   __shared__ unsigned long long list[kList];  // where the block's next steps lie (0: a page outside the pool)
   __shared__ uint32_t issued[R];              // 1 + the last step copied into each stage
   __shared__ float2 sm_ml[W][CT];  // a run's maximum and sum of each warp and column
-  __shared__ long long s_lo, s_hi, s_base;
-  __shared__ int s_entry;
+  __shared__ Runs s_run;  // the block's first run
   __shared__ volatile int give_up;
   __shared__ int pages[NTHR];  // cluster: the first pages of the item's sequence
   // cluster: the partial results of the columns that this block joins, column c
@@ -322,7 +337,6 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
           l_sum == 0.f ? -INFINITY : (M + log2f(l_sum)) * 0.69314718055994530942f;
   };
   Runs run;
-  long long lo;
   if (p.cluster) {  // this block's share of its cluster's item, at once with the first reads of pages and q
     const int item = blockIdx.x >> p.cluster_log, rank = blockIdx.x & (p.cluster - 1);
     const int e = item / p.a.n_kv_heads, head = item - e * p.a.n_kv_heads;
@@ -336,22 +350,24 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     run.nt = nt;
     run.t0 = nt * rank >> p.cluster_log;
     run.t1 = nt * (rank + 1) >> p.cluster_log;
-    lo = run.pos = run.t0;
-    run.hi = run.t1;
     pages[tid] = page;
   } else if (w == 0) {  // this block's share of all tiles
     long long total = 0;
-    for (int e = lane; e < p.n_entries; e += 32) total += tiles_of(p, e, CT, SP);
+    for (int e = lane; e < p.n_entries; e += 32) {
+      const int nt = tiles_of(p, e, CT, SP);
+      if (nt) total += nt + kOver;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     total *= p.a.n_kv_heads;
-    const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+    const long long lo = first_place(total, blockIdx.x, gridDim.x), hi = first_place(total, blockIdx.x + 1, gridDim.x);
     if (blockIdx.x == 0 && lane == 0) *p.total = total;
     long long base = 0;
     int entry = 0;
     if (lo < hi) {
       for (int e0 = 0; e0 < p.n_entries; e0 += 32) {
-        const long long n = e0 + lane < p.n_entries ? (long long)tiles_of(p, e0 + lane, CT, SP) * p.a.n_kv_heads : 0;
+        const int nt = e0 + lane < p.n_entries ? tiles_of(p, e0 + lane, CT, SP) : 0;
+        const long long n = nt ? (long long)(nt + kOver) * p.a.n_kv_heads : 0;
         long long incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -369,21 +385,21 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
       }
     }
     if (lane == 0) {
-      s_lo = lo;
-      s_hi = hi;
-      s_base = base;
-      s_entry = entry;
+      Runs r;
+      r.pos = lo;
+      r.hi = hi;
+      r.base = base;
+      r.e = entry;
+      if (!r.next(p, CT, SP)) r.t0 = r.t1 = 0;
+      s_run = r;
     }
   }
   __syncthreads();
-  if (!p.cluster) {
-    lo = run.pos = s_lo;
-    run.hi = s_hi;
-    run.base = s_base;
-    run.e = s_entry;
-  }
+  if (!p.cluster) run = s_run;
   const Runs mine = run;
-  const uint32_t n_steps = (uint32_t)(run.hi - lo);
+  uint32_t n_steps = run.t1 - run.t0;
+  if (!p.cluster && n_steps)
+    for (Runs r = mine; r.next(p, CT, SP);) n_steps += r.t1 - r.t0;
   uint32_t k = 0;  // steps done
   // Address of the block's step i, looked up by one thread (all of a window at once).
   auto look_up = [&](uint32_t i) {
@@ -402,8 +418,12 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
         pg = page_of(p.a, p.n_ctiles == 1 ? r.e : r.e / p.n_ctiles, r.t0 * SP);
       }
     } else {
-      r.pos += i;
-      if (!r.next(p, CT, SP)) return;
+      uint32_t before = 0;
+      while (i >= before + (r.t1 - r.t0)) {
+        before += r.t1 - r.t0;
+        if (!r.next(p, CT, SP)) return;
+      }
+      r.t0 += i - before;
       pg = page_of(p.a, p.n_ctiles == 1 ? r.e : r.e / p.n_ctiles, r.t0 * SP);
     }
     list[i % kList] = pg < 0 ? 0 : (unsigned long long)tile_of<HD>(p.a, pg, r.head, r.t0 * SP);
@@ -430,8 +450,8 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
   __syncthreads();
   if (p.cluster > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 
-  // a cluster's block has one run, set above
-  for (bool more = p.cluster ? n_steps > 0 : run.next(p, CT, SP); more; more = !p.cluster && run.next(p, CT, SP)) {
+  // a cluster's block has one run
+  for (bool more = n_steps > 0; more; more = !p.cluster && run.next(p, CT, SP)) {
     const int seq = p.n_ctiles == 1 ? run.e : run.e / p.n_ctiles, j = run.e - seq * p.n_ctiles;
     int len, nn;
     seq_extent(p.a, seq, len, nn);
@@ -728,7 +748,7 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
       }
     asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
     const bool whole = p.cluster <= 1 && run.t0 == 0 && run.t1 == run.nt;
-    const size_t slot = 2 * (size_t)blockIdx.x + (run.pos == lo ? 0 : 1);
+    const size_t slot = part_slot(blockIdx.x, run.t0);
     const int ncol = min(CT, p.cols - j * CT);
     for (int x = tid; x < ncol * HD / 2; x += NTHR) {
       const int c = x / (HD / 2), d = x % (HD / 2) * 2;
@@ -758,9 +778,9 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
       }
     }
     if (!p.cluster && tid == 0 && run.t0 == 0)
-      p.item[(size_t)run.e * p.a.n_kv_heads + run.head] = make_longlong2(whole ? -1 : run.pos, blockIdx.x);
-    run.pos += run.t1 - run.t0;
-    if (run.pos < run.hi) asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");  // the buffers are used again
+      p.item[(size_t)run.e * p.a.n_kv_heads + run.head] =
+          make_longlong2(whole ? -1 : run.base + (long long)run.head * (run.nt + kOver), blockIdx.x);
+    if (k < n_steps) asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");  // the buffers are used again
   }
   if (give_up && tid == 0) {  // copies in flight land before the block ends
     int none = 0;
@@ -835,11 +855,11 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
     for (int i = 0; i < V; ++i) o[i] = 0.f;
     if (nt) {
 #pragma unroll 4
-      for (long long b = it.y + w; total * b / G < it.x + nt; b += NW) {
-        const long long lo = total * b / G;
-        if (b >= G) break;
-        if (lo == total * (b + 1) / G) continue;  // a block without tiles
-        const float* src = p.part + ((2 * b + (lo >= it.x ? 0 : 1)) * CT + c) * (HD + 4);
+      for (long long b = it.y + w; b < G; b += NW) {
+        const long long lo = first_place(total, b, G) - it.x - kOver, hi = first_place(total, b + 1, G) - it.x - kOver;
+        if (lo >= nt) break;
+        if (hi <= 0 || hi <= lo) continue;  // a block without steps of this item
+        const float* src = p.part + ((size_t)part_slot(b, lo > 0) * CT + c) * (HD + 4);
         const float2 ml = *reinterpret_cast<const float2*>(src + HD);
         float v[V];
 #pragma unroll
@@ -879,7 +899,7 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
 
 // ---------------------------------------------------------------- host
 
-constexpr int kShort = 4;  // steps of a block, at most, for work that counts as short
+constexpr int kShort = 10;  // steps of a block, at most, for work that counts as short
 
 struct Plan {
   const void *main, *join;
@@ -932,19 +952,21 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
   else take_for<128>(pl, (int)cols, dtype);
   const long long ct = (cols + pl->CT - 1) / pl->CT, entries = ct * c.n_seqs, items = entries * c.n_kv_heads;
   const long long most = (long long)c.max_pages * (kPageTokens / pl->SP);  // steps of an item
-  if (items > INT_MAX / 32 || most * c.n_kv_heads > INT_MAX) return false;
+  if (items > INT_MAX / 32 || (most + kOver) * c.n_kv_heads > INT_MAX) return false;
   pl->n_ctiles = (int)ct;
   pl->n_entries = (int)entries;
   pl->items = (int)items;
   const long long room = (long long)pl->blocks * sm_count();  // blocks that run at once
   pl->cluster = 0;
-  if (items * most <= kShort * room) {
-    // Short work: an item is a cluster of up to 16 blocks, as many as run at
-    // once, joined through their shared memory.  It saves the second kernel and
-    // the scan of all lengths; a ragged batch is not levelled, which matters
-    // once the blocks have more than a few steps.
-    int n = 1;
-    while (n < 16 && 2 * n <= most && 2 * n * items <= room) n *= 2;
+  // Short work: an item is a cluster of up to 16 blocks, as many as run at once,
+  // joined through their shared memory.  It saves the second kernel and the scan
+  // of all lengths (16 sequences of 256 to 8448 positions: 17.2 us against 20.7),
+  // but a ragged batch is not levelled and a long item has 16 blocks at most, which
+  // loses once a block has more than about ten steps (131071 positions: 57.6
+  // us against 28.6).
+  int n = 1;
+  while (n < 16 && 2 * n <= most && 2 * n * items <= room) n *= 2;
+  if ((most + n - 1) / n <= kShort) {
     pl->cluster = n;
     if (n > 1) pl->smem += n * ((pl->CT + n - 1) / n) * (head_dim + 2) * (int)sizeof(float);
     pl->grid = (int)(items * n);
