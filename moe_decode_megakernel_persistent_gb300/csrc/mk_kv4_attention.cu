@@ -47,39 +47,11 @@
 #include <string>
 #include <type_traits>
 
-#include <cuda_fp16.h>
-
-#include "mk_kv4.cuh"
+#include "mk_kv4_att.cuh"
 
 namespace mk {
 namespace {
 
-constexpr uint64_t kWaitNs = 1000000000ull;        // bound of every wait
-constexpr int kList = 256;                         // steps whose addresses a block looks up at a time
-constexpr float kLow = -1e30f;                     // running maximum of a column that has seen nothing
-constexpr float kLazy = 8.f;                       // a maximum moves when a score passes it by this (log2)
-constexpr float kUp = 18446744073709551616.f;      // 2^64, carried by q
-constexpr double kDown = 36893488147419103232.0;   // 2^65 = 2^129 / 2^64, taken out of the scores
-constexpr float kCode = 1048576.f;                 // 2^20, taken out of the second product
-
-struct AttArgs {
-  Kv4Args a;
-  Kv4Rows q, out;
-  float* lse;
-  float c;              // scale * log2(e) * 2^65
-  int32_t n_heads, gqa;
-  int32_t gqa_log;      // log2(gqa), or -1
-  int32_t cols;         // rows * gqa: query columns of a (sequence, kv head)
-  int32_t n_ctiles;     // column tiles of it
-  int32_t n_entries;    // n_seqs * n_ctiles
-  int32_t cluster;      // > 0: an item is one cluster of so many blocks (a power of two), and there is no workspace
-  int32_t cluster_log;
-  long long* total;     // workspace: places of the call (Runs)
-  longlong2* item;      // workspace: [n_entries * n_kv_heads] first place and first block, or -1 (done)
-  float* part;          // workspace: [2 * grid][columns][HD + 4] partial results
-};
-
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -95,38 +67,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// Wait for a phase; gives up after kWaitNs (and at once when another warp of the
-// block has): then *give_up is set and the block runs to its end without data.
-__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* give_up, int32_t* status) {
-  const uint64_t t0 = now_ns();
-  for (uint32_t i = 0;; ++i) {
-    if (bar_try(bar, parity)) return true;
-    if (*give_up) return false;
-    if ((i & 15u) == 15u && now_ns() - t0 > kWaitNs) {
-      *give_up = 1;
-      if (status) atomicCAS(status, 0, MK_ERR_BARRIER_TIMEOUT);
-      return false;
-    }
-  }
-}
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* give_up, int32_t* status) {
-  return bar_try(bar, parity) || bar_wait_long(bar, parity, give_up, status);
-}
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
@@ -151,20 +91,6 @@ __device__ __forceinline__ uint32_t turn(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {  // bf16x2
-  uint32_t y;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack2h(float lo, float hi) {  // f16x2
-  uint32_t y;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
-  return y;
-}
-__device__ __forceinline__ float low_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)x)); }
-__device__ __forceinline__ float high_h(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x >> 16))); }
-__device__ __forceinline__ float low_f(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float high_f(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 // Store into another block's shared memory of the cluster.
 __device__ __forceinline__ void put_peer(const float* local, int rank, float2 v) {
   uint32_t y;
@@ -175,66 +101,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-constexpr uint32_t kNib = 0x80708070u;
-
-// The row of a query column.
-__device__ __forceinline__ int row_of(const AttArgs& p, int col) {
-  return p.gqa_log >= 0 ? col >> p.gqa_log : col / p.gqa;
-}
-
-// Column tile j of sequence s: how many steps of SP positions its columns see.
-__device__ __forceinline__ int tiles_of(const AttArgs& p, int e, int CT, int SP) {
-  const int s = p.n_ctiles == 1 ? e : e / p.n_ctiles, j = e - s * p.n_ctiles;
-  int len, nn;
-  seq_extent(p.a, s, len, nn);
-  if (row_of(p, j * CT) >= nn) return 0;                                  // its rows are padding
-  const int r = min(row_of(p, min((j + 1) * CT, p.cols) - 1), nn - 1);    // its last row
-  const int end = len - nn + r + 1;
-  return end <= 0 ? 0 : (end + SP - 1) / SP;
-}
-
-// The runs of a block.  All items are laid end to end, each as kOver places (an
-// item's set-up and end cost a block about as much as so many steps) and then
-// its steps; the block takes the steps of the places [pos, hi).
-constexpr int kOver = 4;
-struct Runs {
-  long long pos, hi, base;  // base: the first place of entry e
-  int e, nt, head, t0, t1;
-  __device__ __forceinline__ bool next(const AttArgs& p, int CT, int SP) {  // the next run; false: none is left
-    for (;;) {
-      if (pos >= hi) return false;
-      for (;; ++e) {
-        if (e >= p.n_entries) return false;  // lengths that change under the call
-        nt = tiles_of(p, e, CT, SP);
-        const long long n = nt ? (long long)(nt + kOver) * p.a.n_kv_heads : 0;
-        if (pos < base + n) break;
-        base += n;
-      }
-      const int len = nt + kOver, at = (int)(pos - base);  // held to 31 bits by the entry point
-      head = at / len;
-      const int in = at - head * len;
-      const int out = (int)min((long long)len, in + (hi - pos));
-      pos += out - in;
-      t0 = max(0, in - kOver);
-      t1 = max(0, out - kOver);
-      if (t1 > t0) return true;
-    }
-  }
-};
-// The first place of block b of G: the places cut into equal runs.
-__device__ __forceinline__ long long first_place(long long total, long long b, int G) {
-  if (total * G < 1ll << 32) return (uint32_t)total * (uint32_t)b / (uint32_t)G;
-  return total * b / G;
-}
-// A partial run that starts inside an item, and one that ends inside it: a
-// block has one of each at most, with a place of its own in the workspace.
-__device__ __forceinline__ int part_slot(long long block, int t0) { return (int)(2 * block) + (t0 > 0 ? 0 : 1); }
-
 // NT column tiles; W warps of U units of 16 positions in each step; R steps in
 // the ring; B blocks of an SM.
 template <int HD, class T, int NT, int W, int U, int R, int B>
@@ -352,47 +218,8 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     run.t1 = nt * (rank + 1) >> p.cluster_log;
     pages[tid] = page;
   } else if (w == 0) {  // this block's share of all tiles
-    long long total = 0;
-    for (int e = lane; e < p.n_entries; e += 32) {
-      const int nt = tiles_of(p, e, CT, SP);
-      if (nt) total += nt + kOver;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    total *= p.a.n_kv_heads;
-    const long long lo = first_place(total, blockIdx.x, gridDim.x), hi = first_place(total, blockIdx.x + 1, gridDim.x);
-    if (blockIdx.x == 0 && lane == 0) *p.total = total;
-    long long base = 0;
-    int entry = 0;
-    if (lo < hi) {
-      for (int e0 = 0; e0 < p.n_entries; e0 += 32) {
-        const int nt = e0 + lane < p.n_entries ? tiles_of(p, e0 + lane, CT, SP) : 0;
-        const long long n = nt ? (long long)(nt + kOver) * p.a.n_kv_heads : 0;
-        long long incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += up;
-        }
-        const uint32_t has = __ballot_sync(0xffffffffu, lo < base + incl);
-        if (has) {
-          const int f = __ffs(has) - 1;
-          entry = e0 + f;
-          base += __shfl_sync(0xffffffffu, incl - n, f);
-          break;
-        }
-        base += __shfl_sync(0xffffffffu, incl, 31);
-      }
-    }
-    if (lane == 0) {
-      Runs r;
-      r.pos = lo;
-      r.hi = hi;
-      r.base = base;
-      r.e = entry;
-      if (!r.next(p, CT, SP)) r.t0 = r.t1 = 0;
-      s_run = r;
-    }
+    const Runs r = first_run(p, CT, SP, lane);
+    if (lane == 0) s_run = r;
   }
   __syncthreads();
   if (!p.cluster) run = s_run;
@@ -899,9 +726,11 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
 
 // ---------------------------------------------------------------- host
 
+constexpr int kWideCols = 65;  // from so many bf16 columns on, tiles of 128 on tcgen05 (mk_kv4_wide.cu)
 constexpr int kShort = 10;  // steps of a block, at most, for work that counts as short
 
 struct Plan {
+  bool wide = false;
   const void *main, *join;
   int id;                    // of the variant
   int CT, SP, smem, base_smem, blocks, threads;  // columns of a tile, positions of a step; blocks of an SM
@@ -928,6 +757,19 @@ void take(Plan* pl) {
 // (registers hold the sums of 32 and 16 columns).
 template <int HD>
 void take_for(Plan* pl, int cols, int dtype) {
+  if (dtype == MK_BF16 && cols >= kWideCols) {
+    const WideKernel w = kv4_wide_kernel(HD);
+    pl->main = w.fn;
+    pl->join = reinterpret_cast<const void*>(&k_kv4_join<HD, __nv_bfloat16>);
+    pl->id = (HD == 64 ? 0 : 16) + 7;
+    pl->CT = w.CT;
+    pl->SP = w.SP;
+    pl->smem = pl->base_smem = w.smem;
+    pl->blocks = w.blocks;
+    pl->threads = w.threads;
+    pl->wide = true;
+    return;
+  }
   if (dtype == MK_F32) cols <= 8 ? take<HD, float, 1, 4, 1, 4, 3>(pl) : take<HD, float, 2, 4, 1, 4, 2>(pl);
   else if (cols <= 8) take<HD, __nv_bfloat16, 1, 4, 2, 2, 4>(pl);
   else if (cols <= 16) take<HD, __nv_bfloat16, 2, 4, 1, 4, 3>(pl);
@@ -966,7 +808,7 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
   // us against 28.6).
   int n = 1;
   while (n < 16 && 2 * n <= most && 2 * n * items <= room) n *= 2;
-  if ((most + n - 1) / n <= kShort) {
+  if (!pl->wide && (most + n - 1) / n <= kShort) {
     pl->cluster = n;
     if (n > 1) pl->smem += n * ((pl->CT + n - 1) / n) * (head_dim + 2) * (int)sizeof(float);
     pl->grid = (int)(items * n);
@@ -993,7 +835,8 @@ cudaError_t allow_smem(const Plan& pl) {
   if (e != cudaSuccess) return e;
   if (dev < 64 && (done[dev].load() >> pl.id & 1u)) return cudaSuccess;
   // a cluster's blocks take 16 x (columns / 16, rounded up) partial columns more, at most
-  e = cudaFuncSetAttribute(pl.main, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.base_smem + (pl.CT + 16) * 130 * 4);
+  e = cudaFuncSetAttribute(pl.main, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           pl.base_smem + (pl.wide ? 0 : (pl.CT + 16) * 130 * 4));
   if (e == cudaSuccess) e = cudaFuncSetAttribute(pl.main, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev < 64) done[dev].fetch_or(1u << pl.id);
   return e;
