@@ -1,27 +1,31 @@
 // Attention over the 4-bit paged cache for many query columns (prompt chunks):
 // tiles of 128 columns on the 5th-generation tensor cores (tcgen05).  The
 // mathematics, the split of the work and the join are those of
-// mk_kv4_attention.cu; what differs is who does what in a block.
+// mk_kv4_attention.cu; what differs is where the scales go and who does what.
 //
-//   S_g = Q_g K_g^T   for each group g of 64 dimensions: 128 columns x 64
-//                     positions, K = the codes as bf16 subnormals +-m 2^-129 (exact),
-//                     Q carrying 2^64; both groups' sums stay apart in TMEM, since
-//                     K's scales (one per position and group) multiply them;
-//   O_g += P_g V_g    P_g = weight x V's scale in fp16, read from TMEM over S's
-//                     place, V = the codes as fp16 subnormals +-m 2^-20.
+//   S = Q K^T   128 columns x 64 positions.  K = code x scale in fp16: 3 bits x 8
+//               bits are exact in its 11, the code as the subnormal +-m 2^-20, the
+//               scale times a power of two of the tile (its largest scale maps to
+//               2^14..2^15; rows 2^-9 of it and below lose low bits, an error of 2^-23 of
+//               the tile's largest values).  Q is fp16 times a power of two of the
+//               row (a bf16 value is exact down to 2^-29 of its row's largest).  The
+//               powers multiply the fp32 scores.
+//   O += P V    P = weights in fp16 (rounded by 2^-12, where the output is rounded
+//               to 2^-9) over S's place in TMEM; V as K, its power following the largest
+//               scale of the run, O rescaled when it moves.
+// So the 128 x 64 scores of a step need no scale of their own, and one pass: 64
+// scores a thread in registers, their maximum, one exponential each.  (With the
+// scales applied to scores and weights, as the narrow kernel does, a step took
+// 3,700 cycles of a column warp, and 195 us a chunk of 1024 rows at 8022 positions.)
 //
-// Warps 0..3: a thread has a query column (a TMEM lane).  It loads its 64 scores,
-// applies K's scales, keeps the running maximum and sum, and stores the two
-// groups' weights.  Running maxima and the normalisation of V's scales move only
-// when they are passed (by 2^8, by the next power of two and 2^3); then the warp
-// rescales its sums in TMEM.
-// Warps 4..7 unpack the tiles: 16 bytes of codes become four 16-byte words of
-// operands (1 instruction a value) in the 128-byte swizzled layout, dimensions
-// 0 2 1 3 4 6 5 7 of every eight (q is laid the same, and the sums are put back).
-// The next tile's codes are in registers meanwhile.  One lane of warp 4 issues the
-// products.
-// A block has one tile of S in flight (256 TMEM columns with O); two blocks
-// of an SM fill each other's waits.
+// Warps 0..3: a thread has a query column (a TMEM lane).  Its maximum moves only
+// when a score passes it by 2^8; then the warp rescales its sums in TMEM.
+// Warps 4..7 unpack: 16 bytes of codes become four 16-byte words of operands in
+// the 128-byte swizzled layout, dimensions 0 2 1 3 4 6 5 7 of every eight (q is laid
+// the same, and the sums are put back).  The next tile's codes are in registers
+// meanwhile.  One lane of warp 4 issues the products, S of a step while the
+// columns work on the one before it.
+// Two blocks of an SM (256 TMEM columns each) fill each other's waits.
 #include <algorithm>
 
 #include "mk_kv4_att.cuh"
@@ -34,18 +38,18 @@ struct Wide {
   static constexpr int NG = HD / kGroup, CT = 128, SP = kTile;
   static constexpr int QB = NG * CT * 128;          // bytes of q's operand
   static constexpr int KVB = NG * SP * 128;         // of K's (or V's) operand of a step
-  static constexpr int SCB = 2 * NG * SP * 4;       // of a step's scales, fp32
-  static constexpr int SMEM = 1024 + QB + 2 * (2 * KVB + SCB);
-  static constexpr int TM = NG * 128;               // TMEM columns: S [NG][64], O [NG][64]
+  static constexpr int SMEM = 1024 + QB + 4 * KVB;
+  static constexpr int TM = 256;                    // TMEM columns: S of two steps [2][64], O [HD]
 };
 
 // Shared-memory operand, 128-byte swizzle, rows of 128 bytes in atoms of 8 rows.
 __device__ __forceinline__ uint64_t operand(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFF) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+template <bool ADD>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
   asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-               "l"(a), "l"(b), "r"(idesc), "r"(add)
+               "l"(a), "l"(b), "r"(idesc), "n"(ADD ? 1 : 0)
                : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
@@ -84,13 +88,31 @@ __device__ __forceinline__ void tm_store16(uint32_t at, const uint32_t (&x)[16])
 }
 __device__ __forceinline__ void tm_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Four bytes of codes as eight operand values, dimensions 0 2 1 3 4 6 5 7.
-__device__ __forceinline__ uint4 unpack(uint32_t w) {
-  const uint32_t x = __byte_perm(w, 0, 0x1100), y = __byte_perm(w, 0, 0x3322);
-  return make_uint4((x << 4) & kNib, x & kNib, (y << 4) & kNib, y & kNib);
+__device__ __forceinline__ uint32_t mul2h(uint32_t a, uint32_t b) {  // f16x2
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
 }
+// Four bytes of codes times the scale pair h as eight operand values, dimensions
+// 0 2 1 3 4 6 5 7.
+__device__ __forceinline__ uint4 unpack(uint32_t w, uint32_t h) {
+  const uint32_t x = __byte_perm(w, 0, 0x1100), y = __byte_perm(w, 0, 0x3322);
+  return make_uint4(mul2h((x << 4) & kNib, h), mul2h(x & kNib, h), mul2h((y << 4) & kNib, h), mul2h(y & kNib, h));
+}
+// 2^n, n held to fp32's normal range.
+__device__ __forceinline__ float power(int n) { return __uint_as_float((uint32_t)(min(max(n, -126), 127) + 127) << 23); }
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 constexpr int kFirst = 1 << 8;  // of a step's note: the first of a run (low bits: positions that exist)
+constexpr float kRoom = 6.f;    // the weights are at most 2^(kLazy + kRoom) in fp16
+
+// What the unpacking warps say of a step.
+struct StepSays {
+  float k_mul;       // what the scores are times, but for the row's power
+  float v_exp;       // V's power of two: the operand is V 2^(v_exp - 20)
+  uint32_t bad[4];   // V scales that are no numbers: [group][positions 0..31, 32..63]
+};
 
 template <int HD>
 __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ AttArgs p) {
@@ -99,23 +121,24 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
   constexpr int NG = W::NG, CT = W::CT, SP = W::SP;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
-  __shared__ __align__(8) uint64_t kv_full[2], s_full, p_full, pv_done, q_full;
+  __shared__ __align__(8) uint64_t kv_full[2], s_full[2], pv_done[2], p_full, q_full;
   __shared__ unsigned long long list[kList];
   __shared__ int note[kList];
-  __shared__ float top_vs[2][2];  // the largest V scale of a step, by warp of 32 positions
+  __shared__ StepSays says[2];
+  __shared__ float raw[2][2 * NG][SP];   // a step's scales as they are: K's groups, V's groups
+  __shared__ float tops[2][2][2];        // their largest, by warp of 32 positions: K's, V's
   __shared__ uint32_t tm_base;
   __shared__ Runs s_run;
   __shared__ volatile int give_up;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   uint8_t* q_op = sm;
-  uint8_t* kv_op = sm + W::QB;                                        // [stage][K | V][g][64][128]
-  float* scales = reinterpret_cast<float*>(sm + W::QB + 4 * W::KVB);  // [stage][K g.., V g..][64]
+  uint8_t* kv_op = sm + W::QB;  // [stage][K | V][g][64][128]
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
-    const uint32_t bars[6] = {smem_addr(&kv_full[0]), smem_addr(&kv_full[1]), smem_addr(&s_full),
-                              smem_addr(&p_full), smem_addr(&pv_done), smem_addr(&q_full)};
-    const uint32_t n[6] = {4, 4, 1, 4, 1, 4};
-    for (int i = 0; i < 6; ++i)
+    const uint32_t bars[8] = {smem_addr(&kv_full[0]), smem_addr(&kv_full[1]), smem_addr(&s_full[0]), smem_addr(&s_full[1]),
+                              smem_addr(&pv_done[0]), smem_addr(&pv_done[1]), smem_addr(&p_full), smem_addr(&q_full)};
+    const uint32_t n[8] = {4, 4, 1, 1, 1, 1, 4, 4};
+    for (int i = 0; i < 8; ++i)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars[i]), "r"(n[i]) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     give_up = 0;
@@ -132,7 +155,7 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
   before_sync();
   __syncthreads();
   after_sync();
-  const uint32_t tm = tm_base;
+  const uint32_t tm = tm_base, tm_o = tm + 2 * SP;
   Runs run = s_run;
   const Runs mine = run;
   uint32_t n_steps = run.t1 - run.t0;
@@ -170,7 +193,7 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
         vc[c] = src ? __ldg(reinterpret_cast<const uint4*>(src + L::V) + u + 128 * c) : make_uint4(0, 0, 0, 0);
       }
       ks = vs = 0;
-      if (u < have) {  // a slot behind the end may hold anything
+      if (u < have) {  // a slot behind the end may hold anything: its scales count as 0
         if constexpr (NG == 2) {
           ks = __ldg(reinterpret_cast<const uint32_t*>(src + L::CODES) + u);
           vs = __ldg(reinterpret_cast<const uint32_t*>(src + L::V + L::CODES) + u);
@@ -182,20 +205,22 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
     };
     if (n_steps) fetch(0);
     uint32_t n_runs = 0;
-    constexpr uint32_t id_qk = (1u << 4) | (1u << 7) | (1u << 10) | ((SP >> 3) << 17) | ((CT >> 4) << 24);   // bf16
-    constexpr uint32_t id_pv = (1u << 4) | (1u << 16) | ((64 >> 3) << 17) | ((CT >> 4) << 24);               // fp16, V by rows
+    float cap = 0.f;  // V's scales of the run are below it
+    constexpr uint32_t id_qk = (1u << 4) | ((SP >> 3) << 17) | ((CT >> 4) << 24);               // fp16, fp32 sums
+    constexpr uint32_t id_pv = (1u << 4) | (1u << 16) | ((64 >> 3) << 17) | ((CT >> 4) << 24);  // V by rows
     // the second product of step i, once its weights are there
     auto second = [&](uint32_t i) {
       const bool ok = bar_wait(smem_addr(&p_full), i & 1, &give_up, p.a.status);
       after_sync();
       if (lane == 0 && ok && !give_up) {
-        const uint32_t first = note[i % kList] & kFirst, v = smem_addr(kv_op + ((i & 1) * 2 + 1) * W::KVB);
+        const uint32_t add = note[i % kList] & kFirst ? 0 : 1, pw = tm + SP * (i & 1);
+        const uint64_t v = operand(smem_addr(kv_op + ((i & 1) * 2 + 1) * W::KVB));
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
           for (int kk = 0; kk < SP / 16; ++kk)
-            mma_ts(tm + 64 * (NG + g), tm + 32 * g + 8 * kk, operand(v + g * SP * 128 + kk * 16 * 128), id_pv, !first || kk);
-        commit(smem_addr(&pv_done));
+            mma_ts(tm_o + 64 * g, pw + 8 * kk, v + ((g * SP * 128 + kk * 16 * 128) >> 4), id_pv, kk ? 1 : add);
+        commit(smem_addr(&pv_done[i & 1]));
       }
       __syncwarp();
     };
@@ -207,34 +232,62 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
         asm volatile("bar.sync 2, 128;" ::: "memory");
       }
       const int st = i & 1;
-      if (i >= 2) bar_wait(smem_addr(&pv_done), i & 1, &give_up, p.a.status);  // step i - 2 has left the stage
+      const bool first = note[i % kList] & kFirst;
+      uint32_t bad[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) bad[g] = 0;
+      if (u < SP) {
+        float tk = 0.f, tv = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float k = g ? high_f(ks) : low_f(ks), v = g ? high_f(vs) : low_f(vs);
+          raw[st][g][u] = k;
+          raw[st][NG + g][u] = finite(v) ? v : 0.f;  // what sees such a position is told of it instead
+          bad[g] = __ballot_sync(0xffffffffu, !finite(v));
+          if (finite(k)) tk = fmaxf(tk, fabsf(k));
+          if (finite(v)) tv = fmaxf(tv, fabsf(v));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          tk = fmaxf(tk, __shfl_xor_sync(0xffffffffu, tk, o));
+          tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, o));
+        }
+        if (lane == 0) {
+          tops[st][0][w - 4] = tk;
+          tops[st][1][w - 4] = tv;
+        }
+      }
+      if (i >= 2) bar_wait(smem_addr(&pv_done[st]), ((i - 2) >> 1) & 1, &give_up, p.a.status);  // step i - 2 has left the stage
+      asm volatile("bar.sync 2, 128;" ::: "memory");
       {
+        const float tk = fmaxf(tops[st][0][0], tops[st][0][1]), tv = fmaxf(tops[st][1][0], tops[st][1][1]);
+        const int nk = min(max(14 - exponent(tk), -100), 100);  // K's scales times 2^nk: below 2^15
+        if (first) cap = 0.f;
+        if (tv > cap || cap == 0.f) cap = power(min(max(exponent(tv) + 4, -80), 100));  // the next power of two, and 2^3 of room
+        const int nv = 15 - exponent(cap);
+        const float fk = power(nk), fv = power(nv);
+        if (u < SP && lane == 0) {
+#pragma unroll
+          for (int g = 0; g < NG; ++g) says[st].bad[2 * g + w - 4] = bad[g];
+          if (u == 0) {
+            says[st].k_mul = power(20 - nk);
+            says[st].v_exp = (float)nv;
+          }
+        }
         uint8_t* kd = kv_op + st * 2 * W::KVB;
         uint8_t* vd = kd + W::KVB;
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
           const int x = u + 128 * c, r = x / (2 * NG), cc = x % (2 * NG), g = cc / 2;
+          const float k = raw[st][g][r] * fk, v = raw[st][NG + g][r] * fv;
+          const uint32_t hk = pack2h(k, k), hv = pack2h(v, v);
           const uint32_t kw[4] = {kc[c].x, kc[c].y, kc[c].z, kc[c].w}, vw[4] = {vc[c].x, vc[c].y, vc[c].z, vc[c].w};
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
             const int at = g * SP * 128 + r * 128 + ((((cc & 1) * 4 + i4) ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(kd + at) = unpack(kw[i4]);
-            *reinterpret_cast<uint4*>(vd + at) = unpack(vw[i4]);
+            *reinterpret_cast<uint4*>(kd + at) = unpack(kw[i4], hk);
+            *reinterpret_cast<uint4*>(vd + at) = unpack(vw[i4], hv);
           }
-        }
-        if (u < SP) {
-          float* sc = scales + st * 2 * NG * SP + u;
-          float top = 0.f;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const float v = g ? high_f(vs) : low_f(vs);
-            sc[g * SP] = (g ? high_f(ks) : low_f(ks)) * p.c;
-            sc[(NG + g) * SP] = v;
-            top = fmaxf(top, v);
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (lane == 0) top_vs[st][w - 4] = top;
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -242,33 +295,37 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       if (lane == 0) arrive(smem_addr(&kv_full[st]));
       if (i + 1 < n_steps) fetch(i + 1);
       if (w == 4) {
-        // all warps have unpacked step i (and so have passed their wait for step
-        // i - 2) before step i - 1's end can be announced
+        // all warps have unpacked step i, and so have passed their wait for step
+        // i - 2, before step i - 1's end can be announced
         bool ok = bar_wait(smem_addr(&kv_full[st]), (i >> 1) & 1, &give_up, p.a.status);
-        if (i) {
-          second(i - 1);
-          ok = bar_wait(smem_addr(&pv_done), (i - 1) & 1, &give_up, p.a.status) && ok;  // the weights' place is free
-        }
-        if (note[i % kList] & kFirst) {
+        if (first) {
+          // q's operand and the sums are the next run's once the columns have
+          // read the last one's, whose weights they have left before
+          if (i) second(i - 1);
           ok = bar_wait(smem_addr(&q_full), n_runs & 1, &give_up, p.a.status) && ok;
           ++n_runs;
         }
         after_sync();
         if (lane == 0 && ok && !give_up) {
-          const uint32_t q = smem_addr(q_op), k = smem_addr(kv_op + st * 2 * W::KVB);
+          const uint64_t q = operand(smem_addr(q_op)), k = operand(smem_addr(kv_op + st * 2 * W::KVB));
+          const uint32_t to = tm + SP * st;
 #pragma unroll
           for (int g = 0; g < NG; ++g)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ss(tm + 64 * g, operand(q + g * CT * 128 + kk * 32), operand(k + g * SP * 128 + kk * 32), id_qk, kk);
-          commit(smem_addr(&s_full));
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t qa = q + ((g * CT * 128 + kk * 32) >> 4), kb = k + ((g * SP * 128 + kk * 32) >> 4);
+              if (g == 0 && kk == 0) mma_ss<false>(to, qa, kb, id_qk);
+              else mma_ss<true>(to, qa, kb, id_qk);
+            }
+          commit(smem_addr(&s_full[st]));
         }
         __syncwarp();
+        if (i && !first) second(i - 1);
       }
     }
     if (w == 4 && n_steps) second(n_steps - 1);
   } else {  // ---- a query column each
-    const uint32_t my = tm + ((uint32_t)(32 * w) << 16);  // this warp's lanes
+    const uint32_t mine_tm = (uint32_t)(32 * w) << 16;  // this warp's lanes
     uint32_t k = 0;
     for (bool more = n_steps > 0; more; more = run.next(p, CT, SP)) {
       const int seq = p.n_ctiles == 1 ? run.e : run.e / p.n_ctiles, j = run.e - seq * p.n_ctiles;
@@ -278,14 +335,26 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       int len, nn;
       seq_extent(p.a, seq, len, nn);
       const int lim = there && row < nn ? max(0, len - nn + row + 1) : 0;  // positions that it sees
+      float c_row;  // times a step's k_mul, the scores' factor
       {
         const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q.p) + seq * p.q.seq + row * p.q.row + hd * p.q.head;
+        float top = 0.f;
 #pragma unroll 4
         for (int x = 0; x < HD / 8; ++x) {
           uint4 v = make_uint4(0, 0, 0, 0);
           if (there) v = *reinterpret_cast<const uint4*>(src + 8 * x);
-          const uint4 y = make_uint4(pack2(low_f(v.x) * kUp, low_f(v.y) * kUp), pack2(high_f(v.x) * kUp, high_f(v.y) * kUp),
-                                     pack2(low_f(v.z) * kUp, low_f(v.w) * kUp), pack2(high_f(v.z) * kUp, high_f(v.w) * kUp));
+          top = fmaxf(top, fmaxf(fmaxf(fmaxf(fabsf(low_f(v.x)), fabsf(high_f(v.x))), fmaxf(fabsf(low_f(v.y)), fabsf(high_f(v.y)))),
+                                 fmaxf(fmaxf(fabsf(low_f(v.z)), fabsf(high_f(v.z))), fmaxf(fabsf(low_f(v.w)), fabsf(high_f(v.w))))));
+        }
+        const int nq = min(max(14 - exponent(top), -100), 100);
+        const float f = p.c < 0.f ? -power(nq) : power(nq);
+        c_row = fabsf(p.c) * power(-65) * power(-nq);
+#pragma unroll 4
+        for (int x = 0; x < HD / 8; ++x) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (there) v = *reinterpret_cast<const uint4*>(src + 8 * x);
+          const uint4 y = make_uint4(pack2h(low_f(v.x) * f, low_f(v.y) * f), pack2h(high_f(v.x) * f, high_f(v.y) * f),
+                                     pack2h(low_f(v.z) * f, low_f(v.w) * f), pack2h(high_f(v.z) * f, high_f(v.w) * f));
           const int g = x / 8, unit = x % 8;
           *reinterpret_cast<uint4*>(q_op + g * CT * 128 + tid * 128 + ((unit ^ (tid & 7)) << 4)) = y;
         }
@@ -293,101 +362,88 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive(smem_addr(&q_full));
-      // running maximum (log2) and sum, the sum and the weights times 2^e where
-      // V's scales are below cap = 2^(6 - e)
-      float m = kLow, l = 0.f, cap = 0.f, e = 0.f;
+      // running maximum (log2), the sum of the weights times 2^kRoom, V's power,
+      // and whether a V that is no number was seen in a group
+      float m = kLow, l = 0.f, e = 0.f;
+      bool bad[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) bad[g] = false;
       for (int t = run.t0; t < run.t1; ++t, ++k) {
         const int st = k & 1;
         bool ok = bar_wait(smem_addr(&kv_full[st]), (k >> 1) & 1, &give_up, p.a.status);
-        ok = bar_wait(smem_addr(&s_full), k & 1, &give_up, p.a.status) && ok;
+        ok = bar_wait(smem_addr(&s_full[st]), (k >> 1) & 1, &give_up, p.a.status) && ok;
         after_sync();
         if (ok && !give_up) {
-          const float* sc = scales + st * 2 * NG * SP;
           const int vis = min(lim - t * SP, note[k % kList] & (kFirst - 1));  // of the step's positions
+          const float cf = c_row * says[st].k_mul, ne = says[st].v_exp;
+          const uint32_t at = tm + mine_tm + SP * st;
           auto step = [&](auto cut_) {
             constexpr bool CUT = decltype(cut_)::value;
-            float s[SP], mx = -INFINITY;
+            float s[4][16], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < SP; c += 16) {
-              float a[NG][16];
+            for (int c = 0; c < 4; ++c) tm_load16(at + 16 * c, s[c]);
 #pragma unroll
-              for (int g = 0; g < NG; ++g) tm_load16(my + 64 * g + c, a[g]);
+            for (int c = 0; c < 4; ++c) tm_loaded(s[c]);
 #pragma unroll
-              for (int g = 0; g < NG; ++g) tm_loaded(a[g]);
-#pragma unroll
-              for (int x = 0; x < 16; x += 4) {
-                const float4 k0 = *reinterpret_cast<const float4*>(sc + c + x);
-                s[c + x] = a[0][x] * k0.x, s[c + x + 1] = a[0][x + 1] * k0.y;
-                s[c + x + 2] = a[0][x + 2] * k0.z, s[c + x + 3] = a[0][x + 3] * k0.w;
-                if constexpr (NG == 2) {
-                  const float4 k1 = *reinterpret_cast<const float4*>(sc + SP + c + x);
-                  s[c + x] = fmaf(a[1][x], k1.x, s[c + x]), s[c + x + 1] = fmaf(a[1][x + 1], k1.y, s[c + x + 1]);
-                  s[c + x + 2] = fmaf(a[1][x + 2], k1.z, s[c + x + 2]), s[c + x + 3] = fmaf(a[1][x + 3], k1.w, s[c + x + 3]);
-                }
-              }
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
               for (int x = 0; x < 16; ++x) {
-                if (CUT && c + x >= vis) s[c + x] = -INFINITY;
-                mx = fmaxf(mx, s[c + x]);
+                if (CUT && 16 * c + x >= vis) s[c][x] = -INFINITY;
+                mx[x & 3] = fmaxf(mx[x & 3], s[c][x]);
               }
-            }
-            const float top = fmaxf(top_vs[st][0], top_vs[st][1]);
-            if (__any_sync(0xffffffffu, mx > m + kLazy || top > cap)) {
-              float move = 1.f;
-              if (top > cap) {  // the next power of two, and 2^3 of room
-                const int b = min(max((int)(__float_as_uint(top) >> 23) + 4, 40), 200);  // 2^e stays within 2^+-93
-                const float ne = (float)(133 - b);
-                move = exp2_fast(ne - e);
-                cap = __uint_as_float((uint32_t)b << 23);
-                e = ne;
-              }
-              const float nm = fmaxf(m, mx), f = exp2_fast(m - nm) * move;
+            float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            most = most == -INFINITY ? most : most * cf;
+            if (__any_sync(0xffffffffu, most > m + kLazy || ne != e)) {
+              const float nm = fmaxf(m, most), f = exp2_fast(m - nm), fo = f * exp2_fast(ne - e);
               m = nm;
+              e = ne;
               l *= f;
               if (t > run.t0) {
+                bar_wait(smem_addr(&pv_done[(k - 1) & 1]), ((k - 1) >> 1) & 1, &give_up, p.a.status);  // the sums hold the last step
+                after_sync();
 #pragma unroll 1
-                for (int c = 0; c < NG * 64; c += 16) {
+                for (int c = 0; c < HD; c += 16) {
                   float o[16];
-                  uint32_t b[16];
-                  tm_load16(my + 64 * NG + c, o);
+                  uint32_t x16[16];
+                  tm_load16(tm_o + mine_tm + c, o);
                   tm_loaded(o);
 #pragma unroll
-                  for (int x = 0; x < 16; ++x) b[x] = __float_as_uint(o[x] * f);
-                  tm_store16(my + 64 * NG + c, b);
+                  for (int x = 0; x < 16; ++x) x16[x] = __float_as_uint(o[x] * fo);
+                  tm_store16(tm_o + mine_tm + c, x16);
                 }
               }
             }
-            const float sub = m - e;
+            const float sub = kRoom - m;
+            float la[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < SP; c += 32) {
-              uint32_t b[NG][16];
+            for (int c = 0; c < 4; c += 2) {
+              uint32_t b[16];
 #pragma unroll
-              for (int x = 0; x < 32; x += 4) {
-                float w4[4];
+              for (int x = 0; x < 32; x += 2) {
+                float w2[2];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  w4[y] = exp2_fast(s[c + x + y] - sub);
-                  l += w4[y];
+                for (int y = 0; y < 2; ++y) {
+                  float& z = s[c + x / 16][x % 16 + y];
+                  w2[y] = CUT && z == -INFINITY ? 0.f : exp2_fast(fmaf(z, cf, sub));
+                  la[(x + y) & 3] += w2[y];
                 }
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                  const float4 v = *reinterpret_cast<const float4*>(sc + (NG + g) * SP + c + x);
-                  float z[4] = {w4[0] * v.x, w4[1] * v.y, w4[2] * v.z, w4[3] * v.w};
-                  if constexpr (CUT) {  // whatever the scale of what is not seen
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                      if (c + x + y >= vis) z[y] = 0.f;
-                  }
-                  b[g][x / 2] = pack2h(z[0], z[1]);
-                  b[g][x / 2 + 1] = pack2h(z[2], z[3]);
-                }
+                b[x / 2] = pack2h(w2[0], w2[1]);
               }
-#pragma unroll
-              for (int g = 0; g < NG; ++g) tm_store16(my + 32 * g + c / 2, b[g]);
+              tm_store16(at + 8 * c, b);  // over the scores, which are all in registers
             }
+            l += (la[0] + la[1]) + (la[2] + la[3]);
           };
           if (__all_sync(0xffffffffu, vis >= SP)) step(std::false_type());
           else step(std::true_type());
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const uint32_t b0 = says[st].bad[2 * g], b1 = says[st].bad[2 * g + 1];
+            if (b0 | b1) {
+              const uint32_t v0 = vis >= 32 ? ~0u : vis > 0 ? (1u << vis) - 1 : 0u;
+              const uint32_t v1 = vis >= 64 ? ~0u : vis > 32 ? (1u << (vis - 32)) - 1 : 0u;
+              bad[g] |= (b0 & v0) || (b1 & v1);
+            }
+          }
           tm_stored();
         }
         before_sync();
@@ -395,23 +451,23 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
         if (lane == 0) arrive(smem_addr(&p_full));
       }
       // ---- the run's end: this column's sums, dimensions put back in order
-      bar_wait(smem_addr(&pv_done), (k - 1) & 1, &give_up, p.a.status);
+      bar_wait(smem_addr(&pv_done[(k - 1) & 1]), ((k - 1) >> 1) & 1, &give_up, p.a.status);
       after_sync();
       const bool whole = run.t0 == 0 && run.t1 == run.nt;
-      const float undo = kCode * exp2f(-e);
-      float f = whole ? (l == 0.f ? 0.f : kCode / l) : undo;
-      if (give_up) f = NAN;
+      const float undo = kCode * exp2f(-e), M = m - kRoom;
+      const float f = whole ? (l == 0.f ? 0.f : undo / l) : undo;
       float* part = p.part + ((size_t)part_slot(blockIdx.x, run.t0) * CT + tid) * (HD + 4);
       __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row +
                            hd * p.out.head;
 #pragma unroll 1
       for (int c = 0; c < HD; c += 16) {
         float o[16];
-        tm_load16(my + 64 * NG + c, o);
+        tm_load16(tm_o + mine_tm + c, o);
         tm_loaded(o);
         if (!there) continue;
+        const bool nan = give_up || (NG == 2 && c >= 64 ? bad[NG - 1] : bad[0]);
 #pragma unroll
-        for (int x = 0; x < 16; ++x) o[x] *= f;
+        for (int x = 0; x < 16; ++x) o[x] = nan ? NAN : o[x] * f;
 #pragma unroll
         for (int x = 0; x < 16; x += 8) {  // 0 2 1 3 4 6 5 7
           if (whole) {
@@ -423,12 +479,11 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
           }
         }
       }
-      const float sum = l * exp2f(-e);
       if (there) {
-        if (!whole) *reinterpret_cast<float2*>(part + HD) = make_float2(m, give_up ? NAN : sum);
+        if (!whole) *reinterpret_cast<float2*>(part + HD) = l == 0.f ? make_float2(kLow, 0.f) : make_float2(M, give_up ? NAN : l);
         else if (p.lse)
           p.lse[((size_t)seq * p.a.rows + row) * p.n_heads + hd] =
-              sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
+              l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994530942f;
       }
       if (tid == 0 && run.t0 == 0)
         p.item[(size_t)run.e * p.a.n_kv_heads + run.head] =
