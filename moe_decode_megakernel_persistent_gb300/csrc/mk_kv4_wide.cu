@@ -42,9 +42,10 @@ struct Wide {
   static constexpr int TM = 256;                    // TMEM columns: S of two steps [2][64], O [HD]
 };
 
-// Shared-memory operand, 128-byte swizzle, rows of 128 bytes in atoms of 8 rows.
-__device__ __forceinline__ uint64_t operand(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory operand, 128-byte swizzle, rows of 128 bytes in atoms of 8 rows;
+// far: from 64 columns of one taken by rows to the next 64.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t far = 16) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(far >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 template <bool ADD>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
   constexpr int NG = W::NG, CT = W::CT, SP = W::SP;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
-  __shared__ __align__(8) uint64_t kv_full[2], s_full[2], pv_done[2], p_full, q_full;
+  __shared__ __align__(8) uint64_t kv_full[2], s_full[2], p_full[2], pv_done[2], q_full;
   __shared__ unsigned long long list[kList];
   __shared__ int note[kList];
   __shared__ StepSays says[2];
@@ -134,11 +135,15 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
   uint8_t* q_op = sm;
   uint8_t* kv_op = sm + W::QB;  // [stage][K | V][g][64][128]
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // A barrier for each stage: a wait's one bit tells neighbouring phases apart, and
+  // none of these is two ahead of who waits for it: a stage's next round needs
+  // pv_done of this one, which needs every other.
   if (tid == 0) {
-    const uint32_t bars[8] = {smem_addr(&kv_full[0]), smem_addr(&kv_full[1]), smem_addr(&s_full[0]), smem_addr(&s_full[1]),
-                              smem_addr(&pv_done[0]), smem_addr(&pv_done[1]), smem_addr(&p_full), smem_addr(&q_full)};
-    const uint32_t n[8] = {4, 4, 1, 1, 1, 1, 4, 4};
-    for (int i = 0; i < 8; ++i)
+    const uint32_t bars[9] = {smem_addr(&kv_full[0]), smem_addr(&kv_full[1]), smem_addr(&s_full[0]), smem_addr(&s_full[1]),
+                              smem_addr(&p_full[0]), smem_addr(&p_full[1]), smem_addr(&pv_done[0]), smem_addr(&pv_done[1]),
+                              smem_addr(&q_full)};
+    const uint32_t n[9] = {4, 4, 1, 1, 4, 4, 1, 1, 4};
+    for (int i = 0; i < 9; ++i)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars[i]), "r"(n[i]) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     give_up = 0;
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
   if (n_steps)
     for (Runs r = mine; r.next(p, CT, SP);) n_steps += r.t1 - r.t0;
 
-  if (w >= 4) {  // ---- unpacking, and the products
+  if (w >= 4) {  // ---- unpacking, and the products (warp 4 the first, warp 5 the second)
     const int u = tid - 128;
     auto look_up = [&](uint32_t i) {
       Runs r = mine;
@@ -184,13 +189,24 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
     // (the first 64 threads) a position's scales
     uint4 kc[NG], vc[NG];
     uint32_t ks = 0, vs = 0;
+    // (eight neighbouring threads take eight rows: their stores meet all banks once)
+    auto place = [&](int c, int& r, int& cc) {
+      const int x = u + 128 * c;
+      r = (x >> 3) / (2 * NG) * 8 + (x & 7);
+      cc = (x >> 3) % (2 * NG);
+    };
+    auto word = [&](int c) {
+      int r, cc;
+      place(c, r, cc);
+      return r * 2 * NG + cc;
+    };
     auto fetch = [&](uint32_t i) {
       const uint8_t* src = reinterpret_cast<const uint8_t*>(list[i % kList]);
       const int have = note[i % kList] & (kFirst - 1);
 #pragma unroll
       for (int c = 0; c < NG; ++c) {
-        kc[c] = src ? __ldg(reinterpret_cast<const uint4*>(src) + u + 128 * c) : make_uint4(0, 0, 0, 0);
-        vc[c] = src ? __ldg(reinterpret_cast<const uint4*>(src + L::V) + u + 128 * c) : make_uint4(0, 0, 0, 0);
+        kc[c] = src ? __ldg(reinterpret_cast<const uint4*>(src) + word(c)) : make_uint4(0, 0, 0, 0);
+        vc[c] = src ? __ldg(reinterpret_cast<const uint4*>(src + L::V) + word(c)) : make_uint4(0, 0, 0, 0);
       }
       ks = vs = 0;
       if (u < have) {  // a slot behind the end may hold anything: its scales count as 0
@@ -205,25 +221,22 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
     };
     if (n_steps) fetch(0);
     uint32_t n_runs = 0;
-    float cap = 0.f;  // V's scales of the run are below it
     constexpr uint32_t id_qk = (1u << 4) | ((SP >> 3) << 17) | ((CT >> 4) << 24);               // fp16, fp32 sums
-    constexpr uint32_t id_pv = (1u << 4) | (1u << 16) | ((64 >> 3) << 17) | ((CT >> 4) << 24);  // V by rows
+    constexpr uint32_t id_pv = (1u << 4) | (1u << 16) | ((HD >> 3) << 17) | ((CT >> 4) << 24);  // V by rows
     // the second product of step i, once its weights are there
     auto second = [&](uint32_t i) {
-      const bool ok = bar_wait(smem_addr(&p_full), i & 1, &give_up, p.a.status);
+      const bool ok = bar_wait(smem_addr(&p_full[i & 1]), (i >> 1) & 1, &give_up, p.a.status);
       after_sync();
       if (lane == 0 && ok && !give_up) {
         const uint32_t add = note[i % kList] & kFirst ? 0 : 1, pw = tm + SP * (i & 1);
-        const uint64_t v = operand(smem_addr(kv_op + ((i & 1) * 2 + 1) * W::KVB));
+        const uint64_t v = operand(smem_addr(kv_op + ((i & 1) * 2 + 1) * W::KVB), SP * 128);
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int kk = 0; kk < SP / 16; ++kk)
-            mma_ts(tm_o + 64 * g, pw + 8 * kk, v + ((g * SP * 128 + kk * 16 * 128) >> 4), id_pv, kk ? 1 : add);
+        for (int kk = 0; kk < SP / 16; ++kk) mma_ts(tm_o, pw + 8 * kk, v + ((kk * 16 * 128) >> 4), id_pv, kk ? 1 : add);
         commit(smem_addr(&pv_done[i & 1]));
       }
       __syncwarp();
     };
+    float cap = 0.f;  // V's scales of the run are below it
     for (uint32_t i = 0; i < n_steps; ++i) {
       if (i % (kList / 2) == 0 && i) {
         asm volatile("bar.sync 2, 128;" ::: "memory");
@@ -247,11 +260,9 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
           if (finite(k)) tk = fmaxf(tk, fabsf(k));
           if (finite(v)) tv = fmaxf(tv, fabsf(v));
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          tk = fmaxf(tk, __shfl_xor_sync(0xffffffffu, tk, o));
-          tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, o));
-        }
+        // (the order of non-negative floats is that of their bits)
+        tk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(tk)));
+        tv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(tv)));
         if (lane == 0) {
           tops[st][0][w - 4] = tk;
           tops[st][1][w - 4] = tv;
@@ -278,7 +289,9 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
         uint8_t* vd = kd + W::KVB;
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
-          const int x = u + 128 * c, r = x / (2 * NG), cc = x % (2 * NG), g = cc / 2;
+          int r, cc;
+          place(c, r, cc);
+          const int g = cc / 2;
           const float k = raw[st][g][r] * fk, v = raw[st][NG + g][r] * fv;
           const uint32_t hk = pack2h(k, k), hv = pack2h(v, v);
           const uint32_t kw[4] = {kc[c].x, kc[c].y, kc[c].z, kc[c].w}, vw[4] = {vc[c].x, vc[c].y, vc[c].z, vc[c].w};
@@ -296,12 +309,9 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       if (i + 1 < n_steps) fetch(i + 1);
       if (w == 4) {
         // all warps have unpacked step i, and so have passed their wait for step
-        // i - 2, before step i - 1's end can be announced
+        // i - 2, before step i's weights can be there
         bool ok = bar_wait(smem_addr(&kv_full[st]), (i >> 1) & 1, &give_up, p.a.status);
-        if (first) {
-          // q's operand and the sums are the next run's once the columns have
-          // read the last one's, whose weights they have left before
-          if (i) second(i - 1);
+        if (first) {  // the columns lay q after they have read the last run's sums
           ok = bar_wait(smem_addr(&q_full), n_runs & 1, &give_up, p.a.status) && ok;
           ++n_runs;
         }
@@ -320,10 +330,10 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
           commit(smem_addr(&s_full[st]));
         }
         __syncwarp();
-        if (i && !first) second(i - 1);
       }
+      if (w == 5 && i) second(i - 1);
     }
-    if (w == 4 && n_steps) second(n_steps - 1);
+    if (w == 5 && n_steps) second(n_steps - 1);
   } else {  // ---- a query column each
     const uint32_t mine_tm = (uint32_t)(32 * w) << 16;  // this warp's lanes
     uint32_t k = 0;
@@ -448,7 +458,7 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
         }
         before_sync();
         __syncwarp();
-        if (lane == 0) arrive(smem_addr(&p_full));
+        if (lane == 0) arrive(smem_addr(&p_full[st]));
       }
       // ---- the run's end: this column's sums, dimensions put back in order
       bar_wait(smem_addr(&pv_done[(k - 1) & 1]), ((k - 1) >> 1) & 1, &give_up, p.a.status);
