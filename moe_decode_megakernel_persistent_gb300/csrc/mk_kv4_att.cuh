@@ -110,6 +110,7 @@ __device__ __forceinline__ int tiles_of(const AttArgs& p, int e, int CT, int SP)
 // item's set-up and end cost a block about as much as so many steps) and then
 // its steps; the block takes the steps of the places [pos, hi).
 constexpr int kOver = 4;
+constexpr int kMaxBlocks = 1024;
 struct Runs {
   long long pos, hi, base;  // base: the first place of entry e
   int e, nt, head, t0, t1;

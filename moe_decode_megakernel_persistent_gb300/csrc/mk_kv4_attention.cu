@@ -661,52 +661,95 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
   }
 }
 
-// Items cut between blocks: block (item, column) joins the partial results in
-// the blocks' order, each warp every NW-th of them with a running maximum, the
-// warps at the end.  Items without a tile (nothing seen) get zeros here.
+// Items cut between blocks: a block joins the partial results of CC columns of
+// an item, in the blocks' order.  First the places of the item's parts, once for
+// all of its columns; then up to kFewParts of them are a warp's work, a column
+// each, and more are all warps' work, every NW-th part each with a running maximum,
+// the warps at the end.  Items without a tile (nothing seen) get zeros here.
+// (1024 rows at 8022 positions, 16384 columns of about 3 parts: a block for every column
+// with the places found by every warp took 33 us.)
+constexpr int kFewParts = 4;
 template <int HD, class T>
-__global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArgs p, int CT, int SP, int G) {
+__global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArgs p, int CT, int SP, int G, int CC) {
   constexpr int V = HD / 32;  // dimensions of a lane
   __shared__ float red[16][HD], red_m[16], red_l[16];
+  __shared__ int slot[kMaxBlocks], n_parts;  // -1: a block without steps of this item
   const int e = blockIdx.x / p.a.n_kv_heads, head = blockIdx.x - e * p.a.n_kv_heads;
   const int seq = e / p.n_ctiles, j = e - seq * p.n_ctiles;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, NW = blockDim.x >> 5;
+  const int c0 = blockIdx.y * CC, c1 = min(min(c0 + CC, CT), p.cols - j * CT);
+  if (c0 >= c1) return;
   const int nt = tiles_of(p, e, CT, SP);
+  if (threadIdx.x == 0) n_parts = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const longlong2 it = nt ? p.item[blockIdx.x] : make_longlong2(0, 0);
-  const long long total = *p.total;
-  if (nt && (it.x < 0 || it.y < 0 || it.y >= G)) return;
-  for (int c = blockIdx.y; c < CT && j * CT + c < p.cols; c += gridDim.y) {
-    float m = kLow, l = 0.f, o[V];
+  __syncthreads();
+  if (nt) {
+    const longlong2 it = p.item[blockIdx.x];
+    const long long total = *p.total;
+    if (it.x < 0 || it.y < 0 || it.y >= G) return;  // done by its block
+    for (int i = threadIdx.x; it.y + i < G; i += blockDim.x) {
+      const long long lo = first_place(total, it.y + i, G) - it.x - kOver;
+      if (lo >= nt) break;
+      const long long hi = first_place(total, it.y + i + 1, G) - it.x - kOver;
+      slot[i] = hi <= 0 || hi <= lo ? -1 : part_slot(it.y + i, lo > 0);
+      atomicMax(&n_parts, i + 1);
+    }
+    __syncthreads();
+  }
+  const int n = n_parts;
+  float m, l, o[V];
+  auto gather = [&](int c, int first, int by) {
+    m = kLow, l = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = 0.f;
-    if (nt) {
 #pragma unroll 4
-      for (long long b = it.y + w; b < G; b += NW) {
-        const long long lo = first_place(total, b, G) - it.x - kOver, hi = first_place(total, b + 1, G) - it.x - kOver;
-        if (lo >= nt) break;
-        if (hi <= 0 || hi <= lo) continue;  // a block without steps of this item
-        const float* src = p.part + ((size_t)part_slot(b, lo > 0) * CT + c) * (HD + 4);
-        const float2 ml = *reinterpret_cast<const float2*>(src + HD);
-        float v[V];
+    for (int i = first; i < n; i += by) {
+      const int at = slot[i];
+      if (at < 0) continue;
+      const float* src = p.part + ((size_t)at * CT + c) * (HD + 4);
+      const float2 ml = *reinterpret_cast<const float2*>(src + HD);
+      float v[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = src[lane * V + i];
-        const float M = fmaxf(m, ml.x), f0 = exp2_fast(m - M), f1 = exp2_fast(ml.x - M);
-        m = M;
-        l = l * f0 + ml.y * f1;
+      for (int x = 0; x < V; ++x) v[x] = src[lane * V + x];
+      const float M = fmaxf(m, ml.x), f0 = exp2_fast(m - M), f1 = exp2_fast(ml.x - M);
+      m = M;
+      l = l * f0 + ml.y * f1;
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = o[i] * f0 + v[i] * f1;
-      }
+      for (int x = 0; x < V; ++x) o[x] = o[x] * f0 + v[x] * f1;
     }
+  };
+  auto place = [&](int c, int& row, int& hd) {
+    const int col = j * CT + c;
+    row = row_of(p, col);
+    hd = head * p.gqa + col - row * p.gqa;
+    return reinterpret_cast<T*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row + hd * p.out.head;
+  };
+  auto put_lse = [&](int row, int hd, float M, float ls) {
+    p.lse[((size_t)seq * p.a.rows + row) * p.n_heads + hd] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994530942f;
+  };
+  if (n <= kFewParts) {
+    for (int c = c0 + w; c < c1; c += NW) {
+      gather(c, 0, 1);
+      int row, hd;
+      T* dst = place(c, row, hd);
+#pragma unroll
+      for (int x = 0; x < V; ++x) dst[lane * V + x] = (T)(l == 0.f ? 0.f : o[x] / l);
+      if (p.lse && lane == 0) put_lse(row, hd, m, l);
+    }
+    return;
+  }
+  for (int c = c0; c < c1; ++c) {
+    gather(c, w, NW);
     __syncthreads();
     if (lane == 0) {
       red_m[w] = m;
       red_l[w] = l;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) red[w][lane * V + i] = o[i];
+    for (int x = 0; x < V; ++x) red[w][lane * V + x] = o[x];
     __syncthreads();
-    const int col = j * CT + c, row = col / p.gqa, hd = head * p.gqa + col - row * p.gqa;
+    int row, hd;
+    T* dst = place(c, row, hd);
     for (int d = threadIdx.x; d < HD; d += blockDim.x) {
       float M = kLow, ls = 0.f, v = 0.f;
       for (int i = 0; i < NW; ++i) M = fmaxf(M, red_m[i]);
@@ -715,11 +758,8 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
         ls += red_l[i] * f;
         v += red[i][d] * f;
       }
-      const float r = ls == 0.f ? 0.f : v / ls;
-      (reinterpret_cast<T*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row + hd * p.out.head)[d] = (T)r;
-      if (p.lse && d == 0)
-        p.lse[((size_t)seq * p.a.rows + row) * p.n_heads + hd] =
-            ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994530942f;
+      dst[d] = (T)(ls == 0.f ? 0.f : v / ls);
+      if (p.lse && d == 0) put_lse(row, hd, M, ls);
     }
   }
 }
@@ -734,7 +774,7 @@ struct Plan {
   const void *main, *join;
   int id;                    // of the variant
   int CT, SP, smem, base_smem, blocks, threads;  // columns of a tile, positions of a step; blocks of an SM
-  int n_ctiles, n_entries, items, grid, join_y, join_threads;
+  int n_ctiles, n_entries, items, grid, join_cols, join_threads;
   int cluster;               // blocks of an item's cluster; 0: the tiles of all items in equal runs
   size_t item_off, part_off, bytes;
 };
@@ -798,7 +838,7 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
   pl->n_ctiles = (int)ct;
   pl->n_entries = (int)entries;
   pl->items = (int)items;
-  const long long room = (long long)pl->blocks * sm_count();  // blocks that run at once
+  const long long room = std::min(pl->blocks * sm_count(), kMaxBlocks);  // blocks that run at once
   pl->cluster = 0;
   // Short work: an item is a cluster of up to 16 blocks, as many as run at once,
   // joined through their shared memory.  It saves the second kernel and the scan
@@ -816,11 +856,12 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
     return true;
   }
   pl->grid = (int)std::min<long long>(room, items * most);
-  // an item is joined from about grid / items blocks: as many warps for each column
+  // The join.  An item has about grid / items parts: as many warps for each column, and
+  // a block for a column while that is few blocks.
+  pl->join_cols = (long long)items * pl->CT <= 2048 ? 1 : 16;
   int nw = 2;
   while (nw < 16 && nw * 2 * items <= pl->grid) nw *= 2;
-  pl->join_threads = 32 * nw;
-  pl->join_y = items < 2048 ? pl->CT : 1;
+  pl->join_threads = 32 * (pl->join_cols > 1 ? std::max(nw, 8) : nw);
   pl->item_off = 16;
   pl->part_off = pl->item_off + (size_t)items * sizeof(longlong2);
   pl->bytes = pl->part_off + 2 * (size_t)pl->grid * pl->CT * (head_dim + 4) * sizeof(float);
@@ -905,11 +946,11 @@ int kv4_attention(const Kv4Args& a, int head_dim, int n_heads, const Kv4Rows& q,
   if (e == cudaSuccess && !pl.cluster) {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(pl.items, pl.join_y);
+    cfg.gridDim = dim3(pl.items, (pl.CT + pl.join_cols - 1) / pl.join_cols);
     cfg.blockDim = dim3(pl.join_threads);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    void* args[] = {&p, &pl.CT, &pl.SP, &pl.grid};
+    void* args[] = {&p, &pl.CT, &pl.SP, &pl.grid, &pl.join_cols};
     e = cudaLaunchKernelExC(&cfg, pl.join, args);
   }
   if (e != cudaSuccess) {
