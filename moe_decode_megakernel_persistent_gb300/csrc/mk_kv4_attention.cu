@@ -766,7 +766,12 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
 
 // ---------------------------------------------------------------- host
 
-constexpr int kWideCols = 65;  // from so many bf16 columns on, tiles of 128 on tcgen05 (mk_kv4_wide.cu)
+// From so many bf16 columns on, tiles of 128 on tcgen05 (mk_kv4_wide.cu): what no longer
+// fits one tile of the narrow kernel, which unpacks a cache tile for each 32 columns.  36
+// columns: one sequence of 8022 positions 18.6 us against 26.9, 16 of 700 25 against
+// 32, 16 of 8192 92 against 84; 64 columns: 20.0, 26, 93 against 30.1, 32, 85; 32 columns,
+// one of 8022: 19.4 against 15.6.
+constexpr int kWideCols = 33;
 constexpr int kShort = 10;  // steps of a block, at most, for work that counts as short
 
 struct Plan {

@@ -23,9 +23,16 @@
 // Warps 4..7 unpack: 16 bytes of codes become four 16-byte words of operands in
 // the 128-byte swizzled layout, dimensions 0 2 1 3 4 6 5 7 of every eight (q is laid
 // the same, and the sums are put back).  The next tile's codes are in registers
-// meanwhile.  One lane of warp 4 issues the products, S of a step while the
-// columns work on the one before it.
+// meanwhile.  K's operand of a step is laid while the second product of the step before
+// the last still reads its V, and one lane of the four warps in turn issues the
+// products, S of a step while the columns work on the one before it.  (By one warp
+// for all steps: 122 us; a warp of its own for them, with three that unpack: 127.)
 // Two blocks of an SM (256 TMEM columns each) fill each other's waits.
+//
+// Measured: 1024 rows of 16 heads on 4 kv heads of 128 dimensions, 8022 positions,
+// 115 us, 295 TFLOP/s of 4 x dimensions x seen pairs; tensor cores 25% active.
+// A step takes about 2,900 cycles of a block, in which a column warp works 2,200 and waits
+// for the scores otherwise; 700 cycles of an unpacking warp's share are the codes.
 #include <algorithm>
 
 #include "mk_kv4_att.cuh"
@@ -122,12 +129,10 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
   constexpr int NG = W::NG, CT = W::CT, SP = W::SP;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
-  __shared__ __align__(8) uint64_t kv_full[2], s_full[2], p_full[2], pv_done[2], q_full;
+  __shared__ __align__(8) uint64_t k_full[4], v_full[2], s_full[2], p_full[2], pv_done[2], q_full;
   __shared__ unsigned long long list[kList];
   __shared__ int note[kList];
-  __shared__ StepSays says[2];
-  __shared__ float raw[2][2 * NG][SP];   // a step's scales as they are: K's groups, V's groups
-  __shared__ float tops[2][2][2];        // their largest, by warp of 32 positions: K's, V's
+  __shared__ StepSays says[4];
   __shared__ uint32_t tm_base;
   __shared__ Runs s_run;
   __shared__ volatile int give_up;
@@ -135,16 +140,15 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
   uint8_t* q_op = sm;
   uint8_t* kv_op = sm + W::QB;  // [stage][K | V][g][64][128]
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // A barrier for each stage: a wait's one bit tells neighbouring phases apart, and
-  // none of these is two ahead of who waits for it: a stage's next round needs
-  // pv_done of this one, which needs every other.
+  // A wait's one bit tells neighbouring phases apart, so none may be two ahead of who
+  // waits for it.  K's operand of step i is laid when S of i - 2 is done and V's when
+  // pv_done of i - 2 is, so v_full, s_full, p_full and pv_done of a stage wait for
+  // who reads the last one; k_full may be a stage's round ahead of the columns and has four.
   if (tid == 0) {
-    const uint32_t bars[9] = {smem_addr(&kv_full[0]), smem_addr(&kv_full[1]), smem_addr(&s_full[0]), smem_addr(&s_full[1]),
-                              smem_addr(&p_full[0]), smem_addr(&p_full[1]), smem_addr(&pv_done[0]), smem_addr(&pv_done[1]),
-                              smem_addr(&q_full)};
-    const uint32_t n[9] = {4, 4, 1, 1, 4, 4, 1, 1, 4};
-    for (int i = 0; i < 9; ++i)
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars[i]), "r"(n[i]) : "memory");
+    uint64_t* const bars[13] = {&k_full[0], &k_full[1], &k_full[2], &k_full[3], &v_full[0],  &v_full[1], &p_full[0],
+                                &p_full[1], &q_full,    &s_full[0], &s_full[1], &pv_done[0], &pv_done[1]};
+    for (int i = 0; i < 13; ++i)  // by each of four warps, by one
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bars[i])), "r"(i < 9 ? 4 : 1) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     give_up = 0;
   }
@@ -167,7 +171,7 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
   if (n_steps)
     for (Runs r = mine; r.next(p, CT, SP);) n_steps += r.t1 - r.t0;
 
-  if (w >= 4) {  // ---- unpacking, and the products (warp 4 the first, warp 5 the second)
+  if (w >= 4) {  // ---- unpacking, and the products (the warps take turns)
     const int u = tid - 128;
     auto look_up = [&](uint32_t i) {
       Runs r = mine;
@@ -186,9 +190,9 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
     for (uint32_t i = u; i < kList && i < n_steps; i += 128) look_up(i);
     asm volatile("bar.sync 2, 128;" ::: "memory");
     // a thread's part of a tile: NG 16-byte words of K codes and of V codes, and
-    // (the first 64 threads) a position's scales
+    // each warp all positions' scales
     uint4 kc[NG], vc[NG];
-    uint32_t ks = 0, vs = 0;
+    uint32_t ks[2], vs[2];  // of positions lane and lane + 32, both groups
     // (eight neighbouring threads take eight rows: their stores meet all banks once)
     auto place = [&](int c, int& r, int& cc) {
       const int x = u + 128 * c;
@@ -200,32 +204,75 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       place(c, r, cc);
       return r * 2 * NG + cc;
     };
-    auto fetch = [&](uint32_t i) {
+    auto fetch_k = [&](uint32_t i) {
       const uint8_t* src = reinterpret_cast<const uint8_t*>(list[i % kList]);
       const int have = note[i % kList] & (kFirst - 1);
 #pragma unroll
-      for (int c = 0; c < NG; ++c) {
+      for (int c = 0; c < NG; ++c)
         kc[c] = src ? __ldg(reinterpret_cast<const uint4*>(src) + word(c)) : make_uint4(0, 0, 0, 0);
-        vc[c] = src ? __ldg(reinterpret_cast<const uint4*>(src + L::V) + word(c)) : make_uint4(0, 0, 0, 0);
-      }
-      ks = vs = 0;
-      if (u < have) {  // a slot behind the end may hold anything: its scales count as 0
-        if constexpr (NG == 2) {
-          ks = __ldg(reinterpret_cast<const uint32_t*>(src + L::CODES) + u);
-          vs = __ldg(reinterpret_cast<const uint32_t*>(src + L::V + L::CODES) + u);
-        } else {
-          ks = __ldg(reinterpret_cast<const uint16_t*>(src + L::CODES) + u);
-          vs = __ldg(reinterpret_cast<const uint16_t*>(src + L::V + L::CODES) + u);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = lane + 32 * h;
+        ks[h] = vs[h] = 0;
+        if (at < have) {  // a slot behind the end may hold anything: its scales count as 0
+          if constexpr (NG == 2) {
+            ks[h] = __ldg(reinterpret_cast<const uint32_t*>(src + L::CODES) + at);
+            vs[h] = __ldg(reinterpret_cast<const uint32_t*>(src + L::V + L::CODES) + at);
+          } else {
+            ks[h] = __ldg(reinterpret_cast<const uint16_t*>(src + L::CODES) + at);
+            vs[h] = __ldg(reinterpret_cast<const uint16_t*>(src + L::V + L::CODES) + at);
+          }
         }
       }
     };
-    if (n_steps) fetch(0);
+    auto fetch_v = [&](uint32_t i) {
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(list[i % kList]);
+#pragma unroll
+      for (int c = 0; c < NG; ++c)
+        vc[c] = src ? __ldg(reinterpret_cast<const uint4*>(src + L::V) + word(c)) : make_uint4(0, 0, 0, 0);
+    };
+    // a thread's words of codes as operands, times their scales and f
+    auto lay = [&](uint8_t* to, const uint4* from, uint32_t of0, uint32_t of1, float f, bool v) {
+#pragma unroll
+      for (int c = 0; c < NG; ++c) {
+        int r, cc;
+        place(c, r, cc);
+        const int g = cc / 2;
+        const uint32_t both = __shfl_sync(0xffffffffu, (r & 32) ? of1 : of0, r & 31);  // (a warp's rows of one c are in one half)
+        float x = g ? high_f(both) : low_f(both);
+        if (v && !finite(x)) x = 0.f;  // what sees such a position is told of it instead
+        x *= f;
+        const uint32_t h = pack2h(x, x), word4[4] = {from[c].x, from[c].y, from[c].z, from[c].w};
+#pragma unroll
+        for (int i4 = 0; i4 < 4; ++i4)
+          *reinterpret_cast<uint4*>(to + g * SP * 128 + r * 128 + ((((cc & 1) * 4 + i4) ^ (r & 7)) << 4)) = unpack(word4[i4], h);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+    };
+    // the largest finite of a tile's scales
+    auto largest = [&](uint32_t a, uint32_t b) {
+      float top = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float x = fabsf(g ? high_f(h ? b : a) : low_f(h ? b : a));
+          if (finite(x)) top = fmaxf(top, x);
+        }
+      return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // (non-negative floats: in their bits' order)
+    };
+    if (n_steps) {
+      fetch_k(0);
+      fetch_v(0);
+    }
     uint32_t n_runs = 0;
     constexpr uint32_t id_qk = (1u << 4) | ((SP >> 3) << 17) | ((CT >> 4) << 24);               // fp16, fp32 sums
     constexpr uint32_t id_pv = (1u << 4) | (1u << 16) | ((HD >> 3) << 17) | ((CT >> 4) << 24);  // V by rows
     // the second product of step i, once its weights are there
     auto second = [&](uint32_t i) {
-      const bool ok = bar_wait(smem_addr(&p_full[i & 1]), (i >> 1) & 1, &give_up, p.a.status);
+      bool ok = bar_wait(smem_addr(&p_full[i & 1]), (i >> 1) & 1, &give_up, p.a.status);
+      ok = bar_wait(smem_addr(&v_full[i & 1]), (i >> 1) & 1, &give_up, p.a.status) && ok;
       after_sync();
       if (lane == 0 && ok && !give_up) {
         const uint32_t add = note[i % kList] & kFirst ? 0 : 1, pw = tm + SP * (i & 1);
@@ -246,79 +293,41 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       }
       const int st = i & 1;
       const bool first = note[i % kList] & kFirst;
-      uint32_t bad[NG];
-#pragma unroll
-      for (int g = 0; g < NG; ++g) bad[g] = 0;
-      if (u < SP) {
-        float tk = 0.f, tv = 0.f;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const float k = g ? high_f(ks) : low_f(ks), v = g ? high_f(vs) : low_f(vs);
-          raw[st][g][u] = k;
-          raw[st][NG + g][u] = finite(v) ? v : 0.f;  // what sees such a position is told of it instead
-          bad[g] = __ballot_sync(0xffffffffu, !finite(v));
-          if (finite(k)) tk = fmaxf(tk, fabsf(k));
-          if (finite(v)) tv = fmaxf(tv, fabsf(v));
-        }
-        // (the order of non-negative floats is that of their bits)
-        tk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(tk)));
-        tv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(tv)));
-        if (lane == 0) {
-          tops[st][0][w - 4] = tk;
-          tops[st][1][w - 4] = tv;
-        }
-      }
-      if (i >= 2) bar_wait(smem_addr(&pv_done[st]), ((i - 2) >> 1) & 1, &give_up, p.a.status);  // step i - 2 has left the stage
-      asm volatile("bar.sync 2, 128;" ::: "memory");
-      {
-        const float tk = fmaxf(tops[st][0][0], tops[st][0][1]), tv = fmaxf(tops[st][1][0], tops[st][1][1]);
-        const int nk = min(max(14 - exponent(tk), -100), 100);  // K's scales times 2^nk: below 2^15
-        if (first) cap = 0.f;
-        if (tv > cap || cap == 0.f) cap = power(min(max(exponent(tv) + 4, -80), 100));  // the next power of two, and 2^3 of room
-        const int nv = 15 - exponent(cap);
-        const float fk = power(nk), fv = power(nv);
-        if (u < SP && lane == 0) {
-#pragma unroll
-          for (int g = 0; g < NG; ++g) says[st].bad[2 * g + w - 4] = bad[g];
-          if (u == 0) {
-            says[st].k_mul = power(20 - nk);
-            says[st].v_exp = (float)nv;
-          }
-        }
-        uint8_t* kd = kv_op + st * 2 * W::KVB;
-        uint8_t* vd = kd + W::KVB;
-#pragma unroll
-        for (int c = 0; c < NG; ++c) {
-          int r, cc;
-          place(c, r, cc);
-          const int g = cc / 2;
-          const float k = raw[st][g][r] * fk, v = raw[st][NG + g][r] * fv;
-          const uint32_t hk = pack2h(k, k), hv = pack2h(v, v);
-          const uint32_t kw[4] = {kc[c].x, kc[c].y, kc[c].z, kc[c].w}, vw[4] = {vc[c].x, vc[c].y, vc[c].z, vc[c].w};
-#pragma unroll
-          for (int i4 = 0; i4 < 4; ++i4) {
-            const int at = g * SP * 128 + r * 128 + ((((cc & 1) * 4 + i4) ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(kd + at) = unpack(kw[i4], hk);
-            *reinterpret_cast<uint4*>(vd + at) = unpack(vw[i4], hv);
-          }
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) arrive(smem_addr(&kv_full[st]));
-      if (i + 1 < n_steps) fetch(i + 1);
+      if (first) ++n_runs;
+      if (i >= 2) bar_wait(smem_addr(&s_full[st]), ((i - 2) >> 1) & 1, &give_up, p.a.status);
+      const int nk = min(max(14 - exponent(largest(ks[0], ks[1])), -100), 100);  // K's scales times 2^nk: below 2^15
+      const float tv = largest(vs[0], vs[1]);
+      if (first) cap = 0.f;
+      if (tv > cap || cap == 0.f) cap = power(min(max(exponent(tv) + 4, -80), 100));  // the next power of two, and 2^3 of room
+      const int nv = 15 - exponent(cap);
       if (w == 4) {
-        // all warps have unpacked step i, and so have passed their wait for step
-        // i - 2, before step i's weights can be there
-        bool ok = bar_wait(smem_addr(&kv_full[st]), (i >> 1) & 1, &give_up, p.a.status);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const uint32_t bad = __ballot_sync(0xffffffffu, !finite(g ? high_f(vs[h]) : low_f(vs[h])));
+            if (lane == 0) says[i & 3].bad[2 * g + h] = bad;
+          }
+        if (lane == 0) {
+          says[i & 3].k_mul = power(20 - nk);
+          says[i & 3].v_exp = (float)nv;
+        }
+      }
+      uint8_t* kd = kv_op + st * 2 * W::KVB;
+      lay(kd, kc, ks[0], ks[1], power(nk), false);
+      const uint32_t v0 = vs[0], v1 = vs[1];
+      if (lane == 0) arrive(smem_addr(&k_full[i & 3]));
+      if (i + 1 < n_steps) fetch_k(i + 1);
+      if (i >= 2) bar_wait(smem_addr(&pv_done[st]), ((i - 2) >> 1) & 1, &give_up, p.a.status);
+      if (w - 4 == (i & 3)) {
+        bool ok = bar_wait(smem_addr(&k_full[i & 3]), (i >> 2) & 1, &give_up, p.a.status);
         if (first) {  // the columns lay q after they have read the last run's sums
-          ok = bar_wait(smem_addr(&q_full), n_runs & 1, &give_up, p.a.status) && ok;
-          ++n_runs;
+          ok = bar_wait(smem_addr(&q_full), (n_runs - 1) & 1, &give_up, p.a.status) && ok;
         }
         after_sync();
         if (lane == 0 && ok && !give_up) {
-          const uint64_t q = operand(smem_addr(q_op)), k = operand(smem_addr(kv_op + st * 2 * W::KVB));
-          const uint32_t to = tm + SP * st;
+          const uint64_t q = operand(smem_addr(q_op)), k = operand(smem_addr(kd));
+          const uint32_t to = tm + SP * st;  // the weights of step i - 2 were there
 #pragma unroll
           for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -331,9 +340,16 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
         }
         __syncwarp();
       }
-      if (w == 5 && i) second(i - 1);
+      lay(kd + W::KVB, vc, v0, v1, power(nv), true);
+      if (lane == 0) arrive(smem_addr(&v_full[st]));
+      if (i + 1 < n_steps) fetch_v(i + 1);
+      // (the sums take one step's products after another's: step i - 2's are done)
+      if (w - 4 == ((i + 2) & 3) && i) second(i - 1);
     }
-    if (w == 5 && n_steps) second(n_steps - 1);
+    if (w == 4 && n_steps) {
+      if (n_steps >= 2) bar_wait(smem_addr(&pv_done[n_steps & 1]), ((n_steps - 2) >> 1) & 1, &give_up, p.a.status);
+      second(n_steps - 1);
+    }
   } else {  // ---- a query column each
     const uint32_t mine_tm = (uint32_t)(32 * w) << 16;  // this warp's lanes
     uint32_t k = 0;
@@ -349,20 +365,21 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       {
         const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q.p) + seq * p.q.seq + row * p.q.row + hd * p.q.head;
         float top = 0.f;
-#pragma unroll 4
+        uint4 qr[HD / 8];
+#pragma unroll
+        for (int x = 0; x < HD / 8; ++x) qr[x] = there ? *reinterpret_cast<const uint4*>(src + 8 * x) : make_uint4(0, 0, 0, 0);
+#pragma unroll
         for (int x = 0; x < HD / 8; ++x) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (there) v = *reinterpret_cast<const uint4*>(src + 8 * x);
+          const uint4 v = qr[x];
           top = fmaxf(top, fmaxf(fmaxf(fmaxf(fabsf(low_f(v.x)), fabsf(high_f(v.x))), fmaxf(fabsf(low_f(v.y)), fabsf(high_f(v.y)))),
                                  fmaxf(fmaxf(fabsf(low_f(v.z)), fabsf(high_f(v.z))), fmaxf(fabsf(low_f(v.w)), fabsf(high_f(v.w))))));
         }
         const int nq = min(max(14 - exponent(top), -100), 100);
         const float f = p.c < 0.f ? -power(nq) : power(nq);
         c_row = fabsf(p.c) * power(-65) * power(-nq);
-#pragma unroll 4
+#pragma unroll
         for (int x = 0; x < HD / 8; ++x) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (there) v = *reinterpret_cast<const uint4*>(src + 8 * x);
+          const uint4 v = qr[x];
           const uint4 y = make_uint4(pack2h(low_f(v.x) * f, low_f(v.y) * f), pack2h(high_f(v.x) * f, high_f(v.y) * f),
                                      pack2h(low_f(v.z) * f, low_f(v.w) * f), pack2h(high_f(v.z) * f, high_f(v.w) * f));
           const int g = x / 8, unit = x % 8;
@@ -380,12 +397,12 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       for (int g = 0; g < NG; ++g) bad[g] = false;
       for (int t = run.t0; t < run.t1; ++t, ++k) {
         const int st = k & 1;
-        bool ok = bar_wait(smem_addr(&kv_full[st]), (k >> 1) & 1, &give_up, p.a.status);
+        bool ok = bar_wait(smem_addr(&k_full[k & 3]), (k >> 2) & 1, &give_up, p.a.status);
         ok = bar_wait(smem_addr(&s_full[st]), (k >> 1) & 1, &give_up, p.a.status) && ok;
         after_sync();
         if (ok && !give_up) {
           const int vis = min(lim - t * SP, note[k % kList] & (kFirst - 1));  // of the step's positions
-          const float cf = c_row * says[st].k_mul, ne = says[st].v_exp;
+          const float cf = c_row * says[k & 3].k_mul, ne = says[k & 3].v_exp;
           const uint32_t at = tm + mine_tm + SP * st;
           auto step = [&](auto cut_) {
             constexpr bool CUT = decltype(cut_)::value;
@@ -447,7 +464,7 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
           else step(std::true_type());
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            const uint32_t b0 = says[st].bad[2 * g], b1 = says[st].bad[2 * g + 1];
+            const uint32_t b0 = says[k & 3].bad[2 * g], b1 = says[k & 3].bad[2 * g + 1];
             if (b0 | b1) {
               const uint32_t v0 = vis >= 32 ? ~0u : vis > 0 ? (1u << vis) - 1 : 0u;
               const uint32_t v1 = vis >= 64 ? ~0u : vis > 32 ? (1u << (vis - 32)) - 1 : 0u;
