@@ -478,7 +478,7 @@ typedef struct mk_kv4_rows {
 MK_API size_t mk_kv4_page_bytes(int32_t n_kv_heads, int32_t head_dim);
 
 /* Store the new rows' K and V (dtype MK_BF16 or MK_F32, heads: n_kv_heads) in
- * their places; padding rows are not read or stored.  Two sequences of a call
+ * their places; padding rows are not stored.  Two sequences of a call
  * must not name the same place (a page shared by two sequences is read by
  * both, written by neither).  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 MK_API int mk_kv4_store(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype,
@@ -496,10 +496,14 @@ MK_API int mk_kv4_load(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4
  * rows in q's dtype, lse (may be NULL) float32 [n_seqs][rows][n_heads] the
  * natural logarithm of the sum of exp(scale * q . k).  A row that sees nothing
  * (padding, a length of 0) gets zeros and -infinity.  Positions past the
- * length are never used, whatever their slots hold.  |scale| < 1e18; magnitudes of
- * q and V up to 2^50 are kept whole, terms weight * value below 2^-60 may be lost.
+ * length are never used, whatever their slots hold.  out must not overlap q, the
+ * pool or the workspace.  |scale| < 1e18; magnitudes of q and V up to 2^50 are kept whole,
+ * terms weight * value below 2^-60 may be lost.  Weights are rounded by 2^-12 for bf16
+ * rows and 2^-22 for fp32 rows, sums are fp32.  From 33 query columns (rows x
+ * n_heads / n_kv_heads) of bf16 on, a K value may lose 2^-21 of the largest one of its
+ * page and head, a V value 2^-18 of the largest one of its sequence and head.
  * workspace: device memory of at least mk_kv4_attention_bytes, 16-byte
- * aligned; its contents before the call do not matter, and calls that may
+ * aligned (NULL where that is 0); its contents before the call do not matter, and calls that may
  * overlap on the GPU need workspaces of their own.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, const mk_kv4_rows* q, int32_t dtype,

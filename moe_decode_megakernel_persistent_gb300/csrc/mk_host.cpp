@@ -478,6 +478,17 @@ int host_check_model(const mk_model_desc* d, const mk_weights* w, int* shape, La
 
 }  // namespace mk
 
+// What a call that makes lists on the host answers when there is no memory for
+// them; it makes them before it changes anything.
+template <class F>
+static int without_throw(const F& f) {
+  try {
+    return f();
+  } catch (...) {
+    return host_fail(MK_ERR_INVALID_ARG, "no host memory for the call");
+  }
+}
+
 extern "C" {
 
 MK_API const char* mk_last_error(void) { return g_err.c_str(); }
@@ -1018,18 +1029,18 @@ static int seq_fork(mk_ctx* c, int32_t src_seq, int32_t dst_seq, int32_t n_token
   if (int r = enter_pages(c, dst_seq, 0, pages.data(), (int)pages.size(), (cudaStream_t)stream)) return r;
   if ((int)pages.size() > np) c->free_pages.pop_back();
   for (int32_t pg : pages) ++c->page_ref[pg];
-  b.pages = pages;
+  b.pages = std::move(pages);
   b.open = true;
   b.len = n_tokens;
   return MK_OK;
 }
 
 MK_API int mk_seq_fork(mk_ctx* c, int32_t src_seq, int32_t dst_seq, int32_t n_tokens, void* stream) {
-  return seq_fork(c, src_seq, dst_seq, n_tokens, true, stream);
+  return without_throw([&] { return seq_fork(c, src_seq, dst_seq, n_tokens, true, stream); });
 }
 
 MK_API int mk_seq_fork_at(mk_ctx* c, int32_t src_seq, int32_t dst_seq, int32_t n_tokens, void* stream) {
-  return seq_fork(c, src_seq, dst_seq, n_tokens, false, stream);
+  return without_throw([&] { return seq_fork(c, src_seq, dst_seq, n_tokens, false, stream); });
 }
 
 MK_API int mk_seq_truncate(mk_ctx* c, int32_t seq_id, int32_t n_tokens, void* stream) {
@@ -1063,7 +1074,7 @@ MK_API int mk_seq_truncate(mk_ctx* c, int32_t seq_id, int32_t n_tokens, void* st
   return MK_OK;
 }
 
-MK_API int mk_kv_compact(mk_ctx* c, int32_t* moved_out, void* stream) {
+static int kv_compact(mk_ctx* c, int32_t* moved_out, void* stream) {
   g_err.clear();
   if (moved_out) *moved_out = 0;
   if (!c) return fail(MK_ERR_INVALID_ARG, "ctx is NULL");
@@ -1103,10 +1114,14 @@ MK_API int mk_kv_compact(mk_ctx* c, int32_t* moved_out, void* stream) {
     c->page_ref[dst[i]] = c->page_ref[src[i]];
     c->page_ref[src[i]] = 0;
   }
-  c->free_pages.clear();
+  c->free_pages.clear();  // (its room stays: it has held all pages)
   for (int32_t p = c->n_pages - 1; p >= live; --p) c->free_pages.push_back(p);
   if (moved_out) *moved_out = (int32_t)src.size();
   return MK_OK;
+}
+
+MK_API int mk_kv_compact(mk_ctx* c, int32_t* moved_out, void* stream) {
+  return without_throw([&] { return kv_compact(c, moved_out, stream); });
 }
 
 MK_API int32_t mk_seq_length(mk_ctx* c, int32_t seq_id) {

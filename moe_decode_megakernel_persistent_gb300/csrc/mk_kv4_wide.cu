@@ -6,13 +6,14 @@
 //   S = Q K^T   128 columns x 64 positions.  K = code x scale in fp16: 3 bits x 8
 //               bits are exact in its 11, the code as the subnormal +-m 2^-20, the
 //               scale times a power of two of the tile (its largest scale maps to
-//               2^14..2^15; rows 2^-9 of it and below lose low bits, an error of 2^-23 of
-//               the tile's largest values).  Q is fp16 times a power of two of the
-//               row (a bf16 value is exact down to 2^-29 of its row's largest).  The
-//               powers multiply the fp32 scores.
+//               2^14..2^15; one below 2^-11 of that loses low bits, at most 2^-21 of the
+//               tile's largest value).  Q is fp16 times a power of two of the row (a
+//               bf16 value is exact down to 2^-31 of its row's largest).  The powers
+//               multiply the fp32 scores.
 //   O += P V    P = weights in fp16 (rounded by 2^-12, where the output is rounded
 //               to 2^-9) over S's place in TMEM; V as K, its power following the largest
-//               scale of the run, O rescaled when it moves.
+//               scale of the run with 2^3 of room (so that a value loses at most 2^-18
+//               of the largest), O rescaled when it moves.
 // So the 128 x 64 scores of a step need no scale of their own, and one pass: 64
 // scores a thread in registers, their maximum, one exponential each.  (With the
 // scales applied to scores and weights, as the narrow kernel does, a step took
@@ -30,7 +31,7 @@
 // Two blocks of an SM (256 TMEM columns each) fill each other's waits.
 //
 // Measured: 1024 rows of 16 heads on 4 kv heads of 128 dimensions, 8022 positions,
-// 115 us, 295 TFLOP/s of 4 x dimensions x seen pairs; tensor cores 25% active.
+// 115 us, 548 TFLOP/s of 4 x dimensions x seen pairs; tensor cores 25% active.
 // A step takes about 2,900 cycles of a block, in which a column warp works 2,200 and waits
 // for the scores otherwise; 700 cycles of an unpacking warp's share are the codes.
 #include <algorithm>

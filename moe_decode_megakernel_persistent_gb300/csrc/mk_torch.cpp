@@ -107,6 +107,20 @@ const at::Tensor& heads(PyObject* o, const char* what) {
   return t;
 }
 
+// Whether the spans of two tensors' elements meet.
+bool overlap(const at::Tensor& x, const at::Tensor& y) {
+  const at::Tensor* t[2] = {&x, &y};
+  uintptr_t lo[2], hi[2];
+  for (int i = 0; i < 2; ++i) {
+    if (!t[i]->numel()) return false;
+    int64_t last = 0;
+    for (int64_t d = 0; d < t[i]->dim(); ++d) last += (t[i]->size(d) - 1) * t[i]->stride(d);
+    lo[i] = reinterpret_cast<uintptr_t>(t[i]->data_ptr());
+    hi[i] = lo[i] + (size_t)(last + 1) * t[i]->element_size();
+  }
+  return lo[0] < hi[1] && lo[1] < hi[0];
+}
+
 // The call's device made current, and its current stream there.
 struct On {
   c10::cuda::OptionalCUDAGuard guard;
@@ -182,6 +196,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   On on(pool.device());
   at::Tensor out = a[6] == Py_None ? at::empty(sizes, pool.options().dtype(type)) : tensor(a[6], "out");
   if (!out.is_contiguous()) refuse("out must be contiguous");
+  if (a[6] != Py_None && overlap(q, out)) refuse("out must not overlap q");
   const mk_kv4_rows outr = rows_of(out, sizes, type, pool.device(), "out");
   const bool want_lse = a[7] == Py_True;
   at::Tensor lse;

@@ -55,7 +55,8 @@ def load(pool, table, lengths, rows: int, n_new=None, dtype=torch.bfloat16, stat
 def attention(q, pool, table, lengths, n_new=None, scale=None, out=None, return_lse=False, status=None):
     """Causal attention of the new rows q [n_seqs, rows, n_heads, head_dim] over
     the cache, which holds their own K and V already.  scale defaults to
-    1 / sqrt(head_dim).  Returns out in q's dtype (`out` if given), with
+    1 / sqrt(head_dim).  Returns out in q's dtype (`out` if given: contiguous, and
+    of memory that neither q nor the pool has), with
     return_lse also the log-sum-exp of the scores, float32 [n_seqs, rows,
     n_heads].  Rows that see nothing are zeros, with a log-sum-exp of -inf."""
     return L.torch_module().attention(q, pool, table, lengths, n_new, scale, out, bool(return_lse), status)
