@@ -8,7 +8,7 @@
 #include <string>
 #include <vector>
 
-#include "mk_internal.h"
+#include "mk_kv4_host.h"
 
 using namespace mk;
 
@@ -726,10 +726,9 @@ static int prefill_gemm_chunk(mk_ctx* c, int32_t seq_id, const int32_t* tokens_d
   a.final_norm = c->final_norm;
   a.lm_pk = c->lm_pk;
   a.rope = c->rope_dev;
+  PrefillKv4 kv4;
   if (c->kv_format == MK_INT4_G64) {
-    a.kv4 = reinterpret_cast<uint8_t*>(c->kv_dev);
-    a.kv4_len = c->kv_seqs;
-    a.kv4_slot = c->kv_seqs + kMaxBatch;
+    kv4 = {reinterpret_cast<uint8_t*>(c->kv_dev), c->kv_seqs, c->kv_seqs + kMaxBatch};
     StepSeqs q{};
     q.n = 1;
     q.len[0] = start_pos + n;
@@ -755,7 +754,7 @@ static int prefill_gemm_chunk(mk_ctx* c, int32_t seq_id, const int32_t* tokens_d
     a.trace_rows = rows_traced;
   }
   a.err = c->sc.err;
-  if (int r = prefill_run(&c->prefill, a, st)) {
+  if (int r = kv4.pool ? prefill_run(&c->prefill, a, kv4, st) : prefill_run(&c->prefill, a, st)) {
     rollback();
     return r;
   }

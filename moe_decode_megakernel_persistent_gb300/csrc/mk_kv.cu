@@ -5,7 +5,7 @@
 // 16-byte words between the caller buffer and the pages.
 #include <algorithm>
 
-#include "mk_internal.h"
+#include "mk_kv4_host.h"
 
 namespace mk {
 

@@ -3,7 +3,7 @@
 #pragma once
 #include <cuda_bf16.h>
 
-#include "mk_internal.h"
+#include "mk_kv4_host.h"
 
 namespace mk {
 

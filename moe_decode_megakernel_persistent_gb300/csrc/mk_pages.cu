@@ -5,7 +5,7 @@
 #include <string>
 #include <vector>
 
-#include "mk_internal.h"
+#include "mk_kv4_host.h"
 
 namespace mk {
 namespace {

@@ -33,7 +33,7 @@
 #include <string>
 #include <vector>
 
-#include "mk_internal.h"
+#include "mk_kv4_host.h"
 
 namespace mk {
 
@@ -632,7 +632,9 @@ void prefill_free(PrefillWork* w) {
   delete w;
 }
 
-int prefill_run(PrefillWork** pw, const PrefillArgs& a, cudaStream_t st) {
+int prefill_run(PrefillWork** pw, const PrefillArgs& a, cudaStream_t st) { return prefill_run(pw, a, PrefillKv4(), st); }
+
+int prefill_run(PrefillWork** pw, const PrefillArgs& a, const PrefillKv4& kv4, cudaStream_t st) {
   const mk_model_desc& m = a.d;
   Dims d;
   d.H = m.hidden; d.NH = m.n_heads; d.NKV = m.n_kv_heads; d.HD = m.head_dim; d.QD = m.n_heads * m.head_dim;
@@ -681,7 +683,7 @@ int prefill_run(PrefillWork** pw, const PrefillArgs& a, cudaStream_t st) {
     alloc((void**)&w->pos_of, 4 * ent);
     alloc((void**)&w->lm_v, 4 * kLmBlocks);
     alloc((void**)&w->lm_i, 4 * kLmBlocks);
-    if (a.kv4) {
+    if (kv4.pool) {
       // the attention's workspace for any chunk: the largest one's
       Kv4Args k{};
       k.n_kv_heads = d.NKV;
@@ -730,11 +732,11 @@ int prefill_run(PrefillWork** pw, const PrefillArgs& a, cudaStream_t st) {
                                                                    a.max_pages_per_seq, a.n_pages, l, a.err, w.kv);
     dim3 ag((M + 15) / 16, d.NKV);
     const float scale = 1.f / sqrtf((float)d.HD);
-    if (a.kv4) {
+    if (kv4.pool) {
       // the chunk's rows are stored, then attend to the cache that holds them
       const int QD = d.QD, KD = d.KD;
-      Kv4Args k{a.kv4 + (size_t)l * a.n_pages * mk_kv4_page_bytes(d.NKV, d.HD), a.block_table, a.kv4_len, nullptr, a.err,
-                a.n_pages, d.NKV, 1, (a.start + M + kPageTokens - 1) / kPageTokens, M, a.kv4_slot, a.max_pages_per_seq};
+      Kv4Args k{kv4.pool + (size_t)l * a.n_pages * mk_kv4_page_bytes(d.NKV, d.HD), a.block_table, kv4.len, nullptr, a.err,
+                a.n_pages, d.NKV, 1, (a.start + M + kPageTokens - 1) / kPageTokens, M, kv4.slot, a.max_pages_per_seq};
       if (int r = kv4_store(k, d.HD, {w.kv, 0, 2 * KD, d.HD, 0}, {w.kv + KD, 0, 2 * KD, d.HD, 0}, MK_BF16, st)) return r;
       if (int r = kv4_attention(k, d.HD, d.NH, {w.Q, 0, QD, d.HD, 0}, MK_F32, scale, {w.O, 0, QD, d.HD, 0}, nullptr,
                                 w.kv4_ws, w.kv4_ws_bytes, st))
