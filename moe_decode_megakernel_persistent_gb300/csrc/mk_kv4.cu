@@ -95,9 +95,11 @@ __device__ __forceinline__ float value_of(uint32_t code, float s) {
   return code & 8u ? -m : m;
 }
 
-// One pass over the rows each way, N tokens in flight per thread: bound by the
-// bytes for long calls, for short ones by two dependent reads (length, page),
-// which the rows' own reads do not wait for.
+// One pass over the rows each way, N tokens in flight per thread.  Short calls are
+// bound by two dependent reads (length, page), which the rows' own reads do not wait
+// for (one row each of 16 sequences, 4 heads of 128: 1.8 us); long ones by issue, the
+// quotient and the packing of eight values a thread (4096 rows: 6.3 us for 10.6 MB, issue
+// slots 59% busy).
 // The division |x| / s is the IEEE quotient: r = RN(1 / s), q = RN(x r), then
 // q + r (x - q s) in two fused steps (Markstein), which rounds correctly where
 // nothing under- or overflows; scales outside [2^-60, 2^60] take the division itself.
@@ -164,6 +166,7 @@ __global__ void __launch_bounds__(kThreadsKv) k_kv4_store(const __grid_constant_
   }
 }
 
+// The reverse, bound by issue alike: 4096 rows 5.1 us.
 template <int HD, class T, int N>
 __global__ void __launch_bounds__(kThreadsKv) k_kv4_load(const __grid_constant__ Kv4Args a, Kv4Rows k, Kv4Rows v, int tp, int chunks) {
   const int parts = 16 * Tile<HD>::NG * a.n_kv_heads;

@@ -30,16 +30,25 @@
 // come out transposed for the second product (V^T x weights^T) and turn with
 // movmatrix.
 //
-// Work.  The tiles of 64 positions of all (sequence, column tile, kv head)
-// items are laid end to end and cut into equal runs, one for each block, from
-// the lengths on the device: a ragged batch costs what its sum costs, and a
-// captured graph follows the lengths.  A block's tiles stream (one bulk copy of
-// 8.5 KB each) through a shared-memory ring, refilled by its warps in turn; each
-// warp takes 16 positions of a tile, with running maxima of its own (moved only
-// when a score passes them by 2^8) and one merge at the end of an item.  An item cut
-// between blocks is joined by a second kernel, launched so that its start
-// overlaps the first one's end.  Short work instead makes each item a cluster of
-// blocks that join through their shared memory, in one kernel.
+// Work.  The tiles of all (sequence, column tile, kv head) items are laid end
+// to end and cut into equal runs, one for each block, from the lengths on the
+// device: a ragged batch costs what its sum costs, and a captured graph follows
+// the lengths.  A block's steps of 64 or 128 positions stream (one bulk copy of 8.7 or
+// 17.4 KB each at 128 dimensions) through a shared-memory ring, refilled by its warps
+// in turn; each warp takes 16 or 32 positions of a step, with running maxima of its own
+// (moved only when a score passes them by 2^8) and one merge at the end of an item.
+// An item cut between blocks is joined by a second kernel, launched so that its
+// start overlaps the first one's end.  Short work instead makes each item a cluster
+// of blocks that join through their shared memory, in one kernel.  Calls of many
+// bf16 columns run in mk_kv4_wide.cu.
+//
+// Measured (16 heads on 4 kv heads of 128, bf16 rows).  Short work is bound by its
+// chain of set-up, first copies and join: one sequence of 2049 positions 6.9 us, with 6% of
+// the issue slots busy; 16 of 256 to 8448 16.8 us (38 MB).  Long work is bound by issue
+// and the unpacking: 64 of 4096 to 16384 78.7 us, 4.6 TB/s, the ALU 55% and the issue slots 56%
+// busy, with 14 warps of 114 registers on an SM; one of 131071 27.5 us, 2.6 TB/s.  24 columns
+// hold their sums in 243 registers, which leaves 8 warps an SM (issue slots 30% busy): 16 sequences of
+// up to 8022 positions with up to 5 rows each 31 us.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
