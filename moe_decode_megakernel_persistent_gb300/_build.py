@@ -63,7 +63,7 @@ def _module_commands(obj: str, out: str) -> list:
     abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
     return [[cxx, "-O2", "-std=c++17", "-fPIC", abi, *inc, "-c", os.path.join(CSRC, "mk_torch.cpp"), "-o", obj],
             [cxx, "-shared", obj, "-o", out, "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + libs,
-             "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]]
+             "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda"]]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

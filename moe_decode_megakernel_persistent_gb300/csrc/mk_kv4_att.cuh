@@ -147,27 +147,39 @@ __device__ __forceinline__ int part_slot(long long block, int t0) { return (int)
 // The first run of this block, found by one warp; lane 0 of block 0 leaves the
 // number of places for the join.  Returned in lane 0.
 __device__ __forceinline__ Runs first_run(const AttArgs& p, int CT, int SP, int lane) {
-  long long total = 0;
-  for (int e = lane; e < p.n_entries; e += 32) {
-    const int nt = tiles_of(p, e, CT, SP);
-    if (nt) total += nt + kOver;
-  }
+  auto places = [&](int e) -> long long {
+    const int nt = e < p.n_entries ? tiles_of(p, e, CT, SP) : 0;
+    return nt ? (long long)(nt + kOver) * p.a.n_kv_heads : 0;
+  };
+  auto scan = [&](long long n) {  // inclusive, over the lanes
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  total *= p.a.n_kv_heads;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += up;
+    }
+    return n;
+  };
+  // up to 32 entries are read and scanned once, more are summed first
+  const bool few = p.n_entries <= 32;
+  long long n = places(lane), total = 0, incl = 0;
+  if (few) {
+    incl = scan(n);
+    total = __shfl_sync(0xffffffffu, incl, 31);
+  } else {
+    total = n;
+    for (int e = lane + 32; e < p.n_entries; e += 32) total += places(e);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
   const long long lo = first_place(total, blockIdx.x, gridDim.x), hi = first_place(total, blockIdx.x + 1, gridDim.x);
   if (blockIdx.x == 0 && lane == 0) *p.total = total;
   long long base = 0;
   int entry = 0;
   if (lo < hi) {
     for (int e0 = 0; e0 < p.n_entries; e0 += 32) {
-      const int nt = e0 + lane < p.n_entries ? tiles_of(p, e0 + lane, CT, SP) : 0;
-      const long long n = nt ? (long long)(nt + kOver) * p.a.n_kv_heads : 0;
-      long long incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
+      if (!few) {
+        n = places(e0 + lane);
+        incl = scan(n);
       }
       const uint32_t has = __ballot_sync(0xffffffffu, lo < base + incl);
       if (has) {

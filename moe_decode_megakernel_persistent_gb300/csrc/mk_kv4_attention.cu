@@ -110,6 +110,7 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
+constexpr int kWindow = 128;  // steps whose addresses a block looks up at a time
 // NT column tiles; W warps of U units of 16 positions in each step; R steps in
 // the ring; B blocks of an SM.
 template <int HD, class T, int NT, int W, int U, int R, int B>
@@ -135,15 +136,17 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
   constexpr int NG = S::NG, CT = S::CT, SP = S::SP, NTHR = 32 * W;
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ __align__(8) uint64_t full[R], empty[R];
-  __shared__ unsigned long long list[kList];  // where the block's next steps lie (0: a page outside the pool)
+  __shared__ unsigned long long list[kWindow];  // where the block's next steps lie (0: a page outside the pool)
   __shared__ uint32_t issued[R];              // 1 + the last step copied into each stage
   __shared__ float2 sm_ml[W][CT];  // a run's maximum and sum of each warp and column
   __shared__ Runs s_run;  // the block's first run
   __shared__ volatile int give_up;
-  __shared__ int pages[NTHR];  // cluster: the first pages of the item's sequence
   // cluster: the partial results of the columns that this block joins, column c
   // (joined by block c mod cluster) of block r in [r][c / cluster][HD | M, sum]
   float* fin = reinterpret_cast<float*>(sm + S::SMEM);
+  // cluster: the first pages of the item's sequence, where the sums are joined at the end
+  int* pages = reinterpret_cast<int*>(sm + R * S::BYTES);
+  static_assert(S::RED >= NTHR * (int)sizeof(int), "room for the pages");
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // a block's shared memory is there to be written once the block runs
@@ -262,13 +265,13 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
       r.t0 += i - before;
       pg = page_of(p.a, p.n_ctiles == 1 ? r.e : r.e / p.n_ctiles, r.t0 * SP);
     }
-    list[i % kList] = pg < 0 ? 0 : (unsigned long long)tile_of<HD>(p.a, pg, r.head, r.t0 * SP);
+    list[i % kWindow] = pg < 0 ? 0 : (unsigned long long)tile_of<HD>(p.a, pg, r.head, r.t0 * SP);
   };
   // Copy step i into its stage, which is free; one thread.
   auto copy_step = [&](uint32_t i) {
     const int st = i % R;
     const uint32_t bar = smem_addr(&full[st]);
-    const unsigned long long src = list[i % kList];
+    const unsigned long long src = list[i % kWindow];
     issued[st] = src ? i + 1 : 0;
     if (src) {
       asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "n"(S::BYTES) : "memory");
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     }
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
   };
-  for (uint32_t i = tid; i < kList && i < n_steps; i += NTHR) {
+  for (uint32_t i = tid; i < kWindow && i < n_steps; i += NTHR) {
     look_up(i);
     if (i < R) copy_step(i);
   }
@@ -539,10 +542,10 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
 
 #pragma unroll 1
     for (int t = run.t0; t < run.t1; ++t, ++k) {
-      if (k % (kList / 2) == 0 && k) {  // half of the addresses are used up: the next ones
+      if (k % (kWindow / 2) == 0 && k) {  // half of the addresses are used up: the next ones
         asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
-        for (uint32_t i = tid; i < kList / 2; i += NTHR)
-          if (k + kList / 2 + i < n_steps) look_up(k + kList / 2 + i);
+        for (uint32_t i = tid; i < kWindow / 2; i += NTHR)
+          if (k + kWindow / 2 + i < n_steps) look_up(k + kWindow / 2 + i);
         asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
       }
       // the stage of the last step is refilled as soon as all warps have left it
@@ -678,7 +681,8 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
 // (1024 rows at 8022 positions, 16384 columns of about 3 parts: a block for every column
 // with the places found by every warp took 33 us.)
 constexpr int kFewParts = 4;
-template <int HD, class T>
+// NB: parts in flight in each warp.
+template <int HD, class T, int NB>
 __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArgs p, int CT, int SP, int G, int CC) {
   constexpr int V = HD / 32;  // dimensions of a lane
   __shared__ float red[16][HD], red_m[16], red_l[16];
@@ -707,24 +711,44 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
   }
   const int n = n_parts;
   float m, l, o[V];
+  // parts first, first + by .. of column c, NB at a time
   auto gather = [&](int c, int first, int by) {
+    constexpr int N = NB;
     m = kLow, l = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = 0.f;
-#pragma unroll 4
-    for (int i = first; i < n; i += by) {
-      const int at = slot[i];
-      if (at < 0) continue;
-      const float* src = p.part + ((size_t)at * CT + c) * (HD + 4);
-      const float2 ml = *reinterpret_cast<const float2*>(src + HD);
-      float v[V];
+#pragma unroll 1
+    for (int i0 = first; i0 < n; i0 += N * by) {
+      float2 ml[N];
+      float v[N][V];
 #pragma unroll
-      for (int x = 0; x < V; ++x) v[x] = src[lane * V + x];
-      const float M = fmaxf(m, ml.x), f0 = exp2_fast(m - M), f1 = exp2_fast(ml.x - M);
+      for (int y = 0; y < N; ++y) {
+        const int i = i0 + y * by, at = i < n ? slot[i] : -1;
+        ml[y] = make_float2(kLow, 0.f);
+#pragma unroll
+        for (int x = 0; x < V; ++x) v[y][x] = 0.f;
+        if (at >= 0) {
+          const float* src = p.part + ((size_t)at * CT + c) * (HD + 4);
+          ml[y] = *reinterpret_cast<const float2*>(src + HD);
+#pragma unroll
+          for (int x = 0; x < V; ++x) v[y][x] = src[lane * V + x];
+        }
+      }
+      float M = m;
+#pragma unroll
+      for (int y = 0; y < N; ++y) M = fmaxf(M, ml[y].x);
+      const float f0 = exp2_fast(m - M);
       m = M;
-      l = l * f0 + ml.y * f1;
+      l *= f0;
 #pragma unroll
-      for (int x = 0; x < V; ++x) o[x] = o[x] * f0 + v[x] * f1;
+      for (int x = 0; x < V; ++x) o[x] *= f0;
+#pragma unroll
+      for (int y = 0; y < N; ++y) {
+        const float f1 = exp2_fast(ml[y].x - M);
+        l += ml[y].y * f1;
+#pragma unroll
+        for (int x = 0; x < V; ++x) o[x] += v[y][x] * f1;
+      }
     }
   };
   auto place = [&](int c, int& row, int& hd) {
@@ -785,10 +809,10 @@ constexpr int kShort = 10;  // steps of a block, at most, for work that counts a
 
 struct Plan {
   bool wide = false;
-  const void *main, *join;
+  const void *main, *join[2];  // the join with 4 or 12 parts in flight in a warp
   int id;                    // of the variant
   int CT, SP, smem, base_smem, blocks, threads;  // columns of a tile, positions of a step; blocks of an SM
-  int n_ctiles, n_entries, items, grid, join_cols, join_threads;
+  int n_ctiles, n_entries, items, grid, join_cols, join_threads, join_many;
   int cluster;               // blocks of an item's cluster; 0: the tiles of all items in equal runs
   size_t item_off, part_off, bytes;
 };
@@ -797,7 +821,8 @@ template <int HD, class T, int NT, int W, int U, int R, int B>
 void take(Plan* pl) {
   using S = Shape<HD, T, NT, W, U, R, B>;
   pl->main = reinterpret_cast<const void*>(&k_kv4_attention<HD, T, NT, W, U, R, B>);
-  pl->join = reinterpret_cast<const void*>(&k_kv4_join<HD, T>);
+  pl->join[0] = reinterpret_cast<const void*>(&k_kv4_join<HD, T, 4>);
+  pl->join[1] = reinterpret_cast<const void*>(&k_kv4_join<HD, T, 12>);
   pl->id = (HD == 64 ? 0 : 16) + (S::F32 ? 8 : 0) + NT;
   pl->CT = S::CT;
   pl->SP = S::SP;
@@ -814,7 +839,8 @@ void take_for(Plan* pl, int cols, int dtype) {
   if (dtype == MK_BF16 && cols >= kWideCols) {
     const WideKernel w = kv4_wide_kernel(HD);
     pl->main = w.fn;
-    pl->join = reinterpret_cast<const void*>(&k_kv4_join<HD, __nv_bfloat16>);
+    pl->join[0] = reinterpret_cast<const void*>(&k_kv4_join<HD, __nv_bfloat16, 4>);
+    pl->join[1] = reinterpret_cast<const void*>(&k_kv4_join<HD, __nv_bfloat16, 12>);
     pl->id = (HD == 64 ? 0 : 16) + 7;
     pl->CT = w.CT;
     pl->SP = w.SP;
@@ -840,6 +866,55 @@ int sm_count() {
   return n;
 }
 
+// The kernels take more shared memory than the default: asked for once per device.
+cudaError_t allow_smem(const Plan& pl) {
+  static std::atomic<uint32_t> done[64];  // variants, by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done[dev].load() >> pl.id & 1u)) return cudaSuccess;
+  // a cluster's blocks take 16 x (columns / 16, rounded up) partial columns more, at most
+  e = cudaFuncSetAttribute(pl.main, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           pl.base_smem + (pl.wide ? 0 : (pl.CT + 16) * 130 * 4));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(pl.main, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && dev < 64) done[dev].fetch_or(1u << pl.id);
+  return e;
+}
+
+// Bytes that a block of a cluster of n takes more, for the partial columns it joins.
+int join_room(const Plan& pl, int head_dim, int n) {
+  return n > 1 ? n * ((pl.CT + n - 1) / n) * (head_dim + 2) * (int)sizeof(float) : 0;
+}
+
+// How many clusters of n blocks run at once, asked for once per variant, size and device.
+int clusters_at_once(const Plan& pl, int head_dim, int n) {
+  static std::atomic<int> known[64][32][5];  // 1 + the number
+  int dev = 0, log = 0, count = 0;
+  while (1 << log < n) ++log;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) count = known[dev][pl.id][log].load();
+  if (count) return count - 1;
+  count = pl.blocks * sm_count() / n;
+  if (allow_smem(pl) == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = n;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(pl.threads);
+    cfg.dynamicSmemBytes = pl.base_smem + join_room(pl, head_dim, n);
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int c = 0;
+    if (cudaOccupancyMaxActiveClusters(&c, pl.main, &cfg) == cudaSuccess) {
+      count = c;
+      if (dev < 64) known[dev][pl.id][log].store(count + 1);
+    }
+  }
+  cudaGetLastError();
+  return count;
+}
+
 // Variant, grid and workspace of a call with rows; false: too many columns.
 bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
   const long long cols = (long long)c.rows * (n_heads / c.n_kv_heads);
@@ -854,47 +929,35 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
   pl->items = (int)items;
   const long long room = std::min(pl->blocks * sm_count(), kMaxBlocks);  // blocks that run at once
   pl->cluster = 0;
-  // Short work: an item is a cluster of up to 16 blocks, as many as run at once,
-  // joined through their shared memory.  It saves the second kernel and the scan
-  // of all lengths (16 sequences of 256 to 8448 positions: 17.2 us against 20.7),
-  // but a ragged batch is not levelled and a long item has 16 blocks at most, which
-  // loses once a block has more than about ten steps (131071 positions: 57.6
-  // us against 28.6).
+  // Short work: an item is a cluster of up to 16 blocks, while all clusters run at
+  // once (16 sequences of 256 to 8448 positions with clusters of 8: 15.7 us; where a few had to wait
+  // for a place, 16.8), joined through their shared memory.  It saves the second kernel and the
+  // scan of all lengths (20.7 us), but a ragged batch is not levelled and a long item has
+  // 16 blocks at most, which loses once a block has more than about ten steps (131071
+  // positions: 57.6 us against 27.5).
   int n = 1;
-  while (n < 16 && 2 * n <= most && 2 * n * items <= room) n *= 2;
+  while (n < 16 && 2 * n <= most && items <= clusters_at_once(*pl, head_dim, 2 * n)) n *= 2;
   if (!pl->wide && (most + n - 1) / n <= kShort) {
     pl->cluster = n;
-    if (n > 1) pl->smem += n * ((pl->CT + n - 1) / n) * (head_dim + 2) * (int)sizeof(float);
+    pl->smem += join_room(*pl, head_dim, n);
     pl->grid = (int)(items * n);
     pl->item_off = pl->part_off = pl->bytes = 0;
     return true;
   }
   pl->grid = (int)std::min<long long>(room, items * most);
-  // The join.  An item has about grid / items parts: as many warps for each column, and
-  // a block for a column while that is few blocks.
+  // The join.  An item has about grid / items parts: as many warps for each column, up to 16
+  // with 12 parts in flight in each where that is not enough (131071 positions, 152 parts: 24.5 us
+  // against 26.5 with 4, whose fewer registers the other cases need), and a block for a column
+  // while that is few blocks.
   pl->join_cols = (long long)items * pl->CT <= 2048 ? 1 : 16;
   int nw = 2;
   while (nw < 16 && nw * 2 * items <= pl->grid) nw *= 2;
+  pl->join_many = pl->grid / 64 >= items;
   pl->join_threads = 32 * (pl->join_cols > 1 ? std::max(nw, 8) : nw);
   pl->item_off = 16;
   pl->part_off = pl->item_off + (size_t)items * sizeof(longlong2);
   pl->bytes = pl->part_off + 2 * (size_t)pl->grid * pl->CT * (head_dim + 4) * sizeof(float);
   return true;
-}
-
-// The kernels take more shared memory than the default: asked for once per device.
-cudaError_t allow_smem(const Plan& pl) {
-  static std::atomic<uint32_t> done[64];  // variants, by device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && (done[dev].load() >> pl.id & 1u)) return cudaSuccess;
-  // a cluster's blocks take 16 x (columns / 16, rounded up) partial columns more, at most
-  e = cudaFuncSetAttribute(pl.main, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           pl.base_smem + (pl.wide ? 0 : (pl.CT + 16) * 130 * 4));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(pl.main, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess && dev < 64) done[dev].fetch_or(1u << pl.id);
-  return e;
 }
 
 }  // namespace
@@ -965,7 +1028,7 @@ int kv4_attention(const Kv4Args& a, int head_dim, int n_heads, const Kv4Rows& q,
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     void* args[] = {&p, &pl.CT, &pl.SP, &pl.grid, &pl.join_cols};
-    e = cudaLaunchKernelExC(&cfg, pl.join, args);
+    e = cudaLaunchKernelExC(&cfg, pl.join[pl.join_many], args);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();

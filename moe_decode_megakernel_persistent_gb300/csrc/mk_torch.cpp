@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -128,6 +128,11 @@ struct On {
   explicit On(c10::Device dev) : guard(dev), stream(c10::cuda::getCurrentCUDAStream(dev.index()).stream()) {}
 };
 
+// A tensor of the current stream's allocator (without the dispatcher's 0.3 us).
+at::Tensor fresh(c10::IntArrayRef sizes, at::ScalarType type, c10::Device dev) {
+  return at::Tensor(at::detail::empty_cuda(sizes, type, dev, std::nullopt));
+}
+
 #define MK_BEGIN     \
   HANDLE_TH_ERRORS { \
     try {
@@ -170,8 +175,7 @@ PyObject* py_load(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::ScalarType type = a[5] == Py_True ? at::kBFloat16 : at::kFloat;
   const int64_t sizes[4] = {c.n_seqs, c.rows, c.n_kv_heads, c.head_dim};
   On on(pool.device());
-  const at::TensorOptions opt = pool.options().dtype(type);
-  at::Tensor k = at::empty(sizes, opt), v = at::empty(sizes, opt);
+  at::Tensor k = fresh(sizes, type, pool.device()), v = fresh(sizes, type, pool.device());
   const mk_kv4_rows kr = rows_of(k, sizes, type, pool.device(), "k"), vr = rows_of(v, sizes, type, pool.device(), "v");
   check(mk_kv4_load(&c, &kr, &vr, dtype_of(type), on.stream));
   return Py_BuildValue("(NN)", THPVariable_Wrap(std::move(k)), THPVariable_Wrap(std::move(v)));
@@ -194,20 +198,20 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (scale == -1.0 && PyErr_Occurred()) return nullptr;
   }
   On on(pool.device());
-  at::Tensor out = a[6] == Py_None ? at::empty(sizes, pool.options().dtype(type)) : tensor(a[6], "out");
+  at::Tensor out = a[6] == Py_None ? fresh(sizes, type, pool.device()) : tensor(a[6], "out");
   if (!out.is_contiguous()) refuse("out must be contiguous");
   if (a[6] != Py_None && overlap(q, out)) refuse("out must not overlap q");
   const mk_kv4_rows outr = rows_of(out, sizes, type, pool.device(), "out");
   const bool want_lse = a[7] == Py_True;
   at::Tensor lse;
-  if (want_lse) lse = at::empty(c10::IntArrayRef(sizes, 3), pool.options().dtype(at::kFloat));
+  if (want_lse) lse = fresh(c10::IntArrayRef(sizes, 3), at::kFloat, pool.device());
   // The workspace is taken anew for each call from the stream's allocator and
   // given back once the call is enqueued (the stream orders its next use), so
   // that calls on two streams, or two captured graphs, never share one.
   const int dt = dtype_of(type);
   const size_t nws = mk_kv4_attention_bytes(&c, n_heads, dt);
   at::Tensor ws;
-  if (nws) ws = at::empty({(int64_t)nws}, pool.options());
+  if (nws) ws = fresh({(int64_t)nws}, at::kByte, pool.device());
   check(mk_kv4_attention(&c, n_heads, &qr, dt, (float)scale, &outr, want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
                          nws ? ws.data_ptr() : nullptr, nws, on.stream));
   if (!want_lse) {
