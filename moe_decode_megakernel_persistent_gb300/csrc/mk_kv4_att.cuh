@@ -114,6 +114,15 @@ constexpr int kMaxBlocks = 1024;
 struct Runs {
   long long pos, hi, base;  // base: the first place of entry e
   int e, nt, head, t0, t1;
+  __device__ __forceinline__ void take() {  // the steps of entry e from place pos on
+    const int len = nt + kOver, at = (int)(pos - base);  // held to 31 bits by the entry point
+    head = at / len;
+    const int in = at - head * len;
+    const int out = (int)min((long long)len, in + (hi - pos));
+    pos += out - in;
+    t0 = max(0, in - kOver);
+    t1 = max(0, out - kOver);
+  }
   __device__ __forceinline__ bool next(const AttArgs& p, int CT, int SP) {  // the next run; false: none is left
     for (;;) {
       if (pos >= hi) return false;
@@ -124,13 +133,7 @@ struct Runs {
         if (pos < base + n) break;
         base += n;
       }
-      const int len = nt + kOver, at = (int)(pos - base);  // held to 31 bits by the entry point
-      head = at / len;
-      const int in = at - head * len;
-      const int out = (int)min((long long)len, in + (hi - pos));
-      pos += out - in;
-      t0 = max(0, in - kOver);
-      t1 = max(0, out - kOver);
+      take();
       if (t1 > t0) return true;
     }
   }
@@ -145,41 +148,55 @@ __device__ __forceinline__ long long first_place(long long total, long long b, i
 __device__ __forceinline__ int part_slot(long long block, int t0) { return (int)(2 * block) + (t0 > 0 ? 0 : 1); }
 
 // The first run of this block, found by one warp; lane 0 of block 0 leaves the
-// number of places for the join.  Returned in lane 0.
+// number of places for the join.  Returned in all lanes.
 __device__ __forceinline__ Runs first_run(const AttArgs& p, int CT, int SP, int lane) {
-  auto places = [&](int e) -> long long {
-    const int nt = e < p.n_entries ? tiles_of(p, e, CT, SP) : 0;
-    return nt ? (long long)(nt + kOver) * p.a.n_kv_heads : 0;
-  };
-  auto scan = [&](long long n) {  // inclusive, over the lanes
+  int nt = lane < p.n_entries ? tiles_of(p, lane, CT, SP) : 0;
+  auto places = [&] { return nt ? (long long)(nt + kOver) * p.a.n_kv_heads : 0ll; };
+  Runs r;
+  r.t0 = r.t1 = 0;
+  if (p.n_entries <= 32 && __all_sync(0xffffffffu, places() < 1 << 26)) {  // one scan, in 32 bits
+    const int n = (int)places();
+    int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, n, o);
-      if (lane >= o) n += up;
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
     }
-    return n;
-  };
-  // up to 32 entries are read and scanned once, more are summed first
-  const bool few = p.n_entries <= 32;
-  long long n = places(lane), total = 0, incl = 0;
-  if (few) {
-    incl = scan(n);
-    total = __shfl_sync(0xffffffffu, incl, 31);
-  } else {
-    total = n;
-    for (int e = lane + 32; e < p.n_entries; e += 32) total += places(e);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
+    const int lo = (int)first_place(total, blockIdx.x, gridDim.x), hi = (int)first_place(total, blockIdx.x + 1, gridDim.x);
+    if (blockIdx.x == 0 && lane == 0) *p.total = total;
+    r.pos = lo;
+    r.hi = hi;
+    if (lo >= hi) return r;
+    const int f = __ffs(__ballot_sync(0xffffffffu, lo < incl)) - 1;
+    const int base = __shfl_sync(0xffffffffu, incl - n, f);
+    r.base = base;
+    r.e = f;
+    r.nt = __shfl_sync(0xffffffffu, nt, f);
+    r.take();
+    if (r.t1 <= r.t0 && !r.next(p, CT, SP)) r.t0 = r.t1 = 0;
+    return r;
   }
+  long long total = places();
+  for (int e = lane + 32; e < p.n_entries; e += 32) {
+    nt = tiles_of(p, e, CT, SP);
+    total += places();
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const long long lo = first_place(total, blockIdx.x, gridDim.x), hi = first_place(total, blockIdx.x + 1, gridDim.x);
   if (blockIdx.x == 0 && lane == 0) *p.total = total;
   long long base = 0;
   int entry = 0;
   if (lo < hi) {
     for (int e0 = 0; e0 < p.n_entries; e0 += 32) {
-      if (!few) {
-        n = places(e0 + lane);
-        incl = scan(n);
+      nt = e0 + lane < p.n_entries ? tiles_of(p, e0 + lane, CT, SP) : 0;
+      const long long n = places();
+      long long incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
       }
       const uint32_t has = __ballot_sync(0xffffffffu, lo < base + incl);
       if (has) {
@@ -191,13 +208,11 @@ __device__ __forceinline__ Runs first_run(const AttArgs& p, int CT, int SP, int 
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  Runs r;
   r.pos = lo;
   r.hi = hi;
   r.base = base;
   r.e = entry;
-  r.t0 = r.t1 = 0;
-  if (lane == 0 && !r.next(p, CT, SP)) r.t0 = r.t1 = 0;
+  if (!r.next(p, CT, SP)) r.t0 = r.t1 = 0;
   return r;
 }
 
