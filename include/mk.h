@@ -500,8 +500,9 @@ MK_API int mk_kv4_load(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4
  * pool or the workspace.  |scale| < 1e18; magnitudes of q and V up to 2^50 are kept whole,
  * terms weight * value below 2^-60 may be lost.  Weights are rounded by 2^-12 for bf16
  * rows and 2^-22 for fp32 rows, sums are fp32.  From 33 query columns (rows x
- * n_heads / n_kv_heads) of bf16 on, a K value may lose 2^-21 of the largest one of its
- * page and head, a V value 2^-18 of the largest one of its sequence and head.
+ * n_heads / n_kv_heads) of bf16 and 81 of fp32 on, an fp32 q is rounded by 2^-22 too, a K
+ * value may lose 2^-21 of the largest one of its 64 positions and head, a V value 2^-18 (bf16
+ * rows) or 2^-21 (fp32 rows) of the largest one of its sequence and head.
  * workspace: device memory of at least mk_kv4_attention_bytes, 16-byte
  * aligned (NULL where that is 0); its contents before the call do not matter, and calls that may
  * overlap on the GPU need workspaces of their own.

@@ -216,11 +216,11 @@ __device__ __forceinline__ Runs first_run(const AttArgs& p, int CT, int SP, int 
   return r;
 }
 
-// The wide kernel (mk_kv4_wide.cu): 128 columns a tile.
+// The wide kernel (mk_kv4_wide.cu).
 struct WideKernel {
   const void* fn;
   int CT, SP, smem, blocks, threads;
 };
-WideKernel kv4_wide_kernel(int head_dim);
+WideKernel kv4_wide_kernel(int head_dim, int dtype);
 
 }  // namespace mk

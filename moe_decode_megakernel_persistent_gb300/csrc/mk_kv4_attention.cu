@@ -675,12 +675,10 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
 
 // Items cut between blocks: a block joins the partial results of CC columns of
 // an item, in the blocks' order.  First the places of the item's parts, once for
-// all of its columns; then up to kFewParts of them are a warp's work, a column
-// each, and more are all warps' work, every NW-th part each with a running maximum,
-// the warps at the end.  Items without a tile (nothing seen) get zeros here.
-// (1024 rows at 8022 positions, 16384 columns of about 3 parts: a block for every column
-// with the places found by every warp took 33 us.)
-constexpr int kFewParts = 4;
+// all of its columns.  Of several columns each is a warp's work (1024 rows at 8022 positions,
+// 16384 columns of about 3 parts: a block for every column with the places found by every
+// warp took 33 us); a single column is all warps', every NW-th part each, the warps at the
+// end.  Items without a tile (nothing seen) get zeros here.
 // NB: parts in flight in each warp.
 template <int HD, class T, int NB>
 __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArgs p, int CT, int SP, int G, int CC) {
@@ -760,7 +758,7 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
   auto put_lse = [&](int row, int hd, float M, float ls) {
     p.lse[((size_t)seq * p.a.rows + row) * p.n_heads + hd] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994530942f;
   };
-  if (n <= kFewParts) {
+  if (CC > 1) {
     for (int c = c0 + w; c < c1; c += NW) {
       gather(c, 0, 1);
       int row, hd;
@@ -771,9 +769,9 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
     }
     return;
   }
-  for (int c = c0; c < c1; ++c) {
+  {
+    const int c = c0;
     gather(c, w, NW);
-    __syncthreads();
     if (lane == 0) {
       red_m[w] = m;
       red_l[w] = l;
@@ -799,12 +797,15 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
 
 // ---------------------------------------------------------------- host
 
-// From so many bf16 columns on, tiles of 128 on tcgen05 (mk_kv4_wide.cu): what no longer
-// fits one tile of the narrow kernel, which unpacks a cache tile for each 32 columns.  36
-// columns: one sequence of 8022 positions 18.6 us against 26.9, 16 of 700 25 against
-// 32, 16 of 8192 92 against 84; 64 columns: 20.0, 26, 93 against 30.1, 32, 85; 32 columns,
-// one of 8022: 19.4 against 15.6.
+// From so many columns on, tiles of 128 on tcgen05 (mk_kv4_wide.cu), us against the narrow
+// kernel's, for 16 sequences of 8192 / one of 8022 / 16 of 700 positions and 4 heads a kv head.
+// bf16: what no longer fits one tile of the narrow kernel, which unpacks a cache tile
+// for each 32 columns: 36 columns 71 / 18.1 / 19.9 against 79 / 18.0 / 23.2, 32 columns
+// 71 / 17.3 / 19.5 against 48 / 15.7 / 16.9.  fp32 (tiles of 16 columns, blocks of 256): 96
+// columns 178 / 30.2 / 39.1 against 226 / 26.0 / 39.7, 80 columns 175 / 29.5 / 38.1 against
+// 191 / 23.6 / 36.3.
 constexpr int kWideCols = 33;
+constexpr int kWideColsF32 = 81;
 constexpr int kShort = 10;  // steps of a block, at most, for work that counts as short
 
 struct Plan {
@@ -836,12 +837,14 @@ void take(Plan* pl) {
 // (registers hold the sums of 32 and 16 columns).
 template <int HD>
 void take_for(Plan* pl, int cols, int dtype) {
-  if (dtype == MK_BF16 && cols >= kWideCols) {
-    const WideKernel w = kv4_wide_kernel(HD);
+  if (cols >= (dtype == MK_F32 ? kWideColsF32 : kWideCols)) {
+    const WideKernel w = kv4_wide_kernel(HD, dtype);
     pl->main = w.fn;
-    pl->join[0] = reinterpret_cast<const void*>(&k_kv4_join<HD, __nv_bfloat16, 4>);
-    pl->join[1] = reinterpret_cast<const void*>(&k_kv4_join<HD, __nv_bfloat16, 12>);
-    pl->id = (HD == 64 ? 0 : 16) + 7;
+    pl->join[0] = dtype == MK_F32 ? reinterpret_cast<const void*>(&k_kv4_join<HD, float, 4>)
+                                  : reinterpret_cast<const void*>(&k_kv4_join<HD, __nv_bfloat16, 4>);
+    pl->join[1] = dtype == MK_F32 ? reinterpret_cast<const void*>(&k_kv4_join<HD, float, 12>)
+                                  : reinterpret_cast<const void*>(&k_kv4_join<HD, __nv_bfloat16, 12>);
+    pl->id = (HD == 64 ? 0 : 16) + (dtype == MK_F32 ? 8 : 0) + 7;
     pl->CT = w.CT;
     pl->SP = w.SP;
     pl->smem = pl->base_smem = w.smem;
@@ -945,15 +948,17 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
     return true;
   }
   pl->grid = (int)std::min<long long>(room, items * most);
-  // The join.  An item has about grid / items parts: as many warps for each column, up to 16
-  // with 12 parts in flight in each where that is not enough (131071 positions, 152 parts: 24.5 us
-  // against 26.5 with 4, whose fewer registers the other cases need), and a block for a column
-  // while that is few blocks.
-  pl->join_cols = (long long)items * pl->CT <= 2048 ? 1 : 16;
+  // The join.  Up to ten columns an SM are a block each, with as many warps as the item has
+  // parts (about grid / items), and 12 parts in flight in each warp where blocks are few
+  // (131071 positions, 152 parts: 23.8 us; 26.5 with 4, whose fewer registers serve more
+  // blocks).  More columns are a warp each, 8 or 16 a block (128 rows at 8022 positions, 2048
+  // columns: 34.6 us, 49 by blocks; 16 sequences with up to 5 drafted rows, 1280: 30.9 by warps, 29.9).
+  const long long all_cols = items * std::min<long long>(cols, pl->CT);
+  pl->join_cols = all_cols <= 1520 ? 1 : all_cols <= 8192 ? 8 : 16;
   int nw = 2;
   while (nw < 16 && nw * 2 * items <= pl->grid) nw *= 2;
-  pl->join_many = pl->grid / 64 >= items;
-  pl->join_threads = 32 * (pl->join_cols > 1 ? std::max(nw, 8) : nw);
+  pl->join_many = pl->grid / 64 >= items && all_cols <= 152;
+  pl->join_threads = 32 * (pl->join_cols > 1 ? 8 : nw);
   pl->item_off = 16;
   pl->part_off = pl->item_off + (size_t)items * sizeof(longlong2);
   pl->bytes = pl->part_off + 2 * (size_t)pl->grid * pl->CT * (head_dim + 4) * sizeof(float);

@@ -30,10 +30,16 @@
 // for all steps: 122 us; a warp of its own for them, with three that unpack: 127.)
 // Two blocks of an SM (256 TMEM columns each) fill each other's waits.
 //
-// Measured: 1024 rows of 16 heads on 4 kv heads of 128 dimensions, 8022 positions,
-// 115 us, 548 TFLOP/s of 4 x dimensions x seen pairs; tensor cores 25% active.
-// A step takes about 2,900 cycles of a block, in which a column warp works 2,200 and waits
-// for the scores otherwise; 700 cycles of an unpacking warp's share are the codes.
+// fp32 rows: q and the weights are two fp16 parts each (22 bits), the products run on
+// both, and V has no room but rescales O each time its largest scale passes a power of two
+// (a value loses at most 2^-21 of the largest).  Their q fills the shared memory that a second
+// block would need, so a block has two tiles of 128 columns, which share the unpacked operands.  (For
+// bf16 rows that is no faster: 115 us against 113.)
+//
+// Measured, 1024 rows of 16 heads on 4 kv heads of 128 dimensions at 8022 positions: bf16
+// 113 us, 561 TFLOP/s of 4 x dimensions x seen pairs, tensor cores 25% active; fp32 154 us
+// (546 by the narrow kernel).  A bf16 step takes about 2,900 cycles of a block, in which a column
+// warp works 2,200 and waits for the scores otherwise.
 #include <algorithm>
 
 #include "mk_kv4_att.cuh"
@@ -41,13 +47,20 @@
 namespace mk {
 namespace {
 
-template <int HD>
+// TB tiles of 128 columns of a block, for rows of type T.
+template <int HD, class T, int TB>
 struct Wide {
-  static constexpr int NG = HD / kGroup, CT = 128, SP = kTile;
-  static constexpr int QB = NG * CT * 128;          // bytes of q's operand
+  static constexpr bool F32 = std::is_same<T, float>::value;
+  static constexpr int NG = HD / kGroup, CT = 128 * TB, SP = kTile;
+  static constexpr int QP = F32 ? 2 : 1;            // fp16 parts of q, and of the weights
+  static constexpr int QT = NG * 128 * 128;         // bytes of a tile's q operand of one part
+  static constexpr int QB = TB * QP * QT;
   static constexpr int KVB = NG * SP * 128;         // of K's (or V's) operand of a step
   static constexpr int SMEM = 1024 + QB + 4 * KVB;
-  static constexpr int TM = 256;                    // TMEM columns: S of two steps [2][64], O [HD]
+  static constexpr int TM = 256;                    // TMEM columns of a tile: S of two steps [2][64], O [HD]
+  static constexpr int UW = 4 * TB;                 // the first unpacking warp
+  static constexpr int THREADS = 32 * (UW + 4), BLOCKS = TB == 1 ? 2 : 1;
+  static constexpr int ROOM = F32 ? 0 : 3;          // V's scales may grow by 2^ROOM before O is rescaled
 };
 
 // Shared-memory operand, 128-byte swizzle, rows of 128 bytes in atoms of 8 rows;
@@ -123,14 +136,14 @@ struct StepSays {
   uint32_t bad[4];   // V scales that are no numbers: [group][positions 0..31, 32..63]
 };
 
-template <int HD>
-__global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ AttArgs p) {
-  using W = Wide<HD>;
+template <int HD, class T, int TB>
+__global__ void __launch_bounds__(Wide<HD, T, TB>::THREADS, Wide<HD, T, TB>::BLOCKS) k_kv4_wide(const __grid_constant__ AttArgs p) {
+  using W = Wide<HD, T, TB>;
   using L = Tile<HD>;
-  constexpr int NG = W::NG, CT = W::CT, SP = W::SP;
+  constexpr int NG = W::NG, CT = W::CT, SP = W::SP, UW = W::UW;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
-  __shared__ __align__(8) uint64_t k_full[4], v_full[2], s_full[2], p_full[2], pv_done[2], q_full;
+  __shared__ __align__(8) uint64_t k_full[4], v_full[2], s_full[2][TB], p_full[2][TB], pv_done[2], q_full;
   __shared__ unsigned long long list[kList];
   __shared__ int note[kList];
   __shared__ StepSays says[4];
@@ -146,10 +159,19 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
   // pv_done of i - 2 is, so v_full, s_full, p_full and pv_done of a stage wait for
   // who reads the last one; k_full may be a stage's round ahead of the columns and has four.
   if (tid == 0) {
-    uint64_t* const bars[13] = {&k_full[0], &k_full[1], &k_full[2], &k_full[3], &v_full[0],  &v_full[1], &p_full[0],
-                                &p_full[1], &q_full,    &s_full[0], &s_full[1], &pv_done[0], &pv_done[1]};
-    for (int i = 0; i < 13; ++i)  // by each of four warps, by one
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bars[i])), "r"(i < 9 ? 4 : 1) : "memory");
+    auto init = [](uint64_t* b, int n) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(n) : "memory");
+    };
+    for (int i = 0; i < 4; ++i) init(&k_full[i], 4);  // by each unpacking warp
+    for (int i = 0; i < 2; ++i) {
+      init(&v_full[i], 4);
+      init(&pv_done[i], 1);
+      for (int t = 0; t < TB; ++t) {
+        init(&s_full[i][t], 1);
+        init(&p_full[i][t], 4);  // by each of the tile's warps
+      }
+    }
+    init(&q_full, 4 * TB);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     give_up = 0;
   }
@@ -158,22 +180,22 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
     if (lane == 0) s_run = r;
   }
   if (w == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tm_base)), "n"(W::TM)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tm_base)), "n"(W::TM * TB)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   before_sync();
   __syncthreads();
   after_sync();
-  const uint32_t tm = tm_base, tm_o = tm + 2 * SP;
+  const uint32_t tm = tm_base;  // tile t: S at 256 t, O at 256 t + 128
   Runs run = s_run;
   const Runs mine = run;
   uint32_t n_steps = run.t1 - run.t0;
   if (n_steps)
     for (Runs r = mine; r.next(p, CT, SP);) n_steps += r.t1 - r.t0;
 
-  if (w >= 4) {  // ---- unpacking, and the products (the warps take turns)
-    const int u = tid - 128;
+  if (w >= UW) {  // ---- unpacking, and the products (the warps take turns)
+    const int u = tid - 32 * UW;
     auto look_up = [&](uint32_t i) {
       Runs r = mine;
       uint32_t before = 0;
@@ -268,21 +290,28 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       fetch_v(0);
     }
     uint32_t n_runs = 0;
-    constexpr uint32_t id_qk = (1u << 4) | ((SP >> 3) << 17) | ((CT >> 4) << 24);               // fp16, fp32 sums
-    constexpr uint32_t id_pv = (1u << 4) | (1u << 16) | ((HD >> 3) << 17) | ((CT >> 4) << 24);  // V by rows
+    constexpr uint32_t id_qk = (1u << 4) | ((SP >> 3) << 17) | ((128 >> 4) << 24);               // fp16, fp32 sums
+    constexpr uint32_t id_pv = (1u << 4) | (1u << 16) | ((HD >> 3) << 17) | ((128 >> 4) << 24);  // V by rows
     // the second product of step i, once its weights are there
     auto second = [&](uint32_t i) {
-      bool ok = bar_wait(smem_addr(&p_full[i & 1]), (i >> 1) & 1, &give_up, p.a.status);
-      ok = bar_wait(smem_addr(&v_full[i & 1]), (i >> 1) & 1, &give_up, p.a.status) && ok;
-      after_sync();
-      if (lane == 0 && ok && !give_up) {
-        const uint32_t add = note[i % kList] & kFirst ? 0 : 1, pw = tm + SP * (i & 1);
-        const uint64_t v = operand(smem_addr(kv_op + ((i & 1) * 2 + 1) * W::KVB), SP * 128);
+      bool ok = bar_wait(smem_addr(&v_full[i & 1]), (i >> 1) & 1, &give_up, p.a.status);
+      const uint32_t add = note[i % kList] & kFirst ? 0 : 1;
+      const uint64_t v = operand(smem_addr(kv_op + ((i & 1) * 2 + 1) * W::KVB), SP * 128);
 #pragma unroll
-        for (int kk = 0; kk < SP / 16; ++kk) mma_ts(tm_o, pw + 8 * kk, v + ((kk * 16 * 128) >> 4), id_pv, kk ? 1 : add);
-        commit(smem_addr(&pv_done[i & 1]));
+      for (int t = 0; t < TB; ++t) {
+        ok = bar_wait(smem_addr(&p_full[i & 1][t]), (i >> 1) & 1, &give_up, p.a.status) && ok;
+        after_sync();
+        if (lane == 0 && ok && !give_up) {
+          const uint32_t pw = tm + W::TM * t + SP * (i & 1), to = tm + W::TM * t + 2 * SP;
+#pragma unroll
+          for (int x = W::QP - 1; x >= 0; --x)  // the weights' low part first
+#pragma unroll
+            for (int kk = 0; kk < SP / 16; ++kk)
+              mma_ts(to, pw + 32 * x + 8 * kk, v + ((kk * 16 * 128) >> 4), id_pv, kk || x < W::QP - 1 ? 1 : add);
+          if (t == TB - 1) commit(smem_addr(&pv_done[i & 1]));
+        }
+        __syncwarp();
       }
-      __syncwarp();
     };
     float cap = 0.f;  // V's scales of the run are below it
     for (uint32_t i = 0; i < n_steps; ++i) {
@@ -295,13 +324,14 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       const int st = i & 1;
       const bool first = note[i % kList] & kFirst;
       if (first) ++n_runs;
-      if (i >= 2) bar_wait(smem_addr(&s_full[st]), ((i - 2) >> 1) & 1, &give_up, p.a.status);
+      if (i >= 2)
+        for (int t = 0; t < TB; ++t) bar_wait(smem_addr(&s_full[st][t]), ((i - 2) >> 1) & 1, &give_up, p.a.status);
       const int nk = min(max(14 - exponent(largest(ks[0], ks[1])), -100), 100);  // K's scales times 2^nk: below 2^15
       const float tv = largest(vs[0], vs[1]);
       if (first) cap = 0.f;
-      if (tv > cap || cap == 0.f) cap = power(min(max(exponent(tv) + 4, -80), 100));  // the next power of two, and 2^3 of room
+      if (tv > cap || cap == 0.f) cap = power(min(max(exponent(tv) + 1 + W::ROOM, -80), 100));  // the next power of two, and some room
       const int nv = 15 - exponent(cap);
-      if (w == 4) {
+      if (w == UW) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -320,24 +350,31 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       if (lane == 0) arrive(smem_addr(&k_full[i & 3]));
       if (i + 1 < n_steps) fetch_k(i + 1);
       if (i >= 2) bar_wait(smem_addr(&pv_done[st]), ((i - 2) >> 1) & 1, &give_up, p.a.status);
-      if (w - 4 == (i & 3)) {
+      if (w - UW == (i & 3)) {
         bool ok = bar_wait(smem_addr(&k_full[i & 3]), (i >> 2) & 1, &give_up, p.a.status);
         if (first) {  // the columns lay q after they have read the last run's sums
           ok = bar_wait(smem_addr(&q_full), (n_runs - 1) & 1, &give_up, p.a.status) && ok;
         }
         after_sync();
         if (lane == 0 && ok && !give_up) {
-          const uint64_t q = operand(smem_addr(q_op)), k = operand(smem_addr(kd));
-          const uint32_t to = tm + SP * st;  // the weights of step i - 2 were there
+          const uint64_t k = operand(smem_addr(kd));
 #pragma unroll
-          for (int g = 0; g < NG; ++g)
+          for (int t = 0; t < TB; ++t) {
+            const uint32_t to = tm + W::TM * t + SP * st;  // the weights of step i - 2 were there
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t qa = q + ((g * CT * 128 + kk * 32) >> 4), kb = k + ((g * SP * 128 + kk * 32) >> 4);
-              if (g == 0 && kk == 0) mma_ss<false>(to, qa, kb, id_qk);
-              else mma_ss<true>(to, qa, kb, id_qk);
+            for (int x = W::QP - 1; x >= 0; --x) {  // q's low part first
+              const uint64_t q = operand(smem_addr(q_op + (t * W::QP + x) * W::QT));
+#pragma unroll
+              for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  const uint64_t qa = q + ((g * 128 * 128 + kk * 32) >> 4), kb = k + ((g * SP * 128 + kk * 32) >> 4);
+                  if (g == 0 && kk == 0 && x == W::QP - 1) mma_ss<false>(to, qa, kb, id_qk);
+                  else mma_ss<true>(to, qa, kb, id_qk);
+                }
             }
-          commit(smem_addr(&s_full[st]));
+            commit(smem_addr(&s_full[st][t]));
+          }
         }
         __syncwarp();
       }
@@ -345,14 +382,16 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       if (lane == 0) arrive(smem_addr(&v_full[st]));
       if (i + 1 < n_steps) fetch_v(i + 1);
       // (the sums take one step's products after another's: step i - 2's are done)
-      if (w - 4 == ((i + 2) & 3) && i) second(i - 1);
+      if (w - UW == ((i + 2) & 3) && i) second(i - 1);
     }
-    if (w == 4 && n_steps) {
+    if (w == UW && n_steps) {
       if (n_steps >= 2) bar_wait(smem_addr(&pv_done[n_steps & 1]), ((n_steps - 2) >> 1) & 1, &give_up, p.a.status);
       second(n_steps - 1);
     }
   } else {  // ---- a query column each
-    const uint32_t mine_tm = (uint32_t)(32 * w) << 16;  // this warp's lanes
+    const int tile = w >> 2, tt = tid & 127;
+    // this warp's lanes of its tile's scores and sums
+    const uint32_t tm_s = tm + W::TM * tile + ((uint32_t)(32 * (w & 3)) << 16), tm_o = tm_s + 2 * SP;
     uint32_t k = 0;
     for (bool more = n_steps > 0; more; more = run.next(p, CT, SP)) {
       const int seq = p.n_ctiles == 1 ? run.e : run.e / p.n_ctiles, j = run.e - seq * p.n_ctiles;
@@ -364,27 +403,54 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       const int lim = there && row < nn ? max(0, len - nn + row + 1) : 0;  // positions that it sees
       float c_row;  // times a step's k_mul, the scores' factor
       {
-        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q.p) + seq * p.q.seq + row * p.q.row + hd * p.q.head;
-        float top = 0.f;
-        uint4 qr[HD / 8];
+        const T* src = reinterpret_cast<const T*>(p.q.p) + seq * p.q.seq + row * p.q.row + hd * p.q.head;
+        // (bf16 rows wait in registers for their largest value, fp32 rows are read twice)
+        uint4 qr[W::F32 ? 1 : HD / 8];
+        if constexpr (!W::F32) {
 #pragma unroll
-        for (int x = 0; x < HD / 8; ++x) qr[x] = there ? *reinterpret_cast<const uint4*>(src + 8 * x) : make_uint4(0, 0, 0, 0);
+          for (int x = 0; x < HD / 8; ++x) qr[x] = there ? *reinterpret_cast<const uint4*>(src + 8 * x) : make_uint4(0, 0, 0, 0);
+        }
+        auto eight = [&](int x, float (&y)[8]) {
+          if constexpr (W::F32) {
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+            if (there) {
+              a = __ldg(reinterpret_cast<const float4*>(src + 8 * x));
+              b = __ldg(reinterpret_cast<const float4*>(src + 8 * x + 4));
+            }
+            y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w, y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
+          } else {
+            const uint32_t u4[4] = {qr[x].x, qr[x].y, qr[x].z, qr[x].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[2 * i] = low_f(u4[i]), y[2 * i + 1] = high_f(u4[i]);
+          }
+        };
+        float top = 0.f;
 #pragma unroll
         for (int x = 0; x < HD / 8; ++x) {
-          const uint4 v = qr[x];
-          top = fmaxf(top, fmaxf(fmaxf(fmaxf(fabsf(low_f(v.x)), fabsf(high_f(v.x))), fmaxf(fabsf(low_f(v.y)), fabsf(high_f(v.y)))),
-                                 fmaxf(fmaxf(fabsf(low_f(v.z)), fabsf(high_f(v.z))), fmaxf(fabsf(low_f(v.w)), fabsf(high_f(v.w))))));
+          float y[8];
+          eight(x, y);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[i]));
         }
         const int nq = min(max(14 - exponent(top), -100), 100);
         const float f = p.c < 0.f ? -power(nq) : power(nq);
         c_row = fabsf(p.c) * power(-65) * power(-nq);
 #pragma unroll
         for (int x = 0; x < HD / 8; ++x) {
-          const uint4 v = qr[x];
-          const uint4 y = make_uint4(pack2h(low_f(v.x) * f, low_f(v.y) * f), pack2h(high_f(v.x) * f, high_f(v.y) * f),
-                                     pack2h(low_f(v.z) * f, low_f(v.w) * f), pack2h(high_f(v.z) * f, high_f(v.w) * f));
-          const int g = x / 8, unit = x % 8;
-          *reinterpret_cast<uint4*>(q_op + g * CT * 128 + tid * 128 + ((unit ^ (tid & 7)) << 4)) = y;
+          float y[8];
+          eight(x, y);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] *= f;
+          uint8_t* to = q_op + tile * W::QP * W::QT + x / 8 * 128 * 128 + tt * 128 + (((x % 8) ^ (tt & 7)) << 4);
+#pragma unroll
+          for (int q = 0; q < W::QP; ++q) {
+            const uint4 h = make_uint4(pack2h(y[0], y[2]), pack2h(y[1], y[3]), pack2h(y[4], y[6]), pack2h(y[5], y[7]));
+            *reinterpret_cast<uint4*>(to + q * W::QT) = h;
+            if (q + 1 < W::QP) {
+              y[0] -= low_h(h.x), y[2] -= high_h(h.x), y[1] -= low_h(h.y), y[3] -= high_h(h.y);
+              y[4] -= low_h(h.z), y[6] -= high_h(h.z), y[5] -= low_h(h.w), y[7] -= high_h(h.w);
+            }
+          }
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -399,12 +465,12 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       for (int t = run.t0; t < run.t1; ++t, ++k) {
         const int st = k & 1;
         bool ok = bar_wait(smem_addr(&k_full[k & 3]), (k >> 2) & 1, &give_up, p.a.status);
-        ok = bar_wait(smem_addr(&s_full[st]), (k >> 1) & 1, &give_up, p.a.status) && ok;
+        ok = bar_wait(smem_addr(&s_full[st][tile]), (k >> 1) & 1, &give_up, p.a.status) && ok;
         after_sync();
         if (ok && !give_up) {
           const int vis = min(lim - t * SP, note[k % kList] & (kFirst - 1));  // of the step's positions
           const float cf = c_row * says[k & 3].k_mul, ne = says[k & 3].v_exp;
-          const uint32_t at = tm + mine_tm + SP * st;
+          const uint32_t at = tm_s + SP * st;
           auto step = [&](auto cut_) {
             constexpr bool CUT = decltype(cut_)::value;
             float s[4][16], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -433,11 +499,11 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
                 for (int c = 0; c < HD; c += 16) {
                   float o[16];
                   uint32_t x16[16];
-                  tm_load16(tm_o + mine_tm + c, o);
+                  tm_load16(tm_o + c, o);
                   tm_loaded(o);
 #pragma unroll
                   for (int x = 0; x < 16; ++x) x16[x] = __float_as_uint(o[x] * fo);
-                  tm_store16(tm_o + mine_tm + c, x16);
+                  tm_store16(tm_o + c, x16);
                 }
               }
             }
@@ -446,6 +512,7 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
 #pragma unroll
             for (int c = 0; c < 4; c += 2) {
               uint32_t b[16];
+              [[maybe_unused]] uint32_t low[W::F32 ? 16 : 1];
 #pragma unroll
               for (int x = 0; x < 32; x += 2) {
                 float w2[2];
@@ -456,8 +523,10 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
                   la[(x + y) & 3] += w2[y];
                 }
                 b[x / 2] = pack2h(w2[0], w2[1]);
+                if constexpr (W::F32) low[x / 2] = pack2h(w2[0] - low_h(b[x / 2]), w2[1] - high_h(b[x / 2]));
               }
               tm_store16(at + 8 * c, b);  // over the scores, which are all in registers
+              if constexpr (W::F32) tm_store16(at + 32 + 8 * c, low);
             }
             l += (la[0] + la[1]) + (la[2] + la[3]);
           };
@@ -476,7 +545,7 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
         }
         before_sync();
         __syncwarp();
-        if (lane == 0) arrive(smem_addr(&p_full[st]));
+        if (lane == 0) arrive(smem_addr(&p_full[st][tile]));
       }
       // ---- the run's end: this column's sums, dimensions put back in order
       bar_wait(smem_addr(&pv_done[(k - 1) & 1]), ((k - 1) >> 1) & 1, &give_up, p.a.status);
@@ -485,12 +554,11 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
       const float undo = kCode * exp2f(-e), M = m - kRoom;
       const float f = whole ? (l == 0.f ? 0.f : undo / l) : undo;
       float* part = p.part + ((size_t)part_slot(blockIdx.x, run.t0) * CT + tid) * (HD + 4);
-      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row +
-                           hd * p.out.head;
+      T* dst = reinterpret_cast<T*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row + hd * p.out.head;
 #pragma unroll 1
       for (int c = 0; c < HD; c += 16) {
         float o[16];
-        tm_load16(tm_o + mine_tm + c, o);
+        tm_load16(tm_o + c, o);
         tm_loaded(o);
         if (!there) continue;
         const bool nan = give_up || (NG == 2 && c >= 64 ? bad[NG - 1] : bad[0]);
@@ -498,12 +566,13 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
         for (int x = 0; x < 16; ++x) o[x] = nan ? NAN : o[x] * f;
 #pragma unroll
         for (int x = 0; x < 16; x += 8) {  // 0 2 1 3 4 6 5 7
-          if (whole) {
+          if (whole && !W::F32) {
             *reinterpret_cast<uint4*>(dst + c + x) = make_uint4(pack2(o[x], o[x + 2]), pack2(o[x + 1], o[x + 3]),
                                                                 pack2(o[x + 4], o[x + 6]), pack2(o[x + 5], o[x + 7]));
           } else {
-            *reinterpret_cast<float4*>(part + c + x) = make_float4(o[x], o[x + 2], o[x + 1], o[x + 3]);
-            *reinterpret_cast<float4*>(part + c + x + 4) = make_float4(o[x + 4], o[x + 6], o[x + 5], o[x + 7]);
+            float* to = whole ? reinterpret_cast<float*>(dst) : part;
+            *reinterpret_cast<float4*>(to + c + x) = make_float4(o[x], o[x + 2], o[x + 1], o[x + 3]);
+            *reinterpret_cast<float4*>(to + c + x + 4) = make_float4(o[x + 4], o[x + 6], o[x + 5], o[x + 7]);
           }
         }
       }
@@ -521,16 +590,20 @@ __global__ void __launch_bounds__(256, 2) k_kv4_wide(const __grid_constant__ Att
   }
   before_sync();
   __syncthreads();
-  if (w == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(W::TM));
+  if (w == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(W::TM * TB));
 }
 
-template <int HD>
+template <int HD, class T, int TB>
 WideKernel info() {
-  return {reinterpret_cast<const void*>(&k_kv4_wide<HD>), Wide<HD>::CT, Wide<HD>::SP, Wide<HD>::SMEM, 2, 256};
+  using W = Wide<HD, T, TB>;
+  return {reinterpret_cast<const void*>(&k_kv4_wide<HD, T, TB>), W::CT, W::SP, W::SMEM, W::BLOCKS, W::THREADS};
 }
 
 }  // namespace
 
-WideKernel kv4_wide_kernel(int head_dim) { return head_dim == 64 ? info<64>() : info<128>(); }
+WideKernel kv4_wide_kernel(int head_dim, int dtype) {
+  if (dtype == MK_F32) return head_dim == 64 ? info<64, float, 2>() : info<128, float, 2>();
+  return head_dim == 64 ? info<64, __nv_bfloat16, 1>() : info<128, __nv_bfloat16, 1>();
+}
 
 }  // namespace mk

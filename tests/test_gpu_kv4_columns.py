@@ -9,61 +9,66 @@ import torch
 
 from moe_decode_megakernel_persistent_gb300 import kv4
 from tests import _kv4 as R
-from tests.test_gpu_kv4 import BF, check, i32, make, poisoned_pool, rows_of, run, table_for
+from tests.test_gpu_kv4 import BF, F32, check, i32, make, poisoned_pool, rows_of, run, table_for
 
 pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("H,G,hd,rows", [
     (4, 4, 128, 32), (4, 4, 128, 33), (4, 4, 64, 33), (2, 2, 128, 127), (2, 2, 64, 128), (2, 2, 128, 129),
-    (8, 2, 128, 9), (8, 2, 64, 65), (1, 1, 128, 257), (5, 1, 64, 26), (64, 1, 128, 3)])
-def test_edges_of_the_column_tiles(gpu_lib, H, G, hd, rows):
+    (8, 2, 128, 9), (8, 2, 64, 65), (1, 1, 128, 257), (5, 1, 64, 26), (64, 1, 128, 3), (4, 4, 128, 81), (4, 1, 64, 20)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_edges_of_the_column_tiles(gpu_lib, dtype, H, G, hd, rows):
     lengths = [rows, 0, 63, 64, 65, 200, 1]
     n_new = [rows, 0, min(rows, 63), 1, min(rows, 65), rows // 2, min(rows, 3)]
     pool, table = make(lengths, G, hd, seed=21)
-    run(rows_of(len(lengths), rows, H, hd, BF), pool, table, lengths, n_new)
-    run(rows_of(len(lengths), rows, H, hd, BF), pool, table, lengths)
+    run(rows_of(len(lengths), rows, H, hd, dtype), pool, table, lengths, n_new)
+    run(rows_of(len(lengths), rows, H, hd, dtype), pool, table, lengths)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("H,G,hd,rows,n,length", [
     (4, 1, 128, 40, 1, 9000),      # one item, joined from every block
     (4, 4, 64, 40, 1, 5000),
     (8, 2, 128, 300, 3, 700),      # more items than blocks have time for alone: few parts each
     (2, 2, 64, 130, 40, 70),       # many short ones: several items a block
     (16, 4, 128, 512, 2, 513)])
-def test_splits_and_joins(gpu_lib, H, G, hd, rows, n, length):
+def test_splits_and_joins(gpu_lib, dtype, H, G, hd, rows, n, length):
     lengths = [max(1, length - 31 * i % length) for i in range(n)]
     pool, table = make(lengths, G, hd, seed=22)
-    q = rows_of(n, rows, H, hd, BF)
+    q = rows_of(n, rows, H, hd, dtype)
     out, _ = run(q, pool, table, lengths)
     for _ in range(20):                    # the same bits whatever the blocks' timing
         assert torch.equal(kv4.attention(q, pool, table, i32(lengths)), out)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0, None])
 @pytest.mark.parametrize("mul", [1e-3, 1.0, 60.0])
-def test_flat_negative_and_steep_scores(gpu_lib, mul, scale):
+def test_flat_negative_and_steep_scores(gpu_lib, dtype, mul, scale):
     lengths = [700, 65]
     pool, table = make(lengths, 2, 128, seed=23)
-    run(rows_of(2, 20, 8, 128, BF, mul=mul), pool, table, lengths, scale=scale)
+    run(rows_of(2, 24, 8, 128, dtype, mul=mul), pool, table, lengths, scale=scale)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("spread", [1e-9, 1e4, 1e9])
-def test_cache_values_of_any_size(gpu_lib, spread):
+def test_cache_values_of_any_size(gpu_lib, dtype, spread):
     lengths = [400, 33]
     pool, table = make(lengths, 1, 64, seed=24, spread=spread)
-    run(rows_of(2, 40, 2, 64, BF, mul=1.5 / spread), pool, table, lengths)
+    run(rows_of(2, 45, 2, 64, dtype, mul=1.5 / spread), pool, table, lengths)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("times", [256.0, 4096.0])
-def test_outliers_among_the_cached_values(gpu_lib, hd, times):
+def test_outliers_among_the_cached_values(gpu_lib, dtype, hd, times):
     """Some positions' K or V far larger than the rest.  A K operand keeps 2^-21 of the
     largest value of its 64 positions (2^-25 absolutely, where the largest is at least
-    7 x 2^-6), a V operand 2^-18 of the sequence's largest (7 x 2^-9).  So a score may be
-    off by scale sum|q| 2^-21 max|K| more, each weight by twice that (numerator and
-    denominator), and the result by 2^-18 max|V| more."""
-    n, H, rows = 700, 4, 16
+    7 x 2^-6), a V operand 2^-18 of the sequence's largest for bf16 rows (7 x 2^-9),
+    2^-21 for fp32 rows.  So a score may be off by scale sum|q| 2^-21 max|K| more, each weight
+    by twice that (numerator and denominator), and the result by so much of max|V| more."""
+    n, H, rows = 700, 4, 21
     table, n_pages = table_for([n])
     pool = poisoned_pool(n_pages, 1, hd)
     g = torch.Generator(device="cuda").manual_seed(31)
@@ -71,24 +76,25 @@ def test_outliers_among_the_cached_values(gpu_lib, hd, times):
     k[5::97] *= times
     v[11::131] *= times
     R.fill(pool, hd, table[0].long()[:-(-n // R.PAGE)], k, v)
-    q = rows_of(1, rows, H, hd, BF)
+    q = rows_of(1, rows, H, hd, dtype)
     out, lse = kv4.attention(q, pool, table, i32([n]), return_lse=True)
     kc, vc = R.cache_values(pool, hd, table[0].long(), n)
     o, l, A, D = R.attend(q[0], kc, vc, n - rows, 1 / math.sqrt(hd))
-    inner, half, le = R.bounds(A, D, l, n, hd, BF, float(vc.abs().max()))
+    inner, half, le = R.bounds(A, D, l, n, hd, dtype, float(vc.abs().max()))
     score = q[0].double().abs().sum(-1) / math.sqrt(hd) * 2.0 ** -21 * float(kc.abs().max())
     # a factor e^x of a weight is off by at most e^x - 1 relatively
-    inner = inner + torch.expm1(2 * score)[..., None] * A + 2.0 ** -18 * float(vc.abs().max())
+    inner = inner + torch.expm1(2 * score)[..., None] * A + (2.0 ** -18 if dtype == BF else 2.0 ** -21) * float(vc.abs().max())
     off = (out[0].double() - o).abs() - (inner * (1 + half) + half * o.abs())
     assert off.max() <= 0, off.max().item()
     assert ((lse[0].double() - l).abs() <= le + score).all()
 
 
-def test_what_is_not_a_number_stays_with_who_sees_it(gpu_lib):
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_what_is_not_a_number_stays_with_who_sees_it(gpu_lib, dtype):
     """NaN and infinities in q, and groups of K and V that hold NaN, at positions that some rows see."""
     hd, n, rows, H = 128, 300, 70, 4
     pool, table = make([n, n], 1, hd, seed=25)
-    q = rows_of(2, rows, H, hd, BF)
+    q = rows_of(2, rows, H, hd, dtype)
     lengths = [n, n]
     clean, _ = run(q, pool, table, lengths)
     bad_q = q.clone()
@@ -121,7 +127,7 @@ def test_two_streams_at_once(gpu_lib):
     """Calls of many columns next to each other and to single rows."""
     lengths = [3000, 2500, 10]
     pool, table = make(lengths, 4, 128, seed=26)
-    qs = [rows_of(3, (100, 1, 33)[s % 3], 16, 128, BF, seed=s) for s in range(9)]
+    qs = [rows_of(3, (100, 1, 33)[s % 3], 16, 128, BF if s < 6 else F32, seed=s) for s in range(9)]
     ln = i32(lengths)
     want = [kv4.attention(q, pool, table, ln) for q in qs]
     torch.cuda.synchronize()
