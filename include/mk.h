@@ -498,7 +498,7 @@ MK_API int mk_kv4_load(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4
  * (padding, a length of 0) gets zeros and -infinity.  Positions past the
  * length are never used, whatever their slots hold.  out must not overlap q, the
  * pool or the workspace.  |scale| < 1e18; magnitudes of q and V up to 2^50 are kept whole,
- * terms weight * value below 2^-60 may be lost.  Weights are rounded by 2^-12 for bf16
+ * terms weight * value below 2^-60 may be lost.  Weights are rounded by 2^-11 for bf16
  * rows and 2^-22 for fp32 rows, sums are fp32.  From 33 query columns (rows x
  * n_heads / n_kv_heads) of bf16 and 81 of fp32 on, an fp32 q is rounded by 2^-22 too, a K
  * value may lose 2^-21 of the largest one of its 64 positions and head, a V value 2^-18 (bf16

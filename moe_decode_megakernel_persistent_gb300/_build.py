@@ -26,7 +26,8 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + IN
               "-I" + CSRC]
 # (source, object name, extra flags)
 SOURCES = [("mk_kernel.cu", f"mk_kernel_p{p}", [f"-DMK_KERNEL_PART={p}"]) for p in range(4)] + [
-    (f, os.path.splitext(f)[0], []) for f in ("mk_host.cpp", "mk_static.cu", "mk_pack.cu", "mk_kv.cu", "mk_kv4.cu", "mk_kv4_attention.cu", "mk_kv4_wide.cu", "mk_pages.cu", "mk_prefill.cu")]
+    (f, os.path.splitext(f)[0], []) for f in ("mk_host.cpp", "mk_static.cu", "mk_pack.cu", "mk_kv.cu", "mk_kv4.cu", "mk_kv4_attention.cu",
+                                                  "mk_kv4_wide.cu", "mk_pages.cu", "mk_prefill.cu")]
 
 
 def _nvcc() -> str:

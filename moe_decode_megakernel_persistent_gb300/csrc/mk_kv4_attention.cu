@@ -20,7 +20,7 @@
 //   weight x V code runs in fp16: the weight (at most 2^8, see below) times V's
 // scale is normalised by a power of two that follows the largest scale the warp
 // has met, to at most 2^14; fp16 then keeps 11 bits over 28 binades below it and
-// the weight is rounded by 2^-12 at most, where the output is rounded to 2^-9.  For
+// the weight is rounded by 2^-11 at most, where the output is rounded by 2^-8.  For
 // fp32 rows it is split into two parts (22 bits).
 // Everything else is fp32.
 //
@@ -40,15 +40,15 @@
 // An item cut between blocks is joined by a second kernel, launched so that its
 // start overlaps the first one's end.  Short work instead makes each item a cluster
 // of blocks that join through their shared memory, in one kernel.  Calls of many
-// bf16 columns run in mk_kv4_wide.cu.
+// columns run in mk_kv4_wide.cu.
 //
 // Measured (16 heads on 4 kv heads of 128, bf16 rows).  Short work is bound by its
 // chain of set-up, first copies and join: one sequence of 2049 positions 6.9 us, with 6% of
-// the issue slots busy; 16 of 256 to 8448 16.8 us (38 MB).  Long work is bound by issue
-// and the unpacking: 64 of 4096 to 16384 78.7 us, 4.6 TB/s, the ALU 55% and the issue slots 56%
-// busy, with 14 warps of 114 registers on an SM; one of 131071 27.5 us, 2.6 TB/s.  24 columns
+// the issue slots busy; 16 of 256 to 8448 15.7 us (38 MB).  Long work is bound by issue
+// and the unpacking: 64 of 4096 to 16384 78.3 us, 4.6 TB/s, the ALU 55% and the issue slots 56%
+// busy, with 14 warps of 114 registers on an SM; one of 131071 23.8 us, 3.0 TB/s.  24 columns
 // hold their sums in 243 registers, which leaves 8 warps an SM (issue slots 30% busy): 16 sequences of
-// up to 8022 positions with up to 5 rows each 31 us.
+// up to 8022 positions with up to 5 rows each 29.9 us.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -711,16 +711,15 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
   float m, l, o[V];
   // parts first, first + by .. of column c, NB at a time
   auto gather = [&](int c, int first, int by) {
-    constexpr int N = NB;
     m = kLow, l = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = 0.f;
 #pragma unroll 1
-    for (int i0 = first; i0 < n; i0 += N * by) {
-      float2 ml[N];
-      float v[N][V];
+    for (int i0 = first; i0 < n; i0 += NB * by) {
+      float2 ml[NB];
+      float v[NB][V];
 #pragma unroll
-      for (int y = 0; y < N; ++y) {
+      for (int y = 0; y < NB; ++y) {
         const int i = i0 + y * by, at = i < n ? slot[i] : -1;
         ml[y] = make_float2(kLow, 0.f);
 #pragma unroll
@@ -734,14 +733,14 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
       }
       float M = m;
 #pragma unroll
-      for (int y = 0; y < N; ++y) M = fmaxf(M, ml[y].x);
+      for (int y = 0; y < NB; ++y) M = fmaxf(M, ml[y].x);
       const float f0 = exp2_fast(m - M);
       m = M;
       l *= f0;
 #pragma unroll
       for (int x = 0; x < V; ++x) o[x] *= f0;
 #pragma unroll
-      for (int y = 0; y < N; ++y) {
+      for (int y = 0; y < NB; ++y) {
         const float f1 = exp2_fast(ml[y].x - M);
         l += ml[y].y * f1;
 #pragma unroll
@@ -769,29 +768,26 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
     }
     return;
   }
-  {
-    const int c = c0;
-    gather(c, w, NW);
-    if (lane == 0) {
-      red_m[w] = m;
-      red_l[w] = l;
-    }
+  gather(c0, w, NW);
+  if (lane == 0) {
+    red_m[w] = m;
+    red_l[w] = l;
+  }
 #pragma unroll
-    for (int x = 0; x < V; ++x) red[w][lane * V + x] = o[x];
-    __syncthreads();
-    int row, hd;
-    T* dst = place(c, row, hd);
-    for (int d = threadIdx.x; d < HD; d += blockDim.x) {
-      float M = kLow, ls = 0.f, v = 0.f;
-      for (int i = 0; i < NW; ++i) M = fmaxf(M, red_m[i]);
-      for (int i = 0; i < NW; ++i) {
-        const float f = exp2_fast(red_m[i] - M);
-        ls += red_l[i] * f;
-        v += red[i][d] * f;
-      }
-      dst[d] = (T)(ls == 0.f ? 0.f : v / ls);
-      if (p.lse && d == 0) put_lse(row, hd, M, ls);
+  for (int x = 0; x < V; ++x) red[w][lane * V + x] = o[x];
+  __syncthreads();
+  int row, hd;
+  T* dst = place(c0, row, hd);
+  for (int d = threadIdx.x; d < HD; d += blockDim.x) {
+    float M = kLow, ls = 0.f, v = 0.f;
+    for (int i = 0; i < NW; ++i) M = fmaxf(M, red_m[i]);
+    for (int i = 0; i < NW; ++i) {
+      const float f = exp2_fast(red_m[i] - M);
+      ls += red_l[i] * f;
+      v += red[i][d] * f;
     }
+    dst[d] = (T)(ls == 0.f ? 0.f : v / ls);
+    if (p.lse && d == 0) put_lse(row, hd, M, ls);
   }
 }
 
@@ -937,7 +933,7 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
   // for a place, 16.8), joined through their shared memory.  It saves the second kernel and the
   // scan of all lengths (20.7 us), but a ragged batch is not levelled and a long item has
   // 16 blocks at most, which loses once a block has more than about ten steps (131071
-  // positions: 57.6 us against 27.5).
+  // positions: 57.6 us against 27.5 then).
   int n = 1;
   while (n < 16 && 2 * n <= most && items <= clusters_at_once(*pl, head_dim, 2 * n)) n *= 2;
   if (!pl->wide && (most + n - 1) / n <= kShort) {

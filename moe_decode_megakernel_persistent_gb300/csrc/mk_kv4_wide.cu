@@ -1,5 +1,5 @@
-// Attention over the 4-bit paged cache for many query columns (prompt chunks):
-// tiles of 128 columns on the 5th-generation tensor cores (tcgen05).  The
+// Attention over the 4-bit paged cache for many query columns (prompt chunks, batches
+// of drafts): tiles of 128 columns on the 5th-generation tensor cores (tcgen05).  The
 // mathematics, the split of the work and the join are those of
 // mk_kv4_attention.cu; what differs is where the scales go and who does what.
 //
@@ -10,14 +10,14 @@
 //               tile's largest value).  Q is fp16 times a power of two of the row (a
 //               bf16 value is exact down to 2^-31 of its row's largest).  The powers
 //               multiply the fp32 scores.
-//   O += P V    P = weights in fp16 (rounded by 2^-12, where the output is rounded
-//               to 2^-9) over S's place in TMEM; V as K, its power following the largest
+//   O += P V    P = weights in fp16 (rounded by 2^-11, where the output is rounded
+//               by 2^-8) over S's place in TMEM; V as K, its power following the largest
 //               scale of the run with 2^3 of room (so that a value loses at most 2^-18
 //               of the largest), O rescaled when it moves.
 // So the 128 x 64 scores of a step need no scale of their own, and one pass: 64
 // scores a thread in registers, their maximum, one exponential each.  (With the
 // scales applied to scores and weights, as the narrow kernel does, a step took
-// 3,700 cycles of a column warp, and 195 us a chunk of 1024 rows at 8022 positions.)
+// 3,700 cycles of a column warp, and the call below 195 us.)
 //
 // Warps 0..3: a thread has a query column (a TMEM lane).  Its maximum moves only
 // when a score passes it by 2^8; then the warp rescales its sums in TMEM.
@@ -27,7 +27,7 @@
 // meanwhile.  K's operand of a step is laid while the second product of the step before
 // the last still reads its V, and one lane of the four warps in turn issues the
 // products, S of a step while the columns work on the one before it.  (By one warp
-// for all steps: 122 us; a warp of its own for them, with three that unpack: 127.)
+// for all steps 122 us where this took 115, by a warp of its own next to three that unpack 127.)
 // Two blocks of an SM (256 TMEM columns each) fill each other's waits.
 //
 // fp32 rows: q and the weights are two fp16 parts each (22 bits), the products run on
