@@ -49,16 +49,17 @@ __device__ __forceinline__ void write8(__nv_bfloat16* p, const V8& v) {
   *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// A thread's part of a token's rows: eight values of one group, so that eight
-// lanes take a group (one 16-byte load of bf16, one 4-byte store of codes each)
-// and a token is 16 * NG * n_kv_heads parts.
+// A thread's part of a token's rows: sixteen values of one group, so that four
+// lanes take a group (two 16-byte loads of bf16, one 8-byte store of codes each)
+// and a token is 8 * NG * n_kv_heads parts.
+constexpr int kLanes = 4;
 template <int HD>
 struct Part {
   int kv, head, group, lane;
   __device__ __forceinline__ explicit Part(int i, int n_kv_heads) {
-    lane = i % 8;
-    group = i / 8 % Tile<HD>::NG;
-    head = i / (8 * Tile<HD>::NG);
+    lane = i % kLanes;
+    group = i / kLanes % Tile<HD>::NG;
+    head = i / (kLanes * Tile<HD>::NG);
     kv = head >= n_kv_heads;
     head -= kv ? n_kv_heads : 0;
   }
@@ -69,25 +70,15 @@ constexpr int kThreadsKv = 256;  // the most threads of a block
 // Rows of one pass over a block's threads (a block stays within a sequence).
 inline int pass_rows(int parts, int rows) { return std::max(1, std::min(kThreadsKv / parts, rows)); }
 
-// The N rows row0 + j * step of a sequence: the tile half that each one's values
-// of this part lie in (null: padding, or a page outside the pool) and its row
-// there.
-template <int HD, int N>
-__device__ __forceinline__ void places_of(const Kv4Args& a, const Part<HD>& pt, int seq, int row0, int step,
-                                          uint8_t* (&t)[N], int (&at)[N]) {
-  int len, nn, p[N], page[N];
+// The tile half that a row's values of this part lie in (null: padding, or a page
+// outside the pool), and its row there.
+template <int HD>
+__device__ __forceinline__ uint8_t* place_of(const Kv4Args& a, const Part<HD>& pt, int seq, int row, int* at) {
+  int len, nn;
   seq_extent(a, seq, len, nn);
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int row = row0 + j * step;
-    p[j] = row < nn ? len - nn + row : -1;
-    page[j] = p[j] >= 0 ? page_of(a, seq, p[j]) : -1;
-  }
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    at[j] = p[j] % kTile;
-    t[j] = page[j] >= 0 ? tile_of<HD>(a, page[j], pt.head, p[j]) + pt.kv * Tile<HD>::V : nullptr;
-  }
+  const int p = row < nn ? len - nn + row : -1, page = p >= 0 ? page_of(a, seq, p) : -1;
+  *at = p % kTile;
+  return page >= 0 ? tile_of<HD>(a, page, pt.head, p) + pt.kv * Tile<HD>::V : nullptr;
 }
 
 __device__ __forceinline__ float value_of(uint32_t code, float s) {
@@ -95,104 +86,96 @@ __device__ __forceinline__ float value_of(uint32_t code, float s) {
   return code & 8u ? -m : m;
 }
 
-// One pass over the rows each way, N tokens in flight per thread.  Short calls are
+// One pass over the rows each way, a part of a row each thread.  Short calls are
 // bound by two dependent reads (length, page), which the rows' own reads do not wait
-// for (one row each of 16 sequences, 4 heads of 128: 1.8 us); long ones by issue, the
-// quotient and the packing of eight values a thread (4096 rows: 6.3 us for 10.6 MB, issue
-// slots 59% busy).
+// for (one row each of 16 sequences, 4 heads of 128: 2.0 us); long ones by issue, the
+// quotient and the packing (4096 rows: 5.3 us for 10.6 MB; with eight values a thread, half
+// the work beside a fixed part, 6.3; with two rows a thread 5.9).
 // The division |x| / s is the IEEE quotient: r = RN(1 / s), q = RN(x r), then
 // q + r (x - q s) in two fused steps (Markstein), which rounds correctly where
 // nothing under- or overflows; scales outside [2^-60, 2^60] take the division itself.
-template <int HD, class T, int N>
+template <int HD, class T>
 __global__ void __launch_bounds__(kThreadsKv) k_kv4_store(const __grid_constant__ Kv4Args a, Kv4Rows k, Kv4Rows v, int tp, int chunks) {
-  const int parts = 16 * Tile<HD>::NG * a.n_kv_heads;
-  const int seq = blockIdx.x / chunks, row_base = (blockIdx.x - seq * chunks) * tp * N;
-  const int tk = parts < (int)blockDim.x ? threadIdx.x / parts : 0, row0 = row_base + tk;
+  const int parts = 2 * kLanes * Tile<HD>::NG * a.n_kv_heads;
+  const int seq = blockIdx.x / chunks, row_base = (blockIdx.x - seq * chunks) * tp;
+  const int tk = parts < (int)blockDim.x ? threadIdx.x / parts : 0, row = row_base + tk;
   for (int i0 = 0; i0 < parts; i0 += blockDim.x) {
     const int i = i0 + threadIdx.x - tk * parts;
     const bool mine = tk < tp && i < parts;
     const Part<HD> pt(mine ? i : 0, a.n_kv_heads);
     const Kv4Rows& r = pt.kv ? v : k;
-    const T* src = reinterpret_cast<const T*>(r.p) + seq * r.seq + pt.head * r.head + pt.group * kGroup + 8 * pt.lane;
-    V8 x[N];
-    uint8_t* t[N];
-    int at[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int row = min(row0 + j * tp, a.rows - 1);
-      long long off = row * r.row;
-      if (r.slot) {  // rows that lie in their slots of a page
-        int len, nn;
-        seq_extent(a, seq, len, nn);
-        off += max(len - nn + row, 0) % kPageTokens * r.slot;
-      }
-      x[j] = read8(src + off);
+    const int there = min(row, a.rows - 1);
+    long long off = seq * r.seq + there * r.row + pt.head * r.head;
+    if (r.slot) {  // rows that lie in their slots of a page
+      int len, nn;
+      seq_extent(a, seq, len, nn);
+      off += max(len - nn + there, 0) % kPageTokens * r.slot;
     }
-    places_of<HD, N>(a, pt, seq, row0, tp, t, at);
+    const T* src = reinterpret_cast<const T*>(r.p) + off + pt.group * kGroup + 16 * pt.lane;
+    const V8 x[2] = {read8(src), read8(src + 8)};
+    int at;
+    uint8_t* t = place_of<HD>(a, pt, seq, row, &at);
+    // largest |x| of the group as bits (a NaN's are above an infinity's); every lane takes part
+    uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      // largest |x| of the group as bits (a NaN's are above an infinity's); every lane takes part
-      uint32_t top = 0;
+    for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(fabsf(x[e / 8].x[e % 8])));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(fabsf(x[j].x[e])));
+    for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (!t || !mine) continue;
+    // a group with a NaN or an infinity reads back as NaN
+    const bool finite = top < 0x7F800000u;
+    const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.f);
+    const float s = finite ? __bfloat162float(sb) : 0.f;
+    uint32_t c[2] = {0, 0};
+    if (s >= 8.6736174e-19f && s <= 1.1529215e18f) {
+      const float rs = __frcp_rn(s);
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (!t[j] || !mine) continue;
-      // a group with a NaN or an infinity reads back as NaN
-      const bool finite = top < 0x7F800000u;
-      const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.f);
-      const float s = finite ? __bfloat162float(sb) : 0.f;
-      uint32_t c = 0;
-      if (s >= 8.6736174e-19f && s <= 1.1529215e18f) {
-        const float rs = __frcp_rn(s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y = fabsf(x[j].x[e]), q0 = y * rs, q = fmaf(fmaf(-q0, s, y), rs, q0);
-          const uint32_t m = __float_as_uint(q + 12582912.f) & 7u;  // rounds to even; at most 7 (q <= 7 (1 + 2^-8))
-          c |= (m | (m ? __float_as_uint(x[j].x[e]) >> 28 & 8u : 0u)) << (4 * e);
-        }
-      } else if (s > 0.f) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t m = (uint32_t)fminf(rintf(fabsf(x[j].x[e]) / s), 7.f);
-          c |= (m | (m && x[j].x[e] < 0.f ? 8u : 0u)) << (4 * e);
-        }
+      for (int e = 0; e < 16; ++e) {
+        const float z = x[e / 8].x[e % 8], y = fabsf(z), q0 = y * rs, q = fmaf(fmaf(-q0, s, y), rs, q0);
+        const uint32_t m = __float_as_uint(q + 12582912.f) & 7u;  // rounds to even; at most 7 (q <= 7 (1 + 2^-8))
+        c[e / 8] |= (m | (m ? __float_as_uint(z) >> 28 & 8u : 0u)) << (4 * (e % 8));
       }
-      *reinterpret_cast<uint32_t*>(t[j] + at[j] * Tile<HD>::ROW + pt.group * (kGroup / 2) + 4 * pt.lane) = c;
-      if (pt.lane == 0)
-        *reinterpret_cast<uint16_t*>(t[j] + Tile<HD>::CODES + (at[j] * Tile<HD>::NG + pt.group) * 2) =
-            finite ? __bfloat16_as_ushort(sb) : (uint16_t)0x7FC0;
+    } else if (s > 0.f) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float z = x[e / 8].x[e % 8];
+        const uint32_t m = (uint32_t)fminf(rintf(fabsf(z) / s), 7.f);
+        c[e / 8] |= (m | (m && z < 0.f ? 8u : 0u)) << (4 * (e % 8));
+      }
     }
+    *reinterpret_cast<uint2*>(t + at * Tile<HD>::ROW + pt.group * (kGroup / 2) + 8 * pt.lane) = make_uint2(c[0], c[1]);
+    if (pt.lane == 0)
+      *reinterpret_cast<uint16_t*>(t + Tile<HD>::CODES + (at * Tile<HD>::NG + pt.group) * 2) =
+          finite ? __bfloat16_as_ushort(sb) : (uint16_t)0x7FC0;
   }
 }
 
-// The reverse, bound by issue alike: 4096 rows 5.1 us.
-template <int HD, class T, int N>
+// The reverse, bound alike: 4096 rows 4.6 us.
+template <int HD, class T>
 __global__ void __launch_bounds__(kThreadsKv) k_kv4_load(const __grid_constant__ Kv4Args a, Kv4Rows k, Kv4Rows v, int tp, int chunks) {
-  const int parts = 16 * Tile<HD>::NG * a.n_kv_heads;
-  const int seq = blockIdx.x / chunks, row_base = (blockIdx.x - seq * chunks) * tp * N;
-  const int tk = parts < (int)blockDim.x ? threadIdx.x / parts : 0, row0 = row_base + tk;
-  if (tk >= tp) return;
+  const int parts = 2 * kLanes * Tile<HD>::NG * a.n_kv_heads;
+  const int seq = blockIdx.x / chunks, row_base = (blockIdx.x - seq * chunks) * tp;
+  const int tk = parts < (int)blockDim.x ? threadIdx.x / parts : 0, row = row_base + tk;
+  if (tk >= tp || row >= a.rows) return;
   for (int i = threadIdx.x - tk * parts; i < parts; i += blockDim.x) {
     const Part<HD> pt(i, a.n_kv_heads);
     const Kv4Rows& r = pt.kv ? v : k;
-    T* dst = reinterpret_cast<T*>(const_cast<void*>(r.p)) + seq * r.seq + pt.head * r.head + pt.group * kGroup + 8 * pt.lane;
-    uint8_t* t[N];
-    int at[N];
-    uint32_t c[N], sc[N];
-    places_of<HD, N>(a, pt, seq, row0, tp, t, at);
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      c[j] = t[j] ? *reinterpret_cast<const uint32_t*>(t[j] + at[j] * Tile<HD>::ROW + pt.group * (kGroup / 2) + 4 * pt.lane) : 0u;
-      sc[j] = t[j] ? *reinterpret_cast<const uint16_t*>(t[j] + Tile<HD>::CODES + (at[j] * Tile<HD>::NG + pt.group) * 2) : 0u;
+    T* dst = reinterpret_cast<T*>(const_cast<void*>(r.p)) + seq * r.seq + row * r.row + pt.head * r.head +
+             pt.group * kGroup + 16 * pt.lane;
+    int at;
+    const uint8_t* t = place_of<HD>(a, pt, seq, row, &at);
+    uint2 c = make_uint2(0, 0);
+    uint32_t sc = 0;
+    if (t) {
+      c = *reinterpret_cast<const uint2*>(t + at * Tile<HD>::ROW + pt.group * (kGroup / 2) + 8 * pt.lane);
+      sc = *reinterpret_cast<const uint16_t*>(t + Tile<HD>::CODES + (at * Tile<HD>::NG + pt.group) * 2);
     }
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      if (row0 + j * tp >= a.rows) continue;
+    for (int h = 0; h < 2; ++h) {
       V8 x;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x.x[e] = value_of(c[j] >> (4 * e), __uint_as_float(sc[j] << 16));
-      write8(dst + (row0 + j * tp) * r.row, x);
+      for (int e = 0; e < 8; ++e) x.x[e] = value_of((h ? c.y : c.x) >> (4 * e), __uint_as_float(sc << 16));
+      write8(dst + 8 * h, x);
     }
   }
 }
@@ -232,34 +215,25 @@ int kv4_check_rows(const mk_kv4_rows* r, int dtype, const char* what) {
 }
 
 
-// Launch KERNEL<head_dim, element type, rows in flight>: two rows a thread once
-// that still gives every SM two blocks (7.1 us against 7.8 with one and 8.5 with
-// four, for 4096 tokens of 4 heads of 128), one below (a step of a few sequences
-// is bound by its chain of reads).
-#define MK_KV4_LAUNCH(KERNEL, C, HDIM, DT, ST, ...)                                                                        \
-  do {                                                                                                               \
-    const int parts_ = 16 * (HDIM / kGroup) * (C).n_kv_heads, tp_ = pass_rows(parts_, (C).rows);              \
-    const int threads_ = std::min(kThreadsKv, tp_ * parts_);                                                         \
-    const int c2_ = ((C).rows + 2 * tp_ - 1) / (2 * tp_), c1_ = ((C).rows + tp_ - 1) / tp_;                           \
-    if ((C).n_seqs * c2_ >= 304) MK_KV4_LAUNCH_N(KERNEL, 2, C, HDIM, DT, ST, __VA_ARGS__, tp_, c2_);                       \
-    else MK_KV4_LAUNCH_N(KERNEL, 1, C, HDIM, DT, ST, __VA_ARGS__, tp_, c1_);                                               \
-  } while (0)
-#define MK_KV4_LAUNCH_N(KERNEL, N, C, HDIM, DT, ST, A, K, V, TP, CH)                                                       \
-  do {                                                                                                               \
-    const int g_ = (C).n_seqs * CH;                                                                                  \
-    if (HDIM == 64 && DT == MK_F32) KERNEL<64, float, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);           \
-    else if (HDIM == 64) KERNEL<64, __nv_bfloat16, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);              \
-    else if (DT == MK_F32) KERNEL<128, float, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);                          \
-    else KERNEL<128, __nv_bfloat16, N><<<g_, threads_, 0, ST>>>(A, K, V, TP, CH);                                    \
+// Launch KERNEL<head_dim, element type>.
+#define MK_KV4_LAUNCH(KERNEL, C, HDIM, DT, ST, K, V)                                                     \
+  do {                                                                                                   \
+    const int parts_ = 2 * kLanes * (HDIM / kGroup) * (C).n_kv_heads, tp_ = pass_rows(parts_, (C).rows); \
+    const int threads_ = std::min(kThreadsKv, (tp_ * parts_ + 31) / 32 * 32);                            \
+    const int chunks_ = ((C).rows + tp_ - 1) / tp_, grid_ = (C).n_seqs * chunks_;                        \
+    if (HDIM == 64 && DT == MK_F32) KERNEL<64, float><<<grid_, threads_, 0, ST>>>(C, K, V, tp_, chunks_); \
+    else if (HDIM == 64) KERNEL<64, __nv_bfloat16><<<grid_, threads_, 0, ST>>>(C, K, V, tp_, chunks_);   \
+    else if (DT == MK_F32) KERNEL<128, float><<<grid_, threads_, 0, ST>>>(C, K, V, tp_, chunks_);        \
+    else KERNEL<128, __nv_bfloat16><<<grid_, threads_, 0, ST>>>(C, K, V, tp_, chunks_);                  \
   } while (0)
 
 int kv4_store(const Kv4Args& a, int head_dim, const Kv4Rows& k, const Kv4Rows& v, int dtype, cudaStream_t st) {
-  MK_KV4_LAUNCH(k_kv4_store, a, head_dim, dtype, st, a, k, v);
+  MK_KV4_LAUNCH(k_kv4_store, a, head_dim, dtype, st, k, v);
   return cuda_status("kv4 store");
 }
 
 int kv4_load(const Kv4Args& a, int head_dim, const Kv4Rows& k, const Kv4Rows& v, int dtype, cudaStream_t st) {
-  MK_KV4_LAUNCH(k_kv4_load, a, head_dim, dtype, st, a, k, v);
+  MK_KV4_LAUNCH(k_kv4_load, a, head_dim, dtype, st, k, v);
   return cuda_status("kv4 load");
 }
 
