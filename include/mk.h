@@ -439,7 +439,8 @@ MK_API int mk_static_bytes(const mk_model_desc* d, int32_t grid, int64_t* need_o
  * The pool, the table and the lengths belong to the caller and lie on the
  * current device.  The calls only enqueue on `stream`: no allocation, no
  * synchronisation, so they can be captured into a graph, which reads lengths,
- * table and n_new anew at every replay.
+ * table and n_new anew at every replay (whoever writes them orders that before or
+ * after the call; otherwise its results mean nothing).
  *
  * Sequence i of a call has lengths[i] positions, the row's own new ones among
  * them, position p in slot p % 128 of page table[i][p / 128].  Of the call's

@@ -123,6 +123,12 @@ struct Runs {
     t0 = max(0, in - kOver);
     t1 = max(0, out - kOver);
   }
+  __device__ __forceinline__ uint32_t steps(const AttArgs& p, int CT, int SP) const {  // of this run and all after it
+    uint32_t n = t1 - t0;
+    if (n)
+      for (Runs r = *this; r.next(p, CT, SP);) n += r.t1 - r.t0;
+    return n;
+  }
   __device__ __forceinline__ bool next(const AttArgs& p, int CT, int SP) {  // the next run; false: none is left
     for (;;) {
       if (pos >= hi) return false;

@@ -139,7 +139,10 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
   __shared__ unsigned long long list[kWindow];  // where the block's next steps lie (0: a page outside the pool)
   __shared__ uint32_t issued[R];              // 1 + the last step copied into each stage
   __shared__ float2 sm_ml[W][CT];  // a run's maximum and sum of each warp and column
-  __shared__ Runs s_run;  // the block's first run
+  // The block's run and its number of steps, found by one thread: all warps pass the
+  // same barriers even where someone writes the lengths while the call runs.
+  __shared__ Runs s_run;
+  __shared__ uint32_t s_steps;
   __shared__ volatile int give_up;
   // cluster: the partial results of the columns that this block joins, column c
   // (joined by block c mod cluster) of block r in [r][c / cluster][HD | M, sum]
@@ -229,16 +232,21 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     run.t0 = nt * rank >> p.cluster_log;
     run.t1 = nt * (rank + 1) >> p.cluster_log;
     pages[tid] = page;
+    if (tid == 0) {
+      s_run = run;
+      s_steps = run.t1 - run.t0;
+    }
   } else if (w == 0) {  // this block's share of all tiles
     const Runs r = first_run(p, CT, SP, lane);
-    if (lane == 0) s_run = r;
+    if (lane == 0) {
+      s_run = r;
+      s_steps = r.steps(p, CT, SP);
+    }
   }
   __syncthreads();
-  if (!p.cluster) run = s_run;
+  run = s_run;
   const Runs mine = run;
-  uint32_t n_steps = run.t1 - run.t0;
-  if (!p.cluster && n_steps)
-    for (Runs r = mine; r.next(p, CT, SP);) n_steps += r.t1 - r.t0;
+  const uint32_t n_steps = s_steps;
   uint32_t k = 0;  // steps done
   // Address of the block's step i, looked up by one thread (all of a window at once).
   auto look_up = [&](uint32_t i) {
@@ -260,7 +268,10 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
       uint32_t before = 0;
       while (i >= before + (r.t1 - r.t0)) {
         before += r.t1 - r.t0;
-        if (!r.next(p, CT, SP)) return;
+        if (!r.next(p, CT, SP)) {
+          list[i % kWindow] = 0;
+          return;
+        }
       }
       r.t0 += i - before;
       pg = page_of(p.a, p.n_ctiles == 1 ? r.e : r.e / p.n_ctiles, r.t0 * SP);
@@ -290,7 +301,7 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
   if (p.cluster > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 
   // a cluster's block has one run
-  for (bool more = n_steps > 0; more; more = !p.cluster && run.next(p, CT, SP)) {
+  for (bool more = n_steps > 0; more;) {
     const int seq = p.n_ctiles == 1 ? run.e : run.e / p.n_ctiles, j = run.e - seq * p.n_ctiles;
     int len, nn;
     seq_extent(p.a, seq, len, nn);
@@ -619,9 +630,20 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
     if (!p.cluster && tid == 0 && run.t0 == 0)
       p.item[(size_t)run.e * p.a.n_kv_heads + run.head] =
           make_longlong2(whole ? -1 : run.base + (long long)run.head * (run.nt + kOver), blockIdx.x);
-    if (k < n_steps) asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");  // the buffers are used again
+    more = k < n_steps;
+    if (more) {
+      if (tid == 0) {
+        Runs r = run;
+        if (!r.next(p, CT, SP)) r.t0 = r.t1 = 0;
+        s_run = r;
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");  // the buffers are used again
+      run = s_run;
+      run.t1 = min(run.t1, run.t0 + (int)(n_steps - k));
+      more = run.t1 > run.t0;
+    }
   }
-  if (give_up && tid == 0) {  // copies in flight land before the block ends
+  if ((give_up || k < n_steps) && tid == 0) {  // copies in flight land before the block ends
     int none = 0;
     for (int i = 0; i < R; ++i)
       if (issued[i]) bar_wait_long(smem_addr(&full[i]), ((issued[i] - 1) / R) & 1, &none, nullptr);

@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(Wide<HD, T, TB>::THREADS, Wide<HD, T, TB>::BLO
   __shared__ int note[kList];
   __shared__ StepSays says[4];
   __shared__ uint32_t tm_base;
-  __shared__ Runs s_run;
+  __shared__ Runs s_run;       // the block's first run and number of steps, the same for all warps
+  __shared__ uint32_t s_steps;  // (should someone write the lengths while the call runs)
   __shared__ volatile int give_up;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   uint8_t* q_op = sm;
@@ -177,7 +178,10 @@ __global__ void __launch_bounds__(Wide<HD, T, TB>::THREADS, Wide<HD, T, TB>::BLO
   }
   if (w == 0) {
     const Runs r = first_run(p, CT, SP, lane);
-    if (lane == 0) s_run = r;
+    if (lane == 0) {
+      s_run = r;
+      s_steps = r.steps(p, CT, SP);
+    }
   }
   if (w == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tm_base)), "n"(W::TM * TB)
@@ -190,9 +194,7 @@ __global__ void __launch_bounds__(Wide<HD, T, TB>::THREADS, Wide<HD, T, TB>::BLO
   const uint32_t tm = tm_base;  // tile t: S at 256 t, O at 256 t + 128
   Runs run = s_run;
   const Runs mine = run;
-  uint32_t n_steps = run.t1 - run.t0;
-  if (n_steps)
-    for (Runs r = mine; r.next(p, CT, SP);) n_steps += r.t1 - r.t0;
+  const uint32_t n_steps = s_steps;
 
   if (w >= UW) {  // ---- unpacking, and the products (the warps take turns)
     const int u = tid - 32 * UW;
@@ -201,7 +203,11 @@ __global__ void __launch_bounds__(Wide<HD, T, TB>::THREADS, Wide<HD, T, TB>::BLO
       uint32_t before = 0;
       while (i >= before + (r.t1 - r.t0)) {
         before += r.t1 - r.t0;
-        if (!r.next(p, CT, SP)) return;
+        if (!r.next(p, CT, SP)) {
+          list[i % kList] = 0;
+          note[i % kList] = 0;
+          return;
+        }
       }
       const int t = r.t0 + (int)(i - before), seq = p.n_ctiles == 1 ? r.e : r.e / p.n_ctiles;
       int len, nn;
