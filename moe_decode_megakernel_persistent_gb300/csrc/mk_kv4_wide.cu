@@ -4,16 +4,19 @@
 // mk_kv4_attention.cu; what differs is where the scales go and who does what.
 //
 //   S = Q K^T   128 columns x 64 positions.  K = code x scale in fp16: 3 bits x 8
-//               bits are exact in its 11, the code as the subnormal +-m 2^-20, the
-//               scale times a power of two of the tile (its largest scale maps to
-//               2^14..2^15; one below 2^-11 of that loses low bits, at most 2^-21 of the
-//               tile's largest value).  Q is fp16 times a power of two of the row (a
-//               bf16 value is exact down to 2^-31 of its row's largest).  The powers
-//               multiply the fp32 scores.
+//               bits are exact in its 11.  The code is the subnormal +-m 2^-20 times 2^15,
+//               the scale is times a power of two of the tile (its largest maps to
+//               2^14..2^15), so that all is exact down to a scale of 2^-26 of the tile's
+//               largest: positions that a row does not see, or gives no weight, may be so much
+//               larger than those that it does.  (A smaller scale's values are rounded to
+//               2^-25, at most 2^-36 of the tile's largest value.  With the codes left
+//               subnormal that was 2^-21, and a hidden outlier of 2^12 showed.)  Q is fp16
+//               times a power of two of the row (a bf16 value is exact down to 2^-31 of
+//               its row's largest).  The powers multiply the fp32 scores.
 //   O += P V    P = weights in fp16 (rounded by 2^-11, where the output is rounded
 //               by 2^-8) over S's place in TMEM; V as K, its power following the largest
-//               scale of the run with 2^3 of room (so that a value loses at most 2^-18
-//               of the largest), O rescaled when it moves.
+//               scale of the run with 2^3 of room (exact down to 2^-23 of the largest, else
+//               rounded by at most 2^-33 of it), O rescaled when it moves.
 // So the 128 x 64 scores of a step need no scale of their own, and one pass: 64
 // scores a thread in registers, their maximum, one exponential each.  (With the
 // scales applied to scores and weights, as the narrow kernel does, a step took
@@ -32,7 +35,7 @@
 //
 // fp32 rows: q and the weights are two fp16 parts each (22 bits), the products run on
 // both, and V has no room but rescales O each time its largest scale passes a power of two
-// (a value loses at most 2^-21 of the largest).  Their q fills the shared memory that a second
+// (exact down to 2^-26 of the largest, else rounded by at most 2^-36 of it).  Their q fills the shared memory that a second
 // block would need, so a block has two tiles of 128 columns, which share the unpacked operands.  (For
 // bf16 rows that is no faster: 115 us against 113.)
 //
@@ -110,16 +113,18 @@ __device__ __forceinline__ void tm_store16(uint32_t at, const uint32_t (&x)[16])
 }
 __device__ __forceinline__ void tm_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ uint32_t mul2h(uint32_t a, uint32_t b) {  // f16x2
+// Two codes as subnormals, times 2^15 (+-m 2^-5, exactly), times b.
+__device__ __forceinline__ uint32_t scaled(uint32_t a, uint32_t b) {  // f16x2
   uint32_t y;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  asm("{ .reg .b32 t; mul.rn.f16x2 t, %1, %3; mul.rn.f16x2 %0, t, %2; }" : "=r"(y) : "r"(a), "r"(b), "r"(0x78007800));
   return y;
 }
+constexpr float kUnit = 32.f;  // an operand value is code x scale / kUnit
 // Four bytes of codes times the scale pair h as eight operand values, dimensions
 // 0 2 1 3 4 6 5 7.
 __device__ __forceinline__ uint4 unpack(uint32_t w, uint32_t h) {
   const uint32_t x = __byte_perm(w, 0, 0x1100), y = __byte_perm(w, 0, 0x3322);
-  return make_uint4(mul2h((x << 4) & kNib, h), mul2h(x & kNib, h), mul2h((y << 4) & kNib, h), mul2h(y & kNib, h));
+  return make_uint4(scaled((x << 4) & kNib, h), scaled(x & kNib, h), scaled((y << 4) & kNib, h), scaled(y & kNib, h));
 }
 // 2^n, n held to fp32's normal range.
 __device__ __forceinline__ float power(int n) { return __uint_as_float((uint32_t)(min(max(n, -126), 127) + 127) << 23); }
@@ -132,7 +137,7 @@ constexpr float kRoom = 6.f;    // the weights are at most 2^(kLazy + kRoom) in 
 // What the unpacking warps say of a step.
 struct StepSays {
   float k_mul;       // what the scores are times, but for the row's power
-  float v_exp;       // V's power of two: the operand is V 2^(v_exp - 20)
+  float v_exp;       // V's power of two: the operand is V 2^v_exp / kUnit
   uint32_t bad[4];   // V scales that are no numbers: [group][positions 0..31, 32..63]
 };
 
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(Wide<HD, T, TB>::THREADS, Wide<HD, T, TB>::BLO
             if (lane == 0) says[i & 3].bad[2 * g + h] = bad;
           }
         if (lane == 0) {
-          says[i & 3].k_mul = power(20 - nk);
+          says[i & 3].k_mul = kUnit * power(-nk);
           says[i & 3].v_exp = (float)nv;
         }
       }
@@ -557,7 +562,7 @@ __global__ void __launch_bounds__(Wide<HD, T, TB>::THREADS, Wide<HD, T, TB>::BLO
       bar_wait(smem_addr(&pv_done[(k - 1) & 1]), ((k - 1) >> 1) & 1, &give_up, p.a.status);
       after_sync();
       const bool whole = run.t0 == 0 && run.t1 == run.nt;
-      const float undo = kCode * exp2f(-e), M = m - kRoom;
+      const float undo = kUnit * exp2f(-e), M = m - kRoom;
       const float f = whole ? (l == 0.f ? 0.f : undo / l) : undo;
       float* part = p.part + ((size_t)part_slot(blockIdx.x, run.t0) * CT + tid) * (HD + 4);
       T* dst = reinterpret_cast<T*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row + hd * p.out.head;
