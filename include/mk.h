@@ -500,7 +500,8 @@ MK_API int mk_kv4_load(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4
  * length are never used, whatever their slots hold.  out must not overlap q, the
  * pool or the workspace.  |scale| < 1e18; magnitudes of q and V up to 2^50 are kept whole,
  * terms weight * value below 2^-60 may be lost.  Weights are rounded by 2^-11 for bf16
- * rows and 2^-22 for fp32 rows, sums are fp32.  From 33 query columns (rows x
+ * rows and 2^-22 for fp32 rows, a term weight * value by at most 2^-27 of the row's largest weight
+ * times the largest V that the row sees; sums are fp32.  From 33 query columns (rows x
  * n_heads / n_kv_heads) of bf16 and 81 of fp32 on, an fp32 q is rounded by 2^-22 too, a K
  * value may lose 2^-36 of the largest one of its 64 positions and head, a V value 2^-33 (bf16
  * rows) or 2^-36 (fp32 rows) of the largest one of its sequence and head.

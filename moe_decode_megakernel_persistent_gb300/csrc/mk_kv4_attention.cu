@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
         float move = 1.f;
+        const int old = (int)(__float_as_uint(cap) >> 23);  // the cap's exponent, 0: none yet
         if (top > cap) {  // the next power of two, and 2^3 of room
           const int e = min(max((int)(__float_as_uint(top) >> 23) + 4, 8), 254);
           const float mul = __uint_as_float((uint32_t)(260 - e) << 23);
@@ -489,6 +490,46 @@ __global__ void __launch_bounds__(32 * W, B) k_kv4_attention(const __grid_consta
               for (int r = 0; r < 2; ++r)
                 if (d[u][nt][x + 2 * r] != -INFINITY) d[u][nt][x + 2 * r] = fmaf(v[u][nt][x + 2 * r], p.c, -t);
           }
+        const int now = (int)(__float_as_uint(cap) >> 23);
+        if constexpr (CUT) {
+          // A column that sees the last of its positions here must not pay for a cap that
+          // moved for one it does not see (its terms would fall below fp16's range): its
+          // maximum goes down by what the cap went up beyond its own, its weights and sums up.
+          if (now != old && any != all) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                float seen = 0.f;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int h = 0; h < NG; ++h)
+                      if (p0 + 16 * u + g + 8 * r < lim[nt][x]) seen = fmaxf(seen, vs[u][r][h]);
+#pragma unroll
+                for (int y = 4; y < 32; y <<= 1) seen = fmaxf(seen, __shfl_xor_sync(0xffffffffu, seen, y));
+                const int own = max(old, seen > 0.f ? min(max((int)(__float_as_uint(seen) >> 23) + 4, 8), 254) : 0);
+                const int up = own && lim[nt][x] < p0 + 16 * U ? min(now - own, 90) : 0;
+                const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+                m[nt][x] -= (float)up;
+                l[nt][x] *= f;
+#pragma unroll
+                for (int h = 0; h < NG; ++h)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    o[nt][h][i][x] *= f;
+                    o[nt][h][i][x + 2] *= f;
+                  }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r)
+                    if (d[u][nt][x + 2 * r] != -INFINITY) d[u][nt][x + 2 * r] = fmaf(v[u][nt][x + 2 * r], p.c, -m[nt][x]);
+              }
+          }
+        }
       }
       // weights times V's scales, as B fragments
       uint2 wf[U][S::WP][NT][NG];

@@ -26,7 +26,8 @@ def check_rows(q, kc, vc, out, lse, first, lo, hi, scale):
 
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("dtype,rows,H,G", [
-    (BF, 20, 4, 1), (BF, 33, 4, 4), (BF, 40, 4, 1), (F32, 40, 4, 1), (BF, 130, 2, 1), (F32, 130, 2, 1)])   # tiles of 128 columns
+    (BF, 20, 4, 1), (BF, 33, 4, 4), (BF, 40, 4, 1), (F32, 40, 4, 1), (BF, 130, 2, 1), (F32, 130, 2, 1),   # tiles of 128 columns
+    *((t, *c) for t in (BF, F32) for c in ((2, 1, 1), (5, 4, 1), (8, 8, 2))), (F32, 20, 4, 1), (F32, 33, 4, 4)])
 @pytest.mark.parametrize("power", [8, 14, 20])
 @pytest.mark.parametrize("which", ["k", "v", "both"])
 def test_rows_that_do_not_see_an_outlier(gpu_lib, dtype, hd, rows, H, G, power, which):
@@ -50,7 +51,7 @@ def test_rows_that_do_not_see_an_outlier(gpu_lib, dtype, hd, rows, H, G, power, 
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("rows", [40])
+@pytest.mark.parametrize("rows", [4, 40])
 def test_growing_values_stay_with_who_sees_them(gpu_lib, dtype, rows):
     """V doubles with every position that the call adds, so that each row sees a larger one than the row before."""
     n, hd, H = 300, 64, 4
