@@ -17,6 +17,8 @@ namespace {
 thread_local std::string g_err;
 
 int fail(int code, const std::string& msg) {
+  // the runtime keeps a failed call's error until it is read, and the next launch's check would take it for its own
+  if (code == MK_ERR_CUDA) cudaGetLastError();
   g_err = msg;
   return code;
 }

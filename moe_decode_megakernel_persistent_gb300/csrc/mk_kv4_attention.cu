@@ -956,7 +956,8 @@ int clusters_at_once(const Plan& pl, int head_dim, int n) {
   if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) count = known[dev][pl.id][log].load();
   if (count) return count - 1;
   count = pl.blocks * sm_count() / n;
-  if (allow_smem(pl) == cudaSuccess) {
+  cudaError_t e = allow_smem(pl);
+  if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -968,12 +969,13 @@ int clusters_at_once(const Plan& pl, int head_dim, int n) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int c = 0;
-    if (cudaOccupancyMaxActiveClusters(&c, pl.main, &cfg) == cudaSuccess) {
+    e = cudaOccupancyMaxActiveClusters(&c, pl.main, &cfg);
+    if (e == cudaSuccess) {
       count = c;
       if (dev < 64) known[dev][pl.id][log].store(count + 1);
     }
   }
-  cudaGetLastError();
+  if (e != cudaSuccess) cudaGetLastError();  // this query's own, no one else's
   return count;
 }
 
