@@ -39,7 +39,6 @@ namespace mk {
 
 struct PrefillWork {
   cublasHandle_t blas = nullptr;
-  int max_m = 0;
   size_t a_elems = 0, c_elems = 0, wb_elems = 0;
   float* X = nullptr;        // [M][H] residual
   float* Hr = nullptr;       // [M][H] residual after attention
@@ -632,6 +631,81 @@ void prefill_free(PrefillWork* w) {
   delete w;
 }
 
+namespace {
+
+// The chunks' workspace (four_bit: with the 4-bit cache's parts).
+int fill_work(PrefillWork* w, const Dims& d, bool four_bit, int max_pages_per_seq) {
+  if (cublasCreate(&w->blas) != CUBLAS_STATUS_SUCCESS) {
+    w->blas = nullptr;
+    return host_fail(MK_ERR_CUDA, "cublasCreate failed");
+  }
+  const size_t MM = kMaxPrefill, H = d.H, QD = d.QD, E = d.E, K = d.K, ent = MM * K;
+  const size_t kmax = std::max({H, QD, (size_t)d.FD, (size_t)d.FE});
+  w->a_elems = std::max({ent * H, MM * kmax, ent * (size_t)d.FE});
+  w->c_elems = std::max({MM * d.NQKV, MM * 2 * (size_t)d.FD, ent * 2 * (size_t)d.FE, MM * H, MM * E});
+  w->wb_elems = d.wdtype == MK_INT4_G64 || d.xdtype == MK_INT3_G64
+                    ? std::max({E * 2 * d.FE * H, E * H * d.FE, 2 * (size_t)d.FD * H, H * (size_t)d.FD,
+                                (size_t)d.NQKV * H, H * QD})
+                    : 0;
+  cudaError_t e = cudaSuccess;
+  auto alloc = [&](void** p, size_t bytes) {
+    if (e == cudaSuccess && bytes) e = cudaMalloc(p, bytes);
+  };
+  alloc((void**)&w->X, 4 * MM * H);
+  alloc((void**)&w->Hr, 4 * MM * H);
+  alloc((void**)&w->Q, 4 * MM * QD);
+  alloc((void**)&w->O, 4 * MM * QD);
+  alloc(&w->A, 4 * w->a_elems);
+  alloc((void**)&w->C, 4 * w->c_elems);
+  alloc((void**)&w->D, 4 * ent * H);
+  alloc((void**)&w->Wb, 2 * w->wb_elems);
+  alloc((void**)&w->Z, 4 * MM * H);
+  alloc((void**)&w->logits, 4 * MM * E);
+  alloc((void**)&w->ids, 4 * ent);
+  alloc((void**)&w->wts, 4 * ent);
+  alloc((void**)&w->cnt, 4 * (2 * E + 1));
+  alloc((void**)&w->ent, 4 * ent);
+  alloc((void**)&w->pos_of, 4 * ent);
+  alloc((void**)&w->lm_v, 4 * kLmBlocks);
+  alloc((void**)&w->lm_i, 4 * kLmBlocks);
+  if (four_bit) {
+    // the attention's workspace for any chunk: the largest one's
+    Kv4Args k{};
+    k.n_kv_heads = d.NKV;
+    k.n_seqs = 1;
+    k.max_pages = max_pages_per_seq;
+    for (int rows : {kMaxBatch + 1, 32, 64, 128, 512, kMaxPrefill}) {
+      size_t b = 0;
+      k.rows = rows;
+      if (!kv4_attention_bytes(k, d.HD, d.NH, MK_F32, &b))
+        return host_fail(MK_ERR_UNSUPPORTED, "a chunk's attention over the 4-bit cache is too large");
+      w->kv4_ws_bytes = std::max(w->kv4_ws_bytes, b);
+    }
+    alloc((void**)&w->kv, 2 * MM * 2 * d.KD);
+    alloc(&w->kv4_ws, w->kv4_ws_bytes);
+  }
+  if (e != cudaSuccess) return host_fail(MK_ERR_CUDA, (std::string("prefill workspace: ") + cudaGetErrorString(e)).c_str());
+  return MK_OK;
+}
+
+// *out is set once all of it is there: a chunk after a failed one starts over.
+int make_work(const Dims& d, bool four_bit, int max_pages_per_seq, PrefillWork** out) {
+  PrefillWork* w = nullptr;
+  int r;
+  try {
+    w = new PrefillWork();
+    w->cnt_host.resize(2 * (size_t)d.E + 1);
+    r = fill_work(w, d, four_bit, max_pages_per_seq);
+  } catch (...) {
+    r = host_fail(MK_ERR_INVALID_ARG, "prefill workspace: no host memory");
+  }
+  if (r) prefill_free(w);
+  else *out = w;
+  return r;
+}
+
+}  // namespace
+
 int prefill_run(PrefillWork** pw, const PrefillArgs& a, cudaStream_t st) { return prefill_run(pw, a, PrefillKv4(), st); }
 
 int prefill_run(PrefillWork** pw, const PrefillArgs& a, const PrefillKv4& kv4, cudaStream_t st) {
@@ -647,62 +721,8 @@ int prefill_run(PrefillWork** pw, const PrefillArgs& a, const PrefillKv4& kv4, c
   const int M = a.n;
   if (M < 1 || M > kMaxPrefill) return host_fail(MK_ERR_INVALID_ARG, "prefill chunk of 1..4096 positions");
   // ---- workspace, made on first use and kept by the context
-  if (!*pw) {
-    PrefillWork* w = new PrefillWork();
-    *pw = w;
-    if (cublasCreate(&w->blas) != CUBLAS_STATUS_SUCCESS) {
-      w->blas = nullptr;
-      return host_fail(MK_ERR_CUDA, "cublasCreate failed");
-    }
-    const size_t MM = kMaxPrefill, H = d.H, QD = d.QD, E = d.E, K = d.K, ent = MM * K;
-    const size_t kmax = std::max({H, QD, (size_t)d.FD, (size_t)d.FE});
-    w->a_elems = std::max({ent * H, MM * kmax, ent * (size_t)d.FE});
-    w->c_elems = std::max({MM * d.NQKV, MM * 2 * (size_t)d.FD, ent * 2 * (size_t)d.FE, MM * H, MM * E});
-    w->wb_elems = d.wdtype == MK_INT4_G64 || d.xdtype == MK_INT3_G64
-                      ? std::max({E * 2 * d.FE * H, E * H * d.FE, 2 * (size_t)d.FD * H, H * (size_t)d.FD,
-                                  (size_t)d.NQKV * H, H * QD})
-                      : 0;
-    cudaError_t e = cudaSuccess;
-    auto alloc = [&](void** p, size_t bytes) {
-      if (e == cudaSuccess && bytes) e = cudaMalloc(p, bytes);
-    };
-    alloc((void**)&w->X, 4 * MM * H);
-    alloc((void**)&w->Hr, 4 * MM * H);
-    alloc((void**)&w->Q, 4 * MM * QD);
-    alloc((void**)&w->O, 4 * MM * QD);
-    alloc(&w->A, 4 * w->a_elems);
-    alloc((void**)&w->C, 4 * w->c_elems);
-    alloc((void**)&w->D, 4 * ent * H);
-    alloc((void**)&w->Wb, 2 * w->wb_elems);
-    alloc((void**)&w->Z, 4 * MM * H);
-    alloc((void**)&w->logits, 4 * MM * E);
-    alloc((void**)&w->ids, 4 * ent);
-    alloc((void**)&w->wts, 4 * ent);
-    alloc((void**)&w->cnt, 4 * (2 * E + 1));
-    alloc((void**)&w->ent, 4 * ent);
-    alloc((void**)&w->pos_of, 4 * ent);
-    alloc((void**)&w->lm_v, 4 * kLmBlocks);
-    alloc((void**)&w->lm_i, 4 * kLmBlocks);
-    if (kv4.pool) {
-      // the attention's workspace for any chunk: the largest one's
-      Kv4Args k{};
-      k.n_kv_heads = d.NKV;
-      k.n_seqs = 1;
-      k.max_pages = a.max_pages_per_seq;
-      for (int rows : {kMaxBatch + 1, 32, 64, 128, 512, kMaxPrefill}) {
-        size_t b = 0;
-        k.rows = rows;
-        if (!kv4_attention_bytes(k, d.HD, d.NH, MK_F32, &b))
-          return host_fail(MK_ERR_UNSUPPORTED, "a chunk's attention over the 4-bit cache is too large");
-        w->kv4_ws_bytes = std::max(w->kv4_ws_bytes, b);
-      }
-      alloc((void**)&w->kv, 2 * MM * 2 * d.KD);
-      alloc(&w->kv4_ws, w->kv4_ws_bytes);
-    }
-    if (e != cudaSuccess) return host_fail(MK_ERR_CUDA, (std::string("prefill workspace: ") + cudaGetErrorString(e)).c_str());
-    w->max_m = kMaxPrefill;
-    w->cnt_host.resize(2 * E + 1);
-  }
+  if (!*pw)
+    if (int r = make_work(d, kv4.pool != nullptr, a.max_pages_per_seq, pw)) return r;
   PrefillWork& w = **pw;
   if (int r = blas_err(cublasSetStream(w.blas, st), "cublasSetStream")) return r;
   const size_t lo = w.a_elems;  // bf16 lo parts follow the hi parts (the buffer holds 4 bytes per element)
@@ -729,7 +749,7 @@ int prefill_run(PrefillWork** pw, const PrefillArgs& a, const PrefillKv4& kv4, c
     if (int r = gemm(w, d, M, d.NQKV, d.H, W, d.H, w.A, lo, w.C, d.NQKV)) return r;
     k_qkv_epi<<<grid_for((long long)M * d.NQKV / 2), TB, 0, st>>>(w.C, d.NQKV, d.NH, d.NKV, d.HD, a.rope, a.start, M,
                                                                    w.Q, a.kv, a.block_table, a.slot,
-                                                                   a.max_pages_per_seq, a.n_pages, l, a.err, w.kv);
+                                                                   a.max_pages_per_seq, a.n_pages, l, a.err, kv4.pool ? w.kv : nullptr);
     dim3 ag((M + 15) / 16, d.NKV);
     const float scale = 1.f / sqrtf((float)d.HD);
     if (kv4.pool) {
