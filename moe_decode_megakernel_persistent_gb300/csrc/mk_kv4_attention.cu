@@ -991,7 +991,8 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
   pl->n_ctiles = (int)ct;
   pl->n_entries = (int)entries;
   pl->items = (int)items;
-  const long long room = std::min(pl->blocks * sm_count(), kMaxBlocks);  // blocks that run at once
+  const int sms = sm_count();
+  const long long room = std::min(pl->blocks * sms, kMaxBlocks);  // blocks that run at once
   pl->cluster = 0;
   // Short work: an item is a cluster of up to 16 blocks, while all clusters run at
   // once (16 sequences of 256 to 8448 positions with clusters of 8: 15.7 us; where a few had to wait
@@ -1010,15 +1011,15 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
   }
   pl->grid = (int)std::min<long long>(room, items * most);
   // The join.  Up to ten columns an SM are a block each, with as many warps as the item has
-  // parts (about grid / items), and 12 parts in flight in each warp where blocks are few
+  // parts (about grid / items), and 12 parts in flight in each warp where blocks are few and parts many
   // (131071 positions, 152 parts: 23.8 us; 26.5 with 4, whose fewer registers serve more
-  // blocks).  More columns are a warp each, 8 or 16 a block (128 rows at 8022 positions, 2048
+  // blocks).  More columns are a warp each, 8 a block up to 54 an SM, then 16 (128 rows at 8022 positions, 2048
   // columns: 34.6 us, 49 by blocks; 16 sequences with up to 5 drafted rows, 1280: 30.9 by warps, 29.9).
   const long long all_cols = items * std::min<long long>(cols, pl->CT);
-  pl->join_cols = all_cols <= 1520 ? 1 : all_cols <= 8192 ? 8 : 16;
+  pl->join_cols = all_cols <= 10 * sms ? 1 : all_cols <= 54 * sms ? 8 : 16;
   int nw = 2;
   while (nw < 16 && nw * 2 * items <= pl->grid) nw *= 2;
-  pl->join_many = pl->grid / 64 >= items && all_cols <= 152;
+  pl->join_many = pl->grid / 64 >= items && all_cols <= sms;  // 64 parts an item and more, a block an SM at most
   pl->join_threads = 32 * (pl->join_cols > 1 ? 8 : nw);
   pl->item_off = 16;
   pl->part_off = pl->item_off + (size_t)items * sizeof(longlong2);
