@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -107,6 +108,13 @@ const at::Tensor& heads(PyObject* o, const char* what) {
   return t;
 }
 
+// The calls record nothing for autograd: a tensor that would need it is refused
+// rather than its gradient lost.
+void no_gradient(const at::Tensor& t, const char* what) {
+  if ((t.requires_grad() && c10::GradMode::is_enabled()) || t._fw_grad(0).defined())
+    refuse(std::string(what) + " requires a gradient, which this call has none of (torch.no_grad() or detach())");
+}
+
 // Whether the spans of two tensors' elements meet.
 bool overlap(const at::Tensor& x, const at::Tensor& y) {
   const at::Tensor* t[2] = {&x, &y};
@@ -152,6 +160,8 @@ PyObject* py_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
   MK_BEGIN
   count(n, 7);
   const at::Tensor &pool = tensor(a[0], "pool"), &k = heads(a[3], "k"), &v = heads(a[4], "v");
+  no_gradient(k, "k");
+  no_gradient(v, "v");
   const mk_kv4_cache c = cache_of(pool, a[1], a[2], a[5], a[6], k.size(1), k.size(3));
   const int64_t sizes[4] = {c.n_seqs, c.rows, c.n_kv_heads, c.head_dim};
   const mk_kv4_rows kr = rows_of(k, sizes, k.scalar_type(), pool.device(), "k");
@@ -187,6 +197,8 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   MK_BEGIN
   count(n, 9);
   const at::Tensor &q = heads(a[0], "q"), &pool = tensor(a[1], "pool");
+  no_gradient(q, "q");
+  if (a[6] != Py_None) no_gradient(tensor(a[6], "out"), "out");
   const mk_kv4_cache c = cache_of(pool, a[2], a[3], a[4], a[8], q.size(1), q.size(3));
   const int64_t sizes[4] = {c.n_seqs, c.rows, q.size(2), c.head_dim};
   const at::ScalarType type = q.scalar_type();
@@ -249,6 +261,7 @@ PyObject* py_page_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
   MK_BEGIN
   count(n, 3);
   const at::Tensor& pool = tensor(a[0], "pool");
+  no_gradient(pool, "pool");
   if (!pool.is_cuda() || pool.dim() < 3 || !pool.is_contiguous())
     refuse("pool must be a contiguous CUDA tensor [n_layers, n_pages, ...]");
   if (pool.size(0) == 0 || pool.size(1) == 0) refuse("pool has no page");

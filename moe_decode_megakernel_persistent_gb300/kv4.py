@@ -14,6 +14,9 @@ is done.  They can be captured into a CUDA graph, which reads table, lengths and
 n_new anew at every replay.  A length, n_new or page outside its range is
 reported in `status` (a zeroed int32 CUDA tensor of one element) as
 MK_ERR_DEVICE_INDEX and never read or written past.
+
+They have no gradient: a q, k, v or out that requires one is refused (call them
+under torch.no_grad(), or detach the tensor).
 """
 from __future__ import annotations
 

@@ -12,5 +12,6 @@ def copy(pool: torch.Tensor, src, dst):
     tensor [n_layers, n_pages, ...] of any dtype whose pages are multiples of
     16 bytes.  src, dst: host lists of the same length; destinations are
     distinct and none is a source (the moves run at once).  Runs on the current
-    stream of the pool's device; a captured graph repeats these very moves."""
+    stream of the pool's device; a captured graph repeats these very moves.  A pool
+    that requires a gradient is refused."""
     L.torch_module().page_copy(pool, src, dst)
