@@ -2,13 +2,16 @@
 the Python module _torch (tensor calls on it) with the host compiler.
 
 The translation units compile in parallel (the decode kernel's file once
-per group of its instantiations, MK_KERNEL_PART 0..3); the shared object
-lands next to this file.  Rebuilds only when a
-source or header is newer than the library.
+per group of its instantiations, MK_KERNEL_PART 0..3); the shared objects
+land next to this file.  Rebuilds only what is older than its sources, the
+module also when another torch or Python is installed than it was built for.
+libmk.so needs nvcc alone: it is in place whatever becomes of the module,
+which is left out where there is no torch.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -37,18 +40,46 @@ def _nvcc() -> str:
     return "nvcc"
 
 
-def _inputs():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "mk.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+MODULE_SOURCE = "mk_torch.cpp"
+
+
+def _inputs(module: bool):
+    files = [MODULE_SOURCE] if module else [f for f in os.listdir(CSRC) if f != MODULE_SOURCE]
+    return [os.path.join(CSRC, f) for f in files] + [os.path.join(INCLUDE, "mk.h"), os.path.abspath(__file__)]
+
+
+def _built_for():
+    """What the module is compiled against: this Python and the installed torch; None without one."""
+    try:
+        return f"{sys.implementation.cache_tag} torch {importlib.metadata.version('torch')}"
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+def _stamp() -> str:
+    return os.path.join(BUILD, "mk_torch.for")
+
+
+def _newer(path: str, files) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in files)
+
+
+def _lib_current() -> bool:
+    return _newer(LIB, _inputs(False))
+
+
+def _module_current() -> bool:
+    built_for = _built_for()
+    if built_for is None:
+        return True  # there is none to build
+    if not _newer(MODULE, _inputs(True)) or not os.path.exists(_stamp()):
+        return False
+    with open(_stamp()) as f:
+        return f.read() == built_for
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MODULE):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _lib_current() and _module_current()
 
 
 def _module_commands(obj: str, out: str) -> list:
@@ -63,7 +94,7 @@ def _module_commands(obj: str, out: str) -> list:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
     return [[cxx, "-O2", "-std=c++17", "-fPIC", abi, *inc, "-c", os.path.join(CSRC, "mk_torch.cpp"), "-o", obj],
-            [cxx, "-shared", obj, "-o", out, "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + libs,
+            [cxx, "-shared", obj, "-o", out, "-L" + os.path.dirname(LIB), "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + libs,
              "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda"]]
 
 
@@ -93,24 +124,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"{what} failed:\n{r.stderr[-6000:]}")
 
-    mod_tmp = MODULE + ".tmp"
-    mod_compile, mod_link = _module_commands(os.path.join(BUILD, "mk_torch.o"), mod_tmp)
-    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        module = ex.submit(run, mod_compile, "the Python module's compilation")
-        objs = list(ex.map(compile_one, SOURCES))
-        module.result()
-    tmp = LIB + ".tmp"
-    # cuBLAS (the chunked prefill's GEMMs) is found through the toolkit's
-    # library directory
-    cudalib = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "lib64")
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs, "-lcublas",
-           "-Xlinker", "-rpath=" + cudalib]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
-    os.replace(tmp, LIB)
-    run(mod_link, "the Python module's link")
-    os.replace(mod_tmp, MODULE)
+    def build_lib():
+        with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+            objs = list(ex.map(compile_one, SOURCES))
+        # cuBLAS (the chunked prefill's GEMMs) is found through the toolkit's
+        # library directory
+        cudalib = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "lib64")
+        run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", LIB + ".tmp", *objs, "-lcublas",
+             "-Xlinker", "-rpath=" + cudalib], "link")
+        os.replace(LIB + ".tmp", LIB)
+
+    def compile_module():
+        commands = _module_commands(os.path.join(BUILD, "mk_torch.o"), MODULE + ".tmp")
+        run(commands[0], "the Python module's compilation")
+        return commands[1]
+
+    with cf.ThreadPoolExecutor(1) as ex:
+        module = ex.submit(compile_module) if _built_for() and (force or not _module_current()) else None
+        if force or not _lib_current():
+            build_lib()
+        if module:
+            run(module.result(), "the Python module's link")
+            os.replace(MODULE + ".tmp", MODULE)
+            with open(_stamp(), "w") as f:
+                f.write(_built_for())
     return LIB
 
 

@@ -154,7 +154,11 @@ def torch_module():
         load()
         import torch  # noqa: F401  (the module is linked against its libraries)
 
-        from . import _torch
+        try:
+            from . import _torch
+        except ImportError as e:
+            raise RuntimeError(f"the module of the tensor calls is missing or of another torch; build it with "
+                               f"`python -m moe_decode_megakernel_persistent_gb300._build` ({e})") from e
         _torch.set_error(MKError)
         _module = _torch
     return _module
