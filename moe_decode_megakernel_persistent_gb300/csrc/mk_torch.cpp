@@ -213,6 +213,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   at::Tensor out = a[6] == Py_None ? fresh(sizes, type, pool.device()) : tensor(a[6], "out");
   if (!out.is_contiguous()) refuse("out must be contiguous");
   if (a[6] != Py_None && overlap(q, out)) refuse("out must not overlap q");
+  if (a[6] != Py_None && overlap(pool, out)) refuse("out must not overlap the pool");
   const mk_kv4_rows outr = rows_of(out, sizes, type, pool.device(), "out");
   const bool want_lse = a[7] == Py_True;
   at::Tensor lse;
