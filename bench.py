@@ -49,7 +49,7 @@ def load_peaks():
 
 # ------------------------------------------------------------------ bytes model
 
-def step_bytes(m, ctxs, distinct_experts_per_layer) -> int:
+def step_bytes(m, ctxs, distinct_experts_per_layer, kv_dtype="bf16") -> int:
     """Algorithmic HBM bytes of one decode step: every weight byte the step
     needs once (norms, attention, router, the distinct selected experts,
     dense MLPs, lm_head, the embedding rows) + the KV cache read (all cached
@@ -75,7 +75,8 @@ def step_bytes(m, ctxs, distinct_experts_per_layer) -> int:
         else:
             total += E * H * aux + distinct_experts_per_layer * expert
     total += lin(m.vocab, H) + H * aux + len(ctxs) * H * aux
-    kv_tok = m.n_layers * 2 * m.kv_dim * 2
+    # a cached position's K and V: bf16, or 4-bit codes with a bf16 scale for each 64
+    kv_tok = m.n_layers * 2 * (m.kv_dim * 2 if kv_dtype == "bf16" else m.kv_dim // 2 + m.kv_dim // 64 * 2)
     total += sum(ctxs) * kv_tok                 # read (includes the new position)
     total += len(ctxs) * kv_tok                 # write
     return int(total)
@@ -241,10 +242,10 @@ def run_ours(args, rank, world):
     prompt_len = w.prompt_len
     max_ctx = prompt_len + K + 2 * args.e2e_steps + W + 64 + args.split_steps + 2
     pages = 3 * ((max_ctx + 127) // 128) + 8
-    eng = Engine(m, weights, n_pages=pages, max_ctx=max_ctx, max_seqs=4)
+    eng = Engine(m, weights, n_pages=pages, max_ctx=max_ctx, max_seqs=4, kv_dtype=args.kv_dtype)
 
     def eng_factory(n_pages, max_ctx16, max_seqs):
-        return Engine(m, weights, n_pages=n_pages, max_ctx=max_ctx16, max_seqs=max_seqs)
+        return Engine(m, weights, n_pages=n_pages, max_ctx=max_ctx16, max_seqs=max_seqs, kv_dtype=args.kv_dtype)
     stream = torch.cuda.current_stream()
 
     # warm-up sequence: a short prompt and W decode steps
@@ -348,7 +349,7 @@ def run_ours(args, rank, world):
     # per-phase timeline of one more decode launch (MK_DBG_TIMING), outside
     # the timed region: medians over the MoE layers
     timeline = None
-    if not args.no_timeline:
+    if not args.no_timeline and args.kv_dtype == "bf16":  # its stamps are of the bf16 cache's one launch
         eng.enable_timing()
         pos_t = prompt_len + K + K_extra
         for _ in range(2):          # the second launch is the one kept
@@ -362,10 +363,10 @@ def run_ours(args, rank, world):
         eng.disable_trace()
 
     ctxs = [prompt_len + i + 1 for i in range(K)]
-    bytes_avg = sum(step_bytes(m, [c], m.top_k) for c in ctxs) / K
+    bytes_avg = sum(step_bytes(m, [c], m.top_k, args.kv_dtype) for c in ctxs) / K
     peaks, peak_kind = load_peaks()
     achieved = bytes_avg / (ms_per_step * 1e-3) / 1e9
-    traffic = measured_traffic(w.name)
+    traffic = measured_traffic(w.name) if args.kv_dtype == "bf16" else None
     out = {
         "metric": METRIC,
         "value": round(total_tokens / (ms / 1e3), 2),
@@ -394,6 +395,7 @@ def run_ours(args, rank, world):
                      "traffic": traffic, "peak_kind": peak_kind,
                      "bytes_per_step": int(bytes_avg)},
         "clocks": clk,
+        **({} if args.kv_dtype == "bf16" else {"kv_dtype": "4-bit K/V cache (not the default workload)"}),
         "setup_s": {"weights": round(gen_s, 1), "prefill": round(prefill_s, 3)},
     }
     if timeline is not None:
@@ -409,7 +411,7 @@ def run_ours(args, rank, world):
             sched = __import__("synth").prompts.schedule(__import__("synth").CONFIGS[5])
             mean_ctx = statistics.mean(L for _, L in sched) + 128
             distinct = 64 * (1 - (1 - 6 / 64) ** 16)
-            bps = step_bytes(m, [int(mean_ctx)] * 16, distinct)
+            bps = step_bytes(m, [int(mean_ctx)] * 16, distinct, args.kv_dtype)
             ach = bps / (fb["ms_per_step"] * 1e-3) / 1e9
             fb["roofline"] = {"bound": "hbm", "achieved": round(ach, 1), "peak": peaks["hbm_gbs"], "unit": "GB/s",
                               "frac": round(ach / peaks["hbm_gbs"], 4), "bytes_per_step": int(bps),
@@ -418,7 +420,7 @@ def run_ours(args, rank, world):
     if rank == 0 and world == 1 and not args.no_cpu_baseline:
         out["cpu_baseline"] = cpu_baseline(m, weights)
     eng.close()
-    if args.int3_steps > 0 and args.config == 3:
+    if args.int3_steps > 0 and args.config == 3 and args.kv_dtype == "bf16":
         del weights
         torch.cuda.empty_cache()
         out["int3_experts"] = run_int3(args, dev)
@@ -682,6 +684,8 @@ def main():
     ap.add_argument("--warmup", type=int, default=8)
     ap.add_argument("--impl", default="ours", choices=["ours", "reference"])
     ap.add_argument("--config", type=int, default=3)
+    ap.add_argument("--kv-dtype", default="bf16", choices=["bf16", "int4"],
+                    help="the engine's K/V cache (the workload's is bf16)")
     ap.add_argument("--e2e-steps", type=int, default=64)
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--batch16-steps", type=int, default=1,
