@@ -505,6 +505,8 @@ MK_API int mk_kv4_load(const mk_kv4_cache* c, const mk_kv4_rows* k, const mk_kv4
  * n_heads / n_kv_heads) of bf16 and 81 of fp32 on, an fp32 q is rounded by 2^-22 too, a K
  * value may lose 2^-36 of the largest one of its 64 positions and head, a V value 2^-33 (bf16
  * rows) or 2^-36 (fp32 rows) of the largest one of its sequence and head.
+ * How the work is split follows max_pages, not the lengths (which only the device knows): short
+ * sequences are faster in a table that is not far wider than they need.
  * workspace: device memory of at least mk_kv4_attention_bytes, 16-byte
  * aligned (NULL where that is 0); its contents before the call do not matter, and calls that may
  * overlap on the GPU need workspaces of their own.

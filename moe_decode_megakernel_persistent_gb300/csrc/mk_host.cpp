@@ -1138,7 +1138,7 @@ MK_API int mk_sync(mk_ctx* c, void* stream) {
   MK_CUDA(cudaMemcpy(err, c->sc.err, sizeof(err), cudaMemcpyDeviceToHost));
   if (err[0] != 0) {
     MK_CUDA(cudaMemset(c->sc.err, 0, sizeof(err)));
-    static const char* sites[] = {"4-bit cache (length or page)", "grid barrier", "page table", "attention unit", "token id",
+    static const char* sites[] = {"4-bit cache (a length, a page or a wait)", "grid barrier", "page table", "attention unit", "token id",
                                   "weight ring", "shared-memory plan", "flagged residual word"};
     const int site = err[1] >= 1 && err[1] <= SITE_FLAG ? err[1] : 0;
     return fail(err[0], std::string("device reported error ") + std::to_string(err[0]) + " at " +

@@ -43,12 +43,12 @@
 // columns run in mk_kv4_wide.cu.
 //
 // Measured (16 heads on 4 kv heads of 128, bf16 rows).  Short work is bound by its
-// chain of set-up, first copies and join: one sequence of 2049 positions 6.9 us, with 6% of
-// the issue slots busy; 16 of 256 to 8448 15.7 us (38 MB).  Long work is bound by issue
-// and the unpacking: 64 of 4096 to 16384 78.3 us, 4.6 TB/s, the ALU 55% and the issue slots 56%
-// busy, with 14 warps of 114 registers on an SM; one of 131071 23.8 us, 3.0 TB/s.  24 columns
+// chain of set-up, first copies and join: one sequence of 2049 positions 7.0 us, with 6% of
+// the issue slots busy; 16 of 256 to 8448 15.8 us (38 MB).  Long work is bound by issue
+// and the unpacking: 64 of 4096 to 16384 76.9 us, 4.6 TB/s, the ALU 53% and the issue slots 55%
+// busy, with 14 warps of 118 registers on an SM; one of 131071 23.6 us, 3.0 TB/s.  24 columns
 // hold their sums in 243 registers, which leaves 8 warps an SM (issue slots 30% busy): 16 sequences of
-// up to 8022 positions with up to 5 rows each 29.9 us.
+// up to 8022 positions with up to 5 rows each 31.2 us.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -859,10 +859,11 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
 // From so many columns on, tiles of 128 on tcgen05 (mk_kv4_wide.cu), us against the narrow
 // kernel's, for 16 sequences of 8192 / one of 8022 / 16 of 700 positions and 4 heads a kv head.
 // bf16: what no longer fits one tile of the narrow kernel, which unpacks a cache tile
-// for each 32 columns: 36 columns 71 / 18.1 / 19.9 against 79 / 18.0 / 23.2, 32 columns
-// 71 / 17.3 / 19.5 against 48 / 15.7 / 16.9.  fp32 (tiles of 16 columns, blocks of 256): 96
-// columns 178 / 30.2 / 39.1 against 226 / 26.0 / 39.7, 80 columns 175 / 29.5 / 38.1 against
-// 191 / 23.6 / 36.3.
+// for each 32 columns: 36 columns 73 / 18.2 / 20.0 against 81 / 18.0 / 23.9, 32 columns
+// 73 / 17.6 / 19.7 against 48 / 15.7 / 17.2.  fp32 (tiles of 16 columns, blocks of 256): 96
+// columns 185 / 30.9 / 40.8 against 232 / 25.9 / 40.3, 80 columns 182 / 30.1 / 39.7 against
+// 196 / 23.7 / 37.4.  The rule is one for batches: a single fp32 sequence is faster in the
+// narrow kernel up to about 160 columns (128: 32.4 against 30.8, 192: 39.0 against 39.9).
 constexpr int kWideCols = 33;
 constexpr int kWideColsF32 = 81;
 constexpr int kShort = 10;  // steps of a block, at most, for work that counts as short
@@ -995,11 +996,11 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
   const long long room = std::min(pl->blocks * sms, kMaxBlocks);  // blocks that run at once
   pl->cluster = 0;
   // Short work: an item is a cluster of up to 16 blocks, while all clusters run at
-  // once (16 sequences of 256 to 8448 positions with clusters of 8: 15.7 us; where a few had to wait
-  // for a place, 16.8), joined through their shared memory.  It saves the second kernel and the
-  // scan of all lengths (20.7 us), but a ragged batch is not levelled and a long item has
-  // 16 blocks at most, which loses once a block has more than about ten steps (131071
-  // positions: 57.6 us against 27.5 then).
+  // once (16 sequences of 256 to 8448 positions with clusters of 8: 15.8 us; as equal runs, with
+  // the second kernel and the scan of all lengths, 18.0), joined through their shared memory.
+  // But a ragged batch is not levelled and a long item has 16 blocks at most, which loses once
+  // a block has more than about ten steps (131071 positions: 57.6 us against 23.6, 64 sequences of
+  // 4096 to 16384: 112 against 77).
   int n = 1;
   while (n < 16 && 2 * n <= most && items <= clusters_at_once(*pl, head_dim, 2 * n)) n *= 2;
   if (!pl->wide && (most + n - 1) / n <= kShort) {

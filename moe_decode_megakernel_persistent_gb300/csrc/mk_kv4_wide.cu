@@ -40,8 +40,8 @@
 // bf16 rows that is no faster: 115 us against 113.)
 //
 // Measured, 1024 rows of 16 heads on 4 kv heads of 128 dimensions at 8022 positions: bf16
-// 113 us, 561 TFLOP/s of 4 x dimensions x seen pairs, tensor cores 25% active; fp32 154 us
-// (546 by the narrow kernel).  A bf16 step takes about 2,900 cycles of a block, in which a column
+// 116 us, 545 TFLOP/s of 4 x dimensions x seen pairs, tensor cores 24% active (113 us with the
+// codes left subnormal); fp32 157 us (546 by the narrow kernel).  A bf16 step takes about 2,900 cycles of a block, in which a column
 // warp works 2,200 and waits for the scores otherwise.
 #include <algorithm>
 

@@ -61,5 +61,7 @@ def attention(q, pool, table, lengths, n_new=None, scale=None, out=None, return_
     1 / sqrt(head_dim).  Returns out in q's dtype (`out` if given: contiguous, and
     of memory that neither q nor the pool has), with
     return_lse also the log-sum-exp of the scores, float32 [n_seqs, rows,
-    n_heads].  Rows that see nothing are zeros, with a log-sum-exp of -inf."""
+    n_heads].  Rows that see nothing are zeros, with a log-sum-exp of -inf.  The
+    work is split by the table's width: short sequences are faster in a table
+    that is not far wider than they need."""
     return L.torch_module().attention(q, pool, table, lengths, n_new, scale, out, bool(return_lse), status)
