@@ -519,6 +519,75 @@ MK_API int mk_kv4_attention(const mk_kv4_cache* c, int32_t n_heads, const mk_kv4
  * lengths).  0 for a description that mk_kv4_attention refuses, or that needs none. */
 MK_API size_t mk_kv4_attention_bytes(const mk_kv4_cache* c, int32_t n_heads, int32_t dtype);
 
+/* ---- operators on the 16-bit K/V cache ----
+ *
+ * The same calls over pools in the layout of mk_kv_alloc: one layer is bfloat16
+ * [n_pages][K|V][n_kv_heads][128][head_dim].  The description is that of the 4-bit
+ * cache (pool, table, lengths, n_new and status mean the same, head_dim is 64 or 128)
+ * with n_pages x 2 x n_kv_heads x 128 < 2^31; the calls only enqueue on `stream` and
+ * can be captured into a graph, which reads table, lengths and n_new anew at
+ * every replay. */
+typedef mk_kv4_cache mk_paged_cache;
+typedef mk_kv4_rows mk_paged_rows;
+
+/* Store the new rows' K and V (dtype MK_BF16 or MK_F32, heads: n_kv_heads) in their
+ * places, rounded to bfloat16; padding rows are not stored.  Two sequences of a call
+ * must not name the same place.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+MK_API int mk_paged_store(const mk_paged_cache* c, const mk_paged_rows* k, const mk_paged_rows* v, int32_t dtype,
+                          void* stream);
+
+/* What each cached position has received: float32 [n_seqs][n_kv_heads][128 x
+ * max_pages] of the caller's, strides in elements (positions are contiguous). */
+typedef struct mk_paged_mass {
+  float* data;
+  int64_t seq_stride, head_stride;
+  float decay;  /* finite */
+} mk_paged_mass;
+
+/* Causal attention of the new rows over the cache (which holds their own K and V
+ * already): row r of sequence i sees positions below lengths[i] - n_new[i] + r + 1;
+ * query head h reads kv head h / (n_heads / n_kv_heads); weights softmax(scale * q . k).
+ * out gets the rows in q's dtype, lse (may be NULL) float32 [n_seqs][rows][n_heads]
+ * the natural logarithm of the sum of exp(scale * q . k).  A row that sees nothing
+ * gets zeros and -infinity.  What a position that a row does not see holds (NaN,
+ * infinities) never shows in that row.  out must not overlap q, the pool, the masses or
+ * the workspace.  |scale| < 1e18.  Scores, maxima and sums are fp32; the weights are
+ * rounded to bfloat16 (2^-9) for bf16 rows; an fp32 q and its weights are three
+ * bfloat16 parts (2^-24).
+ * mass (may be NULL): for every sequence with a new row, and p < lengths[i],
+ *     mass[i][g][p] = (p < lengths[i] - n_new[i] ? decay * mass[i][g][p] : 0)
+ *                   + the sum of the weights that the rows and the heads of kv head g give p,
+ * in fp32 and in a fixed order; other values stay as they are.
+ * workspace: device memory of at least mk_paged_attention_bytes, 16-byte aligned (NULL
+ * where that is 0); its contents before the call do not matter, and calls that may overlap
+ * on the GPU need workspaces of their own.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+MK_API int mk_paged_attention(const mk_paged_cache* c, int32_t n_heads, const mk_paged_rows* q, int32_t dtype,
+                              float scale, const mk_paged_rows* out, float* lse, const mk_paged_mass* mass,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that mk_paged_attention needs for calls of this shape (any lengths),
+ * with masses or without.  0 for a description that it refuses, or that needs none. */
+MK_API size_t mk_paged_attention_bytes(const mk_paged_cache* c, int32_t n_heads, int32_t dtype, int32_t with_mass);
+
+/* Leave at most `keep` positions of each (sequence, kv head): of a sequence of more, the
+ * last `recent` ones and the keep - recent of largest mass among the others, ties to the
+ * lower position (a NaN counts as the largest).  Kept positions below `keep` stay where they
+ * are; the others' K and V move, in order, into the slots below `keep` that are free.
+ *   kept         int32 [n_seqs][n_kv_heads][keep]: the position that each slot now holds, -1
+ *                behind the end of a shorter sequence
+ *   new_lengths  int32 [n_seqs]: min(length, keep); may be c->lengths
+ *   new_mass     the masses moved along, 0 behind the new length; may be `mass` itself, whose
+ *                values behind the new length then stay
+ * rows and n_new of the description are not used.  1 <= keep, 0 <= recent <= keep, n_seqs x
+ * n_kv_heads x keep < 2^31.  Pages that hold positions below `keep` are written: no other
+ * sequence may share them.  A page outside the pool is reported in status, and moves from or to
+ * it are left out.  workspace: mk_paged_evict_bytes, as above.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+MK_API int mk_paged_evict(const mk_paged_cache* c, const mk_paged_mass* mass, int32_t keep, int32_t recent,
+                          int32_t* kept, int32_t* new_lengths, const mk_paged_mass* new_mass, void* workspace,
+                          size_t workspace_bytes, void* stream);
+MK_API size_t mk_paged_evict_bytes(const mk_paged_cache* c, int32_t keep);
+
 /* Copy page src_host[i] to page dst_host[i] in every layer of a pool
  * [n_layers][n_pages][page_bytes] (device, 16-byte aligned, page_bytes a
  * multiple of 16), whatever its pages hold.  The lists are host int32[n], read

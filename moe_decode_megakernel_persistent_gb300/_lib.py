@@ -80,6 +80,13 @@ class mk_kv4_rows(C.Structure):
                 ("head_stride", C.c_int64)]
 
 
+mk_paged_cache, mk_paged_rows = mk_kv4_cache, mk_kv4_rows
+
+
+class mk_paged_mass(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("seq_stride", C.c_int64), ("head_stride", C.c_int64), ("decay", C.c_float)]
+
+
 # every symbol include/mk.h declares, with its ctypes signature
 SIGNATURES = {
     "mk_create": (C.c_int, [C.POINTER(mk_model_desc), C.POINTER(mk_weights), C.POINTER(C.c_void_p)]),
@@ -120,6 +127,13 @@ SIGNATURES = {
     "mk_kv4_attention": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_float, C.c_void_p,
                                    C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
     "mk_kv4_attention_bytes": (C.c_size_t, [C.c_void_p, C.c_int32, C.c_int32]),
+    "mk_paged_store": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p]),
+    "mk_paged_attention": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_float, C.c_void_p,
+                                     C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "mk_paged_attention_bytes": (C.c_size_t, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32]),
+    "mk_paged_evict": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
+                                 C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "mk_paged_evict_bytes": (C.c_size_t, [C.c_void_p, C.c_int32]),
     "mk_page_copy": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_size_t, C.c_void_p,
                                C.c_void_p, C.c_int32, C.c_void_p]),
     "mk_static_bytes": (C.c_int, [C.POINTER(mk_model_desc), C.c_int32, C.POINTER(C.c_int64),
@@ -148,7 +162,7 @@ def load(path: str = LIB_PATH):
 
 
 def torch_module():
-    """The module _torch (csrc/mk_torch.cpp): the tensor calls of kv4 and pages."""
+    """The module _torch (csrc/mk_torch.cpp): the tensor calls of kv4, paged and pages."""
     global _module
     if _module is None:
         load()
@@ -328,6 +342,32 @@ def mk_kv4_attention(cache: mk_kv4_cache, n_heads: int, q: mk_kv4_rows, dtype: i
 
 def mk_kv4_attention_bytes(cache: mk_kv4_cache, n_heads: int, dtype: int) -> int:
     return int(load().mk_kv4_attention_bytes(_ref(cache), n_heads, dtype))
+
+
+def mk_paged_store(cache: mk_paged_cache, k: mk_paged_rows, v: mk_paged_rows, dtype: int, stream: int = 0):
+    _check(load().mk_paged_store(_ref(cache), _ref(k), _ref(v), dtype, stream))
+
+
+def mk_paged_attention(cache: mk_paged_cache, n_heads: int, q: mk_paged_rows, dtype: int, scale: float,
+                       out: mk_paged_rows, lse_dev: int | None, mass: mk_paged_mass | None, workspace_dev: int,
+                       workspace_bytes: int, stream: int = 0):
+    _check(load().mk_paged_attention(_ref(cache), n_heads, _ref(q), dtype, scale, _ref(out), lse_dev, _ref(mass),
+                                     workspace_dev, workspace_bytes, stream))
+
+
+def mk_paged_attention_bytes(cache: mk_paged_cache, n_heads: int, dtype: int, with_mass: bool = False) -> int:
+    return int(load().mk_paged_attention_bytes(_ref(cache), n_heads, dtype, int(with_mass)))
+
+
+def mk_paged_evict(cache: mk_paged_cache, mass: mk_paged_mass, keep: int, recent: int, kept_dev: int,
+                   new_lengths_dev: int, new_mass: mk_paged_mass, workspace_dev: int, workspace_bytes: int,
+                   stream: int = 0):
+    _check(load().mk_paged_evict(_ref(cache), _ref(mass), keep, recent, kept_dev, new_lengths_dev, _ref(new_mass),
+                                 workspace_dev, workspace_bytes, stream))
+
+
+def mk_paged_evict_bytes(cache: mk_paged_cache, keep: int) -> int:
+    return int(load().mk_paged_evict_bytes(_ref(cache), keep))
 
 
 def mk_page_copy(pool_dev: int, n_layers: int, n_pages: int, page_bytes: int, src, dst, stream: int = 0):

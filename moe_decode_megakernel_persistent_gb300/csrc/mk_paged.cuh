@@ -1,0 +1,29 @@
+// What the operators on the 16-bit paged cache share (mk_paged.cu,
+// mk_paged_attention.cu, mk_paged_evict.cu).  Arguments are those of the 4-bit
+// cache's calls; a pool of one layer is bf16 [page][K|V][kv head][128][head_dim].
+#pragma once
+#include "mk_kv4.cuh"
+
+namespace mk {
+
+// Masses of the cached positions: [n_seqs][n_kv_heads][128 * max_pages].
+struct PagedMass {
+  float* p;
+  long long seq, head;  // strides in elements
+  float decay;
+};
+
+// Row of a page's slot in the pool taken as rows of head_dim (held to 31 bits by the entry points).
+__device__ __forceinline__ int paged_row(const Kv4Args& a, int page, int kv, int head, int p) {
+  return ((page * 2 + kv) * a.n_kv_heads + head) * kPageTokens + p % kPageTokens;
+}
+template <int HD>
+__device__ __forceinline__ __nv_bfloat16* paged_at(const Kv4Args& a, int row) {
+  return reinterpret_cast<__nv_bfloat16*>(a.pool) + (size_t)row * HD;
+}
+
+// Host checks of a description (*empty: the call has no row), and of masses.
+int paged_check_cache(const mk_paged_cache* c, bool* empty);
+int paged_check_mass(const mk_paged_mass* m, const mk_paged_cache* c, const char* what);
+
+}  // namespace mk
