@@ -552,7 +552,7 @@ typedef struct mk_paged_mass {
  * gets zeros and -infinity.  What a position that a row does not see holds (NaN,
  * infinities) never shows in that row.  out must not overlap q, the pool, the masses or
  * the workspace.  |scale| < 1e18.  Scores, maxima and sums are fp32; the weights are
- * rounded to bfloat16 (2^-9) for bf16 rows; an fp32 q and its weights are three
+ * rounded to bfloat16 (2^-8) for bf16 rows; an fp32 q and its weights are three
  * bfloat16 parts (2^-24).
  * mass (may be NULL): for every sequence with a new row, and p < lengths[i],
  *     mass[i][g][p] = (p < lengths[i] - n_new[i] ? decay * mass[i][g][p] : 0)

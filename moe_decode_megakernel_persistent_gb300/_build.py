@@ -31,7 +31,7 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + IN
 SOURCES = [("mk_kernel.cu", f"mk_kernel_p{p}", [f"-DMK_KERNEL_PART={p}"]) for p in range(4)] + [
     (f, os.path.splitext(f)[0], []) for f in ("mk_host.cpp", "mk_static.cu", "mk_pack.cu", "mk_kv.cu", "mk_kv4.cu", "mk_kv4_attention.cu",
                                                   "mk_kv4_wide.cu", "mk_pages.cu", "mk_paged.cu", "mk_paged_attention.cu",
-                                                  "mk_paged_evict.cu", "mk_prefill.cu")]
+                                                  "mk_paged_wide.cu", "mk_paged_mass.cu", "mk_paged_evict.cu", "mk_prefill.cu")]
 
 
 def _nvcc() -> str:

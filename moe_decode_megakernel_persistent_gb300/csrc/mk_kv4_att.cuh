@@ -228,5 +228,7 @@ struct WideKernel {
   int CT, SP, smem, blocks, threads;
 };
 WideKernel kv4_wide_kernel(int head_dim, int dtype);
+// The join of split items (mk_kv4_attention.cu), with 4 or 12 (many) parts in flight in a warp.
+const void* kv4_join_kernel(int head_dim, int dtype, bool many);
 
 }  // namespace mk

@@ -1028,7 +1028,17 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, Plan* pl) {
   return true;
 }
 
+template <int HD, class T>
+const void* join_of(bool many) {
+  return many ? reinterpret_cast<const void*>(&k_kv4_join<HD, T, 12>) : reinterpret_cast<const void*>(&k_kv4_join<HD, T, 4>);
+}
+
 }  // namespace
+
+const void* kv4_join_kernel(int head_dim, int dtype, bool many) {
+  if (dtype == MK_F32) return head_dim == 64 ? join_of<64, float>(many) : join_of<128, float>(many);
+  return head_dim == 64 ? join_of<64, __nv_bfloat16>(many) : join_of<128, __nv_bfloat16>(many);
+}
 
 bool kv4_attention_bytes(const Kv4Args& a, int head_dim, int n_heads, int dtype, size_t* bytes) {
   Plan pl;

@@ -1,0 +1,81 @@
+// What the attention kernels over the 16-bit paged cache share (mk_paged_attention.cu,
+// mk_paged_wide.cu, mk_paged_mass.cu).  The split of the work, the bounded waits and the
+// join of split items are those of the 4-bit cache's attention (mk_kv4_att.cuh).
+//
+// A page's K (or V) of one kv head is 128 rows of head_dim values in one range, which one
+// tensor copy (TMA) brings into shared memory as [head_dim / 64][positions][128 bytes]
+// with the 128-byte swizzle: what ldmatrix reads without bank conflicts and what
+// tcgen05.mma takes as an operand, K by dimensions and V by positions.  A page outside the
+// pool is copied from rows behind it, which the copy fills with zeros.
+#pragma once
+#include <cuda.h>
+
+#include "mk_kv4_att.cuh"
+#include "mk_paged.cuh"
+
+namespace mk {
+
+struct PagedAtt {
+  AttArgs t;         // t.c = scale * log2(e)
+  float* scores;     // workspace: [n_seqs][n_kv_heads][128 * max_pages][score_cols] in log2, or null
+  int32_t score_cols;
+};
+
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(row), "r"(0), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Of two bf16 values, bits 15 and 31: those that are no finite numbers.
+__device__ __forceinline__ uint32_t odd_ones(uint32_t x) { return ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// An fp32 value as three bf16 ones of its sign, by truncation: 3 x 8 bits are all of its 24.  A part
+// that would be 0 is 2^-126 instead (2^-26 of the value at most, else left 0), because 0 times an
+// infinite K is NaN where the value times it is infinite.
+struct Parts {
+  uint32_t h[3];  // bf16 in the high half
+};
+__device__ __forceinline__ Parts parts_of(float x) {
+  Parts r;
+  float rest = x;
+  const uint32_t tiny = fabsf(x) >= 7.8886091e-31f ? (__float_as_uint(x) & 0x80000000u) | 0x00800000u : 0u;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    r.h[i] = __float_as_uint(rest) & 0xFFFF0000u;
+    rest -= __uint_as_float(r.h[i]);
+    if (i && !(r.h[i] << 1)) r.h[i] = tiny;
+  }
+  return r;
+}
+// Part i of two values as a word.
+__device__ __forceinline__ uint32_t both(const Parts& lo, const Parts& hi, int i) { return __byte_perm(lo.h[i], hi.h[i], 0x7632); }
+
+// The sum of the values of V that are no finite numbers, of dimensions d, d + 1 and the positions
+// a .. b.  Where one is seen, the products may have made NaN of an infinity (times a weight, or a
+// part of it, that is 0 or negative): the result is this sum instead.  Rare, and so plain.
+template <int HD>
+static __device__ __noinline__ float2 odd_sum(const Kv4Args& a, int seq, int head, int d, int from, int to) {
+  float2 s = make_float2(0.f, 0.f);
+  for (int q = from; q < to; ++q) {
+    const int page = table_row(a, seq)[q / kPageTokens];
+    if (page < 0 || page >= a.n_pages) continue;
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(paged_at<HD>(a, paged_row(a, page, 1, head, q)) + d), odd = odd_ones(v);
+    if (odd >> 15 & 1u) s.x += low_f(v);
+    if (odd >> 31) s.y += high_f(v);
+  }
+  return s;
+}
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// The wide kernel (mk_paged_wide.cu): tiles of CT columns and SP positions; null: none.
+WideKernel paged_wide_kernel(int head_dim, int dtype, int cols);
+// The pool's rows as a tensor map whose copies bring `positions` rows.
+int paged_map(CUtensorMap* map, const Kv4Args& a, int head_dim, int positions);
+// Masses from the scores that the narrow kernel kept, or formed again (mk_paged_mass.cu).
+cudaError_t paged_mass(const PagedAtt& p, const PagedMass& m, int head_dim, int dtype, const CUtensorMap& map, cudaStream_t st);
+
+}  // namespace mk

@@ -70,11 +70,11 @@ def bounds(A, D, lse, n, hd, dtype):
     argument, of magnitude at most 2 D + |lse|, is rounded a few times and whose result is
     off by 2^-22: delta is the relative error of a weight.  Numerator and denominator sum n
     terms (n 2^-24 each at worst).  Weights enter the second product rounded to bf16 (half a
-    step: 2^-9) for bf16 rows, in three parts (2^-24) for fp32 rows.  Returns the absolute
+    step: 2^-8) for bf16 rows, in three parts (2^-24) for fp32 rows.  Returns the absolute
     bound of out before its own rounding, that rounding's relative bound, and lse's bound."""
     e = 2.0 ** -24
     delta = (2 * hd + 16) * e * D + 8 * e * (2 * D + 1) + 2.0 ** -21
-    part = 2.0 ** -9 if dtype == torch.bfloat16 else 2.0 ** -24
+    part = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
     inner = A * (2 * delta + 2 * n * e + part + 8 * e)[..., None]
     return inner, torch.finfo(dtype).eps / 2, delta + n * e + 4 * e * (1 + lse.abs())
 
