@@ -19,6 +19,7 @@ struct PagedAtt {
   AttArgs t;         // t.c = scale * log2(e)
   float* scores;     // workspace: [n_seqs][n_kv_heads][128 * max_pages][score_cols] in log2, or null
   int32_t score_cols;
+  char* mass_ws;     // workspace of the masses without scores
 };
 
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
@@ -73,9 +74,14 @@ __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823
 
 // The wide kernel (mk_paged_wide.cu): tiles of CT columns and SP positions; null: none.
 WideKernel paged_wide_kernel(int head_dim, int dtype, int cols);
-// The pool's rows as a tensor map whose copies bring `positions` rows.
-int paged_map(CUtensorMap* map, const Kv4Args& a, int head_dim, int positions);
-// Masses from the scores that the narrow kernel kept, or formed again (mk_paged_mass.cu).
+// Rows of head_dim bf16 values as a tensor map whose copies bring `box` rows.
+int rows_map(CUtensorMap* map, const void* base, long long rows, int head_dim, int box);
+int device_sms();
+// Masses from the scores that the narrow kernel kept, or formed again (mk_paged_mass.cu), and
+// the workspace that these take.
+size_t paged_mass_bytes(const Kv4Args& a, int head_dim, int n_heads, int dtype);
+// What needs no log-sum-exp, before the attention.
+cudaError_t paged_mass_begin(const PagedAtt& p, int head_dim, int dtype, cudaStream_t st);
 cudaError_t paged_mass(const PagedAtt& p, const PagedMass& m, int head_dim, int dtype, const CUtensorMap& map, cudaStream_t st);
 
 }  // namespace mk

@@ -579,7 +579,7 @@ struct Plan {
   int n_ctiles, n_entries, items, grid, join_cols, join_threads, join_many;
   int cluster;                                   // blocks of an item's cluster; 0: the steps of all items in equal runs
   int score_cols;                                // columns of the scores kept for the masses; 0: none
-  size_t item_off, part_off, lse_off, score_off, bytes;
+  size_t item_off, part_off, lse_off, score_off, mass_off, bytes;
 };
 
 template <int HD, class T, int NT, int W, int U, int R, int B>
@@ -613,15 +613,6 @@ void take_for(Plan* pl, int cols, int dtype) {
   else cols <= 8 ? take<HD, __nv_bfloat16, 1, 4, 1, R, 1>(pl) : take<HD, __nv_bfloat16, 2, 4, 1, R, 1>(pl);
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return 152;
-  }
-  return n;
-}
-
 // The kernels take more shared memory than the default: asked for once per device.
 cudaError_t allow_smem(const Plan& pl) {
   static std::atomic<uint32_t> done[64];  // variants, by device
@@ -649,7 +640,7 @@ int clusters_at_once(const Plan& pl, int head_dim, int n) {
   while (1 << log < n) ++log;
   if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) count = known[dev][pl.id][log].load();
   if (count) return count - 1;
-  count = pl.blocks * sm_count() / n;
+  count = pl.blocks * device_sms() / n;
   cudaError_t e = allow_smem(pl);
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
@@ -687,7 +678,7 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, bool mass, 
   pl->n_ctiles = (int)ct;
   pl->n_entries = (int)entries;
   pl->items = (int)items;
-  const int sms = sm_count();
+  const int sms = device_sms();
   const long long room = std::min(pl->blocks * sms, kMaxBlocks);  // blocks that run at once
   pl->cluster = 0;
   pl->item_off = pl->part_off = pl->bytes = 0;
@@ -717,6 +708,9 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, bool mass, 
       pl->score_cols = (int)(cols + 3) & ~3;
       pl->score_off = up16(pl->bytes);
       pl->bytes = pl->score_off + (size_t)c.n_seqs * c.n_kv_heads * c.max_pages * kPageTokens * pl->score_cols * sizeof(float);
+    } else {
+      pl->mass_off = (pl->bytes + 127) & ~(size_t)127;
+      pl->bytes = pl->mass_off + paged_mass_bytes(c, head_dim, n_heads, dtype);
     }
   }
   return true;
@@ -724,8 +718,17 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, bool mass, 
 
 }  // namespace
 
+int device_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 152;
+  }
+  return n;
+}
+
 // The driver's encoder, looked up once.
-int paged_map(CUtensorMap* map, const Kv4Args& a, int head_dim, int positions) {
+int rows_map(CUtensorMap* map, const void* base, long long rows, int head_dim, int box_rows) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -740,13 +743,12 @@ int paged_map(CUtensorMap* map, const Kv4Args& a, int head_dim, int positions) {
     }
     known.store(f);
   }
-  const cuuint64_t rows = (cuuint64_t)a.n_pages * 2 * a.n_kv_heads * kPageTokens;
-  const cuuint64_t dims[3] = {64, rows, (cuuint64_t)head_dim / 64}, strides[2] = {(cuuint64_t)head_dim * 2, 128};
-  const cuuint32_t box[3] = {64, (cuuint32_t)positions, (cuuint32_t)head_dim / 64}, one[3] = {1, 1, 1};
-  const CUresult r = reinterpret_cast<Encode>(f)(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.pool, dims, strides, box, one,
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)head_dim / 64}, strides[2] = {(cuuint64_t)head_dim * 2, 128};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)head_dim / 64}, one[3] = {1, 1, 1};
+  const CUresult r = reinterpret_cast<Encode>(f)(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
                                                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? MK_OK : host_fail(MK_ERR_CUDA, "the pool has no tensor map");
+  return r == CUDA_SUCCESS ? MK_OK : host_fail(MK_ERR_CUDA, "no tensor map of these rows");
 }
 
 static int run_attention(const Kv4Args& a, int head_dim, int n_heads, const Kv4Rows& q, int dtype, float scale, const Kv4Rows& out,
@@ -757,7 +759,7 @@ static int run_attention(const Kv4Args& a, int head_dim, int n_heads, const Kv4R
   if (pl.bytes && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < pl.bytes))
     return host_fail(MK_ERR_INVALID_ARG, "workspace is NULL, not 16-byte aligned or smaller than mk_paged_attention_bytes");
   CUtensorMap map;
-  if (int r = paged_map(&map, a, head_dim, pl.SP)) return r;
+  if (int r = rows_map(&map, a.pool, (long long)a.n_pages * 2 * a.n_kv_heads * kPageTokens, head_dim, pl.SP)) return r;
   char* ws = static_cast<char*>(workspace);
   PagedAtt pa;
   AttArgs& p = pa.t;
@@ -787,7 +789,9 @@ static int run_attention(const Kv4Args& a, int head_dim, int n_heads, const Kv4R
   }
   pa.score_cols = pl.score_cols;
   pa.scores = pl.score_cols ? reinterpret_cast<float*>(ws + pl.score_off) : nullptr;
+  pa.mass_ws = mass && !pl.score_cols ? ws + pl.mass_off : nullptr;
   cudaError_t e = allow_smem(pl);
+  if (e == cudaSuccess && pa.mass_ws) e = paged_mass_begin(pa, head_dim, dtype, stream);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3(pl.grid);
