@@ -28,6 +28,20 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
       "l"(map), "r"(0), "r"(row), "r"(0), "r"(bar)
       : "memory");
 }
+// As bar_wait, without a call: a kernel whose warps split its registers unequally has none.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* give_up, int32_t* status) {
+  if (bar_try(bar, parity)) return true;
+  const uint64_t t0 = now_ns();
+  for (uint32_t i = 0;; ++i) {
+    if (bar_try(bar, parity)) return true;
+    if (*give_up) return false;
+    if ((i & 15u) == 15u && now_ns() - t0 > kWaitNs) {
+      *give_up = 1;
+      if (status) atomicCAS(status, 0, MK_ERR_BARRIER_TIMEOUT);
+      return false;
+    }
+  }
+}
 __device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -59,7 +73,7 @@ __device__ __forceinline__ uint32_t both(const Parts& lo, const Parts& hi, int i
 // a .. b.  Where one is seen, the products may have made NaN of an infinity (times a weight, or a
 // part of it, that is 0 or negative): the result is this sum instead.  Rare, and so plain.
 template <int HD>
-static __device__ __noinline__ float2 odd_sum(const Kv4Args& a, int seq, int head, int d, int from, int to) {
+__device__ __forceinline__ float2 odd_sum(const Kv4Args& a, int seq, int head, int d, int from, int to) {
   float2 s = make_float2(0.f, 0.f);
   for (int q = from; q < to; ++q) {
     const int page = table_row(a, seq)[q / kPageTokens];

@@ -67,7 +67,7 @@ struct MassShape {
   static constexpr int QT = NG * N * 128;            // bytes of a part of a tile of columns
   static constexpr int QS = 2;                       // places of tiles
   static constexpr int SMEM = 1024 + KS * 2 * KB + QS * P * QT;
-  static constexpr int CW = 8, THREADS = 32 * (CW + 2);
+  static constexpr int CW = 8, THREADS = 32 * (CW + 3);  // a page's four warps twice, copies, products of each page
 };
 constexpr int kSpan = 2 * kPageTokens;  // positions of an item
 constexpr int kSetUp = 2;               // tiles that an item's set-up counts as
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
   const AttArgs& p = a.pa.t;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024 - (smem_addr(sm_raw) & 1023)) & 1023);
-  __shared__ __align__(8) uint64_t k_full[KS], k_empty[KS], q_full[QS], q_empty[QS], s_full[2], s_empty[2], l_full[kLse], l_empty[kLse], run_full[kMassRuns], drain;
+  __shared__ __align__(8) uint64_t k_full[KS], k_empty[KS], q_full[QS], q_empty[QS], s_full[2][2], s_empty[2][2], l_full[kLse], l_empty[kLse], run_full[kMassRuns], drain;
   __shared__ MassRun says[kMassRuns];
   __shared__ __align__(16) float lse2[kLse][N];  // log2; +infinity: a column that gives nothing
   __shared__ int lims[kLse][N];                  // positions that a column sees
@@ -193,12 +193,12 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
     auto init = [](uint64_t* b, int n) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(n) : "memory");
     };
-    for (int i = 0; i < KS; ++i) init(&k_full[i], 1), init(&k_empty[i], 1);
-    for (int i = 0; i < QS; ++i) init(&q_full[i], 1), init(&q_empty[i], 1);
-    for (int i = 0; i < 2; ++i) init(&s_full[i], 1), init(&s_empty[i], CW);
+    for (int i = 0; i < KS; ++i) init(&k_full[i], 1), init(&k_empty[i], 2);
+    for (int i = 0; i < QS; ++i) init(&q_full[i], 1), init(&q_empty[i], 2);
+    for (int i = 0; i < 4; ++i) init(&s_full[i >> 1][i & 1], 1), init(&s_empty[i >> 1][i & 1], CW / 2);
     for (int i = 0; i < kLse; ++i) init(&l_full[i], 1), init(&l_empty[i], CW);
     for (int i = 0; i < kMassRuns; ++i) init(&run_full[i], 1);
-    init(&drain, 1);
+    init(&drain, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     give_up = 0;
   }
@@ -322,8 +322,10 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
       for (uint32_t i = n_items > KS ? n_items - KS : 0; i < n_items; ++i) bar_wait_long(smem_addr(&k_full[i % KS]), (i / KS) & 1, &none, nullptr);
       for (uint32_t i = tile > QS ? tile - QS : 0; i <= tile; ++i) bar_wait_long(smem_addr(&q_full[i % QS]), (i / QS) & 1, &none, nullptr);
     }
-  } else if (w == CW + 1) {  // ---- the products
+  } else if (w > CW) {  // ---- a page's products
     constexpr uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((128 >> 4) << 24);  // bf16, fp32 sums
+    const int pg = w - CW - 1;
+    const uint32_t tmu = uniform(tm + 128 * pg), ku = uniform(smem_addr(k_op + pg * S::KB)), qu = uniform(smem_addr(q_op));
     uint32_t tile = 0;
     MassRun r;
     for (uint32_t n_runs = 0; take_run(n_runs, r); ++n_runs) {
@@ -332,28 +334,26 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
       for (int t = r.t0; t < r.t1; ++t, ++tile) {
         const int qs = tile % QS, b = tile & 1;
         ok = bar_wait(smem_addr(&q_full[qs]), (tile / QS) & 1, &give_up, p.a.status) && ok;
-        if (tile >= 2) ok = bar_wait(smem_addr(&s_empty[b]), (tile / 2 - 1) & 1, &give_up, p.a.status) && ok;
+        if (tile >= 2) ok = bar_wait(smem_addr(&s_empty[pg][b]), (tile / 2 - 1) & 1, &give_up, p.a.status) && ok;
         after_sync();
-        if (lane == 0 && ok && !give_up) {
+        const uint32_t qsu = uniform(qs), bu = uniform(b), ksu = uniform(ks), end = uniform(t + 1 == r.t1);
+        if (ok && !give_up && elect_one()) {
+          const uint64_t kd = operand(ku + ksu * 2 * S::KB);
 #pragma unroll
-          for (int pg = 0; pg < 2; ++pg) {
-            const uint64_t kd = operand(smem_addr(k_op + (ks * 2 + pg) * S::KB));
+          for (int x = S::P - 1; x >= 0; --x) {  // q's low parts first
+            const uint64_t qd = operand(qu + (qsu * S::P + x) * S::QT);
 #pragma unroll
-            for (int x = S::P - 1; x >= 0; --x) {  // q's low parts first
-              const uint64_t qd = operand(smem_addr(q_op + (qs * S::P + x) * S::QT));
+            for (int g = 0; g < NG; ++g)
 #pragma unroll
-              for (int g = 0; g < NG; ++g)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                  const uint64_t ka = kd + ((g * 128 * 128 + kk * 32) >> 4), qb = qd + ((g * N * 128 + kk * 32) >> 4);
-                  if (g == 0 && kk == 0 && x == S::P - 1) mma_ss<false>(tm + 256 * b + 128 * pg, ka, qb, id);
-                  else mma_ss<true>(tm + 256 * b + 128 * pg, ka, qb, id);
-                }
-            }
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t ka = kd + ((g * 128 * 128 + kk * 32) >> 4), qb = qd + ((g * N * 128 + kk * 32) >> 4);
+                if (g == 0 && kk == 0 && x == S::P - 1) mma_ss<false>(tmu + 256 * bu, ka, qb, id);
+                else mma_ss<true>(tmu + 256 * bu, ka, qb, id);
+              }
           }
-          commit(smem_addr(&s_full[b]));
-          commit(smem_addr(&q_empty[qs]));
-          if (t + 1 == r.t1) commit(smem_addr(&k_empty[ks]));
+          commit(smem_addr(&s_full[pg][bu]));
+          commit(smem_addr(&q_empty[qsu]));
+          if (end) commit(smem_addr(&k_empty[ksu]));
         }
         __syncwarp();
       }
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
       for (int t = r.t0; t < r.t1; ++t, ++tile) {
         const int ls = tile % kLse, b = tile & 1;
         ok = bar_wait(smem_addr(&l_full[ls]), (tile / kLse) & 1, &give_up, p.a.status) && ok;
-        ok = bar_wait(smem_addr(&s_full[b]), (tile / 2) & 1, &give_up, p.a.status) && ok;
+        ok = bar_wait(smem_addr(&s_full[pg][b]), (tile / 2) & 1, &give_up, p.a.status) && ok;
         after_sync();
         if (ok && !give_up) {
           auto add = [&](auto cut_) {
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
         before_sync();
         __syncwarp();
         if (lane == 0) {
-          arrive(smem_addr(&s_empty[b]));
+          arrive(smem_addr(&s_empty[pg][b]));
           arrive(smem_addr(&l_empty[ls]));
         }
       }

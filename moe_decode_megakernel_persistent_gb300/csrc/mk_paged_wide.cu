@@ -8,7 +8,7 @@
 // its maximum is its own and moves only when a score passes it by 2^8; then it rescales its
 // sums, which the next product waits for.  An fp32 q is three bf16 parts, and so are its weights.
 //
-// Warps 4 TB: the columns.  One warp more looks up pages and issues the copies, another the
+// Warps 4 TB: the columns.  One warp more looks up pages and issues the copies, one for each tile its
 // products.  With two tiles a block (TB = 2) the tensor cores work on one tile while the
 // columns of the other form weights; with one tile there are two places of scores, so that S of a step
 // runs before the second product of the last.
@@ -44,7 +44,7 @@ struct PWide {
   static constexpr int SUMS = NS * 128, THIRD = SUMS + 128;
   static constexpr int TM = TB == 2 ? 256 : 512;    // of a tile
   static constexpr int CW = 4 * TB;                 // warps of the columns
-  static constexpr int THREADS = 32 * (CW + 2);
+  static constexpr int THREADS = 32 * (CW + 1 + TB);
 };
 
 // What the copying warp says of a run (t1 = t0: there is none more).
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
   const AttArgs& p = pa.t;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024 - (smem_addr(sm_raw) & 1023)) & 1023);
-  __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], s_full[TB][NS], p_full[TB][NS], pv_done[TB], q_full, run_full[kRuns], o_full, drain;
+  __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], s_full[TB][NS], p_full[TB][NS][2], pv_done[TB], q_full, run_full[kRuns], o_full, v_clean, drain;
   __shared__ RunSays says[kRuns];
   __shared__ int odd[2];  // a run's V had values that are no finite numbers where columns differ
   __shared__ uint32_t tm_base;
@@ -74,18 +74,19 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
     auto init = [](uint64_t* b, int n) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(n) : "memory");
     };
-    for (int i = 0; i < ST; ++i) init(&kv_full[i], 1), init(&kv_empty[i], 1);
+    for (int i = 0; i < ST; ++i) init(&kv_full[i], 1), init(&kv_empty[i], TB);
     for (int t = 0; t < TB; ++t) {
       for (int i = 0; i < NS; ++i) {
         init(&s_full[t][i], 1);
-        init(&p_full[t][i], 4);  // by each of the tile's warps (of which one may be a place of scores ahead)
+        for (int h = 0; h < 2; ++h) init(&p_full[t][i][h], 4);  // by each of the tile's warps (of which one may be a place of scores ahead)
       }
       init(&pv_done[t], 1);
     }
     init(&q_full, CW);
     for (int i = 0; i < kRuns; ++i) init(&run_full[i], 1);
-    init(&o_full, 1);
-    init(&drain, 1);
+    init(&o_full, TB);
+    init(&v_clean, TB);
+    init(&drain, TB);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     give_up = 0;
     odd[0] = odd[1] = 0;
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
   const uint32_t tm = tm_base;
   // A run as the other warps take it; false: there is none more.
   auto take_run = [&](uint32_t i, RunSays& rs) {
-    if (!bar_wait(smem_addr(&run_full[i % kRuns]), (i / kRuns) & 1, &give_up, p.a.status)) return false;
+    if (!wait_for(smem_addr(&run_full[i % kRuns]), (i / kRuns) & 1, &give_up, p.a.status)) return false;
     rs = says[i % kRuns];
     return rs.t1 > rs.t0;
   };
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
     // K (kv = 0) or V of the run's step; false: the wait for its stage ran out
     auto copy = [&](int row, int kv) {
       const int st = slot % ST;
-      const bool ok = slot < ST || bar_wait(smem_addr(&kv_empty[st]), (slot / ST - 1) & 1, &give_up, p.a.status);
+      const bool ok = slot < ST || wait_for(smem_addr(&kv_empty[st]), (slot / ST - 1) & 1, &give_up, p.a.status);
       if (ok && lane == 0) {
         const uint32_t bar = smem_addr(&kv_full[st]);
         expect(bar, W::KVB);
@@ -168,20 +169,23 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
     }
     if (give_up && lane == 0) {  // copies in flight land before the block ends
       int none = 0;
-      for (uint32_t i = slot > ST ? slot - ST : 0; i < slot; ++i) bar_wait_long(smem_addr(&kv_full[i % ST]), (i / ST) & 1, &none, nullptr);
+      for (uint32_t i = slot > ST ? slot - ST : 0; i < slot; ++i) wait_for(smem_addr(&kv_full[i % ST]), (i / ST) & 1, &none, nullptr);
     }
-  } else if (w == CW + 1) {  // ---- the products
+  } else if (w > CW && w <= CW + TB) {  // ---- the products of a tile
+    const int tile = TB == 1 ? 0 : w - CW - 1;
     constexpr uint32_t id_qk = (1u << 4) | (1u << 7) | (1u << 10) | ((SP >> 3) << 17) | ((128 >> 4) << 24);               // bf16, fp32 sums
     constexpr uint32_t id_pv = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((HD >> 3) << 17) | ((128 >> 4) << 24);  // V by rows
     uint32_t slot = 0, k = 0;  // stages and steps taken
+    [[maybe_unused]] uint32_t n_clean = 0;
     RunSays rs;
-    auto arrived = [&](uint32_t s) { return bar_wait(smem_addr(&kv_full[s % ST]), (s / ST) & 1, &give_up, p.a.status); };
-    auto scores = [&](int tile, uint32_t step, uint32_t s) {  // lane 0: of the step into its place
-      const uint32_t to = tm + W::TM * tile + 128 * (step % NS);
-      const uint64_t kd = operand(smem_addr(kv_op + s % ST * W::KVB));
+    auto arrived = [&](uint32_t s) { return wait_for(smem_addr(&kv_full[s % ST]), (s / ST) & 1, &give_up, p.a.status); };
+    const uint32_t tmu = uniform(tm + W::TM * tile), qu = uniform(smem_addr(q_op + tile * W::P * W::QT)), kvu = uniform(smem_addr(kv_op));
+    auto scores = [&](uint32_t step, uint32_t s) {  // one lane: of the step into its place
+      const uint32_t to = tmu + 128 * (step % NS);
+      const uint64_t kd = operand(kvu + s % ST * W::KVB);
 #pragma unroll
       for (int x = W::P - 1; x >= 0; --x) {  // q's low parts first
-        const uint64_t q = operand(smem_addr(q_op + (tile * W::P + x) * W::QT));
+        const uint64_t q = operand(qu + x * W::QT);
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -192,21 +196,24 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
           }
       }
       commit(smem_addr(&s_full[tile][step % NS]));
+      commit(smem_addr(&kv_empty[s % ST]));
     };
     for (uint32_t n_runs = 0; take_run(n_runs, rs); ++n_runs) {
       const int n = rs.t1 - rs.t0, seq = p.n_ctiles == 1 ? rs.e : rs.e / p.n_ctiles, j = rs.e - seq * p.n_ctiles;
       const int last = min(row_of(p, min((j + 1) * CT, p.cols) - 1), rs.nn - 1);
       const int end = rs.len - rs.nn + last + 1;                                    // what some column sees
       const int common = max(0, rs.len - rs.nn + row_of(p, j * CT) + 1);            // what all columns (with a row) do
-      if (lane == 0) odd[n_runs & 1] = 0;
-      bool ok = bar_wait(smem_addr(&q_full), n_runs & 1, &give_up, p.a.status);
+      bool ok = wait_for(smem_addr(&q_full), n_runs & 1, &give_up, p.a.status);
+      // The second tile begins when the first has its first weights, so that one forms weights while the
+      // other's products run (both at once: 4,500 cycles a step, in turn 3,100).
+      if (TB > 1 && tile) ok = wait_for(smem_addr(&p_full[0][0][0]), k & 1, &give_up, p.a.status) && ok;
+      if (lane == 0 && tile == 0) odd[(n_runs + 1) & 1] = 0;  // which the columns have read: the next run's
       for (int i = 0; i < NS && i < n; ++i, ++slot) {
         ok = arrived(slot) && ok;
         after_sync();
-        if (lane == 0 && ok && !give_up) {
-#pragma unroll
-          for (int t = 0; t < TB; ++t) scores(t, k + i, slot);
-          commit(smem_addr(&kv_empty[slot % ST]));
+        const uint32_t su = uniform(slot), ku = uniform(k + i);
+        if (ok && !give_up && elect_one()) {
+          scores(ku, su);
         }
         __syncwarp();
       }
@@ -217,11 +224,11 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
         ok = arrived(v) && ok;
         const int have = end - (rs.t0 + i) * SP;
         const int from = max(common - (rs.t0 + i) * SP, 0);
-        if (ok && (have < SP || from < SP)) {
+        if (have < SP || from < SP) {  // (the same in all of these warps)
           uint8_t* vb = kv_op + v % ST * W::KVB;
           // words of 16 bytes of the rows a .. b: f(word) where it is to be written
           auto each = [&](int a, int b, auto f) {
-            for (int x = a * NG * 8 + lane; x < b * NG * 8; x += 32)
+            for (int x = a * NG * 8 + lane + 32 * tile; x < b * NG * 8; x += 32 * TB)
               f(*reinterpret_cast<uint4*>(vb + (x / 8 % NG) * SP * 128 + x / (8 * NG) * 128 + x % 8 * 16));
           };
           each(max(have, 0), SP, [](uint4& x) { x = make_uint4(0, 0, 0, 0); });
@@ -237,32 +244,33 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
+          if constexpr (TB > 1) {  // (a wait like the others: bounded)
+            if (lane == 0) arrive(smem_addr(&v_clean));
+            ok = wait_for(smem_addr(&v_clean), n_clean++ & 1, &give_up, p.a.status) && ok;
+          }
         }
-        const uint64_t vd = operand(smem_addr(kv_op + v % ST * W::KVB), SP * 128);
+        const uint32_t vu = uniform(v), knu = uniform(kn), ku = uniform(k);
+        const uint64_t vd = operand(kvu + vu % ST * W::KVB, SP * 128);
+        if (next) ok = arrived(kn) && ok;
+        // the weights come in halves of 64 positions
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-          ok = bar_wait(smem_addr(&p_full[t][k % NS]), (k / NS) & 1, &give_up, p.a.status) && ok;
+        for (int h = 0; h < 2; ++h) {
+          ok = wait_for(smem_addr(&p_full[tile][k % NS][h]), (k / NS) & 1, &give_up, p.a.status) && ok;
           after_sync();
-          if (lane == 0 && ok && !give_up) {
-            const uint32_t base = tm + W::TM * t, to = base + W::SUMS;
+          if (ok && !give_up && elect_one()) {
 #pragma unroll
             for (int x = W::P - 1; x >= 0; --x) {  // the weights' low parts first
-              const uint32_t pw = x < 2 ? base + 128 * (k % NS) + 64 * x : base + W::THIRD + 64 * (k % NS);
+              const uint32_t pw = x < 2 ? tmu + 128 * (ku % NS) + 64 * x : tmu + W::THIRD + 64 * (ku % NS);
 #pragma unroll
-              for (int kk = 0; kk < SP / 16; ++kk)
-                mma_ts(to, pw + 8 * kk, vd + ((kk * 16 * 128) >> 4), id_pv, kk || x < W::P - 1 || i ? 1 : 0);
+              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                mma_ts(tmu + W::SUMS, pw + 8 * kk, vd + ((kk * 16 * 128) >> 4), id_pv, kk || x < W::P - 1 || i ? 1 : 0);
             }
-            commit(smem_addr(&pv_done[t]));
-          }
-          __syncwarp();
-          if (next) {
-            if (t == 0) ok = arrived(kn) && ok;
-            if (lane == 0 && ok && !give_up) {
-              scores(t, k + NS, kn);
-              if (t == TB - 1) commit(smem_addr(&kv_empty[kn % ST]));
+            if (h) {
+              commit(smem_addr(&pv_done[tile]));
+              commit(smem_addr(&kv_empty[vu % ST]));
+              if (next) scores(ku + NS, knu);
             }
           }
-          if (t == TB - 1 && lane == 0 && ok && !give_up) commit(smem_addr(&kv_empty[v % ST]));
           __syncwarp();
         }
       }
@@ -272,42 +280,56 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
     if (give_up) {  // products in flight end before the block does
       int none = 0;
       if (lane == 0) commit(smem_addr(&drain));
-      bar_wait_long(smem_addr(&drain), 0, &none, nullptr);
+      wait_for(smem_addr(&drain), 0, &none, nullptr);
     }
   } else if (w < CW) {  // ---- a query column each
-    const int tile = w >> 2, tt = tid & 127;
+    const int tile = w >> 2;
     // this warp's lanes of its tile's scores and sums
     const uint32_t tm_s = tm + W::TM * tile + ((uint32_t)(32 * (w & 3)) << 16), tm_o = tm_s + W::SUMS;
     uint32_t k = 0;
     RunSays rs;
     const float cf = fabsf(p.c);
+    // word x of row y of this warp's part of the q operand, which also holds the sums on their way out
+    auto place = [&](int y, int x) { return q_op + tile * W::P * W::QT + x / 8 * 128 * 128 + (32 * (w & 3) + y) * 128 + (((x % 8) ^ (y & 7)) << 4); };
     for (uint32_t n_runs = 0; take_run(n_runs, rs); ++n_runs) {
       const int seq = p.n_ctiles == 1 ? rs.e : rs.e / p.n_ctiles, j = rs.e - seq * p.n_ctiles;
       const int col = j * CT + tid;
       const bool there = col < p.cols;
       const int row = there ? row_of(p, col) : 0, hd = rs.head * p.gqa + (there ? col - row * p.gqa : 0);
       const int lim = there && row < rs.nn ? max(0, rs.len - rs.nn + row + 1) : 0;  // positions that it sees
-      {
-        const T* src = reinterpret_cast<const T*>(p.q.p) + seq * p.q.seq + row * p.q.row + hd * p.q.head;
+      {  // the warp's 32 rows of q, a row after another, so that its lanes read them in one piece
         const uint32_t flip = p.c < 0.f ? 0x80008000u : 0u;  // a negative scale goes into q
+        constexpr int AT = W::F32 ? 4 : NG * 8;  // reads in flight
+        const int x = lane % (NG * 8);           // 16-byte word of the operand
+#pragma unroll 1
+        for (int i0 = 0; i0 < NG * 8; i0 += AT) {
+          uint4 h[AT][W::F32 ? 2 : 1];
+          bool some[AT];
 #pragma unroll
-        for (int x = 0; x < HD / 8; ++x) {
-          uint8_t* to = q_op + tile * W::P * W::QT + x / 8 * 128 * 128 + tt * 128 + (((x % 8) ^ (tt & 7)) << 4);
-          if constexpr (W::F32) {
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-            if (lim) {
-              a = __ldg(reinterpret_cast<const float4*>(src + 8 * x));
-              b = __ldg(reinterpret_cast<const float4*>(src + 8 * x + 4));
+          for (int i = 0; i < AT; ++i) {
+            // (a row that is none, or padding, reads another's and counts as 0)
+            const int c = col - lane + (32 * (i0 + i) + lane) / (NG * 8), cc = min(c, p.cols - 1), rw = row_of(p, cc);
+            const T* src = reinterpret_cast<const T*>(p.q.p) + seq * p.q.seq + rw * p.q.row + (rs.head * p.gqa + cc - rw * p.gqa) * p.q.head + 8 * x;
+            some[i] = c < p.cols && rw < rs.nn && rs.len - rs.nn + rw >= 0;
+#pragma unroll
+            for (int z = 0; z < (W::F32 ? 2 : 1); ++z) h[i][z] = __ldg(reinterpret_cast<const uint4*>(src) + z);
+          }
+#pragma unroll
+          for (int i = 0; i < AT; ++i) {
+            uint8_t* to = place((32 * (i0 + i) + lane) / (NG * 8), x);
+            if constexpr (W::F32) {
+              const uint32_t u[8] = {h[i][0].x, h[i][0].y, h[i][0].z, h[i][0].w, h[i][1].x, h[i][1].y, h[i][1].z, h[i][1].w};
+              Parts z[8];
+#pragma unroll
+              for (int y = 0; y < 8; ++y) z[y] = parts_of(some[i] ? __uint_as_float(u[y] ^ (flip & 0x80000000u)) : 0.f);
+#pragma unroll
+              for (int q = 0; q < 3; ++q)
+                *reinterpret_cast<uint4*>(to + q * W::QT) = make_uint4(both(z[0], z[1], q), both(z[2], z[3], q), both(z[4], z[5], q), both(z[6], z[7], q));
+            } else {
+              uint4 v = h[i][0];
+              v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+              *reinterpret_cast<uint4*>(to) = some[i] ? v : make_uint4(0, 0, 0, 0);
             }
-            const Parts y[8] = {parts_of(a.x), parts_of(a.y), parts_of(a.z), parts_of(a.w), parts_of(b.x), parts_of(b.y), parts_of(b.z), parts_of(b.w)};
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-              *reinterpret_cast<uint4*>(to + i * W::QT) = make_uint4(both(y[0], y[1], i) ^ flip, both(y[2], y[3], i) ^ flip,
-                                                                     both(y[4], y[5], i) ^ flip, both(y[6], y[7], i) ^ flip);
-          } else {
-            uint4 h = lim ? __ldg(reinterpret_cast<const uint4*>(src + 8 * x)) : make_uint4(0, 0, 0, 0);
-            h.x ^= flip, h.y ^= flip, h.z ^= flip, h.w ^= flip;
-            *reinterpret_cast<uint4*>(to) = h;
           }
         }
       }
@@ -320,10 +342,16 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
       for (int t = rs.t0; t < rs.t1; ++t, ++k) {
         const bool in = page >= 0 && page < p.a.n_pages;
         if (t + 1 < rs.t1) page = pages[t + 1];
-        const bool ok = bar_wait(smem_addr(&s_full[tile][k % NS]), (k / NS) & 1, &give_up, p.a.status);
+        const bool ok = wait_for(smem_addr(&s_full[tile][k % NS]), (k / NS) & 1, &give_up, p.a.status);
         after_sync();
         if (ok && !give_up) {
           const int vis = in ? lim - t * SP : 0;  // of the step's positions
+          auto given = [&](int h) {  // half of the weights are in TMEM
+            tm_stored();
+            before_sync();
+            __syncwarp();
+            if (lane == 0) arrive(smem_addr(&p_full[tile][k % NS][h]));
+          };
           const uint32_t at = tm_s + 128 * (k % NS);
           auto step = [&](auto cut_) {
             constexpr bool CUT = decltype(cut_)::value;
@@ -344,7 +372,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
               m = nm;
               l *= f;
               if (t > rs.t0) {
-                bar_wait(smem_addr(&pv_done[tile]), (k - 1) & 1, &give_up, p.a.status);  // the sums hold the last step
+                wait_for(smem_addr(&pv_done[tile]), (k - 1) & 1, &give_up, p.a.status);  // the sums hold the last step
                 after_sync();
 #pragma unroll 1
                 for (int c = 0; c < HD; c += 16) {
@@ -366,8 +394,8 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
                 float w2[2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                  const float z = s[c][x + y];
-                  w2[y] = CUT && z == -INFINITY ? 0.f : exp2_fast(fmaf(z, cf, -m));
+                  const float z = exp2_fast(fmaf(s[c][x + y], cf, -m));
+                  w2[y] = CUT && 32 * c + x + y >= vis ? 0.f : z;
                   la[(x + y) & 3] += w2[y];
                 }
 #pragma unroll
@@ -381,55 +409,82 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
                 tm_store16(at + 64 + 16 * c, b[1]);
                 tm_store16(tm_s + W::THIRD + 64 * (k % NS) + 16 * c, b[2]);
               }
+              if (c == 1) given(0);
             }
             l += (la[0] + la[1]) + (la[2] + la[3]);
           };
-          if (__all_sync(0xffffffffu, vis >= SP)) step(std::false_type());
+          // (fp32's three parts are long code, and bound by the products: one form of it)
+          if (!W::F32 && __all_sync(0xffffffffu, vis >= SP)) step(std::false_type());
           else step(std::true_type());
-          tm_stored();
+          given(1);
         }
-        before_sync();
-        __syncwarp();
-        if (lane == 0) arrive(smem_addr(&p_full[tile][k % NS]));
       }
       // ---- the run's end: this column's sums
-      bool ok = bar_wait(smem_addr(&pv_done[tile]), (k - 1) & 1, &give_up, p.a.status);
-      ok = bar_wait(smem_addr(&o_full), n_runs & 1, &give_up, p.a.status) && ok && !give_up;
+      bool ok = wait_for(smem_addr(&pv_done[tile]), (k - 1) & 1, &give_up, p.a.status);
+      ok = wait_for(smem_addr(&o_full), n_runs & 1, &give_up, p.a.status) && ok && !give_up;
       after_sync();
       const bool whole = rs.t0 == 0 && rs.t1 == rs.nt;
       const float f = whole ? 1.f / l : 1.f;
       const bool look = odd[n_runs & 1];
       float* part = p.part + ((size_t)part_slot(blockIdx.x, rs.t0) * CT + tid) * (HD + 4);
-      T* dst = reinterpret_cast<T*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + row * p.out.row + hd * p.out.head;
+      // Through the operand's place in shared memory, so that a warp writes its rows in one piece
+      // each: DP dimensions of 32 rows at a time (the columns' own rows, 16 bytes a lane, took 11,000 cycles).
+      auto leave = [&](auto wide_) {
+        constexpr bool F = decltype(wide_)::value;  // fp32 words
+        constexpr int DP = F ? NG * 32 : HD;
 #pragma unroll 1
-      for (int c = 0; c < HD; c += 16) {
-        float o[16];
-        tm_read16(tm_o + c, o);
-        bool fine = !look;
+        for (int c0 = 0; c0 < HD; c0 += DP) {
+#pragma unroll 1
+          for (int c = c0; c < c0 + DP; c += 32) {
+            float o[32], top = 0.f;
+            tm_read32(tm_o + c, o);
+            bool nan = look;
 #pragma unroll
-        for (int x = 0; x < 16; ++x) fine = fine && is_finite(o[x]);
-        if (!fine && lim && is_finite(l)) {  // (positions that all columns see went through the products as they are)
+            for (int x = 0; x < 32; ++x) top = fmaxf(top, fabsf(o[x])), nan = nan || o[x] != o[x];
+            const bool fine = !nan && is_finite(top);
+            if (!fine && lim && is_finite(l)) {  // (positions that all columns see went through the products as they are)
+#pragma unroll 1
+              for (int q = 0; q < 32; q += 2) {
+                const float2 s = odd_sum<HD>(p.a, seq, rs.head, c + q, rs.t0 * SP, min(lim, rs.t1 * SP));
 #pragma unroll
-          for (int x = 0; x < 16; x += 2) {
-            const float2 s = odd_sum<HD>(p.a, seq, rs.head, c + x, rs.t0 * SP, min(lim, rs.t1 * SP));
-            if (s.x != 0.f) o[x] = s.x;
-            if (s.y != 0.f) o[x + 1] = s.y;
+                for (int x = 0; x < 32; x += 2) {
+                  if (x == q && s.x != 0.f) o[x] = s.x;
+                  if (x == q && s.y != 0.f) o[x + 1] = s.y;
+                }
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = !ok ? NAN : l == 0.f ? 0.f : o[x] * f;
+            if constexpr (F) {
+#pragma unroll
+              for (int x = 0; x < 32; x += 4)
+                *reinterpret_cast<float4*>(place(lane, (c - c0 + x) / 4)) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 32; x += 8)
+                *reinterpret_cast<uint4*>(place(lane, (c + x) / 8)) =
+                    make_uint4(pack2(o[x], o[x + 1]), pack2(o[x + 2], o[x + 3]), pack2(o[x + 4], o[x + 5]), pack2(o[x + 6], o[x + 7]));
+            }
           }
+          __syncwarp();
+#pragma unroll 8
+          for (int i = 0; i < NG * 8; ++i) {
+            const int y = (32 * i + lane) / (NG * 8), x = lane % (NG * 8), c = col - lane + y;
+            if (c >= p.cols) continue;
+            const uint4 v = *reinterpret_cast<const uint4*>(place(y, x));
+            if (!whole) {
+              reinterpret_cast<uint4*>(part + (ptrdiff_t)(y - lane) * (HD + 4) + c0)[x] = v;
+            } else {
+              const int rw = row_of(p, c), at = rs.head * p.gqa + c - rw * p.gqa;
+              T* dst = reinterpret_cast<T*>(const_cast<void*>(p.out.p)) + seq * p.out.seq + rw * p.out.row + at * p.out.head;
+              reinterpret_cast<uint4*>(dst + c0)[x] = v;
+            }
+          }
+          __syncwarp();
         }
-        if (!there) continue;
-#pragma unroll
-        for (int x = 0; x < 16; ++x) o[x] = !ok ? NAN : l == 0.f ? 0.f : o[x] * f;
-        if (whole && !W::F32) {
-#pragma unroll
-          for (int x = 0; x < 16; x += 8)
-            *reinterpret_cast<uint4*>(dst + c + x) =
-                make_uint4(pack2(o[x], o[x + 1]), pack2(o[x + 2], o[x + 3]), pack2(o[x + 4], o[x + 5]), pack2(o[x + 6], o[x + 7]));
-        } else {
-          float* to = whole ? reinterpret_cast<float*>(dst) : part;
-#pragma unroll
-          for (int x = 0; x < 16; x += 4) *reinterpret_cast<float4*>(to + c + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-        }
-      }
+      };
+      if (whole && !W::F32) leave(std::false_type());
+      else leave(std::true_type());
       if (there) {
         if (!whole) *reinterpret_cast<float2*>(part + HD) = l == 0.f ? make_float2(kLow, 0.f) : make_float2(m, ok ? l : NAN);
         else if (p.lse)
