@@ -8,7 +8,7 @@
 // its maximum is its own and moves only when a score passes it by 2^8; then it rescales its
 // sums, which the next product waits for.  An fp32 q is three bf16 parts, and so are its weights.
 //
-// Warps 4 TB: the columns.  One warp more looks up pages and issues the copies, one for each tile its
+// Warps 4 TB: the columns.  One warp more looks up pages and issues the copies, another the
 // products.  With two tiles a block (TB = 2) the tensor cores work on one tile while the
 // columns of the other form weights; with one tile there are two places of scores, so that S of a step
 // runs before the second product of the last.
@@ -44,7 +44,7 @@ struct PWide {
   static constexpr int SUMS = NS * 128, THIRD = SUMS + 128;
   static constexpr int TM = TB == 2 ? 256 : 512;    // of a tile
   static constexpr int CW = 4 * TB;                 // warps of the columns
-  static constexpr int THREADS = 32 * (CW + 1 + TB);
+  static constexpr int THREADS = 32 * (CW + 2);
 };
 
 // What the copying warp says of a run (t1 = t0: there is none more).
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
   const AttArgs& p = pa.t;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024 - (smem_addr(sm_raw) & 1023)) & 1023);
-  __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], s_full[TB][NS], p_full[TB][NS][2], pv_done[TB], q_full, run_full[kRuns], o_full, v_clean, drain;
+  __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], s_full[TB][NS], p_full[TB][NS][2], pv_done[TB], q_full, run_full[kRuns], o_full, drain;
   __shared__ RunSays says[kRuns];
   __shared__ int odd[2];  // a run's V had values that are no finite numbers where columns differ
   __shared__ uint32_t tm_base;
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
     auto init = [](uint64_t* b, int n) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(n) : "memory");
     };
-    for (int i = 0; i < ST; ++i) init(&kv_full[i], 1), init(&kv_empty[i], TB);
+    for (int i = 0; i < ST; ++i) init(&kv_full[i], 1), init(&kv_empty[i], 1);
     for (int t = 0; t < TB; ++t) {
       for (int i = 0; i < NS; ++i) {
         init(&s_full[t][i], 1);
@@ -84,9 +84,8 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
     }
     init(&q_full, CW);
     for (int i = 0; i < kRuns; ++i) init(&run_full[i], 1);
-    init(&o_full, TB);
-    init(&v_clean, TB);
-    init(&drain, TB);
+    init(&o_full, 1);
+    init(&drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     give_up = 0;
     odd[0] = odd[1] = 0;
@@ -171,21 +170,23 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
       int none = 0;
       for (uint32_t i = slot > ST ? slot - ST : 0; i < slot; ++i) wait_for(smem_addr(&kv_full[i % ST]), (i / ST) & 1, &none, nullptr);
     }
-  } else if (w > CW && w <= CW + TB) {  // ---- the products of a tile
-    const int tile = TB == 1 ? 0 : w - CW - 1;
+  } else if (w == CW + 1) {  // ---- the products
     constexpr uint32_t id_qk = (1u << 4) | (1u << 7) | (1u << 10) | ((SP >> 3) << 17) | ((128 >> 4) << 24);               // bf16, fp32 sums
     constexpr uint32_t id_pv = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((HD >> 3) << 17) | ((128 >> 4) << 24);  // V by rows
-    uint32_t slot = 0, k = 0;  // stages and steps taken
-    [[maybe_unused]] uint32_t n_clean = 0;
+    const uint32_t tmu = uniform(tm), qu = uniform(smem_addr(q_op)), kvu = uniform(smem_addr(kv_op));
+    uint32_t st = 0, round = 0, k = 0;  // the next stage and its phase, steps taken
     RunSays rs;
-    auto arrived = [&](uint32_t s) { return wait_for(smem_addr(&kv_full[s % ST]), (s / ST) & 1, &give_up, p.a.status); };
-    const uint32_t tmu = uniform(tm + W::TM * tile), qu = uniform(smem_addr(q_op + tile * W::P * W::QT)), kvu = uniform(smem_addr(kv_op));
-    auto scores = [&](uint32_t step, uint32_t s) {  // one lane: of the step into its place
-      const uint32_t to = tmu + 128 * (step % NS);
-      const uint64_t kd = operand(kvu + s % ST * W::KVB);
+    bool ok = true;
+    auto arrived = [&]() { ok = wait_for(smem_addr(&kv_full[st]), round, &give_up, p.a.status) && ok; };
+    auto advance = [&]() {
+      if (++st == ST) st = 0, round ^= 1;
+    };
+    auto scores = [&](int tile, uint32_t place, uint32_t stage) {  // one lane: of a tile into its place
+      const uint32_t to = tmu + W::TM * tile + 128 * place;
+      const uint64_t kd = operand(kvu + stage * W::KVB);
 #pragma unroll
       for (int x = W::P - 1; x >= 0; --x) {  // q's low parts first
-        const uint64_t q = operand(qu + x * W::QT);
+        const uint64_t q = operand(qu + (tile * W::P + x) * W::QT);
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -195,40 +196,45 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
             else mma_ss<true>(to, qa, kb, id_qk);
           }
       }
-      commit(smem_addr(&s_full[tile][step % NS]));
-      commit(smem_addr(&kv_empty[s % ST]));
+      commit(smem_addr(&s_full[tile][place]));
+      if (tile == TB - 1) commit(smem_addr(&kv_empty[stage]));
     };
     for (uint32_t n_runs = 0; take_run(n_runs, rs); ++n_runs) {
       const int n = rs.t1 - rs.t0, seq = p.n_ctiles == 1 ? rs.e : rs.e / p.n_ctiles, j = rs.e - seq * p.n_ctiles;
       const int last = min(row_of(p, min((j + 1) * CT, p.cols) - 1), rs.nn - 1);
       const int end = rs.len - rs.nn + last + 1;                                    // what some column sees
       const int common = max(0, rs.len - rs.nn + row_of(p, j * CT) + 1);            // what all columns (with a row) do
-      bool ok = wait_for(smem_addr(&q_full), n_runs & 1, &give_up, p.a.status);
-      // The second tile begins when the first has its first weights, so that one forms weights while the
-      // other's products run (both at once: 4,500 cycles a step, in turn 3,100).
-      if (TB > 1 && tile) ok = wait_for(smem_addr(&p_full[0][0][0]), k & 1, &give_up, p.a.status) && ok;
-      if (lane == 0 && tile == 0) odd[(n_runs + 1) & 1] = 0;  // which the columns have read: the next run's
-      for (int i = 0; i < NS && i < n; ++i, ++slot) {
-        ok = arrived(slot) && ok;
+      ok = wait_for(smem_addr(&q_full), n_runs & 1, &give_up, p.a.status) && ok;
+      if (lane == 0) odd[(n_runs + 1) & 1] = 0;  // which the columns have read: the next run's
+      for (int i = 0; i < NS && i < n; ++i) {
+        arrived();
         after_sync();
-        const uint32_t su = uniform(slot), ku = uniform(k + i);
+        const uint32_t su = uniform(st), pu = uniform((k + i) % NS);
         if (ok && !give_up && elect_one()) {
-          scores(ku, su);
+#pragma unroll
+          for (int t = 0; t < TB; ++t) scores(t, pu, su);
         }
         __syncwarp();
+        advance();
       }
       for (int i = 0; i < n; ++i, ++k) {
-        const uint32_t v = slot++, kn = slot;
         const bool next = i + NS < n;
-        if (next) ++slot;
-        ok = arrived(v) && ok;
+        const uint32_t v = uniform(st);
+        arrived();
+        advance();
+        const uint32_t kn = uniform(st), pu = uniform(k % NS);
+        if (next) {
+          arrived();
+          advance();
+        }
         const int have = end - (rs.t0 + i) * SP;
         const int from = max(common - (rs.t0 + i) * SP, 0);
-        if (have < SP || from < SP) {  // (the same in all of these warps)
-          uint8_t* vb = kv_op + v % ST * W::KVB;
+        if (ok && (have < SP || from < SP)) {
+          uint8_t* vb = kv_op + v * W::KVB;
           // words of 16 bytes of the rows a .. b: f(word) where it is to be written
           auto each = [&](int a, int b, auto f) {
-            for (int x = a * NG * 8 + lane + 32 * tile; x < b * NG * 8; x += 32 * TB)
+#pragma unroll 4
+            for (int x = a * NG * 8 + lane; x < b * NG * 8; x += 32)
               f(*reinterpret_cast<uint4*>(vb + (x / 8 % NG) * SP * 128 + x / (8 * NG) * 128 + x % 8 * 16));
           };
           each(max(have, 0), SP, [](uint4& x) { x = make_uint4(0, 0, 0, 0); });
@@ -244,34 +250,33 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if constexpr (TB > 1) {  // (a wait like the others: bounded)
-            if (lane == 0) arrive(smem_addr(&v_clean));
-            ok = wait_for(smem_addr(&v_clean), n_clean++ & 1, &give_up, p.a.status) && ok;
-          }
         }
-        const uint32_t vu = uniform(v), knu = uniform(kn), ku = uniform(k);
-        const uint64_t vd = operand(kvu + vu % ST * W::KVB, SP * 128);
-        if (next) ok = arrived(kn) && ok;
-        // the weights come in halves of 64 positions
+        const uint64_t vd = operand(kvu + v * W::KVB, SP * 128);
+        const uint32_t add = uniform(i ? 1 : 0), nu = uniform(next), lu = uniform(i + 1 == n);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          ok = wait_for(smem_addr(&p_full[tile][k % NS][h]), (k / NS) & 1, &give_up, p.a.status) && ok;
-          after_sync();
-          if (ok && !give_up && elect_one()) {
+        for (int t = 0; t < TB; ++t) {
+          // the weights come in halves of 64 positions
 #pragma unroll
-            for (int x = W::P - 1; x >= 0; --x) {  // the weights' low parts first
-              const uint32_t pw = x < 2 ? tmu + 128 * (ku % NS) + 64 * x : tmu + W::THIRD + 64 * (ku % NS);
+          for (int h = 0; h < 2; ++h) {
+            ok = wait_for(smem_addr(&p_full[t][pu][h]), (k / NS) & 1, &give_up, p.a.status) && ok;
+            after_sync();
+            if (ok && !give_up && elect_one()) {
+              const uint32_t base = tmu + W::TM * t;
 #pragma unroll
-              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                mma_ts(tmu + W::SUMS, pw + 8 * kk, vd + ((kk * 16 * 128) >> 4), id_pv, kk || x < W::P - 1 || i ? 1 : 0);
+              for (int x = W::P - 1; x >= 0; --x) {  // the weights' low parts first
+                const uint32_t pw = x < 2 ? base + 128 * pu + 64 * x : base + W::THIRD + 64 * pu;
+#pragma unroll
+                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                  mma_ts(base + W::SUMS, pw + 8 * kk, vd + ((kk * 16 * 128) >> 4), id_pv, kk || x < W::P - 1 ? 1 : add);
+              }
+              if (h) {
+                if (t == TB - 1) commit(smem_addr(&kv_empty[v]));
+                if (NS > 1 || lu) commit(smem_addr(&pv_done[t]));
+                if (nu) scores(t, pu, kn);
+              }
             }
-            if (h) {
-              commit(smem_addr(&pv_done[tile]));
-              commit(smem_addr(&kv_empty[vu % ST]));
-              if (next) scores(ku + NS, knu);
-            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
       if (lane == 0) arrive(smem_addr(&o_full));
@@ -372,8 +377,10 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
               m = nm;
               l *= f;
               if (t > rs.t0) {
-                wait_for(smem_addr(&pv_done[tile]), (k - 1) & 1, &give_up, p.a.status);  // the sums hold the last step
-                after_sync();
+                if (NS > 1) {  // the sums hold the last step (with one place of scores these have waited for it)
+                  wait_for(smem_addr(&pv_done[tile]), (k - 1) & 1, &give_up, p.a.status);
+                  after_sync();
+                }
 #pragma unroll 1
                 for (int c = 0; c < HD; c += 16) {
                   float o[16];
@@ -420,7 +427,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
         }
       }
       // ---- the run's end: this column's sums
-      bool ok = wait_for(smem_addr(&pv_done[tile]), (k - 1) & 1, &give_up, p.a.status);
+      bool ok = wait_for(smem_addr(&pv_done[tile]), (NS > 1 ? k - 1 : n_runs) & 1, &give_up, p.a.status);
       ok = wait_for(smem_addr(&o_full), n_runs & 1, &give_up, p.a.status) && ok && !give_up;
       after_sync();
       const bool whole = rs.t0 == 0 && rs.t1 == rs.nt;
