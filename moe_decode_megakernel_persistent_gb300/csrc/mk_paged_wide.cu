@@ -177,9 +177,12 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
     uint32_t st = 0, round = 0, k = 0;  // the next stage and its phase, steps taken
     RunSays rs;
     bool ok = true;
-    auto arrived = [&]() { ok = wait_for(smem_addr(&kv_full[st]), round, &give_up, p.a.status) && ok; };
-    auto advance = [&]() {
+    // the next stage, once it has arrived
+    auto arrived = [&]() {
+      ok = wait_for(smem_addr(&kv_full[st]), round, &give_up, p.a.status) && ok;
+      const uint32_t got = uniform(st);
       if (++st == ST) st = 0, round ^= 1;
+      return got;
     };
     auto scores = [&](int tile, uint32_t place, uint32_t stage) {  // one lane: of a tile into its place
       const uint32_t to = tmu + W::TM * tile + 128 * place;
@@ -207,52 +210,46 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
       ok = wait_for(smem_addr(&q_full), n_runs & 1, &give_up, p.a.status) && ok;
       if (lane == 0) odd[(n_runs + 1) & 1] = 0;  // which the columns have read: the next run's
       for (int i = 0; i < NS && i < n; ++i) {
-        arrived();
+        const uint32_t su = arrived(), pu = uniform((k + i) % NS);
         after_sync();
-        const uint32_t su = uniform(st), pu = uniform((k + i) % NS);
-        if (ok && !give_up && elect_one()) {
+        if (ok && elect_one()) {
 #pragma unroll
           for (int t = 0; t < TB; ++t) scores(t, pu, su);
         }
         __syncwarp();
-        advance();
       }
-      for (int i = 0; i < n; ++i, ++k) {
-        const bool next = i + NS < n;
-        const uint32_t v = uniform(st);
-        arrived();
-        advance();
-        const uint32_t kn = uniform(st), pu = uniform(k % NS);
-        if (next) {
-          arrived();
-          advance();
-        }
+      // V of a step in its stage, with zeros where no column sees it and for what is no finite number where columns differ
+      auto clean = [&](int i, uint32_t v) {
         const int have = end - (rs.t0 + i) * SP;
         const int from = max(common - (rs.t0 + i) * SP, 0);
-        if (ok && (have < SP || from < SP)) {
-          uint8_t* vb = kv_op + v * W::KVB;
-          // words of 16 bytes of the rows a .. b: f(word) where it is to be written
-          auto each = [&](int a, int b, auto f) {
+        if (!ok || (have >= SP && from >= SP)) return;
+        uint8_t* vb = kv_op + v * W::KVB;
+        // words of 16 bytes of the rows a .. b: f(word) where it is to be written
+        auto each = [&](int a, int b, auto f) {
 #pragma unroll 4
-            for (int x = a * NG * 8 + lane; x < b * NG * 8; x += 32)
-              f(*reinterpret_cast<uint4*>(vb + (x / 8 % NG) * SP * 128 + x / (8 * NG) * 128 + x % 8 * 16));
+          for (int x = a * NG * 8 + lane; x < b * NG * 8; x += 32)
+            f(*reinterpret_cast<uint4*>(vb + (x / 8 % NG) * SP * 128 + x / (8 * NG) * 128 + x % 8 * 16));
+        };
+        each(max(have, 0), SP, [](uint4& x) { x = make_uint4(0, 0, 0, 0); });
+        uint32_t any = 0;
+        each(from, min(have, SP), [&](uint4& x) { any |= odd_ones(x.x) | odd_ones(x.y) | odd_ones(x.z) | odd_ones(x.w); });
+        if (__any_sync(0xffffffffu, any)) {
+          auto clear = [](uint32_t& x) {
+            const uint32_t bad = odd_ones(x);
+            x &= ~((bad >> 15 & 1u) * 0xFFFFu | (bad >> 31) * 0xFFFF0000u);
           };
-          each(max(have, 0), SP, [](uint4& x) { x = make_uint4(0, 0, 0, 0); });
-          uint32_t any = 0;
-          each(from, min(have, SP), [&](uint4& x) { any |= odd_ones(x.x) | odd_ones(x.y) | odd_ones(x.z) | odd_ones(x.w); });
-          if (__any_sync(0xffffffffu, any)) {
-            auto clear = [](uint32_t& x) {
-              const uint32_t bad = odd_ones(x);
-              x &= ~((bad >> 15 & 1u) * 0xFFFFu | (bad >> 31) * 0xFFFF0000u);
-            };
-            each(from, min(have, SP), [&](uint4& x) { clear(x.x), clear(x.y), clear(x.z), clear(x.w); });
-            if (lane == 0) odd[n_runs & 1] = 1;
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
+          each(from, min(have, SP), [&](uint4& x) { clear(x.x), clear(x.y), clear(x.z), clear(x.w); });
+          if (lane == 0) odd[n_runs & 1] = 1;
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      };
+      uint32_t v = arrived(), kn = NS < n ? arrived() : 0;
+      clean(0, v);
+      for (int i = 0; i < n; ++i, ++k) {
+        const uint32_t pu = uniform(k % NS), add = uniform(i ? 1 : 0), nu = uniform(i + NS < n), lu = uniform(i + 1 == n);
         const uint64_t vd = operand(kvu + v * W::KVB, SP * 128);
-        const uint32_t add = uniform(i ? 1 : 0), nu = uniform(next), lu = uniform(i + 1 == n);
+        uint32_t vn = 0, kn2 = 0;
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
           // the weights come in halves of 64 positions
@@ -260,7 +257,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
           for (int h = 0; h < 2; ++h) {
             ok = wait_for(smem_addr(&p_full[t][pu][h]), (k / NS) & 1, &give_up, p.a.status) && ok;
             after_sync();
-            if (ok && !give_up && elect_one()) {
+            if (ok && elect_one()) {
               const uint32_t base = tmu + W::TM * t;
 #pragma unroll
               for (int x = W::P - 1; x >= 0; --x) {  // the weights' low parts first
@@ -276,8 +273,17 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
               }
             }
             __syncwarp();
+            // The next step's operands are waited for behind products: the queue holds a few of them, and
+            // what takes longer between two groups leaves the tensor cores idle.
+            if (t == 0 && h == 0 && i + 1 < n) {
+              vn = arrived();
+              clean(i + 1, vn);
+            }
+            if (t == TB - 1 && h == (TB == 1) && i + 1 + NS < n) kn2 = arrived();
           }
         }
+        v = vn;
+        kn = kn2;
       }
       if (lane == 0) arrive(smem_addr(&o_full));
       if (!ok || give_up) break;
