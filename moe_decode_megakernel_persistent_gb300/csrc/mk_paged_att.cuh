@@ -84,6 +84,32 @@ __device__ __forceinline__ float2 odd_sum(const Kv4Args& a, int seq, int head, i
   }
   return s;
 }
+// Pairs of fp32 in one instruction, and the largest of three.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t z;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(x), "f"(y));
+  return z;
+}
+__device__ __forceinline__ float2 unpair(uint64_t z) {
+  float2 x;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(z));
+  return x;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 // The wide kernel (mk_paged_wide.cu): tiles of CT columns and SP positions; null: none.

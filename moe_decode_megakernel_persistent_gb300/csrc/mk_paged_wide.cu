@@ -34,16 +34,18 @@ struct PWide {
   static constexpr int NG = HD / 64, CT = 128 * TB, SP = kPageTokens;
   static constexpr int P = F32 ? 3 : 1;             // bf16 parts of q, and of the weights
   static constexpr int NS = TB == 1 ? 2 : 1;        // places of scores of a tile
+  static constexpr int GR = NS;                     // groups of four warps of a tile, which take the steps in turn
   static constexpr int QT = NG * 128 * 128;         // bytes of a tile's q of one part
   static constexpr int QB = TB * P * QT;
   static constexpr int KVB = NG * SP * 128;         // of a page's K, or V, of a head
-  static constexpr int ROOM = (226 * 1024 - QB) / KVB;
-  static constexpr int STAGES = ROOM < 6 ? ROOM : 6;
-  static constexpr int SMEM = 1024 + QB + STAGES * KVB;
+  static constexpr int ROOM = (225 * 1024 - QB) / KVB;
+  static constexpr int STAGES = F32 && HD == 128 ? 4 : ROOM < 6 ? ROOM : 6;
+  static constexpr int EX = GR > 1 ? 3 * CT * 4 : 0;  // what the groups tell each other: maxima, two sums
+  static constexpr int SMEM = 1024 + QB + STAGES * KVB + EX;
   // TMEM columns of a tile: scores [NS][128], sums [HD], and with three parts the third of the weights [NS][64]
   static constexpr int SUMS = NS * 128, THIRD = SUMS + 128;
   static constexpr int TM = TB == 2 ? 256 : 512;    // of a tile
-  static constexpr int CW = 4 * TB;                 // warps of the columns
+  static constexpr int CW = 4 * TB * GR;            // warps of the columns: eight
   static constexpr int THREADS = 32 * (CW + 2);
 };
 
@@ -52,16 +54,16 @@ struct RunSays {
   int e, head, nt, t0, t1, len, nn;
   long long base;
 };
-constexpr int kRuns = 8;  // the copying warp is at most five runs ahead of the columns
+constexpr int kRuns = 5;  // the copying warp is at most four runs ahead of the columns
 
 template <int HD, class T, int TB>
 __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(const __grid_constant__ PagedAtt pa, const __grid_constant__ CUtensorMap map) {
   using W = PWide<HD, T, TB>;
-  constexpr int NG = W::NG, CT = W::CT, SP = W::SP, NS = W::NS, CW = W::CW, ST = W::STAGES;
+  constexpr int NG = W::NG, CT = W::CT, SP = W::SP, NS = W::NS, GR = W::GR, CW = W::CW, ST = W::STAGES;
   const AttArgs& p = pa.t;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024 - (smem_addr(sm_raw) & 1023)) & 1023);
-  __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], s_full[TB][NS], p_full[TB][NS][2], pv_done[TB], q_full, run_full[kRuns], o_full, drain;
+  __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], s_full[TB][NS], p_full[TB][NS][2], pv_done, run_done[TB], q_full, run_full[kRuns], o_full, m_full[GR][4], l_full, drain;
   __shared__ RunSays says[kRuns];
   __shared__ int odd[2];  // a run's V had values that are no finite numbers where columns differ
   __shared__ uint32_t tm_base;
@@ -80,8 +82,11 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
         init(&s_full[t][i], 1);
         for (int h = 0; h < 2; ++h) init(&p_full[t][i][h], 4);  // by each of the tile's warps (of which one may be a place of scores ahead)
       }
-      init(&pv_done[t], 1);
+      init(&run_done[t], 1);
     }
+    init(&pv_done, 1);
+    for (int i = 0; i < 4 * GR; ++i) init(&m_full[i >> 2][i & 3], 1);
+    init(&l_full, CW);
     init(&q_full, CW);
     for (int i = 0; i < kRuns; ++i) init(&run_full[i], 1);
     init(&o_full, 1);
@@ -268,7 +273,8 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
               }
               if (h) {
                 if (t == TB - 1) commit(smem_addr(&kv_empty[v]));
-                if (NS > 1 || lu) commit(smem_addr(&pv_done[t]));
+                if (NS > 1) commit(smem_addr(&pv_done));
+                if (lu) commit(smem_addr(&run_done[t]));
                 if (nu) scores(t, pu, kn);
               }
             }
@@ -294,26 +300,29 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
       wait_for(smem_addr(&drain), 0, &none, nullptr);
     }
   } else if (w < CW) {  // ---- a query column each
-    const int tile = w >> 2;
+    // With one tile a column has two threads, which take the steps in turn: a step's maximum passes
+    // from one to the other before its exponentials, and each has the sum of its own steps' weights.
+    const int tile = GR > 1 ? 0 : w >> 2, group = GR > 1 ? w >> 2 : 0, quarter = w & 3, me = GR > 1 ? tid & 127 : tid;
     // this warp's lanes of its tile's scores and sums
-    const uint32_t tm_s = tm + W::TM * tile + ((uint32_t)(32 * (w & 3)) << 16), tm_o = tm_s + W::SUMS;
+    const uint32_t tm_s = tm + W::TM * tile + ((uint32_t)(32 * quarter) << 16), tm_o = tm_s + W::SUMS;
+    [[maybe_unused]] float* ex = reinterpret_cast<float*>(kv_op + ST * W::KVB);  // maxima [CT], sums [2][CT]
     uint32_t k = 0;
     RunSays rs;
     const float cf = fabsf(p.c);
-    // word x of row y of this warp's part of the q operand, which also holds the sums on their way out
-    auto place = [&](int y, int x) { return q_op + tile * W::P * W::QT + x / 8 * 128 * 128 + (32 * (w & 3) + y) * 128 + (((x % 8) ^ (y & 7)) << 4); };
+    // word x of row y of these lanes' part of the q operand, which also holds the sums on their way out
+    auto place = [&](int y, int x) { return q_op + tile * W::P * W::QT + x / 8 * 128 * 128 + (32 * quarter + y) * 128 + (((x % 8) ^ (y & 7)) << 4); };
     for (uint32_t n_runs = 0; take_run(n_runs, rs); ++n_runs) {
       const int seq = p.n_ctiles == 1 ? rs.e : rs.e / p.n_ctiles, j = rs.e - seq * p.n_ctiles;
-      const int col = j * CT + tid;
+      const int col = j * CT + me;
       const bool there = col < p.cols;
       const int row = there ? row_of(p, col) : 0, hd = rs.head * p.gqa + (there ? col - row * p.gqa : 0);
       const int lim = there && row < rs.nn ? max(0, rs.len - rs.nn + row + 1) : 0;  // positions that it sees
-      {  // the warp's 32 rows of q, a row after another, so that its lanes read them in one piece
+      {  // these lanes' 32 rows of q, a row after another, so that a warp reads them in one piece
         const uint32_t flip = p.c < 0.f ? 0x80008000u : 0u;  // a negative scale goes into q
-        constexpr int AT = W::F32 ? 4 : NG * 8;  // reads in flight
-        const int x = lane % (NG * 8);           // 16-byte word of the operand
+        constexpr int ALL = NG * 8 / GR, AT = W::F32 ? 4 : ALL;  // reads, and reads in flight
+        const int x = lane % (NG * 8);                           // 16-byte word of the operand
 #pragma unroll 1
-        for (int i0 = 0; i0 < NG * 8; i0 += AT) {
+        for (int i0 = group * ALL; i0 < (group + 1) * ALL; i0 += AT) {
           uint4 h[AT][W::F32 ? 2 : 1];
           bool some[AT];
 #pragma unroll
@@ -348,12 +357,14 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
       __syncwarp();
       if (lane == 0) arrive(smem_addr(&q_full));
       const int32_t* pages = table_row(p.a, seq);
-      int page = pages[rs.t0];
-      float m = kLow, l = 0.f;  // running maximum (log2) and the sum of the weights
-      for (int t = rs.t0; t < rs.t1; ++t, ++k) {
+      const int skip = GR > 1 ? (k ^ group) & 1 : 0;  // the group's first step of the run
+      int page = rs.t0 + skip < rs.t1 ? pages[rs.t0 + skip] : -1;
+      float m = kLow, l = 0.f;  // running maximum (log2) that l is relative to, and the sum of the weights
+      for (int t = rs.t0 + skip; t < rs.t1; t += GR) {
+        const uint32_t kk = k + (t - rs.t0);
         const bool in = page >= 0 && page < p.a.n_pages;
-        if (t + 1 < rs.t1) page = pages[t + 1];
-        const bool ok = wait_for(smem_addr(&s_full[tile][k % NS]), (k / NS) & 1, &give_up, p.a.status);
+        if (t + GR < rs.t1) page = pages[t + GR];
+        bool ok = wait_for(smem_addr(&s_full[tile][kk % NS]), (kk / NS) & 1, &give_up, p.a.status);
         after_sync();
         if (ok && !give_up) {
           const int vis = in ? lim - t * SP : 0;  // of the step's positions
@@ -361,9 +372,9 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
             tm_stored();
             before_sync();
             __syncwarp();
-            if (lane == 0) arrive(smem_addr(&p_full[tile][k % NS][h]));
+            if (lane == 0) arrive(smem_addr(&p_full[tile][kk % NS][h]));
           };
-          const uint32_t at = tm_s + 128 * (k % NS);
+          const uint32_t at = tm_s + 128 * (kk % NS);
           auto step = [&](auto cut_) {
             constexpr bool CUT = decltype(cut_)::value;
             float s[4][32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -371,120 +382,148 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
             for (int c = 0; c < 4; ++c) {
               tm_read32(at + 32 * c, s[c]);
 #pragma unroll
-              for (int x = 0; x < 32; ++x) {
+              for (int x = 0; x < 32; x += 2) {
                 if (CUT && 32 * c + x >= vis) s[c][x] = -INFINITY;
-                mx[x & 3] = fmaxf(mx[x & 3], s[c][x]);
+                if (CUT && 32 * c + x + 1 >= vis) s[c][x + 1] = -INFINITY;
+                mx[x / 2 & 3] = max3(mx[x / 2 & 3], s[c][x], s[c][x + 1]);
               }
             }
             float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             most = most == -INFINITY ? most : most * cf;
-            if (__any_sync(0xffffffffu, most > m + kLazy)) {
-              const float nm = fmaxf(m, most), f = exp2_fast(m - nm);
-              m = nm;
-              l *= f;
+            float last = m;  // the column's maximum so far, which the sums are relative to
+            if constexpr (GR > 1) {
+              last = kLow;
               if (t > rs.t0) {
-                if (NS > 1) {  // the sums hold the last step (with one place of scores these have waited for it)
-                  wait_for(smem_addr(&pv_done[tile]), (k - 1) & 1, &give_up, p.a.status);
-                  after_sync();
-                }
-#pragma unroll 1
-                for (int c = 0; c < HD; c += 16) {
-                  float o[16];
-                  uint32_t x16[16];
-                  tm_read16(tm_o + c, o);
-#pragma unroll
-                  for (int x = 0; x < 16; ++x) x16[x] = __float_as_uint(o[x] * f);
-                  tm_store16(tm_o + c, x16);
-                }
+                wait_for(smem_addr(&m_full[group ^ 1][quarter]), ((kk - 1) >> 1) & 1, &give_up, p.a.status);
+                last = *reinterpret_cast<volatile float*>(ex + me);
               }
             }
-            float la[4] = {0.f, 0.f, 0.f, 0.f};
+            float now = last;
+            const bool moves = __any_sync(0xffffffffu, most > last + kLazy);
+            if (moves) now = fmaxf(last, most);
+            if constexpr (GR > 1) {
+              ex[me] = now;
+              __syncwarp();
+              if (lane == 0) arrive(smem_addr(&m_full[group][quarter]));
+            }
+            l *= exp2_fast(m - now);
+            m = now;
+            if (moves && t > rs.t0) {
+              if constexpr (NS > 1) {  // the sums hold the last step (with one place of scores these have waited for it)
+                wait_for(smem_addr(&pv_done), (kk - 1) & 1, &give_up, p.a.status);
+                after_sync();
+              }
+              const float f = exp2_fast(last - now);
+#pragma unroll 1
+              for (int c = 0; c < HD; c += 16) {
+                float o[16];
+                uint32_t x16[16];
+                tm_read16(tm_o + c, o);
+#pragma unroll
+                for (int x = 0; x < 16; ++x) x16[x] = __float_as_uint(o[x] * f);
+                tm_store16(tm_o + c, x16);
+              }
+            }
+            const uint64_t cf2 = pair(cf, cf), sub2 = pair(-m, -m);
+            uint64_t la[2] = {0, 0};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t b[W::P][16];
 #pragma unroll
               for (int x = 0; x < 32; x += 2) {
-                float w2[2];
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  const float z = exp2_fast(fmaf(s[c][x + y], cf, -m));
-                  w2[y] = CUT && 32 * c + x + y >= vis ? 0.f : z;
-                  la[(x + y) & 3] += w2[y];
-                }
+                float2 z = unpair(fma2(pair(s[c][x], s[c][x + 1]), cf2, sub2));
+                z.x = exp2_fast(z.x), z.y = exp2_fast(z.y);
+                if (CUT && 32 * c + x >= vis) z.x = 0.f;
+                if (CUT && 32 * c + x + 1 >= vis) z.y = 0.f;
+                la[x / 2 & 1] = add2(la[x / 2 & 1], pair(z.x, z.y));
 #pragma unroll
                 for (int i = 0; i < W::P; ++i) {
-                  b[i][x / 2] = pack2(w2[0], w2[1]);
-                  if (i + 1 < W::P) w2[0] -= low_f(b[i][x / 2]), w2[1] -= high_f(b[i][x / 2]);
+                  b[i][x / 2] = pack2(z.x, z.y);
+                  if (i + 1 < W::P) z.x -= low_f(b[i][x / 2]), z.y -= high_f(b[i][x / 2]);
                 }
               }
               tm_store16(at + 16 * c, b[0]);  // over the scores, which are all in registers
               if constexpr (W::P == 3) {
                 tm_store16(at + 64 + 16 * c, b[1]);
-                tm_store16(tm_s + W::THIRD + 64 * (k % NS) + 16 * c, b[2]);
+                tm_store16(tm_s + W::THIRD + 64 * (kk % NS) + 16 * c, b[2]);
               }
               if (c == 1) given(0);
             }
-            l += (la[0] + la[1]) + (la[2] + la[3]);
+            const float2 a = unpair(add2(la[0], la[1]));
+            l += a.x + a.y;
           };
-          // (fp32's three parts are long code, and bound by the products: one form of it)
-          if (!W::F32 && __all_sync(0xffffffffu, vis >= SP)) step(std::false_type());
+          if (__all_sync(0xffffffffu, vis >= SP)) step(std::false_type());
           else step(std::true_type());
           given(1);
         }
       }
+      k += rs.t1 - rs.t0;
       // ---- the run's end: this column's sums
-      bool ok = wait_for(smem_addr(&pv_done[tile]), (NS > 1 ? k - 1 : n_runs) & 1, &give_up, p.a.status);
+      bool ok = wait_for(smem_addr(&run_done[tile]), n_runs & 1, &give_up, p.a.status);
       ok = wait_for(smem_addr(&o_full), n_runs & 1, &give_up, p.a.status) && ok && !give_up;
       after_sync();
+      if constexpr (GR > 1) {  // both threads' sums, relative to the last maximum
+        const float now = ex[me];
+        ex[CT * (1 + group) + me] = l * exp2_fast(m - now);
+        m = now;
+        __syncwarp();
+        if (lane == 0) arrive(smem_addr(&l_full));
+        ok = wait_for(smem_addr(&l_full), n_runs & 1, &give_up, p.a.status) && ok;
+        l = ex[CT + me] + ex[2 * CT + me];
+      }
       const bool whole = rs.t0 == 0 && rs.t1 == rs.nt;
       const float f = whole ? 1.f / l : 1.f;
       const bool look = odd[n_runs & 1];
-      float* part = p.part + ((size_t)part_slot(blockIdx.x, rs.t0) * CT + tid) * (HD + 4);
+      float* part = p.part + ((size_t)part_slot(blockIdx.x, rs.t0) * CT + me) * (HD + 4);
       // Through the operand's place in shared memory, so that a warp writes its rows in one piece
-      // each: DP dimensions of 32 rows at a time (the columns' own rows, 16 bytes a lane, took 11,000 cycles).
+      // each (the columns' own rows, 16 bytes a lane, took 11,000 cycles).  A group takes its half of the dimensions
+      // in words of its own: of another part of q, or its half of a row's.
       auto leave = [&](auto wide_) {
-        constexpr bool F = decltype(wide_)::value;  // fp32 words
-        constexpr int DP = F ? NG * 32 : HD;
+        constexpr bool F = decltype(wide_)::value;                                    // fp32 words
+        constexpr int WORDS = GR > 1 && W::P == 1 ? NG * 4 : NG * 8;                  // 16-byte words of a row
+        constexpr int DP = WORDS * (F ? 4 : 8), CH = DP < 32 ? DP : 32;               // dimensions of a pass, of a read
+        const int w0 = GR > 1 && W::P == 1 ? group * WORDS : 0, part0 = GR > 1 && W::P == 3 ? group * W::QT : 0;
 #pragma unroll 1
-        for (int c0 = 0; c0 < HD; c0 += DP) {
+        for (int c0 = group * (HD / GR); c0 < (group + 1) * (HD / GR); c0 += DP) {
 #pragma unroll 1
-          for (int c = c0; c < c0 + DP; c += 32) {
-            float o[32], top = 0.f;
-            tm_read32(tm_o + c, o);
+          for (int c = c0; c < c0 + DP; c += CH) {
+            float o[CH], top = 0.f;
+            if constexpr (CH == 32) tm_read32(tm_o + c, o);
+            else tm_read16(tm_o + c, o);
             bool nan = look;
 #pragma unroll
-            for (int x = 0; x < 32; ++x) top = fmaxf(top, fabsf(o[x])), nan = nan || o[x] != o[x];
+            for (int x = 0; x < CH; ++x) top = fmaxf(top, fabsf(o[x])), nan = nan || o[x] != o[x];
             const bool fine = !nan && is_finite(top);
             if (!fine && lim && is_finite(l)) {  // (positions that all columns see went through the products as they are)
 #pragma unroll 1
-              for (int q = 0; q < 32; q += 2) {
+              for (int q = 0; q < CH; q += 2) {
                 const float2 s = odd_sum<HD>(p.a, seq, rs.head, c + q, rs.t0 * SP, min(lim, rs.t1 * SP));
 #pragma unroll
-                for (int x = 0; x < 32; x += 2) {
+                for (int x = 0; x < CH; x += 2) {
                   if (x == q && s.x != 0.f) o[x] = s.x;
                   if (x == q && s.y != 0.f) o[x + 1] = s.y;
                 }
               }
             }
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = !ok ? NAN : l == 0.f ? 0.f : o[x] * f;
+            for (int x = 0; x < CH; ++x) o[x] = !ok ? NAN : l == 0.f ? 0.f : o[x] * f;
             if constexpr (F) {
 #pragma unroll
-              for (int x = 0; x < 32; x += 4)
-                *reinterpret_cast<float4*>(place(lane, (c - c0 + x) / 4)) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+              for (int x = 0; x < CH; x += 4)
+                *reinterpret_cast<float4*>(place(lane, w0 + (c - c0 + x) / 4) + part0) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
             } else {
 #pragma unroll
-              for (int x = 0; x < 32; x += 8)
-                *reinterpret_cast<uint4*>(place(lane, (c + x) / 8)) =
+              for (int x = 0; x < CH; x += 8)
+                *reinterpret_cast<uint4*>(place(lane, w0 + (c - c0 + x) / 8) + part0) =
                     make_uint4(pack2(o[x], o[x + 1]), pack2(o[x + 2], o[x + 3]), pack2(o[x + 4], o[x + 5]), pack2(o[x + 6], o[x + 7]));
             }
           }
           __syncwarp();
 #pragma unroll 8
-          for (int i = 0; i < NG * 8; ++i) {
-            const int y = (32 * i + lane) / (NG * 8), x = lane % (NG * 8), c = col - lane + y;
+          for (int i = 0; i < WORDS; ++i) {
+            const int y = (32 * i + lane) / WORDS, x = lane % WORDS, c = col - lane + y;
             if (c >= p.cols) continue;
-            const uint4 v = *reinterpret_cast<const uint4*>(place(y, x));
+            const uint4 v = *reinterpret_cast<const uint4*>(place(y, w0 + x) + part0);
             if (!whole) {
               reinterpret_cast<uint4*>(part + (ptrdiff_t)(y - lane) * (HD + 4) + c0)[x] = v;
             } else {
@@ -498,7 +537,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
       };
       if (whole && !W::F32) leave(std::false_type());
       else leave(std::true_type());
-      if (there) {
+      if (there && group == 0) {
         if (!whole) *reinterpret_cast<float2*>(part + HD) = l == 0.f ? make_float2(kLow, 0.f) : make_float2(m, ok ? l : NAN);
         else if (p.lse)
           p.lse[((size_t)seq * p.a.rows + row) * p.n_heads + hd] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
