@@ -266,10 +266,9 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
               const uint32_t base = tmu + W::TM * t;
 #pragma unroll
               for (int x = W::P - 1; x >= 0; --x) {  // the weights' low parts first
-                const uint32_t pw = x < 2 ? base + 128 * pu + 64 * x : base + W::THIRD + 64 * pu;
 #pragma unroll
                 for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                  mma_ts(base + W::SUMS, pw + 8 * kk, vd + ((kk * 16 * 128) >> 4), id_pv, kk || x < W::P - 1 ? 1 : add);
+                  mma_ts(base + W::SUMS, x < 2 ? base + 128 * pu + 32 * (kk / 2) + 16 * x + 8 * (kk % 2) : base + W::THIRD + 64 * pu + 8 * kk, vd + ((kk * 16 * 128) >> 4), id_pv, kk || x < W::P - 1 ? 1 : add);
               }
               if (h) {
                 if (t == TB - 1) commit(smem_addr(&kv_empty[v]));
@@ -377,16 +376,22 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
           const uint32_t at = tm_s + 128 * (kk % NS);
           auto step = [&](auto cut_) {
             constexpr bool CUT = decltype(cut_)::value;
-            float s[4][32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            // 32 scores at a time: held for the exponentials, or (fp32's three parts, whose code would not fit the
+            // instruction cache four times over) read again
+            constexpr int HOLD = W::F32 ? 1 : 4;
+            float s[HOLD][32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto read = [&](int c, float (&z)[32]) {
+              tm_read32(at + 32 * c, z);
+              const int v = vis - 32 * c;
 #pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (CUT && x >= v) z[x] = -INFINITY;
+            };
+#pragma unroll(HOLD)
             for (int c = 0; c < 4; ++c) {
-              tm_read32(at + 32 * c, s[c]);
+              read(c, s[c % HOLD]);
 #pragma unroll
-              for (int x = 0; x < 32; x += 2) {
-                if (CUT && 32 * c + x >= vis) s[c][x] = -INFINITY;
-                if (CUT && 32 * c + x + 1 >= vis) s[c][x + 1] = -INFINITY;
-                mx[x / 2 & 3] = max3(mx[x / 2 & 3], s[c][x], s[c][x + 1]);
-              }
+              for (int x = 0; x < 32; x += 2) mx[x / 2 & 3] = max3(mx[x / 2 & 3], s[c % HOLD][x], s[c % HOLD][x + 1]);
             }
             float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             most = most == -INFINITY ? most : most * cf;
@@ -426,15 +431,18 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
             }
             const uint64_t cf2 = pair(cf, cf), sub2 = pair(-m, -m);
             uint64_t la[2] = {0, 0};
-#pragma unroll
+#pragma unroll(HOLD)
             for (int c = 0; c < 4; ++c) {
               uint32_t b[W::P][16];
+              float(&sc)[32] = s[c % HOLD];
+              if constexpr (HOLD == 1) read(c, sc);
+              const int v = vis - 32 * c;
 #pragma unroll
               for (int x = 0; x < 32; x += 2) {
-                float2 z = unpair(fma2(pair(s[c][x], s[c][x + 1]), cf2, sub2));
+                float2 z = unpair(fma2(pair(sc[x], sc[x + 1]), cf2, sub2));
                 z.x = exp2_fast(z.x), z.y = exp2_fast(z.y);
-                if (CUT && 32 * c + x >= vis) z.x = 0.f;
-                if (CUT && 32 * c + x + 1 >= vis) z.y = 0.f;
+                if (CUT && x >= v) z.x = 0.f;
+                if (CUT && x + 1 >= v) z.y = 0.f;
                 la[x / 2 & 1] = add2(la[x / 2 & 1], pair(z.x, z.y));
 #pragma unroll
                 for (int i = 0; i < W::P; ++i) {
@@ -442,9 +450,10 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
                   if (i + 1 < W::P) z.x -= low_f(b[i][x / 2]), z.y -= high_f(b[i][x / 2]);
                 }
               }
-              tm_store16(at + 16 * c, b[0]);  // over the scores, which are all in registers
+              // over these scores, which are in registers; the third part has a place of its own
+              tm_store16(at + 32 * c, b[0]);
               if constexpr (W::P == 3) {
-                tm_store16(at + 64 + 16 * c, b[1]);
+                tm_store16(at + 32 * c + 16, b[1]);
                 tm_store16(tm_s + W::THIRD + 64 * (kk % NS) + 16 * c, b[2]);
               }
               if (c == 1) given(0);
