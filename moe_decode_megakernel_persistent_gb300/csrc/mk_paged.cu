@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(256) k_paged_store(const __grid_constant__ Kv4
   const long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long sr = at / parts;
   if (sr >= (long long)a.n_seqs * a.rows) return;
+  behind();
   const int part = (int)(at - sr * parts), seq = (int)(sr / a.rows), row = (int)(sr - (long long)seq * a.rows);
   const int w = part % W, kh = part / W, kv = kh >= a.n_kv_heads, head = kh - (kv ? a.n_kv_heads : 0);
   const Kv4Rows& r = kv ? v : k;
@@ -81,15 +82,15 @@ extern "C" MK_API int mk_paged_store(const mk_paged_cache* c, const mk_paged_row
   if (empty) return MK_OK;
   if (int r = kv4_check_rows(k, dtype, "k")) return r;
   if (int r = kv4_check_rows(v, dtype, "v")) return r;
-  const Kv4Args a = kv4_args(*c);
-  const Kv4Rows kr = kv4_rows(*k), vr = kv4_rows(*v);
+  Kv4Args a = kv4_args(*c);
+  Kv4Rows kr = kv4_rows(*k), vr = kv4_rows(*v);
   const long long n = (long long)c->n_seqs * c->rows * 2 * c->n_kv_heads * (c->head_dim / 8);  // at most 2^19 x 2^15
-  const dim3 grid((unsigned)((n + 255) / 256));
-  cudaStream_t st = (cudaStream_t)stream;
-  if (c->head_dim == 64 && dtype == MK_F32) k_paged_store<64, float><<<grid, 256, 0, st>>>(a, kr, vr);
-  else if (c->head_dim == 64) k_paged_store<64, __nv_bfloat16><<<grid, 256, 0, st>>>(a, kr, vr);
-  else if (dtype == MK_F32) k_paged_store<128, float><<<grid, 256, 0, st>>>(a, kr, vr);
-  else k_paged_store<128, __nv_bfloat16><<<grid, 256, 0, st>>>(a, kr, vr);
-  const cudaError_t e = cudaGetLastError();
+  void* args[] = {&a, &kr, &vr};
+  const void* f = c->head_dim == 64 ? dtype == MK_F32 ? reinterpret_cast<const void*>(&k_paged_store<64, float>)
+                                                      : reinterpret_cast<const void*>(&k_paged_store<64, __nv_bfloat16>)
+                  : dtype == MK_F32 ? reinterpret_cast<const void*>(&k_paged_store<128, float>)
+                                    : reinterpret_cast<const void*>(&k_paged_store<128, __nv_bfloat16>);
+  const cudaError_t e = launch(f, (unsigned)((n + 255) / 256), 256, 0, (cudaStream_t)stream, args);
+  if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? MK_OK : host_fail(MK_ERR_CUDA, (std::string("paged store: ") + cudaGetErrorString(e)).c_str());
 }

@@ -108,7 +108,6 @@ __global__ void __launch_bounds__(32 * W, B) k_paged_attention(const __grid_cons
   // cluster: the first pages of the item's sequence, where the sums are joined at the end
   int* pages = reinterpret_cast<int*>(red);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // a block's shared memory is there to be written once the block runs
   if (p.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   if (tid == 0) {
@@ -120,6 +119,7 @@ __global__ void __launch_bounds__(32 * W, B) k_paged_attention(const __grid_cons
     for (int i = 0; i < R; ++i) issued[i] = 0;
     give_up = 0;
   }
+  behind();
   // lane (g, t) of the mma fragments
   const int g = lane >> 2, t4 = lane & 3;
   // the B fragments of q: column nt * 8 + g, dimensions 16 j + 2 t + {0, 1} and 8 more
@@ -792,32 +792,12 @@ static int run_attention(const Kv4Args& a, int head_dim, int n_heads, const Kv4R
   pa.mass_ws = mass && !pl.score_cols ? ws + pl.mass_off : nullptr;
   cudaError_t e = allow_smem(pl);
   if (e == cudaSuccess && pa.mass_ws) e = paged_mass_begin(pa, head_dim, dtype, stream);
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  cfg.gridDim = dim3(pl.grid);
-  cfg.blockDim = dim3(pl.threads);
-  cfg.dynamicSmemBytes = pl.smem;
-  cfg.stream = stream;
-  cfg.attrs = at;
-  if (e == cudaSuccess) {
-    if (pl.cluster > 1) {
-      at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = pl.cluster;
-      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-      cfg.numAttrs = 1;
-    }
-    void* args[] = {&pa, &map};
-    e = cudaLaunchKernelExC(&cfg, pl.main, args);
-  }
+  void* args[] = {&pa, &map};
+  if (e == cudaSuccess) e = launch(pl.main, pl.grid, pl.threads, pl.smem, stream, args, pl.cluster);
   if (e == cudaSuccess && !pl.cluster) {
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(pl.items, (pl.CT + pl.join_cols - 1) / pl.join_cols);
-    cfg.blockDim = dim3(pl.join_threads);
-    cfg.dynamicSmemBytes = 0;
-    cfg.numAttrs = 1;
-    void* args[] = {&p, &pl.CT, &pl.SP, &pl.grid, &pl.join_cols};
-    e = cudaLaunchKernelExC(&cfg, kv4_join_kernel(head_dim, dtype, pl.join_many), args);
+    void* jargs[] = {&p, &pl.CT, &pl.SP, &pl.grid, &pl.join_cols};
+    e = launch(kv4_join_kernel(head_dim, dtype, pl.join_many), pl.items, pl.join_threads, 0, stream, jargs, 0,
+               (pl.CT + pl.join_cols - 1) / pl.join_cols);
   }
   if (e == cudaSuccess && mass) e = paged_mass(pa, *mass, head_dim, dtype, map, stream);
   if (e != cudaSuccess) {

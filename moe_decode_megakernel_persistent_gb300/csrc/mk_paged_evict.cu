@@ -2,15 +2,15 @@
 // stay, and their moves.
 //
 // Which.  The keep - recent largest masses among the others are found by their
-// bits (an order-preserving map to unsigned numbers): three passes over the masses
-// count the next 11, 11 and 10 bits of those that agree so far, and the digit is
-// where the count from the top passes what is left to take.  That gives the least
-// mass that stays and how many of its ties do; ties, free slots and late positions
-// (kept ones at or above `keep`) are then numbered in order.  An item is a cluster
-// of blocks, each with a run of the positions and each of its warps a run of that,
-// so that numbers are sums over the warps before; counts go through distributed
-// shared memory.  Every block passes the same barriers whatever it reads, so that lengths
-// written meanwhile give a wrong answer, not a hang.
+// bits (an order-preserving map to unsigned numbers): three passes count the next 11, 11
+// and 10 bits of those that agree so far, and the digit is where the count from the top
+// passes what is left to take.  That gives the least mass that stays and how many of its
+// ties do; ties, free slots and late positions (kept ones at or above `keep`) are then
+// numbered in order.  An item is a cluster of blocks, each with a run of the positions, which
+// it holds in shared memory (read from the masses again in each pass, an item of 131071 took 64 us),
+// and each of its warps a run of that, so that numbers are sums over the warps before; counts go through
+// distributed shared memory.  Every block passes the same barriers whatever it reads, so that
+// lengths written meanwhile give a wrong answer, not a hang.
 //
 // Moves.  Only late positions move, into free slots: never more rows than it takes, sources
 // (>= keep) and destinations (< keep) are apart, and nothing is read after it is written.
@@ -18,12 +18,12 @@
 #include <climits>
 #include <string>
 
-#include "mk_paged.cuh"
+#include "mk_paged_att.cuh"
 
 namespace mk {
 namespace {
 
-constexpr int kSelWarps = 16, kSelThreads = 32 * kSelWarps, kBins = 2048;
+constexpr int kSelWarps = 16, kSelThreads = 32 * kSelWarps, kBins = 4 * kSelThreads;
 
 struct EvictArgs {
   Kv4Args a;
@@ -60,71 +60,90 @@ __device__ __forceinline__ int peer_load(const void* p, int rank) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(peer_addr(p, rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ void peer_store(const void* p, int rank, int v) {
-  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_addr(p, rank)), "r"(v) : "memory");
+__device__ __forceinline__ int4 peer_load4(const void* p, int rank) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(peer_addr(p, rank))
+               : "memory");
+  return v;
 }
 
-// The sum over all warps of the cluster before this one, of a number of each warp.
+// Two numbers' sums over all warps of the cluster before this one.
 struct Before {
-  int warp[kSelWarps], block;
+  int2 warp[kSelWarps];
+  int x, y;  // of the block
 };
-__device__ __forceinline__ int before(Before& b, int n, int rank, int C) {
+__device__ __forceinline__ int2 before(Before& b, int x, int y, int rank) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) b.warp[w] = n;
+  if (lane == 0) b.warp[w] = make_int2(x, y);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int s = 0;
-    for (int i = 0; i < kSelWarps; ++i) s += b.warp[i];
-    b.block = s;
+  if (w == 0) {
+    const int2 n = lane < kSelWarps ? b.warp[lane] : make_int2(0, 0);
+    const int sx = __reduce_add_sync(0xffffffffu, n.x), sy = __reduce_add_sync(0xffffffffu, n.y);
+    if (lane == 0) b.x = sx, b.y = sy;
   }
   cluster_sync();
-  int s = lane < w ? b.warp[lane] : 0;
-  if (lane < rank && lane < C) s += peer_load(&b.block, lane);
-  return __reduce_add_sync(0xffffffffu, s);
+  int2 n = lane < w ? b.warp[lane] : make_int2(0, 0);
+  if (lane < rank) n.x += peer_load(&b.x, lane), n.y += peer_load(&b.y, lane);
+  return make_int2(__reduce_add_sync(0xffffffffu, n.x), __reduce_add_sync(0xffffffffu, n.y));
 }
 
+// HELD: the block's masses are in shared memory as unsigned numbers; else (contexts too long for it) read each time.
+template <bool HELD>
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictArgs p, int C) {
-  __shared__ int hist[kBins], total[kBins];
-  __shared__ Before cnt[3];
-  __shared__ int scan[kSelWarps], s_digit, s_left;
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ __align__(16) int hist[2][kBins];
+  __shared__ Before cnt[2];
+  __shared__ int scan[kSelWarps], s_digit, s_left, s_ties;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int item = blockIdx.x / C, rank = blockIdx.x - item * C;
   const int seq = item / p.a.n_kv_heads, head = item - seq * p.a.n_kv_heads;
+  behind();
   const int len = held_length(p.a, seq), keep = p.keep;
   const bool all = len <= keep;
   const int others = max(0, len - p.recent);
   const float* mass = p.mass.p + seq * p.mass.seq + head * p.mass.head;
   int* kept = p.kept + (size_t)item * keep;
   int* late = p.late + (size_t)item * keep;
-  // this warp's run of the positions
-  const int per = ((len + C * kSelWarps - 1) / (C * kSelWarps) + 31) & ~31;
-  const int lo = (int)min((long long)len, (long long)(rank * kSelWarps + w) * per), hi = min(len, lo + per);
+  // the block's run of the positions (a multiple of the warps' 32), and this warp's of it
+  const int per = ((len + C - 1) / C + kSelThreads - 1) / kSelThreads * kSelThreads;
+  const int lo = (int)min((long long)len, (long long)rank * per), n = min(len - lo, per);
+  const int per_warp = per / kSelWarps, w0 = min(n, w * per_warp), w1 = min(n, w0 + per_warp);
+  auto key = [&](int i) { return HELD ? keys[i] : key_of(mass[lo + i]); };
+  if (HELD) {
+#pragma unroll 4
+    for (int i = 4 * tid; i < n; i += 4 * kSelThreads) {  // (rows are multiples of 128 positions: no word passes their end)
+      const float4 m = *reinterpret_cast<const float4*>(mass + lo + i);
+      *reinterpret_cast<uint4*>(keys + i) = make_uint4(key_of(m.x), key_of(m.y), key_of(m.z), key_of(m.w));
+    }
+  }
+  for (int i = tid; i < 2 * kBins; i += kSelThreads) hist[0][i] = 0;
+  if (tid == 0) s_digit = s_left = s_ties = 0;
+  __syncthreads();
 
   // ---- the least mass that stays (its bits), and how many of its ties do
   uint32_t least = 0;
   int left = all ? 0 : keep - p.recent;
+  const int m_others = min(n, max(0, others - lo));
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-    if (tid == 0) s_digit = s_left = 0;
-    __syncthreads();
-    for (int q = lo + lane; q < hi && q < others; q += 32) {
-      const uint32_t k = key_of(mass[q]);
-      if (pass == 0 || k >> (shift + bits) == least >> (shift + bits)) atomicAdd(&hist[k >> shift & ((1u << bits) - 1)], 1);
+    int* h = hist[pass & 1];
+#pragma unroll 4
+    for (int i = tid; i < m_others; i += kSelThreads) {
+      const uint32_t k = key(i);
+      if (pass == 0 || k >> (shift + bits) == least >> (shift + bits)) atomicAdd(&h[k >> shift & ((1u << bits) - 1)], 1);
     }
     cluster_sync();
-    // each block adds a part of the bins over the cluster and gives every block the sums
-    const int seg = kBins / C;
-    for (int i = tid; i < seg; i += kSelThreads) {
-      int s = 0;
-      for (int r = 0; r < C; ++r) s += peer_load(&hist[rank * seg + i], r);
-      for (int r = 0; r < C; ++r) peer_store(&total[rank * seg + i], r, s);
+    // four bins a thread, from the top, over the cluster
+    int4 c4 = make_int4(0, 0, 0, 0);
+    for (int r = 0; r < C; ++r) {
+      const int4 v = peer_load4(&h[kBins - 4 - 4 * tid], r);
+      c4.x += v.x, c4.y += v.y, c4.z += v.z, c4.w += v.w;
     }
-    cluster_sync();
-    int n[4], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum += n[i] = total[kBins - 1 - 4 * tid - i];
+    const int c[4] = {c4.w, c4.z, c4.y, c4.x};
+    const int sum = (c[0] + c[1]) + (c[2] + c[3]);
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -133,53 +152,60 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     }
     if (lane == 31) scan[w] = incl;
     __syncthreads();
-    for (int i = 0; i < w; ++i) incl += scan[i];
+    const int whole = lane < w ? scan[lane] : 0;
+    incl += __reduce_add_sync(0xffffffffu, whole);
     int above = incl - sum;
     if (above < left && left <= incl) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (above < left && left <= above + n[i]) {
+        if (above < left && left <= above + c[i]) {
           s_digit = kBins - 1 - 4 * tid - i;
           s_left = left - above;
+          s_ties = c[i];
         }
-        above += n[i];
+        above += c[i];
       }
     }
+    if (pass == 1)  // the third pass counts where the first did, which all blocks have read
+      for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
     __syncthreads();
     least |= (uint32_t)s_digit << shift;
     left = s_left;
-    __syncthreads();
   }
 
   // ---- numbers in order
-  // whether position q stays, of the warp's next 32; `tie`: ties before them
-  auto stays = [&](int q, int& tie) {
-    bool t = false, s = q < hi;
-    if (s && !all && q < others) {
-      const uint32_t k = key_of(mass[q]);
-      t = k == least;
-      s = k > least && p.keep > p.recent;
+  // Whether the warp's next 32 positions stay; `tie`: ties before them.  Where all ties stay, or none, they need no number.
+  const bool some = left > 0 && left < s_ties;
+  auto stays = [&](int i, int& tie) {
+    bool t = false, s = i < w1;
+    if (s && !all && lo + i < others) {
+      const uint32_t k = key(i);
+      t = some && k == least;
+      s = (left > 0 ? k >= least : false) && p.keep > p.recent;
     }
-    const uint32_t ties = __ballot_sync(0xffffffffu, t);
-    if (t) s = tie + __popc(ties & ((1u << lane) - 1)) < left;
-    tie += __popc(ties);
+    if (some) {
+      const uint32_t ties = __ballot_sync(0xffffffffu, t);
+      if (t) s = tie + __popc(ties & ((1u << lane) - 1)) < left;
+      tie += __popc(ties);
+    }
     return s;
   };
   int n_tie = 0;
-  for (int q0 = lo; q0 < hi; q0 += 32) stays(q0 + lane, n_tie);
-  const int tie0 = before(cnt[0], n_tie, rank, C);
+  if (some)
+    for (int i = w0; i < w1; i += 32) stays(i + lane, n_tie);
+  const int tie0 = before(cnt[0], n_tie, 0, rank).x;
   int n_free = 0, n_late = 0, tie = tie0;
-  for (int q0 = lo; q0 < hi; q0 += 32) {
-    const int q = q0 + lane;
-    const bool s = stays(q, tie);
-    n_free += __popc(__ballot_sync(0xffffffffu, q < hi && q < keep && !s));
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const int i = i0 + lane, q = lo + i;
+    const bool s = stays(i, tie);
+    n_free += __popc(__ballot_sync(0xffffffffu, i < w1 && q < keep && !s));
     n_late += __popc(__ballot_sync(0xffffffffu, q >= keep && s));
   }
-  const int free0 = before(cnt[1], n_free, rank, C), late0 = before(cnt[2], n_late, rank, C);
+  const int2 at0 = before(cnt[1], n_free, n_late, rank);
   tie = tie0;
-  for (int q0 = lo, nl = late0; q0 < hi; q0 += 32) {
-    const int q = q0 + lane;
-    const bool s = stays(q, tie), l = s && q >= keep;
+  for (int i0 = w0, nl = at0.y; i0 < w1; i0 += 32) {
+    const int i = i0 + lane, q = lo + i;
+    const bool s = stays(i, tie), l = s && q >= keep;
     const uint32_t ls = __ballot_sync(0xffffffffu, l);
     if (s && q < keep) kept[q] = q;
     const int at = nl + __popc(ls & ((1u << lane) - 1));
@@ -189,9 +215,9 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   for (int q = len + rank * kSelThreads + tid; q < keep; q += C * kSelThreads) kept[q] = -1;
   cluster_sync();
   tie = tie0;
-  for (int q0 = lo, nf = free0; q0 < hi && q0 < keep; q0 += 32) {
-    const int q = q0 + lane;
-    const bool s = stays(q, tie), f = q < hi && q < keep && !s;
+  for (int i0 = w0, nf = at0.x; i0 < w1 && lo + i0 < keep; i0 += 32) {
+    const int i = i0 + lane, q = lo + i;
+    const bool s = stays(i, tie), f = i < w1 && q < keep && !s;
     const uint32_t fs = __ballot_sync(0xffffffffu, f);
     const int at = nf + __popc(fs & ((1u << lane) - 1));
     if (f) kept[q] = __ldcg(&late[at]);
@@ -209,6 +235,7 @@ __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ Evic
   const int s0 = ((blockIdx.x - item * chunks) * 8 + (threadIdx.x >> 5)) * 32;
   const int seq = item / p.a.n_kv_heads, head = item - seq * p.a.n_kv_heads;
   const int most = p.a.max_pages * kPageTokens;
+  behind();
   if (head == 0 && s0 == 0 && lane == 0) p.lengths[seq] = min(held_length(p.a, seq), p.keep);
   const int slot = s0 + lane;
   int src = slot < p.keep ? p.kept[(size_t)item * p.keep + slot] : -1;
@@ -307,26 +334,25 @@ extern "C" MK_API int mk_paged_evict(const mk_paged_cache* c, const mk_paged_mas
   p.lengths = new_lengths;
   cudaStream_t st = (cudaStream_t)stream;
   const int items = c->n_seqs * c->n_kv_heads, positions = c->max_pages * kPageTokens;
+  if ((long long)items * ((positions + 255) / 256) > INT_MAX || (long long)items * 8 > INT_MAX)
+    return host_fail(MK_ERR_INVALID_ARG, "n_seqs x n_kv_heads x max_pages is too large");
+  // Blocks of an item: while they run at once (two an SM) and have 2048 positions each, or until they hold theirs.
+  constexpr int kMost = 48 * 1024;  // positions that a block holds
+  const int sms = device_sms();
   int C = 1;
-  while (C < 8 && (long long)items * C * 2 <= 304 && positions / (2 * C) >= 2048) C *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = C;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)items * C);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, k_evict_select, p, C);
+  while (C < 8 && (((long long)items * C * 2 <= 2 * sms && positions / (2 * C) >= 2048) || positions / C > kMost)) C *= 2;
+  const int per = ((positions + C - 1) / C + kSelThreads - 1) / kSelThreads * kSelThreads;
+  const bool held = per <= kMost;
+  const void* select = held ? reinterpret_cast<const void*>(&k_evict_select<true>) : reinterpret_cast<const void*>(&k_evict_select<false>);
+  cudaError_t e = held ? cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost * 4) : cudaSuccess;
+  void* args[] = {&p, &C};
+  if (e == cudaSuccess) e = launch(select, (unsigned)items * C, kSelThreads, held ? (size_t)per * 4 : 0, st, args, C);
   if (e == cudaSuccess) {
-    const int width = p.in_place ? std::min(keep, positions) : positions;
-    const int chunks = (std::max(width, std::min(keep, positions)) + 255) / 256;
-    if ((long long)items * chunks > INT_MAX) return host_fail(MK_ERR_INVALID_ARG, "n_seqs x n_kv_heads x max_pages is too large");
-    if (c->head_dim == 64) k_evict_move<64><<<(unsigned)items * chunks, 256, 0, st>>>(p, width, chunks);
-    else k_evict_move<128><<<(unsigned)items * chunks, 256, 0, st>>>(p, width, chunks);
-    e = cudaGetLastError();
+    int width = p.in_place ? std::min(keep, positions) : positions;
+    int chunks = (std::max(width, std::min(keep, positions)) + 255) / 256;
+    void* margs[] = {&p, &width, &chunks};
+    const void* move = c->head_dim == 64 ? reinterpret_cast<const void*>(&k_evict_move<64>) : reinterpret_cast<const void*>(&k_evict_move<128>);
+    e = launch(move, (unsigned)items * chunks, 256, 0, st, margs);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();

@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(256) k_mass_scores(const __grid_constant__ Pag
   const AttArgs& p = pa.t;
   const int item = blockIdx.x / chunks, t = (blockIdx.x - item * chunks) * 256 + threadIdx.x;
   const int seq = item / p.a.n_kv_heads, head = item - seq * p.a.n_kv_heads;
+  behind();
   int len, nn;
   seq_extent(p.a, seq, len, nn);
   if (t >= len || nn == 0) return;
@@ -28,7 +29,6 @@ __global__ void __launch_bounds__(256) k_mass_scores(const __grid_constant__ Pag
   float sum = 0.f;  // (the weights by themselves: next to a large mass each would be rounded to its step)
   const bool there = page_of(p.a, seq, t) >= 0;
   const float* sc = pa.scores + ((size_t)item * p.a.max_pages * kPageTokens + t) * pa.score_cols;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (there)
     for (int c0 = 0; c0 < p.cols; c0 += 4) {
       const float4 s4 = *reinterpret_cast<const float4*>(sc + c0);
@@ -146,7 +146,7 @@ template <int HD, class T>
 __global__ void __launch_bounds__(256) k_columns(const __grid_constant__ MassArgs a) {
   constexpr int W = HD / 8;
   const AttArgs& p = a.pa.t;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  behind();
   const long long x = (long long)blockIdx.x * 256 + threadIdx.x, row = x / W;
   if (row >= a.part_rows) return;
   const int w = (int)(x % W), col = (int)(row % a.cols_up);
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
     r = says[i % kMassRuns];
     return r.t1 > r.t0;
   };
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  behind();
 
   if (w == CW) {  // ---- runs, copies and log-sum-exps
     // the block's places, and the sequence of the first
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
 // Items cut between blocks: their parts added in the blocks' order, a thread for a position.
 __global__ void __launch_bounds__(kSpan) k_mass_join(const __grid_constant__ MassArgs a, int G, int items) {
   const Kv4Args& c = a.pa.t.a;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  behind();
   for (int i = blockIdx.x; i < items; i += gridDim.x) {
     const int span = i % a.spans, sh = i / a.spans, seq = sh / c.n_kv_heads, head = sh - seq * c.n_kv_heads;
     int len, nn;
@@ -493,12 +493,14 @@ cudaError_t launch_wide(const MassArgs& a, const MassPlan& m, const CUtensorMap&
   using S = MassShape<HD, T>;
   cudaError_t e = cudaFuncSetAttribute(k_mass_wide<HD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
-  k_mass_wide<HD, T><<<m.grid, S::THREADS, S::SMEM, st>>>(a, kmap, qmap);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int items = p_items(a);
-  k_mass_join<<<std::min(items, 16 * m.grid), kSpan, 0, st>>>(a, m.grid, items);
-  return cudaGetLastError();
+  MassArgs g = a;
+  CUtensorMap km = kmap, qm = qmap;
+  int G = m.grid, items = p_items(a);
+  void* args[] = {&g, &km, &qm};
+  e = launch(reinterpret_cast<const void*>(&k_mass_wide<HD, T>), m.grid, S::THREADS, S::SMEM, st, args);
+  void* jargs[] = {&g, &G, &items};
+  if (e == cudaSuccess) e = launch(reinterpret_cast<const void*>(&k_mass_join), std::min(items, 16 * m.grid), kSpan, 0, st, jargs);
+  return e;
 }
 
 }  // namespace
@@ -509,12 +511,13 @@ cudaError_t paged_mass_begin(const PagedAtt& p, int head_dim, int dtype, cudaStr
   const MassArgs a = args_of(p, plan_of(p.t.a, head_dim, p.t.n_heads, dtype), head_dim);
   const long long threads = a.part_rows * (head_dim / 8);
   if ((threads + 255) / 256 > 0x7FFFFFFF || a.part_rows * 3 > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const unsigned grid = (unsigned)((threads + 255) / 256);
-  if (head_dim == 64 && dtype == MK_F32) k_columns<64, float><<<grid, 256, 0, st>>>(a);
-  else if (head_dim == 64) k_columns<64, __nv_bfloat16><<<grid, 256, 0, st>>>(a);
-  else if (dtype == MK_F32) k_columns<128, float><<<grid, 256, 0, st>>>(a);
-  else k_columns<128, __nv_bfloat16><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  MassArgs g = a;
+  void* args[] = {&g};
+  const void* f = head_dim == 64 ? dtype == MK_F32 ? reinterpret_cast<const void*>(&k_columns<64, float>)
+                                                   : reinterpret_cast<const void*>(&k_columns<64, __nv_bfloat16>)
+                  : dtype == MK_F32 ? reinterpret_cast<const void*>(&k_columns<128, float>)
+                                    : reinterpret_cast<const void*>(&k_columns<128, __nv_bfloat16>);
+  return launch(f, (unsigned)((threads + 255) / 256), 256, 0, st, args);
 }
 
 cudaError_t paged_mass(const PagedAtt& p, const PagedMass& m, int head_dim, int dtype, const CUtensorMap& map, cudaStream_t st) {
@@ -523,8 +526,11 @@ cudaError_t paged_mass(const PagedAtt& p, const PagedMass& m, int head_dim, int 
   if (p.scores) {
     const int chunks = (a.max_pages * kPageTokens + 255) / 256;
     if (items * chunks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    k_mass_scores<<<(unsigned)(items * chunks), 256, 0, st>>>(p, m, chunks);
-    return cudaGetLastError();
+    PagedAtt pa = p;
+    PagedMass ms = m;
+    int n = chunks;
+    void* args[] = {&pa, &ms, &n};
+    return launch(reinterpret_cast<const void*>(&k_mass_scores), (unsigned)(items * chunks), 256, 0, st, args);
   }
   const MassPlan pl = plan_of(a, head_dim, p.t.n_heads, dtype);
   MassArgs g = args_of(p, pl, head_dim);
