@@ -23,13 +23,14 @@
 namespace mk {
 namespace {
 
-constexpr int kSelWarps = 16, kSelThreads = 32 * kSelWarps, kBins = 4 * kSelThreads;
+constexpr int kSelWarps = 32, kSelThreads = 32 * kSelWarps, kBins = 2 * kSelThreads;  // two bins a thread
+constexpr int kMostBlocks = 8;  // of an item's cluster
 
 struct EvictArgs {
   Kv4Args a;
   PagedMass mass, to;
   int32_t keep, recent, in_place;
-  int32_t* kept;     // [n_seqs][n_kv_heads][keep]
+  int32_t* kept;     // [n_seqs][n_kv_heads][keep]; between the kernels -2 - i in the i-th free slot
   int32_t* late;     // workspace, as kept: late positions in order
   int32_t* lengths;  // new ones
 };
@@ -60,13 +61,8 @@ __device__ __forceinline__ int peer_load(const void* p, int rank) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(peer_addr(p, rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ int4 peer_load4(const void* p, int rank) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(peer_addr(p, rank))
-               : "memory");
-  return v;
+__device__ __forceinline__ void peer_store(const void* p, int rank, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_addr(p, rank)), "r"(v) : "memory");
 }
 
 // Two numbers' sums over all warps of the cluster before this one.
@@ -93,7 +89,7 @@ __device__ __forceinline__ int2 before(Before& b, int x, int y, int rank) {
 template <bool HELD>
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictArgs p, int C) {
   extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ __align__(16) int hist[2][kBins];
+  __shared__ __align__(16) int hist[2][kBins], total[kBins];
   __shared__ Before cnt[2];
   __shared__ int scan[kSelWarps], s_digit, s_left, s_ties;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -135,15 +131,30 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
       const uint32_t k = key(i);
       if (pass == 0 || k >> (shift + bits) == least >> (shift + bits)) atomicAdd(&h[k >> shift & ((1u << bits) - 1)], 1);
     }
-    cluster_sync();
-    // four bins a thread, from the top, over the cluster
-    int4 c4 = make_int4(0, 0, 0, 0);
-    for (int r = 0; r < C; ++r) {
-      const int4 v = peer_load4(&h[kBins - 4 - 4 * tid], r);
-      c4.x += v.x, c4.y += v.y, c4.z += v.z, c4.w += v.w;
+    // Each block adds a part of the bins over the cluster and gives every block the sums (all bins of all blocks read
+    // by every block: 2.4 us a pass in a cluster of 8, 11 in one of 16).
+    if (C > 1) {
+      cluster_sync();
+      const int seg = kBins / C;
+      for (int i = rank * seg + tid; i < (rank + 1) * seg; i += kSelThreads) {
+        int sum = 0;
+        for (int r0 = 0; r0 < C; r0 += 8) {  // (eight reads on their way)
+          int v[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) v[r] = r0 + r < C ? peer_load(&h[i], r0 + r) : 0;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) sum += v[r];
+        }
+        for (int r = 0; r < C; ++r) peer_store(&total[i], r, sum);
+      }
+      cluster_sync();
+    } else {
+      __syncthreads();
     }
-    const int c[4] = {c4.w, c4.z, c4.y, c4.x};
-    const int sum = (c[0] + c[1]) + (c[2] + c[3]);
+    // two bins a thread, from the top
+    const int2 c2 = *reinterpret_cast<const int2*>((C > 1 ? total : h) + kBins - 2 - 2 * tid);
+    const int c[2] = {c2.y, c2.x};
+    const int sum = c[0] + c[1];
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -157,16 +168,16 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     int above = incl - sum;
     if (above < left && left <= incl) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         if (above < left && left <= above + c[i]) {
-          s_digit = kBins - 1 - 4 * tid - i;
+          s_digit = kBins - 1 - 2 * tid - i;
           s_left = left - above;
           s_ties = c[i];
         }
         above += c[i];
       }
     }
-    if (pass == 1)  // the third pass counts where the first did, which all blocks have read
+    if (pass == 1)  // the third pass counts where the first did, which all blocks have read by now
       for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
     __syncthreads();
     least |= (uint32_t)s_digit << shift;
@@ -174,56 +185,60 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   }
 
   // ---- numbers in order
-  // Whether the warp's next 32 positions stay; `tie`: ties before them.  Where all ties stay, or none, they need no number.
+  // Which of the warp's next 32 positions stay (a word of the warp); `tie`: ties before them.  Where all ties stay, or none,
+  // they need no number.
   const bool some = left > 0 && left < s_ties;
-  auto stays = [&](int i, int& tie) {
+  auto stays = [&](int i, uint32_t k, int& tie) {
     bool t = false, s = i < w1;
     if (s && !all && lo + i < others) {
-      const uint32_t k = key(i);
       t = some && k == least;
-      s = (left > 0 ? k >= least : false) && p.keep > p.recent;
+      s = left > 0 && k >= least;
     }
     if (some) {
       const uint32_t ties = __ballot_sync(0xffffffffu, t);
       if (t) s = tie + __popc(ties & ((1u << lane) - 1)) < left;
       tie += __popc(ties);
     }
-    return s;
+    return __ballot_sync(0xffffffffu, s);
   };
-  int n_tie = 0;
-  if (some)
-    for (int i = w0; i < w1; i += 32) stays(i + lane, n_tie);
+  // f(first position of 32, which stay), four words of keys read ahead
+  auto walk = [&](int tie, auto f) {
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+      uint32_t k[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) k[u] = i0 + 32 * u + lane < w1 ? key(i0 + 32 * u + lane) : 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + 32 * u < w1) f(i0 + 32 * u, stays(i0 + 32 * u + lane, k[u], tie));
+    }
+    return tie;
+  };
+  // of 32 positions, those there are and those below keep
+  auto there = [&](int i) { return i + 32 <= w1 ? ~0u : (1u << (w1 - i)) - 1; };
+  auto below = [&](int i) { return lo + i + 32 <= keep ? ~0u : lo + i >= keep ? 0u : (1u << (keep - lo - i)) - 1; };
+  const int n_tie = some ? walk(0, [](int, uint32_t) {}) : 0;
   const int tie0 = before(cnt[0], n_tie, 0, rank).x;
-  int n_free = 0, n_late = 0, tie = tie0;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane, q = lo + i;
-    const bool s = stays(i, tie);
-    n_free += __popc(__ballot_sync(0xffffffffu, i < w1 && q < keep && !s));
-    n_late += __popc(__ballot_sync(0xffffffffu, q >= keep && s));
-  }
+  int n_free = 0, n_late = 0;
+  walk(tie0, [&](int i, uint32_t s) {
+    n_free += __popc(there(i) & below(i) & ~s);
+    n_late += __popc(s & ~below(i));
+  });
   const int2 at0 = before(cnt[1], n_free, n_late, rank);
-  tie = tie0;
-  for (int i0 = w0, nl = at0.y; i0 < w1; i0 += 32) {
-    const int i = i0 + lane, q = lo + i;
-    const bool s = stays(i, tie), l = s && q >= keep;
-    const uint32_t ls = __ballot_sync(0xffffffffu, l);
-    if (s && q < keep) kept[q] = q;
-    const int at = nl + __popc(ls & ((1u << lane) - 1));
-    if (l && at < keep) late[at] = q;
-    nl += __popc(ls);
-  }
-  for (int q = len + rank * kSelThreads + tid; q < keep; q += C * kSelThreads) kept[q] = -1;
-  cluster_sync();
-  tie = tie0;
-  for (int i0 = w0, nf = at0.x; i0 < w1 && lo + i0 < keep; i0 += 32) {
-    const int i = i0 + lane, q = lo + i;
-    const bool s = stays(i, tie), f = i < w1 && q < keep && !s;
-    const uint32_t fs = __ballot_sync(0xffffffffu, f);
-    const int at = nf + __popc(fs & ((1u << lane) - 1));
-    if (f) kept[q] = __ldcg(&late[at]);
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");  // (this block reads no other's shared memory any more)
+  const uint32_t under = (1u << lane) - 1;
+  int nf = at0.x, nl = at0.y;
+  walk(tie0, [&](int i, uint32_t s) {
+    const uint32_t fs = there(i) & below(i) & ~s, ls = s & ~below(i), me = 1u << lane;
+    const int q = lo + i + lane;
+    if (s & below(i) & me) kept[q] = q;
+    if (fs & me) kept[q] = -2 - (nf + __popc(fs & under));
+    const int at = nl + __popc(ls & under);
+    if ((ls & me) && at < keep) late[at] = q;
     nf += __popc(fs);
-  }
-  cluster_sync();  // no block leaves while others read its shared memory
+    nl += __popc(ls);
+  });
+  for (int q = len + rank * kSelThreads + tid; q < keep; q += C * kSelThreads) kept[q] = -1;
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // no block leaves while others read its shared memory
 }
 
 // A warp takes 32 slots of an item: their masses, then the rows that move, K in the first
@@ -239,7 +254,12 @@ __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ Evic
   if (head == 0 && s0 == 0 && lane == 0) p.lengths[seq] = min(held_length(p.a, seq), p.keep);
   const int slot = s0 + lane;
   int src = slot < p.keep ? p.kept[(size_t)item * p.keep + slot] : -1;
-  if (src >= most) src = -1;
+  if (src < -1) {  // a free slot takes the late position of its number
+    const int i = -2 - src;
+    src = i < p.keep ? p.late[(size_t)item * p.keep + i] : -1;
+    p.kept[(size_t)item * p.keep + slot] = src;
+  }
+  if (src < 0 || src >= most) src = -1;
   const float* mass = p.mass.p + seq * p.mass.seq + head * p.mass.head;
   float* to = p.to.p + seq * p.to.seq + head * p.to.head;
   if (slot < width && !(p.in_place && (src < 0 || src == slot))) to[slot] = src >= 0 ? mass[src] : 0.f;
@@ -259,10 +279,10 @@ __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ Evic
   uint32_t todo = __ballot_sync(0xffffffffu, from >= 0);
   const int mine = lane / LP, word = lane % LR, kv = lane % LP / LR;
   while (todo) {
-    uint4 x[4];
-    int d[4];
+    uint4 x[8];
+    int d[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       int pick = -1;
 #pragma unroll
       for (int j = 0; j < 32 / LP; ++j) {
@@ -276,7 +296,7 @@ __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ Evic
       else x[i] = reinterpret_cast<const uint4*>(paged_at<HD>(p.a, f + kv * half))[word];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
       if (d[i] >= 0) reinterpret_cast<uint4*>(paged_at<HD>(p.a, d[i] + kv * half))[word] = x[i];
   }
 }
@@ -334,13 +354,13 @@ extern "C" MK_API int mk_paged_evict(const mk_paged_cache* c, const mk_paged_mas
   p.lengths = new_lengths;
   cudaStream_t st = (cudaStream_t)stream;
   const int items = c->n_seqs * c->n_kv_heads, positions = c->max_pages * kPageTokens;
-  if ((long long)items * ((positions + 255) / 256) > INT_MAX || (long long)items * 8 > INT_MAX)
+  if ((long long)items * ((positions + 255) / 256) > INT_MAX || (long long)items * kMostBlocks > INT_MAX)
     return host_fail(MK_ERR_INVALID_ARG, "n_seqs x n_kv_heads x max_pages is too large");
   // Blocks of an item: while they run at once (two an SM) and have 2048 positions each, or until they hold theirs.
-  constexpr int kMost = 48 * 1024;  // positions that a block holds
+  constexpr int kMost = 40 * 1024;  // positions that a block holds, a multiple of its threads
   const int sms = device_sms();
   int C = 1;
-  while (C < 8 && (((long long)items * C * 2 <= 2 * sms && positions / (2 * C) >= 2048) || positions / C > kMost)) C *= 2;
+  while (C < kMostBlocks && (((long long)items * C * 2 <= 2 * sms && positions / (2 * C) >= 2048) || positions / C > kMost)) C *= 2;
   const int per = ((positions + C - 1) / C + kSelThreads - 1) / kSelThreads * kSelThreads;
   const bool held = per <= kMost;
   const void* select = held ? reinterpret_cast<const void*>(&k_evict_select<true>) : reinterpret_cast<const void*>(&k_evict_select<false>);
