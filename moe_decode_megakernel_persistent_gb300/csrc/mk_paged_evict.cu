@@ -13,7 +13,9 @@
 // lengths written meanwhile give a wrong answer, not a hang.
 //
 // Moves.  Only late positions move, into free slots: never more rows than it takes, sources
-// (>= keep) and destinations (< keep) are apart, and nothing is read after it is written.
+// (>= keep) and destinations (< keep) are apart, and nothing is read after it is written.  The
+// item's own blocks make them, from the lists of free slots and late positions in order; where there may be many, a second
+// kernel of all SMs does.
 #include <algorithm>
 #include <climits>
 #include <string>
@@ -23,15 +25,17 @@
 namespace mk {
 namespace {
 
-constexpr int kSelWarps = 32, kSelThreads = 32 * kSelWarps, kBins = 2 * kSelThreads;  // two bins a thread
-constexpr int kMostBlocks = 8;  // of an item's cluster
+constexpr int kSelWarps = 16, kSelThreads = 32 * kSelWarps, kBins = 4 * kSelThreads;  // four bins a thread
+constexpr int kMostBlocks = 16;  // of an item's cluster
+constexpr int kFew = 256;        // moves of an item, at most, that its own blocks make
 
 struct EvictArgs {
   Kv4Args a;
   PagedMass mass, to;
   int32_t keep, recent, in_place;
-  int32_t* kept;     // [n_seqs][n_kv_heads][keep]; between the kernels -2 - i in the i-th free slot
-  int32_t* late;     // workspace, as kept: late positions in order
+  int32_t* kept;     // [n_seqs][n_kv_heads][keep]
+  int32_t *free, *late;  // workspace, as kept: free slots and late positions in order
+  int32_t* counts;   // workspace: moves of each item, where another kernel makes them
   int32_t* lengths;  // new ones
 };
 
@@ -84,10 +88,59 @@ __device__ __forceinline__ int2 before(Before& b, int x, int y, int rank) {
   if (lane < rank) n.x += peer_load(&b.x, lane), n.y += peer_load(&b.y, lane);
   return make_int2(__reduce_add_sync(0xffffffffu, n.x), __reduce_add_sync(0xffffffffu, n.y));
 }
+// The first number's sum over the cluster.
+__device__ __forceinline__ int total_of(Before& b, int C) {
+  const int lane = threadIdx.x & 31;
+  return __reduce_add_sync(0xffffffffu, lane < C ? peer_load(&b.x, lane) : 0);
+}
+
+// The moves of an item by warps `first`, `first` + 1 .. of `warps`, MV at a time: K in the first half of the lanes
+// that a position's 4 * HD bytes take and V in the second.
+template <int HD>
+__device__ __forceinline__ void make_moves(const EvictArgs& p, int item, int seq, int head, int moves, int first, int warps) {
+  constexpr int LP = HD / 4, LR = LP / 2, MV = 8;
+  const int lane = threadIdx.x & 31, mine = lane / LP, word = lane % LR, kv = lane % LP / LR;
+  const int half = p.a.n_kv_heads * kPageTokens;  // rows from K to V
+  const int positions = p.a.max_pages * kPageTokens, keep = p.keep;
+  const float* mass = p.mass.p + seq * p.mass.seq + head * p.mass.head;
+  float* to = p.to.p + seq * p.to.seq + head * p.to.head;
+  const int *free = p.free + (size_t)item * keep, *late = p.late + (size_t)item * keep;
+  for (int r0 = first * MV; r0 < moves; r0 += warps * MV) {
+    int from = -1, dst = -1;
+    const int r = r0 + lane;
+    if (lane < MV && r < moves) {
+      const int src = __ldcg(&late[r]), slot = __ldcg(&free[r]);
+      if (src >= 0 && src < positions && slot >= 0 && slot < min(keep, positions)) {  // (always, but for lengths that change under the call)
+        p.kept[(size_t)item * keep + slot] = src;
+        to[slot] = mass[src];
+        from = page_of(p.a, seq, src);
+        dst = page_of(p.a, seq, slot);
+        if (from >= 0 && dst >= 0) {
+          from = paged_row(p.a, from, 0, head, src);
+          dst = paged_row(p.a, dst, 0, head, slot);
+        } else {
+          from = -1;
+        }
+      }
+    }
+    uint4 x[MV * LP / 32];
+    int d[MV * LP / 32];
+#pragma unroll
+    for (int i = 0; i < MV * LP / 32; ++i) {
+      const int pick = i * (32 / LP) + mine, f = __shfl_sync(0xffffffffu, from, pick);
+      d[i] = __shfl_sync(0xffffffffu, dst, pick);
+      if (f < 0) d[i] = -1;
+      else x[i] = reinterpret_cast<const uint4*>(paged_at<HD>(p.a, f + kv * half))[word];
+    }
+#pragma unroll
+    for (int i = 0; i < MV * LP / 32; ++i)
+      if (d[i] >= 0) reinterpret_cast<uint4*>(paged_at<HD>(p.a, d[i] + kv * half))[word] = x[i];
+  }
+}
 
 // HELD: the block's masses are in shared memory as unsigned numbers; else (contexts too long for it) read each time.
-template <bool HELD>
-__global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictArgs p, int C) {
+template <int HD, bool HELD>
+__global__ void __launch_bounds__(kSelThreads) k_evict(const __grid_constant__ EvictArgs p, int C) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(16) int hist[2][kBins], total[kBins];
   __shared__ Before cnt[2];
@@ -101,7 +154,8 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   const int others = max(0, len - p.recent);
   const float* mass = p.mass.p + seq * p.mass.seq + head * p.mass.head;
   int* kept = p.kept + (size_t)item * keep;
-  int* late = p.late + (size_t)item * keep;
+  int *free = p.free + (size_t)item * keep, *late = p.late + (size_t)item * keep;
+  float* to = p.to.p + seq * p.to.seq + head * p.to.head;
   // the block's run of the positions (a multiple of the warps' 32), and this warp's of it
   const int per = ((len + C - 1) / C + kSelThreads - 1) / kSelThreads * kSelThreads;
   const int lo = (int)min((long long)len, (long long)rank * per), n = min(len - lo, per);
@@ -151,10 +205,10 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     } else {
       __syncthreads();
     }
-    // two bins a thread, from the top
-    const int2 c2 = *reinterpret_cast<const int2*>((C > 1 ? total : h) + kBins - 2 - 2 * tid);
-    const int c[2] = {c2.y, c2.x};
-    const int sum = c[0] + c[1];
+    // four bins a thread, from the top
+    const int4 c4 = *reinterpret_cast<const int4*>((C > 1 ? total : h) + kBins - 4 - 4 * tid);
+    const int c[4] = {c4.w, c4.z, c4.y, c4.x};
+    const int sum = (c[0] + c[1]) + (c[2] + c[3]);
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -168,9 +222,9 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     int above = incl - sum;
     if (above < left && left <= incl) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         if (above < left && left <= above + c[i]) {
-          s_digit = kBins - 1 - 2 * tid - i;
+          s_digit = kBins - 1 - 4 * tid - i;
           s_left = left - above;
           s_ties = c[i];
         }
@@ -224,81 +278,48 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     n_late += __popc(s & ~below(i));
   });
   const int2 at0 = before(cnt[1], n_free, n_late, rank);
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");  // (this block reads no other's shared memory any more)
-  const uint32_t under = (1u << lane) - 1;
+  const int moves = min(total_of(cnt[1], C), keep);
+  const uint32_t under = (1u << lane) - 1, me = 1u << lane;
   int nf = at0.x, nl = at0.y;
   walk(tie0, [&](int i, uint32_t s) {
-    const uint32_t fs = there(i) & below(i) & ~s, ls = s & ~below(i), me = 1u << lane;
-    const int q = lo + i + lane;
-    if (s & below(i) & me) kept[q] = q;
-    if (fs & me) kept[q] = -2 - (nf + __popc(fs & under));
-    const int at = nl + __popc(ls & under);
-    if ((ls & me) && at < keep) late[at] = q;
+    const uint32_t fs = there(i) & below(i) & ~s, ls = s & ~below(i);
+    const int q = lo + i + lane, af = nf + __popc(fs & under), al = nl + __popc(ls & under);
+    if (s & below(i) & me) {
+      kept[q] = q;
+      if (!p.in_place) to[q] = mass[q];
+    }
+    if ((fs & me) && af < keep) free[af] = q;
+    if ((ls & me) && al < keep) late[al] = q;
+    if ((there(i) & ~below(i) & me) && !p.in_place) to[q] = 0.f;
     nf += __popc(fs);
     nl += __popc(ls);
   });
+  const int positions = p.a.max_pages * kPageTokens;
   for (int q = len + rank * kSelThreads + tid; q < keep; q += C * kSelThreads) kept[q] = -1;
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // no block leaves while others read its shared memory
+  if (!p.in_place)
+    for (int q = len + rank * kSelThreads + tid; q < positions; q += C * kSelThreads) to[q] = 0.f;
+  cluster_sync();  // the lists are whole, and no block reads another's shared memory any more
+
+  if (p.counts) {  // the moves are another kernel's
+    if (rank == 0 && tid == 0) p.counts[item] = moves;
+  } else {
+    make_moves<HD>(p, item, seq, head, moves, rank * kSelWarps + w, C * kSelWarps);
+  }
+  if (p.lengths != p.a.lengths && head == 0 && rank == 0 && tid == 0) p.lengths[seq] = min(len, keep);
 }
 
-// A warp takes 32 slots of an item: their masses, then the rows that move, K in the first
-// half of the lanes that a position's 4 * HD bytes take and V in the second.
 template <int HD>
-__global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ EvictArgs p, int width, int chunks) {
-  constexpr int LP = HD / 4, LR = LP / 2;  // lanes of a move, of a row
-  const int item = blockIdx.x / chunks, lane = threadIdx.x & 31;
-  const int s0 = ((blockIdx.x - item * chunks) * 8 + (threadIdx.x >> 5)) * 32;
-  const int seq = item / p.a.n_kv_heads, head = item - seq * p.a.n_kv_heads;
-  const int most = p.a.max_pages * kPageTokens;
+__global__ void __launch_bounds__(256) k_evict_moves(const __grid_constant__ EvictArgs p, int blocks) {
   behind();
-  if (head == 0 && s0 == 0 && lane == 0) p.lengths[seq] = min(held_length(p.a, seq), p.keep);
-  const int slot = s0 + lane;
-  int src = slot < p.keep ? p.kept[(size_t)item * p.keep + slot] : -1;
-  if (src < -1) {  // a free slot takes the late position of its number
-    const int i = -2 - src;
-    src = i < p.keep ? p.late[(size_t)item * p.keep + i] : -1;
-    p.kept[(size_t)item * p.keep + slot] = src;
-  }
-  if (src < 0 || src >= most) src = -1;
-  const float* mass = p.mass.p + seq * p.mass.seq + head * p.mass.head;
-  float* to = p.to.p + seq * p.to.seq + head * p.to.head;
-  if (slot < width && !(p.in_place && (src < 0 || src == slot))) to[slot] = src >= 0 ? mass[src] : 0.f;
-  const bool moves = src >= 0 && src != slot && slot < most;
-  int from = -1, dst = -1;
-  if (moves) {
-    from = page_of(p.a, seq, src);
-    dst = page_of(p.a, seq, slot);
-    if (from < 0 || dst < 0) {
-      from = -1;
-    } else {
-      from = paged_row(p.a, from, 0, head, src);
-      dst = paged_row(p.a, dst, 0, head, slot);
-    }
-  }
-  const int half = p.a.n_kv_heads * kPageTokens;  // rows from K to V
-  uint32_t todo = __ballot_sync(0xffffffffu, from >= 0);
-  const int mine = lane / LP, word = lane % LR, kv = lane % LP / LR;
-  while (todo) {
-    uint4 x[8];
-    int d[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      int pick = -1;
-#pragma unroll
-      for (int j = 0; j < 32 / LP; ++j) {
-        const int b = __ffs(todo) - 1;
-        if (j == mine) pick = b;
-        if (b >= 0) todo &= todo - 1;
-      }
-      const int f = __shfl_sync(0xffffffffu, from, max(pick, 0));
-      d[i] = __shfl_sync(0xffffffffu, dst, max(pick, 0));
-      if (pick < 0) d[i] = -1;
-      else x[i] = reinterpret_cast<const uint4*>(paged_at<HD>(p.a, f + kv * half))[word];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (d[i] >= 0) reinterpret_cast<uint4*>(paged_at<HD>(p.a, d[i] + kv * half))[word] = x[i];
-  }
+  const int item = blockIdx.x / blocks, seq = item / p.a.n_kv_heads, head = item - seq * p.a.n_kv_heads;
+  make_moves<HD>(p, item, seq, head, min(p.counts[item], p.keep), (blockIdx.x - item * blocks) * 8 + (threadIdx.x >> 5), blocks * 8);
+}
+
+// New lengths in the place of the old ones, once all blocks have read those.
+__global__ void __launch_bounds__(256) k_evict_lengths(const __grid_constant__ EvictArgs p) {
+  behind();
+  const int s = blockIdx.x * 256 + threadIdx.x;
+  if (s < p.a.n_seqs) p.lengths[s] = min(held_length(p.a, s), p.keep);
 }
 
 int check(const mk_paged_cache* c, int keep, bool* empty) {
@@ -313,7 +334,7 @@ int check(const mk_paged_cache* c, int keep, bool* empty) {
   return MK_OK;
 }
 
-size_t bytes_of(const mk_paged_cache& c, int keep) { return (size_t)c.n_seqs * c.n_kv_heads * keep * sizeof(int32_t); }
+size_t bytes_of(const mk_paged_cache& c, int keep) { return (size_t)c.n_seqs * c.n_kv_heads * (2 * (size_t)keep + 1) * sizeof(int32_t); }
 
 }  // namespace
 }  // namespace mk
@@ -350,7 +371,8 @@ extern "C" MK_API int mk_paged_evict(const mk_paged_cache* c, const mk_paged_mas
   p.keep = keep;
   p.recent = recent;
   p.kept = kept;
-  p.late = static_cast<int32_t*>(workspace);
+  p.free = static_cast<int32_t*>(workspace);
+  p.late = p.free + (size_t)c->n_seqs * c->n_kv_heads * keep;
   p.lengths = new_lengths;
   cudaStream_t st = (cudaStream_t)stream;
   const int items = c->n_seqs * c->n_kv_heads, positions = c->max_pages * kPageTokens;
@@ -363,17 +385,23 @@ extern "C" MK_API int mk_paged_evict(const mk_paged_cache* c, const mk_paged_mas
   while (C < kMostBlocks && (((long long)items * C * 2 <= 2 * sms && positions / (2 * C) >= 2048) || positions / C > kMost)) C *= 2;
   const int per = ((positions + C - 1) / C + kSelThreads - 1) / kSelThreads * kSelThreads;
   const bool held = per <= kMost;
-  const void* select = held ? reinterpret_cast<const void*>(&k_evict_select<true>) : reinterpret_cast<const void*>(&k_evict_select<false>);
-  cudaError_t e = held ? cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost * 4) : cudaSuccess;
+  const void* f = c->head_dim == 64 ? held ? reinterpret_cast<const void*>(&k_evict<64, true>) : reinterpret_cast<const void*>(&k_evict<64, false>)
+                  : held            ? reinterpret_cast<const void*>(&k_evict<128, true>)
+                                    : reinterpret_cast<const void*>(&k_evict<128, false>);
+  cudaError_t e = held ? cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost * 4) : cudaSuccess;
+  if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   void* args[] = {&p, &C};
-  if (e == cudaSuccess) e = launch(select, (unsigned)items * C, kSelThreads, held ? (size_t)per * 4 : 0, st, args, C);
-  if (e == cudaSuccess) {
-    int width = p.in_place ? std::min(keep, positions) : positions;
-    int chunks = (std::max(width, std::min(keep, positions)) + 255) / 256;
-    void* margs[] = {&p, &width, &chunks};
-    const void* move = c->head_dim == 64 ? reinterpret_cast<const void*>(&k_evict_move<64>) : reinterpret_cast<const void*>(&k_evict_move<128>);
-    e = launch(move, (unsigned)items * chunks, 256, 0, st, margs);
+  // Many moves (a cut of whole prompts) are levelled over all SMs by a kernel of their own; a cache at its budget has few.
+  p.counts = std::min(keep, positions - keep) > kFew ? p.late + (size_t)items * keep : nullptr;
+  if (e == cudaSuccess) e = launch(f, (unsigned)items * C, kSelThreads, held ? (size_t)per * 4 : 0, st, args, C);
+  if (e == cudaSuccess && p.counts) {
+    int blocks = (8 * sms + items - 1) / items;
+    void* margs[] = {&p, &blocks};
+    e = launch(c->head_dim == 64 ? reinterpret_cast<const void*>(&k_evict_moves<64>) : reinterpret_cast<const void*>(&k_evict_moves<128>),
+               (unsigned)items * blocks, 256, 0, st, margs);
   }
+  if (e == cudaSuccess && new_lengths == c->lengths)
+    e = launch(reinterpret_cast<const void*>(&k_evict_lengths), (unsigned)(c->n_seqs + 255) / 256, 256, 0, st, args);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return host_fail(MK_ERR_CUDA, (std::string("paged evict: ") + cudaGetErrorString(e)).c_str());
