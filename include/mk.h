@@ -579,7 +579,7 @@ MK_API size_t mk_paged_attention_bytes(const mk_paged_cache* c, int32_t n_heads,
  *   new_mass     the masses moved along, 0 behind the new length; may be `mass` itself, whose
  *                values behind the new length then stay
  * rows and n_new of the description are not used.  1 <= keep, 0 <= recent <= keep, n_seqs x
- * n_kv_heads x keep < 2^31.  Pages that hold positions below `keep` are written: no other
+ * n_kv_heads x keep < 2^31, max_pages <= 6144 (else UNSUPPORTED).  Pages that hold positions below `keep` are written: no other
  * sequence may share them.  A page outside the pool is reported in status, and moves from or to
  * it are left out.  workspace: mk_paged_evict_bytes, as above.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */

@@ -8,8 +8,8 @@
 // ties do; ties, free slots and late positions (kept ones at or above `keep`) are then
 // numbered in order.  An item is a cluster of blocks, each with a run of the positions, which
 // it holds in shared memory (read from the masses again in each pass, an item of 131071 took 64 us),
-// and each of its warps a run of that, so that numbers are sums over the warps before; counts go through
-// distributed shared memory.  Every block passes the same barriers whatever it reads, so that
+// and each of its threads a run of that, so that numbers are sums over the threads before (numbers by ballots of
+// a warp's 32 positions took ten times the instructions); counts go through distributed shared memory.  Every block passes the same barriers whatever it reads, so that
 // lengths written meanwhile give a wrong answer, not a hang.
 //
 // Moves.  Only late positions move, into free slots: never more rows than it takes, sources
@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kSelWarps = 16, kSelThreads = 32 * kSelWarps, kBins = 4 * kSelThreads;  // four bins a thread
 constexpr int kMostBlocks = 16;  // of an item's cluster
+constexpr int kMostHeld = 96 * kSelThreads;  // positions that a block holds
 constexpr int kFew = 256;        // moves of an item, at most, that its own blocks make
 
 struct EvictArgs {
@@ -69,29 +70,33 @@ __device__ __forceinline__ void peer_store(const void* p, int rank, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_addr(p, rank)), "r"(v) : "memory");
 }
 
-// Two numbers' sums over all warps of the cluster before this one.
+// Two numbers' sums over all threads of the cluster before this one, and the first one's over all.
 struct Before {
   int2 warp[kSelWarps];
   int x, y;  // of the block
 };
-__device__ __forceinline__ int2 before(Before& b, int x, int y, int rank) {
+__device__ __forceinline__ int3 before(Before& b, int x, int y, int rank, int C) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) b.warp[w] = make_int2(x, y);
+  int ix = x, iy = y;  // over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int ux = __shfl_up_sync(0xffffffffu, ix, o), uy = __shfl_up_sync(0xffffffffu, iy, o);
+    if (lane >= o) ix += ux, iy += uy;
+  }
+  if (lane == 31) b.warp[w] = make_int2(ix, iy);
   __syncthreads();
+  int2 n = lane < kSelWarps ? b.warp[lane] : make_int2(0, 0);
   if (w == 0) {
-    const int2 n = lane < kSelWarps ? b.warp[lane] : make_int2(0, 0);
     const int sx = __reduce_add_sync(0xffffffffu, n.x), sy = __reduce_add_sync(0xffffffffu, n.y);
     if (lane == 0) b.x = sx, b.y = sy;
   }
-  cluster_sync();
-  int2 n = lane < w ? b.warp[lane] : make_int2(0, 0);
-  if (lane < rank) n.x += peer_load(&b.x, lane), n.y += peer_load(&b.y, lane);
-  return make_int2(__reduce_add_sync(0xffffffffu, n.x), __reduce_add_sync(0xffffffffu, n.y));
-}
-// The first number's sum over the cluster.
-__device__ __forceinline__ int total_of(Before& b, int C) {
-  const int lane = threadIdx.x & 31;
-  return __reduce_add_sync(0xffffffffu, lane < C ? peer_load(&b.x, lane) : 0);
+  if (C > 1) cluster_sync();
+  else __syncthreads();
+  if (lane >= w) n = make_int2(0, 0);
+  const int px = lane < C ? peer_load(&b.x, lane) : 0;
+  if (lane < rank) n.x += px, n.y += peer_load(&b.y, lane);
+  return make_int3(__reduce_add_sync(0xffffffffu, n.x) + ix - x, __reduce_add_sync(0xffffffffu, n.y) + iy - y,
+                   __reduce_add_sync(0xffffffffu, px));
 }
 
 // The moves of an item by warps `first`, `first` + 1 .. of `warps`, MV at a time: K in the first half of the lanes
@@ -138,10 +143,9 @@ __device__ __forceinline__ void make_moves(const EvictArgs& p, int item, int seq
   }
 }
 
-// HELD: the block's masses are in shared memory as unsigned numbers; else (contexts too long for it) read each time.
-template <int HD, bool HELD>
+template <int HD>
 __global__ void __launch_bounds__(kSelThreads) k_evict(const __grid_constant__ EvictArgs p, int C) {
-  extern __shared__ __align__(16) uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t held[];  // of a thread's PT positions: masses as unsigned numbers, later what becomes of them
   __shared__ __align__(16) int hist[2][kBins], total[kBins];
   __shared__ Before cnt[2];
   __shared__ int scan[kSelWarps], s_digit, s_left, s_ties;
@@ -151,23 +155,19 @@ __global__ void __launch_bounds__(kSelThreads) k_evict(const __grid_constant__ E
   behind();
   const int len = held_length(p.a, seq), keep = p.keep;
   const bool all = len <= keep;
-  const int others = max(0, len - p.recent);
+  const int others = max(0, len - p.recent), positions = p.a.max_pages * kPageTokens;
   const float* mass = p.mass.p + seq * p.mass.seq + head * p.mass.head;
-  int* kept = p.kept + (size_t)item * keep;
-  int *free = p.free + (size_t)item * keep, *late = p.late + (size_t)item * keep;
   float* to = p.to.p + seq * p.to.seq + head * p.to.head;
-  // the block's run of the positions (a multiple of the warps' 32), and this warp's of it
-  const int per = ((len + C - 1) / C + kSelThreads - 1) / kSelThreads * kSelThreads;
+  int* kept = p.kept + (size_t)item * keep;
+  // Threads have runs of PT positions, PT | 1 words apart (an odd number: 32 threads' words are in 32 banks).
+  const int PT = max(4, ((len + C - 1) / C + kSelThreads - 1) / kSelThreads), apart = PT | 1, per = PT * kSelThreads;
+  const uint32_t magic = (uint32_t)((0x100000000ull + PT - 1) / PT);  // i / PT for i < 2^16 (PT <= 96)
+  auto at = [&](int i) { return i + (int)__umulhi((uint32_t)i, magic) * (apart - PT); };
   const int lo = (int)min((long long)len, (long long)rank * per), n = min(len - lo, per);
-  const int per_warp = per / kSelWarps, w0 = min(n, w * per_warp), w1 = min(n, w0 + per_warp);
-  auto key = [&](int i) { return HELD ? keys[i] : key_of(mass[lo + i]); };
-  if (HELD) {
+  const int i0 = min(n, tid * PT), i1 = min(n, i0 + PT);  // this thread's run
+  const uint32_t* mine = held + tid * apart;
 #pragma unroll 4
-    for (int i = 4 * tid; i < n; i += 4 * kSelThreads) {  // (rows are multiples of 128 positions: no word passes their end)
-      const float4 m = *reinterpret_cast<const float4*>(mass + lo + i);
-      *reinterpret_cast<uint4*>(keys + i) = make_uint4(key_of(m.x), key_of(m.y), key_of(m.z), key_of(m.w));
-    }
-  }
+  for (int i = tid; i < n; i += kSelThreads) held[at(i)] = key_of(mass[lo + i]);
   for (int i = tid; i < 2 * kBins; i += kSelThreads) hist[0][i] = 0;
   if (tid == 0) s_digit = s_left = s_ties = 0;
   __syncthreads();
@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(kSelThreads) k_evict(const __grid_constant__ E
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
     int* h = hist[pass & 1];
 #pragma unroll 4
-    for (int i = tid; i < m_others; i += kSelThreads) {
-      const uint32_t k = key(i);
+    for (int i = i0; i < min(i1, m_others); ++i) {
+      const uint32_t k = mine[i - i0];
       if (pass == 0 || k >> (shift + bits) == least >> (shift + bits)) atomicAdd(&h[k >> shift & ((1u << bits) - 1)], 1);
     }
     // Each block adds a part of the bins over the cluster and gives every block the sums (all bins of all blocks read
@@ -239,66 +239,59 @@ __global__ void __launch_bounds__(kSelThreads) k_evict(const __grid_constant__ E
   }
 
   // ---- numbers in order
-  // Which of the warp's next 32 positions stay (a word of the warp); `tie`: ties before them.  Where all ties stay, or none,
-  // they need no number.
+  // Where all ties stay, or none, they need no number.
   const bool some = left > 0 && left < s_ties;
-  auto stays = [&](int i, uint32_t k, int& tie) {
-    bool t = false, s = i < w1;
-    if (s && !all && lo + i < others) {
-      t = some && k == least;
-      s = left > 0 && k >= least;
-    }
-    if (some) {
-      const uint32_t ties = __ballot_sync(0xffffffffu, t);
-      if (t) s = tie + __popc(ties & ((1u << lane) - 1)) < left;
-      tie += __popc(ties);
-    }
-    return __ballot_sync(0xffffffffu, s);
+  int ties = 0;
+  if (some)
+    for (int i = i0; i < min(i1, m_others); ++i) ties += mine[i - i0] == least;
+  const int tie0 = before(cnt[0], ties, 0, rank, C).x;
+  const uint32_t above = left > 0 ? least : 0xFFFFFFFFu;  // (left = 0: of the others none stays, whatever its mass)
+  auto stays = [&](int i, int& tie) {
+    if (all || i >= m_others) return true;
+    const uint32_t k = mine[i - i0];
+    if (some && k == least) return tie++ < left;
+    return left > 0 && k >= above;
   };
-  // f(first position of 32, which stay), four words of keys read ahead
-  auto walk = [&](int tie, auto f) {
-    for (int i0 = w0; i0 < w1; i0 += 128) {
-      uint32_t k[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) k[u] = i0 + 32 * u + lane < w1 ? key(i0 + 32 * u + lane) : 0;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i0 + 32 * u < w1) f(i0 + 32 * u, stays(i0 + 32 * u + lane, k[u], tie));
-    }
-    return tie;
-  };
-  // of 32 positions, those there are and those below keep
-  auto there = [&](int i) { return i + 32 <= w1 ? ~0u : (1u << (w1 - i)) - 1; };
-  auto below = [&](int i) { return lo + i + 32 <= keep ? ~0u : lo + i >= keep ? 0u : (1u << (keep - lo - i)) - 1; };
-  const int n_tie = some ? walk(0, [](int, uint32_t) {}) : 0;
-  const int tie0 = before(cnt[0], n_tie, 0, rank).x;
-  int n_free = 0, n_late = 0;
-  walk(tie0, [&](int i, uint32_t s) {
-    n_free += __popc(there(i) & below(i) & ~s);
-    n_late += __popc(s & ~below(i));
-  });
-  const int2 at0 = before(cnt[1], n_free, n_late, rank);
-  const int moves = min(total_of(cnt[1], C), keep);
-  const uint32_t under = (1u << lane) - 1, me = 1u << lane;
+  int n_free = 0, n_late = 0, tie = tie0;
+  const int below = keep - lo;  // of the block's positions
+  for (int i = i0; i < i1; ++i) {
+    const bool s = stays(i, tie);
+    n_free += i < below && !s;
+    n_late += i >= below && s;
+  }
+  const int3 at0 = before(cnt[1], n_free, n_late, rank, C);
+  const int moves = min(at0.z, keep);
+  // what becomes of a position: its number among the free slots or late positions, or kStay
+  constexpr uint32_t kStay = 0xFFFFFFFFu, kGone = 0xFFFFFFFEu;
   int nf = at0.x, nl = at0.y;
-  walk(tie0, [&](int i, uint32_t s) {
-    const uint32_t fs = there(i) & below(i) & ~s, ls = s & ~below(i);
-    const int q = lo + i + lane, af = nf + __popc(fs & under), al = nl + __popc(ls & under);
-    if (s & below(i) & me) {
-      kept[q] = q;
-      if (!p.in_place) to[q] = mass[q];
+  tie = tie0;
+  for (int i = i0; i < i1; ++i) {
+    const bool s = stays(i, tie);
+    held[tid * apart + i - i0] = i < below ? s ? kStay : (uint32_t)nf++ : s ? (uint32_t)nl++ : kGone;
+  }
+  __syncthreads();
+  int *free = p.free + (size_t)item * keep, *late = p.late + (size_t)item * keep;
+#pragma unroll 4
+  for (int i = tid; i < n; i += kSelThreads) {
+    const int q = lo + i;
+    const uint32_t x = held[at(i)];
+    if (q < keep) {
+      if (x == kStay) {
+        kept[q] = q;
+        if (!p.in_place) to[q] = mass[q];
+      } else if (x < (uint32_t)keep) {
+        free[x] = q;
+      }
+    } else {
+      if (x < (uint32_t)keep) late[x] = q;
+      if (!p.in_place) to[q] = 0.f;
     }
-    if ((fs & me) && af < keep) free[af] = q;
-    if ((ls & me) && al < keep) late[al] = q;
-    if ((there(i) & ~below(i) & me) && !p.in_place) to[q] = 0.f;
-    nf += __popc(fs);
-    nl += __popc(ls);
-  });
-  const int positions = p.a.max_pages * kPageTokens;
+  }
   for (int q = len + rank * kSelThreads + tid; q < keep; q += C * kSelThreads) kept[q] = -1;
   if (!p.in_place)
     for (int q = len + rank * kSelThreads + tid; q < positions; q += C * kSelThreads) to[q] = 0.f;
-  cluster_sync();  // the lists are whole, and no block reads another's shared memory any more
+  if (C > 1) cluster_sync();  // the lists are whole, and no block reads another's shared memory any more
+  else __syncthreads();
 
   if (p.counts) {  // the moves are another kernel's
     if (rank == 0 && tid == 0) p.counts[item] = moves;
@@ -330,7 +323,8 @@ int check(const mk_paged_cache* c, int keep, bool* empty) {
   if (keep < 1) return host_fail(MK_ERR_INVALID_ARG, "keep must be >= 1");
   if ((long long)c->n_seqs * c->n_kv_heads * keep > INT_MAX)
     return host_fail(MK_ERR_INVALID_ARG, "n_seqs x n_kv_heads x keep passes 31 bits");
-  if (c->max_pages > INT_MAX / kPageTokens / 2) return host_fail(MK_ERR_INVALID_ARG, "max_pages is too large");
+  if (c->max_pages > kMostBlocks * kMostHeld / kPageTokens)
+    return host_fail(MK_ERR_UNSUPPORTED, "eviction takes tables of at most 6144 pages (786432 positions)");
   return MK_OK;
 }
 
@@ -379,21 +373,18 @@ extern "C" MK_API int mk_paged_evict(const mk_paged_cache* c, const mk_paged_mas
   if ((long long)items * ((positions + 255) / 256) > INT_MAX || (long long)items * kMostBlocks > INT_MAX)
     return host_fail(MK_ERR_INVALID_ARG, "n_seqs x n_kv_heads x max_pages is too large");
   // Blocks of an item: while they run at once (two an SM) and have 2048 positions each, or until they hold theirs.
-  constexpr int kMost = 40 * 1024;  // positions that a block holds, a multiple of its threads
   const int sms = device_sms();
   int C = 1;
-  while (C < kMostBlocks && (((long long)items * C * 2 <= 2 * sms && positions / (2 * C) >= 2048) || positions / C > kMost)) C *= 2;
-  const int per = ((positions + C - 1) / C + kSelThreads - 1) / kSelThreads * kSelThreads;
-  const bool held = per <= kMost;
-  const void* f = c->head_dim == 64 ? held ? reinterpret_cast<const void*>(&k_evict<64, true>) : reinterpret_cast<const void*>(&k_evict<64, false>)
-                  : held            ? reinterpret_cast<const void*>(&k_evict<128, true>)
-                                    : reinterpret_cast<const void*>(&k_evict<128, false>);
-  cudaError_t e = held ? cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost * 4) : cudaSuccess;
+  while (C < kMostBlocks && (((long long)items * C * 2 <= 2 * sms && positions / (2 * C) >= 2048) || positions > C * kMostHeld)) C *= 2;
+  const int PT = std::max(4, ((positions + C - 1) / C + kSelThreads - 1) / kSelThreads);
+  const size_t smem = (size_t)kSelThreads * (PT + 1) * sizeof(uint32_t);
+  const void* f = c->head_dim == 64 ? reinterpret_cast<const void*>(&k_evict<64>) : reinterpret_cast<const void*>(&k_evict<128>);
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelThreads * (kMostHeld / kSelThreads + 1) * 4);
   if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   void* args[] = {&p, &C};
   // Many moves (a cut of whole prompts) are levelled over all SMs by a kernel of their own; a cache at its budget has few.
   p.counts = std::min(keep, positions - keep) > kFew ? p.late + (size_t)items * keep : nullptr;
-  if (e == cudaSuccess) e = launch(f, (unsigned)items * C, kSelThreads, held ? (size_t)per * 4 : 0, st, args, C);
+  if (e == cudaSuccess) e = launch(f, (unsigned)items * C, kSelThreads, smem, st, args, C);
   if (e == cudaSuccess && p.counts) {
     int blocks = (8 * sms + items - 1) / items;
     void* margs[] = {&p, &blocks};

@@ -35,7 +35,10 @@ def test_descriptions_are_refused_by_every_call(lib, kw, want):
     heads = 2000 if kw.get("n_kv_heads") == 2000 else 2
     assert attention(c, heads) == want
     assert L.mk_paged_attention_bytes(c, heads, L.MK_BF16) == L.mk_paged_attention_bytes(c, heads, L.MK_F32, True) == 0
-    if "rows" not in kw:                      # eviction has no rows
+    if kw == dict(max_pages=1 << 25):
+        assert evict(c) == want and L.mk_paged_evict_bytes(c, 16) == 0
+        assert evict(cache(max_pages=6145)) == L.MK_ERR_UNSUPPORTED and L.mk_paged_evict_bytes(cache(max_pages=6144), 16) > 0
+    elif "rows" not in kw:                    # eviction has no rows
         if kw != dict(n_seqs=1000):
             assert evict(c) == want
             assert L.mk_paged_evict_bytes(c, 16) == 0
