@@ -608,9 +608,11 @@ void take_for(Plan* pl, int cols, int dtype) {
     pl->wide = true;
     return;
   }
-  constexpr int R = HD == 128 ? 5 : 8;
-  if (dtype == MK_F32) cols <= 8 ? take<HD, float, 1, 4, 1, R, 1>(pl) : take<HD, float, 2, 4, 1, R, 1>(pl);
-  else cols <= 8 ? take<HD, __nv_bfloat16, 1, 4, 1, R, 1>(pl) : take<HD, __nv_bfloat16, 2, 4, 1, R, 1>(pl);
+  // Two blocks an SM with two stages each (four of 64 dimensions): one fills the memory system while the other starts or
+  // joins its warps (64 sequences of 4096 to 16384 202 us, 16 of 256 to 8448 with masses 38; one block with five stages 208 and 43).
+  constexpr int R = HD == 128 ? 2 : 4;
+  if (dtype == MK_F32) cols <= 8 ? take<HD, float, 1, 4, 1, R, 2>(pl) : take<HD, float, 2, 4, 1, R, 2>(pl);
+  else cols <= 8 ? take<HD, __nv_bfloat16, 1, 4, 1, R, 2>(pl) : take<HD, __nv_bfloat16, 2, 4, 1, R, 2>(pl);
 }
 
 // The kernels take more shared memory than the default: asked for once per device.
