@@ -24,10 +24,11 @@ __device__ __forceinline__ __nv_bfloat16* paged_at(const Kv4Args& a, int row) {
 
 // Every kernel here begins behind the stream's last one as soon as that has no block left to
 // start, and waits for its end before it reads or writes memory (so a kernel's start, about 2 us of
-// a short call, overlaps what runs before it).
+// a short call, overlaps what runs before it).  The next one may begin only then: what it reads before its own wait (the
+// join reads the lengths) must be final.
 __device__ __forceinline__ void behind() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 inline cudaError_t launch(const void* kernel, unsigned grid, int block, size_t smem, cudaStream_t st, void** args, int cluster = 0,
                           unsigned grid_y = 1) {

@@ -693,7 +693,7 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, bool mass, 
   } else {
     pl->grid = (int)std::min<long long>(room, items * most);
     const long long all_cols = items * std::min<long long>(cols, pl->CT);
-    pl->join_cols = all_cols <= 10 * sms ? 1 : all_cols <= 54 * sms ? 8 : 16;
+    pl->join_cols = all_cols <= 10 * sms ? 1 : 8;
     int nw = 2;
     while (nw < 16 && nw * 2 * items <= pl->grid) nw *= 2;
     pl->join_many = pl->grid / 64 >= items && all_cols <= sms;  // 64 parts an item and more, a block an SM at most
@@ -798,7 +798,8 @@ static int run_attention(const Kv4Args& a, int head_dim, int n_heads, const Kv4R
   if (e == cudaSuccess) e = launch(pl.main, pl.grid, pl.threads, pl.smem, stream, args, pl.cluster);
   if (e == cudaSuccess && !pl.cluster) {
     void* jargs[] = {&p, &pl.CT, &pl.SP, &pl.grid, &pl.join_cols};
-    e = launch(kv4_join_kernel(head_dim, dtype, pl.join_many), pl.items, pl.join_threads, 0, stream, jargs, 0,
+    if (pl.wide) e = launch(paged_wide_join(head_dim, dtype), pl.items, 256, 0, stream, jargs, 0, pl.CT / 16);
+    else e = launch(kv4_join_kernel(head_dim, dtype, pl.join_many), pl.items, pl.join_threads, 0, stream, jargs, 0,
                (pl.CT + pl.join_cols - 1) / pl.join_cols);
   }
   if (e == cudaSuccess && mass) e = paged_mass(pa, *mass, head_dim, dtype, map, stream);
