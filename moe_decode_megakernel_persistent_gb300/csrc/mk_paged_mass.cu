@@ -71,7 +71,7 @@ struct MassShape {
 };
 constexpr int kSpan = 2 * kPageTokens;  // positions of an item
 constexpr int kSetUp = 2;               // tiles that an item's set-up counts as
-constexpr int kLse = 4;                 // tiles whose log-sum-exps are held
+constexpr int kLse = 8;                 // tiles whose log-sum-exps are held
 
 struct MassArgs {
   PagedAtt pa;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
   uint8_t* sm = sm_raw + ((1024 - (smem_addr(sm_raw) & 1023)) & 1023);
   __shared__ __align__(8) uint64_t k_full[KS], k_empty[KS], q_full[QS], q_empty[QS], s_full[2][2], s_empty[2][2], l_full[kLse], l_empty[kLse], run_full[kMassRuns], drain;
   __shared__ MassRun says[kMassRuns];
-  __shared__ __align__(16) float lse2[kLse][N];  // log2; +infinity: a column that gives nothing
+  __shared__ __align__(16) float less[kLse][N];  // minus the log-sum-exp (log2); -infinity: a column that gives nothing
   __shared__ int lims[kLse][N];                  // positions that a column sees
   __shared__ int cut[kLse];                      // a column of the tile does not see all of an item's positions
   __shared__ uint32_t tm_base;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
   after_sync();
   const uint32_t tm = tm_base;  // scores of page x in place b at 256 b + 128 x
   auto take_run = [&](uint32_t i, MassRun& r) {
-    if (!bar_wait(smem_addr(&run_full[i % kMassRuns]), (i / kMassRuns) & 1, &give_up, p.a.status)) return false;
+    if (!wait_for(smem_addr(&run_full[i % kMassRuns]), (i / kMassRuns) & 1, &give_up, p.a.status)) return false;
     r = says[i % kMassRuns];
     return r.t1 > r.t0;
   };
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
       ++n_runs;
       // the two pages' K; a page outside the pool, or none: zeros
       const int ks = n_items % KS;
-      ok = n_items < KS || bar_wait(smem_addr(&k_empty[ks]), (n_items / KS - 1) & 1, &give_up, p.a.status);
+      ok = n_items < KS || wait_for(smem_addr(&k_empty[ks]), (n_items / KS - 1) & 1, &give_up, p.a.status);
       ++n_items;
       if (ok && lane == 0) {
         const uint32_t bar = smem_addr(&k_full[ks]);
@@ -277,9 +277,22 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
         }
       }
       __syncwarp();
+      // a tile's log-sum-exps, read while the last tile's are handed on
+      float ahead[N / 32];
+      auto read = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) {
+          const int col = min((r.c0 + t) * N + 32 * i + lane, p.cols - 1), row = row_of(p, col);
+          ahead[i] = __ldcg(&p.lse[((size_t)r.seq * p.a.rows + row) * p.n_heads + r.head * p.gqa + col - row * p.gqa]);
+        }
+      };
+      read(r.t0);
       for (int t = r.t0; t < r.t1 && ok; ++t, ++tile) {
         const int qs = tile % QS, ls = tile % kLse, col0 = (r.c0 + t) * N;
-        ok = tile < QS || bar_wait(smem_addr(&q_empty[qs]), (tile / QS - 1) & 1, &give_up, p.a.status);
+        float now[N / 32];
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) now[i] = ahead[i];
+        ok = tile < QS || wait_for(smem_addr(&q_empty[qs]), (tile / QS - 1) & 1, &give_up, p.a.status);
         if (ok && lane == 0) {
           const uint32_t bar = smem_addr(&q_full[qs]);
           expect(bar, S::P * S::QT);
@@ -289,20 +302,20 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
         }
         __syncwarp();
         if (!ok) break;
-        ok = tile < kLse || bar_wait(smem_addr(&l_empty[ls]), (tile / kLse - 1) & 1, &give_up, p.a.status);
+        ok = tile < kLse || wait_for(smem_addr(&l_empty[ls]), (tile / kLse - 1) & 1, &give_up, p.a.status);
         if (!ok) break;
+        if (t + 1 < r.t1) read(t + 1);
         bool some = false;
 #pragma unroll
-        for (int x = lane; x < N; x += 32) {
-          const int col = col0 + x, row = row_of(p, col);
+        for (int i = 0; i < N / 32; ++i) {
+          const int x = 32 * i + lane, col = col0 + x, row = row_of(p, col);
           const int lim = col < p.cols && row < r.nn ? max(0, r.len - r.nn + row + 1) : 0;
-          float l = INFINITY;
+          float l = -INFINITY;
           if (lim) {
-            l = p.lse[((size_t)r.seq * p.a.rows + row) * p.n_heads + r.head * p.gqa + col - row * p.gqa] * kLog2e;
-            if (l == -INFINITY) l = INFINITY;  // its scores have no weight
+            l = now[i] == -INFINITY ? now[i] : now[i] * -kLog2e;  // (its scores have no weight)
             some = some || lim < min(r.len, (r.span + 1) * kSpan);
           }
-          lse2[ls][x] = l;
+          less[ls][x] = l;
           lims[ls][x] = lim;
         }
         some = __any_sync(0xffffffffu, some);
@@ -319,8 +332,8 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
     }
     if (give_up && lane == 0) {  // copies in flight land before the block ends
       int none = 0;
-      for (uint32_t i = n_items > KS ? n_items - KS : 0; i < n_items; ++i) bar_wait_long(smem_addr(&k_full[i % KS]), (i / KS) & 1, &none, nullptr);
-      for (uint32_t i = tile > QS ? tile - QS : 0; i <= tile; ++i) bar_wait_long(smem_addr(&q_full[i % QS]), (i / QS) & 1, &none, nullptr);
+      for (uint32_t i = n_items > KS ? n_items - KS : 0; i < n_items; ++i) wait_for(smem_addr(&k_full[i % KS]), (i / KS) & 1, &none, nullptr);
+      for (uint32_t i = tile > QS ? tile - QS : 0; i <= tile; ++i) wait_for(smem_addr(&q_full[i % QS]), (i / QS) & 1, &none, nullptr);
     }
   } else if (w > CW) {  // ---- a page's products
     constexpr uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((128 >> 4) << 24);  // bf16, fp32 sums
@@ -330,11 +343,11 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
     MassRun r;
     for (uint32_t n_runs = 0; take_run(n_runs, r); ++n_runs) {
       const int ks = n_runs % KS;
-      bool ok = bar_wait(smem_addr(&k_full[ks]), (n_runs / KS) & 1, &give_up, p.a.status);
+      bool ok = wait_for(smem_addr(&k_full[ks]), (n_runs / KS) & 1, &give_up, p.a.status);
       for (int t = r.t0; t < r.t1; ++t, ++tile) {
         const int qs = tile % QS, b = tile & 1;
-        ok = bar_wait(smem_addr(&q_full[qs]), (tile / QS) & 1, &give_up, p.a.status) && ok;
-        if (tile >= 2) ok = bar_wait(smem_addr(&s_empty[pg][b]), (tile / 2 - 1) & 1, &give_up, p.a.status) && ok;
+        ok = wait_for(smem_addr(&q_full[qs]), (tile / QS) & 1, &give_up, p.a.status) && ok;
+        if (tile >= 2) ok = wait_for(smem_addr(&s_empty[pg][b]), (tile / 2 - 1) & 1, &give_up, p.a.status) && ok;
         after_sync();
         const uint32_t qsu = uniform(qs), bu = uniform(b), ksu = uniform(ks), end = uniform(t + 1 == r.t1);
         if (ok && !give_up && elect_one()) {
@@ -362,7 +375,7 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
     if (give_up) {  // products in flight end before the block does
       int none = 0;
       if (lane == 0) commit(smem_addr(&drain));
-      bar_wait_long(smem_addr(&drain), 0, &none, nullptr);
+      wait_for(smem_addr(&drain), 0, &none, nullptr);
     }
   } else {  // ---- a position each
     const int pg = w >> 2;
@@ -376,28 +389,32 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
         const int page = table_row(p.a, r.seq)[at / kPageTokens];
         in = page >= 0 && page < p.a.n_pages;
       }
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t sum[2] = {0, 0};
+      const uint64_t c2 = pair(p.c, p.c);
       bool ok = true;
       for (int t = r.t0; t < r.t1; ++t, ++tile) {
         const int ls = tile % kLse, b = tile & 1;
-        ok = bar_wait(smem_addr(&l_full[ls]), (tile / kLse) & 1, &give_up, p.a.status) && ok;
-        ok = bar_wait(smem_addr(&s_full[pg][b]), (tile / 2) & 1, &give_up, p.a.status) && ok;
+        ok = wait_for(smem_addr(&l_full[ls]), (tile / kLse) & 1, &give_up, p.a.status) && ok;
+        ok = wait_for(smem_addr(&s_full[pg][b]), (tile / 2) & 1, &give_up, p.a.status) && ok;
         after_sync();
         if (ok && !give_up) {
           auto add = [&](auto cut_) {
             constexpr bool CUT = decltype(cut_)::value;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < N; c += 32) {
               float s[32];
               tm_read32(tm_s + 256 * b + c, s);
 #pragma unroll
               for (int x = 0; x < 32; x += 4) {
-                const float4 l = *reinterpret_cast<const float4*>(&lse2[ls][c + x]);
-                const float l4[4] = {l.x, l.y, l.z, l.w};
+                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(&less[ls][c + x]);
+                const uint64_t l2[2] = {l.x, l.y};
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  const float e = exp2_fast(fmaf(s[x + y], p.c, -l4[y]));
-                  if (!CUT || at < lims[ls][c + x + y]) sum[y] += e;
+                for (int y = 0; y < 2; ++y) {
+                  float2 e = unpair(fma2(pair(s[x + 2 * y], s[x + 2 * y + 1]), c2, l2[y]));
+                  e.x = exp2_fast(e.x), e.y = exp2_fast(e.y);
+                  if (CUT && at >= lims[ls][c + x + 2 * y]) e.x = 0.f;
+                  if (CUT && at >= lims[ls][c + x + 2 * y + 1]) e.y = 0.f;
+                  sum[y] = add2(sum[y], pair(e.x, e.y));
                 }
               }
             }
@@ -412,7 +429,8 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
           arrive(smem_addr(&l_empty[ls]));
         }
       }
-      const float v = !ok ? NAN : in ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
+      const float2 both = unpair(add2(sum[0], sum[1]));
+      const float v = !ok ? NAN : in ? both.x + both.y : 0.f;
       const bool whole = r.t0 == 0 && r.t1 == r.nt;
       if (!whole) {
         a.part[(size_t)part_slot(blockIdx.x, r.t0) * kSpan + tid] = v;
