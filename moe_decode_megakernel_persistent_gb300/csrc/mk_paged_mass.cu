@@ -67,7 +67,7 @@ struct MassShape {
   static constexpr int QT = NG * N * 128;            // bytes of a part of a tile of columns
   static constexpr int QS = 2;                       // places of tiles
   static constexpr int SMEM = 1024 + KS * 2 * KB + QS * P * QT;
-  static constexpr int CW = 8, THREADS = 32 * (CW + 3);  // a page's four warps twice, copies, products of each page
+  static constexpr int CW = 16, THREADS = 32 * (CW + 3);  // a page's four warps for each half of a tile's columns, copies, products of each page
 };
 constexpr int kSpan = 2 * kPageTokens;  // positions of an item
 constexpr int kSetUp = 2;               // tiles that an item's set-up counts as
@@ -180,11 +180,12 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
   const AttArgs& p = a.pa.t;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024 - (smem_addr(sm_raw) & 1023)) & 1023);
-  __shared__ __align__(8) uint64_t k_full[KS], k_empty[KS], q_full[QS], q_empty[QS], s_full[2][2], s_empty[2][2], l_full[kLse], l_empty[kLse], run_full[kMassRuns], drain;
+  __shared__ __align__(8) uint64_t k_full[KS], k_empty[KS], q_full[QS], q_empty[QS], s_full[2][2], s_empty[2][2], l_full[kLse], l_empty[kLse], run_full[kMassRuns], h_full, h_empty, drain;
   __shared__ MassRun says[kMassRuns];
   __shared__ __align__(16) float less[kLse][N];  // minus the log-sum-exp (log2); -infinity: a column that gives nothing
   __shared__ int lims[kLse][N];                  // positions that a column sees
   __shared__ int cut[kLse];                      // a column of the tile does not see all of an item's positions
+  __shared__ float halves[kSpan];                // a run's sums of the second half of the columns
   __shared__ uint32_t tm_base;
   __shared__ volatile int give_up;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -198,6 +199,8 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
     for (int i = 0; i < 4; ++i) init(&s_full[i >> 1][i & 1], 1), init(&s_empty[i >> 1][i & 1], CW / 2);
     for (int i = 0; i < kLse; ++i) init(&l_full[i], 1), init(&l_empty[i], CW);
     for (int i = 0; i < kMassRuns; ++i) init(&run_full[i], 1);
+    init(&h_full, CW / 2);
+    init(&h_empty, CW / 2);
     init(&drain, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     give_up = 0;
@@ -378,12 +381,13 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
       wait_for(smem_addr(&drain), 0, &none, nullptr);
     }
   } else {  // ---- a position each
-    const int pg = w >> 2;
+    // (two threads: a half of the columns each)
+    const int pg = w >> 2 & 1, half = w >> 3, me = tid & (kSpan - 1);
     const uint32_t tm_s = tm + 128 * pg + ((uint32_t)(32 * (w & 3)) << 16);
     uint32_t tile = 0;
     MassRun r;
     for (uint32_t n_runs = 0; take_run(n_runs, r); ++n_runs) {
-      const int at = r.span * kSpan + tid;  // the position (tid: page pg, lane of TMEM)
+      const int at = r.span * kSpan + me;  // the position (me: page pg, lane of TMEM)
       bool in = false;
       if (at < r.len) {
         const int page = table_row(p.a, r.seq)[at / kPageTokens];
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
           auto add = [&](auto cut_) {
             constexpr bool CUT = decltype(cut_)::value;
 #pragma unroll 1
-            for (int c = 0; c < N; c += 32) {
+            for (int c = half * (N / 2); c < (half + 1) * (N / 2); c += 32) {
               float s[32];
               tm_read32(tm_s + 256 * b + c, s);
 #pragma unroll
@@ -430,16 +434,27 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
         }
       }
       const float2 both = unpair(add2(sum[0], sum[1]));
-      const float v = !ok ? NAN : in ? both.x + both.y : 0.f;
-      const bool whole = r.t0 == 0 && r.t1 == r.nt;
-      if (!whole) {
-        a.part[(size_t)part_slot(blockIdx.x, r.t0) * kSpan + tid] = v;
-      } else if (at < r.len) {
-        float* to = a.ms.p + r.seq * a.ms.seq + r.head * a.ms.head + at;
-        *to = at < r.len - r.nn ? fmaf(a.ms.decay, *to, v) : v;
+      float v = !ok ? NAN : in ? both.x + both.y : 0.f;
+      if (half) {
+        if (n_runs) ok = wait_for(smem_addr(&h_empty), (n_runs - 1) & 1, &give_up, p.a.status) && ok;  // the last run's are read
+        halves[me] = v;
+        __syncwarp();
+        if (lane == 0) arrive(smem_addr(&h_full));
+      } else {
+        ok = wait_for(smem_addr(&h_full), n_runs & 1, &give_up, p.a.status) && ok;
+        v = ok ? v + halves[me] : NAN;
+        __syncwarp();
+        if (lane == 0) arrive(smem_addr(&h_empty));
+        const bool whole = r.t0 == 0 && r.t1 == r.nt;
+        if (!whole) {
+          a.part[(size_t)part_slot(blockIdx.x, r.t0) * kSpan + me] = v;
+        } else if (at < r.len) {
+          float* to = a.ms.p + r.seq * a.ms.seq + r.head * a.ms.head + at;
+          *to = at < r.len - r.nn ? fmaf(a.ms.decay, *to, v) : v;
+        }
+        if (tid == 0 && r.t0 == 0)
+          a.item[((size_t)r.seq * p.a.n_kv_heads + r.head) * a.spans + r.span] = make_longlong2(whole ? -1 : r.base, blockIdx.x);
       }
-      if (tid == 0 && r.t0 == 0)
-        a.item[((size_t)r.seq * p.a.n_kv_heads + r.head) * a.spans + r.span] = make_longlong2(whole ? -1 : r.base, blockIdx.x);
       if (!ok) break;
     }
   }
