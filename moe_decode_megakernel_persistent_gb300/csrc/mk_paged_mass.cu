@@ -67,7 +67,7 @@ struct MassShape {
   static constexpr int QT = NG * N * 128;            // bytes of a part of a tile of columns
   static constexpr int QS = 2;                       // places of tiles
   static constexpr int SMEM = 1024 + KS * 2 * KB + QS * P * QT;
-  static constexpr int CW = 16, THREADS = 32 * (CW + 3);  // a page's four warps for each half of a tile's columns, copies, products of each page
+  static constexpr int CW = 16, THREADS = 32 * (CW + 2);  // a page's four warps for each half of a tile's columns, copies, products
 };
 constexpr int kSpan = 2 * kPageTokens;  // positions of an item
 constexpr int kSetUp = 2;               // tiles that an item's set-up counts as
@@ -194,14 +194,14 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
     auto init = [](uint64_t* b, int n) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(n) : "memory");
     };
-    for (int i = 0; i < KS; ++i) init(&k_full[i], 1), init(&k_empty[i], 2);
-    for (int i = 0; i < QS; ++i) init(&q_full[i], 1), init(&q_empty[i], 2);
+    for (int i = 0; i < KS; ++i) init(&k_full[i], 1), init(&k_empty[i], 1);
+    for (int i = 0; i < QS; ++i) init(&q_full[i], 1), init(&q_empty[i], 1);
     for (int i = 0; i < 4; ++i) init(&s_full[i >> 1][i & 1], 1), init(&s_empty[i >> 1][i & 1], CW / 2);
     for (int i = 0; i < kLse; ++i) init(&l_full[i], 1), init(&l_empty[i], CW);
     for (int i = 0; i < kMassRuns; ++i) init(&run_full[i], 1);
     init(&h_full, CW / 2);
     init(&h_empty, CW / 2);
-    init(&drain, 2);
+    init(&drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     give_up = 0;
   }
@@ -338,40 +338,42 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
       for (uint32_t i = n_items > KS ? n_items - KS : 0; i < n_items; ++i) wait_for(smem_addr(&k_full[i % KS]), (i / KS) & 1, &none, nullptr);
       for (uint32_t i = tile > QS ? tile - QS : 0; i <= tile; ++i) wait_for(smem_addr(&q_full[i % QS]), (i / QS) & 1, &none, nullptr);
     }
-  } else if (w > CW) {  // ---- a page's products
+  } else if (w == CW + 1) {  // ---- the products
     constexpr uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((128 >> 4) << 24);  // bf16, fp32 sums
-    const int pg = w - CW - 1;
-    const uint32_t tmu = uniform(tm + 128 * pg), ku = uniform(smem_addr(k_op + pg * S::KB)), qu = uniform(smem_addr(q_op));
+    const uint32_t tmu = uniform(tm), ku = uniform(smem_addr(k_op)), qu = uniform(smem_addr(q_op));
     uint32_t tile = 0;
     MassRun r;
+    bool ok = true;
     for (uint32_t n_runs = 0; take_run(n_runs, r); ++n_runs) {
-      const int ks = n_runs % KS;
-      bool ok = wait_for(smem_addr(&k_full[ks]), (n_runs / KS) & 1, &give_up, p.a.status);
+      const uint32_t ks = uniform(n_runs % KS);
+      ok = wait_for(smem_addr(&k_full[ks]), (n_runs / KS) & 1, &give_up, p.a.status) && ok;
       for (int t = r.t0; t < r.t1; ++t, ++tile) {
-        const int qs = tile % QS, b = tile & 1;
+        const uint32_t qs = uniform(tile % QS), b = uniform(tile & 1), end = uniform(t + 1 == r.t1);
         ok = wait_for(smem_addr(&q_full[qs]), (tile / QS) & 1, &give_up, p.a.status) && ok;
-        if (tile >= 2) ok = wait_for(smem_addr(&s_empty[pg][b]), (tile / 2 - 1) & 1, &give_up, p.a.status) && ok;
-        after_sync();
-        const uint32_t qsu = uniform(qs), bu = uniform(b), ksu = uniform(ks), end = uniform(t + 1 == r.t1);
-        if (ok && !give_up && elect_one()) {
-          const uint64_t kd = operand(ku + ksu * 2 * S::KB);
 #pragma unroll
-          for (int x = S::P - 1; x >= 0; --x) {  // q's low parts first
-            const uint64_t qd = operand(qu + (qsu * S::P + x) * S::QT);
+        for (int pg = 0; pg < 2; ++pg) {
+          if (tile >= 2) ok = wait_for(smem_addr(&s_empty[pg][b]), (tile / 2 - 1) & 1, &give_up, p.a.status) && ok;
+          after_sync();
+          if (ok && elect_one()) {
+            const uint64_t kd = operand(ku + (ks * 2 + pg) * S::KB);
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
+            for (int x = S::P - 1; x >= 0; --x) {  // q's low parts first
+              const uint64_t qd = operand(qu + (qs * S::P + x) * S::QT);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t ka = kd + ((g * 128 * 128 + kk * 32) >> 4), qb = qd + ((g * N * 128 + kk * 32) >> 4);
-                if (g == 0 && kk == 0 && x == S::P - 1) mma_ss<false>(tmu + 256 * bu, ka, qb, id);
-                else mma_ss<true>(tmu + 256 * bu, ka, qb, id);
-              }
+              for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  const uint64_t ka = kd + ((g * 128 * 128 + kk * 32) >> 4), qb = qd + ((g * N * 128 + kk * 32) >> 4);
+                  if (g == 0 && kk == 0 && x == S::P - 1) mma_ss<false>(tmu + 256 * b + 128 * pg, ka, qb, id);
+                  else mma_ss<true>(tmu + 256 * b + 128 * pg, ka, qb, id);
+                }
+            }
+            commit(smem_addr(&s_full[pg][b]));
+            if (pg) commit(smem_addr(&q_empty[qs]));
+            if (pg && end) commit(smem_addr(&k_empty[ks]));
           }
-          commit(smem_addr(&s_full[pg][bu]));
-          commit(smem_addr(&q_empty[qsu]));
-          if (end) commit(smem_addr(&k_empty[ksu]));
+          __syncwarp();
         }
-        __syncwarp();
       }
       if (!ok || give_up) break;
     }
