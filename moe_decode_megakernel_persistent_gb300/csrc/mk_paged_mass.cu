@@ -67,7 +67,7 @@ struct MassShape {
   static constexpr int QT = NG * N * 128;            // bytes of a part of a tile of columns
   static constexpr int QS = 2;                       // places of tiles
   static constexpr int SMEM = 1024 + KS * 2 * KB + QS * P * QT;
-  static constexpr int CW = 16, THREADS = 32 * (CW + 2);  // a page's four warps for each half of a tile's columns, copies, products
+  static constexpr int CW = 16, THREADS = 32 * (CW + 3);  // a page's four warps for each half of a tile's columns, copies, products, log-sum-exps
 };
 constexpr int kSpan = 2 * kPageTokens;  // positions of an item
 constexpr int kSetUp = 2;               // tiles that an item's set-up counts as
@@ -280,21 +280,8 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
         }
       }
       __syncwarp();
-      // a tile's log-sum-exps, read while the last tile's are handed on
-      float ahead[N / 32];
-      auto read = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < N / 32; ++i) {
-          const int col = min((r.c0 + t) * N + 32 * i + lane, p.cols - 1), row = row_of(p, col);
-          ahead[i] = __ldcg(&p.lse[((size_t)r.seq * p.a.rows + row) * p.n_heads + r.head * p.gqa + col - row * p.gqa]);
-        }
-      };
-      read(r.t0);
       for (int t = r.t0; t < r.t1 && ok; ++t, ++tile) {
-        const int qs = tile % QS, ls = tile % kLse, col0 = (r.c0 + t) * N;
-        float now[N / 32];
-#pragma unroll
-        for (int i = 0; i < N / 32; ++i) now[i] = ahead[i];
+        const int qs = tile % QS, col0 = (r.c0 + t) * N;
         ok = tile < QS || wait_for(smem_addr(&q_empty[qs]), (tile / QS - 1) & 1, &give_up, p.a.status);
         if (ok && lane == 0) {
           const uint32_t bar = smem_addr(&q_full[qs]);
@@ -305,13 +292,43 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
         }
         __syncwarp();
         if (!ok) break;
+      }
+    }
+    if (lane == 0) {
+      says[n_runs % kMassRuns].t0 = says[n_runs % kMassRuns].t1 = 0;
+      arrive(smem_addr(&run_full[n_runs % kMassRuns]));
+    }
+    if (give_up && lane == 0) {  // copies in flight land before the block ends
+      int none = 0;
+      for (uint32_t i = n_items > KS ? n_items - KS : 0; i < n_items; ++i) wait_for(smem_addr(&k_full[i % KS]), (i / KS) & 1, &none, nullptr);
+      for (uint32_t i = tile > QS ? tile - QS : 0; i < tile; ++i) wait_for(smem_addr(&q_full[i % QS]), (i / QS) & 1, &none, nullptr);
+    }
+  } else if (w == CW + 2) {  // ---- log-sum-exps (next to the copies they took 1,200 cycles of a tile's 1,900)
+    uint32_t tile = 0;
+    bool ok = true;
+    MassRun r;
+    for (uint32_t n_runs = 0; ok && take_run(n_runs, r); ++n_runs) {
+      float ahead[N / 32];  // a tile's, read while the last tile's are handed on
+      auto read = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) {
+          const int col = min((r.c0 + t) * N + 32 * i + lane, p.cols - 1), row = row_of(p, col);
+          ahead[i] = __ldcg(&p.lse[((size_t)r.seq * p.a.rows + row) * p.n_heads + r.head * p.gqa + col - row * p.gqa]);
+        }
+      };
+      read(r.t0);
+      for (int t = r.t0; t < r.t1 && ok; ++t, ++tile) {
+        const int ls = tile % kLse;
+        float now[N / 32];
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) now[i] = ahead[i];
+        if (t + 1 < r.t1) read(t + 1);
         ok = tile < kLse || wait_for(smem_addr(&l_empty[ls]), (tile / kLse - 1) & 1, &give_up, p.a.status);
         if (!ok) break;
-        if (t + 1 < r.t1) read(t + 1);
         bool some = false;
 #pragma unroll
         for (int i = 0; i < N / 32; ++i) {
-          const int x = 32 * i + lane, col = col0 + x, row = row_of(p, col);
+          const int x = 32 * i + lane, col = (r.c0 + t) * N + x, row = row_of(p, col);
           const int lim = col < p.cols && row < r.nn ? max(0, r.len - r.nn + row + 1) : 0;
           float l = -INFINITY;
           if (lim) {
@@ -328,15 +345,6 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
         }
         __syncwarp();
       }
-    }
-    if (lane == 0) {
-      says[n_runs % kMassRuns].t0 = says[n_runs % kMassRuns].t1 = 0;
-      arrive(smem_addr(&run_full[n_runs % kMassRuns]));
-    }
-    if (give_up && lane == 0) {  // copies in flight land before the block ends
-      int none = 0;
-      for (uint32_t i = n_items > KS ? n_items - KS : 0; i < n_items; ++i) wait_for(smem_addr(&k_full[i % KS]), (i / KS) & 1, &none, nullptr);
-      for (uint32_t i = tile > QS ? tile - QS : 0; i <= tile; ++i) wait_for(smem_addr(&q_full[i % QS]), (i / QS) & 1, &none, nullptr);
     }
   } else if (w == CW + 1) {  // ---- the products
     constexpr uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((128 >> 4) << 24);  // bf16, fp32 sums
@@ -382,7 +390,7 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
       if (lane == 0) commit(smem_addr(&drain));
       wait_for(smem_addr(&drain), 0, &none, nullptr);
     }
-  } else {  // ---- a position each
+  } else if (w < CW) {  // ---- a position each
     // (two threads: a half of the columns each)
     const int pg = w >> 2 & 1, half = w >> 3, me = tid & (kSpan - 1);
     const uint32_t tm_s = tm + 128 * pg + ((uint32_t)(32 * (w & 3)) << 16);
