@@ -410,9 +410,17 @@ __global__ void __launch_bounds__(32 * W, B) k_paged_attention(const __grid_cons
           }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (S::F32) {  // 16 positions' terms by themselves: the products' own sums are cut off, not rounded
+            float f[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int y = S::P - 1; y >= 0; --y) mma(o[nt][i], x, wf[y][nt]);
+            for (int y = S::P - 1; y >= 0; --y) mma(f, x, wf[y][nt]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][i][e] += f[e];
+          } else {
+            mma(o[nt][i], x, wf[0][nt]);
+          }
+        }
       }
     };
 

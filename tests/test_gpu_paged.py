@@ -367,6 +367,79 @@ def test_same_bits_each_time(gpu_lib):
         assert all(torch.equal(a, b) for g in got[1:] for a, b in zip(got[0], g))
 
 
+@pytest.mark.parametrize("dtype,rows,hd", [(F32, 10, 128), (BF, 10, 128), (F32, 9, 64), (BF, 33, 64), (BF, 60, 128)])
+def test_blocks_of_several_runs(gpu_lib, dtype, rows, hd):
+    """Blocks whose runs follow one another (a run's sums leave through the place of the next one's queries), many times."""
+    lengths = [(701 * i) % 3000 + 200 for i in range(60)]
+    pool, table = make(lengths, 4, hd, seed=20)
+    q = randn((60, rows, 16, hd), 21, dtype, 1.5)
+    out, lse, m = check(q, pool, table, lengths, mass=masses(table, 4))
+    for _ in range(40):
+        mm = masses(table, 4)
+        o, l = paged.attention(q, pool, table, i32(lengths), return_lse=True, mass=mm)
+        assert torch.equal(o, out) and torch.equal(l, lse) and torch.equal(mm, m)
+
+
+@pytest.mark.parametrize("hd,rows", [(128, 40), (64, 40), (128, 1)])
+def test_long_sums_of_fp32_rows(gpu_lib, hd, rows):
+    """One kv head, 30000 positions: runs of many steps.  The products cut off up to 2^-23 of the sum with each of the
+    24 that a step of 128 positions has, of which 8 steps go into one sum: 192 2^-23 at most, next to the rounded sums of all
+    steps and the weights' own error (tests/_paged.py), as norms."""
+    n = 30000
+    pool, table = make([n] * 6, 1, hd, seed=22)
+    q = randn((6, rows, 4, hd), 23, F32, 1.5)
+    out = paged.attention(q, pool, table, i32([n] * 6))
+    for i in range(6):
+        k, v = R.rows_of(pool, table, i, n)
+        want, wl, w, A, D = R.attend(q[i], k, v, n - rows, 1 / math.sqrt(hd))
+        assert float((out[i].double() - want).norm() / want.norm()) < 192 * 2.0 ** -23
+
+
+def test_kernels_behind_one_another_see_new_lengths(gpu_lib):
+    """Store, attention, eviction in place and again, without a pause: each reads what the last one wrote."""
+    G, H, hd, keep = 4, 16, 128, 300
+    table, n_pages = R.table_for([1024] * 8, seed=24)
+    k, v = randn((8, 200, G, hd), 1, BF), randn((8, 200, G, hd), 2, BF)
+    q = randn((8, 200, H, hd), 3, BF)
+
+    def go(wait):
+        pool, mass, ln, got = paged.new_pool(n_pages, G, hd), paged.new_mass(table, G), i32([0] * 8), []
+        for step in range(12):
+            rows = 200 if step < 3 else 1 + step % 3
+            ln += rows
+            paged.store(pool, table, ln, k[:, :rows], v[:, :rows])
+            if wait:
+                torch.cuda.synchronize()
+            out, lse = paged.attention(q[:, :rows], pool, table, ln, mass=mass, decay=0.9, return_lse=True)
+            if wait:
+                torch.cuda.synchronize()
+            kept, _, _ = paged.evict(pool, table, ln, mass, keep, recent=20, new_lengths=ln, new_mass=mass)
+            if wait:
+                torch.cuda.synchronize()
+            got += [out, lse, kept, ln.clone(), mass.clone()]
+        return got
+
+    want = go(True)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(go(False), want))
+
+
+def test_calls_on_two_streams_at_once(gpu_lib):
+    pool, table = make([2000, 900], 4, 128, seed=25)
+    qs = [randn((2, rows, 16, 128), rows, dtype) for rows, dtype in ((1, BF), (60, BF), (60, F32), (3, F32))]
+    want = [paged.attention(q, pool, table, i32([2000, 900]), return_lse=True) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = [[] for _ in qs]
+    for _ in range(10):
+        for i, (q, s) in enumerate(zip(qs, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(paged.attention(q, pool, table, i32([2000, 900]), return_lse=True))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, b) for x in g for a, b in zip(x, w))
+
+
 def test_captured_graphs_follow_their_inputs(gpu_lib):
     """Two graphs over the same tensors, replayed in turn and with other lengths, pages and rows."""
     G, H, hd = 2, 8, 64
@@ -464,6 +537,18 @@ def test_evictions(gpu_lib, G, hd, lengths, keep, recent, in_place):
     mass = masses(table, G)
     mass[mass < 0.4] = 0.0                       # many ties
     check_evict(pool, table, lengths, mass, keep, recent, in_place)
+
+
+def test_evictions_into_masses_of_other_strides(gpu_lib):
+    pool, table = make([700, 300], 3, 64, seed=26)
+    mass = masses(table, 3)
+    want = paged.evict(pool.clone(), table, i32([700, 300]), mass, 250, recent=9)
+    wide = torch.full((3, 2, mass.shape[2] + 8), 7.0, device="cuda")
+    to, ln = wide[:, :, :mass.shape[2]].transpose(0, 1), i32([-1, -1])
+    kept, nl, nm = paged.evict(pool, table, i32([700, 300]), mass, 250, recent=9, new_lengths=ln, new_mass=to)
+    assert nl is ln and nm is to
+    assert torch.equal(kept, want[0]) and torch.equal(nl, want[1]) and torch.equal(nm, want[2])
+    assert bool((wide[:, :, mass.shape[2]:] == 7.0).all())
 
 
 @pytest.mark.parametrize("seqs,n", [(1, 131071), (3, 20000), (40, 4097), (100, 300)])
