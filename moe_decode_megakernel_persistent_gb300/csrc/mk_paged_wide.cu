@@ -388,11 +388,24 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
         __syncwarp();
         if (lane == 0) arrive(smem_addr(&flushed));
         const float f = exp2_fast(m_held - now);
+#pragma unroll
         for (int c = 0; c < HD / 2; ++c) held[c] = m_held == kLow ? o[c] : fmaf(held[c], f, o[c]);
         m_held = now;
       };
-      for (int t = rs.t0 + skip; t < rs.t1; t += GR) {
+      for (int t = rs.t0 + skip;; t += GR) {
         const uint32_t kk = k + (t - rs.t0);
+        if constexpr (W::FLUSH > 0) {  // both groups, before the first step of new sums or the one behind it
+          const int i = t - rs.t0, in = i % W::FLUSH;
+          if (i >= W::FLUSH && in < GR && i - in < rs.t1 - rs.t0) {
+            float now = m;
+            if (in == 0) {  // (the other group had the last step)
+              wait_for(smem_addr(&m_full[group ^ 1][quarter]), ((kk - 1) >> 1) & 1, &give_up, p.a.status);
+              now = *reinterpret_cast<volatile float*>(ex + me);
+            }
+            flush(now);
+          }
+        }
+        if (t >= rs.t1) break;
         const bool in = page >= 0 && page < p.a.n_pages;
         if (t + GR < rs.t1) page = pages[t + GR];
         bool ok = wait_for(smem_addr(&s_full[tile][kk % NS]), (kk / NS) & 1, &give_up, p.a.status);
@@ -445,8 +458,6 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
             l *= exp2_fast(m - now);
             m = now;
             const bool fresh = W::FLUSH ? (t - rs.t0) % W::FLUSH == 0 : t == rs.t0;  // the sums begin with this step
-            if constexpr (W::FLUSH > 0)
-              if (fresh && t > rs.t0) flush(last);
             if (moves && !fresh) {
               if constexpr (NS > 1) {  // the sums hold the last step (with one place of scores these have waited for it)
                 wait_for(smem_addr(&pv_done), (kk - 1) & 1, &give_up, p.a.status);
@@ -497,8 +508,6 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
           if (__all_sync(0xffffffffu, vis >= SP)) step(std::false_type());
           else step(std::true_type());
           given(1);
-          if constexpr (W::FLUSH > 0)
-            if (t + 1 < rs.t1 && (t + 1 - rs.t0) % W::FLUSH == 0) flush(m);  // the other thread's step is the next, and begins new sums
         }
       }
       k += rs.t1 - rs.t0;
