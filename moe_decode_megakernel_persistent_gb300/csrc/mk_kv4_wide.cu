@@ -440,9 +440,7 @@ __global__ void __launch_bounds__(Wide<HD, T, TB>::THREADS, Wide<HD, T, TB>::BLO
             constexpr bool CUT = decltype(cut_)::value;
             float s[4][16], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tm_load16(at + 16 * c, s[c]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tm_loaded(s[c]);
+            for (int c = 0; c < 4; c += 2) tm_read32(at + 16 * c, *reinterpret_cast<float(*)[32]>(s[c]));
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -464,8 +462,7 @@ __global__ void __launch_bounds__(Wide<HD, T, TB>::THREADS, Wide<HD, T, TB>::BLO
                 for (int c = 0; c < HD; c += 16) {
                   float o[16];
                   uint32_t x16[16];
-                  tm_load16(tm_o + c, o);
-                  tm_loaded(o);
+                  tm_read16(tm_o + c, o);
 #pragma unroll
                   for (int x = 0; x < 16; ++x) x16[x] = __float_as_uint(o[x] * fo);
                   tm_store16(tm_o + c, x16);
@@ -523,8 +520,7 @@ __global__ void __launch_bounds__(Wide<HD, T, TB>::THREADS, Wide<HD, T, TB>::BLO
 #pragma unroll 1
       for (int c = 0; c < HD; c += 16) {
         float o[16];
-        tm_load16(tm_o + c, o);
-        tm_loaded(o);
+        tm_read16(tm_o + c, o);
         if (!there) continue;
         const bool nan = give_up || (NG == 2 && c >= 64 ? bad[NG - 1] : bad[0]);
 #pragma unroll
