@@ -550,10 +550,12 @@ typedef struct mk_paged_mass {
  * out gets the rows in q's dtype, lse (may be NULL) float32 [n_seqs][rows][n_heads]
  * the natural logarithm of the sum of exp(scale * q . k).  A row that sees nothing
  * gets zeros and -infinity.  What a position that a row does not see holds (NaN,
- * infinities) never shows in that row.  out must not overlap q, the pool, the masses or
- * the workspace.  |scale| < 1e18.  Scores, maxima and sums are fp32; the weights are
- * rounded to bfloat16 (2^-8) for bf16 rows; an fp32 q and its weights are three
- * bfloat16 parts (2^-24).
+ * infinities) never shows in that row; of what it sees, a score of -infinity has no weight,
+ * one of +infinity or NaN makes the row NaN, and an infinite or NaN V reaches its own dimension
+ * whatever its weight.  out must not overlap q, the pool, the masses or
+ * the workspace.  |scale| < 1e18; a score below -6.9e29 has no weight.  Scores, maxima and sums are
+ * fp32; the weights are rounded to bfloat16 (2^-8) for bf16 rows; an fp32 q and its weights are
+ * three bfloat16 parts (2^-24), and each result is off by a few 10^-6 of its values' size at most.
  * mass (may be NULL): for every sequence with a new row, and p < lengths[i],
  *     mass[i][g][p] = (p < lengths[i] - n_new[i] ? decay * mass[i][g][p] : 0)
  *                   + the sum of the weights that the rows and the heads of kv head g give p,
@@ -579,8 +581,9 @@ MK_API size_t mk_paged_attention_bytes(const mk_paged_cache* c, int32_t n_heads,
  *   new_mass     the masses moved along, 0 behind the new length; may be `mass` itself, whose
  *                values behind the new length then stay
  * rows and n_new of the description are not used.  1 <= keep, 0 <= recent <= keep, n_seqs x
- * n_kv_heads x keep < 2^31, max_pages <= 6144 (else UNSUPPORTED).  Pages that hold positions below `keep` are written: no other
- * sequence may share them.  A page outside the pool is reported in status, and moves from or to
+ * n_kv_heads x keep < 2^31, max_pages <= 6144 (else UNSUPPORTED).  Pages that hold
+ * positions below `keep` are written: no other sequence may share them, and the sequence's own
+ * table names them once.  new_lengths must not overlap the table.  A page outside the pool is reported in status, and moves from or to
  * it are left out.  workspace: mk_paged_evict_bytes, as above.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 MK_API int mk_paged_evict(const mk_paged_cache* c, const mk_paged_mass* mass, int32_t keep, int32_t recent,

@@ -113,7 +113,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 // The wide kernel (mk_paged_wide.cu): tiles of CT columns and SP positions; null: none.
-WideKernel paged_wide_kernel(int head_dim, int dtype, int cols);
+WideKernel paged_wide_kernel(int head_dim, int dtype, int cols, long long steps);
 const void* paged_wide_join(int head_dim, int dtype);  // blocks of 256 threads for 16 columns of an item
 // Rows of head_dim bf16 values as a tensor map whose copies bring `box` rows.
 int rows_map(CUtensorMap* map, const void* base, long long rows, int head_dim, int box);

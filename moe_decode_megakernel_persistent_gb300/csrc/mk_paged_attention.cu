@@ -1,5 +1,5 @@
 // Causal attention over the 16-bit paged K/V cache (mk_paged_attention): single rows of a
-// decode step and a few rows of a sequence; prompt chunks run in mk_paged_wide.cu.
+// decode step and a few rows of a sequence (up to 16 to 32 query columns); prompt chunks run in mk_paged_wide.cu.
 //
 // Mathematics.  For a row q and the positions p it sees, s_p = c q . K_p with c = scale log2 e,
 // out = sum_p 2^(s_p - m) V_p / sum_p 2^(s_p - m).  Products are bf16 (mma.sync m16n8k16) with
@@ -23,6 +23,12 @@
 // What a column does not see must not show in it, and 0 x NaN is NaN: V of positions that no
 // column of a step sees is taken as 0, and where columns differ, a V that is no finite number is taken out
 // of the product and added to the columns that see it.
+//
+// Bounds.  Large batches run at the memory's rate: 64 sequences of 4096 to 16384 positions, one row of 16 heads on 4 of 128
+// dimensions, read 1.34 GB in 196 us and take 202 with the join (the copy's rate gives 197).  16 of 256 to 8448 take 31
+// (21 by bytes: the join is 5, the start and the runs' ends as much).  One of 2049 takes 7.2, which is the chain
+// launch, lengths and pages, first copies, a step or two, join in the cluster.  The few columns leave the tensor cores 9 %
+// and the issue slots 11 % busy.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -576,8 +582,16 @@ __global__ void __launch_bounds__(32 * W, B) k_paged_attention(const __grid_cons
 
 // ---------------------------------------------------------------- host
 
-constexpr int kShort = 10;       // steps of a block, at most, for work that counts as short
-constexpr int kNarrow = 16;      // columns up to which the narrow kernel runs
+// A cluster for each item saves the second kernel but leaves SMs idle: it runs for blocks of up to kShort steps, and up to
+// twice that where equal runs would save fewer than kJoin steps each (one row of 16 heads on 4 of 128; with the second part and
+// without: 40 sequences of 1000 positions 20.0 and 25.4 us, 16 of 4100 26.7 and 30.1, 16 of 100 to 4100 20.7 and 20.1; one of
+// 20000, 20 steps a block against 4, 19.6 and 16.9).
+constexpr int kShort = 10, kJoin = 8;
+// Columns up to which the narrow kernel runs, as far as registers hold the sums and q of a warp's columns (one sequence of
+// 8022 positions of 4 heads; narrow and wide): fp32 16 (128 dimensions, 18.1 and 32.0 us; more would spill), bf16 24 (128
+// dimensions, 15.0 and 27.3; 32, which spill, 19.9 and 28.4 but with 64 sequences 222 and 169) and 32 (64 dimensions, 12.9 and 22.2; with 64
+// sequences of 100 to 8022 positions 78 and 153).
+constexpr int narrow_cols(int head_dim, int dtype) { return dtype == MK_F32 ? 16 : head_dim == 64 ? 32 : 24; }
 
 struct Plan {
   bool wide = false;
@@ -594,7 +608,7 @@ template <int HD, class T, int NT, int W, int U, int R, int B>
 void take(Plan* pl) {
   using S = Shape<HD, T, NT, W, U, R, B>;
   pl->main = reinterpret_cast<const void*>(&k_paged_attention<HD, T, NT, W, U, R, B>);
-  pl->id = (HD == 64 ? 0 : 8) + (S::F32 ? 4 : 0) + NT;
+  pl->id = (HD == 64 ? 0 : 10) + (S::F32 ? 5 : 0) + NT;
   pl->CT = S::CT;
   pl->SP = S::SP;
   pl->smem = pl->base_smem = S::SMEM;
@@ -602,12 +616,13 @@ void take(Plan* pl) {
   pl->threads = 32 * W;
 }
 
+// steps: of the wide kernel's tiles of 128 columns, for an SM
 template <int HD>
-void take_for(Plan* pl, int cols, int dtype) {
-  if (cols > kNarrow) {
-    const WideKernel w = paged_wide_kernel(HD, dtype, cols);
+void take_for(Plan* pl, int cols, int dtype, long long steps) {
+  if (cols > narrow_cols(HD, dtype)) {
+    const WideKernel w = paged_wide_kernel(HD, dtype, cols, steps);
     pl->main = w.fn;
-    pl->id = (HD == 64 ? 0 : 8) + (dtype == MK_F32 ? 4 : 0) + (w.CT > 128 ? 3 : 0);
+    pl->id = (HD == 64 ? 0 : 10) + (w.CT > 128 ? 8 : dtype == MK_F32 ? 5 : 0);
     pl->CT = w.CT;
     pl->SP = w.SP;
     pl->smem = pl->base_smem = w.smem;
@@ -618,9 +633,12 @@ void take_for(Plan* pl, int cols, int dtype) {
   }
   // Two blocks an SM with two stages each (four of 64 dimensions): one fills the memory system while the other starts or
   // joins its warps (64 sequences of 4096 to 16384 202 us, 16 of 256 to 8448 with masses 38; one block with five stages 208 and 43).
+  // Three tiles of 128 dimensions need the shared memory for the sums' join: one block with four stages.
   constexpr int R = HD == 128 ? 2 : 4;
   if (dtype == MK_F32) cols <= 8 ? take<HD, float, 1, 4, 1, R, 2>(pl) : take<HD, float, 2, 4, 1, R, 2>(pl);
-  else cols <= 8 ? take<HD, __nv_bfloat16, 1, 4, 1, R, 2>(pl) : take<HD, __nv_bfloat16, 2, 4, 1, R, 2>(pl);
+  else if (cols <= 16) cols <= 8 ? take<HD, __nv_bfloat16, 1, 4, 1, R, 2>(pl) : take<HD, __nv_bfloat16, 2, 4, 1, R, 2>(pl);
+  else if (HD == 128 || cols <= 24) take<HD, __nv_bfloat16, 3, 4, 1, 4, HD == 128 ? 1 : 2>(pl);
+  else if constexpr (HD == 64) take<HD, __nv_bfloat16, 4, 4, 1, 4, 2>(pl);
 }
 
 // The kernels take more shared memory than the default: asked for once per device.
@@ -645,7 +663,7 @@ int join_room(const Plan& pl, int head_dim, int n) {
 
 // How many clusters of n blocks run at once, asked for once per variant, size and device.
 int clusters_at_once(const Plan& pl, int head_dim, int n) {
-  static std::atomic<int> known[64][16][5];  // 1 + the number
+  static std::atomic<int> known[64][20][5];  // 1 + the number
   int dev = 0, log = 0, count = 0;
   while (1 << log < n) ++log;
   if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) count = known[dev][pl.id][log].load();
@@ -680,21 +698,23 @@ size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, bool mass, Plan* pl) {
   const long long cols = (long long)c.rows * (n_heads / c.n_kv_heads);
   if (cols > INT_MAX / 64) return false;
-  if (head_dim == 64) take_for<64>(pl, (int)cols, dtype);
-  else take_for<128>(pl, (int)cols, dtype);
+  const int sms = device_sms();
+  const long long steps = (cols + 127) / 128 * c.n_seqs * c.n_kv_heads * c.max_pages / sms;
+  if (head_dim == 64) take_for<64>(pl, (int)cols, dtype, steps);
+  else take_for<128>(pl, (int)cols, dtype, steps);
   const long long ct = (cols + pl->CT - 1) / pl->CT, entries = ct * c.n_seqs, items = entries * c.n_kv_heads;
   const long long most = (long long)c.max_pages * (kPageTokens / pl->SP);  // steps of an item
   if (items > INT_MAX / 32 || (most + kOver) * c.n_kv_heads > INT_MAX) return false;
   pl->n_ctiles = (int)ct;
   pl->n_entries = (int)entries;
   pl->items = (int)items;
-  const int sms = device_sms();
   const long long room = std::min(pl->blocks * sms, kMaxBlocks);  // blocks that run at once
   pl->cluster = 0;
   pl->item_off = pl->part_off = pl->bytes = 0;
   int n = 1;
   while (n < 16 && 2 * n <= most && items <= clusters_at_once(*pl, head_dim, 2 * n)) n *= 2;
-  if (!pl->wide && (most + n - 1) / n <= kShort) {
+  const long long each = (most + n - 1) / n;  // steps of a cluster's block
+  if (!pl->wide && (each <= kShort || (each <= 2 * kShort && each <= items * most / room + kJoin))) {
     pl->cluster = n;
     pl->smem += join_room(*pl, head_dim, n);
     pl->grid = (int)(items * n);

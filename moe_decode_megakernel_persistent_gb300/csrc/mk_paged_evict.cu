@@ -16,6 +16,11 @@
 // (>= keep) and destinations (< keep) are apart, and nothing is read after it is written.  The
 // item's own blocks make them, from the lists of free slots and late positions in order; where there may be many, a second
 // kernel of all SMs does.
+//
+// Bounds.  16 sequences of 256 to 8448 positions cut to 2048 (4 kv heads of 128) read and write 30 MB of K and V each, with the
+// masses 9 us at the memory's rate, and take 30: 17 for the choice, a chain of three passes over shared memory with
+// barriers of the cluster between them (28 % of the issue slots), and 10 for the moves.  64 sequences at a budget of 4096 take 15,
+// nearly all of it the read of the masses and that chain.
 #include <algorithm>
 #include <climits>
 #include <string>

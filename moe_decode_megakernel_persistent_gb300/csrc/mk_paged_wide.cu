@@ -18,6 +18,13 @@
 // columns see are searched for values that are no finite numbers; those are set to 0 too, and at the
 // end given to the columns that see them.
 //
+// Bounds.  1024 rows of 16 heads over 8022 positions (4 kv heads of 128) are 33 us of products at the measured
+// rate; this kernel takes 60 and the join 11 (70 for the call).  Neither bytes (4 % of the memory's) nor the
+// tensor cores (39 % active) bound it: a step of two tiles and 128 positions takes about 4,000 cycles, of which
+// the products are 2,048; the columns' reads from TMEM, maxima, exponentials (32 a cycle and SM: 1,024) and writes do
+// not hide wholly behind the other tile's products.  fp32 rows (6 sequences, up to 100 rows) do the products of three parts, 26 us,
+// in 56 + 12.
+//
 // One warp decides the block's runs and hands them to the others with the lengths it saw, so that all
 // agree should someone write the lengths while the call runs.
 #include <algorithm>
@@ -48,7 +55,8 @@ struct PWide {
   static constexpr int TM = TB == 2 ? 256 : 512;    // of a tile
   // The products cut off what they add, about 2^-24 of the sum each time and always towards 0: after so many steps the
   // sums of fp32 rows are added, rounded, to others that the columns hold (even: the same group's step begins new
-  // sums throughout a run).  Of 16000 positions 4 steps are 1.8e-6 off and 3 us of 80 slower, 16 steps 6e-6 off and 3 us faster.
+  // sums throughout a run).  Of 16000 positions 8 steps are 3.3e-6 off, 4 steps 1.8e-6 and 3 us of 77 slower, 16 steps 6e-6 and
+  // 3 us faster.
   static constexpr int FLUSH = F32 ? 8 : 0;
   static constexpr int CW = 4 * TB * GR;            // warps of the columns: eight
   static constexpr int THREADS = 32 * (CW + 2);
@@ -730,9 +738,14 @@ const void* paged_wide_join(int head_dim, int dtype) {
                         : reinterpret_cast<const void*>(&k_wide_join<128, __nv_bfloat16>);
 }
 
-WideKernel paged_wide_kernel(int head_dim, int dtype, int cols) {
+WideKernel paged_wide_kernel(int head_dim, int dtype, int cols, long long steps) {
   if (dtype == MK_F32) return head_dim == 64 ? info<64, float, 1>() : info<128, float, 1>();
-  if (cols <= 128) return head_dim == 64 ? info<64, __nv_bfloat16, 1>() : info<128, __nv_bfloat16, 1>();
+  // Two tiles a block read K and V half as often and leave the products less idle, one tile runs in finer shares (rows of 4
+  // columns, 4 heads of 128; one and two tiles: one sequence of 8022 positions, 64 rows 24.7 and 34.1 us, 512 44.1 and 47.0, 1024 71.2
+  // and 70.1; two of 20000, 1024 rows 285 and 258; 32 of 8022, 40 rows 185 and 152, 64 rows 189 and 139).  An odd tile leaves a half
+  // of its block idle: no more than one of nine.
+  const int tiles = (cols - 1) / 128 + 1;
+  if (steps <= 40 || (tiles < 8 && tiles % 2)) return head_dim == 64 ? info<64, __nv_bfloat16, 1>() : info<128, __nv_bfloat16, 1>();
   return head_dim == 64 ? info<64, __nv_bfloat16, 2>() : info<128, __nv_bfloat16, 2>();
 }
 

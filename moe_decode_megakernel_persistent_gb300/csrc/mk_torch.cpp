@@ -410,6 +410,7 @@ PyObject* py_paged_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ints(a[6], "new_lengths", c.n_seqs, dev);
     lengths = tensor(a[6], "new_lengths");
     if (lengths.data_ptr() != len.data_ptr() && overlap(lengths, len)) refuse("new_lengths must be lengths or not overlap them");
+    if (overlap(lengths, tensor(a[1], "table"))) refuse("new_lengths must not overlap table");
   }
   const int64_t sizes[3] = {c.n_seqs, c.n_kv_heads, keep};
   kept = fresh(sizes, at::kInt, dev);

@@ -83,7 +83,8 @@ def evict(pool, table, lengths, mass, keep: int, recent: int = 0, new_lengths=No
     sequence the last `recent` ones and the heaviest others, ties to the lower
     position.  Kept positions below `keep` stay in their slots; the others' K and V
     move, in order, into the free slots below `keep`.  The pages of the first `keep`
-    positions are written: no other sequence may share them.
+    positions are written: no other sequence may share them, nor may the table name
+    them twice.  Tables of at most 6144 pages.
 
     Returns (kept, new_lengths, new_mass): int32 [n_seqs, n_kv_heads, keep], the
     position that each slot now holds (-1 behind the end of a shorter sequence);

@@ -183,7 +183,7 @@ def test_maxima_that_move_at_every_step(gpu_lib, rising, rows):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
-@pytest.mark.parametrize("rows", [3, 12, 100, 300])
+@pytest.mark.parametrize("rows", [3, 6, 12, 100, 300])
 def test_what_a_row_does_not_see_never_shows(gpu_lib, dtype, bad, rows):
     """Values that are no numbers in the K of one of the call's own positions and the V of another:
     rows before them are whole, rows behind them are as the formula has them."""
@@ -313,7 +313,7 @@ def test_strides_out_streams_and_refusals(gpu_lib):
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(again, want)
     q, m = randn((2, 1, H, hd), 1, BF), masses(table, G)
-    ln = i32(lengths)
+    ln, ones = i32(lengths), table[:, :1].contiguous()
     bad = [
         lambda: paged.attention(q.half(), pool, table, ln), lambda: paged.attention(q, pool.half(), table, ln),
         lambda: paged.attention(q, pool[:, :1], table, ln), lambda: paged.attention(q, pool, table.long(), ln),
@@ -332,6 +332,8 @@ def test_strides_out_streams_and_refusals(gpu_lib):
         lambda: paged.evict(pool, table, ln, m, 5, recent=-1), lambda: paged.evict(pool, table, ln, m[:1], 5),
         lambda: paged.evict(pool, table, ln, m, 5, new_mass=m[:, :, :128]), lambda: paged.evict(pool, table, ln, m, 5, new_lengths=ln[:1]),
         lambda: paged.evict(pool, table, ln, m, 2 ** 40),
+        lambda: paged.evict(pool, ones, ln, m[..., :128].contiguous(), 5, new_lengths=ones.view(-1)),
+        lambda: paged.evict(pool, table, ln, m, 5, new_lengths=ln[:1].expand(2)),
     ]
     for f in bad:
         with pytest.raises((ValueError, L.MKError)):
@@ -367,7 +369,7 @@ def test_same_bits_each_time(gpu_lib):
         assert all(torch.equal(a, b) for g in got[1:] for a, b in zip(got[0], g))
 
 
-@pytest.mark.parametrize("dtype,rows,hd", [(F32, 10, 128), (BF, 10, 128), (F32, 9, 64), (BF, 33, 64), (BF, 60, 128)])
+@pytest.mark.parametrize("dtype,rows,hd", [(F32, 10, 128), (BF, 10, 128), (F32, 9, 64), (BF, 33, 64), (BF, 60, 128), (BF, 6, 128), (BF, 5, 64), (BF, 8, 64)])
 def test_blocks_of_several_runs(gpu_lib, dtype, rows, hd):
     """Blocks whose runs follow one another (a run's sums leave through the place of the next one's queries), many times."""
     lengths = [(701 * i) % 3000 + 200 for i in range(60)]
@@ -393,6 +395,37 @@ def test_long_sums_of_fp32_rows(gpu_lib, hd, rows):
         k, v = R.rows_of(pool, table, i, n)
         want, wl, w, A, D = R.attend(q[i], k, v, n - rows, 1 / math.sqrt(hd))
         assert float((out[i].double() - want).norm() / want.norm()) < 192 * 2.0 ** -23
+
+
+@pytest.mark.parametrize("dtype,hd,rows", [(BF, 128, 5), (BF, 128, 6), (BF, 64, 6), (BF, 64, 8), (F32, 128, 4), (F32, 64, 4)])
+@pytest.mark.parametrize("lengths", [[8], [300, 0, 131], [9000], [2500, 700] * 16, [900] * 70])
+def test_the_most_columns_of_each_variant(gpu_lib, dtype, hd, rows, lengths):
+    """Few columns, as many as a variant takes and a row less: clusters of all sizes, equal runs, rows that see nothing."""
+    pool, table = make(lengths, 4, hd, seed=27)
+    q = randn((len(lengths), rows, 16, hd), 28, dtype, 1.5)
+    check(q, pool, table, lengths, n_new=[(5 * i) % (rows + 1) if i else rows for i in range(len(lengths))], mass=masses(table, 4), decay=0.7)
+
+
+@pytest.mark.parametrize("case", [
+    *[lambda lib, h=h, c=c: test_several_rows(lib, *h, BF, *c) for h in ((16, 4, 128), (10, 2, 128), (3, 1, 64))
+      for c in (([1000], 100, None), ([900, 40, 300], 130, [130, 130, 1]), ([1300], 257, None), ([70], 70, None), ([140, 700], 33, [33, 17]))],
+    lambda lib: test_many_sequences(lib, BF, 300), lambda lib: test_long_contexts(lib, BF, 1024, 8022),
+    *[lambda lib, s=s: test_scales_and_peaked_scores(lib, BF, 200, *s) for s in ((4.0, 1.0), (-0.3, 1.0), (0.0, 1.0), (0.1, 30.0))],
+    *[lambda lib, r=r: test_maxima_that_move_at_every_step(lib, r, 200) for r in (True, False)],
+    *[lambda lib, b=b: test_what_a_row_does_not_see_never_shows(lib, BF, b, 300) for b in (math.nan, math.inf, -math.inf)],
+    lambda lib: test_rows_that_see_nothing(lib, BF, 200), lambda lib: test_keys_of_minus_infinity_and_lowest_values(lib, BF, 200),
+    lambda lib: test_bad_lengths_and_pages_are_reported_and_left_out(lib), lambda lib: test_same_bits_each_time(lib),
+    lambda lib: test_blocks_of_several_runs(lib, BF, 60, 128)])
+def test_wide_tables(gpu_lib, monkeypatch, case):
+    """The width of a table, not the lengths in it, is what a call's work is judged by: wide ones take two tiles of columns a block."""
+    plain, sms = R.table_for, torch.cuda.get_device_properties(0).multi_processor_count
+
+    def wide(lengths, spare=2, seed=0, width=None, device="cuda"):
+        need = max(-(-n // R.PAGE) for n in lengths)
+        return plain(lengths, spare, seed, max(need, width or 0, min(6144, 42 * sms // max(1, len(lengths)))), device)
+
+    monkeypatch.setattr(R, "table_for", wide)
+    case(gpu_lib)
 
 
 def test_kernels_behind_one_another_see_new_lengths(gpu_lib):
@@ -558,6 +591,17 @@ def test_evictions_of_all_widths(gpu_lib, seqs, n):
     mass = masses(table, 2)
     check_evict(pool, table, lengths, mass, max(1, n // 3), n // 50)
     check_evict(pool, table, lengths, mass, n - 60, 0, in_place=True)
+
+
+def test_evictions_of_the_largest_table(gpu_lib):
+    n = 6144 * 128                                    # more are refused (also by the C call)
+    pool, table = paged.new_pool(6144, 1, 64), torch.arange(6143, -1, -1, dtype=torch.int32, device="cuda")[None]
+    pool.copy_(randn((6144, 1, 1, 128, 1), 31, BF).expand_as(pool))
+    for length in (n, n - 5, 700):
+        check_evict(pool, table, [length], masses(table, 1), 5000, 100)
+    wider = torch.zeros((1, 6145), dtype=torch.int32, device="cuda")
+    with pytest.raises(L.MKError):
+        paged.evict(pool, wider, i32([5]), masses(wider, 1), 4)
 
 
 def test_evictions_of_special_masses(gpu_lib):
