@@ -22,8 +22,8 @@
 // rate; this kernel takes 60 and the join 11 (70 for the call).  Neither bytes (4 % of the memory's) nor the
 // tensor cores (39 % active) bound it: a step of two tiles and 128 positions takes about 4,000 cycles, of which
 // the products are 2,048; the columns' reads from TMEM, maxima, exponentials (32 a cycle and SM: 1,024) and writes do
-// not hide wholly behind the other tile's products.  fp32 rows (6 sequences, up to 100 rows) do the products of three parts, 26 us,
-// in 56 + 12.
+// not hide wholly behind the other tile's products.  fp32 rows (three sequences of up to 2049 positions, 641 rows) do the products of
+// three parts, 26 us, in 77 + 12, of which handing the sums over every second step is 15.
 //
 // One warp decides the block's runs and hands them to the others with the lengths it saw, so that all
 // agree should someone write the lengths while the call runs.
@@ -55,9 +55,9 @@ struct PWide {
   static constexpr int TM = TB == 2 ? 256 : 512;    // of a tile
   // The products cut off what they add, about 2^-24 of the sum each time and always towards 0: after so many steps the
   // sums of fp32 rows are added, rounded, to others that the columns hold (even: the same group's step begins new
-  // sums throughout a run).  Of 16000 positions 8 steps are 3.3e-6 off, 4 steps 1.8e-6 and 3 us of 77 slower, 16 steps 6e-6 and
-  // 3 us faster.
-  static constexpr int FLUSH = F32 ? 8 : 0;
+  // sums throughout a run).  Three sequences of 700 to 2049 positions, 641 rows: 2 steps are 8.2e-7 off (the same sums by fp32
+  // products 7.9e-7) in 90 us, 4 steps 1.3e-6 in 79, 8 steps 1.9e-6 in 74.
+  static constexpr int FLUSH = F32 ? 2 : 0;
   static constexpr int CW = 4 * TB * GR;            // warps of the columns: eight
   static constexpr int THREADS = 32 * (CW + 2);
 };

@@ -385,8 +385,8 @@ def test_blocks_of_several_runs(gpu_lib, dtype, rows, hd):
 @pytest.mark.parametrize("hd,rows", [(128, 40), (64, 40), (128, 1)])
 def test_long_sums_of_fp32_rows(gpu_lib, hd, rows):
     """One kv head, 30000 positions: runs of many steps.  The products cut off up to 2^-23 of the sum with each of the
-    24 that a step of 128 positions has, of which 8 steps go into one sum: 192 2^-23 at most, next to the rounded sums of all
-    steps and the weights' own error (tests/_paged.py), as norms."""
+    24 that a step of 128 positions has, of which 2 steps go into one sum: 48 2^-23 at most, and each of the 118 sums that
+    are then added is rounded by 2^-24 of theirs at most, as norms."""
     n = 30000
     pool, table = make([n] * 6, 1, hd, seed=22)
     q = randn((6, rows, 4, hd), 23, F32, 1.5)
@@ -394,7 +394,7 @@ def test_long_sums_of_fp32_rows(gpu_lib, hd, rows):
     for i in range(6):
         k, v = R.rows_of(pool, table, i, n)
         want, wl, w, A, D = R.attend(q[i], k, v, n - rows, 1 / math.sqrt(hd))
-        assert float((out[i].double() - want).norm() / want.norm()) < 192 * 2.0 ** -23
+        assert float((out[i].double() - want).norm() / want.norm()) < (48 + 59) * 2.0 ** -23
 
 
 @pytest.mark.parametrize("dtype,hd,rows", [(BF, 128, 5), (BF, 128, 6), (BF, 64, 6), (BF, 64, 8), (F32, 128, 4), (F32, 64, 4)])
