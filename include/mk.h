@@ -568,7 +568,8 @@ MK_API int mk_paged_attention(const mk_paged_cache* c, int32_t n_heads, const mk
                               void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace that mk_paged_attention needs for calls of this shape (any lengths),
- * with masses or without.  0 for a description that it refuses, or that needs none. */
+ * with masses or without (with masses and few rows, 4 bytes for each row, query head and position
+ * of the tables: 16 heads, one row and 64 tables of 128 pages 67 MB).  0 for a description that it refuses, or that needs none. */
 MK_API size_t mk_paged_attention_bytes(const mk_paged_cache* c, int32_t n_heads, int32_t dtype, int32_t with_mass);
 
 /* Leave at most `keep` positions of each (sequence, kv head): of a sequence of more, the

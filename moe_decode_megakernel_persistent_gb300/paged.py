@@ -74,7 +74,9 @@ def attention(q, pool, table, lengths, n_new=None, scale=None, out=None, return_
     what each position has received.  For every sequence with a new row the
     masses of its earlier positions are multiplied by decay, those of its new
     positions start from 0, and each gets the sum of the weights that the rows and
-    the query heads of its kv head give it."""
+    the query heads of its kv head give it.  Calls of few rows (at most 32 rows x
+    query heads of a kv head) keep their scores meanwhile: 4 bytes for each row, query
+    head and position of the tables."""
     return L.torch_module().paged_attention(q, pool, table, lengths, n_new, scale, out, bool(return_lse), mass, decay, status)
 
 
