@@ -554,8 +554,8 @@ typedef struct mk_paged_mass {
  * one of +infinity or NaN makes the row NaN, and an infinite or NaN V reaches its own dimension
  * whatever its weight.  out must not overlap q, the pool, the masses or
  * the workspace.  |scale| < 1e18; a score below -6.9e29 has no weight.  Scores, maxima and sums are
- * fp32; the weights are rounded to bfloat16 (2^-8) for bf16 rows; an fp32 q and its weights are
- * three bfloat16 parts (2^-24), and each result is off by a few 10^-6 of its values' size at most.
+ * fp32; the weights of bf16 rows are two bfloat16 parts (2^-16); an fp32 q and its weights are
+ * three (2^-24), and each such result is off by a few 10^-6 of its values' size at most.
  * mass (may be NULL): for every sequence with a new row, and p < lengths[i],
  *     mass[i][g][p] = (p < lengths[i] - n_new[i] ? decay * mass[i][g][p] : 0)
  *                   + the sum of the weights that the rows and the heads of kv head g give p,

@@ -2,11 +2,12 @@
 // drafts) on the 5th-generation tensor cores (tcgen05).
 //
 //   S = Q K^T   128 columns x the 128 positions of a page, fp32 in TMEM
-//   O += P V    P = 2^(c S - m) in bf16 over S's place in TMEM, V by positions
+//   O += P V    P = 2^(c S - m) in bf16 parts over S's place in TMEM, V by positions
 //
 // K and V are operands as the tensor copies bring them.  A thread has a column (a TMEM lane):
 // its maximum is its own and moves only when a score passes it by 2^8; then it rescales its
-// sums, which the next product waits for.  An fp32 q is three bf16 parts, and so are its weights.
+// sums, which the next product waits for.  An fp32 q is three bf16 parts, and so are its weights; a bf16 one's
+// are two (one part, 2^-8, took 11 us less of the 81.5 below, and left an error of 0.0026 of the outputs' size for 0.0017).
 //
 // Warps 4 TB: the columns.  One warp more looks up pages and issues the copies, another the
 // products.  With two tiles a block (TB = 2) the tensor cores work on one tile while the
@@ -18,10 +19,10 @@
 // columns see are searched for values that are no finite numbers; those are set to 0 too, and at the
 // end given to the columns that see them.
 //
-// Bounds.  1024 rows of 16 heads over 8022 positions (4 kv heads of 128) are 33 us of products at the measured
-// rate; this kernel takes 60 and the join 11 (70 for the call).  Neither bytes (4 % of the memory's) nor the
-// tensor cores (39 % active) bound it: a step of two tiles and 128 positions takes about 4,000 cycles, of which
-// the products are 2,048; the columns' reads from TMEM, maxima, exponentials (32 a cycle and SM: 1,024) and writes do
+// Bounds.  1024 rows of 16 heads over 8022 positions (4 kv heads of 128) are 49 us of products at the measured
+// rate (33 with weights of one part); this kernel takes 71 and the join 11 (81.5 for the call).  Bytes (4 % of the memory's) do
+// not bound it: a step of two tiles and 128 positions takes about 4,700 cycles, of which
+// the products are 3,072; the columns' reads from TMEM, maxima, exponentials (32 a cycle and SM: 1,024) and writes do
 // not hide wholly behind the other tile's products.  fp32 rows (three sequences of up to 2049 positions, 641 rows) do the products of
 // three parts, 26 us, in 77 + 12, of which handing the sums over every second step is 15.
 //
@@ -39,7 +40,8 @@ template <int HD, class T, int TB>
 struct PWide {
   static constexpr bool F32 = std::is_same<T, float>::value;
   static constexpr int NG = HD / 64, CT = 128 * TB, SP = kPageTokens;
-  static constexpr int P = F32 ? 3 : 1;             // bf16 parts of q, and of the weights
+  static constexpr int P = F32 ? 3 : 1;             // bf16 parts of q
+  static constexpr int WP = F32 ? 3 : 2;            // and of the weights
   static constexpr int NS = TB == 1 ? 2 : 1;        // places of scores of a tile
   static constexpr int GR = NS;                     // groups of four warps of a tile, which take the steps in turn
   static constexpr int QT = NG * 128 * 128;         // bytes of a tile's q of one part
@@ -285,10 +287,10 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
             if (ok && elect_one()) {
               const uint32_t base = tmu + W::TM * t;
 #pragma unroll
-              for (int x = W::P - 1; x >= 0; --x) {  // the weights' low parts first
+              for (int x = W::WP - 1; x >= 0; --x) {  // the weights' low parts first
 #pragma unroll
                 for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                  mma_ts(base + W::SUMS, x < 2 ? base + 128 * pu + 32 * (kk / 2) + 16 * x + 8 * (kk % 2) : base + W::THIRD + 64 * pu + 8 * kk, vd + ((kk * 16 * 128) >> 4), id_pv, kk || x < W::P - 1 ? 1 : add);
+                  mma_ts(base + W::SUMS, x < 2 ? base + 128 * pu + 32 * (kk / 2) + 16 * x + 8 * (kk % 2) : base + W::THIRD + 64 * pu + 8 * kk, vd + ((kk * 16 * 128) >> 4), id_pv, kk || x < W::WP - 1 ? 1 : add);
               }
               if (h) {
                 if (t == TB - 1) commit(smem_addr(&kv_empty[v]));
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
             uint64_t la[2] = {0, 0};
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              uint32_t b[W::P][16];
+              uint32_t b[W::WP][16];
               read(c, s);
               const int v = vis - 32 * c;
 #pragma unroll
@@ -497,15 +499,15 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
                 if (CUT && x + 1 >= v) z.y = 0.f;
                 la[x / 2 & 1] = add2(la[x / 2 & 1], pair(z.x, z.y));
 #pragma unroll
-                for (int i = 0; i < W::P; ++i) {
+                for (int i = 0; i < W::WP; ++i) {
                   b[i][x / 2] = pack2(z.x, z.y);
-                  if (i + 1 < W::P) z.x -= low_f(b[i][x / 2]), z.y -= high_f(b[i][x / 2]);
+                  if (i + 1 < W::WP) z.x -= low_f(b[i][x / 2]), z.y -= high_f(b[i][x / 2]);
                 }
               }
               // over these scores, which are in registers; the third part has a place of its own
               tm_store16(at + 32 * c, b[0]);
-              if constexpr (W::P == 3) {
-                tm_store16(at + 32 * c + 16, b[1]);
+              tm_store16(at + 32 * c + 16, b[1]);
+              if constexpr (W::WP == 3) {
                 tm_store16(tm_s + W::THIRD + 64 * (kk % NS) + 16 * c, b[2]);
               }
               if (c == 1) given(0);

@@ -1,0 +1,43 @@
+"""What the operators on the 16-bit paged cache make of values: the bits of bf16 rows' weights."""
+import math
+
+import pytest
+import torch
+
+from moe_decode_megakernel_persistent_gb300 import paged
+from tests import _paged as R
+from tests.test_gpu_paged import BF, i32, make, randn
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- weights of bf16 rows
+
+@pytest.mark.parametrize("hd,rows,seqs,width", [
+    (128, 1, 1, None), (128, 4, 1, None), (128, 6, 1, None), (64, 8, 1, None), (64, 1, 1, None),   # clusters, 4 to 32 columns
+    (128, 1, 700, None), (64, 7, 300, None),                                                      # equal runs
+    (128, 40, 1, None), (64, 60, 3, None),                                                        # one tile of 128 columns a block
+    (128, 60, 1, 2000), (64, 64, 2, 2000)])                                                       # two
+def test_weights_of_bf16_rows_have_16_bits(gpu_lib, hd, rows, seqs, width):
+    """Values of V are +-1, whose sums nearly cancel, so that an output's own rounding is small next to what a
+    weight of 8 bits would be off by (2^-9 / sqrt(3 n) of the weights' sum, 1, as a norm: 1e-4 at n = 100).  A score is
+    one product, exact, then scaled and taken from the maximum with an error of a few 2^-24 of magnitudes up to 2:
+    with the exponential's 2^-22 a weight is off by 2^-20, which enters twice.  Each of the 2 n terms of the sums
+    of two parts is cut off by 2^-23 of the sum at most, each of the n terms below by 2^-24; two parts of a weight leave 2^-16."""
+    n = max(100, rows + 20)
+    G, H = 2, 8
+    pool, table = make([n] * seqs, G, hd, seed=30, width=width)
+    ones = torch.where(randn((2, n, G, hd), 31) < 0, -1.0, 1.0)
+    k = torch.zeros((n, G, hd), device="cuda")
+    k[..., 0] = randn((n, G), 32).clamp(-2, 2)
+    for i in range(seqs):
+        R.put(pool, table, i, 0, k, ones[i % 2])
+    q = torch.zeros((seqs, rows, H, hd), dtype=BF, device="cuda")
+    q[..., 0] = (1 + torch.rand((seqs, rows, H), device="cuda", generator=torch.Generator(device="cuda").manual_seed(33)))
+    out = paged.attention(q, pool, table, i32([n] * seqs), scale=0.5)
+    inner = 2 * 2.0 ** -20 + 2 * n * 2.0 ** -23 + n * 2.0 ** -24 + 2.0 ** -16
+    for i in sorted({0, 1, seqs // 2, seqs - 1} & set(range(seqs))):
+        want, _, _, A, _ = R.attend(q[i], *R.rows_of(pool, table, i, n), n - rows, 0.5)
+        assert bool(((A - 1).abs() < 1e-12).all())
+        err = (out[i].double() - want).abs()
+        assert bool((err <= inner + (want.abs() + inner) * 2.0 ** -8).all()), (i, float((err / (inner + want.abs() * 2.0 ** -8)).max()))
