@@ -334,10 +334,9 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
           const int x = 32 * i + lane, col = (r.c0 + t) * N + x, row = row_of(p, col);
           const int lim = col < p.cols && row < r.nn ? max(0, r.len - r.nn + row + 1) : 0;
           float l = -INFINITY;
-          if (lim) {
-            l = now[i] == -INFINITY ? now[i] : now[i] * -kLog2e;  // (its scores have no weight)
-            some = some || lim < min(r.len, (r.span + 1) * kSpan);
-          }
+          if (lim) l = now[i] == -INFINITY ? now[i] : now[i] * -kLog2e;  // (its scores have no weight)
+          // (a column that is none counts: its row of zeros times an infinite K is NaN)
+          some = some || lim < min(r.len, (r.span + 1) * kSpan);
           less[ls][x] = l;
           lims[ls][x] = lim;
         }

@@ -1,4 +1,5 @@
-"""What the operators on the 16-bit paged cache make of values: the bits of bf16 rows' weights."""
+"""What the operators on the 16-bit paged cache make of values: the bits of bf16 rows' weights,
+infinite keys."""
 import math
 
 import pytest
@@ -6,7 +7,7 @@ import torch
 
 from moe_decode_megakernel_persistent_gb300 import paged
 from tests import _paged as R
-from tests.test_gpu_paged import BF, i32, make, randn
+from tests.test_gpu_paged import BF, F32, check, i32, make, masses, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +42,35 @@ def test_weights_of_bf16_rows_have_16_bits(gpu_lib, hd, rows, seqs, width):
         assert bool(((A - 1).abs() < 1e-12).all())
         err = (out[i].double() - want).abs()
         assert bool((err <= inner + (want.abs() + inner) * 2.0 ** -8).all()), (i, float((err / (inner + want.abs() * 2.0 ** -8)).max()))
+
+
+# ---------------------------------------------------------------- infinities
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows,n_new", [(1, None), (9, None), (40, None), (150, None), (150, [131]), (257, [256])])
+def test_masses_of_keys_of_minus_infinity(gpu_lib, dtype, hd, rows, n_new):
+    """Positions whose scores are all -infinity receive nothing, next to columns that are none (a tile's padding,
+    rows behind n_new), whose queries are taken as 0: 0 times infinity is NaN."""
+    n = 600
+    pool, table = make([n], 1, hd, seed=34)
+    k = torch.zeros((n, 1, hd), device="cuda")
+    k[:, :, 0] = randn((n, 1), 4)
+    gone = torch.zeros(n, dtype=torch.bool, device="cuda")
+    gone[5:90] = gone[250:260] = gone[300:310] = True
+    k[gone, :, 0] = -math.inf
+    R.put(pool, table, 0, 0, k, randn((n, 1, hd), 5))
+    q = torch.zeros((1, rows, 2, hd), dtype=dtype, device="cuda")
+    q[..., 0] = 1 + randn((1, rows, 2), 6).abs()
+    m = masses(table, 1)
+    _, _, got = check(q, pool, table, [n], n_new=n_new, scale=1.0, left_out=[gone], mass=m, decay=0.5)
+    old = gone & (torch.arange(n, device="cuda") < n - (rows if n_new is None else n_new[0]))
+    assert torch.equal(got[0, 0, :n][old], 0.5 * m[0, 0, :n][old])
+    k[:, :, 0] = -math.inf                     # no score has a weight: old masses fade, new positions have none
+    R.put(pool, table, 0, 0, k, randn((n, 1, hd), 5))
+    got = m.clone()
+    out, lse = paged.attention(q, pool, table, i32([n]), n_new=None if n_new is None else i32(n_new), scale=1.0, return_lse=True, mass=got, decay=0.5)
+    assert not out.any() and bool((lse == -math.inf).all())
+    first = n - (rows if n_new is None else n_new[0])
+    assert torch.equal(got[0, 0, :first], 0.5 * m[0, 0, :first]) and not got[0, 0, first:n].any()
+    assert torch.equal(got[0, 0, n:], m[0, 0, n:])
