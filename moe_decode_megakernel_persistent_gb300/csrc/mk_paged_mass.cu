@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(MassShape<HD, T>::THREADS, 1)
           lims[ls][x] = lim;
         }
         some = __any_sync(0xffffffffu, some);
+        __syncwarp();  // (a vote does not order memory: lane 0 arrives for what all lanes have stored)
         if (lane == 0) {
           cut[ls] = some;
           arrive(smem_addr(&l_full[ls]));
