@@ -88,6 +88,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// A part's sum of values, taken to the joined maximum.  A factor of 0 leaves infinities and NaN, which reach their
+// dimension whatever their weight.
+__device__ __forceinline__ float taken(float x, float f) { return f == 0.f && !(fabsf(x) <= 3.402823466e38f) ? x : x * f; }
 constexpr uint32_t kNib = 0x80708070u;
 
 // The row of a query column.

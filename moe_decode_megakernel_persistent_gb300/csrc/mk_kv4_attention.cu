@@ -801,13 +801,13 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
       m = M;
       l *= f0;
 #pragma unroll
-      for (int x = 0; x < V; ++x) o[x] *= f0;
+      for (int x = 0; x < V; ++x) o[x] = taken(o[x], f0);
 #pragma unroll
       for (int y = 0; y < NB; ++y) {
         const float f1 = exp2_fast(ml[y].x - M);
         l += ml[y].y * f1;
 #pragma unroll
-        for (int x = 0; x < V; ++x) o[x] += v[y][x] * f1;
+        for (int x = 0; x < V; ++x) o[x] += taken(v[y][x], f1);
       }
     }
   };
@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
     for (int i = 0; i < NW; ++i) {
       const float f = exp2_fast(red_m[i] - M);
       ls += red_l[i] * f;
-      v += red[i][d] * f;
+      v += taken(red[i][d], f);
     }
     dst[d] = (T)(ls == 0.f ? 0.f : v / ls);
     if (p.lse && d == 0) put_lse(row, hd, M, ls);

@@ -549,21 +549,22 @@ __global__ void __launch_bounds__(32 * W, B) k_paged_attention(const __grid_cons
       return;
     }
     const int slots = (CT + p.cluster - 1) >> p.cluster_log;
-    if (n_steps == 0)  // nothing to add: a sum of 0 stands for it
+    if (n_steps == 0)  // nothing to add: a sum below 0 stands for it
       for (int c = tid; c < ncol; c += NTHR)
-        put_peer(fin + (rank * slots + (c >> p.cluster_log)) * S::RS + HD, c & (p.cluster - 1), make_float2(kLow, 0.f));
+        put_peer(fin + (rank * slots + (c >> p.cluster_log)) * S::RS + HD, c & (p.cluster - 1), make_float2(kLow, -1.f));
     cluster_sync();
     for (int x = tid; x < slots * (HD / 2); x += NTHR) {
       const int sl = x / (HD / 2), d = x % (HD / 2) * 2, c = (sl << p.cluster_log) + rank;
       if (c >= ncol) break;  // (a warp's elements are of one column)
       // lane r takes block r's maximum and sum, every lane all blocks' values
       const float* from = fin + sl * S::RS;
-      float2 ml = make_float2(kLow, 0.f);
+      float2 ml = make_float2(kLow, -1.f);
       if ((lane & 15) < p.cluster) ml = *reinterpret_cast<const float2*>(from + (lane & 15) * slots * S::RS + HD);
       float M = ml.x;
 #pragma unroll
       for (int o2 = 8; o2 > 0; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o2));
-      const uint32_t some = __ballot_sync(0xffffffffu, ml.x != kLow || ml.y != 0.f);  // others have stored no values
+      const uint32_t some = __ballot_sync(0xffffffffu, !(ml.y < 0.f));  // others have stored no values
+      if (ml.y < 0.f) ml.y = 0.f;
       const float f = exp2_fast(ml.x - M);
       float l_sum = ml.y * f;
 #pragma unroll
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(32 * W, B) k_paged_attention(const __grid_cons
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const float fr = __shfl_sync(0xffffffffu, f, r);
-        if (some >> r & 1u) v.x += y[r].x * fr, v.y += y[r].y * fr;
+        if (some >> r & 1u) v.x += taken(y[r].x, fr), v.y += taken(y[r].y, fr);
       }
       put_out(seq, j * CT + c, head, d, M, l_sum, v);
     }

@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
       int page = rs.t0 + skip < rs.t1 ? pages[rs.t0 + skip] : -1;
       float m = kLow, l = 0.f;  // running maximum (log2) that l is relative to, and the sum of the weights
       // sums of earlier steps of this thread's half of the dimensions (in local memory), and the maximum they are relative to
-      [[maybe_unused]] float held[W::FLUSH ? HD / 2 : 1], m_held = kLow;
+      [[maybe_unused]] float held[W::FLUSH ? HD / 2 : 1], m_held = -INFINITY;  // (none yet)
       // the sums so far, relative to the maximum `now`, to those held
       [[maybe_unused]] auto flush = [&](float now) {
         wait_for(smem_addr(&sums_done), n_flush++ & 1, &give_up, p.a.status);
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
         if (lane == 0) arrive(smem_addr(&flushed));
         const float f = exp2_fast(m_held - now);
 #pragma unroll
-        for (int c = 0; c < HD / 2; ++c) held[c] = m_held == kLow ? o[c] : fmaf(held[c], f, o[c]);
+        for (int c = 0; c < HD / 2; ++c) held[c] = m_held == -INFINITY ? o[c] : fmaf(held[c], f, o[c]);
         m_held = now;
       };
       for (int t = rs.t0 + skip;; t += GR) {
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
             if constexpr (CH == 32) tm_read32(tm_o + c, o);
             else tm_read16(tm_o + c, o);
             if constexpr (W::FLUSH > 0)
-              if (m_held != kLow) {
+              if (m_held != -INFINITY) {
                 const float g = exp2_fast(m_held - m);
                 for (int x = 0; x < CH; ++x) o[x] = fmaf(held[c - group * (HD / 2) + x], g, o[x]);
               }
@@ -574,7 +574,8 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
               }
             }
 #pragma unroll
-            for (int x = 0; x < CH; ++x) o[x] = !ok ? NAN : l == 0.f ? 0.f : o[x] * f;
+            for (int x = 0; x < CH; ++x)  // (a part of a column's positions without a weight: infinities and NaN are the join's)
+              o[x] = !ok ? NAN : l != 0.f ? o[x] * f : whole || !lim || is_finite(o[x]) ? 0.f : o[x];
             if constexpr (F) {
 #pragma unroll
               for (int x = 0; x < CH; x += 4)
@@ -692,13 +693,13 @@ __global__ void __launch_bounds__(256) k_wide_join(const __grid_constant__ AttAr
         m[c] = M;
         l[c] *= f0;
 #pragma unroll
-        for (int x = 0; x < V; ++x) o[c][x] *= f0;
+        for (int x = 0; x < V; ++x) o[c][x] = taken(o[c][x], f0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float f1 = exp2_fast(ml[i][c].x - M);
           l[c] += ml[i][c].y * f1;
 #pragma unroll
-          for (int x = 0; x < V; ++x) o[c][x] += v[i][c][x] * f1;
+          for (int x = 0; x < V; ++x) o[c][x] += taken(v[i][c][x], f1);
         }
       }
     }

@@ -1,5 +1,5 @@
 """What the operators on the 16-bit paged cache make of values: the bits of bf16 rows' weights,
-infinite keys."""
+infinite keys and values."""
 import math
 
 import pytest
@@ -74,3 +74,41 @@ def test_masses_of_keys_of_minus_infinity(gpu_lib, dtype, hd, rows, n_new):
     first = n - (rows if n_new is None else n_new[0])
     assert torch.equal(got[0, 0, :first], 0.5 * m[0, 0, :first]) and not got[0, 0, first:n].any()
     assert torch.equal(got[0, 0, n:], m[0, 0, n:])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("heavy_first", [False, True])
+@pytest.mark.parametrize("light", [0.0, -math.inf])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows,lengths", [(1, [2049]), (3, [700]), (1, [60000]), (1, [6000] * 40), (3, [30000, 900]), (40, [9000]), (100, [3000, 20000])])
+def test_infinite_values_of_hardly_any_weight(gpu_lib, dtype, light, heavy_first, hd, rows, lengths):
+    """An infinite V reaches its dimension however the work is cut, where its position's weight (2^-432 of the largest,
+    or none) and that of every position of its block are below all fp32."""
+    G, H = 2, 4
+    pool, table = make(lengths, G, hd, seed=35)
+    at = torch.arange(max(lengths), device="cuda")
+    bad = {3: math.inf, 4: -math.inf, 9: math.nan}
+    v = randn((max(lengths), G, hd), 36)
+    for i, n in enumerate(lengths):
+        k = torch.zeros((n, G, hd), device="cuda")
+        first = n - max(rows, 8)               # (what all rows see)
+        heavy = at[:n] < first // 2 if heavy_first else at[:n] >= first // 2
+        k[..., 0] = torch.where(heavy, 300.0, light)[:, None]
+        vi = v[:n].clone()
+        for j, (d, x) in enumerate(bad.items()):
+            vi[(first - 5 if heavy_first else 5) + j, :, d] = x
+        R.put(pool, table, i, 0, k, vi)
+    q = torch.zeros((len(lengths), rows, H, hd), dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    out = paged.attention(q, pool, table, i32(lengths), scale=1.0)
+    for d, x in bad.items():
+        assert bool((out[..., d].isnan() if math.isnan(x) else out[..., d] == x).all()), (d, out[..., d].flatten()[:8])
+    rest = [d for d in range(hd) if d not in bad]
+    assert bool(torch.isfinite(out[..., rest]).all())
+    for i, n in list(enumerate(lengths))[:2]:
+        k, vv = R.rows_of(pool, table, i, n)
+        gone = k[:, 0, 0] == -math.inf
+        want, wl, w, A, D = R.attend(q[i], k, torch.where(torch.isfinite(vv), vv, 0.0), n - rows, 1.0, gone)
+        inner, half, _ = R.bounds(A, D, wl, n, hd, dtype)
+        err = (out[i].double() - want).abs()[..., rest]
+        assert bool((err <= (inner + (want.abs() + inner) * half)[..., rest]).all())
