@@ -1,5 +1,5 @@
 """What the operators on the 16-bit paged cache make of values: the bits of bf16 rows' weights,
-infinite keys and values."""
+infinite keys, values and queries."""
 import math
 
 import pytest
@@ -112,3 +112,25 @@ def test_infinite_values_of_hardly_any_weight(gpu_lib, dtype, light, heavy_first
         inner, half, _ = R.bounds(A, D, wl, n, hd, dtype)
         err = (out[i].double() - want).abs()[..., rest]
         assert bool((err <= (inner + (want.abs() + inner) * half)[..., rest]).all())
+
+
+@pytest.mark.parametrize("rows", [1, 5, 150])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_an_infinite_query(gpu_lib, rows, sign):
+    """An fp32 q that is infinite, against keys whose sign makes every score -infinity (no weight) or, for one
+    position, +infinity (the rows that see it are NaN), as the products of whole fp32 numbers have it."""
+    n, hd = 400, 64
+    pool, table = make([n], 1, hd, seed=37)
+    k = torch.zeros((n, 1, hd), device="cuda")
+    k[:, :, 0] = -sign * (1 + randn((n, 1), 38).abs())
+    k[:, :, 1:] = 1 + randn((n, 1, hd - 1), 39).abs()
+    R.put(pool, table, 0, 0, k, randn((n, 1, hd), 40))
+    q = randn((1, rows, 2, hd), 41)
+    q[..., 0] = sign * math.inf
+    m = masses(table, 1)
+    m0 = m.clone()
+    out, lse = paged.attention(q, pool, table, i32([n]), scale=1.0, return_lse=True, mass=m)
+    assert not out.any() and bool((lse == -math.inf).all())
+    assert torch.equal(m[..., :n - rows], m0[..., :n - rows]) and not m[..., n - rows:n].any()
+    out, lse = paged.attention(q, pool, table, i32([n]), scale=-1.0, return_lse=True)
+    assert bool(out.isnan().all()) and bool(lse.isnan().all())
