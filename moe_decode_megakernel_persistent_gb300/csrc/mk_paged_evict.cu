@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kSelThreads) k_evict(const __grid_constant__ E
       if (!p.in_place) to[q] = 0.f;
     }
   }
-  for (int q = len + rank * kSelThreads + tid; q < keep; q += C * kSelThreads) kept[q] = -1;
+  for (uint32_t q = len + rank * kSelThreads + tid; q < (uint32_t)keep; q += C * kSelThreads) kept[q] = -1;  // (keep may be 2^31 - 1)
   if (!p.in_place)
     for (int q = len + rank * kSelThreads + tid; q < positions; q += C * kSelThreads) to[q] = 0.f;
   if (C > 1) cluster_sync();  // the lists are whole, and no block reads another's shared memory any more
