@@ -69,21 +69,58 @@ __device__ __forceinline__ Parts parts_of(float x) {
 // Part i of two values as a word.
 __device__ __forceinline__ uint32_t both(const Parts& lo, const Parts& hi, int i) { return __byte_perm(lo.h[i], hi.h[i], 0x7632); }
 
-// The sum of the values of V that are no finite numbers, of dimensions d, d + 1 and the positions
-// a .. b.  Where one is seen, the products may have made NaN of an infinity (times a weight, or a
-// part of it, that is 0 or negative): the result is this sum instead.  Rare, and so plain.
+// What of V is no finite number, over a run's positions: the first +infinity, -infinity and NaN of the dimensions
+// HD / 32 lane + i.  Where one is seen, the products may have made NaN of an infinity (times a weight, or a
+// part of it, that is 0 or negative): the result is these values' sum instead.  Called by a warp, which reads the run's rows
+// once (a thread for a column and two dimensions at a time took 280 times as long as the attention of 16384 positions,
+// and other warps' waits ran out beyond 200000).
 template <int HD>
-__device__ __forceinline__ float2 odd_sum(const Kv4Args& a, int seq, int head, int d, int from, int to) {
-  float2 s = make_float2(0.f, 0.f);
-  for (int q = from; q < to; ++q) {
-    const int page = table_row(a, seq)[q / kPageTokens];
-    if (page < 0 || page >= a.n_pages) continue;
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(paged_at<HD>(a, paged_row(a, page, 1, head, q)) + d), odd = odd_ones(v);
-    if (odd >> 15 & 1u) s.x += low_f(v);
-    if (odd >> 31) s.y += high_f(v);
+struct Odd {
+  int first[HD / 32][3];
+  __device__ __forceinline__ void search(const Kv4Args& a, int seq, int head, int from, int to) {
+    constexpr int V = HD / 32;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < V; ++i) first[i][0] = first[i][1] = first[i][2] = INT_MAX;
+#pragma unroll 1
+    for (int q = from, end; q < to; q = end) {
+      end = min(to, (q / kPageTokens + 1) * kPageTokens);
+      const int page = table_row(a, seq)[q / kPageTokens];
+      if (page < 0 || page >= a.n_pages) continue;
+      const uint32_t* v = reinterpret_cast<const uint32_t*>(paged_at<HD>(a, paged_row(a, page, 1, head, q)) + V * lane);
+#pragma unroll 8
+      for (int p = q; p < end; ++p, v += HD / 2) {
+        uint32_t x[V / 2];
+        if constexpr (V == 4) {
+          const uint2 y = *reinterpret_cast<const uint2*>(v);
+          x[0] = y.x, x[1] = y.y;
+        } else {
+          x[0] = *v;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const uint32_t w = i & 1 ? x[i / 2] >> 16 : x[i / 2] & 0xFFFFu;
+          first[i][0] = min(first[i][0], w == 0x7F80u ? p : INT_MAX);
+          first[i][1] = min(first[i][1], w == 0xFF80u ? p : INT_MAX);
+          first[i][2] = min(first[i][2], (w & 0x7FFFu) > 0x7F80u ? p : INT_MAX);
+        }
+      }
+    }
   }
-  return s;
-}
+  // The sum over the positions below lim in dimension d (0: there is none); called by the whole warp.
+  __device__ __forceinline__ float sum(int d, int lim) const {
+    constexpr int V = HD / 32;
+    int at[3] = {INT_MAX, INT_MAX, INT_MAX};
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        const int y = __shfl_sync(0xffffffffu, first[i][x], d / V);
+        if (d % V == i) at[x] = y;
+      }
+    return at[2] < lim || (at[0] < lim && at[1] < lim) ? NAN : at[0] < lim ? INFINITY : at[1] < lim ? -INFINITY : 0.f;
+  }
+};
 // Pairs of fp32 in one instruction, and the largest of three.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
   uint64_t z;

@@ -482,7 +482,9 @@ __global__ void __launch_bounds__(32 * W, B) k_paged_attention(const __grid_cons
     const bool whole = p.cluster <= 1 && run.t0 == 0 && run.t1 == run.nt;
     const size_t slot = part_slot(blockIdx.x, run.t0);
     const int ncol = min(CT, p.cols - j * CT);
-    for (int x = tid; x < ncol * HD / 2; x += NTHR) {
+    Odd<HD> odd;
+    bool searched = false;
+    for (int x = tid; x < ncol * HD / 2; x += NTHR) {  // (a warp's elements are of one column)
       const int c = x / (HD / 2), d = x % (HD / 2) * 2;
       float M = kLow, l_sum = 0.f;
 #pragma unroll
@@ -495,8 +497,11 @@ __global__ void __launch_bounds__(32 * W, B) k_paged_attention(const __grid_cons
         const float2 y = *reinterpret_cast<const float2*>(red + (i * CT + c) * S::RS + d);
         v.x += y.x * f, v.y += y.y * f;
       }
-      if (!(is_finite(v.x) && is_finite(v.y)) && is_finite(l_sum)) {
-        const float2 s = odd_sum<HD>(p.a, seq, run.head, d, run.t0 * SP, min(run.t1 * SP, max(0, len - nn + row_of(p, j * CT + c) + 1)));
+      if (__any_sync(0xffffffffu, !(is_finite(v.x) && is_finite(v.y)) && is_finite(l_sum))) {
+        if (!searched) odd.search(p.a, seq, run.head, run.t0 * SP, min(run.t1 * SP, any));
+        searched = true;
+        const int sees = len - nn + row_of(p, j * CT + c) + 1;
+        const float2 s = make_float2(odd.sum(d, sees), odd.sum(d + 1, sees));
         if (s.x != 0.f) v.x = s.x;
         if (s.y != 0.f) v.y = s.y;
       }

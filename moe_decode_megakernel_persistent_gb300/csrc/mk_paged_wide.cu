@@ -546,6 +546,8 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
         constexpr int WORDS = GR > 1 && W::P == 1 ? NG * 4 : NG * 8;                  // 16-byte words of a row
         constexpr int DP = WORDS * (F ? 4 : 8), CH = DP < 32 ? DP : 32;               // dimensions of a pass, of a read
         const int w0 = GR > 1 && W::P == 1 ? group * WORDS : 0, part0 = GR > 1 && W::P == 3 ? group * W::QT : 0;
+        Odd<HD> search;
+        bool searched = false;
 #pragma unroll 1
         for (int c0 = group * (HD / GR); c0 < (group + 1) * (HD / GR); c0 += DP) {
 #pragma unroll 1
@@ -562,15 +564,16 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
 #pragma unroll
             for (int x = 0; x < CH; ++x) top = fmaxf(top, fabsf(o[x])), nan = nan || o[x] != o[x];
             const bool fine = !nan && is_finite(top);
-            if (!fine && lim && is_finite(l)) {  // (positions that all columns see went through the products as they are)
+            const bool mend = !fine && lim && is_finite(l);  // (positions that all columns see went through the products as they are)
+            if (__any_sync(0xffffffffu, mend)) {
+              if (!searched) search.search(p.a, seq, rs.head, rs.t0 * SP, min(__reduce_max_sync(0xffffffffu, lim), rs.t1 * SP));
+              searched = true;
 #pragma unroll 1
-              for (int q = 0; q < CH; q += 2) {
-                const float2 s = odd_sum<HD>(p.a, seq, rs.head, c + q, rs.t0 * SP, min(lim, rs.t1 * SP));
+              for (int q = 0; q < CH; ++q) {
+                const float s = search.sum(c + q, lim);
 #pragma unroll
-                for (int x = 0; x < CH; x += 2) {
-                  if (x == q && s.x != 0.f) o[x] = s.x;
-                  if (x == q && s.y != 0.f) o[x + 1] = s.y;
-                }
+                for (int x = 0; x < CH; ++x)
+                  if (x == q && mend && s != 0.f) o[x] = s;
               }
             }
 #pragma unroll

@@ -1,9 +1,11 @@
 """The operators on the 16-bit paged cache at the ends of what their arguments may be."""
+import math
+
 import pytest
 import torch
 
 from moe_decode_megakernel_persistent_gb300 import paged
-from tests.test_gpu_paged import i32, make, masses
+from tests.test_gpu_paged import BF, F32, gen, i32, make, masses, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -22,3 +24,30 @@ def test_an_eviction_that_keeps_2_31_positions(gpu_lib):
     assert torch.equal(pool.view(torch.int16), before.view(torch.int16))
     del kept, part
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,hd,n", [(40, 128, 400000), (100, 64, 400000), (1, 128, 400000), (3, 64, 60000)])
+def test_a_value_that_is_no_number_costs_little(gpu_lib, dtype, rows, hd, n):
+    """Runs of whole items, several a block: the search for what of V is no finite number, at a run's end, is over
+    long before another warp's wait runs out, which would spoil other sequences.  (All sequences are made of 64 pages;
+    four have one of their own with such a value.)"""
+    seqs, G, H = 80, 2, 4
+    pool = randn((68, 2, G, 128, hd), 51, BF)
+    table = torch.randint(0, 64, (seqs, n // 128), dtype=torch.int32, device="cuda", generator=gen(52))
+    odd = {0: (0, 9, 5, math.nan), 5: (1, n // 2, 63, math.inf), 37: (0, 70, 0, -math.inf), 79: (1, 0, 17, math.nan)}
+    for j, (i, (g, p, d, x)) in enumerate(odd.items()):
+        table[i, p // 128] = 64 + j
+    q = randn((seqs, rows, H, hd), 53, dtype)
+    lengths = i32([n // 128 * 128 - 7 * i for i in range(seqs)])
+    want = paged.attention(q, pool, table, lengths)
+    for j, (g, p, d, x) in enumerate(odd.values()):
+        pool[64 + j, 1, g, p % 128, d] = x
+    status = i32([0])
+    out = paged.attention(q, pool, table, lengths, status=status)
+    assert status.item() == 0
+    for i, (g, p, d, x) in odd.items():
+        got = out[i, :, 2 * g:2 * g + 2, d]
+        assert bool((got.isnan() if math.isnan(x) else got == x).all()), i
+        out[i, :, 2 * g:2 * g + 2, d] = want[i, :, 2 * g:2 * g + 2, d]
+    assert torch.equal(out, want)
