@@ -781,6 +781,7 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
     for (int i0 = first; i0 < n; i0 += NB * by) {
       float2 ml[NB];
       float v[NB][V];
+      uint32_t there = 0;
 #pragma unroll
       for (int y = 0; y < NB; ++y) {
         const int i = i0 + y * by, at = i < n ? slot[i] : -1;
@@ -788,6 +789,7 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
 #pragma unroll
         for (int x = 0; x < V; ++x) v[y][x] = 0.f;
         if (at >= 0) {
+          there |= 1u << y;
           const float* src = p.part + ((size_t)at * CT + c) * (HD + 4);
           ml[y] = *reinterpret_cast<const float2*>(src + HD);
 #pragma unroll
@@ -798,16 +800,31 @@ __global__ void __launch_bounds__(512) k_kv4_join(const __grid_constant__ AttArg
 #pragma unroll
       for (int y = 0; y < NB; ++y) M = fmaxf(M, ml[y].x);
       const float f0 = exp2_fast(m - M);
+      float f[NB];
+      bool lost = i0 != first && f0 == 0.f;
+#pragma unroll
+      for (int y = 0; y < NB; ++y) {
+        f[y] = exp2_fast(ml[y].x - M);
+        lost = lost || (f[y] == 0.f && there >> y & 1u);
+      }
       m = M;
       l *= f0;
 #pragma unroll
-      for (int x = 0; x < V; ++x) o[x] = taken(o[x], f0);
+      for (int y = 0; y < NB; ++y) l += ml[y].y * f[y];
+      if (lost) {
 #pragma unroll
-      for (int y = 0; y < NB; ++y) {
-        const float f1 = exp2_fast(ml[y].x - M);
-        l += ml[y].y * f1;
+        for (int x = 0; x < V; ++x) {
+          o[x] = taken(o[x], f0);
 #pragma unroll
-        for (int x = 0; x < V; ++x) o[x] += taken(v[y][x], f1);
+          for (int y = 0; y < NB; ++y) o[x] += taken(v[y][x], f[y]);
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < V; ++x) {
+          o[x] *= f0;
+#pragma unroll
+          for (int y = 0; y < NB; ++y) o[x] += v[y][x] * f[y];
+        }
       }
     }
   };

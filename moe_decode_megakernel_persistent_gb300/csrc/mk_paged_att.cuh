@@ -61,7 +61,8 @@ __device__ __forceinline__ Parts parts_of(float x) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     r.h[i] = __float_as_uint(rest) & 0xFFFF0000u;
-    rest = fabsf(x) == INFINITY ? 0.f : rest - __uint_as_float(r.h[i]);  // (an infinity has no rest)
+    rest -= __uint_as_float(r.h[i]);
+    if (i == 0 && fabsf(x) == INFINITY) rest = 0.f;  // (not inf - inf)
     if (i && !(r.h[i] << 1)) r.h[i] = tiny;
   }
   return r;

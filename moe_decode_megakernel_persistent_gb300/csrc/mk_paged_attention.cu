@@ -574,14 +574,23 @@ __global__ void __launch_bounds__(32 * W, B) k_paged_attention(const __grid_cons
       float l_sum = ml.y * f;
 #pragma unroll
       for (int o2 = 8; o2 > 0; o2 >>= 1) l_sum += __shfl_xor_sync(0xffffffffu, l_sum, o2);
+      const uint32_t lost = __ballot_sync(0xffffffffu, f == 0.f) & some;
       float2 y[16], v = make_float2(0.f, 0.f);
 #pragma unroll
       for (int r = 0; r < 16; ++r)
         y[r] = some >> r & 1u ? *reinterpret_cast<const float2*>(from + r * slots * S::RS + d) : make_float2(0.f, 0.f);
+      if (lost) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float fr = __shfl_sync(0xffffffffu, f, r);
-        if (some >> r & 1u) v.x += taken(y[r].x, fr), v.y += taken(y[r].y, fr);
+        for (int r = 0; r < 16; ++r) {
+          const float fr = __shfl_sync(0xffffffffu, f, r);
+          v.x += taken(y[r].x, fr), v.y += taken(y[r].y, fr);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float fr = __shfl_sync(0xffffffffu, f, r);
+          v.x += y[r].x * fr, v.y += y[r].y * fr;
+        }
       }
       put_out(seq, j * CT + c, head, d, M, l_sum, v);
     }

@@ -536,6 +536,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
       }
       const bool whole = rs.t0 == 0 && rs.t1 == rs.nt;
       const float f = whole ? 1.f / l : 1.f;
+      const bool none = l == 0.f && (whole || !lim);  // (of a part without a weight, infinities and NaN are the join's; the rest is 0)
       const bool look = odd[n_runs & 1];
       float* part = p.part + ((size_t)part_slot(blockIdx.x, rs.t0) * CT + me) * (HD + 4);
       // Through the operand's place in shared memory, so that a warp writes its rows in one piece
@@ -577,8 +578,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
               }
             }
 #pragma unroll
-            for (int x = 0; x < CH; ++x)  // (a part of a column's positions without a weight: infinities and NaN are the join's)
-              o[x] = !ok ? NAN : l != 0.f ? o[x] * f : whole || !lim || is_finite(o[x]) ? 0.f : o[x];
+            for (int x = 0; x < CH; ++x) o[x] = !ok ? NAN : none ? 0.f : o[x] * f;
             if constexpr (F) {
 #pragma unroll
               for (int x = 0; x < CH; x += 4)
@@ -644,6 +644,7 @@ __global__ void __launch_bounds__(256) k_wide_join(const __grid_constant__ AttAr
   const int nt = tiles_of(p, e, CT, SP);
   if (nt && (it.x < 0 || it.y < 0 || it.y >= G)) return;  // done by its block
   float m[2] = {kLow, kLow}, l[2] = {0.f, 0.f}, o[2][V];
+  bool none = true;  // no part yet
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -693,18 +694,34 @@ __global__ void __launch_bounds__(256) k_wide_join(const __grid_constant__ AttAr
 #pragma unroll
         for (int i = 0; i < 4; ++i) M = fmaxf(M, ml[i][c].x);
         const float f0 = exp2_fast(m[c] - M);
+        float f[4];
+        bool lost = !none && f0 == 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[i] = exp2_fast(ml[i][c].x - M);
+          lost = lost || (f[i] == 0.f && part[i]);
+        }
         m[c] = M;
         l[c] *= f0;
 #pragma unroll
-        for (int x = 0; x < V; ++x) o[c][x] = taken(o[c][x], f0);
+        for (int i = 0; i < 4; ++i) l[c] += ml[i][c].y * f[i];
+        if (lost) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f1 = exp2_fast(ml[i][c].x - M);
-          l[c] += ml[i][c].y * f1;
+          for (int x = 0; x < V; ++x) {
+            o[c][x] = taken(o[c][x], f0);
 #pragma unroll
-          for (int x = 0; x < V; ++x) o[c][x] += taken(v[i][c][x], f1);
+            for (int i = 0; i < 4; ++i) o[c][x] += taken(v[i][c][x], f[i]);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < V; ++x) {
+            o[c][x] *= f0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[c][x] += v[i][c][x] * f[i];
+          }
         }
       }
+      none = false;
     }
     if (end) break;
   }
