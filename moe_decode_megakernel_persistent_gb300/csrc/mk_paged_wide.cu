@@ -352,12 +352,13 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
           bool some[AT];
 #pragma unroll
           for (int i = 0; i < AT; ++i) {
-            // (a row that is none, or padding, reads another's and counts as 0)
+            // (a row that is none, or padding, reads another's and counts as 0; not by the read-only path, for the
+            // kernel may begin while its predecessor writes q)
             const int c = col - lane + (32 * (i0 + i) + lane) / (NG * 8), cc = min(c, p.cols - 1), rw = row_of(p, cc);
             const T* src = reinterpret_cast<const T*>(p.q.p) + seq * p.q.seq + rw * p.q.row + (rs.head * p.gqa + cc - rw * p.gqa) * p.q.head + 8 * x;
             some[i] = c < p.cols && rw < rs.nn && rs.len - rs.nn + rw >= 0;
 #pragma unroll
-            for (int z = 0; z < (W::F32 ? 2 : 1); ++z) h[i][z] = __ldg(reinterpret_cast<const uint4*>(src) + z);
+            for (int z = 0; z < (W::F32 ? 2 : 1); ++z) h[i][z] = __ldcg(reinterpret_cast<const uint4*>(src) + z);
           }
 #pragma unroll
           for (int i = 0; i < AT; ++i) {
