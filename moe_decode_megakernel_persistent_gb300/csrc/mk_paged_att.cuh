@@ -158,6 +158,7 @@ int rows_map(CUtensorMap* map, const void* base, long long rows, int head_dim, i
 int device_sms();
 // Masses from the scores that the narrow kernel kept, or formed again (mk_paged_mass.cu), and
 // the workspace that these take.
+bool paged_mass_fits(const Kv4Args& a, int n_heads, int dtype, bool wide);  // false: too large a call
 size_t paged_mass_bytes(const Kv4Args& a, int head_dim, int n_heads, int dtype);
 // What needs no log-sum-exp, before the attention.
 cudaError_t paged_mass_begin(const PagedAtt& p, int head_dim, int dtype, cudaStream_t st);

@@ -749,6 +749,7 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, bool mass, 
   }
   pl->score_cols = 0;
   if (mass) {
+    if (!paged_mass_fits(c, n_heads, dtype, pl->wide)) return false;
     pl->lse_off = up16(pl->bytes);
     pl->bytes = pl->lse_off + (size_t)c.n_seqs * c.rows * n_heads * sizeof(float);
     if (!pl->wide) {

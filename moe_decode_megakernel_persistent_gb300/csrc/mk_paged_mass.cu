@@ -533,7 +533,6 @@ MassArgs args_of(const PagedAtt& p, const MassPlan& m, int head_dim) {
   a.N = m.N;
   return a;
 }
-int p_items(const MassArgs& a) { return (int)std::min<long long>((long long)a.pa.t.a.n_seqs * a.pa.t.a.n_kv_heads * a.spans, 0x7FFFFFFF); }
 template <int HD, class T>
 cudaError_t launch_wide(const MassArgs& a, const MassPlan& m, const CUtensorMap& kmap, const CUtensorMap& qmap, cudaStream_t st) {
   using S = MassShape<HD, T>;
@@ -541,7 +540,7 @@ cudaError_t launch_wide(const MassArgs& a, const MassPlan& m, const CUtensorMap&
   if (e != cudaSuccess) return e;
   MassArgs g = a;
   CUtensorMap km = kmap, qm = qmap;
-  int G = m.grid, items = p_items(a);
+  int G = m.grid, items = a.pa.t.a.n_seqs * a.pa.t.a.n_kv_heads * a.spans;
   void* args[] = {&g, &km, &qm};
   e = launch(reinterpret_cast<const void*>(&k_mass_wide<HD, T>), m.grid, S::THREADS, S::SMEM, st, args);
   void* jargs[] = {&g, &G, &items};
@@ -551,12 +550,19 @@ cudaError_t launch_wide(const MassArgs& a, const MassPlan& m, const CUtensorMap&
 
 }  // namespace
 
+// Grids, rows of a tensor map and positions (of whole spans) in 31 bits.
+bool paged_mass_fits(const Kv4Args& a, int n_heads, int dtype, bool wide) {
+  const long long items = (long long)a.n_seqs * a.n_kv_heads, positions = (long long)a.max_pages * kPageTokens;
+  if (positions + kSpan - 1 > INT_MAX || items * ((positions + kSpan - 1) / kSpan) > INT_MAX) return false;
+  if (!wide) return true;
+  const long long N = dtype == MK_F32 ? 64 : 128, cols = (long long)a.rows * (n_heads / a.n_kv_heads);
+  return items * ((cols + N - 1) / N * N) * (dtype == MK_F32 ? 3 : 1) <= INT_MAX;
+}
 size_t paged_mass_bytes(const Kv4Args& a, int head_dim, int n_heads, int dtype) { return plan_of(a, head_dim, n_heads, dtype).bytes; }
 
 cudaError_t paged_mass_begin(const PagedAtt& p, int head_dim, int dtype, cudaStream_t st) {
   const MassArgs a = args_of(p, plan_of(p.t.a, head_dim, p.t.n_heads, dtype), head_dim);
   const long long threads = a.part_rows * (head_dim / 8);
-  if ((threads + 255) / 256 > 0x7FFFFFFF || a.part_rows * 3 > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   MassArgs g = a;
   void* args[] = {&g};
   const void* f = head_dim == 64 ? dtype == MK_F32 ? reinterpret_cast<const void*>(&k_columns<64, float>)
@@ -568,10 +574,8 @@ cudaError_t paged_mass_begin(const PagedAtt& p, int head_dim, int dtype, cudaStr
 
 cudaError_t paged_mass(const PagedAtt& p, const PagedMass& m, int head_dim, int dtype, const CUtensorMap& map, cudaStream_t st) {
   const Kv4Args& a = p.t.a;
-  const long long items = (long long)a.n_seqs * a.n_kv_heads;
   if (p.scores) {
-    const int chunks = (a.max_pages * kPageTokens + 255) / 256;
-    if (items * chunks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const int chunks = (a.max_pages * kPageTokens + 255) / 256, items = a.n_seqs * a.n_kv_heads;
     PagedAtt pa = p;
     PagedMass ms = m;
     int n = chunks;
