@@ -413,8 +413,10 @@ PyObject* py_paged_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (overlap(lengths, tensor(a[1], "table"))) refuse("new_lengths must not overlap table");
   }
   const int64_t sizes[3] = {c.n_seqs, c.n_kv_heads, keep};
-  kept = fresh(sizes, at::kInt, dev);
   const size_t nws = mk_paged_evict_bytes(&c, keep);
+  if (!nws && c.n_seqs)  // a description or keep that the call refuses: before a tensor of its size is made
+    check(mk_paged_evict(&c, &mass, keep, recent, nullptr, nullptr, &to, nullptr, 0, on.stream));
+  kept = fresh(sizes, at::kInt, dev);
   at::Tensor ws;
   if (nws) ws = fresh({(int64_t)nws}, at::kByte, dev);
   check(mk_paged_evict(&c, &mass, keep, recent, static_cast<int32_t*>(kept.data_ptr()), static_cast<int32_t*>(lengths.data_ptr()),

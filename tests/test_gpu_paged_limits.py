@@ -4,6 +4,7 @@ import math
 import pytest
 import torch
 
+from moe_decode_megakernel_persistent_gb300 import _lib as L
 from moe_decode_megakernel_persistent_gb300 import paged
 from tests.test_gpu_paged import BF, F32, gen, i32, make, masses, randn
 
@@ -51,3 +52,15 @@ def test_a_value_that_is_no_number_costs_little(gpu_lib, dtype, rows, hd, n):
         assert bool((got.isnan() if math.isnan(x) else got == x).all()), i
         out[i, :, 2 * g:2 * g + 2, d] = want[i, :, 2 * g:2 * g + 2, d]
     assert torch.equal(out, want)
+
+
+def test_a_refused_eviction_takes_no_memory(gpu_lib):
+    pool, table = make([300], 2, 64, seed=54)
+    m = masses(table, 2)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    with pytest.raises(L.MKError):             # two lists of 2^31 - 1
+        paged.evict(pool, table, i32([300]), m, 2 ** 31 - 1)
+    assert torch.cuda.max_memory_allocated() < before + (1 << 20)
