@@ -555,7 +555,9 @@ typedef struct mk_paged_mass {
  * whatever its weight.  out must not overlap q, the pool, the masses or
  * the workspace.  |scale| < 1e18; a score below -6.9e29 has no weight.  Scores, maxima and sums are
  * fp32; the weights of bf16 rows are two bfloat16 parts (2^-16); an fp32 q and its weights are
- * three (2^-24), and each such result is off by a few 10^-6 of its values' size at most.
+ * three (2^-24), and each such result is off by a few 10^-6 of its values' size at most.  With V of one sign
+ * the products of bf16 rows cut off up to 6e-5 of a result (few columns: 2e-9 for each position of its block's run).
+ * Finite V of magnitudes up to 2^95 stay finite.
  * mass (may be NULL): for every sequence with a new row, and p < lengths[i],
  *     mass[i][g][p] = (p < lengths[i] - n_new[i] ? decay * mass[i][g][p] : 0)
  *                   + the sum of the weights that the rows and the heads of kv head g give p,

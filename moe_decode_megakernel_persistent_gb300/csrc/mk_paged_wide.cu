@@ -59,7 +59,10 @@ struct PWide {
   // sums of fp32 rows are added, rounded, to others that the columns hold (even: the same group's step begins new
   // sums throughout a run).  Three sequences of 700 to 2049 positions, 641 rows: 2 steps are 8.2e-7 off (the same sums by fp32
   // products 7.9e-7) in 90 us, 4 steps 1.3e-6 in 79, 8 steps 1.9e-6 in 74.
-  static constexpr int FLUSH = F32 ? 2 : 0;
+  // Of bf16 rows every 4096 positions: with V of one sign, 131072 in one sum left outputs 9.2e-4 too small, where their own
+  // rounding is 2^-9 to 2^-8 (1024 rows at 8022 positions 83.3 us without, 85.0 with).
+  static constexpr int FLUSH = F32 ? 2 : 32;
+  static constexpr int DIMS = HD / GR;              // of a thread's sums
   static constexpr int CW = 4 * TB * GR;            // warps of the columns: eight
   static constexpr int THREADS = 32 * (CW + 2);
 };
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
     constexpr uint32_t id_pv = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((HD >> 3) << 17) | ((128 >> 4) << 24);  // V by rows
     const uint32_t tmu = uniform(tm), qu = uniform(smem_addr(q_op)), kvu = uniform(smem_addr(kv_op));
     uint32_t st = 0, round = 0, k = 0;  // the next stage and its phase, steps taken
-    [[maybe_unused]] uint32_t n_flush = 0;
+    uint32_t n_flush = 0;
     RunSays rs;
     bool ok = true;
     // the next stage, once it has arrived
@@ -271,12 +274,11 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
       uint32_t v = arrived(), kn = NS < n ? arrived() : 0;
       clean(0, v);
       for (int i = 0; i < n; ++i, ++k) {
-        const uint32_t pu = uniform(k % NS), add = uniform(W::FLUSH ? i % W::FLUSH != 0 : i ? 1 : 0), nu = uniform(i + NS < n), lu = uniform(i + 1 == n);
-        [[maybe_unused]] const uint32_t last = uniform(W::FLUSH ? i + 1 < n && (i + 1) % W::FLUSH == 0 : 0);  // of these sums
+        const uint32_t pu = uniform(k % NS), add = uniform(i % W::FLUSH != 0), nu = uniform(i + NS < n), lu = uniform(i + 1 == n);
+        const uint32_t last = uniform(i + 1 < n && (i + 1) % W::FLUSH == 0);  // of these sums
         const uint64_t vd = operand(kvu + v * W::KVB, SP * 128);
         uint32_t vn = 0, kn2 = 0;
-        if constexpr (W::FLUSH > 0)
-          if (i && i % W::FLUSH == 0) ok = wait_for(smem_addr(&flushed), n_flush++ & 1, &give_up, p.a.status) && ok;  // the sums are read
+        if (i && i % W::FLUSH == 0) ok = wait_for(smem_addr(&flushed), n_flush++ & 1, &give_up, p.a.status) && ok;  // the sums are read
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
           // the weights come in halves of 64 positions
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
               if (h) {
                 if (t == TB - 1) commit(smem_addr(&kv_empty[v]));
                 if (NS > 1) commit(smem_addr(&pv_done));
-                if (W::FLUSH && last) commit(smem_addr(&sums_done));
+                if (t == TB - 1 && last) commit(smem_addr(&sums_done));
                 if (lu) commit(smem_addr(&run_done[t]));
                 if (nu) scores(t, pu, kn);
               }
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
     const uint32_t tm_s = tm + W::TM * tile + ((uint32_t)(32 * quarter) << 16), tm_o = tm_s + W::SUMS;
     [[maybe_unused]] float* ex = reinterpret_cast<float*>(kv_op + ST * W::KVB);  // maxima [CT], sums [2][CT]
     uint32_t k = 0;
-    [[maybe_unused]] uint32_t n_flush = 0;
+    uint32_t n_flush = 0;
     RunSays rs;
     const float cf = fabsf(p.c);
     // word x of row y of these lanes' part of the q operand, which also holds the sums on their way out
@@ -386,30 +388,36 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
       const int skip = GR > 1 ? (k ^ group) & 1 : 0;  // the group's first step of the run
       int page = rs.t0 + skip < rs.t1 ? pages[rs.t0 + skip] : -1;
       float m = kLow, l = 0.f;  // running maximum (log2) that l is relative to, and the sum of the weights
-      // sums of earlier steps of this thread's half of the dimensions (in local memory), and the maximum they are relative to
-      [[maybe_unused]] float held[W::FLUSH ? HD / 2 : 1], m_held = -INFINITY;  // (none yet)
+      // sums of earlier steps of this thread's dimensions (in local memory), and the maximum they are relative to
+      float held[W::DIMS], m_held = -INFINITY;  // (none yet)
       // the sums so far, relative to the maximum `now`, to those held
-      [[maybe_unused]] auto flush = [&](float now) {
+      auto flush = [&](float now) {
         wait_for(smem_addr(&sums_done), n_flush++ & 1, &give_up, p.a.status);
         after_sync();
-        float o[HD / 2];
-#pragma unroll
-        for (int c = 0; c < HD / 2; c += 32) tm_read32(tm_o + group * (HD / 2) + c, *reinterpret_cast<float(*)[32]>(o + c));
-        before_sync();
-        __syncwarp();
-        if (lane == 0) arrive(smem_addr(&flushed));
         const float f = exp2_fast(m_held - now);
+        constexpr int AT = W::F32 ? W::DIMS : 32;  // (of fp32 rows often: the products go on before the sums are added)
+#pragma unroll 1
+        for (int c0 = 0; c0 < W::DIMS; c0 += AT) {
+          float o[AT];
 #pragma unroll
-        for (int c = 0; c < HD / 2; ++c) held[c] = m_held == -INFINITY ? o[c] : fmaf(held[c], f, o[c]);
+          for (int c = 0; c < AT; c += 32) tm_read32(tm_o + group * W::DIMS + c0 + c, *reinterpret_cast<float(*)[32]>(o + c));
+          if (c0 + AT == W::DIMS) {
+            before_sync();
+            __syncwarp();
+            if (lane == 0) arrive(smem_addr(&flushed));
+          }
+#pragma unroll
+          for (int c = 0; c < AT; ++c) held[c0 + c] = m_held == -INFINITY ? o[c] : fmaf(held[c0 + c], f, o[c]);
+        }
         m_held = now;
       };
       for (int t = rs.t0 + skip;; t += GR) {
         const uint32_t kk = k + (t - rs.t0);
-        if constexpr (W::FLUSH > 0) {  // both groups, before the first step of new sums or the one behind it
-          const int i = t - rs.t0, in = i % W::FLUSH;
+        {  // all groups, before the first step of new sums or the one behind it
+          const int i = t - rs.t0, in = (int)((uint32_t)i % W::FLUSH);
           if (i >= W::FLUSH && in < GR && i - in < rs.t1 - rs.t0) {
             float now = m;
-            if (in == 0) {  // (the other group had the last step)
+            if (GR > 1 && in == 0) {  // (the other group had the last step)
               wait_for(smem_addr(&m_full[group ^ 1][quarter]), ((kk - 1) >> 1) & 1, &give_up, p.a.status);
               now = *reinterpret_cast<volatile float*>(ex + me);
             }
@@ -468,7 +476,7 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
             }
             l *= exp2_fast(m - now);
             m = now;
-            const bool fresh = W::FLUSH ? (t - rs.t0) % W::FLUSH == 0 : t == rs.t0;  // the sums begin with this step
+            const bool fresh = (uint32_t)(t - rs.t0) % W::FLUSH == 0;  // the sums begin with this step
             if (moves && !fresh) {
               if constexpr (NS > 1) {  // the sums hold the last step (with one place of scores these have waited for it)
                 wait_for(smem_addr(&pv_done), (kk - 1) & 1, &give_up, p.a.status);
@@ -557,11 +565,11 @@ __global__ void __launch_bounds__(PWide<HD, T, TB>::THREADS, 1) k_paged_wide(con
             float o[CH], top = 0.f;
             if constexpr (CH == 32) tm_read32(tm_o + c, o);
             else tm_read16(tm_o + c, o);
-            if constexpr (W::FLUSH > 0)
-              if (m_held != -INFINITY) {
-                const float g = exp2_fast(m_held - m);
-                for (int x = 0; x < CH; ++x) o[x] = fmaf(held[c - group * (HD / 2) + x], g, o[x]);
-              }
+            if (m_held != -INFINITY) {
+              const float g = exp2_fast(m_held - m);
+#pragma unroll
+              for (int x = 0; x < CH; ++x) o[x] = fmaf(held[c - group * W::DIMS + x], g, o[x]);
+            }
             bool nan = look;
 #pragma unroll
             for (int x = 0; x < CH; ++x) top = fmaxf(top, fabsf(o[x])), nan = nan || o[x] != o[x];

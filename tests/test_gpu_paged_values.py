@@ -134,3 +134,23 @@ def test_an_infinite_query(gpu_lib, rows, sign):
     assert torch.equal(m[..., :n - rows], m0[..., :n - rows]) and not m[..., n - rows:n].any()
     out, lse = paged.attention(q, pool, table, i32([n]), scale=-1.0, return_lse=True)
     assert bool(out.isnan().all()) and bool(lse.isnan().all())
+
+
+@pytest.mark.parametrize("rows,seqs", [(1, 19), (6, 19), (40, 19), (64, 38)])
+def test_long_sums_of_one_sign_of_bf16_rows(gpu_lib, rows, seqs):
+    """Runs of whole items of 131072 positions (pages in common) and V above 0: what the products cut off adds up.  An
+    output's own rounding is off by 2^-8 at most, evenly to both sides: as a mean over 1024 dimensions of sizes over
+    an octave 2^-8 / sqrt(3 x 1024), of which six times that are allowed.  Many columns: 4096 positions' 512 products cut
+    off up to 2^-23 of their sum each, 32 such sums are added with 2^-24 (all in one sum: 9.2e-4 off).  Few: each of four
+    warps adds the 4096 products of its positions, of which a product cuts off 2^-23 of the sum so far, a half of the whole."""
+    n, hd, G = 131072, 128, 8
+    pool = randn((512, 2, G, 128, hd), 60, BF)
+    size = torch.exp2(torch.rand((G, 1, hd), device="cuda", generator=torch.Generator(device="cuda").manual_seed(61)))
+    pool[:, 1] = (pool[:, 1].float().abs() * size).to(BF)
+    table = torch.randint(0, 512, (seqs, n // 128), dtype=torch.int32, device="cuda", generator=torch.Generator(device="cuda").manual_seed(62))
+    q = randn((seqs, rows, 4 * G, hd), 63, BF, 1.5)
+    out = paged.attention(q, pool, table, i32([n] * seqs))
+    k, v = R.rows_of(pool, table, seqs - 1, n)
+    want = torch.cat([R.attend(q[-1, :, 4 * g:4 * g + 4], k[:, g:g + 1], v[:, g:g + 1], n - rows, 1 / math.sqrt(hd))[0] for g in range(G)], 1)
+    most = (512 + 16 if rows > 8 else 4096 / 2) * 2.0 ** -23 + 6 * 2.0 ** -8 / math.sqrt(3 * 1024)
+    assert abs(float(((out[-1].double() - want) / want).mean())) < most
