@@ -154,3 +154,55 @@ def test_long_sums_of_one_sign_of_bf16_rows(gpu_lib, rows, seqs):
     want = torch.cat([R.attend(q[-1, :, 4 * g:4 * g + 4], k[:, g:g + 1], v[:, g:g + 1], n - rows, 1 / math.sqrt(hd))[0] for g in range(G)], 1)
     most = (512 + 16 if rows > 8 else 4096 / 2) * 2.0 ** -23 + 6 * 2.0 ** -8 / math.sqrt(3 * 1024)
     assert abs(float(((out[-1].double() - want) / want).mean())) < most
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,n", [(1, 30), (1, 40000), (5, 700), (40, 9000), (200, 2100)])
+def test_large_values(gpu_lib, dtype, rows, n):
+    """V of magnitudes 2^93 to 2^95: sums over the positions, by weights up to 2^8, stay in fp32."""
+    pool, table = make([n], 2, 64, seed=42)
+    v = torch.exp2(93 + 2 * torch.rand((n, 2, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(43)))
+    k = randn((n, 2, 64), 44)
+    R.put(pool, table, 0, 0, k, torch.where(k < 0, -v, v).clamp(-2.0 ** 95, 2.0 ** 95))
+    check(randn((1, rows, 4, 64), 45, dtype), pool, table, [n], scale=0.5)
+
+
+# ---------------------------------------------------------------- masses behind the ends, long sums
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,n_new", [(1, None), (5, [5, 0, 2, 5]), (60, [60, 1, 0, 33])])
+def test_masses_behind_the_ends_are_not_used(gpu_lib, dtype, rows, n_new):
+    """Behind a sequence's end and in its new positions masses are NaN: kept as they are there, not used here."""
+    lengths = [300, 130, 1, 257]
+    pool, table = make(lengths, 2, 64, seed=46, width=4)
+    m = masses(table, 2)
+    for i, n in enumerate(lengths):
+        m[i, :, max(0, n - (rows if n_new is None else n_new[i])):] = math.nan
+    q = randn((4, rows, 4, 64), 47, dtype)
+    got = m.clone()
+    paged.attention(q, pool, table, i32(lengths), n_new=None if n_new is None else i32(n_new), mass=got, decay=0.5)
+    m[:] = torch.where(m.isnan(), 0.0, m)
+    want = m.clone()
+    paged.attention(q, pool, table, i32(lengths), n_new=None if n_new is None else i32(n_new), mass=want, decay=0.5)
+    for i, n in enumerate(lengths):
+        assert torch.equal(got[i, :, :n], want[i, :, :n]) and bool(torch.isfinite(got[i, :, :n]).all())
+        assert bool(got[i, :, n:].isnan().all())
+
+
+@pytest.mark.parametrize("rows", [40, 1])
+def test_long_sums_of_one_sign(gpu_lib, rows):
+    """152 items of 30000 positions, so that a run is a whole item, and V above 0, so that what the products
+    cut off adds up.  Many columns: two steps' 48 products cut off up to 2^-23 of their sum each, of which there are
+    118, each added with 2^-24: (48 + 59) 2^-23.  (All 235 steps in one sum would lose about 235 x 24 x 2^-24 / 2,
+    1.7e-4.)  Few: the 16 positions of three products lose 3 x 2^-23, and 470 sums are added to a warp's, each
+    rounded by 2^-24 at most, evenly to both sides: sqrt(470 / 3) 2^-24 as a norm, of which six times that are allowed."""
+    n, hd, G = 30000, 64, 8
+    pool, table = make([n] * 19, G, hd, seed=48)
+    pool.abs_()
+    q = randn((19, rows, 4 * G, hd), 49, F32, 1.5)
+    out = paged.attention(q, pool, table, i32([n] * 19))
+    most = (48 + 59) * 2.0 ** -23 if rows > 1 else 3 * 2.0 ** -23 + 6 * math.sqrt(470 / 3) * 2.0 ** -24
+    for i in (0, 18):
+        k, v = R.rows_of(pool, table, i, n)
+        want = torch.cat([R.attend(q[i, :, 4 * g:4 * g + 4], k[:, g:g + 1], v[:, g:g + 1], n - rows, 1 / math.sqrt(hd))[0] for g in range(G)], 1)
+        assert float((out[i].double() - want).norm() / want.norm()) < most
