@@ -33,7 +33,6 @@ namespace {
 constexpr int kSelWarps = 16, kSelThreads = 32 * kSelWarps, kBins = 4 * kSelThreads;  // four bins a thread
 constexpr int kMostBlocks = 16;  // of an item's cluster
 constexpr int kMostHeld = 96 * kSelThreads;  // positions that a block holds
-constexpr int kFew = 256;        // moves of an item, at most, that its own blocks make
 
 struct EvictArgs {
   Kv4Args a;
@@ -387,8 +386,12 @@ extern "C" MK_API int mk_paged_evict(const mk_paged_cache* c, const mk_paged_mas
   cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelThreads * (kMostHeld / kSelThreads + 1) * 4);
   if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   void* args[] = {&p, &C};
-  // Many moves (a cut of whole prompts) are levelled over all SMs by a kernel of their own; a cache at its budget has few.
-  p.counts = std::min(keep, positions - keep) > kFew ? p.late + (size_t)items * keep : nullptr;
+  // As many moves as the table and keep allow: few are made by the item's own blocks, many levelled over all SMs by a kernel of
+  // their own, unless the items fill the SMs themselves (keep 4096; own blocks and a second kernel, us: 4 items of 256 moves
+  // 15.5 and 16.4, 512 17.7 and 16.7; 16 of 512 18.0 and 18.5, 1024 22.1 and 22.2, 2048 30.8 and 22.6; 64 of 1024 26.5 and 28.1,
+  // 2048 47.3 and 44.4; 256 of 256 24.1 and 25.9, 2048 110 and 119).
+  const int few = items >= sms ? INT_MAX : items >= 16 ? 1024 : 256;
+  p.counts = std::min(keep, positions - keep) > few ? p.late + (size_t)items * keep : nullptr;
   if (e == cudaSuccess) e = launch(f, (unsigned)items * C, kSelThreads, smem, st, args, C);
   if (e == cudaSuccess && p.counts) {
     int blocks = (8 * sms + items - 1) / items;
