@@ -604,11 +604,19 @@ __global__ void __launch_bounds__(32 * W, B) k_paged_attention(const __grid_cons
 // without: 40 sequences of 1000 positions 20.0 and 25.4 us, 16 of 4100 26.7 and 30.1, 16 of 100 to 4100 20.7 and 20.1; one of
 // 20000, 20 steps a block against 4, 19.6 and 16.9).
 constexpr int kShort = 10, kJoin = 8;
-// Columns up to which the narrow kernel runs, as far as registers hold the sums and q of a warp's columns (one sequence of
-// 8022 positions of 4 heads; narrow and wide): fp32 16 (128 dimensions, 18.1 and 32.0 us; more would spill), bf16 24 (128
-// dimensions, 15.0 and 27.3; 32, which spill, 19.9 and 28.4 but with 64 sequences 222 and 169) and 32 (64 dimensions, 12.9 and 22.2; with 64
-// sequences of 100 to 8022 positions 78 and 153).
-constexpr int narrow_cols(int head_dim, int dtype) { return dtype == MK_F32 ? 16 : head_dim == 64 ? 32 : 24; }
+// Columns up to which the narrow kernel runs, as far as registers hold the sums and q of a warp's columns (4 heads; one sequence
+// of 8022 positions and 64 of 100 to 8022, narrow and wide, us): fp32 16 (128 dimensions 18.9 and 33.0, 127 and 236; 64 dimensions
+// 12.8 and 26.3, 75 and 159), bf16 of 64 dimensions 32 (14.2 and 25.7, 81 and 103), of 128 dimensions 16 (13.8 and 27.5, 95 and 117) or 24.
+// The third tile of 128 dimensions has one block an SM, so that large batches are faster in the wide kernel unless masses follow, for
+// which that forms the scores again (24 columns: one sequence 16.7 and 28.7, 16 of 8022 68.2 and 63.6, 32 of 2049 45.5 and 48.8, 32 of
+// 100 to 8022 83 and 67, 64 of these 163 and 118; with masses 32 116 and 121, 64 of 2049 111 and 136).
+// steps: of tiles of 128 columns and pages, for an SM.
+constexpr long long kBatch = 24;
+int narrow_cols(int head_dim, int dtype, bool mass, long long steps) {
+  if (dtype == MK_F32) return 16;
+  if (head_dim == 64) return 32;
+  return mass || steps <= kBatch ? 24 : 16;
+}
 
 struct Plan {
   bool wide = false;
@@ -633,10 +641,9 @@ void take(Plan* pl) {
   pl->threads = 32 * W;
 }
 
-// steps: of the wide kernel's tiles of 128 columns, for an SM
 template <int HD>
-void take_for(Plan* pl, int cols, int dtype, long long steps) {
-  if (cols > narrow_cols(HD, dtype)) {
+void take_for(Plan* pl, int cols, int dtype, bool mass, long long steps) {
+  if (cols > narrow_cols(HD, dtype, mass, steps)) {
     const WideKernel w = paged_wide_kernel(HD, dtype, cols, steps);
     pl->main = w.fn;
     pl->id = (HD == 64 ? 0 : 10) + (w.CT > 128 ? 8 : dtype == MK_F32 ? 5 : 0);
@@ -717,8 +724,8 @@ bool plan_of(const Kv4Args& c, int head_dim, int n_heads, int dtype, bool mass, 
   if (cols > INT_MAX / 64) return false;
   const int sms = device_sms();
   const long long steps = (cols + 127) / 128 * c.n_seqs * c.n_kv_heads * c.max_pages / sms;
-  if (head_dim == 64) take_for<64>(pl, (int)cols, dtype, steps);
-  else take_for<128>(pl, (int)cols, dtype, steps);
+  if (head_dim == 64) take_for<64>(pl, (int)cols, dtype, mass, steps);
+  else take_for<128>(pl, (int)cols, dtype, mass, steps);
   const long long ct = (cols + pl->CT - 1) / pl->CT, entries = ct * c.n_seqs, items = entries * c.n_kv_heads;
   const long long most = (long long)c.max_pages * (kPageTokens / pl->SP);  // steps of an item
   if (items > INT_MAX / 32 || (most + kOver) * c.n_kv_heads > INT_MAX) return false;
