@@ -6,7 +6,7 @@ import torch
 
 from moe_decode_megakernel_persistent_gb300 import _lib as L
 from moe_decode_megakernel_persistent_gb300 import paged
-from tests.test_gpu_paged import BF, F32, gen, i32, make, masses, randn
+from tests.test_gpu_paged import BF, F32, check, check_evict, gen, i32, make, masses, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,27 @@ def test_a_refused_eviction_takes_no_memory(gpu_lib):
     with pytest.raises(L.MKError):             # two lists of 2^31 - 1
         paged.evict(pool, table, i32([300]), m, 2 ** 31 - 1)
     assert torch.cuda.max_memory_allocated() < before + (1 << 20)
+
+
+@pytest.mark.parametrize("kind", ["zeros", "equal", "two values"])
+@pytest.mark.parametrize("seqs,n,keep,recent", [(8, 4097, 4096, 32), (1, 131071, 32768, 1024), (3, 8448, 2048, 0), (2, 300, 7, 7)])
+def test_evictions_of_equal_masses(gpu_lib, kind, seqs, n, keep, recent):
+    """Ties for all of a sequence: every position counts in the same place of each pass, and the lowest stay."""
+    pool, table = make([n] * seqs, 2, 64, seed=55)
+    m = torch.zeros((seqs, 2, table.shape[1] * 128), device="cuda")
+    if kind != "zeros":
+        m[:] = 0.75
+    if kind == "two values":
+        m[..., ::3] = 0.5
+    check_evict(pool, table, [n] * seqs, m, keep, recent)
+
+
+@pytest.mark.parametrize("rows", [5, 6])
+@pytest.mark.parametrize("width", [None, 700])
+def test_drafts_in_tables_of_both_forms(gpu_lib, rows, width):
+    """20 and 24 columns of 128 dimensions: the wide kernel where the table stands for much work and no masses follow."""
+    lengths = [2500, 0, 700, 4]
+    pool, table = make(lengths, 4, 128, seed=56, width=width)
+    q = randn((4, rows, 16, 128), 57, BF, 1.5)
+    check(q, pool, table, lengths)
+    check(q, pool, table, lengths, n_new=[rows, rows, 2, 3], mass=masses(table, 4))
