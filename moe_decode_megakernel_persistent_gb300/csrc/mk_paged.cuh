@@ -30,6 +30,10 @@ __device__ __forceinline__ void behind() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 inline cudaError_t launch(const void* kernel, unsigned grid, int block, size_t smem, cudaStream_t st, void** args, int cluster = 0,
                           unsigned grid_y = 1) {
   cudaLaunchConfig_t cfg = {};

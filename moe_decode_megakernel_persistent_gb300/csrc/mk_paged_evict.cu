@@ -56,10 +56,6 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   if (x != x) return 0xFFFFFFFFu;
   return u >> 31 ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
 __device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
   uint32_t y;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
