@@ -25,10 +25,10 @@
 // of the product and added to the columns that see it.
 //
 // Bounds.  Large batches run at the memory's rate: 64 sequences of 4096 to 16384 positions, one row of 16 heads on 4 of 128
-// dimensions, read 1.34 GB in 196 us and take 202 with the join (the copy's rate gives 197).  16 of 256 to 8448 take 31
-// (21 by bytes: the join is 5, the start and the runs' ends as much).  One of 2049 takes 7.2, which is the chain
-// launch, lengths and pages, first copies, a step or two, join in the cluster.  The few columns leave the tensor cores 9 %
-// and the issue slots 11 % busy.
+// dimensions, read 1.34 GB in 196 us and take 200 to 203 with the join (the copy's rate gives 197).  16 of 256 to 8448 take 31
+// (21 by bytes: the join is 5, the start and the runs' ends as much).  One of 2049 takes 7.6, which is the chain
+// launch, lengths and pages, first copies, a step or two, join in the cluster.  The few columns leave the tensor cores 13 %
+// and the issue slots 13 % busy; 20 columns of one sequence of 8022 take 16.0 (2.4 by bytes: 16 blocks a head, 64 SMs).
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(32 * W, B) k_paged_attention(const __grid_cons
 // A cluster for each item saves the second kernel but leaves SMs idle: it runs for blocks of up to kShort steps, and up to
 // twice that where equal runs would save fewer than kJoin steps each (one row of 16 heads on 4 of 128; with the second part and
 // without: 40 sequences of 1000 positions 20.0 and 25.4 us, 16 of 4100 26.7 and 30.1, 16 of 100 to 4100 20.7 and 20.1; one of
-// 20000, 20 steps a block against 4, 19.6 and 16.9).
+// 20000, 20 steps a block against 4, 19.6 and 16.9).  Steps are those of the table's width, which the host knows.
 constexpr int kShort = 10, kJoin = 8;
 // Columns up to which the narrow kernel runs, as far as registers hold the sums and q of a warp's columns (4 heads; one sequence
 // of 8022 positions and 64 of 100 to 8022, narrow and wide, us): fp32 16 (128 dimensions 18.9 and 33.0, 127 and 236; 64 dimensions

@@ -7,7 +7,7 @@
 // K and V are operands as the tensor copies bring them.  A thread has a column (a TMEM lane):
 // its maximum is its own and moves only when a score passes it by 2^8; then it rescales its
 // sums, which the next product waits for.  An fp32 q is three bf16 parts, and so are its weights; a bf16 one's
-// are two (one part, 2^-8, took 11 us less of the 81.5 below, and left an error of 0.0026 of the outputs' size for 0.0017).
+// are two (one part, 2^-8, took 11 us less of the 85 below, and left an error of 0.0026 of the outputs' size for 0.0017).
 //
 // Warps 4 TB: the columns.  One warp more looks up pages and issues the copies, another the
 // products.  With two tiles a block (TB = 2) the tensor cores work on one tile while the
@@ -20,11 +20,11 @@
 // end given to the columns that see them.
 //
 // Bounds.  1024 rows of 16 heads over 8022 positions (4 kv heads of 128) are 49 us of products at the measured
-// rate (33 with weights of one part); this kernel takes 71 and the join 11 (81.5 for the call).  Bytes (4 % of the memory's) do
-// not bound it: a step of two tiles and 128 positions takes about 4,700 cycles, of which
-// the products are 3,072; the columns' reads from TMEM, maxima, exponentials (32 a cycle and SM: 1,024) and writes do
+// rate (33 with weights of one part); the call takes 85, of which the join is about 12.  Bytes (3 % of the memory's) do
+// not bound it, nor do the tensor cores alone (50 % active): a step of two tiles and 128 positions takes about 4,900 cycles, of
+// which the products are 3,072; the columns' reads from TMEM, maxima, exponentials (32 a cycle and SM: 1,024) and writes do
 // not hide wholly behind the other tile's products.  fp32 rows (three sequences of up to 2049 positions, 641 rows) do the products of
-// three parts, 26 us, in 77 + 12, of which handing the sums over every second step is 15.
+// three parts, 26 us, in 94 with the join's 12, of which handing the sums over every second step is about 15.
 //
 // One warp decides the block's runs and hands them to the others with the lengths it saw, so that all
 // agree should someone write the lengths while the call runs.
@@ -58,7 +58,7 @@ struct PWide {
   // The products cut off what they add, about 2^-24 of the sum each time and always towards 0: after so many steps the
   // sums of fp32 rows are added, rounded, to others that the columns hold (even: the same group's step begins new
   // sums throughout a run).  Three sequences of 700 to 2049 positions, 641 rows: 2 steps are 8.2e-7 off (the same sums by fp32
-  // products 7.9e-7) in 90 us, 4 steps 1.3e-6 in 79, 8 steps 1.9e-6 in 74.
+  // products 7.9e-7) in 94 us; when that was 90, 4 steps were 1.3e-6 off in 79 and 8 steps 1.9e-6 in 74.
   // Of bf16 rows every 4096 positions: with V of one sign, 131072 in one sum left outputs 9.2e-4 too small, where their own
   // rounding is 2^-9 to 2^-8 (1024 rows at 8022 positions 83.3 us without, 85.0 with).
   static constexpr int FLUSH = F32 ? 2 : 32;
@@ -773,8 +773,8 @@ const void* paged_wide_join(int head_dim, int dtype) {
 WideKernel paged_wide_kernel(int head_dim, int dtype, int cols, long long steps) {
   if (dtype == MK_F32) return head_dim == 64 ? info<64, float, 1>() : info<128, float, 1>();
   // Two tiles a block read K and V half as often and leave the products less idle, one tile runs in finer shares (rows of 4
-  // columns, 4 heads of 128; one and two tiles: one sequence of 8022 positions, 64 rows 24.7 and 34.1 us, 512 44.1 and 47.0, 1024 71.2
-  // and 70.1; two of 20000, 1024 rows 285 and 258; 32 of 8022, 40 rows 185 and 152, 64 rows 189 and 139).  An odd tile leaves a half
+  // columns, 4 heads of 128; one and two tiles: one sequence of 8022 positions, 64 rows 26.3 and 36.1 us, 512 52.3 and 54.3, 1024 89.6
+  // and 83.8; two of 20000, 1024 rows 529 and 504; 32 of 8022, 40 rows 206 and 182, 64 rows 206 and 176).  An odd tile leaves a half
   // of its block idle: no more than one of nine.
   const int tiles = (cols - 1) / 128 + 1;
   if (steps <= 40 || (tiles < 8 && tiles % 2)) return head_dim == 64 ? info<64, __nv_bfloat16, 1>() : info<128, __nv_bfloat16, 1>();

@@ -6,7 +6,7 @@ csrc/mk_torch.cpp).
 
 A pool of one layer is a bfloat16 CUDA tensor [n_pages, 2, n_kv_heads, 128,
 head_dim] (`new_pool`; one layer of a pool of several is `pool[l]`), the layout of
-the engine's own cache.  table is int32 [n_seqs, max_pages], lengths int32
+the engine's own cache (which stays inside the engine).  table is int32 [n_seqs, max_pages], lengths int32
 [n_seqs], n_new int32 [n_seqs] or None, all on the pool's device.  Sequence i
 holds lengths[i] positions, position p in slot p % 128 of page table[i, p // 128];
 its n_new[i] new rows (all rows of the call without n_new) are the last of them,
@@ -75,8 +75,8 @@ def attention(q, pool, table, lengths, n_new=None, scale=None, out=None, return_
     masses of its earlier positions are multiplied by decay, those of its new
     positions start from 0, and each gets the sum of the weights that the rows and
     the query heads of its kv head give it.  Calls of few rows (at most 32 rows x
-    query heads of a kv head) keep their scores meanwhile: 4 bytes for each row, query
-    head and position of the tables."""
+    query heads of a kv head) keep their scores meanwhile: 4 bytes for each of these,
+    rounded up to a multiple of 4, and each kv head and position of the tables."""
     return L.torch_module().paged_attention(q, pool, table, lengths, n_new, scale, out, bool(return_lse), mass, decay, status)
 
 
