@@ -89,8 +89,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 // A part's sum of values, taken to the joined maximum.  A factor of 0 leaves infinities and NaN, which reach their
-// dimension whatever their weight.  (The joins multiply alone where no part has a factor of 0: selected for every value, 1024
-// rows at 8022 positions took 8 us more.)
+// dimension whatever their weight.  (The joins multiply alone where no part has a factor of 0: selected for every value, one
+// row at 2049 positions took 0.3 us more of 7.6.)
 __device__ __forceinline__ float taken(float x, float f) { return f == 0.f && !(fabsf(x) <= 3.402823466e38f) ? x : x * f; }
 constexpr uint32_t kNib = 0x80708070u;
 
