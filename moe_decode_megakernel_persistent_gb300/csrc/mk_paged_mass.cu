@@ -550,10 +550,10 @@ cudaError_t launch_wide(const MassArgs& a, const MassPlan& m, const CUtensorMap&
 
 }  // namespace
 
-// Grids, rows of a tensor map and positions (of whole spans) in 31 bits.
+// Grids (with room for the join's stride), rows of a tensor map and positions (of whole spans) in 31 bits.
 bool paged_mass_fits(const Kv4Args& a, int n_heads, int dtype, bool wide) {
   const long long items = (long long)a.n_seqs * a.n_kv_heads, positions = (long long)a.max_pages * kPageTokens;
-  if (positions + kSpan - 1 > INT_MAX || items * ((positions + kSpan - 1) / kSpan) > INT_MAX) return false;
+  if (positions + kSpan - 1 > INT_MAX || items * ((positions + kSpan - 1) / kSpan) > INT_MAX / 2) return false;
   if (!wide) return true;
   const long long N = dtype == MK_F32 ? 64 : 128, cols = (long long)a.rows * (n_heads / a.n_kv_heads);
   return items * ((cols + N - 1) / N * N) * (dtype == MK_F32 ? 3 : 1) <= INT_MAX;

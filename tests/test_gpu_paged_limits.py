@@ -88,3 +88,69 @@ def test_drafts_in_tables_of_both_forms(gpu_lib, rows, width):
     q = randn((4, rows, 16, 128), 57, BF, 1.5)
     check(q, pool, table, lengths)
     check(q, pool, table, lengths, n_new=[rows, rows, 2, 3], mass=masses(table, 4))
+
+
+@pytest.mark.parametrize("dtype,rows,weigh", [(BF, 1, False), (F32, 1, True), (BF, 40, False), (BF, 40, True)])
+def test_the_largest_table(gpu_lib, dtype, rows, weigh):
+    """2^31 - 384 positions of one kv head (masses: a page fewer than without), 64 pages over and over: as good as a softmax over these
+    with the logarithm of their counts.  A block's run is 7 (few columns) or 14 million positions, whose sums lose 2^-23 with every addition at
+    worst: of the products' as the header says, of the weights' one for each of 16 positions of a lane."""
+    hd, pages = 64, 64
+    width = 16777214 if weigh else 16777215
+    n = width * 128
+    pool = randn((pages, 2, 1, 128, hd), 58, BF)
+    table = torch.randint(0, pages, (1, width), dtype=torch.int32, device="cuda", generator=gen(59))
+    q = randn((1, rows, 1, hd), 60, dtype)
+    m = torch.zeros((1, 1, n), device="cuda") if weigh else None
+    status = i32([0])
+    out, lse = paged.attention(q, pool, table, i32([n]), return_lse=True, mass=m, status=status)
+    assert status.item() == 0
+    # the last page, of which rows see a part, apart from the counts of the others
+    count = torch.bincount(table[0, :-1].long(), minlength=pages).double()
+    k, v = (pool[:, j, 0].reshape(-1, hd).double() for j in (0, 1))
+    last = table[0, -1].long()
+    kk, vv = torch.cat([k, pool[last, 0, 0].double()]), torch.cat([v, pool[last, 1, 0].double()])
+    s = torch.einsum("rd,nd->rn", q[0, :, 0].double(), kk) / math.sqrt(hd)
+    s[:, :pages * 128] += torch.log(count.repeat_interleave(128))
+    sees = torch.arange(128, device="cuda")[None] <= torch.arange(128 - rows, 128, device="cuda")[:, None]
+    s[:, pages * 128:] = torch.where(sees, s[:, pages * 128:], -math.inf)
+    want, A = torch.softmax(s, -1) @ vv, torch.softmax(s, -1) @ vv.abs()
+    off = 2.0 ** -23 * n / 152 / 16
+    assert bool(((out[0, :, 0].double() - want).abs() <= off * A + 2.0 ** -8 * (want.abs() + off * A)).all())
+    assert bool(((lse[0, :, 0].double() - torch.logsumexp(s, -1)).abs() <= off).all())
+    if weigh:
+        one = torch.exp(s[:, :pages * 128] - torch.log(count.repeat_interleave(128)) - torch.logsumexp(s, -1)[:, None]).sum(0).view(pages, 128)
+        got = m[0, 0].view(width, 128)
+        for i in (0, 1, width // 2, width - 2):
+            assert bool(((got[i].double() - one[table[0, i].long()]).abs() <= 2 * off * one[table[0, i].long()]).all()), i
+        total = sum(float(x.double().sum()) for x in m.view(-1).split(1 << 27))
+        assert abs(total - rows) <= off * rows
+    del m
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype,rows,width", [(BF, 1, 1), (BF, 1, 200), (F32, 1, 200), (BF, 40, 3)])
+def test_twenty_thousand_sequences(gpu_lib, dtype, rows, width):
+    """Sequences of 0 to 90 positions that share 64 pages: a block each, or many runs a block."""
+    seqs, hd, pages = min(20000, 524287 // rows), 64, 64
+    pool = randn((pages, 2, 1, 128, hd), 64, BF)
+    table = torch.randint(0, pages, (seqs, width), dtype=torch.int32, device="cuda", generator=gen(65))
+    lengths = torch.randint(0, 91, (seqs,), dtype=torch.int32, device="cuda", generator=gen(66))
+    q = randn((seqs, rows, 1, hd), 67, dtype)
+    m = torch.ones((seqs, 1, 128 * width), device="cuda")
+    out, lse = paged.attention(q, pool, table, lengths, return_lse=True, mass=m, decay=0.5)
+    k, v = (pool[table[:, 0].long(), j, 0].float() for j in (0, 1))
+    s = torch.einsum("srd,snd->srn", q[:, :, 0].float(), k).double() / math.sqrt(hd)
+    at = torch.arange(128, device="cuda")
+    first = lengths.long()[:, None] - rows
+    sees = at[None, None] <= (first + torch.arange(rows, device="cuda"))[..., None]
+    s = s.masked_fill(~sees, -math.inf)
+    want = torch.logsumexp(s, -1)
+    fine = torch.isfinite(want)
+    assert torch.equal(torch.isfinite(lse[..., 0]), fine) and bool(((lse[..., 0].double() - want).abs()[fine] <= 1e-4).all())
+    w = torch.where(sees & fine[..., None], torch.exp(s - torch.where(fine, want, 0.0)[..., None]), 0.0)
+    o = torch.einsum("srn,snd->srd", w, v.double())
+    assert bool(((out[:, :, 0].double() - o).abs() <= 1e-4 * (1 + o.abs()) + (2.0 ** -8 if dtype == BF else 0) * o.abs()).all())
+    there = at < lengths[:, None]
+    old = torch.where(there, torch.where(at < first, 0.5, 0.0), 1.0)
+    assert bool(((m[:, 0, :128].double() - old - w.sum(1)).abs() <= 1e-4 * (1 + w.sum(1))).all()) and bool((m[:, 0, 128:] == 1).all())
